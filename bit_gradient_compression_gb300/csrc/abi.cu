@@ -15,13 +15,14 @@
 #include <string.h>
 
 #include "loco.h"
+#include "abi_checks.h"
 #include "loco_internal.h"
 
 namespace loco {
 
 static thread_local char g_last_error[512] = "";
 
-static loco_status fail(loco_status st, const char* fmt, ...) {
+loco_status fail(loco_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
@@ -73,7 +74,7 @@ static AddressRangeFn address_range_fn() {
 }
 
 // Null and alignment check (no CUDA call).
-static loco_status check_ptr(const void* p, size_t align, const char* name) {
+loco_status check_ptr(const void* p, size_t align, const char* name) {
   if (p == nullptr) return fail(LOCO_ERR_INVALID_ARG, "%s is NULL", name);
   if (reinterpret_cast<uintptr_t>(p) % align != 0)
     return fail(LOCO_ERR_MISALIGNED, "%s (%p) is not %zu-byte aligned", name, p, align);
@@ -82,7 +83,7 @@ static loco_status check_ptr(const void* p, size_t align, const char* name) {
 
 // Checks that [p, p + bytes) is device memory of the current device inside one
 // allocation.  name is used in the error text.
-static loco_status check_extent(const void* p, size_t bytes, const char* name) {
+loco_status check_extent(const void* p, size_t bytes, const char* name) {
   cudaPointerAttributes attr;
   cudaError_t e = cudaPointerGetAttributes(&attr, p);
   if (e != cudaSuccess) {
@@ -109,17 +110,7 @@ static loco_status check_extent(const void* p, size_t bytes, const char* name) {
   return LOCO_OK;
 }
 
-// A list of buffers checked together: every null/alignment rule first, then
-// the device-memory and extent rules, so the status does not depend on which
-// buffer happens to be listed first.
-struct BufCheck {
-  const void* p;
-  size_t bytes;
-  size_t align;
-  const char* name;
-};
-
-static loco_status check_buffers(const BufCheck* b, int count) {
+loco_status check_buffers(const BufCheck* b, int count) {
   for (int i = 0; i < count; ++i) {
     loco_status st = check_ptr(b[i].p, b[i].align, b[i].name);
     if (st != LOCO_OK) return st;
@@ -131,7 +122,7 @@ static loco_status check_buffers(const BufCheck* b, int count) {
   return LOCO_OK;
 }
 
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
@@ -143,7 +134,7 @@ static loco_status check_layout(int32_t bits, int32_t block) {
   return LOCO_OK;
 }
 
-static loco_status launch_result(cudaError_t e, const char* what) {
+loco_status launch_result(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return fail(LOCO_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
   g_last_error[0] = '\0';
   return LOCO_OK;

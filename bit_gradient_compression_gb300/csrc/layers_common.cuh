@@ -1,0 +1,150 @@
+// Device helpers of the layer kernels: element access, activations, and the
+// arithmetic of 8-bit checkpoints.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "layers_internal.h"
+#include "loco.h"
+
+namespace loco {
+
+__device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// One element of an array of bf16 or fp32 (a uniform branch on the type).
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int bf16) {
+  return bf16 ? bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p) + i)) : __ldg(static_cast<const float*>(p) + i);
+}
+__device__ __forceinline__ void store_elem(void* p, int64_t i, int bf16, float v) {
+  if (bf16)
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(p)[i] = v;
+}
+
+// One element of an array that the same kernel may write (an output that is also the residual).
+__device__ __forceinline__ float load_elem_rw(const void* p, int64_t i, int bf16) {
+  return bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// Eight consecutive elements through 16-byte accesses (the address is 16-byte aligned).
+template <bool RW = false>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int bf16, float v[8]) {
+  if (bf16) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint4 w = RW ? *q : __ldg(q);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(u[k] << 16);
+      v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    }
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = RW ? q[0] : __ldg(q), b = RW ? q[1] : __ldg(q + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store8(void* p, int64_t i, int bf16, const float v[8]) {
+  if (bf16) {
+    uint4 w;
+    w.x = pack_bf16x2(v[0], v[1]), w.y = pack_bf16x2(v[2], v[3]);
+    w.z = pack_bf16x2(v[4], v[5]), w.w = pack_bf16x2(v[6], v[7]);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = w;
+  } else {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit checkpoints: a block of 32 values shares the step 2^e, e = max(floor(log2 A) - 6, -126).
+// The exponent field of A's bits is floor(log2 A) + 127 (0 for a subnormal A), so the scale byte
+// e + 127 needs no logarithm, and 2^-e and 2^e are built from it: products with them are exact.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kCkptBad = 255;  // a block with a NaN or an infinity
+
+// Magnitude bits order like the magnitudes, with infinity and then NaN on top.
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t ckpt_scale(uint32_t amax_bits) {
+  const int f = int(amax_bits >> 23);
+  return f == 255 ? kCkptBad : uint32_t(max(f - 6, 1));
+}
+// 2^-e, or 0 for a bad block (whose codes are then all 0).
+__device__ __forceinline__ float ckpt_inv_step(uint32_t scale) {
+  return scale == kCkptBad ? 0.0f : __uint_as_float((254u - scale) << 23);
+}
+// 2^e, or NaN for a bad block.
+__device__ __forceinline__ float ckpt_step(uint32_t scale) {
+  return __uint_as_float(scale == kCkptBad ? 0x7FC00000u : scale << 23);
+}
+// The code of v: rint_even(v * inv) clamped to [-127, 127]; 0 for a NaN product (a bad block's).
+__device__ __forceinline__ int ckpt_code(float v, float inv) {
+  return __float2int_rn(fminf(fmaxf(inv == 0.0f ? 0.0f : v * inv, -127.0f), 127.0f));
+}
+__device__ __forceinline__ uint32_t ckpt_pack4(const float v[4], float inv) {
+  return (uint32_t(ckpt_code(v[0], inv)) & 0xFFu) | (uint32_t(ckpt_code(v[1], inv)) & 0xFFu) << 8 |
+         (uint32_t(ckpt_code(v[2], inv)) & 0xFFu) << 16 | uint32_t(ckpt_code(v[3], inv)) << 24;
+}
+// Four codes of a word as floats (exact): each byte, offset to unsigned, is placed in the low
+// mantissa bits of 2^23 and the offset subtracted.
+__device__ __forceinline__ void ckpt_unpack4(uint32_t w, float step, float v[4]) {
+  const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    v[k] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 | k)) - 8388736.0f) * step;
+}
+
+// ---------------------------------------------------------------------------
+// Activations and their slopes, in fp32.  exp is __expf (within 2 + |x| * 2^-22 units of the last
+// place) and the quotients are __fdividef (2 units); both stay below 1e-6 relative here.
+// A NaN stays one through every activation and slope.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+constexpr float kGeluK2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr float kGeluC = 0.044715f;
+
+__device__ __forceinline__ float act_value(float v, int act) {
+  switch (act) {
+    case LOCO_ACT_RELU: return v <= 0.0f ? 0.0f : v;
+    case LOCO_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case LOCO_ACT_GELU_TANH: {
+      // (1 + tanh u) / 2 = sigmoid(2u); beyond |v| = 20 it is 0 or 1 in fp32
+      const float c = fminf(fmaxf(v, -20.0f), 20.0f);
+      return v * sigmoid_f(kGeluK2 * fmaf(kGeluC * c * c, c, c));
+    }
+    case LOCO_ACT_SILU: return v * sigmoid_f(v);
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ float act_slope(float v, int act) {
+  switch (act) {
+    case LOCO_ACT_RELU: return v > 0.0f ? 1.0f : (v == v ? 0.0f : v);
+    case LOCO_ACT_GELU:
+      return fmaf(v * 0.3989422804014327f, __expf(-0.5f * fminf(v * v, 160.0f)),
+                  0.5f * (1.0f + erff(v * 0.70710678118654752f)));
+    case LOCO_ACT_GELU_TANH: {
+      const float c = fminf(fmaxf(v, -20.0f), 20.0f), q = c * c;
+      const float s = sigmoid_f(kGeluK2 * fmaf(kGeluC * q, c, c));
+      const float d = fmaf(c * s * (1.0f - s), kGeluK2 * fmaf(3.0f * kGeluC, q, 1.0f), s);
+      return v == v ? d : v;
+    }
+    case LOCO_ACT_SILU: {
+      const float s = sigmoid_f(v);
+      return s * fmaf(v, 1.0f - s, 1.0f);
+    }
+    default: return 1.0f;
+  }
+}
+
+}  // namespace loco

@@ -18,12 +18,19 @@ LIB_PATH = os.path.join(PKG, "libloco.so")
 LOCO_OK, LOCO_ERR_INVALID_ARG, LOCO_ERR_UNSUPPORTED, LOCO_ERR_MISALIGNED, LOCO_ERR_CUDA = 0, 1, 2, 3, 4
 LOCO_F32, LOCO_BF16 = 0, 1
 LOCO_SCALE_ABSMAX, LOCO_SCALE_FIXED = 0, 1
+LOCO_ACT_NONE, LOCO_ACT_RELU, LOCO_ACT_GELU, LOCO_ACT_GELU_TANH, LOCO_ACT_SILU = 0, 1, 2, 3, 4
+LOCO_NORM_LAYER, LOCO_NORM_RMS = 0, 1
+LOCO_CKPT_BLOCK = 32
+LOCO_MAX_DIM = 0x7FFFFFFF
 LOCO_MAX_RANKS = 16
 LOCO_MAX_N = 1 << 48
 
 EXPORTS = ("loco_num_blocks", "loco_code_bytes", "loco_compress", "loco_compress_e8", "loco_decode_reduce",
            "loco_adam_step", "loco_adam_step_bf16", "loco_sgd_step", "loco_shard_range", "loco_status_string",
-           "loco_last_error")
+           "loco_last_error", "loco_ckpt_code_bytes", "loco_ckpt_scale_bytes", "loco_ckpt_encode", "loco_ckpt_decode",
+           "loco_norm_forward", "loco_norm_workspace_bytes", "loco_norm_backward", "loco_linear_forward",
+           "loco_linear_backward_input", "loco_linear_workspace_bytes", "loco_linear_backward_weight",
+           "loco_linear_timeouts")
 
 
 class LocoError(RuntimeError):
@@ -44,6 +51,15 @@ class loco_adam_hparams(ctypes.Structure):
                 ("bias_correction", ctypes.c_int32), ("eps_inside_sqrt", ctypes.c_int32)]
 
 
+class loco_norm_config(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("x_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class loco_linear_config(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32)]
+
+
 def make_config(bits=4, block=256, beta=0.9, err_scale_mult=4.0, reset_period=0, fixed_scale=None):
     return loco_config(bits, block, LOCO_SCALE_FIXED if fixed_scale is not None else LOCO_SCALE_ABSMAX,
                        float(fixed_scale or 0.0), float(beta), float(err_scale_mult), int(reset_period))
@@ -52,6 +68,11 @@ def make_config(bits=4, block=256, beta=0.9, err_scale_mult=4.0, reset_period=0,
 def make_adam(lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, bias_correction=True,
               eps_inside_sqrt=False):
     return loco_adam_hparams(lr, beta1, beta2, eps, weight_decay, int(bias_correction), int(eps_inside_sqrt))
+
+
+def make_norm(kind=LOCO_NORM_LAYER, eps=1e-5):
+    """A norm's kind and eps; the calls fill in the types of the tensors they are given."""
+    return loco_norm_config(kind, float(eps), LOCO_F32, LOCO_F32, LOCO_F32, LOCO_F32)
 
 
 if not os.path.exists(LIB_PATH):
@@ -80,6 +101,35 @@ lib.loco_sgd_step.argtypes = [ctypes.POINTER(loco_config), _vp, _vp, _i32, _i64,
 lib.loco_sgd_step.restype = ctypes.c_int
 lib.loco_shard_range.argtypes = [_i64, _i32, _i32, _i32, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]
 lib.loco_shard_range.restype = ctypes.c_int
+_norm, _lin = ctypes.POINTER(loco_norm_config), ctypes.POINTER(loco_linear_config)
+lib.loco_ckpt_code_bytes.argtypes = [_i64, _i64]
+lib.loco_ckpt_code_bytes.restype = _i64
+lib.loco_ckpt_scale_bytes.argtypes = [_i64, _i64]
+lib.loco_ckpt_scale_bytes.restype = _i64
+lib.loco_ckpt_encode.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]
+lib.loco_ckpt_encode.restype = ctypes.c_int
+lib.loco_ckpt_decode.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _i32, _i64, _vp]
+lib.loco_ckpt_decode.restype = ctypes.c_int
+lib.loco_norm_forward.argtypes = [_norm, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]
+lib.loco_norm_forward.restype = ctypes.c_int
+lib.loco_norm_workspace_bytes.argtypes = [_i64, _i64]
+lib.loco_norm_workspace_bytes.restype = _i64
+lib.loco_norm_backward.argtypes = [_norm, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
+                                   _i64, _vp, _vp, _vp, _i64, _vp]
+lib.loco_norm_backward.restype = ctypes.c_int
+lib.loco_linear_forward.argtypes = [_lin, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp,
+                                    _vp]
+lib.loco_linear_forward.restype = ctypes.c_int
+lib.loco_linear_backward_input.argtypes = [_lin, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp,
+                                           _i64, _vp]
+lib.loco_linear_backward_input.restype = ctypes.c_int
+lib.loco_linear_workspace_bytes.argtypes = [_i64]
+lib.loco_linear_workspace_bytes.restype = _i64
+lib.loco_linear_backward_weight.argtypes = [_lin, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp,
+                                            _i64, _vp, _vp, _i64, _vp]
+lib.loco_linear_backward_weight.restype = ctypes.c_int
+lib.loco_linear_timeouts.argtypes = [ctypes.POINTER(_i64)]
+lib.loco_linear_timeouts.restype = ctypes.c_int
 lib.loco_status_string.argtypes = [ctypes.c_int]
 lib.loco_status_string.restype = ctypes.c_char_p
 lib.loco_last_error.argtypes = []
@@ -195,3 +245,201 @@ def loco_shard_range(n: int, block: int, W: int, j: int) -> tuple[int, int]:
     lo, hi = ctypes.c_int64(), ctypes.c_int64()
     _check(lib.loco_shard_range(n, block, W, j, ctypes.byref(lo), ctypes.byref(hi)))
     return lo.value, hi.value
+
+
+# --------------------------------------------------------------------------
+# Layers: norms, linear layers and 8-bit activation checkpoints.  Matrices are
+# two-dimensional tensors whose rows are contiguous (any row pitch).
+# --------------------------------------------------------------------------
+
+def _dtype(t, name: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return LOCO_BF16
+    if t.dtype == torch.float32:
+        return LOCO_F32
+    raise ValueError(f"{name}: dtype {t.dtype} is not supported (float32 or bfloat16)")
+
+
+def _mat(t, name: str, shape=None):
+    """(address, row pitch) of a matrix; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be two-dimensional (got {t.dim()} dimensions)")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+
+
+def _vec(t, name: str, count: int, dtype=None) -> int:
+    """Address of a contiguous vector of count elements; 0 for None."""
+    if t is None:
+        return 0
+    if t.dim() != 1 or t.numel() != count:
+        raise ValueError(f"{name} must be a vector of {count} (got {tuple(t.shape)})")
+    if count > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    return t.data_ptr()
+
+
+def _f32(t, name: str, count: int) -> int:
+    import torch
+    return _vec(t, name, count, torch.float32)
+
+
+def _ckpt(codes, scales, rows: int, cols: int):
+    """Addresses of a checkpoint of [rows, cols]: int8 codes and uint8 scales of the sizes the library states."""
+    import torch
+    for t, name, dtype, size in ((codes, "codes", torch.int8, lib.loco_ckpt_code_bytes(rows, cols)),
+                                 (scales, "scales", torch.uint8, lib.loco_ckpt_scale_bytes(rows, cols))):
+        if t is not None and (t.dtype != dtype or t.numel() != size or not t.is_contiguous()):
+            raise ValueError(f"{name} must be {size} contiguous {dtype} (got {t.numel()} {t.dtype})")
+    return (0 if codes is None else codes.data_ptr()), (0 if scales is None else scales.data_ptr())
+
+
+def _same_dtype(name: str, *tensors):
+    """The one dtype of the tensors that are given (LOCO_F32 where none is)."""
+    kinds = {t.dtype for t in tensors if t is not None}
+    if len(kinds) > 1:
+        raise ValueError(f"{name} must have one dtype (got {sorted(map(str, kinds))})")
+    return next((_dtype(t, name) for t in tensors if t is not None), LOCO_F32)
+
+
+def _bf16(t, name: str):
+    import torch
+    if t is not None and t.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: dtype {t.dtype} is not supported (bfloat16)")
+
+
+def _workspace(t):
+    if t is not None and not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return (0, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+
+
+def loco_ckpt_code_bytes(rows: int, cols: int) -> int:
+    return lib.loco_ckpt_code_bytes(rows, cols)
+
+
+def loco_ckpt_scale_bytes(rows: int, cols: int) -> int:
+    return lib.loco_ckpt_scale_bytes(rows, cols)
+
+
+def loco_ckpt_encode(x, codes, scales, *, stream=None):
+    """8-bit checkpoint of x [rows, cols]: int8 codes [rows, nb*32], uint8 scales [rows, nb], nb = ceil(cols/32)."""
+    px, ldx = _mat(x, "x")
+    rows, cols = x.shape
+    pc, ps = _ckpt(codes, scales, rows, cols)
+    _check(lib.loco_ckpt_encode(px, _dtype(x, "x"), ldx, rows, cols, pc, ps, _stream(stream)))
+
+
+def loco_ckpt_decode(codes, scales, out, *, act: int = LOCO_ACT_NONE, gamma=None, beta=None, stream=None):
+    """out [rows, cols] = act(values of the checkpoint * gamma + beta)."""
+    po, ldo = _mat(out, "out")
+    rows, cols = out.shape
+    pc, ps = _ckpt(codes, scales, rows, cols)
+    _check(lib.loco_ckpt_decode(pc, ps, rows, cols, act, _vec(gamma, "gamma", cols), _vec(beta, "beta", cols),
+                                _same_dtype("gamma and beta", gamma, beta), po, _dtype(out, "out"), ldo,
+                                _stream(stream)))
+
+
+def loco_norm_forward(cfg: loco_norm_config, x, gamma, beta, y, *, mean=None, rstd=None, codes=None, scales=None,
+                      stream=None):
+    """y = norm(x) * gamma + beta per row; optionally its statistics and an 8-bit checkpoint of the normalised rows."""
+    rows, cols = x.shape
+    px, ldx = _mat(x, "x")
+    py, ldy = _mat(y, "y", (rows, cols))
+    pc, ps = _ckpt(codes, scales, rows, cols)
+    c = loco_norm_config(cfg.kind, cfg.eps, _dtype(x, "x"), _dtype(y, "y"),
+                         _same_dtype("gamma and beta", gamma, beta), LOCO_F32)
+    _check(lib.loco_norm_forward(ctypes.byref(c), px, ldx, rows, cols, _vec(gamma, "gamma", cols),
+                                 _vec(beta, "beta", cols), py, ldy, _f32(mean, "mean", rows),
+                                 _f32(rstd, "rstd", rows), pc, ps, _stream(stream)))
+
+
+def loco_norm_workspace_bytes(rows: int, cols: int) -> int:
+    return lib.loco_norm_workspace_bytes(rows, cols)
+
+
+def loco_norm_backward(cfg: loco_norm_config, dy, gamma, rstd, dx, *, x=None, mean=None, codes=None, scales=None,
+                       residual=None, dgamma=None, dbeta=None, workspace=None, stream=None):
+    """Gradients of loco_norm_forward, from x or from the checkpoint of the normalised rows."""
+    rows, cols = dy.shape
+    pdy, lddy = _mat(dy, "dy")
+    px, ldx = _mat(x, "x", (rows, cols))
+    pr, ldr = _mat(residual, "residual", (rows, cols))
+    pdx, lddx = _mat(dx, "dx", (rows, cols))
+    pc, ps = _ckpt(codes, scales, rows, cols)
+    pw, nw = _workspace(workspace)
+    c = loco_norm_config(cfg.kind, cfg.eps, _same_dtype("x, residual and dx", x, residual, dx), _dtype(dy, "dy"),
+                         _same_dtype("gamma", gamma), _same_dtype("dgamma and dbeta", dgamma, dbeta))
+    _check(lib.loco_norm_backward(ctypes.byref(c), pdy, lddy, px, ldx, pc, ps, _f32(mean, "mean", rows),
+                                  _f32(rstd, "rstd", rows), rows, cols, _vec(gamma, "gamma", cols), pr, ldr, pdx,
+                                  lddx, _vec(dgamma, "dgamma", cols), _vec(dbeta, "dbeta", cols), pw, nw,
+                                  _stream(stream)))
+
+
+def loco_linear_forward(x, w, y, *, act: int = LOCO_ACT_NONE, bias=None, residual=None, codes=None, scales=None,
+                        stream=None):
+    """y = act(x w^T + bias) + residual; optionally an 8-bit checkpoint of the pre-activation.  x, w bf16."""
+    (T, K), N = x.shape, w.shape[0]
+    _bf16(x, "x")
+    _bf16(w, "w")
+    px, ldx = _mat(x, "x")
+    pw, ldw = _mat(w, "w", (N, K))
+    pr, ldr = _mat(residual, "residual", (T, N))
+    py, ldy = _mat(y, "y", (T, N))
+    pc, ps = _ckpt(codes, scales, T, N)
+    c = loco_linear_config(act, _same_dtype("y and residual", y, residual), _same_dtype("bias", bias))
+    _check(lib.loco_linear_forward(ctypes.byref(c), px, ldx, pw, ldw, _vec(bias, "bias", N), pr, ldr, T, N, K, py, ldy,
+                                   pc, ps, _stream(stream)))
+
+
+def loco_linear_backward_input(dy, w, dx, *, act: int = LOCO_ACT_NONE, codes=None, scales=None, residual=None,
+                               stream=None):
+    """dx = (dy w) * act'(z) + residual, z from the checkpoint of the layer below's pre-activation.  dy, w bf16."""
+    (T, N), K = dy.shape, w.shape[1]
+    _bf16(dy, "dy")
+    _bf16(w, "w")
+    pdy, lddy = _mat(dy, "dy")
+    pw, ldw = _mat(w, "w", (N, K))
+    pr, ldr = _mat(residual, "residual", (T, K))
+    pdx, lddx = _mat(dx, "dx", (T, K))
+    pc, ps = _ckpt(codes, scales, T, K)
+    c = loco_linear_config(act, _same_dtype("dx and residual", dx, residual), LOCO_F32)
+    _check(lib.loco_linear_backward_input(ctypes.byref(c), pdy, lddy, pw, ldw, pc, ps, pr, ldr, T, N, K, pdx, lddx,
+                                          _stream(stream)))
+
+
+def loco_linear_workspace_bytes(N: int) -> int:
+    return lib.loco_linear_workspace_bytes(N)
+
+
+def loco_linear_backward_weight(dy, dw, *, x=None, codes=None, scales=None, gamma=None, beta=None, db=None,
+                                workspace=None, stream=None):
+    """dw = dy^T x, db = column sums of dy; x [T, K] bf16, or gamma * (values of a checkpoint) + beta."""
+    (T, N), K = dy.shape, dw.shape[1]
+    _bf16(dy, "dy")
+    _bf16(x, "x")
+    pdy, lddy = _mat(dy, "dy")
+    px, ldx = _mat(x, "x", (T, K))
+    pdw, lddw = _mat(dw, "dw", (N, K))
+    pc, ps = _ckpt(codes, scales, T, K)
+    pw, nw = _workspace(workspace)
+    c = loco_linear_config(LOCO_ACT_NONE, _same_dtype("dw and db", dw, db), _same_dtype("gamma and beta", gamma, beta))
+    _check(lib.loco_linear_backward_weight(ctypes.byref(c), pdy, lddy, px, ldx, pc, ps, _vec(gamma, "gamma", K),
+                                           _vec(beta, "beta", K), T, N, K, pdw, lddw, _vec(db, "db", N), pw, nw,
+                                           _stream(stream)))
+
+
+def loco_linear_timeouts() -> int:
+    """Waits that the linear-layer kernels gave up on the current device (0 unless something is wrong); synchronises."""
+    v = ctypes.c_int64()
+    _check(lib.loco_linear_timeouts(ctypes.byref(v)))
+    return v.value

@@ -23,8 +23,8 @@
  *    b*block*bits/8.  4-bit codes are two's-complement nibbles, element 2j of
  *    the block in the low nibble of byte j, element 2j+1 in the high nibble.
  *    8-bit codes are int8.  Padding elements of a ragged last block get code 0.
- *  - Alignment: every buffer (grad, err, err_codes, err_steps, codes, scales,
- *    mean, param, m, v, param_bf16) must be 16-byte aligned
+ *  - Alignment: every buffer of the gradient path (grad, err, err_codes,
+ *    err_steps, codes, scales, mean, param, m, v, param_bf16) must be 16-byte aligned
  *    (LOCO_ERR_MISALIGNED otherwise).  The receivers stage each rank's steps
  *    with 16-byte copies, so a rank's scales placed at an offset inside a
  *    larger buffer (an exchange buffer, a shard of a bucket) must start on a
@@ -266,6 +266,180 @@ LOCO_API loco_status loco_sgd_step(const loco_config* cfg, const uint8_t* const*
  * Host only: no CUDA call.
  */
 LOCO_API loco_status loco_shard_range(int64_t n, int32_t block, int32_t W, int32_t j, int64_t* lo, int64_t* hi);
+
+/* ==========================================================================
+ * Layers in front of the gradient bucket: normalisation, linear layers and the
+ * 8-bit activation checkpoints their backward passes read.
+ *
+ * Matrices are row major: element (i, j) of a matrix p is p[i*ld + j], ld >=
+ * cols counted in elements, the columns of a row contiguous.  A matrix or
+ * vector needs only its element type's alignment (a slice of a flat bucket or
+ * a view of a wider matrix is fine); 16-byte aligned bases with ld a multiple
+ * of 8 (bf16) or 4 (fp32) elements take the wide loads.  codes and workspace
+ * must be 16-byte aligned.  rows and cols are at most LOCO_MAX_DIM.
+ * Outputs must not overlap any other buffer, with one exception: the output of
+ * an entry point that takes a residual may be the residual itself (same
+ * pointer, ld and type).  Column ranges of one wider matrix do not overlap.
+ * Statuses are those above: a null, short or overlapping buffer, a size or ld
+ * out of range is LOCO_ERR_INVALID_ARG, an unknown dtype, activation or kind
+ * LOCO_ERR_UNSUPPORTED, a misaligned pointer LOCO_ERR_MISALIGNED.
+ * Arithmetic is binary32 (sums, statistics and accumulators included); an
+ * output is rounded once, to its own type.  NaN and infinities propagate as
+ * the formulas have it: an output that reads none is not touched by them.
+ * Results do not change from run to run.
+ * ========================================================================== */
+
+#define LOCO_MAX_DIM ((int64_t)0x7fffffff)
+
+/* Values of a checkpoint that share one step. */
+#define LOCO_CKPT_BLOCK 32
+
+typedef enum {
+  LOCO_ACT_NONE = 0,      /* v                                                               */
+  LOCO_ACT_RELU = 1,      /* max(v, 0)                                                       */
+  LOCO_ACT_GELU = 2,      /* v * (1 + erf(v / sqrt 2)) / 2                                    */
+  LOCO_ACT_GELU_TANH = 3, /* v * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3))) / 2              */
+  LOCO_ACT_SILU = 4       /* v / (1 + exp(-v))                                               */
+} loco_act;
+
+typedef enum {
+  LOCO_NORM_LAYER = 0, /* rows less their mean, over the root of their variance + eps */
+  LOCO_NORM_RMS = 1    /* rows over the root of their mean square + eps; no mean is taken */
+} loco_norm_kind;
+
+typedef struct {
+  int32_t kind;        /* loco_norm_kind                                              */
+  float   eps;         /* added to the variance; finite, >= 0                         */
+  int32_t x_dtype;     /* loco_dtype of x, dx and the residual gradient               */
+  int32_t y_dtype;     /* loco_dtype of y and dy                                      */
+  int32_t param_dtype; /* loco_dtype of gamma and beta                                */
+  int32_t grad_dtype;  /* loco_dtype of dgamma and dbeta                              */
+} loco_norm_config;
+
+typedef struct {
+  int32_t act;         /* loco_act                                                    */
+  int32_t out_dtype;   /* loco_dtype of the outputs (y; dx; dw and db) and the residual */
+  int32_t param_dtype; /* loco_dtype of bias (forward), gamma and beta (weight gradient) */
+} loco_linear_config;
+
+/*
+ * 8-bit activation checkpoint of a matrix [rows, cols]: every row is cut into
+ * blocks of LOCO_CKPT_BLOCK = 32 values (nb = ceil(cols/32)); with A the
+ * block's largest magnitude,
+ *   e = max(floor(log2 A) - 6, -126)          (-126 for A = 0)
+ *   c = rint_even(v * 2^-e) clamped to [-127, 127]
+ * codes  [rows, nb*32] int8, contiguous; the padding of a ragged block is 0
+ * scales [rows, nb] uint8, contiguous: e + 127; 255 marks a block that held
+ *        a NaN or an infinity (codes 0), which reads back as NaN
+ * The step 2^e is a power of two, so c * 2^e is exact in bf16 (and fp32): a
+ * tensor-core product over restored values rounds none of its operands, and a
+ * bf16 value is off by at most half a step (an fp32 value within the last
+ * step below 2^(e+7) by less than one).
+ */
+
+/* Bytes of codes (rows * nb * 32) and of scales (rows * nb); 0 for rows or cols outside [1, LOCO_MAX_DIM]. */
+LOCO_API int64_t loco_ckpt_code_bytes(int64_t rows, int64_t cols);
+LOCO_API int64_t loco_ckpt_scale_bytes(int64_t rows, int64_t cols);
+
+/* x [rows, cols] (x_dtype, row pitch ldx) -> codes, scales.  rows == 0 or cols == 0 is an empty call. */
+LOCO_API loco_status loco_ckpt_encode(const void* x, int32_t x_dtype, int64_t ldx, int64_t rows, int64_t cols,
+                             int8_t* codes, uint8_t* scales, loco_stream_t stream);
+
+/*
+ * out = act(c * 2^e * gamma_j + beta_j), [rows, cols] of out_dtype, row pitch
+ * ldo.  gamma, beta [cols] of param_dtype, each may be NULL (1 and 0): a norm's
+ * output from its checkpoint.  LOCO_ACT_NONE without them restores the values.
+ */
+LOCO_API loco_status loco_ckpt_decode(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                             int32_t act, const void* gamma, const void* beta, int32_t param_dtype,
+                             void* out, int32_t out_dtype, int64_t ldo, loco_stream_t stream);
+
+/*
+ * loco_norm_forward — per row i of x [rows, cols]:
+ *   LAYER: m = mean_j x_j, r = 1/sqrt(mean_j (x_j - m)^2 + eps)
+ *   RMS:   m = 0,          r = 1/sqrt(mean_j x_j^2 + eps)
+ *   xhat_j = (x_j - m) * r ;  y_j = xhat_j * gamma_j + beta_j
+ * gamma, beta [cols], each may be NULL.  mean, rstd [rows] fp32, out, each may
+ * be NULL (a RMS norm's mean is not written).  codes/scales: checkpoint of
+ * xhat, out, both or neither.  cols >= 1; rows == 0 is an empty call.
+ */
+LOCO_API loco_status loco_norm_forward(const loco_norm_config* cfg, const void* x, int64_t ldx, int64_t rows,
+                              int64_t cols, const void* gamma, const void* beta, void* y, int64_t ldy,
+                              float* mean, float* rstd, int8_t* codes, uint8_t* scales, loco_stream_t stream);
+
+/* Bytes of workspace loco_norm_backward needs for dgamma/dbeta; 0 for sizes out of range. */
+LOCO_API int64_t loco_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * loco_norm_backward — gradients of loco_norm_forward for dy [rows, cols] (y_dtype):
+ *   g_j = dy_j * gamma_j
+ *   dx_j = r * (g_j - [LAYER: mean_k g_k] - xhat_j * mean_k(g_k * xhat_k)) + residual_j
+ *   dgamma_j = sum_i dy_ij * xhat_ij ;  dbeta_j = sum_i dy_ij
+ * xhat comes from x (with mean and rstd as the forward pass wrote them; mean is
+ * not read for RMS) or, where x is NULL, from the checkpoint codes/scales.
+ * residual [rows, cols] of x_dtype (the gradient that reached x past the
+ * norm) may be NULL, and may be dx itself.  dgamma, dbeta [cols] of grad_dtype,
+ * each may be NULL; workspace (ws_bytes >= loco_norm_workspace_bytes) may be
+ * NULL when both are.  rows == 0 writes zeros to dgamma and dbeta.
+ */
+LOCO_API loco_status loco_norm_backward(const loco_norm_config* cfg, const void* dy, int64_t lddy, const void* x,
+                               int64_t ldx, const int8_t* codes, const uint8_t* scales, const float* mean,
+                               const float* rstd, int64_t rows, int64_t cols, const void* gamma,
+                               const void* residual, int64_t ldr, void* dx, int64_t lddx, void* dgamma,
+                               void* dbeta, void* workspace, int64_t ws_bytes, loco_stream_t stream);
+
+/*
+ * loco_linear_forward — z = x w^T + bias ;  y = act(z) + residual.
+ * x [T, K] and w [N, K] bf16, products exact and accumulated in fp32; bias [N]
+ * of param_dtype or NULL; residual [T, N] and y [T, N] of out_dtype, residual
+ * may be NULL or y itself.  codes/scales: checkpoint of z [T, N], out, both or
+ * neither.  T == 0 or N == 0 is an empty call; K == 0 gives z = bias.
+ */
+LOCO_API loco_status loco_linear_forward(const loco_linear_config* cfg, const void* x, int64_t ldx, const void* w,
+                                int64_t ldw, const void* bias, const void* residual, int64_t ldr, int64_t T,
+                                int64_t N, int64_t K, void* y, int64_t ldy, int8_t* codes, uint8_t* scales,
+                                loco_stream_t stream);
+
+/*
+ * loco_linear_backward_input — dx = (dy w) * act'(z) + residual.
+ * dy [T, N] and w [N, K] bf16; z [T, K], the pre-activation of the layer that
+ * produced x, from its checkpoint codes/scales (ignored for LOCO_ACT_NONE):
+ * then dx is that layer's dz.  residual and dx [T, K] of out_dtype, residual
+ * may be NULL or dx itself.  T == 0 or K == 0 is an empty call.
+ */
+LOCO_API loco_status loco_linear_backward_input(const loco_linear_config* cfg, const void* dy, int64_t lddy,
+                                       const void* w, int64_t ldw, const int8_t* codes, const uint8_t* scales,
+                                       const void* residual, int64_t ldr, int64_t T, int64_t N, int64_t K,
+                                       void* dx, int64_t lddx, loco_stream_t stream);
+
+/* Bytes of workspace loco_linear_backward_weight needs where beta is given; 0 for N out of range. */
+LOCO_API int64_t loco_linear_workspace_bytes(int64_t N);
+
+/*
+ * loco_linear_backward_weight — dw = dy^T x ;  db_n = sum_t dy_tn.
+ * dy [T, N] bf16; x [T, K] bf16 or, where x is NULL, v * gamma_k + beta_k of
+ * the values v a checkpoint codes/scales of [T, K] stands for (a norm's output
+ * from the checkpoint of its normalised rows; gamma, beta [K] of param_dtype,
+ * each may be NULL, ignored with x), formed as
+ *   dw_nk = gamma_k * (sum_t dy_tn v_tk) + beta_k * db_n.
+ * dw [N, K] and db [N] of out_dtype; db may be NULL.  cfg->act is not read.
+ * workspace (ws_bytes >= loco_linear_workspace_bytes(N)) may be NULL without
+ * beta.  T == 0 writes zeros.
+ */
+LOCO_API loco_status loco_linear_backward_weight(const loco_linear_config* cfg, const void* dy, int64_t lddy,
+                                        const void* x, int64_t ldx, const int8_t* codes, const uint8_t* scales,
+                                        const void* gamma, const void* beta, int64_t T, int64_t N, int64_t K,
+                                        void* dw, int64_t lddw, void* db, void* workspace, int64_t ws_bytes,
+                                        loco_stream_t stream);
+
+/*
+ * Waits inside the linear-layer kernels (a tile's copies, a tile's products)
+ * end after two seconds and 20 microseconds per 64 of the summed dimension at
+ * most; a kernel that gave one up leaves its output unwritten in part and counts it.  This reads the count of the current
+ * device since the library was loaded into *count (host).  It synchronises
+ * with the device: for diagnosis, not for the training loop.
+ */
+LOCO_API loco_status loco_linear_timeouts(int64_t* count);
 
 /* Static text for a status code. */
 LOCO_API const char* loco_status_string(loco_status s);
