@@ -147,4 +147,34 @@ __device__ __forceinline__ float act_slope(float v, int act) {
   }
 }
 
+// v = act(v) and v *= act'(z), eight values at a time with the branch outside.
+__device__ __forceinline__ void apply_act8(float (&v)[8], int act) {
+#define LOCO_EACH(A)               \
+  case A:                          \
+    _Pragma("unroll") for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], A); \
+    break
+  switch (act) {
+    LOCO_EACH(LOCO_ACT_RELU);
+    LOCO_EACH(LOCO_ACT_GELU);
+    LOCO_EACH(LOCO_ACT_GELU_TANH);
+    LOCO_EACH(LOCO_ACT_SILU);
+    default: break;
+  }
+#undef LOCO_EACH
+}
+__device__ __forceinline__ void mul_slope8(float (&v)[8], const float (&z)[8], int act) {
+#define LOCO_EACH(A)               \
+  case A:                          \
+    _Pragma("unroll") for (int k = 0; k < 8; ++k) v[k] *= act_slope(z[k], A); \
+    break
+  switch (act) {
+    LOCO_EACH(LOCO_ACT_RELU);
+    LOCO_EACH(LOCO_ACT_GELU);
+    LOCO_EACH(LOCO_ACT_GELU_TANH);
+    LOCO_EACH(LOCO_ACT_SILU);
+    default: break;
+  }
+#undef LOCO_EACH
+}
+
 }  // namespace loco

@@ -8,14 +8,11 @@
 //   weight gradient  dw[n][k] = dy^T x      m = k (columns of x),  n = n, k = t
 // A CTA computes tiles of 128 m by BN n, 64 k at a time.  Operands whose memory
 // runs along k, or along m or n, are both taken as they lie (the tensor core's
-// operand descriptors name the direction), so nothing is transposed.  An output
-// row's 32 consecutive columns are the 32 lanes of a warp of the epilogue: its
-// loads and stores are whole sectors, and a checkpoint block is one warp
-// reduction.
+// operand descriptors name the direction), so nothing is transposed.
 //
-// Warps: 0 issues TMA loads, 1 issues products, 4..7 run the epilogue out of
-// tensor memory (two accumulators, so it overlaps the next tile's products),
-// and, in the LOADERS kernels, 8..15 write operands that TMA cannot fetch into
+// Warps: 0 issues TMA loads, 1 issues products, the next 8 (or 4) from warp 4 run
+// the epilogue out of tensor memory (two accumulators, so it overlaps the next
+// tile's products), and, in the LOADERS kernels, 8 more write operands that TMA cannot fetch into
 // the same swizzled layout: rows that start on no 16-byte boundary, and
 // checkpoints, which they turn into bf16 (exactly, as steps are powers of two).
 //
@@ -33,20 +30,27 @@ namespace {
 
 constexpr int kTileM = 128, kTileK = 64;
 constexpr int kLoadWarps = 8;
+constexpr int kChunk = 16;                     // output rows an epilogue warp turns over at a time
+constexpr int kChunkPitch = 36;                // floats per row of 32 columns: 16-byte reads of 8 rows x 4 lanes meet no bank twice
 
 __device__ unsigned long long g_timeouts;
 
-template <int BN>
+template <int BN, bool LOADERS>
 struct Shape {
+  // Epilogue warps: two per quarter of the accumulator's lanes, or one where loader warps need the registers.
+  static constexpr int kEpi = LOADERS ? 4 : 8;
+  static constexpr int kWarps = 4 + kEpi + (LOADERS ? kLoadWarps : 0);
+  static constexpr int kStageOut = kEpi * kChunk * kChunkPitch * 4;
   static constexpr int kABytes = kTileM * kTileK * 2, kBBytes = BN * kTileK * 2, kStage = kABytes + kBBytes;
   static constexpr int kStages = 200 * 1024 / kStage;
   static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 256;
+  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 256 + kStageOut;
 };
 
 struct Params {
   LinearArgs a;
   int a_tma, b_tma;
+  int out_wide, res_wide;  // rows of out and residual start on 16-byte boundaries
   int64_t tiles_m, tiles_n;
   int ktiles, split;
   uint64_t wait_ns;  // limit of every wait, longer than the longest tile
@@ -78,6 +82,17 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+__device__ __forceinline__ void st_shared4(uint32_t dst, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+}
+__device__ __forceinline__ void ld_shared8(uint32_t src, float (&v)[8]) {
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(src) : "memory");
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(src + 16)
+               : "memory");
+}
+
 // A tile of ROWS (m or n) x 64 (k) bf16 values by plain loads; 0 outside the matrix.
 template <int ROWS>
 __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_t ld, int mn, int64_t row0,
@@ -106,116 +121,185 @@ __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_
   }
 }
 
-// A tile of 128 (m) x 64 (k) values of a checkpoint [k][m]; 0 outside it.
-__device__ __forceinline__ void fill_ckpt(uint32_t dst, const int8_t* codes, const uint8_t* scales, int64_t nb,
-                                          int64_t m0, int64_t k0, int64_t ks, int tid) {
+// A thread's share of a tile of 128 (m) x 64 (k) values of a checkpoint [k][m]: 16 codes along m of
+// two k rows, with their scales.  Fetched kAheadCkpt k tiles before they are turned into bf16, as a k
+// tile's products take less time than memory takes to answer.
+constexpr int kAheadCkpt = 3;
+struct CkptPart {
+  uint4 w[2];
+  uint32_t scale[2];
+};
+
+__device__ __forceinline__ void fetch_ckpt(CkptPart& c, const LinearArgs& a, int64_t nb, int64_t m0, int64_t k0, int tid) {
+  const int h = tid & 7;
+  const int64_t blk = m0 / kCkptBlock + h / 2;
 #pragma unroll
-  for (int i = tid; i < kTileM / 16 * kTileK; i += kLoadWarps * 32) {
-    const int r = i / 8, h = i % 8;  // k row, 16 codes along m
-    const int64_t blk = m0 / kCkptBlock + h / 2;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (k0 + r < ks && blk < nb) {
-      const int64_t at = (k0 + r) * nb + blk;
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + at * kCkptBlock) + (h & 1));
-      const float st = ckpt_step(__ldg(scales + at));
-      float v[16];
-      ckpt_unpack4(w.x, st, v), ckpt_unpack4(w.y, st, v + 4), ckpt_unpack4(w.z, st, v + 8), ckpt_unpack4(w.w, st, v + 12);
-      lo = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-      hi = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
-                      pack_bf16x2(v[14], v[15]));
+  for (int i = 0; i < 2; ++i) {
+    const int64_t k = k0 + tid / 8 + i * (kLoadWarps * 4);
+    c.w[i] = make_uint4(0, 0, 0, 0);
+    c.scale[i] = 1;
+    if (k < a.K && blk < nb) {
+      const int64_t at = k * nb + blk;
+      c.w[i] = __ldg(reinterpret_cast<const uint4*>(a.a_codes + at * kCkptBlock) + (h & 1));
+      c.scale[i] = __ldg(a.a_scales + at);
     }
-    st_shared16(dst + unit_offset(1, r, 2 * h), lo);
-    st_shared16(dst + unit_offset(1, r, 2 * h + 1), hi);
+  }
+}
+
+__device__ __forceinline__ void fill_ckpt(uint32_t dst, const CkptPart& c, int tid) {
+  const int h = tid & 7, second = h >> 2;  // the upper 64 columns start with their odd unit: 8 lanes, 8 bank groups
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = tid / 8 + i * (kLoadWarps * 4);
+    const float st = ckpt_step(c.scale[i]);
+    float v[16];
+    ckpt_unpack4(c.w[i].x, st, v), ckpt_unpack4(c.w[i].y, st, v + 4);
+    ckpt_unpack4(c.w[i].z, st, v + 8), ckpt_unpack4(c.w[i].w, st, v + 12);
+    const uint4 lo = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                pack_bf16x2(v[6], v[7]));
+    const uint4 hi = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
+                                pack_bf16x2(v[14], v[15]));
+    st_shared16(dst + unit_offset(1, r, 2 * h + second), second ? hi : lo);
+    st_shared16(dst + unit_offset(1, r, 2 * h + 1 - second), second ? lo : hi);
   }
 }
 
 // ------------------------------------------------------------------ epilogue
 
-// What belongs to the thread's output column m.
-struct Column {
-  int64_t m;
-  bool live;
-  float scale, shift, bias;
+// The epilogue works on eight consecutive columns of a row per lane, four lanes to a checkpoint
+// block, so that every access to memory is a 16- or 8-byte one where alignment allows.
+
+// What belongs to a lane's eight columns.
+struct Columns {
+  int64_t m;      // the first
+  int live;       // how many of them the output has
+  float mul[8];   // col_scale
+  float add[8];   // col_shift, or the bias
 };
 
-__device__ __forceinline__ Column column_of(const LinearArgs& a, int64_t m) {
-  Column c{m, m < a.M, 1.0f, 0.0f, 0.0f};
-  if (c.live) {
-    if (a.col_scale != nullptr) c.scale = load_elem(a.col_scale, m, a.param_bf16);
-    if (a.col_shift != nullptr) c.shift = load_elem(a.col_shift, m, a.param_bf16);
-    if (a.bias != nullptr) c.bias = load_elem(a.bias, m, a.param_bf16);
+__device__ __forceinline__ Columns columns_of(const LinearArgs& a, int64_t m) {
+  Columns c;
+  c.m = m;
+  c.live = int(max(int64_t(0), min(int64_t(8), a.M - m)));
+  const void* add = a.col_shift != nullptr ? a.col_shift : a.bias;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    c.mul[k] = a.col_scale != nullptr && k < c.live ? load_elem(a.col_scale, m + k, a.param_bf16) : 1.0f;
+    c.add[k] = add != nullptr && k < c.live ? load_elem(add, m + k, a.param_bf16) : 0.0f;
   }
   return c;
 }
 
-// NJ output rows n0 .. n0 + count (a warp-uniform count) of the thread's column; every lane takes part.
-template <int NJ>
-__device__ __forceinline__ void finish(const LinearArgs& a, const Column& c, float (&v)[NJ], int64_t n0, int count) {
-  const int64_t nb = (a.M + kCkptBlock - 1) / kCkptBlock, blk = c.m / kCkptBlock;
-  float res[NJ], z[NJ];
+// What the epilogue of one row's eight columns reads, fetched ahead of its use.
+struct Ahead {
+  uint4 r0, r1;   // the residual: eight bf16 in r0, or eight fp32
+  uint2 z;        // eight codes of the checkpointed pre-activation
+  uint32_t zs;    // and their scale
+};
+
+__device__ __forceinline__ Ahead fetch_ahead(const Params& p, const Columns& c, int64_t n, bool row) {
+  const LinearArgs& a = p.a;
+  Ahead h;
+  h.r0 = h.r1 = make_uint4(0, 0, 0, 0);
+  h.z = make_uint2(0, 0);
+  h.zs = 1;
+  if (!row || c.live <= 0) return h;
   if (a.residual != nullptr) {
+    const char* q = static_cast<const char*>(a.residual) + (n * a.ldr + c.m) * (a.out_bf16 ? 2 : 4);
+    if (p.res_wide && c.live == 8) {
+      h.r0 = *reinterpret_cast<const uint4*>(q);
+      if (!a.out_bf16) h.r1 = *reinterpret_cast<const uint4*>(q + 16);
+    } else if (a.out_bf16) {
+      uint32_t e[8];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      res[j] = c.live && j < count ? load_elem_rw(a.residual, (n0 + j) * a.ldr + c.m, a.out_bf16) : 0.0f;
+      for (int k = 0; k < 8; ++k) e[k] = k < c.live ? uint32_t(reinterpret_cast<const uint16_t*>(q)[k]) : 0u;
+      h.r0 = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    } else {
+      uint32_t e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] = k < c.live ? reinterpret_cast<const uint32_t*>(q)[k] : 0u;
+      h.r0 = make_uint4(e[0], e[1], e[2], e[3]);
+      h.r1 = make_uint4(e[4], e[5], e[6], e[7]);
+    }
   }
   if (a.z_codes != nullptr) {
+    const int64_t nb = (a.M + kCkptBlock - 1) / kCkptBlock;
+    h.z = __ldg(reinterpret_cast<const uint2*>(a.z_codes + n * nb * kCkptBlock + c.m));
+    h.zs = __ldg(a.z_scales + n * nb + c.m / kCkptBlock);
+  }
+  return h;
+}
+
+// Row n of the lane's columns, v the sums over k.  Every lane of the warp takes part; `row`: the row exists.
+__device__ __forceinline__ void finish(const Params& p, const Columns& c, float (&v)[8], int64_t n, bool row,
+                                       const Ahead& h) {
+  const LinearArgs& a = p.a;
+  if (a.col_scale != nullptr || a.col_shift != nullptr) {
+    const float rs = a.col_shift != nullptr && row ? __ldg(a.row_sum + n) : 0.0f;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      z[j] = 0.0f;
-      if (c.live && j < count) {
-        const int64_t at = (n0 + j) * nb + blk;
-        z[j] = float(__ldg(a.z_codes + at * kCkptBlock + (c.m & 31))) * ckpt_step(__ldg(a.z_scales + at));
+    for (int k = 0; k < 8; ++k) v[k] = fmaf(c.add[k], rs, v[k] * c.mul[k]);
+  } else if (a.bias != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += c.add[k];
+  }
+  if (a.save_codes != nullptr) {
+    uint32_t mag = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k >= c.live) v[k] = 0.0f;
+      mag = max(mag, mag_bits(v[k]));
+    }
+    mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
+    mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
+    const int64_t nb = (a.M + kCkptBlock - 1) / kCkptBlock, blk = c.m / kCkptBlock;
+    if (row && blk < nb) {
+      const uint32_t sc = ckpt_scale(mag);
+      const float inv = ckpt_inv_step(sc);
+      *reinterpret_cast<uint2*>(a.save_codes + n * nb * kCkptBlock + c.m) =
+          make_uint2(ckpt_pack4(v, inv), ckpt_pack4(v + 4, inv));
+      if ((c.m & 31) == 0) a.save_scales[n * nb + blk] = uint8_t(sc);
+    }
+  }
+  if (!row || c.live <= 0) return;
+  if (a.z_codes != nullptr) {
+    float z[8];
+    const float st = ckpt_step(h.zs);
+    ckpt_unpack4(h.z.x, st, z);
+    ckpt_unpack4(h.z.y, st, z + 4);
+    mul_slope8(v, z, a.act);
+  } else {
+    apply_act8(v, a.act);
+  }
+  if (a.residual != nullptr) {
+    const uint32_t w[8] = {h.r0.x, h.r0.y, h.r0.z, h.r0.w, h.r1.x, h.r1.y, h.r1.z, h.r1.w};
+    if (a.out_bf16) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] += __uint_as_float(w[k] << 16);
+        v[2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += __uint_as_float(w[k]);
     }
   }
-  if (a.col_scale != nullptr) {
+  const int64_t at = n * a.ldo + c.m;
+  if (p.out_wide && c.live == 8) {
+    store8(a.out, at, a.out_bf16, v);
+  } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) v[j] *= c.scale;
-  }
-  if (a.col_shift != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (j < count) v[j] = fmaf(c.shift, __ldg(a.row_sum + n0 + j), v[j]);
-  }
-  if (a.bias != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) v[j] += c.bias;
-  }
-  if (a.save_codes != nullptr && blk < nb) {  // uniform: a warp's 32 columns are one block
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      if (j >= count) continue;
-      const uint32_t sc = ckpt_scale(__reduce_max_sync(0xFFFFFFFFu, c.live ? mag_bits(v[j]) : 0u));
-      const int64_t at = (n0 + j) * nb + blk;
-      a.save_codes[at * kCkptBlock + (c.m & 31)] = c.live ? int8_t(ckpt_code(v[j], ckpt_inv_step(sc))) : int8_t(0);
-      if ((c.m & 31) == 0) a.save_scales[at] = uint8_t(sc);
-    }
-  }
-  if (a.z_codes != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) v[j] *= act_slope(z[j], a.act);
-  } else if (a.act != LOCO_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) v[j] = act_value(v[j], a.act);
-  }
-  if (a.residual != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) v[j] += res[j];
-  }
-  if (c.live) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (j < count) store_elem(a.out, (n0 + j) * a.ldo + c.m, a.out_bf16, v[j]);
+    for (int k = 0; k < 8; ++k)
+      if (k < c.live) store_elem(a.out, at + k, a.out_bf16, v[k]);
   }
 }
 
 // ------------------------------------------------------------------ the kernel
 
 template <int BN, bool LOADERS>
-__global__ void __launch_bounds__(LOADERS ? 256 + kLoadWarps * 32 : 256, 1)
+__global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
     k_linear(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
              const __grid_constant__ Params p) {
-  using S = Shape<BN>;
+  using S = Shape<BN, LOADERS>;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t bars = base + S::kStages * S::kStage;
@@ -240,7 +324,7 @@ __global__ void __launch_bounds__(LOADERS ? 256 + kLoadWarps * 32 : 256, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 4);
+      mbar_init(acc_empty(b), S::kEpi);
     }
     mbar_init(drain, 1);
     mbar_init_fence();
@@ -336,58 +420,100 @@ __global__ void __launch_bounds__(LOADERS ? 256 + kLoadWarps * 32 : 256, 1)
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_ns);
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---- epilogue: lane i of warp 4 + q holds row q*32 + i of the accumulator
-    const int q = warp - 4;
+  } else if (warp >= 4 && warp < 4 + S::kEpi) {
+    // ---- epilogue: lane i of a warp reads row q*32 + i of the accumulator, an output column; 16
+    // output rows at a time are turned over in shared memory so that a lane has 8 columns of a row.
+    const int q = warp & 3, half = (warp - 4) / 4;
+    constexpr int kStride = S::kEpi / 4 * kChunk;  // output rows between a warp's chunks
+    const uint32_t mine = bars + 256 + uint32_t(warp - 4) * (kChunk * kChunkPitch * 4);
+    const int sub = lane / 4, seg = lane & 3;
     int buf = 0, bphase = 0;
     for (int64_t tile = worker; tile < tiles; tile += workers) {
       int64_t tm, tn;
       tile_at(p, tile, &tm, &tn);
-      const Column col = column_of(p.a, tm * kTileM + q * 32 + lane);
       const int64_t n0 = tn * BN;
       const int rows = int(min(int64_t(BN), p.a.N - n0));
+      Columns col;
+      Ahead ahead[kChunk / 8];
+      if (p.split == 1) {
+        col = columns_of(p.a, tm * kTileM + q * 32 + seg * 8);
+#pragma unroll
+        for (int i = 0; i < kChunk / 8; ++i) {
+          const int j = half * kChunk + i * 8 + sub;
+          ahead[i] = fetch_ahead(p, col, n0 + j, j < rows);
+        }
+      }
       if (kt0 < kt1) {
         if (!warp_wait(acc_full(buf), bphase, p.wait_ns)) {
           gave_up = true;
           break;
         }
         tc_fence_after();
+        if (half * kChunk >= rows && lane == 0) mbar_arrive(acc_empty(buf));
       }
 #pragma unroll 1
-      for (int j = 0; j < rows; j += 16) {
+      for (int j0 = half * kChunk; j0 < rows; j0 += kStride) {
         uint32_t w[16];
         if (kt0 < kt1) {
-          tmem_load16(tmem + buf * BN + j + (uint32_t(q * 32) << 16), w);
+          tmem_load16(tmem + buf * BN + j0 + (uint32_t(q * 32) << 16), w);
           tmem_wait_loads();
+          if (j0 + kStride >= rows) {
+            // the warp's part of the accumulator has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty(buf));
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] = 0;
         }
-        if (j + 16 >= rows && kt0 < kt1) {
-          // the accumulator has been read: the next tile but one may overwrite it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(acc_empty(buf));
-        }
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
         if (p.split > 1) {
+          // the whole tile stays in shared memory as [n][m], for the cluster
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + uint32_t(((j + i) * kTileM + q * 32 + lane) * 4)), "f"(v[i])
-                         : "memory");
-        } else {
-          finish<16>(p.a, col, v, n0 + j, min(16, rows - j));
+            st_shared4(base + uint32_t(((j0 + i) * kTileM + q * 32 + lane) * 4), w[i]);
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st_shared4(mine + uint32_t(i * kChunkPitch + lane) * 4, w[i]);
+        __syncwarp();
+        float v[kChunk / 8][8];
+#pragma unroll
+        for (int i = 0; i < kChunk / 8; ++i) ld_shared8(mine + uint32_t((i * 8 + sub) * kChunkPitch + seg * 8) * 4, v[i]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kChunk / 8; ++i) {
+          const Ahead now = ahead[i];
+          const int j = j0 + i * 8 + sub, nx = j + kStride;
+          ahead[i] = fetch_ahead(p, col, n0 + nx, nx < rows);
+          finish(p, col, v[i], n0 + j, j < rows, now);
         }
       }
       buf ^= 1;
       if (buf == 0) bphase ^= 1;
     }
-  } else if (LOADERS && warp >= 8) {
+  } else if (LOADERS && warp >= 4 + S::kEpi) {
     // ---- plain loads and checkpoints
-    const int tid = threadIdx.x - 256;
+    const int tid = threadIdx.x - (4 + S::kEpi) * 32;
     const int64_t nb = (p.a.M + kCkptBlock - 1) / kCkptBlock;
+    const bool ckpt = p.a.a_codes != nullptr;
+    CkptPart part[kAheadCkpt];
+    int64_t ptile = worker, pm0 = 0;  // what is fetched next
+    int pkt = kt0;
+    const auto fetch_next = [&](CkptPart& c) {
+      if (ptile >= tiles) return;
+      if (pkt == kt0) {
+        int64_t tm, tn;
+        tile_at(p, ptile, &tm, &tn);
+        pm0 = tm * kTileM;
+      }
+      fetch_ckpt(c, p.a, nb, pm0, int64_t(pkt) * kTileK, tid);
+      if (++pkt == kt1) pkt = kt0, ptile += workers;
+    };
+    if (ckpt && kt0 < kt1) {
+#pragma unroll
+      for (int i = 0; i < kAheadCkpt; ++i) fetch_next(part[i]);
+    }
     int stage = 0, phase = 0;
     for (int64_t tile = worker; tile < tiles && !gave_up; tile += workers) {
       int64_t tm, tn;
@@ -399,11 +525,13 @@ __global__ void __launch_bounds__(LOADERS ? 256 + kLoadWarps * 32 : 256, 1)
         }
         const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes;
         const int64_t k0 = int64_t(kt) * kTileK;
-        if (!p.a_tma) {
-          if (p.a.a_codes != nullptr)
-            fill_ckpt(sa, p.a.a_codes, p.a.a_scales, nb, tm * kTileM, k0, p.a.K, tid);
-          else
-            fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, tm * kTileM, p.a.M, k0, p.a.K, tid);
+        if (ckpt) {
+          fill_ckpt(sa, part[0], tid);
+#pragma unroll
+          for (int i = 0; i + 1 < kAheadCkpt; ++i) part[i] = part[i + 1];
+          fetch_next(part[kAheadCkpt - 1]);
+        } else if (!p.a_tma) {
+          fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, tm * kTileM, p.a.M, k0, p.a.K, tid);
         }
         if (!p.b_tma) fill_plain<BN>(sb, p.a.b, p.a.ldb, p.a.b_mn, tn * BN, p.a.N, k0, p.a.K, tid);
         fence_async_shared();
@@ -422,22 +550,27 @@ __global__ void __launch_bounds__(LOADERS ? 256 + kLoadWarps * 32 : 256, 1)
     cluster_sync();
     int64_t tm, tn;
     tile_at(p, worker, &tm, &tn);
-    const int q = warp & 3, side = warp / 4, sides = LOADERS ? 4 : 2;
-    const Column col = column_of(p.a, tm * kTileM + q * 32 + lane);
+    const int q = warp & 3, side = warp / 4, sides = S::kWarps / 4;
+    const int sub = lane / 4, seg = lane & 3;
+    const Columns col = columns_of(p.a, tm * kTileM + q * 32 + seg * 8);
     const int64_t n0 = tn * BN;
     const int rows = int(min(int64_t(BN), p.a.N - n0));
     const int share = (rows + p.split - 1) / p.split, lo = share * rank, hi = min(rows, lo + share);
-    for (int j = lo + side * 4; j < hi; j += sides * 4) {
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = lo + side * 8; j0 < hi; j0 += sides * 8) {
+      const int j = min(j0 + sub, hi - 1);
+      const bool row = j0 + sub < hi;
+      const Ahead h = fetch_ahead(p, col, n0 + j, row);
+      const uint32_t at = base + uint32_t((j * kTileM + q * 32 + seg * 8) * 4);
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0.0f;
       for (int r = 0; r < p.split; ++r) {
-        const uint32_t at = cluster_addr(base + uint32_t((j * kTileM + q * 32 + lane) * 4), uint32_t(r));
-        float w[4];
+        float w[8];
+        cluster_load8(cluster_addr(at, uint32_t(r)), w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = cluster_load(at + (j + i < hi ? i : 0) * (kTileM * 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += w[i];
+        for (int k = 0; k < 8; ++k) v[k] += w[k];
       }
-      finish<4>(p.a, col, v, n0 + j, min(4, hi - j));
+      finish(p, col, v, n0 + j, row, h);
     }
     cluster_sync();
   }
@@ -485,7 +618,7 @@ cudaError_t make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols
 
 template <int BN, bool LOADERS>
 cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
-  using S = Shape<BN>;
+  using S = Shape<BN, LOADERS>;
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -510,7 +643,7 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(LOADERS ? 256 + kLoadWarps * 32 : 256);
+  cfg.blockDim = dim3(S::kWarps * 32);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -535,6 +668,9 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   p.ktiles = int((a.K + kTileK - 1) / kTileK);
   if (p.ktiles == 0) p.a_tma = p.b_tma = 1;  // nothing is read
   p.wait_ns = 2000000000ull + uint64_t(p.ktiles) * 20000ull;
+  const size_t oe = a.out_bf16 ? 2 : 4;
+  p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && (a.N <= 1 || a.ldo * oe % 16 == 0);
+  p.res_wide = reinterpret_cast<uintptr_t>(a.residual) % 16 == 0 && (a.N <= 1 || a.ldr * oe % 16 == 0);
   const bool loaders = !p.a_tma || !p.b_tma;
   p.tiles_m = (a.M + kTileM - 1) / kTileM;
 

@@ -85,6 +85,16 @@ __device__ __forceinline__ float cluster_load(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void cluster_load8(uint32_t addr, float (&v)[8]) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr)
+               : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(addr + 16)
+               : "memory");
+}
 
 // ------------------------------------------------------------------ tensor memory and products
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t cols) {
