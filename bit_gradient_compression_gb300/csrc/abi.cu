@@ -82,8 +82,10 @@ loco_status check_ptr(const void* p, size_t align, const char* name) {
 }
 
 // Checks that [p, p + bytes) is device memory of the current device inside one
-// allocation.  name is used in the error text.
-loco_status check_extent(const void* p, size_t bytes, const char* name) {
+// allocation, whose range goes to lo and hi where the driver gives it (else both
+// are 0).  name is used in the error text.
+static loco_status check_extent(const void* p, size_t bytes, const char* name, uintptr_t* range_lo, uintptr_t* range_hi) {
+  *range_lo = *range_hi = 0;
   cudaPointerAttributes attr;
   cudaError_t e = cudaPointerGetAttributes(&attr, p);
   if (e != cudaSuccess) {
@@ -105,6 +107,7 @@ loco_status check_extent(const void* p, size_t bytes, const char* name) {
       if (lo + bytes > uintptr_t(base) + size)
         return fail(LOCO_ERR_INVALID_ARG, "%s: %zu bytes from %p run past the end of its allocation (%zu bytes at %p)",
                     name, bytes, p, size, reinterpret_cast<void*>(base));
+      *range_lo = uintptr_t(base), *range_hi = uintptr_t(base) + size;
     }
   }
   return LOCO_OK;
@@ -115,9 +118,20 @@ loco_status check_buffers(const BufCheck* b, int count) {
     loco_status st = check_ptr(b[i].p, b[i].align, b[i].name);
     if (st != LOCO_OK) return st;
   }
+  // Buffers that lie in an allocation already found in this call need no further question to the
+  // driver (small tensors of one caching allocator mostly share one).
+  constexpr int kFound = 4;
+  uintptr_t lo[kFound], hi[kFound];
+  int found = 0;
   for (int i = 0; i < count; ++i) {
-    loco_status st = check_extent(b[i].p, b[i].bytes, b[i].name);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(b[i].p);
+    bool known = false;
+    for (int k = 0; k < found && k < kFound; ++k) known |= p >= lo[k] && p <= hi[k] && b[i].bytes <= hi[k] - p;
+    if (known) continue;
+    const int at = found % kFound;
+    loco_status st = check_extent(b[i].p, b[i].bytes, b[i].name, &lo[at], &hi[at]);
     if (st != LOCO_OK) return st;
+    if (hi[at] != 0) ++found;
   }
   return LOCO_OK;
 }
@@ -135,7 +149,10 @@ static loco_status check_layout(int32_t bits, int32_t block) {
 }
 
 loco_status launch_result(cudaError_t e, const char* what) {
-  if (e != cudaSuccess) return fail(LOCO_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // reported here: not again by the next call
+    return fail(LOCO_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+  }
   g_last_error[0] = '\0';
   return LOCO_OK;
 }

@@ -15,10 +15,6 @@ loco_status fail(loco_status st, const char* fmt, ...);
 // Null and alignment check (no CUDA call).
 loco_status check_ptr(const void* p, size_t align, const char* name);
 
-// Checks that [p, p + bytes) is device memory of the current device inside one
-// allocation.  name is used in the error text.
-loco_status check_extent(const void* p, size_t bytes, const char* name);
-
 // A list of buffers checked together: every null/alignment rule first, then
 // the device-memory and extent rules, so the status does not depend on which
 // buffer happens to be listed first.

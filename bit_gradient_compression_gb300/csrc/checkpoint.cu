@@ -22,6 +22,24 @@ cudaError_t sm_count(int* sms) {
   return e;
 }
 
+cudaError_t layer_grid(LayerGrid& cache, const void* kernel, int threads, size_t smem_bytes, size_t smem_most, int* cap) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < LayerGrid::kDevices && (*cap = cache.cap[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  if (smem_most > 40 * 1024) {  // the default limit of 48 KB counts static shared memory too
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_most));
+    if (e != cudaSuccess) return e;
+  }
+  int sms = 0, per = 0;
+  if ((e = sm_count(&sms)) != cudaSuccess) return e;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem_bytes)) != cudaSuccess) return e;
+  if (per <= 0) return cudaErrorInvalidConfiguration;
+  *cap = sms * per;
+  if (dev < LayerGrid::kDevices) cache.cap[dev].store(*cap, std::memory_order_release);
+  return cudaSuccess;
+}
+
 namespace {
 
 constexpr int kThreads = 256;
@@ -51,10 +69,8 @@ __global__ void __launch_bounds__(kThreads) k_encode_wide(EncodeArgs a, int64_t 
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     if (!live) continue;
-    const uint32_t sc = ckpt_scale(m);
-    const float inv = ckpt_inv_step(sc);
-    reinterpret_cast<uint2*>(a.codes)[g] = make_uint2(ckpt_pack4(v, inv), ckpt_pack4(v + 4, inv));
-    if ((g & 3) == 0) a.scales[g >> 2] = uint8_t(sc);
+    reinterpret_cast<uint2*>(a.codes)[g] = ckpt_pack8(v, m);
+    if ((g & 3) == 0) a.scales[g >> 2] = uint8_t(ckpt_scale(m));
   }
 }
 

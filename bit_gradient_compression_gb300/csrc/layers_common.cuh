@@ -90,9 +90,22 @@ __device__ __forceinline__ float ckpt_step(uint32_t scale) {
 __device__ __forceinline__ int ckpt_code(float v, float inv) {
   return __float2int_rn(fminf(fmaxf(inv == 0.0f ? 0.0f : v * inv, -127.0f), 127.0f));
 }
-__device__ __forceinline__ uint32_t ckpt_pack4(const float v[4], float inv) {
-  return (uint32_t(ckpt_code(v[0], inv)) & 0xFFu) | (uint32_t(ckpt_code(v[1], inv)) & 0xFFu) << 8 |
-         (uint32_t(ckpt_code(v[2], inv)) & 0xFFu) << 16 | uint32_t(ckpt_code(v[3], inv)) << 24;
+// Eight codes of a block whose largest magnitude has the bits `amax`.  v * 2^-e is exact, so adding
+// 1.5 * 2^23 in one fused operation rounds it to an integer (halves to even) whose low byte is the
+// code.  Only a block with A >= 127.5 * 2^e can round past +-127, and only a bad block holds NaN or
+// infinity: those few take the clamped way.
+__device__ __forceinline__ uint2 ckpt_pack8(const float v[8], uint32_t amax) {
+  const float inv = ckpt_inv_step(ckpt_scale(amax));
+  uint32_t b[8];
+  if ((amax & 0x7FFFFFu) < 0x7F0000u && amax < 0x7F800000u) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = __float_as_uint(fmaf(v[k], inv, 12582912.0f));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = uint32_t(ckpt_code(v[k], inv));
+  }
+  return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
 }
 // Four codes of a word as floats (exact): each byte, offset to unsigned, is placed in the low
 // mantissa bits of 2^23 and the offset subtracted.

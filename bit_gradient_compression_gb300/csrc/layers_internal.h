@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace loco {
 
 constexpr int kCkptBlock = 32;
@@ -107,6 +109,16 @@ cudaError_t launch_norm_backward(const NormBwdArgs& a, cudaStream_t s);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_col_sum(const ColSumArgs& a, cudaStream_t s);
 cudaError_t read_linear_timeouts(int64_t* count);
+
+// Resident CTAs of one kernel on each device (0: not asked yet there).
+struct LayerGrid {
+  static constexpr int kDevices = 64;
+  std::atomic<int> cap[kDevices];
+};
+
+// CTAs of the kernel that the current device holds at once, launched with smem_bytes of dynamic
+// shared memory; smem_most is the most that any launch of this kernel asks for.
+cudaError_t layer_grid(LayerGrid& cache, const void* kernel, int threads, size_t smem_bytes, size_t smem_most, int* cap);
 
 // SMs of the current device (asked once per device).
 cudaError_t sm_count(int* sms);

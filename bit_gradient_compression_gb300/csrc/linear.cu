@@ -253,11 +253,8 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
     mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
     const int64_t nb = (a.M + kCkptBlock - 1) / kCkptBlock, blk = c.m / kCkptBlock;
     if (row && blk < nb) {
-      const uint32_t sc = ckpt_scale(mag);
-      const float inv = ckpt_inv_step(sc);
-      *reinterpret_cast<uint2*>(a.save_codes + n * nb * kCkptBlock + c.m) =
-          make_uint2(ckpt_pack4(v, inv), ckpt_pack4(v + 4, inv));
-      if ((c.m & 31) == 0) a.save_scales[n * nb + blk] = uint8_t(sc);
+      *reinterpret_cast<uint2*>(a.save_codes + n * nb * kCkptBlock + c.m) = ckpt_pack8(v, mag);
+      if ((c.m & 31) == 0) a.save_scales[n * nb + blk] = uint8_t(ckpt_scale(mag));
     }
   }
   if (!row || c.live <= 0) return;
@@ -514,7 +511,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
 #pragma unroll
       for (int i = 0; i < kAheadCkpt; ++i) fetch_next(part[i]);
     }
-    int stage = 0, phase = 0;
+    int stage = 0, phase = 0, turn = 0;
     for (int64_t tile = worker; tile < tiles && !gave_up; tile += workers) {
       int64_t tm, tn;
       tile_at(p, tile, &tm, &tn);
@@ -526,10 +523,14 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
         const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes;
         const int64_t k0 = int64_t(kt) * kTileK;
         if (ckpt) {
-          fill_ckpt(sa, part[0], tid);
+          // each part in its own registers: moving them along would wait for their loads
 #pragma unroll
-          for (int i = 0; i + 1 < kAheadCkpt; ++i) part[i] = part[i + 1];
-          fetch_next(part[kAheadCkpt - 1]);
+          for (int i = 0; i < kAheadCkpt; ++i)
+            if (turn == i) {
+              fill_ckpt(sa, part[i], tid);
+              fetch_next(part[i]);
+            }
+          if (++turn == kAheadCkpt) turn = 0;
         } else if (!p.a_tma) {
           fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, tm * kTileM, p.a.M, k0, p.a.K, tid);
         }
@@ -714,36 +715,58 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
 
 namespace {
 
-// 64 columns per CTA, its 16 warps each every 16th row of the CTA's share; the CTAs of a cluster
-// share the rows, and the first adds their sums in order.
-constexpr int kSumWarps = 16;
+// 64 columns per CTA: 8 lanes of 8 columns (one 16-byte load), 4 rows per warp, 16 warps; the CTAs of
+// a cluster share the rows, and the first adds their sums in order.  Bound by memory: 4 loads per
+// lane are kept in flight.
+constexpr int kSumWarps = 16, kSumRows = kSumWarps * 4;
 
 __global__ void __launch_bounds__(kSumWarps * 32) k_col_sum(ColSumArgs a, int parts) {
   __shared__ float sm[kSumWarps][64];
   __shared__ float part[64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int rank = parts > 1 ? int(cluster_rank()) : 0;
-  const int64_t c = int64_t(blockIdx.x / parts) * 64 + lane * 2;
+  const int64_t c = int64_t(blockIdx.x / parts) * 64 + (lane & 7) * 8;
   const int64_t lo = a.rows * rank / parts, hi = a.rows * (rank + 1) / parts;
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  float s0 = 0.0f, s1 = 0.0f;
-  const bool pair = (reinterpret_cast<uintptr_t>(x) % 4 == 0) && a.ldx % 2 == 0 && c + 1 < a.cols;
-  if (c < a.cols) {
-#pragma unroll 4
-    for (int64_t r = lo + warp; r < hi; r += kSumWarps) {
-      const uint16_t* q = x + r * a.ldx + c;
-      if (pair) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q));
-        s0 += __uint_as_float(w << 16);
-        s1 += __uint_as_float(w & 0xFFFF0000u);
-      } else {
-        s0 += bf16_bits_to_f32(__ldg(q));
-        if (c + 1 < a.cols) s1 += bf16_bits_to_f32(__ldg(q + 1));
+  float s[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[k] = 0.0f;
+  if (c + 8 <= a.cols && reinterpret_cast<uintptr_t>(x) % 16 == 0 && a.ldx % 8 == 0) {
+    int64_t r = lo + warp * 4 + lane / 8;
+    for (; r + 3 * kSumRows < hi; r += 4 * kSumRows) {
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(x + (r + i * kSumRows) * a.ldx + c));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[2 * k] += __uint_as_float(u[k] << 16);
+          s[2 * k + 1] += __uint_as_float(u[k] & 0xFFFF0000u);
+        }
       }
     }
+    for (; r < hi; r += kSumRows) {
+      float v[8];
+      load8(x, r * a.ldx + c, 1, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[k] += v[k];
+    }
+  } else {
+#pragma unroll 2
+    for (int64_t r = lo + warp * 4 + lane / 8; r < hi; r += kSumRows) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < a.cols) s[k] += bf16_bits_to_f32(__ldg(x + r * a.ldx + c + k));
+    }
   }
-  sm[warp][lane * 2] = s0;
-  sm[warp][lane * 2 + 1] = s1;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], 8);
+    s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], 16);
+    if (lane < 8) sm[warp][lane * 8 + k] = s[k];
+  }
   __syncthreads();
   float v = 0.0f;
   if (threadIdx.x < 64) {
@@ -774,7 +797,7 @@ cudaError_t launch_col_sum(const ColSumArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t strips = (a.cols + 63) / 64;
   int parts = 1;
-  while (parts < 8 && strips * parts < sms && a.rows >= int64_t(parts) * 2 * kSumWarps * 4) parts *= 2;
+  while (parts < 8 && strips * parts < 4 * sms && a.rows >= int64_t(parts) * 2 * kSumRows) parts *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(strips * parts));
   cfg.blockDim = dim3(kSumWarps * 32);

@@ -3,20 +3,27 @@
 // reduction of the parameters' gradients.
 //
 // Both directions are bound by memory.  A row belongs to a group of G threads
-// (a warp up to 1024 columns, else a CTA) that keeps it in registers, so it is
-// read once: the mean, then the sum of squared deviations (two passes over
+// (a warp up to 256 columns, else up to a CTA) that keeps it in registers, so it
+// is read once: the mean, then the sum of squared deviations (two passes over
 // registers, no cancellation), then the output.  Thread t of a group holds
 // vectors t, t + G, ... of 8 columns (WIDE), or single columns t, t + G, ...
 // where a row cannot be loaded 16 bytes at a time; either way 32 consecutive
 // columns are 4 lanes or 32 lanes of one warp, which gives a checkpoint block
 // its largest magnitude with two shuffles or one warp reduction.
 //
-// The backward pass walks rows with a fixed grid; each thread keeps the sums of
-// dgamma and dbeta of its own columns in registers over all its CTA's rows, one
-// partial row per CTA goes to the workspace, and a second kernel adds the
-// partial rows in order: no atomics, the same result every run.
+// The grid is as large as fits and walks the rows.  A row's sums need all of it,
+// so the next rows have to be on their way meanwhile: WIDE threads copy their
+// own 16-byte pieces of the next kStages - 1 rows into shared memory (cp.async;
+// nobody else reads them, so no barrier is needed), the others load the next
+// row into registers.
+//
+// In the backward pass each thread keeps the sums of dgamma and dbeta of its own
+// columns in registers over all its rows, one partial row per CTA goes to the
+// workspace, and a second kernel adds the partial rows in order: no atomics, the
+// same result every run.
 #include <atomic>
 
+#include "device_common.cuh"
 #include "layers_common.cuh"
 
 namespace loco {
@@ -29,26 +36,33 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums of N values over the group's G threads, the same in all of them.  `red` holds 32 floats per
-// value; consecutive calls alternate between two such areas, so one barrier per call is enough.
+template <int G>
+constexpr int kCtaThreads = G < 256 ? 256 : G;
+
+// Sums of N values over the group's G threads, the same in all of them; every thread of the CTA
+// takes part.  `red` holds 32 floats per value, and consecutive calls of a loop alternate between
+// two such areas, so that one barrier per call is enough.
 template <int G, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float* red) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
   if constexpr (G > 32) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    constexpr int kWarps = G / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, first = warp / kWarps * kWarps;
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) red[i * 32 + warp] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < G / 32 ? red[i * 32 + lane] : 0.0f);
+    for (int i = 0; i < N; ++i) {
+      v[i] = lane < kWarps ? red[i * 32 + first + lane] : 0.0f;
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+      v[i] = __shfl_sync(0xFFFFFFFFu, v[i], 0);
+    }
   }
 }
-
-template <int G>
-constexpr int kCtaThreads = G == 32 ? 256 : G;
 
 // Column of element k of a thread's vector e.
 template <int G, bool WIDE>
@@ -119,9 +133,7 @@ __device__ __forceinline__ void store_codes(const NormFwdArgs& a, int64_t row, i
     const int g = t + G * e;
     if (g < nb * 4) {
       const uint32_t sc = ckpt_scale(m);
-      const float inv = ckpt_inv_step(sc);
-      reinterpret_cast<uint2*>(a.codes + row * nb * kCkptBlock)[g] =
-          make_uint2(ckpt_pack4(v, inv), ckpt_pack4(v + 4, inv));
+      reinterpret_cast<uint2*>(a.codes + row * nb * kCkptBlock)[g] = ckpt_pack8(v, m);
       if ((g & 3) == 0) a.scales[row * nb + g / 4] = uint8_t(sc);
     }
   } else {
@@ -137,54 +149,169 @@ __device__ __forceinline__ void store_codes(const NormFwdArgs& a, int64_t row, i
   }
 }
 
-template <int G, int NV, bool XBF16, bool WIDE>
-__global__ void __launch_bounds__(kCtaThreads<G>) k_norm_fwd(NormFwdArgs a, bool pwide) {
-  __shared__ float red[2][32];
-  const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t row = G == 32 ? int64_t(blockIdx.x) * (kCtaThreads<G> / 32) + threadIdx.x / 32 : blockIdx.x;
-  if (row >= a.rows) return;  // the whole group: a warp, or (never) a CTA
-  const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
-  const void* xr = at(a.x, row * a.ldx, XBF16);
-  float x[NV][8];
+// ---- the next rows' pieces in shared memory (WIDE)
+
+// A thread's 16-byte pieces: piece i of stage s at ring + ((s * pieces + i) * threads + thread) * 16.
+template <int T>
+__device__ __forceinline__ uint4* piece(uint8_t* ring, int pieces, int stage, int i) {
+  return reinterpret_cast<uint4*>(ring) + (stage * pieces + i) * T + threadIdx.x;
+}
+// Starts the copy of a thread's whole vectors of one row: NV pieces (bf16) or 2 NV (fp32) from piece `first`.
+template <int G, int NV>
+__device__ __forceinline__ void copy_row(uint8_t* ring, int pieces, int stage, int first, const void* row, int cols, int t,
+                                         int bf16) {
+  constexpr int T = kCtaThreads<G>;
 #pragma unroll
-  for (int e = 0; e < NV; ++e) load_vec<G, WIDE, XBF16>(xr, cols, t, e, x[e]);
-  float mean = 0.0f;
-  if (!a.rms) {
-    float s[1] = {0.0f};
+  for (int e = 0; e < NV; ++e) {
+    const int c0 = (t + G * e) * 8;
+    if (c0 + 8 > cols) continue;
+    const char* q = static_cast<const char*>(row) + int64_t(c0) * (bf16 ? 2 : 4);
+    if (bf16) {
+      cp_async16(piece<T>(ring, pieces, stage, first + e), q);
+    } else {
+      cp_async16(piece<T>(ring, pieces, stage, first + 2 * e), q);
+      cp_async16(piece<T>(ring, pieces, stage, first + 2 * e + 1), q + 16);
+    }
+  }
+}
+__device__ __forceinline__ void widen(uint4 a, float v[8]) {
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[2 * k] = __uint_as_float(u[k] << 16), v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+}
+// Vector e of the row that was copied; `row` itself serves a vector the row ends in.
+template <int G, int NV, bool RW = false>
+__device__ __forceinline__ void copied_vec(uint8_t* ring, int pieces, int stage, int first, const void* row, int cols,
+                                           int t, int e, int bf16, float v[8]) {
+  constexpr int T = kCtaThreads<G>;
+  if ((t + G * e) * 8 + 8 <= cols) {
+    if (bf16) {
+      widen(*piece<T>(ring, pieces, stage, first + e), v);
+    } else {
+      const uint4 a = *piece<T>(ring, pieces, stage, first + 2 * e), b = *piece<T>(ring, pieces, stage, first + 2 * e + 1);
+      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
+    }
+  } else if (bf16) {
+    load_vec<G, true, true, RW>(row, cols, t, e, v);
+  } else {
+    load_vec<G, true, false, RW>(row, cols, t, e, v);
+  }
+}
+
+template <int G, int NV, bool XBF16>
+constexpr int kFwdPieces = NV * (XBF16 ? 1 : 2);
+// Stages: a row of 16384 fp32 columns takes 64 KB of shared memory.
+template <int NV, bool XBF16>
+constexpr int kFwdRing = XBF16 || NV < 4 ? 4 : 3;
+
+template <int G, int NV, bool XBF16, bool WIDE>
+__global__ void __launch_bounds__(kCtaThreads<G>, kCtaThreads<G> == 512 ? 1 : 2) k_norm_fwd(NormFwdArgs a, bool pwide) {
+  __shared__ float red[2][32];
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kGroups = kCtaThreads<G> / G, kP = kFwdPieces<G, NV, XBF16>, kFwdStages = kFwdRing<NV, XBF16>;
+  constexpr bool kKeep = NV <= 2;  // gamma and beta stay in registers
+  const int t = threadIdx.x % G, grp = threadIdx.x / G;
+  const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
+  const int64_t step = int64_t(gridDim.x) * kGroups, first = int64_t(blockIdx.x) * kGroups + grp;
+  float gm[NV][8], bt[NV][8], nx[NV][8];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, gm[e]);
+      load_param<G, WIDE>(a.beta, cols, t, e, a.param_bf16, pwide, 0.0f, bt[e]);
+    }
+  }
+  const auto x_row = [&](int64_t row) { return at(a.x, row * a.ldx, XBF16); };
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < kFwdStages - 1; ++i) {
+      const int64_t row = first + i * step;
+      if (row < a.rows) copy_row<G, NV>(ring, kP, i, 0, x_row(row), cols, t, XBF16);
+      cp_async_commit();
+    }
+  } else if (first < a.rows) {
+#pragma unroll
+    for (int e = 0; e < NV; ++e) load_vec<G, WIDE, XBF16>(x_row(first), cols, t, e, nx[e]);
+  }
+  int stage = 0, turn = 0;
+  // the CTA's groups go through the loop together
+  for (int64_t row = first; row - grp < a.rows; row += step) {
+    const bool live = row < a.rows;
+    float x[NV][8];
+    if constexpr (WIDE) {
+      const int64_t ahead = row + (kFwdStages - 1) * step;
+      if (ahead < a.rows)
+        copy_row<G, NV>(ring, kP, (stage + kFwdStages - 1) % kFwdStages, 0, x_row(ahead), cols, t, XBF16);
+      cp_async_commit();
+      cp_async_wait<kFwdStages - 1>();
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        if (live) {
+          copied_vec<G, NV>(ring, kP, stage, 0, x_row(row), cols, t, e, XBF16, x[e]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[e][k] = 0.0f;
+        }
+      }
+      stage = (stage + 1) % kFwdStages;
+    } else {
+#pragma unroll
+      for (int e = 0; e < NV; ++e)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[e][k] = live ? nx[e][k] : 0.0f;
+      if (row + step < a.rows) {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) load_vec<G, WIDE, XBF16>(x_row(row + step), cols, t, e, nx[e]);
+      }
+    }
+    float mean = 0.0f;
+    if (!a.rms) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int e = 0; e < NV; ++e)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[0] += x[e][k];
+      group_sum<G>(s, red[turn]);
+      turn ^= 1;
+      mean = s[0] / float(cols);
+    }
+    float q[1] = {0.0f};
 #pragma unroll
     for (int e = 0; e < NV; ++e)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[0] += x[e][k];
-    group_sum<G>(s, red[0]);
-    mean = s[0] / float(cols);
-  }
-  float q[1] = {0.0f};
-#pragma unroll
-  for (int e = 0; e < NV; ++e)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[e][k] = col_of<G, WIDE>(t, e, k) < cols ? x[e][k] - mean : 0.0f;
-      q[0] = fmaf(x[e][k], x[e][k], q[0]);
+      for (int k = 0; k < 8; ++k) {
+        x[e][k] = col_of<G, WIDE>(t, e, k) < cols ? x[e][k] - mean : 0.0f;
+        q[0] = fmaf(x[e][k], x[e][k], q[0]);
+      }
+    group_sum<G>(q, red[turn]);
+    turn ^= 1;
+    const float rstd = 1.0f / sqrtf(q[0] / float(cols) + a.eps);
+    if (t == 0 && live) {
+      if (a.mean != nullptr && !a.rms) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
-  group_sum<G>(q, red[1]);
-  const float rstd = 1.0f / sqrtf(q[0] / float(cols) + a.eps);
-  if (t == 0) {
-    if (a.mean != nullptr && !a.rms) a.mean[row] = mean;
-    if (a.rstd != nullptr) a.rstd[row] = rstd;
-  }
-  void* yr = at(a.y, row * a.ldy, a.y_bf16);
+    if (!live) continue;  // whole warps
+    void* yr = at(a.y, row * a.ldy, a.y_bf16);
 #pragma unroll
-  for (int e = 0; e < NV; ++e) {
+    for (int e = 0; e < NV; ++e) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[e][k] *= rstd;
-    if (a.codes != nullptr) store_codes<G, WIDE>(a, row, t, e, nb, x[e]);
-    if (col_of<G, WIDE>(t, e, 0) < cols) {
-      float g[8], b[8];
-      load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, g);
-      load_param<G, WIDE>(a.beta, cols, t, e, a.param_bf16, pwide, 0.0f, b);
+      for (int k = 0; k < 8; ++k) x[e][k] *= rstd;
+      if (a.codes != nullptr) store_codes<G, WIDE>(a, row, t, e, nb, x[e]);
+      if (col_of<G, WIDE>(t, e, 0) < cols) {
+        if constexpr (kKeep) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[e][k] = fmaf(x[e][k], g[k], b[k]);
-      store_vec<G, WIDE>(yr, cols, t, e, a.y_bf16, x[e]);
+          for (int k = 0; k < 8; ++k) x[e][k] = fmaf(x[e][k], gm[e][k], bt[e][k]);
+        } else {
+          float g[8], b[8];
+          load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, g);
+          load_param<G, WIDE>(a.beta, cols, t, e, a.param_bf16, pwide, 0.0f, b);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[e][k] = fmaf(x[e][k], g[k], b[k]);
+        }
+        store_vec<G, WIDE>(yr, cols, t, e, a.y_bf16, x[e]);
+      }
     }
   }
 }
@@ -234,96 +361,164 @@ __global__ void __launch_bounds__(kLoop) k_norm_fwd_long(NormFwdArgs a) {
 
 // ---------------------------------------------------------------------------------------- backward
 
-// The normalised values of a thread's vector e, from x and the row's statistics or from the checkpoint.
-template <int G, bool WIDE, bool XBF16, bool CKPT>
-__device__ __forceinline__ void load_xhat(const NormBwdArgs& a, int64_t row, int cols, int nb, int t, int e,
-                                          float mean, float rstd, float v[8]) {
-  if constexpr (CKPT) {
-    if constexpr (WIDE) {
-      const int g = t + G * e;
-      if (g < nb * 4) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.codes + row * nb * kCkptBlock) + g);
-        const float st = ckpt_step(__ldg(a.scales + row * nb + g / 4));
-        ckpt_unpack4(w.x, st, v);
-        ckpt_unpack4(w.y, st, v + 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (g * 8 + k >= cols) v[k] = 0.0f;  // a bad block's padding reads back as NaN
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = col_of<G, WIDE>(t, e, k);
-        v[k] = c < cols ? float(__ldg(a.codes + row * nb * kCkptBlock + c)) *
-                              ckpt_step(__ldg(a.scales + row * nb + c / kCkptBlock))
-                        : 0.0f;
-      }
-    }
-  } else {
-    load_vec<G, WIDE, XBF16>(at(a.x, row * a.ldx, XBF16), cols, t, e, v);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = col_of<G, WIDE>(t, e, k) < cols ? (v[k] - mean) * rstd : 0.0f;
-  }
+// A row's contribution that one thread holds: dy, and x or the codes of the normalised row.
+template <int G, int NV, bool XBF16, bool WIDE, bool CKPT>
+struct BwdRow {
+  float dy[NV][8], x[NV][8], r[NV][8];  // narrow: the values (x normalised only later)
+  uint2 codes[NV];                      // WIDE from a checkpoint
+  uint32_t scale[NV];
+  float mean, rstd;
+};
+
+// 16-byte pieces of one stage: dy, then x, then the residual (fp32 takes two per vector).
+template <int NV>
+__host__ __device__ __forceinline__ int bwd_pieces(int y_bf16, int x_bf16, bool has_x, bool has_residual) {
+  return NV * ((y_bf16 ? 1 : 2) + (x_bf16 ? 1 : 2) * ((has_x ? 1 : 0) + (has_residual ? 1 : 0)));
 }
+// As many rows ahead as shared memory holds for the widest types (a row of 8192 fp32 columns with
+// fp32 dy and residual takes 96 KB).
+template <int G, bool XBF16>
+constexpr int kBwdStages = (G == 512 ? 2 : 3) + (XBF16 ? 1 : 0);
 
 template <int G, int NV, bool XBF16, bool WIDE, bool CKPT>
-__global__ void __launch_bounds__(kCtaThreads<G>) k_norm_bwd(NormBwdArgs a, bool pwide) {
+__global__ void __launch_bounds__(kCtaThreads<G>, kCtaThreads<G> == 512 ? 1 : 2) k_norm_bwd(NormBwdArgs a, bool pwide) {
   __shared__ float red[2][64];
-  extern __shared__ float cols_sm[];  // [2][cols], only where a CTA holds several groups
-  constexpr int kGroups = kCtaThreads<G> / G;
+  extern __shared__ __align__(16) uint8_t ring[];  // the stages; after the rows, [2][cols] floats
+  constexpr int T = kCtaThreads<G>, kGroups = T / G, kStages = kBwdStages<G, XBF16>;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
-  float dg[NV][8], db[NV][8];
+  const int64_t step = int64_t(gridDim.x) * kGroups, first = int64_t(blockIdx.x) * kGroups + grp;
+  const int pieces = bwd_pieces<NV>(a.y_bf16, XBF16, !CKPT, a.residual != nullptr);
+  const int at_x = NV * (a.y_bf16 ? 1 : 2), at_r = at_x + (CKPT ? 0 : NV * (XBF16 ? 1 : 2));
+  constexpr bool kKeep = WIDE || NV == 1;  // gamma stays in registers
+  float dg[NV][8], db[NV][8], gm[NV][8];
 #pragma unroll
-  for (int e = 0; e < NV; ++e)
+  for (int e = 0; e < NV; ++e) {
+    if constexpr (kKeep) load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, gm[e]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) dg[e][k] = db[e][k] = 0.0f;
-  int turn = 0;
-  for (int64_t row = int64_t(blockIdx.x) * kGroups + grp; row < a.rows; row += int64_t(gridDim.x) * kGroups) {
-    const float rstd = __ldg(a.rstd + row);
-    const float mean = CKPT || a.rms ? 0.0f : __ldg(a.mean + row);
-    const void* dyr = at(a.dy, row * a.lddy, a.y_bf16);
-    float g[NV][8], xh[NV][8];
-    float s[2] = {0.0f, 0.0f};
+  }
+  // Starts the wide copies of a row.
+  const auto copy = [&](int64_t row, int stage) {
+    copy_row<G, NV>(ring, pieces, stage, 0, at(a.dy, row * a.lddy, a.y_bf16), cols, t, a.y_bf16);
+    if constexpr (!CKPT) copy_row<G, NV>(ring, pieces, stage, at_x, at(a.x, row * a.ldx, XBF16), cols, t, XBF16);
+    if (a.residual != nullptr)
+      copy_row<G, NV>(ring, pieces, stage, at_r, at(a.residual, row * a.ldr, XBF16), cols, t, XBF16);
+  };
+  // Loads of a row that go to registers: its statistics, its codes, or all of it.
+  BwdRow<G, NV, XBF16, WIDE, CKPT> nx;
+  const auto load = [&](int64_t row) {
+    nx.rstd = __ldg(a.rstd + row);
+    nx.mean = CKPT || a.rms ? 0.0f : __ldg(a.mean + row);
+    if constexpr (CKPT && WIDE) {
 #pragma unroll
-    for (int e = 0; e < NV; ++e) {
-      if (a.y_bf16)
-        load_vec<G, WIDE, true>(dyr, cols, t, e, g[e]);
-      else
-        load_vec<G, WIDE, false>(dyr, cols, t, e, g[e]);
-      load_xhat<G, WIDE, XBF16, CKPT>(a, row, cols, nb, t, e, mean, rstd, xh[e]);
-      float gm[8];
-      load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, gm);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        dg[e][k] = fmaf(g[e][k], xh[e][k], dg[e][k]);
-        db[e][k] += g[e][k];
-        g[e][k] *= gm[k];
-        s[0] += g[e][k];
-        s[1] = fmaf(g[e][k], xh[e][k], s[1]);
+      for (int e = 0; e < NV; ++e) {
+        const int g = t + G * e;
+        nx.codes[e] = make_uint2(0, 0);
+        nx.scale[e] = 1;
+        if (g * 8 < cols) {
+          nx.codes[e] = __ldg(reinterpret_cast<const uint2*>(a.codes + row * nb * kCkptBlock) + g);
+          nx.scale[e] = __ldg(a.scales + row * nb + g / 4);
+        }
       }
     }
+    if constexpr (!WIDE) {
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        if (a.y_bf16)
+          load_vec<G, WIDE, true>(at(a.dy, row * a.lddy, true), cols, t, e, nx.dy[e]);
+        else
+          load_vec<G, WIDE, false>(at(a.dy, row * a.lddy, false), cols, t, e, nx.dy[e]);
+        if constexpr (CKPT) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int c = col_of<G, WIDE>(t, e, k);
+            nx.x[e][k] = c < cols ? float(__ldg(a.codes + row * nb * kCkptBlock + c)) *
+                                        ckpt_step(__ldg(a.scales + row * nb + c / kCkptBlock))
+                                  : 0.0f;
+          }
+        } else {
+          load_vec<G, WIDE, XBF16>(at(a.x, row * a.ldx, XBF16), cols, t, e, nx.x[e]);
+        }
+      }
+    }
+  };
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (first + i * step < a.rows) copy(first + i * step, i);
+      cp_async_commit();
+    }
+  }
+  if (first < a.rows) load(first);
+  int stage = 0, turn = 0;
+  for (int64_t row = first; row - grp < a.rows; row += step) {
+    const bool live = row < a.rows;
+    float g[NV][8], xh[NV][8];
+    float s[2] = {0.0f, 0.0f};
+    const float rstd = live ? nx.rstd : 0.0f, mean = nx.mean;
+    if constexpr (WIDE) {
+      const int64_t ahead = row + (kStages - 1) * step;
+      if (ahead < a.rows) copy(ahead, stage == 0 ? kStages - 1 : stage - 1);
+      cp_async_commit();
+      cp_async_wait<kStages - 1>();
+    }
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      if (live) {
+        if constexpr (WIDE) {
+          copied_vec<G, NV>(ring, pieces, stage, 0, at(a.dy, row * a.lddy, a.y_bf16), cols, t, e, a.y_bf16, g[e]);
+          if constexpr (CKPT) {
+            const float st = ckpt_step(nx.scale[e]);
+            ckpt_unpack4(nx.codes[e].x, st, xh[e]);
+            ckpt_unpack4(nx.codes[e].y, st, xh[e] + 4);
+          } else {
+            copied_vec<G, NV>(ring, pieces, stage, at_x, at(a.x, row * a.ldx, XBF16), cols, t, e, XBF16, xh[e]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) g[e][k] = nx.dy[e][k], xh[e][k] = nx.x[e][k];
+        }
+        if constexpr (!kKeep) load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, gm[e]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if constexpr (!CKPT) xh[e][k] = (xh[e][k] - mean) * rstd;
+          // past the last column (a bad block's padding reads back as NaN)
+          if (col_of<G, WIDE>(t, e, k) >= cols) xh[e][k] = 0.0f;
+          dg[e][k] = fmaf(g[e][k], xh[e][k], dg[e][k]);
+          db[e][k] += g[e][k];
+          g[e][k] *= gm[e][k];
+          s[0] += g[e][k];
+          s[1] = fmaf(g[e][k], xh[e][k], s[1]);
+        }
+      }
+    }
+    if (row + step < a.rows) load(row + step);
     group_sum<G>(s, red[turn]);
     turn ^= 1;
     const float c1 = a.rms ? 0.0f : s[0] / float(cols), c2 = s[1] / float(cols);
-    void* dxr = at(a.dx, row * a.lddx, XBF16);
+    if (live) {
+      void* dxr = at(a.dx, row * a.lddx, XBF16);
 #pragma unroll
-    for (int e = 0; e < NV; ++e) {
-      if (col_of<G, WIDE>(t, e, 0) >= cols) continue;
-      float r[8];
-      if (a.residual != nullptr) {
-        load_vec<G, WIDE, XBF16, true>(at(a.residual, row * a.ldr, XBF16), cols, t, e, r);
-      } else {
+      for (int e = 0; e < NV; ++e) {
+        if (col_of<G, WIDE>(t, e, 0) >= cols) continue;
+        float r[8];
+        if (a.residual != nullptr) {
+          const void* rr = at(a.residual, row * a.ldr, XBF16);
+          if constexpr (WIDE)
+            copied_vec<G, NV, true>(ring, pieces, stage, at_r, rr, cols, t, e, XBF16, r);
+          else
+            load_vec<G, WIDE, XBF16, true>(rr, cols, t, e, r);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) r[k] = 0.0f;
+          for (int k = 0; k < 8; ++k) r[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[k] = fmaf(rstd, fmaf(-xh[e][k], c2, g[e][k] - c1), r[k]);
+        store_vec<G, WIDE>(dxr, cols, t, e, XBF16, r);
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] = fmaf(rstd, fmaf(-xh[e][k], c2, g[e][k] - c1), r[k]);
-      store_vec<G, WIDE>(dxr, cols, t, e, XBF16, r);
     }
+    if (++stage == kStages) stage = 0;
   }
   if (a.partials == nullptr) return;
   float* out = a.partials + int64_t(blockIdx.x) * 2 * cols;
@@ -336,8 +531,11 @@ __global__ void __launch_bounds__(kCtaThreads<G>) k_norm_bwd(NormBwdArgs a, bool
         if (c < cols) out[c] = dg[e][k], out[cols + c] = db[e][k];
       }
   } else {
-    // the CTA's groups add their sums one after another
+    // the CTA's groups add their sums one after another, where the stages were
+    float* sum = reinterpret_cast<float*>(ring);
+    cp_async_wait<0>();
     for (int w = 0; w < kGroups; ++w) {
+      __syncthreads();
       if (grp == w) {
 #pragma unroll
         for (int e = 0; e < NV; ++e)
@@ -345,14 +543,14 @@ __global__ void __launch_bounds__(kCtaThreads<G>) k_norm_bwd(NormBwdArgs a, bool
           for (int k = 0; k < 8; ++k) {
             const int c = col_of<G, WIDE>(t, e, k);
             if (c < cols) {
-              cols_sm[c] = (w ? cols_sm[c] : 0.0f) + dg[e][k];
-              cols_sm[cols + c] = (w ? cols_sm[cols + c] : 0.0f) + db[e][k];
+              sum[c] = (w ? sum[c] : 0.0f) + dg[e][k];
+              sum[cols + c] = (w ? sum[cols + c] : 0.0f) + db[e][k];
             }
           }
       }
-      __syncthreads();
     }
-    for (int c = threadIdx.x; c < 2 * cols; c += kCtaThreads<G>) out[c] = cols_sm[c];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * cols; c += T) out[c] = sum[c];
   }
 }
 
@@ -440,35 +638,42 @@ bool wide_rows(const void* p, int64_t ld, int64_t rows, int bf16) {
 }
 bool wide_vec(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+template <int G, int NV, bool XBF16, bool WIDE>
+cudaError_t fwd_launch(const NormFwdArgs& a, bool pwide, cudaStream_t s) {
+  constexpr int T = kCtaThreads<G>;
+  constexpr size_t sm = WIDE ? size_t(kFwdRing<NV, XBF16>) * kFwdPieces<G, NV, XBF16> * T * 16 : 0;
+  static LayerGrid cache;
+  int cap = 0;
+  const cudaError_t e = layer_grid(cache, reinterpret_cast<const void*>(&k_norm_fwd<G, NV, XBF16, WIDE>), T, sm, sm, &cap);
+  if (e != cudaSuccess) return e;
+  const int64_t want = (a.rows + T / G - 1) / (T / G);
+  k_norm_fwd<G, NV, XBF16, WIDE><<<unsigned(want < cap ? want : cap), T, sm, s>>>(a, pwide);
+  return cudaGetLastError();
+}
+
 template <int G, int NV>
 cudaError_t fwd(const NormFwdArgs& a, bool wide, bool pwide, cudaStream_t s) {
-  constexpr int T = kCtaThreads<G>;
-  const unsigned grid = unsigned((a.rows + T / G - 1) / (T / G));
-  if (a.x_bf16)
-    (wide ? k_norm_fwd<G, NV, true, true> : k_norm_fwd<G, NV, true, false>)<<<grid, T, 0, s>>>(a, pwide);
-  else
-    (wide ? k_norm_fwd<G, NV, false, true> : k_norm_fwd<G, NV, false, false>)<<<grid, T, 0, s>>>(a, pwide);
-  return cudaGetLastError();
+  if (a.x_bf16) return wide ? fwd_launch<G, NV, true, true>(a, pwide, s) : fwd_launch<G, NV, true, false>(a, pwide, s);
+  return wide ? fwd_launch<G, NV, false, true>(a, pwide, s) : fwd_launch<G, NV, false, false>(a, pwide, s);
 }
 
 template <int G, int NV, bool XBF16, bool WIDE, bool CKPT>
 cudaError_t bwd_launch(const NormBwdArgs& a, bool pwide, int* parts, cudaStream_t s) {
   constexpr int T = kCtaThreads<G>, groups = T / G;
-  const size_t sm = groups > 1 ? size_t(a.cols) * 8 : 0;
-  static std::atomic<int> known[64];
-  int dev = 0, cap = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const auto bytes = [](int y_bf16, bool residual) {
+    // the stages, or where several groups join their sums of at most G * NV * 8 columns
+    return WIDE ? size_t(kBwdStages<G, XBF16>) * bwd_pieces<NV>(y_bf16, XBF16, !CKPT, residual) * T * 16
+                : size_t(groups > 1 ? G * NV * 64 : 0);
+  };
+  static_assert(!WIDE || groups == 1 || kBwdStages<G, XBF16> * T * 16 >= G * 64, "the sums fit where the stages were");
+  const size_t sm = bytes(a.y_bf16, a.residual != nullptr);
+  static LayerGrid cache[4];  // occupancy depends on the stage's size, of which there are four
+  int cap = 0;
+  const cudaError_t e = layer_grid(cache[(a.y_bf16 ? 1 : 0) + (a.residual != nullptr ? 2 : 0)],
+                                   reinterpret_cast<const void*>(&k_norm_bwd<G, NV, XBF16, WIDE, CKPT>), T, sm,
+                                   bytes(0, true), &cap);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || (cap = known[dev].load(std::memory_order_relaxed)) == 0) {
-    int sms = 0, per = 0;
-    if ((e = sm_count(&sms)) != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k_norm_bwd<G, NV, XBF16, WIDE, CKPT>, T,
-                                                      groups > 1 ? size_t(G) * NV * 64 : 0);
-    if (e != cudaSuccess) return e;
-    cap = sms * (per < 1 ? 1 : per);
-    if (cap > kNormPartials) cap = kNormPartials;
-    if (dev < 64) known[dev].store(cap, std::memory_order_relaxed);
-  }
+  if (cap > kNormPartials) cap = kNormPartials;
   const int64_t want = (a.rows + groups - 1) / groups;
   *parts = int(want < cap ? want : cap);
   k_norm_bwd<G, NV, XBF16, WIDE, CKPT><<<*parts, T, sm, s>>>(a, pwide);
@@ -493,9 +698,9 @@ cudaError_t launch_norm_forward(const NormFwdArgs& a, cudaStream_t s) {
   const bool pwide = wide_vec(a.gamma) && wide_vec(a.beta);
   const int64_t pitch = (a.cols + kCkptBlock - 1) / kCkptBlock * kCkptBlock;
   if (pitch <= 256) return fwd<32, 1>(a, wide, pwide, s);
-  if (pitch <= 512) return fwd<32, 2>(a, wide, pwide, s);
-  if (pitch <= 1024) return fwd<32, 4>(a, wide, pwide, s);
-  if (pitch <= 2048) return fwd<128, 2>(a, wide, pwide, s);
+  if (pitch <= 512) return fwd<64, 1>(a, wide, pwide, s);
+  if (pitch <= 1024) return fwd<128, 1>(a, wide, pwide, s);
+  if (pitch <= 2048) return fwd<256, 1>(a, wide, pwide, s);
   if (pitch <= 4096) return fwd<256, 2>(a, wide, pwide, s);
   if (pitch <= 8192) return fwd<512, 2>(a, wide, pwide, s);
   if (pitch <= 16384) return fwd<512, 4>(a, wide, pwide, s);
@@ -513,9 +718,9 @@ cudaError_t launch_norm_backward(const NormBwdArgs& a, cudaStream_t s) {
     const bool pwide = wide_vec(a.gamma);
     const int64_t pitch = (a.cols + kCkptBlock - 1) / kCkptBlock * kCkptBlock;
     if (pitch <= 256) e = bwd<32, 1>(a, wide, pwide, &parts, s);
-    else if (pitch <= 512) e = bwd<32, 2>(a, wide, pwide, &parts, s);
-    else if (pitch <= 1024) e = bwd<32, 4>(a, wide, pwide, &parts, s);
-    else if (pitch <= 2048) e = bwd<128, 2>(a, wide, pwide, &parts, s);
+    else if (pitch <= 512) e = bwd<64, 1>(a, wide, pwide, &parts, s);
+    else if (pitch <= 1024) e = bwd<128, 1>(a, wide, pwide, &parts, s);
+    else if (pitch <= 2048) e = bwd<256, 1>(a, wide, pwide, &parts, s);
     else if (pitch <= 4096) e = bwd<256, 2>(a, wide, pwide, &parts, s);
     else if (pitch <= 8192) e = bwd<512, 2>(a, wide, pwide, &parts, s);
     else {

@@ -10,6 +10,7 @@ fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -159,7 +160,10 @@ def _addr(x) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
+        if not torch.cuda.is_available():
+            return 0
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
+        return raw(torch.cuda.current_device()) if raw is not None else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -252,75 +256,101 @@ def loco_shard_range(n: int, block: int, W: int, j: int) -> tuple[int, int]:
 # two-dimensional tensors whose rows are contiguous (any row pitch).
 # --------------------------------------------------------------------------
 
-def _dtype(t, name: str) -> int:
+_DTYPES: dict = {}  # torch.dtype -> loco_dtype, filled on first use (torch is imported only then)
+
+
+def _dtypes():
     import torch
-    if t.dtype == torch.bfloat16:
-        return LOCO_BF16
-    if t.dtype == torch.float32:
-        return LOCO_F32
-    raise ValueError(f"{name}: dtype {t.dtype} is not supported (float32 or bfloat16)")
+    _DTYPES.update({torch.float32: LOCO_F32, torch.bfloat16: LOCO_BF16})
+    return _DTYPES
 
 
-def _mat(t, name: str, shape=None):
-    """(address, row pitch) of a matrix; (0, 0) for None."""
+def _dtype(t, name: str) -> int:
+    d = (_DTYPES or _dtypes()).get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name}: dtype {t.dtype} is not supported (float32 or bfloat16)")
+    return d
+
+
+def _one_dtype(name: str, *tensors) -> int:
+    """The one dtype of the tensors that are given (LOCO_F32 where none is)."""
+    first = None
+    for t in tensors:
+        if t is not None:
+            if first is None:
+                first = t
+            elif t.dtype != first.dtype:
+                raise ValueError(f"{name} must have one dtype (got {first.dtype} and {t.dtype})")
+    return LOCO_F32 if first is None else _dtype(first, name)
+
+
+def _mat(t, name: str, rows: int, cols: int):
+    """(address, row pitch) of a [rows, cols] matrix; (0, 0) for None."""
     if t is None:
         return 0, 0
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {(rows, cols)} (got {tuple(t.shape)})")
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), (cols if rows <= 1 and pitch < cols else pitch)
+
+
+def _dims(t, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must be two-dimensional (got {t.dim()} dimensions)")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+    return t.shape
 
 
-def _vec(t, name: str, count: int, dtype=None) -> int:
+def _vec(t, name: str, count: int) -> int:
     """Address of a contiguous vector of count elements; 0 for None."""
     if t is None:
         return 0
-    if t.dim() != 1 or t.numel() != count:
-        raise ValueError(f"{name} must be a vector of {count} (got {tuple(t.shape)})")
-    if count > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != (count,) or (count > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {count} (got {tuple(t.shape)})")
     return t.data_ptr()
 
 
 def _f32(t, name: str, count: int) -> int:
-    import torch
-    return _vec(t, name, count, torch.float32)
+    if t is not None and (_DTYPES or _dtypes()).get(t.dtype) != LOCO_F32:
+        raise ValueError(f"{name} must be torch.float32 (got {t.dtype})")
+    return _vec(t, name, count)
 
 
 def _ckpt(codes, scales, rows: int, cols: int):
     """Addresses of a checkpoint of [rows, cols]: int8 codes and uint8 scales of the sizes the library states."""
+    if codes is None and scales is None:
+        return 0, 0
     import torch
-    for t, name, dtype, size in ((codes, "codes", torch.int8, lib.loco_ckpt_code_bytes(rows, cols)),
-                                 (scales, "scales", torch.uint8, lib.loco_ckpt_scale_bytes(rows, cols))):
+    nb = -(-cols // LOCO_CKPT_BLOCK)
+    for t, name, dtype, size in ((codes, "codes", torch.int8, rows * nb * LOCO_CKPT_BLOCK),
+                                 (scales, "scales", torch.uint8, rows * nb)):
         if t is not None and (t.dtype != dtype or t.numel() != size or not t.is_contiguous()):
             raise ValueError(f"{name} must be {size} contiguous {dtype} (got {t.numel()} {t.dtype})")
     return (0 if codes is None else codes.data_ptr()), (0 if scales is None else scales.data_ptr())
 
 
-def _same_dtype(name: str, *tensors):
-    """The one dtype of the tensors that are given (LOCO_F32 where none is)."""
-    kinds = {t.dtype for t in tensors if t is not None}
-    if len(kinds) > 1:
-        raise ValueError(f"{name} must have one dtype (got {sorted(map(str, kinds))})")
-    return next((_dtype(t, name) for t in tensors if t is not None), LOCO_F32)
-
-
 def _bf16(t, name: str):
-    import torch
-    if t is not None and t.dtype != torch.bfloat16:
+    if t is not None and (_DTYPES or _dtypes()).get(t.dtype) != LOCO_BF16:
         raise ValueError(f"{name}: dtype {t.dtype} is not supported (bfloat16)")
 
 
 def _workspace(t):
-    if t is not None and not t.is_contiguous():
+    if t is None:
+        return 0, 0
+    if not t.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return (0, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_ref(*fields):
+    return ctypes.byref(loco_norm_config(*fields))
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_ref(*fields):
+    return ctypes.byref(loco_linear_config(*fields))
 
 
 def loco_ckpt_code_bytes(rows: int, cols: int) -> int:
@@ -333,34 +363,32 @@ def loco_ckpt_scale_bytes(rows: int, cols: int) -> int:
 
 def loco_ckpt_encode(x, codes, scales, *, stream=None):
     """8-bit checkpoint of x [rows, cols]: int8 codes [rows, nb*32], uint8 scales [rows, nb], nb = ceil(cols/32)."""
-    px, ldx = _mat(x, "x")
-    rows, cols = x.shape
+    rows, cols = _dims(x, "x")
+    px, ldx = _mat(x, "x", rows, cols)
     pc, ps = _ckpt(codes, scales, rows, cols)
     _check(lib.loco_ckpt_encode(px, _dtype(x, "x"), ldx, rows, cols, pc, ps, _stream(stream)))
 
 
 def loco_ckpt_decode(codes, scales, out, *, act: int = LOCO_ACT_NONE, gamma=None, beta=None, stream=None):
     """out [rows, cols] = act(values of the checkpoint * gamma + beta)."""
-    po, ldo = _mat(out, "out")
-    rows, cols = out.shape
+    rows, cols = _dims(out, "out")
+    po, ldo = _mat(out, "out", rows, cols)
     pc, ps = _ckpt(codes, scales, rows, cols)
     _check(lib.loco_ckpt_decode(pc, ps, rows, cols, act, _vec(gamma, "gamma", cols), _vec(beta, "beta", cols),
-                                _same_dtype("gamma and beta", gamma, beta), po, _dtype(out, "out"), ldo,
+                                _one_dtype("gamma and beta", gamma, beta), po, _dtype(out, "out"), ldo,
                                 _stream(stream)))
 
 
 def loco_norm_forward(cfg: loco_norm_config, x, gamma, beta, y, *, mean=None, rstd=None, codes=None, scales=None,
                       stream=None):
     """y = norm(x) * gamma + beta per row; optionally its statistics and an 8-bit checkpoint of the normalised rows."""
-    rows, cols = x.shape
-    px, ldx = _mat(x, "x")
-    py, ldy = _mat(y, "y", (rows, cols))
+    rows, cols = _dims(x, "x")
+    px, ldx = _mat(x, "x", rows, cols)
+    py, ldy = _mat(y, "y", rows, cols)
     pc, ps = _ckpt(codes, scales, rows, cols)
-    c = loco_norm_config(cfg.kind, cfg.eps, _dtype(x, "x"), _dtype(y, "y"),
-                         _same_dtype("gamma and beta", gamma, beta), LOCO_F32)
-    _check(lib.loco_norm_forward(ctypes.byref(c), px, ldx, rows, cols, _vec(gamma, "gamma", cols),
-                                 _vec(beta, "beta", cols), py, ldy, _f32(mean, "mean", rows),
-                                 _f32(rstd, "rstd", rows), pc, ps, _stream(stream)))
+    c = _norm_ref(cfg.kind, cfg.eps, _dtype(x, "x"), _dtype(y, "y"), _one_dtype("gamma and beta", gamma, beta), LOCO_F32)
+    _check(lib.loco_norm_forward(c, px, ldx, rows, cols, _vec(gamma, "gamma", cols), _vec(beta, "beta", cols), py, ldy,
+                                 _f32(mean, "mean", rows), _f32(rstd, "rstd", rows), pc, ps, _stream(stream)))
 
 
 def loco_norm_workspace_bytes(rows: int, cols: int) -> int:
@@ -370,51 +398,51 @@ def loco_norm_workspace_bytes(rows: int, cols: int) -> int:
 def loco_norm_backward(cfg: loco_norm_config, dy, gamma, rstd, dx, *, x=None, mean=None, codes=None, scales=None,
                        residual=None, dgamma=None, dbeta=None, workspace=None, stream=None):
     """Gradients of loco_norm_forward, from x or from the checkpoint of the normalised rows."""
-    rows, cols = dy.shape
-    pdy, lddy = _mat(dy, "dy")
-    px, ldx = _mat(x, "x", (rows, cols))
-    pr, ldr = _mat(residual, "residual", (rows, cols))
-    pdx, lddx = _mat(dx, "dx", (rows, cols))
+    rows, cols = _dims(dy, "dy")
+    pdy, lddy = _mat(dy, "dy", rows, cols)
+    px, ldx = _mat(x, "x", rows, cols)
+    pr, ldr = _mat(residual, "residual", rows, cols)
+    pdx, lddx = _mat(dx, "dx", rows, cols)
     pc, ps = _ckpt(codes, scales, rows, cols)
     pw, nw = _workspace(workspace)
-    c = loco_norm_config(cfg.kind, cfg.eps, _same_dtype("x, residual and dx", x, residual, dx), _dtype(dy, "dy"),
-                         _same_dtype("gamma", gamma), _same_dtype("dgamma and dbeta", dgamma, dbeta))
-    _check(lib.loco_norm_backward(ctypes.byref(c), pdy, lddy, px, ldx, pc, ps, _f32(mean, "mean", rows),
-                                  _f32(rstd, "rstd", rows), rows, cols, _vec(gamma, "gamma", cols), pr, ldr, pdx,
-                                  lddx, _vec(dgamma, "dgamma", cols), _vec(dbeta, "dbeta", cols), pw, nw,
-                                  _stream(stream)))
+    c = _norm_ref(cfg.kind, cfg.eps, _one_dtype("x, residual and dx", x, residual, dx), _dtype(dy, "dy"),
+                  _one_dtype("gamma", gamma), _one_dtype("dgamma and dbeta", dgamma, dbeta))
+    _check(lib.loco_norm_backward(c, pdy, lddy, px, ldx, pc, ps, _f32(mean, "mean", rows), _f32(rstd, "rstd", rows),
+                                  rows, cols, _vec(gamma, "gamma", cols), pr, ldr, pdx, lddx,
+                                  _vec(dgamma, "dgamma", cols), _vec(dbeta, "dbeta", cols), pw, nw, _stream(stream)))
 
 
 def loco_linear_forward(x, w, y, *, act: int = LOCO_ACT_NONE, bias=None, residual=None, codes=None, scales=None,
                         stream=None):
     """y = act(x w^T + bias) + residual; optionally an 8-bit checkpoint of the pre-activation.  x, w bf16."""
-    (T, K), N = x.shape, w.shape[0]
+    T, K = _dims(x, "x")
+    N, _ = _dims(w, "w")
     _bf16(x, "x")
     _bf16(w, "w")
-    px, ldx = _mat(x, "x")
-    pw, ldw = _mat(w, "w", (N, K))
-    pr, ldr = _mat(residual, "residual", (T, N))
-    py, ldy = _mat(y, "y", (T, N))
+    px, ldx = _mat(x, "x", T, K)
+    pw, ldw = _mat(w, "w", N, K)
+    pr, ldr = _mat(residual, "residual", T, N)
+    py, ldy = _mat(y, "y", T, N)
     pc, ps = _ckpt(codes, scales, T, N)
-    c = loco_linear_config(act, _same_dtype("y and residual", y, residual), _same_dtype("bias", bias))
-    _check(lib.loco_linear_forward(ctypes.byref(c), px, ldx, pw, ldw, _vec(bias, "bias", N), pr, ldr, T, N, K, py, ldy,
-                                   pc, ps, _stream(stream)))
+    c = _linear_ref(act, _one_dtype("y and residual", y, residual), _one_dtype("bias", bias))
+    _check(lib.loco_linear_forward(c, px, ldx, pw, ldw, _vec(bias, "bias", N), pr, ldr, T, N, K, py, ldy, pc, ps,
+                                   _stream(stream)))
 
 
 def loco_linear_backward_input(dy, w, dx, *, act: int = LOCO_ACT_NONE, codes=None, scales=None, residual=None,
                                stream=None):
     """dx = (dy w) * act'(z) + residual, z from the checkpoint of the layer below's pre-activation.  dy, w bf16."""
-    (T, N), K = dy.shape, w.shape[1]
+    T, N = _dims(dy, "dy")
+    _, K = _dims(w, "w")
     _bf16(dy, "dy")
     _bf16(w, "w")
-    pdy, lddy = _mat(dy, "dy")
-    pw, ldw = _mat(w, "w", (N, K))
-    pr, ldr = _mat(residual, "residual", (T, K))
-    pdx, lddx = _mat(dx, "dx", (T, K))
+    pdy, lddy = _mat(dy, "dy", T, N)
+    pw, ldw = _mat(w, "w", N, K)
+    pr, ldr = _mat(residual, "residual", T, K)
+    pdx, lddx = _mat(dx, "dx", T, K)
     pc, ps = _ckpt(codes, scales, T, K)
-    c = loco_linear_config(act, _same_dtype("dx and residual", dx, residual), LOCO_F32)
-    _check(lib.loco_linear_backward_input(ctypes.byref(c), pdy, lddy, pw, ldw, pc, ps, pr, ldr, T, N, K, pdx, lddx,
-                                          _stream(stream)))
+    c = _linear_ref(act, _one_dtype("dx and residual", dx, residual), LOCO_F32)
+    _check(lib.loco_linear_backward_input(c, pdy, lddy, pw, ldw, pc, ps, pr, ldr, T, N, K, pdx, lddx, _stream(stream)))
 
 
 def loco_linear_workspace_bytes(N: int) -> int:
@@ -424,18 +452,18 @@ def loco_linear_workspace_bytes(N: int) -> int:
 def loco_linear_backward_weight(dy, dw, *, x=None, codes=None, scales=None, gamma=None, beta=None, db=None,
                                 workspace=None, stream=None):
     """dw = dy^T x, db = column sums of dy; x [T, K] bf16, or gamma * (values of a checkpoint) + beta."""
-    (T, N), K = dy.shape, dw.shape[1]
+    T, N = _dims(dy, "dy")
+    _, K = _dims(dw, "dw")
     _bf16(dy, "dy")
     _bf16(x, "x")
-    pdy, lddy = _mat(dy, "dy")
-    px, ldx = _mat(x, "x", (T, K))
-    pdw, lddw = _mat(dw, "dw", (N, K))
+    pdy, lddy = _mat(dy, "dy", T, N)
+    px, ldx = _mat(x, "x", T, K)
+    pdw, lddw = _mat(dw, "dw", N, K)
     pc, ps = _ckpt(codes, scales, T, K)
     pw, nw = _workspace(workspace)
-    c = loco_linear_config(LOCO_ACT_NONE, _same_dtype("dw and db", dw, db), _same_dtype("gamma and beta", gamma, beta))
-    _check(lib.loco_linear_backward_weight(ctypes.byref(c), pdy, lddy, px, ldx, pc, ps, _vec(gamma, "gamma", K),
-                                           _vec(beta, "beta", K), T, N, K, pdw, lddw, _vec(db, "db", N), pw, nw,
-                                           _stream(stream)))
+    c = _linear_ref(LOCO_ACT_NONE, _one_dtype("dw and db", dw, db), _one_dtype("gamma and beta", gamma, beta))
+    _check(lib.loco_linear_backward_weight(c, pdy, lddy, px, ldx, pc, ps, _vec(gamma, "gamma", K), _vec(beta, "beta", K),
+                                           T, N, K, pdw, lddw, _vec(db, "db", N), pw, nw, _stream(stream)))
 
 
 def loco_linear_timeouts() -> int:
