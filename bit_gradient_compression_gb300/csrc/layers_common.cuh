@@ -11,11 +11,82 @@
 
 namespace loco {
 
+// Division of indexes below 2^31 by one divisor: n / d = (n * m) >> (31 + l) with 2^(l-1) < d <= 2^l
+// and m = ceil(2^(31+l) / d) < 2^32, exact because n * (m * d - 2^(31+l)) < 2^31 * 2^l.  Larger
+// ranges divide in 64 bits.
+struct Divisor {
+  uint32_t m;
+  int shift;
+  bool wide;
+  int64_t d;
+};
+inline Divisor make_divisor(int64_t d, int64_t range) {
+  Divisor v{0, 0, range > 0x7FFFFFFF, d};
+  if (!v.wide) {
+    int l = 0;
+    while ((int64_t(1) << l) < d) ++l;
+    v.shift = 31 + l;
+    v.m = uint32_t(((uint64_t(1) << v.shift) + uint64_t(d) - 1) / uint64_t(d));
+  }
+  return v;
+}
+__device__ __forceinline__ int64_t divide(int64_t n, const Divisor& v) {
+  return v.wide ? n / v.d : int64_t((uint64_t(uint32_t(n)) * v.m) >> v.shift);
+}
+
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Pairs of fp32 values in one register pair: one instruction for two sums, products or both.
+struct Pair {
+  unsigned long long u;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.u) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ float2 halves(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p.u));
+  return v;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+  return r;
+}
+__device__ __forceinline__ Pair widen(uint32_t bf16x2) {
+  return pair(__uint_as_float(bf16x2 << 16), __uint_as_float(bf16x2 & 0xFFFF0000u));
+}
+// Eight values as four pairs.
+__device__ __forceinline__ void widen8(uint4 w, Pair v[4]) {
+  v[0] = widen(w.x), v[1] = widen(w.y), v[2] = widen(w.z), v[3] = widen(w.w);
+}
+__device__ __forceinline__ void pairs8(const float f[8], Pair v[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = pair(f[2 * k], f[2 * k + 1]);
+}
+__device__ __forceinline__ void floats8(const Pair v[4], float f[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 h = halves(v[k]);
+    f[2 * k] = h.x, f[2 * k + 1] = h.y;
+  }
 }
 
 // One element of an array of bf16 or fp32 (a uniform branch on the type).
@@ -114,6 +185,17 @@ __device__ __forceinline__ void ckpt_unpack4(uint32_t w, float step, float v[4])
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     v[k] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 | k)) - 8388736.0f) * step;
+}
+
+// Four codes of a word under a scale byte as two pairs.
+__device__ __forceinline__ void ckpt_pairs4(uint32_t w, uint32_t scale, Pair v[2]) {
+  const float st = ckpt_step(scale);
+  const Pair off = pair(-8388736.0f, -8388736.0f), st2 = pair(st, st);
+  const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    v[k] = (pair(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 | 2 * k)),
+                 __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 | 2 * k))) + off) * st2;
 }
 
 // ---------------------------------------------------------------------------

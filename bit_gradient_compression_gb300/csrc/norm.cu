@@ -37,7 +37,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 template <int G>
-constexpr int kCtaThreads = G < 256 ? 256 : G;
+constexpr int kCtaThreads = G < 128 ? 128 : G;
 
 // Sums of N values over the group's G threads, the same in all of them; every thread of the CTA
 // takes part.  `red` holds 32 floats per value, and consecutive calls of a loop alternate between
@@ -64,92 +64,12 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red) {
   }
 }
 
-// Column of element k of a thread's vector e.
-template <int G, bool WIDE>
-__device__ __forceinline__ int col_of(int t, int e, int k) {
-  return WIDE ? (t + G * e) * 8 + k : t + G * (e * 8 + k);
-}
-
-// Eight elements of a row held by one thread, 0 past the last column.  RW: the kernel may write the row.
-template <int G, bool WIDE, bool BF16, bool RW = false>
-__device__ __forceinline__ void load_vec(const void* row, int cols, int t, int e, float v[8]) {
-  const int c0 = col_of<G, WIDE>(t, e, 0);
-  if (WIDE && c0 + 8 <= cols) {
-    load8<RW>(row, c0, BF16, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = col_of<G, WIDE>(t, e, k);
-      v[k] = c < cols ? (RW ? load_elem_rw(row, c, BF16) : load_elem(row, c, BF16)) : 0.0f;
-    }
-  }
-}
-template <int G, bool WIDE>
-__device__ __forceinline__ void store_vec(void* row, int cols, int t, int e, int bf16, const float v[8]) {
-  const int c0 = col_of<G, WIDE>(t, e, 0);
-  if (WIDE && c0 + 8 <= cols) {
-    store8(row, c0, bf16, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = col_of<G, WIDE>(t, e, k);
-      if (c < cols) store_elem(row, c, bf16, v[k]);
-    }
-  }
-}
-// A parameter vector's elements; `wide`: it is 16-byte aligned.
-template <int G, bool WIDE>
-__device__ __forceinline__ void load_param(const void* p, int cols, int t, int e, int bf16, bool wide, float none,
-                                           float v[8]) {
-  const int c0 = col_of<G, WIDE>(t, e, 0);
-  if (p == nullptr) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = none;
-  } else if (WIDE && wide && c0 + 8 <= cols) {
-    load8(p, c0, bf16, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = col_of<G, WIDE>(t, e, k);
-      v[k] = c < cols ? load_elem(p, c, bf16) : none;
-    }
-  }
-}
-
-__device__ __forceinline__ const void* at(const void* p, int64_t i, int bf16) {
+__device__ __forceinline__ const char* at(const void* p, int64_t i, int bf16) {
   return static_cast<const char*>(p) + i * (bf16 ? 2 : 4);
 }
-__device__ __forceinline__ void* at(void* p, int64_t i, int bf16) { return static_cast<char*>(p) + i * (bf16 ? 2 : 4); }
+__device__ __forceinline__ char* at(void* p, int64_t i, int bf16) { return static_cast<char*>(p) + i * (bf16 ? 2 : 4); }
 
-// Codes and scales of the vector's 8 values (0 past cols); every lane of the warp takes part.
-template <int G, bool WIDE>
-__device__ __forceinline__ void store_codes(const NormFwdArgs& a, int64_t row, int t, int e, int nb, const float v[8]) {
-  if constexpr (WIDE) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, mag_bits(v[k]));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const int g = t + G * e;
-    if (g < nb * 4) {
-      const uint32_t sc = ckpt_scale(m);
-      reinterpret_cast<uint2*>(a.codes + row * nb * kCkptBlock)[g] = ckpt_pack8(v, m);
-      if ((g & 3) == 0) a.scales[row * nb + g / 4] = uint8_t(sc);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = col_of<G, WIDE>(t, e, k);
-      const uint32_t sc = ckpt_scale(__reduce_max_sync(0xFFFFFFFFu, mag_bits(v[k])));
-      if (c / kCkptBlock < nb) {
-        a.codes[row * nb * kCkptBlock + c] = int8_t(ckpt_code(v[k], ckpt_inv_step(sc)));
-        if ((c & 31) == 0) a.scales[row * nb + c / kCkptBlock] = uint8_t(sc);
-      }
-    }
-  }
-}
-
-// ---- the next rows' pieces in shared memory (WIDE)
+// ---------------------------------------------------------------------------------------- WIDE: 16-byte pieces
 
 // A thread's 16-byte pieces: piece i of stage s at ring + ((s * pieces + i) * threads + thread) * 16.
 template <int T>
@@ -158,133 +78,149 @@ __device__ __forceinline__ uint4* piece(uint8_t* ring, int pieces, int stage, in
 }
 // Starts the copy of a thread's whole vectors of one row: NV pieces (bf16) or 2 NV (fp32) from piece `first`.
 template <int G, int NV>
-__device__ __forceinline__ void copy_row(uint8_t* ring, int pieces, int stage, int first, const void* row, int cols, int t,
+__device__ __forceinline__ void copy_row(uint8_t* ring, int pieces, int stage, int first, const char* row, int cols, int t,
                                          int bf16) {
   constexpr int T = kCtaThreads<G>;
 #pragma unroll
   for (int e = 0; e < NV; ++e) {
     const int c0 = (t + G * e) * 8;
     if (c0 + 8 > cols) continue;
-    const char* q = static_cast<const char*>(row) + int64_t(c0) * (bf16 ? 2 : 4);
     if (bf16) {
-      cp_async16(piece<T>(ring, pieces, stage, first + e), q);
+      cp_async16(piece<T>(ring, pieces, stage, first + e), row + c0 * 2);
     } else {
-      cp_async16(piece<T>(ring, pieces, stage, first + 2 * e), q);
-      cp_async16(piece<T>(ring, pieces, stage, first + 2 * e + 1), q + 16);
+      cp_async16(piece<T>(ring, pieces, stage, first + 2 * e), row + int64_t(c0) * 4);
+      cp_async16(piece<T>(ring, pieces, stage, first + 2 * e + 1), row + int64_t(c0) * 4 + 16);
     }
   }
 }
-__device__ __forceinline__ void widen(uint4 a, float v[8]) {
-  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ Pair bits_pair(uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); }
+// The vector a row ends in, 0 past the end.  (The kernel may write a row that is also its residual.)
+__device__ __forceinline__ void load_last(const char* row, int cols, int c0, int bf16, Pair v[4]) {
+  float f[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) v[2 * k] = __uint_as_float(u[k] << 16), v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+  for (int k = 0; k < 8; ++k) f[k] = c0 + k < cols ? load_elem_rw(row, c0 + k, bf16) : 0.0f;
+  pairs8(f, v);
 }
-// Vector e of the row that was copied; `row` itself serves a vector the row ends in.
-template <int G, int NV, bool RW = false>
-__device__ __forceinline__ void copied_vec(uint8_t* ring, int pieces, int stage, int first, const void* row, int cols,
-                                           int t, int e, int bf16, float v[8]) {
+// Vector e of the row that was copied (it begins inside the row).
+template <int G, int NV>
+__device__ __forceinline__ void copied_vec(uint8_t* ring, int pieces, int stage, int first, const char* row, int cols,
+                                           int t, int e, int bf16, Pair v[4]) {
   constexpr int T = kCtaThreads<G>;
-  if ((t + G * e) * 8 + 8 <= cols) {
-    if (bf16) {
-      widen(*piece<T>(ring, pieces, stage, first + e), v);
-    } else {
-      const uint4 a = *piece<T>(ring, pieces, stage, first + 2 * e), b = *piece<T>(ring, pieces, stage, first + 2 * e + 1);
-      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
-    }
+  const int c0 = (t + G * e) * 8;
+  if (c0 + 8 > cols) {
+    load_last(row, cols, c0, bf16, v);
   } else if (bf16) {
-    load_vec<G, true, true, RW>(row, cols, t, e, v);
+    widen8(*piece<T>(ring, pieces, stage, first + e), v);
   } else {
-    load_vec<G, true, false, RW>(row, cols, t, e, v);
+    const uint4 a = *piece<T>(ring, pieces, stage, first + 2 * e), b = *piece<T>(ring, pieces, stage, first + 2 * e + 1);
+    v[0] = bits_pair(a.x, a.y), v[1] = bits_pair(a.z, a.w), v[2] = bits_pair(b.x, b.y), v[3] = bits_pair(b.z, b.w);
   }
 }
+__device__ __forceinline__ void store_vec(char* row, int cols, int c0, int bf16, const Pair v[4]) {
+  float f[8];
+  floats8(v, f);
+  if (c0 + 8 <= cols) {
+    store8(row, c0, bf16, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c0 + k < cols) store_elem(row, c0 + k, bf16, f[k]);
+  }
+}
+// Eight values of a parameter vector from column c0 on; `wide`: it starts on a 16-byte boundary.
+__device__ __forceinline__ void load_param(const void* p, int cols, int c0, int bf16, bool wide, float none, Pair v[4]) {
+  if (p != nullptr && wide && c0 + 8 <= cols) {
+    if (bf16) {
+      widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c0)), v);
+    } else {
+      float f[8];
+      load8(p, c0, 0, f);
+      pairs8(f, v);
+    }
+  } else {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = p != nullptr && c0 + k < cols ? load_elem(p, c0 + k, bf16) : none;
+    pairs8(f, v);
+  }
+}
+// 0 in the columns past the row's end.
+__device__ __forceinline__ void clear_past(Pair v[4], int cols, int c0) {
+  float f[8];
+  floats8(v, f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (c0 + k >= cols) f[k] = 0.0f;
+  pairs8(f, v);
+}
+
+// Stages: the row at work and the next ones.
+constexpr int kFwdStages = 3;
+template <int NV, bool XBF16>
+constexpr int kFwdPieces = NV * (XBF16 ? 1 : 2);
 
 template <int G, int NV, bool XBF16>
-constexpr int kFwdPieces = NV * (XBF16 ? 1 : 2);
-// Stages: a row of 16384 fp32 columns takes 64 KB of shared memory.
-template <int NV, bool XBF16>
-constexpr int kFwdRing = XBF16 || NV < 4 ? 4 : 3;
-
-template <int G, int NV, bool XBF16, bool WIDE>
-__global__ void __launch_bounds__(kCtaThreads<G>, kCtaThreads<G> == 512 ? 1 : 2) k_norm_fwd(NormFwdArgs a, bool pwide) {
+__global__ void __launch_bounds__(kCtaThreads<G>, 768 / kCtaThreads<G>) k_norm_fwd(NormFwdArgs a, bool pwide) {
   __shared__ float red[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
-  constexpr int kGroups = kCtaThreads<G> / G, kP = kFwdPieces<G, NV, XBF16>, kFwdStages = kFwdRing<NV, XBF16>;
-  constexpr bool kKeep = NV <= 2;  // gamma and beta stay in registers
+  constexpr int kGroups = kCtaThreads<G> / G, kP = kFwdPieces<NV, XBF16>;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const int64_t step = int64_t(gridDim.x) * kGroups, first = int64_t(blockIdx.x) * kGroups + grp;
-  float gm[NV][8], bt[NV][8], nx[NV][8];
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int e = 0; e < NV; ++e) {
-      load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, gm[e]);
-      load_param<G, WIDE>(a.beta, cols, t, e, a.param_bf16, pwide, 0.0f, bt[e]);
-    }
-  }
   const auto x_row = [&](int64_t row) { return at(a.x, row * a.ldx, XBF16); };
-  if constexpr (WIDE) {
 #pragma unroll
-    for (int i = 0; i < kFwdStages - 1; ++i) {
-      const int64_t row = first + i * step;
-      if (row < a.rows) copy_row<G, NV>(ring, kP, i, 0, x_row(row), cols, t, XBF16);
-      cp_async_commit();
-    }
-  } else if (first < a.rows) {
-#pragma unroll
-    for (int e = 0; e < NV; ++e) load_vec<G, WIDE, XBF16>(x_row(first), cols, t, e, nx[e]);
+  for (int i = 0; i < kFwdStages - 1; ++i) {
+    const int64_t row = first + i * step;
+    if (row < a.rows) copy_row<G, NV>(ring, kP, i, 0, x_row(row), cols, t, XBF16);
+    cp_async_commit();
   }
   int stage = 0, turn = 0;
   // the CTA's groups go through the loop together
   for (int64_t row = first; row - grp < a.rows; row += step) {
     const bool live = row < a.rows;
-    float x[NV][8];
-    if constexpr (WIDE) {
-      const int64_t ahead = row + (kFwdStages - 1) * step;
-      if (ahead < a.rows)
-        copy_row<G, NV>(ring, kP, (stage + kFwdStages - 1) % kFwdStages, 0, x_row(ahead), cols, t, XBF16);
-      cp_async_commit();
-      cp_async_wait<kFwdStages - 1>();
+    const int64_t ahead = row + (kFwdStages - 1) * step;
+    if (ahead < a.rows) copy_row<G, NV>(ring, kP, stage == 0 ? kFwdStages - 1 : stage - 1, 0, x_row(ahead), cols, t, XBF16);
+    cp_async_commit();
+    cp_async_wait<kFwdStages - 1>();
+    Pair x[NV][4];
 #pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        if (live) {
-          copied_vec<G, NV>(ring, kP, stage, 0, x_row(row), cols, t, e, XBF16, x[e]);
-        } else {
+    for (int e = 0; e < NV; ++e) {
+      if (live && (t + G * e) * 8 < cols) {
+        copied_vec<G, NV>(ring, kP, stage, 0, x_row(row), cols, t, e, XBF16, x[e]);
+      } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[e][k] = 0.0f;
-        }
-      }
-      stage = (stage + 1) % kFwdStages;
-    } else {
-#pragma unroll
-      for (int e = 0; e < NV; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[e][k] = live ? nx[e][k] : 0.0f;
-      if (row + step < a.rows) {
-#pragma unroll
-        for (int e = 0; e < NV; ++e) load_vec<G, WIDE, XBF16>(x_row(row + step), cols, t, e, nx[e]);
+        for (int k = 0; k < 4; ++k) x[e][k] = pair(0.0f, 0.0f);
       }
     }
+    if (++stage == kFwdStages) stage = 0;
     float mean = 0.0f;
     if (!a.rms) {
-      float s[1] = {0.0f};
+      Pair s2 = pair(0.0f, 0.0f), s3 = s2;
 #pragma unroll
-      for (int e = 0; e < NV; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[0] += x[e][k];
+      for (int e = 0; e < NV; ++e) s2 = s2 + (x[e][0] + x[e][1]), s3 = s3 + (x[e][2] + x[e][3]);
+      const float2 h = halves(s2 + s3);
+      float s[1] = {h.x + h.y};
       group_sum<G>(s, red[turn]);
       turn ^= 1;
       mean = s[0] / float(cols);
     }
-    float q[1] = {0.0f};
+    const Pair less = pair(-mean, -mean);
+    Pair q2 = pair(0.0f, 0.0f), q3 = q2;
 #pragma unroll
-    for (int e = 0; e < NV; ++e)
+    for (int e = 0; e < NV; ++e) {
+      const int c0 = (t + G * e) * 8;
+      if (c0 < cols) {
+        if (!a.rms) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[e][k] = col_of<G, WIDE>(t, e, k) < cols ? x[e][k] - mean : 0.0f;
-        q[0] = fmaf(x[e][k], x[e][k], q[0]);
+          for (int k = 0; k < 4; ++k) x[e][k] = x[e][k] + less;
+          if (c0 + 8 > cols) clear_past(x[e], cols, c0);
+        }
+        q2 = fma(x[e][0], x[e][0], q2), q3 = fma(x[e][1], x[e][1], q3);
+        q2 = fma(x[e][2], x[e][2], q2), q3 = fma(x[e][3], x[e][3], q3);
       }
+    }
+    const float2 h = halves(q2 + q3);
+    float q[1] = {h.x + h.y};
     group_sum<G>(q, red[turn]);
     turn ^= 1;
     const float rstd = 1.0f / sqrtf(q[0] / float(cols) + a.eps);
@@ -293,26 +229,158 @@ __global__ void __launch_bounds__(kCtaThreads<G>, kCtaThreads<G> == 512 ? 1 : 2)
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
     if (!live) continue;  // whole warps
-    void* yr = at(a.y, row * a.ldy, a.y_bf16);
+    const Pair r2 = pair(rstd, rstd);
+    char* yr = at(a.y, row * a.ldy, a.y_bf16);
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
+      const int c0 = (t + G * e) * 8;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[e][k] *= rstd;
-      if (a.codes != nullptr) store_codes<G, WIDE>(a, row, t, e, nb, x[e]);
-      if (col_of<G, WIDE>(t, e, 0) < cols) {
-        if constexpr (kKeep) {
+      for (int k = 0; k < 4; ++k) x[e][k] = x[e][k] * r2;
+      if (a.codes != nullptr) {
+        // a block is four lanes, whether or not the row reaches all of them
+        float f[8];
+        floats8(x[e], f);
+        uint32_t m = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[e][k] = fmaf(x[e][k], gm[e][k], bt[e][k]);
-        } else {
-          float g[8], b[8];
-          load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, g);
-          load_param<G, WIDE>(a.beta, cols, t, e, a.param_bf16, pwide, 0.0f, b);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[e][k] = fmaf(x[e][k], g[k], b[k]);
+        for (int k = 0; k < 8; ++k) m = max(m, mag_bits(f[k]));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        if (c0 < nb * kCkptBlock) {
+          *reinterpret_cast<uint2*>(a.codes + row * nb * kCkptBlock + c0) = ckpt_pack8(f, m);
+          if ((c0 & 31) == 0) a.scales[row * nb + c0 / kCkptBlock] = uint8_t(ckpt_scale(m));
         }
-        store_vec<G, WIDE>(yr, cols, t, e, a.y_bf16, x[e]);
+      }
+      if (c0 < cols) {
+        if (a.gamma != nullptr || a.beta != nullptr) {
+          Pair g[4], b[4];
+          load_param(a.gamma, cols, c0, a.param_bf16, pwide, 1.0f, g);
+          load_param(a.beta, cols, c0, a.param_bf16, pwide, 0.0f, b);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[e][k] = fma(x[e][k], g[k], b[k]);
+        }
+        store_vec(yr, cols, c0, a.y_bf16, x[e]);
       }
     }
+  }
+}
+
+// ---------------------------------------------------------------------------------------- narrow: single columns
+
+// Column j of a thread: t + G * j.  Neighbouring lanes hold neighbouring columns, so that loads and
+// stores of single elements still touch whole sectors, and a checkpoint block is one warp.
+template <bool BF16>
+struct Elem {
+  typedef float type;
+};
+template <>
+struct Elem<true> {
+  typedef uint16_t type;
+};
+__device__ __forceinline__ float elem_value(float v) { return v; }
+__device__ __forceinline__ float elem_value(uint16_t v) { return bf16_bits_to_f32(v); }
+
+template <int G, int NE, bool BF16, bool RW>
+__device__ __forceinline__ void load_cols(const char* row, int cols, int t, float (&v)[NE]) {
+  const typename Elem<BF16>::type* q = reinterpret_cast<const typename Elem<BF16>::type*>(row) + t;
+#pragma unroll
+  for (int j = 0; j < NE; ++j) v[j] = t < cols - G * j ? elem_value(RW ? q[G * j] : __ldg(q + G * j)) : 0.0f;
+}
+template <int G, int NE>
+__device__ __forceinline__ void load_cols(const void* p, int cols, int t, int bf16, float none, float (&v)[NE]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int j = 0; j < NE; ++j) v[j] = none;
+  } else if (bf16) {
+    load_cols<G, NE, true, false>(static_cast<const char*>(p), cols, t, v);
+  } else {
+    load_cols<G, NE, false, false>(static_cast<const char*>(p), cols, t, v);
+  }
+}
+template <int G, int NE>
+__device__ __forceinline__ void store_cols(char* row, int cols, int t, int bf16, const float (&v)[NE]) {
+  if (bf16) {
+    __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(row) + t;
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if (t < cols - G * j) q[G * j] = __float2bfloat16_rn(v[j]);
+  } else {
+    float* q = reinterpret_cast<float*>(row) + t;
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if (t < cols - G * j) q[G * j] = v[j];
+  }
+}
+
+template <int G, int NE, bool XBF16>
+__global__ void __launch_bounds__(kCtaThreads<G>, 768 / kCtaThreads<G>) k_norm_fwd_narrow(NormFwdArgs a) {
+  __shared__ float red[2][32];
+  constexpr int kGroups = kCtaThreads<G> / G;
+  const int t = threadIdx.x % G, grp = threadIdx.x / G;
+  const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
+  const int64_t step = int64_t(gridDim.x) * kGroups;
+  int turn = 0;
+  for (int64_t row = int64_t(blockIdx.x) * kGroups + grp; row - grp < a.rows; row += step) {
+    const bool live = row < a.rows;
+    float x[NE];
+    if (live) {
+      load_cols<G, NE, XBF16, false>(at(a.x, row * a.ldx, XBF16), cols, t, x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) x[j] = 0.0f;
+    }
+    float mean = 0.0f;
+    if (!a.rms) {
+      float s[1] = {0.0f}, s1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NE; j += 2) s[0] += x[j], s1 += x[j + 1];
+      s[0] += s1;
+      group_sum<G>(s, red[turn]);
+      turn ^= 1;
+      mean = s[0] / float(cols);
+    }
+    float q[1] = {0.0f}, q1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NE; j += 2) {
+      x[j] = t < cols - G * j ? x[j] - mean : 0.0f;
+      x[j + 1] = t < cols - G * (j + 1) ? x[j + 1] - mean : 0.0f;
+      q[0] = fmaf(x[j], x[j], q[0]);
+      q1 = fmaf(x[j + 1], x[j + 1], q1);
+    }
+    q[0] += q1;
+    group_sum<G>(q, red[turn]);
+    turn ^= 1;
+    const float rstd = 1.0f / sqrtf(q[0] / float(cols) + a.eps);
+    if (t == 0 && live) {
+      if (a.mean != nullptr && !a.rms) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    if (!live) continue;  // whole warps
+#pragma unroll
+    for (int j = 0; j < NE; ++j) x[j] *= rstd;
+    if (a.codes != nullptr) {
+      int8_t* c = a.codes + row * nb * kCkptBlock + t;
+      uint8_t* sc = a.scales + row * nb + t / kCkptBlock;
+#pragma unroll
+      for (int j = 0; j < NE; ++j) {
+        if (t / kCkptBlock >= nb - G / kCkptBlock * j) continue;  // a warp's 32 columns are one block
+        const uint32_t s = ckpt_scale(__reduce_max_sync(0xFFFFFFFFu, mag_bits(x[j])));
+        c[G * j] = int8_t(ckpt_code(x[j], ckpt_inv_step(s)));
+        if ((t & 31) == 0) sc[G / kCkptBlock * j] = uint8_t(s);
+      }
+    }
+    if (a.gamma != nullptr) {
+      float g[NE];
+      load_cols<G, NE>(a.gamma, cols, t, a.param_bf16, 1.0f, g);
+#pragma unroll
+      for (int j = 0; j < NE; ++j) x[j] *= g[j];
+    }
+    if (a.beta != nullptr) {
+      float b[NE];
+      load_cols<G, NE>(a.beta, cols, t, a.param_bf16, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < NE; ++j) x[j] += b[j];
+    }
+    store_cols<G, NE>(at(a.y, row * a.ldy, a.y_bf16), cols, t, a.y_bf16, x);
   }
 }
 
@@ -325,7 +393,7 @@ __global__ void __launch_bounds__(kLoop) k_norm_fwd_long(NormFwdArgs a) {
   __shared__ float red[2][32];
   const int64_t row = blockIdx.x;
   const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
-  const void* xr = at(a.x, row * a.ldx, XBF16);
+  const char* xr = at(a.x, row * a.ldx, XBF16);
   float mean = 0.0f;
   if (!a.rms) {
     float s[1] = {0.0f};
@@ -344,7 +412,7 @@ __global__ void __launch_bounds__(kLoop) k_norm_fwd_long(NormFwdArgs a) {
     if (a.mean != nullptr && !a.rms) a.mean[row] = mean;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
   }
-  void* yr = at(a.y, row * a.ldy, a.y_bf16);
+  char* yr = at(a.y, row * a.ldy, a.y_bf16);
   const int64_t pitch = int64_t(nb) * kCkptBlock;  // a multiple of 32: whole warps enter and leave together
   for (int64_t c = threadIdx.x; c < pitch; c += kLoop) {
     const float v = c < cols ? (load_elem(xr, c, XBF16) - mean) * rstd : 0.0f;
@@ -361,197 +429,253 @@ __global__ void __launch_bounds__(kLoop) k_norm_fwd_long(NormFwdArgs a) {
 
 // ---------------------------------------------------------------------------------------- backward
 
-// A row's contribution that one thread holds: dy, and x or the codes of the normalised row.
-template <int G, int NV, bool XBF16, bool WIDE, bool CKPT>
-struct BwdRow {
-  float dy[NV][8], x[NV][8], r[NV][8];  // narrow: the values (x normalised only later)
-  uint2 codes[NV];                      // WIDE from a checkpoint
-  uint32_t scale[NV];
-  float mean, rstd;
-};
+// Partial sums of a CTA's rows to the workspace.  `mine(c, i)` gives a thread's sum i (0 dgamma, 1
+// dbeta) of its columns through `each`; where a CTA holds several groups they add up one after another
+// in shared memory first.
+template <int G, typename Each>
+__device__ __forceinline__ void write_partials(const NormBwdArgs& a, float* sum, Each each) {
+  constexpr int T = kCtaThreads<G>, kGroups = T / G;
+  const int cols = int(a.cols), grp = threadIdx.x / G;
+  float* out = a.partials + int64_t(blockIdx.x) * 2 * cols;
+  if constexpr (kGroups == 1) {
+    each([&](int c, float dg, float db) { out[c] = dg, out[cols + c] = db; });
+  } else {
+    for (int w = 0; w < kGroups; ++w) {
+      __syncthreads();
+      if (grp == w)
+        each([&](int c, float dg, float db) {
+          sum[c] = (w ? sum[c] : 0.0f) + dg;
+          sum[cols + c] = (w ? sum[cols + c] : 0.0f) + db;
+        });
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * cols; c += T) out[c] = sum[c];
+  }
+}
 
-// 16-byte pieces of one stage: dy, then x, then the residual (fp32 takes two per vector).
+// 16-byte pieces of one stage: dy, then x (or codes: half a piece per vector), then the residual
+// (fp32 takes two per vector).
 template <int NV>
-__host__ __device__ __forceinline__ int bwd_pieces(int y_bf16, int x_bf16, bool has_x, bool has_residual) {
-  return NV * ((y_bf16 ? 1 : 2) + (x_bf16 ? 1 : 2) * ((has_x ? 1 : 0) + (has_residual ? 1 : 0)));
+__host__ __device__ __forceinline__ int bwd_pieces(int y_bf16, int x_bf16, bool ckpt, bool residual) {
+  return NV * ((y_bf16 ? 1 : 2) + (ckpt || x_bf16 ? 1 : 2) + (residual ? (x_bf16 ? 1 : 2) : 0));
 }
 // As many rows ahead as shared memory holds for the widest types (a row of 8192 fp32 columns with
 // fp32 dy and residual takes 96 KB).
 template <int G, bool XBF16>
-constexpr int kBwdStages = (G == 512 ? 2 : 3) + (XBF16 ? 1 : 0);
+constexpr int kBwdStages = G == 512 && !XBF16 ? 2 : 3;
 
-template <int G, int NV, bool XBF16, bool WIDE, bool CKPT>
-__global__ void __launch_bounds__(kCtaThreads<G>, kCtaThreads<G> == 512 ? 1 : 2) k_norm_bwd(NormBwdArgs a, bool pwide) {
+template <int G, int NV, bool XBF16, bool CKPT>
+__global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (NV == 1 ? 768 : 512) / kCtaThreads<G>)
+    k_norm_bwd(NormBwdArgs a, bool pwide) {
   __shared__ float red[2][64];
-  extern __shared__ __align__(16) uint8_t ring[];  // the stages; after the rows, [2][cols] floats
+  extern __shared__ __align__(16) uint8_t ring[];  // the stages, and gamma; after the rows, [2][cols] sums
   constexpr int T = kCtaThreads<G>, kGroups = T / G, kStages = kBwdStages<G, XBF16>;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const int64_t step = int64_t(gridDim.x) * kGroups, first = int64_t(blockIdx.x) * kGroups + grp;
-  const int pieces = bwd_pieces<NV>(a.y_bf16, XBF16, !CKPT, a.residual != nullptr);
-  const int at_x = NV * (a.y_bf16 ? 1 : 2), at_r = at_x + (CKPT ? 0 : NV * (XBF16 ? 1 : 2));
-  constexpr bool kKeep = WIDE || NV == 1;  // gamma stays in registers
-  float dg[NV][8], db[NV][8], gm[NV][8];
+  const int pieces = bwd_pieces<NV>(a.y_bf16, XBF16, CKPT, a.residual != nullptr);
+  const int at_x = NV * (a.y_bf16 ? 1 : 2), at_r = at_x + NV * (CKPT || XBF16 ? 1 : 2);
+  // gamma: each thread's own values in shared memory behind the stages
+  ulonglong2* gamma = reinterpret_cast<ulonglong2*>(piece<T>(ring, pieces, kStages, 0));
+  Pair dg[NV][4], db[NV][4];
 #pragma unroll
   for (int e = 0; e < NV; ++e) {
-    if constexpr (kKeep) load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, gm[e]);
+    Pair v[4];
+    load_param(a.gamma, cols, (t + G * e) * 8, a.param_bf16, pwide, 1.0f, v);
+    gamma[2 * e * T] = make_ulonglong2(v[0].u, v[1].u);
+    gamma[(2 * e + 1) * T] = make_ulonglong2(v[2].u, v[3].u);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dg[e][k] = db[e][k] = 0.0f;
+    for (int k = 0; k < 4; ++k) dg[e][k] = db[e][k] = pair(0.0f, 0.0f);
   }
-  // Starts the wide copies of a row.
   const auto copy = [&](int64_t row, int stage) {
     copy_row<G, NV>(ring, pieces, stage, 0, at(a.dy, row * a.lddy, a.y_bf16), cols, t, a.y_bf16);
-    if constexpr (!CKPT) copy_row<G, NV>(ring, pieces, stage, at_x, at(a.x, row * a.ldx, XBF16), cols, t, XBF16);
+    if constexpr (CKPT) {
+#pragma unroll
+      for (int e = 0; e < NV; ++e)  // the padding of a ragged block is part of it
+        if ((t + G * e) * 8 < cols)
+          cp_async8(piece<T>(ring, pieces, stage, at_x + e), a.codes + row * nb * kCkptBlock + (t + G * e) * 8);
+    } else {
+      copy_row<G, NV>(ring, pieces, stage, at_x, at(a.x, row * a.ldx, XBF16), cols, t, XBF16);
+    }
     if (a.residual != nullptr)
       copy_row<G, NV>(ring, pieces, stage, at_r, at(a.residual, row * a.ldr, XBF16), cols, t, XBF16);
   };
-  // Loads of a row that go to registers: its statistics, its codes, or all of it.
-  BwdRow<G, NV, XBF16, WIDE, CKPT> nx;
+  // What of the next row goes to registers: its statistics and scales.
+  float next_rstd = 0.0f, next_mean = 0.0f;
+  uint32_t next_scale[NV];
   const auto load = [&](int64_t row) {
-    nx.rstd = __ldg(a.rstd + row);
-    nx.mean = CKPT || a.rms ? 0.0f : __ldg(a.mean + row);
-    if constexpr (CKPT && WIDE) {
+    next_rstd = __ldg(a.rstd + row);
+    if (!CKPT && !a.rms) next_mean = __ldg(a.mean + row);
+    if constexpr (CKPT) {
 #pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        const int g = t + G * e;
-        nx.codes[e] = make_uint2(0, 0);
-        nx.scale[e] = 1;
-        if (g * 8 < cols) {
-          nx.codes[e] = __ldg(reinterpret_cast<const uint2*>(a.codes + row * nb * kCkptBlock) + g);
-          nx.scale[e] = __ldg(a.scales + row * nb + g / 4);
-        }
-      }
-    }
-    if constexpr (!WIDE) {
-#pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        if (a.y_bf16)
-          load_vec<G, WIDE, true>(at(a.dy, row * a.lddy, true), cols, t, e, nx.dy[e]);
-        else
-          load_vec<G, WIDE, false>(at(a.dy, row * a.lddy, false), cols, t, e, nx.dy[e]);
-        if constexpr (CKPT) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int c = col_of<G, WIDE>(t, e, k);
-            nx.x[e][k] = c < cols ? float(__ldg(a.codes + row * nb * kCkptBlock + c)) *
-                                        ckpt_step(__ldg(a.scales + row * nb + c / kCkptBlock))
-                                  : 0.0f;
-          }
-        } else {
-          load_vec<G, WIDE, XBF16>(at(a.x, row * a.ldx, XBF16), cols, t, e, nx.x[e]);
-        }
-      }
+      for (int e = 0; e < NV; ++e)
+        next_scale[e] = (t + G * e) * 8 < cols ? __ldg(a.scales + row * nb + (t + G * e) / 4) : 1u;
     }
   };
-  if constexpr (WIDE) {
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (first + i * step < a.rows) copy(first + i * step, i);
-      cp_async_commit();
-    }
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (first + i * step < a.rows) copy(first + i * step, i);
+    cp_async_commit();
   }
   if (first < a.rows) load(first);
   int stage = 0, turn = 0;
   for (int64_t row = first; row - grp < a.rows; row += step) {
     const bool live = row < a.rows;
-    float g[NV][8], xh[NV][8];
-    float s[2] = {0.0f, 0.0f};
-    const float rstd = live ? nx.rstd : 0.0f, mean = nx.mean;
-    if constexpr (WIDE) {
-      const int64_t ahead = row + (kStages - 1) * step;
-      if (ahead < a.rows) copy(ahead, stage == 0 ? kStages - 1 : stage - 1);
-      cp_async_commit();
-      cp_async_wait<kStages - 1>();
+    const int64_t ahead = row + (kStages - 1) * step;
+    if (ahead < a.rows) copy(ahead, stage == 0 ? kStages - 1 : stage - 1);
+    cp_async_commit();
+    cp_async_wait<kStages - 1>();
+    const float rstd = next_rstd;
+    const Pair r2 = pair(rstd, rstd), m2 = pair(-next_mean * rstd, -next_mean * rstd);
+    uint32_t scale[NV];
+    if constexpr (CKPT) {
+#pragma unroll
+      for (int e = 0; e < NV; ++e) scale[e] = next_scale[e];
     }
+    // dy, the normalised values and gamma of vector e, read from shared memory before and after the sums
+    const auto values = [&](int e, Pair (&d)[4], Pair (&xh)[4], Pair (&gm)[4]) {
+      const int c0 = (t + G * e) * 8;
+      copied_vec<G, NV>(ring, pieces, stage, 0, at(a.dy, row * a.lddy, a.y_bf16), cols, t, e, a.y_bf16, d);
+      if constexpr (CKPT) {
+        const uint2 w = *reinterpret_cast<const uint2*>(piece<T>(ring, pieces, stage, at_x + e));
+        ckpt_pairs4(w.x, scale[e], xh);
+        ckpt_pairs4(w.y, scale[e], xh + 2);
+      } else {
+        copied_vec<G, NV>(ring, pieces, stage, at_x, at(a.x, row * a.ldx, XBF16), cols, t, e, XBF16, xh);
 #pragma unroll
-    for (int e = 0; e < NV; ++e) {
-      if (live) {
-        if constexpr (WIDE) {
-          copied_vec<G, NV>(ring, pieces, stage, 0, at(a.dy, row * a.lddy, a.y_bf16), cols, t, e, a.y_bf16, g[e]);
-          if constexpr (CKPT) {
-            const float st = ckpt_step(nx.scale[e]);
-            ckpt_unpack4(nx.codes[e].x, st, xh[e]);
-            ckpt_unpack4(nx.codes[e].y, st, xh[e] + 4);
-          } else {
-            copied_vec<G, NV>(ring, pieces, stage, at_x, at(a.x, row * a.ldx, XBF16), cols, t, e, XBF16, xh[e]);
-          }
-        } else {
+        for (int k = 0; k < 4; ++k) xh[k] = fma(xh[k], r2, m2);
+      }
+      if (c0 + 8 > cols) clear_past(xh, cols, c0);  // (a bad block's padding reads back as NaN)
+      const ulonglong2 lo = gamma[2 * e * T], hi = gamma[(2 * e + 1) * T];
+      gm[0].u = lo.x, gm[1].u = lo.y, gm[2].u = hi.x, gm[3].u = hi.y;
+    };
+    float s[2] = {0.0f, 0.0f};
+    if (live) {
+      Pair s0 = pair(0.0f, 0.0f), s1 = s0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) g[e][k] = nx.dy[e][k], xh[e][k] = nx.x[e][k];
-        }
-        if constexpr (!kKeep) load_param<G, WIDE>(a.gamma, cols, t, e, a.param_bf16, pwide, 1.0f, gm[e]);
+      for (int e = 0; e < NV; ++e) {
+        if ((t + G * e) * 8 >= cols) continue;
+        Pair d[4], xh[4], gm[4];
+        values(e, d, xh, gm);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if constexpr (!CKPT) xh[e][k] = (xh[e][k] - mean) * rstd;
-          // past the last column (a bad block's padding reads back as NaN)
-          if (col_of<G, WIDE>(t, e, k) >= cols) xh[e][k] = 0.0f;
-          dg[e][k] = fmaf(g[e][k], xh[e][k], dg[e][k]);
-          db[e][k] += g[e][k];
-          g[e][k] *= gm[e][k];
-          s[0] += g[e][k];
-          s[1] = fmaf(g[e][k], xh[e][k], s[1]);
+        for (int k = 0; k < 4; ++k) {
+          dg[e][k] = fma(d[k], xh[k], dg[e][k]);
+          db[e][k] = db[e][k] + d[k];
+          const Pair g = d[k] * gm[k];
+          s0 = s0 + g;
+          s1 = fma(g, xh[k], s1);
         }
       }
+      const float2 h0 = halves(s0), h1 = halves(s1);
+      s[0] = h0.x + h0.y, s[1] = h1.x + h1.y;
     }
     if (row + step < a.rows) load(row + step);
     group_sum<G>(s, red[turn]);
     turn ^= 1;
-    const float c1 = a.rms ? 0.0f : s[0] / float(cols), c2 = s[1] / float(cols);
     if (live) {
-      void* dxr = at(a.dx, row * a.lddx, XBF16);
+      // dx = r (g - c1 - xhat c2) + residual
+      const float c1 = a.rms ? 0.0f : s[0] / float(cols) * -rstd, c2 = s[1] / float(cols) * -rstd;
+      const Pair k1 = pair(c1, c1), k2 = pair(c2, c2);
+      char* dxr = at(a.dx, row * a.lddx, XBF16);
 #pragma unroll
       for (int e = 0; e < NV; ++e) {
-        if (col_of<G, WIDE>(t, e, 0) >= cols) continue;
-        float r[8];
+        const int c0 = (t + G * e) * 8;
+        if (c0 >= cols) continue;
+        Pair d[4], xh[4], gm[4], r[4];
+        values(e, d, xh, gm);
         if (a.residual != nullptr) {
-          const void* rr = at(a.residual, row * a.ldr, XBF16);
-          if constexpr (WIDE)
-            copied_vec<G, NV, true>(ring, pieces, stage, at_r, rr, cols, t, e, XBF16, r);
-          else
-            load_vec<G, WIDE, XBF16, true>(rr, cols, t, e, r);
+          copied_vec<G, NV>(ring, pieces, stage, at_r, at(a.residual, row * a.ldr, XBF16), cols, t, e, XBF16, r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = r[k] + fma(xh[k], k2, fma(d[k] * gm[k], r2, k1));
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) r[k] = 0.0f;
+          for (int k = 0; k < 4; ++k) r[k] = fma(xh[k], k2, fma(d[k] * gm[k], r2, k1));
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) r[k] = fmaf(rstd, fmaf(-xh[e][k], c2, g[e][k] - c1), r[k]);
-        store_vec<G, WIDE>(dxr, cols, t, e, XBF16, r);
+        store_vec(dxr, cols, c0, XBF16, r);
       }
     }
     if (++stage == kStages) stage = 0;
   }
   if (a.partials == nullptr) return;
-  float* out = a.partials + int64_t(blockIdx.x) * 2 * cols;
-  if constexpr (kGroups == 1) {
+  cp_async_wait<0>();
+  write_partials<G>(a, reinterpret_cast<float*>(ring), [&](auto put) {
 #pragma unroll
     for (int e = 0; e < NV; ++e)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = col_of<G, WIDE>(t, e, k);
-        if (c < cols) out[c] = dg[e][k], out[cols + c] = db[e][k];
+      for (int k = 0; k < 4; ++k) {
+        const float2 g = halves(dg[e][k]), b = halves(db[e][k]);
+        const int c = (t + G * e) * 8 + 2 * k;
+        if (c < cols) put(c, g.x, b.x);
+        if (c + 1 < cols) put(c + 1, g.y, b.y);
       }
-  } else {
-    // the CTA's groups add their sums one after another, where the stages were
-    float* sum = reinterpret_cast<float*>(ring);
-    cp_async_wait<0>();
-    for (int w = 0; w < kGroups; ++w) {
-      __syncthreads();
-      if (grp == w) {
+  });
+}
+
+template <int G, int NE, bool XBF16, bool CKPT>
+__global__ void __launch_bounds__(kCtaThreads<G>, 512 / kCtaThreads<G>) k_norm_bwd_narrow(NormBwdArgs a) {
+  __shared__ float red[2][64];
+  extern __shared__ float sums[];  // [2][cols] where a CTA holds several groups
+  constexpr int kGroups = kCtaThreads<G> / G;
+  const int t = threadIdx.x % G, grp = threadIdx.x / G;
+  const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
+  const int64_t step = int64_t(gridDim.x) * kGroups;
+  float dg[NE], db[NE];
 #pragma unroll
-        for (int e = 0; e < NV; ++e)
+  for (int j = 0; j < NE; ++j) dg[j] = db[j] = 0.0f;
+  int turn = 0;
+  for (int64_t row = int64_t(blockIdx.x) * kGroups + grp; row - grp < a.rows; row += step) {
+    const bool live = row < a.rows;
+    float d[NE], xh[NE], s[2] = {0.0f, 0.0f}, rstd = 0.0f;
+    if (live) {
+      rstd = __ldg(a.rstd + row);
+      if (a.y_bf16)
+        load_cols<G, NE, true, false>(at(a.dy, row * a.lddy, true), cols, t, d);
+      else
+        load_cols<G, NE, false, false>(at(a.dy, row * a.lddy, false), cols, t, d);
+      if constexpr (CKPT) {
+        const int8_t* c = a.codes + row * nb * kCkptBlock + t;
+        const uint8_t* sc = a.scales + row * nb + t / kCkptBlock;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int c = col_of<G, WIDE>(t, e, k);
-            if (c < cols) {
-              sum[c] = (w ? sum[c] : 0.0f) + dg[e][k];
-              sum[cols + c] = (w ? sum[cols + c] : 0.0f) + db[e][k];
-            }
-          }
+        for (int j = 0; j < NE; ++j)
+          xh[j] = t < cols - G * j ? float(__ldg(c + G * j)) * ckpt_step(__ldg(sc + G / kCkptBlock * j)) : 0.0f;
+      } else {
+        const float mean = a.rms ? 0.0f : __ldg(a.mean + row);
+        load_cols<G, NE, XBF16, false>(at(a.x, row * a.ldx, XBF16), cols, t, xh);
+#pragma unroll
+        for (int j = 0; j < NE; ++j) xh[j] = t < cols - G * j ? (xh[j] - mean) * rstd : 0.0f;
+      }
+      float gm[NE];
+      load_cols<G, NE>(a.gamma, cols, t, a.param_bf16, 1.0f, gm);
+#pragma unroll
+      for (int j = 0; j < NE; ++j) {
+        dg[j] = fmaf(d[j], xh[j], dg[j]);
+        db[j] += d[j];
+        d[j] *= gm[j];
+        s[0] += d[j];
+        s[1] = fmaf(d[j], xh[j], s[1]);
       }
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < 2 * cols; c += T) out[c] = sum[c];
+    group_sum<G>(s, red[turn]);
+    turn ^= 1;
+    if (!live) continue;  // whole warps
+    const float c1 = a.rms ? 0.0f : s[0] / float(cols), c2 = s[1] / float(cols);
+    if (a.residual != nullptr) {
+      float r[NE];
+      load_cols<G, NE, XBF16, true>(at(a.residual, row * a.ldr, XBF16), cols, t, r);
+#pragma unroll
+      for (int j = 0; j < NE; ++j) d[j] = fmaf(rstd, fmaf(-xh[j], c2, d[j] - c1), r[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) d[j] = rstd * fmaf(-xh[j], c2, d[j] - c1);
+    }
+    store_cols<G, NE>(at(a.dx, row * a.lddx, XBF16), cols, t, XBF16, d);
   }
+  if (a.partials == nullptr) return;
+  write_partials<G>(a, sums, [&](auto put) {
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if (t < cols - G * j) put(t + G * j, dg[j], db[j]);
+  });
 }
 
 // One normalised value, for rows too long for registers.
@@ -638,57 +762,63 @@ bool wide_rows(const void* p, int64_t ld, int64_t rows, int bf16) {
 }
 bool wide_vec(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <int G, int NV, bool XBF16, bool WIDE>
-cudaError_t fwd_launch(const NormFwdArgs& a, bool pwide, cudaStream_t s) {
+// Narrow kernels hold half as many columns a thread, in groups of twice the threads.
+template <int G, int NV>
+cudaError_t fwd(const NormFwdArgs& a, bool wide, bool pwide, cudaStream_t s) {
+  static LayerGrid cache[4];
   constexpr int T = kCtaThreads<G>;
-  constexpr size_t sm = WIDE ? size_t(kFwdRing<NV, XBF16>) * kFwdPieces<G, NV, XBF16> * T * 16 : 0;
-  static LayerGrid cache;
   int cap = 0;
-  const cudaError_t e = layer_grid(cache, reinterpret_cast<const void*>(&k_norm_fwd<G, NV, XBF16, WIDE>), T, sm, sm, &cap);
-  if (e != cudaSuccess) return e;
-  const int64_t want = (a.rows + T / G - 1) / (T / G);
-  k_norm_fwd<G, NV, XBF16, WIDE><<<unsigned(want < cap ? want : cap), T, sm, s>>>(a, pwide);
+  if (wide) {
+    const auto kernel = a.x_bf16 ? k_norm_fwd<G, NV, true> : k_norm_fwd<G, NV, false>;
+    const size_t sm = size_t(kFwdStages) * (a.x_bf16 ? kFwdPieces<NV, true> : kFwdPieces<NV, false>) * T * 16;
+    const cudaError_t e = layer_grid(cache[a.x_bf16], reinterpret_cast<const void*>(kernel), T, sm, sm, &cap);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.rows + T / G - 1) / (T / G);
+    kernel<<<unsigned(want < cap ? want : cap), T, sm, s>>>(a, pwide);
+  } else {
+    constexpr int H = NV == 1 ? G : 2 * G, NE = NV == 1 ? 8 : NV * 4, TN = kCtaThreads<H>;
+    const auto kernel = a.x_bf16 ? k_norm_fwd_narrow<H, NE, true> : k_norm_fwd_narrow<H, NE, false>;
+    const cudaError_t e = layer_grid(cache[2 + a.x_bf16], reinterpret_cast<const void*>(kernel), TN, 0, 0, &cap);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.rows + TN / H - 1) / (TN / H);
+    kernel<<<unsigned(want < cap ? want : cap), TN, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 
-template <int G, int NV>
-cudaError_t fwd(const NormFwdArgs& a, bool wide, bool pwide, cudaStream_t s) {
-  if (a.x_bf16) return wide ? fwd_launch<G, NV, true, true>(a, pwide, s) : fwd_launch<G, NV, true, false>(a, pwide, s);
-  return wide ? fwd_launch<G, NV, false, true>(a, pwide, s) : fwd_launch<G, NV, false, false>(a, pwide, s);
-}
-
-template <int G, int NV, bool XBF16, bool WIDE, bool CKPT>
-cudaError_t bwd_launch(const NormBwdArgs& a, bool pwide, int* parts, cudaStream_t s) {
-  constexpr int T = kCtaThreads<G>, groups = T / G;
+template <int G, int NV, bool XBF16, bool CKPT>
+cudaError_t bwd_launch(const NormBwdArgs& a, bool wide, bool pwide, int* parts, cudaStream_t s) {
+  static LayerGrid cache[5];  // wide: occupancy depends on the stage's size, of which there are four
+  constexpr int H = NV == 1 ? G : 2 * G, NE = NV == 1 ? 8 : NV * 4;
+  const auto wide_kernel = k_norm_bwd<G, NV, XBF16, CKPT>;
+  const auto narrow_kernel = k_norm_bwd_narrow<H, NE, XBF16, CKPT>;
+  const int T = wide ? kCtaThreads<G> : kCtaThreads<H>, groups = T / (wide ? G : H);
   const auto bytes = [](int y_bf16, bool residual) {
-    // the stages, or where several groups join their sums of at most G * NV * 8 columns
-    return WIDE ? size_t(kBwdStages<G, XBF16>) * bwd_pieces<NV>(y_bf16, XBF16, !CKPT, residual) * T * 16
-                : size_t(groups > 1 ? G * NV * 64 : 0);
+    return (size_t(kBwdStages<G, XBF16>) * bwd_pieces<NV>(y_bf16, XBF16, CKPT, residual) + 2 * NV) * kCtaThreads<G> * 16;
   };
-  static_assert(!WIDE || groups == 1 || kBwdStages<G, XBF16> * T * 16 >= G * 64, "the sums fit where the stages were");
-  const size_t sm = bytes(a.y_bf16, a.residual != nullptr);
-  static LayerGrid cache[4];  // occupancy depends on the stage's size, of which there are four
+  static_assert(kCtaThreads<G> * 16 * 2 >= G * 8 * 8 || kCtaThreads<G> == G, "the sums fit where the stages were");
+  const size_t sm = wide ? bytes(a.y_bf16, a.residual != nullptr) : size_t(groups > 1 ? H * NE * 8 : 0);
   int cap = 0;
-  const cudaError_t e = layer_grid(cache[(a.y_bf16 ? 1 : 0) + (a.residual != nullptr ? 2 : 0)],
-                                   reinterpret_cast<const void*>(&k_norm_bwd<G, NV, XBF16, WIDE, CKPT>), T, sm,
-                                   bytes(0, true), &cap);
+  const cudaError_t e = wide ? layer_grid(cache[(a.y_bf16 ? 1 : 0) + (a.residual != nullptr ? 2 : 0)],
+                                          reinterpret_cast<const void*>(wide_kernel), T, sm, bytes(0, true), &cap)
+                             : layer_grid(cache[4], reinterpret_cast<const void*>(narrow_kernel), T, sm, sm, &cap);
   if (e != cudaSuccess) return e;
   if (cap > kNormPartials) cap = kNormPartials;
   const int64_t want = (a.rows + groups - 1) / groups;
   *parts = int(want < cap ? want : cap);
-  k_norm_bwd<G, NV, XBF16, WIDE, CKPT><<<*parts, T, sm, s>>>(a, pwide);
+  if (wide)
+    wide_kernel<<<*parts, T, sm, s>>>(a, pwide);
+  else
+    narrow_kernel<<<*parts, T, sm, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int G, int NV>
 cudaError_t bwd(const NormBwdArgs& a, bool wide, bool pwide, int* parts, cudaStream_t s) {
   const bool ck = a.x == nullptr;
-  if (a.x_bf16) {
-    if (wide) return ck ? bwd_launch<G, NV, true, true, true>(a, pwide, parts, s) : bwd_launch<G, NV, true, true, false>(a, pwide, parts, s);
-    return ck ? bwd_launch<G, NV, true, false, true>(a, pwide, parts, s) : bwd_launch<G, NV, true, false, false>(a, pwide, parts, s);
-  }
-  if (wide) return ck ? bwd_launch<G, NV, false, true, true>(a, pwide, parts, s) : bwd_launch<G, NV, false, true, false>(a, pwide, parts, s);
-  return ck ? bwd_launch<G, NV, false, false, true>(a, pwide, parts, s) : bwd_launch<G, NV, false, false, false>(a, pwide, parts, s);
+  if (a.x_bf16)
+    return ck ? bwd_launch<G, NV, true, true>(a, wide, pwide, parts, s) : bwd_launch<G, NV, true, false>(a, wide, pwide, parts, s);
+  return ck ? bwd_launch<G, NV, false, true>(a, wide, pwide, parts, s) : bwd_launch<G, NV, false, false>(a, wide, pwide, parts, s);
 }
 
 }  // namespace
@@ -698,11 +828,11 @@ cudaError_t launch_norm_forward(const NormFwdArgs& a, cudaStream_t s) {
   const bool pwide = wide_vec(a.gamma) && wide_vec(a.beta);
   const int64_t pitch = (a.cols + kCkptBlock - 1) / kCkptBlock * kCkptBlock;
   if (pitch <= 256) return fwd<32, 1>(a, wide, pwide, s);
-  if (pitch <= 512) return fwd<64, 1>(a, wide, pwide, s);
-  if (pitch <= 1024) return fwd<128, 1>(a, wide, pwide, s);
-  if (pitch <= 2048) return fwd<256, 1>(a, wide, pwide, s);
-  if (pitch <= 4096) return fwd<256, 2>(a, wide, pwide, s);
-  if (pitch <= 8192) return fwd<512, 2>(a, wide, pwide, s);
+  if (pitch <= 512) return fwd<32, 2>(a, wide, pwide, s);
+  if (pitch <= 1024) return fwd<64, 2>(a, wide, pwide, s);
+  if (pitch <= 2048) return fwd<128, 2>(a, wide, pwide, s);
+  if (pitch <= 4096) return fwd<128, 4>(a, wide, pwide, s);
+  if (pitch <= 8192) return fwd<256, 4>(a, wide, pwide, s);
   if (pitch <= 16384) return fwd<512, 4>(a, wide, pwide, s);
   (a.x_bf16 ? k_norm_fwd_long<true> : k_norm_fwd_long<false>)<<<unsigned(a.rows), kLoop, 0, s>>>(a);
   return cudaGetLastError();
