@@ -44,41 +44,43 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight values per thread and step, two steps in flight; groups of 8 values number nb*4 per row
-// (those past cols are padding).  All 32 lanes stay in the loop together.
-constexpr int kUnroll = 2;
+// A warp takes runs of kVec x 256 columns of a row, 8 columns a lane and vector: the position is worked
+// out once per run, and kVec loads are in flight.  `runs` of them per row cover its padded blocks.
+constexpr int kVec = 4, kRunCols = kVec * 256;
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_encode_wide(EncodeArgs a, Divisor per_row, int64_t groups) {
-  for (int64_t g0 = (int64_t(blockIdx.x) * kUnroll) * kThreads + threadIdx.x; g0 - (threadIdx.x & 31) < groups;
-       g0 += int64_t(gridDim.x) * kUnroll * kThreads) {
-    float v[kUnroll][8];
+__global__ void __launch_bounds__(kThreads) k_encode_wide(EncodeArgs a, Divisor per_row, int64_t nb, int64_t runs) {
+  const int lane = threadIdx.x & 31;
+  const int64_t step = int64_t(gridDim.x) * (kThreads / 32);
+  for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < runs; i += step) {
+    const int64_t row = divide(i, per_row), c0 = (i - row * per_row.d) * kRunCols + lane * 8;
+    const char* x = static_cast<const char*>(a.x) + (row * a.ldx + c0) * (BF16 ? 2 : 4);
+    int8_t* codes = a.codes + row * nb * kCkptBlock + c0;
+    uint8_t* scales = a.scales + row * nb + c0 / kCkptBlock;
+    const int64_t left = a.cols - c0, pad = nb * kCkptBlock - c0;  // columns from the lane's first on
+    float v[kVec][8];
+    if (left >= kRunCols - 256 + 8) {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int64_t g = g0 + i * kThreads;
+      for (int e = 0; e < kVec; ++e) load8(x, e * 256, BF16, v[e]);
+    } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
-      if (g >= groups) continue;
-      const int64_t row = divide(g, per_row), col = (g - row * per_row.d) * 8;
-      if (col + 8 <= a.cols) {
-        load8(a.x, row * a.ldx + col, BF16, v[i]);
-      } else {
+      for (int e = 0; e < kVec; ++e) {
+        if (left >= e * 256 + 8) {
+          load8(x, e * 256, BF16, v[e]);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (col + k < a.cols) v[i][k] = load_elem(a.x, row * a.ldx + col + k, BF16);
+          for (int k = 0; k < 8; ++k) v[e][k] = e * 256 + k < left ? load_elem(x, e * 256 + k, BF16) : 0.0f;
+        }
       }
     }
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int64_t g = g0 + i * kThreads;
-      uint32_t m = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) m = max(m, mag_bits(v[i][k]));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      if (g >= groups) continue;
-      reinterpret_cast<uint2*>(a.codes)[g] = ckpt_pack8(v[i], m);
-      if ((g & 3) == 0) a.scales[g >> 2] = uint8_t(ckpt_scale(m));
+    for (int e = 0; e < kVec; ++e) {
+      const uint32_t m = block_magnitude(v[e]);
+      if (e * 256 < pad) {
+        *reinterpret_cast<uint2*>(codes + e * 256) = ckpt_pack8(v[e], m);
+        if ((lane & 3) == 0) scales[e * (256 / kCkptBlock)] = uint8_t(ckpt_scale(m));
+      }
     }
   }
 }
@@ -109,37 +111,77 @@ __global__ void __launch_bounds__(kThreads) k_encode_narrow(EncodeArgs a, Diviso
   }
 }
 
-// Sixteen codes per thread (half a block), for rows of out that start on 16-byte boundaries.
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_decode_wide(DecodeArgs a, Divisor per_row, int64_t halves) {
-  const int64_t step = int64_t(gridDim.x) * kThreads;
-  for (int64_t h = int64_t(blockIdx.x) * kThreads + threadIdx.x; h < halves; h += step) {
-    const int64_t row = divide(h, per_row), col = (h - row * per_row.d) * 16;
-    if (col >= a.cols) continue;
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.codes) + h);
-    const float st = ckpt_step(__ldg(a.scales + (h >> 1)));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    const int64_t at = row * a.ldo + col;
+// Four codes as four bf16, with no detour over fp32.  Under the exponent of 2^7 a bf16's seven
+// mantissa bits count whole units: 0x4300 | (c & 0x7F) is 128 + (c & 0x7F) and 0x4300 | (c & 0x80) is
+// 128 or, for a negative code, 256, so their difference is the code, and its product with a power of
+// two is exact.
+__device__ __forceinline__ uint2 decode4_bf16(uint32_t w, __nv_bfloat162 step) {
+  uint32_t r[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t c = col + i * 8;
-      float v[8];
-      ckpt_unpack4(u[2 * i], st, v);
-      ckpt_unpack4(u[2 * i + 1], st, v + 4);
-      if (a.gamma != nullptr || a.beta != nullptr) {
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = __byte_perm(w, 0x43u, i ? 0x4342 : 0x4140);
+    const uint32_t lo = u & 0xFF7FFF7Fu, hi = u & 0xFF80FF80u;
+    const __nv_bfloat162 v = __hmul2(__hsub2(reinterpret_cast<const __nv_bfloat162&>(lo),
+                                             reinterpret_cast<const __nv_bfloat162&>(hi)), step);
+    r[i] = reinterpret_cast<const uint32_t&>(v);
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+// Runs as in k_encode_wide, for rows of out that start on 16-byte boundaries.  PLAIN: the values as they are.
+template <bool BF16, bool PLAIN>
+__global__ void __launch_bounds__(kThreads) k_decode_wide(DecodeArgs a, Divisor per_row, int64_t nb, int64_t runs) {
+  const int lane = threadIdx.x & 31;
+  const int64_t step = int64_t(gridDim.x) * (kThreads / 32);
+  for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < runs; i += step) {
+    const int64_t row = divide(i, per_row), c0 = (i - row * per_row.d) * kRunCols + lane * 8;
+    const int8_t* codes = a.codes + row * nb * kCkptBlock + c0;
+    const uint8_t* scales = a.scales + row * nb + c0 / kCkptBlock;
+    char* out = static_cast<char*>(a.out) + (row * a.ldo + c0) * (BF16 ? 2 : 4);
+    const int64_t left = a.cols - c0;
+    uint2 w[kVec];
+    uint32_t sc[kVec];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k < a.cols)
-            v[k] = fmaf(v[k], a.gamma ? load_elem(a.gamma, c + k, a.param_bf16) : 1.0f,
-                        a.beta ? load_elem(a.beta, c + k, a.param_bf16) : 0.0f);
+    for (int e = 0; e < kVec; ++e) {
+      w[e] = make_uint2(0, 0);
+      sc[e] = 1;
+      if (e * 256 < left) {
+        w[e] = __ldg(reinterpret_cast<const uint2*>(codes + e * 256));
+        sc[e] = __ldg(scales + e * (256 / kCkptBlock));
       }
-      apply_act8(v, a.act);
-      if (c + 8 <= a.cols) {
-        store8(a.out, at + i * 8, BF16, v);
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      if (e * 256 >= left) continue;
+      const bool full = e * 256 + 8 <= left;
+      if (PLAIN && BF16 && full) {
+        const __nv_bfloat162 st = __float2bfloat162_rn(ckpt_step(sc[e]));
+        const uint2 lo = decode4_bf16(w[e].x, st), hi = decode4_bf16(w[e].y, st);
+        *reinterpret_cast<uint4*>(out + e * 512) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        continue;
+      }
+      Pair p[4];
+      float v[8];
+      ckpt_pairs4(w[e].x, sc[e], p);
+      ckpt_pairs4(w[e].y, sc[e], p + 2);
+      floats8(p, v);
+      if (!PLAIN) {
+        if (a.gamma != nullptr || a.beta != nullptr) {
+          const int64_t c = c0 + e * 256;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (c + k < a.cols)
+              v[k] = fmaf(v[k], a.gamma ? load_elem(a.gamma, c + k, a.param_bf16) : 1.0f,
+                          a.beta ? load_elem(a.beta, c + k, a.param_bf16) : 0.0f);
+        }
+        apply_act8(v, a.act);
+      }
+      if (full) {
+        store8(out, e * 256, BF16, v);
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (c + k < a.cols) store_elem(a.out, at + i * 8 + k, BF16, v[k]);
+          if (e * 256 + k < left) store_elem(out, e * 256 + k, BF16, v[k]);
       }
     }
   }
@@ -184,52 +226,61 @@ bool wide_rows(const void* p, int64_t ld, int64_t rows, int bf16) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld * (bf16 ? 2 : 4) % 16 == 0);
 }
 
-cudaError_t grid_for(int64_t items, int per_block, unsigned* grid) {
-  int sms = 0;
-  const cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
-  const int64_t want = (items + per_block - 1) / per_block, most = int64_t(sms) * 8;
-  *grid = unsigned(want < most ? want : most);
-  return cudaSuccess;
+// As many CTAs as the device holds, or as the items fill.
+template <typename Kernel>
+cudaError_t grid_for(Kernel kernel, LayerGrid& cache, int64_t items, int per_block, unsigned* grid) {
+  int cap = 0;
+  const cudaError_t e = layer_grid(cache, reinterpret_cast<const void*>(kernel), kThreads, 0, 0, &cap);
+  const int64_t want = (items + per_block - 1) / per_block;
+  *grid = unsigned(want < cap ? want : cap);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt_encode(const EncodeArgs& in, cudaStream_t s) {
+  static LayerGrid cache[4];
   EncodeArgs a = in;
   if (a.rows > 1 && a.ldx == a.cols && a.cols % kCkptBlock == 0) a.ldx = a.cols *= a.rows, a.rows = 1;  // one long row
   const int64_t nb = (a.cols + kCkptBlock - 1) / kCkptBlock;
   unsigned grid;
-  cudaError_t e;
   if (wide_rows(a.x, a.ldx, a.rows, a.x_bf16)) {
-    const int64_t groups = a.rows * nb * 4;
-    if ((e = grid_for(groups, kThreads * kUnroll, &grid)) != cudaSuccess) return e;
-    (a.x_bf16 ? k_encode_wide<true> : k_encode_wide<false>)<<<grid, kThreads, 0, s>>>(
-        a, make_divisor(nb * 4, groups + int64_t(kThreads) * kUnroll), groups);
+    const int64_t per = (nb * kCkptBlock + kRunCols - 1) / kRunCols, runs = a.rows * per;
+    const auto kernel = a.x_bf16 ? k_encode_wide<true> : k_encode_wide<false>;
+    const cudaError_t e = grid_for(kernel, cache[a.x_bf16], runs, kThreads / 32, &grid);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, 0, s>>>(a, make_divisor(per, runs), nb, runs);
   } else {
-    if ((e = grid_for(a.rows * nb, kThreads / 32 * kRun, &grid)) != cudaSuccess) return e;
-    (a.x_bf16 ? k_encode_narrow<true> : k_encode_narrow<false>)<<<grid, kThreads, 0, s>>>(
-        a, make_divisor(nb, a.rows * nb), a.rows * nb);
+    const int64_t blocks = a.rows * nb;
+    const auto kernel = a.x_bf16 ? k_encode_narrow<true> : k_encode_narrow<false>;
+    const cudaError_t e = grid_for(kernel, cache[2 + a.x_bf16], blocks, kThreads / 32 * kRun, &grid);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, 0, s>>>(a, make_divisor(nb, blocks), blocks);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_ckpt_decode(const DecodeArgs& in, cudaStream_t s) {
+  static LayerGrid cache[6];
   DecodeArgs a = in;
+  const bool plain = a.act == LOCO_ACT_NONE && a.gamma == nullptr && a.beta == nullptr;
   if (a.rows > 1 && a.ldo == a.cols && a.cols % kCkptBlock == 0 && a.gamma == nullptr && a.beta == nullptr)
     a.ldo = a.cols *= a.rows, a.rows = 1;  // one long row
   const int64_t nb = (a.cols + kCkptBlock - 1) / kCkptBlock;
   unsigned grid;
-  cudaError_t e;
   if (wide_rows(a.out, a.ldo, a.rows, a.out_bf16)) {
-    const int64_t halves = a.rows * nb * 2;
-    if ((e = grid_for(halves, kThreads, &grid)) != cudaSuccess) return e;
-    (a.out_bf16 ? k_decode_wide<true> : k_decode_wide<false>)<<<grid, kThreads, 0, s>>>(a, make_divisor(nb * 2, halves),
-                                                                                       halves);
+    const int64_t per = (a.cols + kRunCols - 1) / kRunCols, runs = a.rows * per;
+    const auto kernel = a.out_bf16 ? (plain ? k_decode_wide<true, true> : k_decode_wide<true, false>)
+                                   : (plain ? k_decode_wide<false, true> : k_decode_wide<false, false>);
+    const cudaError_t e = grid_for(kernel, cache[a.out_bf16 * 2 + plain], runs, kThreads / 32, &grid);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, 0, s>>>(a, make_divisor(per, runs), nb, runs);
   } else {
-    if ((e = grid_for(a.rows * nb, kThreads / 32 * kRun, &grid)) != cudaSuccess) return e;
-    (a.out_bf16 ? k_decode_narrow<true> : k_decode_narrow<false>)<<<grid, kThreads, 0, s>>>(
-        a, make_divisor(nb, a.rows * nb), a.rows * nb);
+    const int64_t blocks = a.rows * nb;
+    const auto kernel = a.out_bf16 ? k_decode_narrow<true> : k_decode_narrow<false>;
+    const cudaError_t e = grid_for(kernel, cache[4 + a.out_bf16], blocks, kThreads / 32 * kRun, &grid);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, 0, s>>>(a, make_divisor(nb, blocks), blocks);
   }
   return cudaGetLastError();
 }

@@ -89,6 +89,27 @@ __device__ __forceinline__ void floats8(const Pair v[4], float f[8]) {
   }
 }
 
+// Shared memory by its 32-bit address: sixteen or eight bytes in, sixteen out.
+__device__ __forceinline__ void copy_to_shared16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_to_shared8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 shared8(uint32_t src) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(src) : "memory");
+  return v;
+}
+__device__ __forceinline__ void to_shared16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // One element of an array of bf16 or fp32 (a uniform branch on the type).
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int bf16) {
   return bf16 ? bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p) + i)) : __ldg(static_cast<const float*>(p) + i);
@@ -160,6 +181,14 @@ __device__ __forceinline__ float ckpt_step(uint32_t scale) {
 // The code of v: rint_even(v * inv) clamped to [-127, 127]; 0 for a NaN product (a bad block's).
 __device__ __forceinline__ int ckpt_code(float v, float inv) {
   return __float2int_rn(fminf(fmaxf(inv == 0.0f ? 0.0f : v * inv, -127.0f), 127.0f));
+}
+// Bits of the largest magnitude of a block of which four neighbouring lanes hold eight values each.
+__device__ __forceinline__ uint32_t block_magnitude(const float v[8]) {
+  uint32_t m = mag_bits(v[0]);
+#pragma unroll
+  for (int k = 1; k < 8; ++k) m = max(m, mag_bits(v[k]));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
 // Eight codes of a block whose largest magnitude has the bits `amax`.  v * 2^-e is exact, so adding
 // 1.5 * 2^23 in one fused operation rounds it to an integer (halves to even) whose low byte is the

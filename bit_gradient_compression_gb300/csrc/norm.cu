@@ -71,60 +71,54 @@ __device__ __forceinline__ char* at(void* p, int64_t i, int bf16) { return stati
 
 // ---------------------------------------------------------------------------------------- WIDE: 16-byte pieces
 
-// A thread's 16-byte pieces: piece i of stage s at ring + ((s * pieces + i) * threads + thread) * 16.
-template <int T>
-__device__ __forceinline__ uint4* piece(uint8_t* ring, int pieces, int stage, int i) {
-  return reinterpret_cast<uint4*>(ring) + (stage * pieces + i) * T + threadIdx.x;
-}
-// Starts the copy of a thread's whole vectors of one row: NV pieces (bf16) or 2 NV (fp32) from piece `first`.
-template <int G, int NV>
-__device__ __forceinline__ void copy_row(uint8_t* ring, int pieces, int stage, int first, const char* row, int cols, int t,
-                                         int bf16) {
-  constexpr int T = kCtaThreads<G>;
+// Piece i of a stage lies at stage + (i * threads + thread) * 16, so that a warp's accesses meet no
+// bank twice.  A thread's addresses are kept as running pointers: with 8 columns a piece, computing
+// them anew for each row took more instructions than the values themselves.
+__device__ __forceinline__ Pair bits_pair(uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); }
+
+// Starts the copies of a thread's NV vectors of one row, G vectors apart; `row` points at its first.
+template <int G, int NV, bool BF16>
+__device__ __forceinline__ void copy_row(uint32_t dst, const char* row, const bool (&full)[NV]) {
+  constexpr int T = kCtaThreads<G>, kBytes = BF16 ? 16 : 32;
 #pragma unroll
   for (int e = 0; e < NV; ++e) {
-    const int c0 = (t + G * e) * 8;
-    if (c0 + 8 > cols) continue;
-    if (bf16) {
-      cp_async16(piece<T>(ring, pieces, stage, first + e), row + c0 * 2);
-    } else {
-      cp_async16(piece<T>(ring, pieces, stage, first + 2 * e), row + int64_t(c0) * 4);
-      cp_async16(piece<T>(ring, pieces, stage, first + 2 * e + 1), row + int64_t(c0) * 4 + 16);
-    }
+    if (!full[e]) continue;
+    copy_to_shared16(dst + e * (T * kBytes), row + e * (G * kBytes));
+    if (!BF16) copy_to_shared16(dst + e * (T * kBytes) + T * 16, row + e * (G * kBytes) + 16);
   }
 }
-__device__ __forceinline__ Pair bits_pair(uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); }
-// The vector a row ends in, 0 past the end.  (The kernel may write a row that is also its residual.)
-__device__ __forceinline__ void load_last(const char* row, int cols, int c0, int bf16, Pair v[4]) {
+// The vector a row ends in, 0 past the end; `left` columns of it exist.  (The kernel may write a row
+// that is also its residual.)
+template <bool BF16>
+__device__ __forceinline__ void load_last(const char* at, int left, Pair v[4]) {
   float f[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = c0 + k < cols ? load_elem_rw(row, c0 + k, bf16) : 0.0f;
+  for (int k = 0; k < 8; ++k) f[k] = k < left ? load_elem_rw(at, k, BF16) : 0.0f;
   pairs8(f, v);
 }
-// Vector e of the row that was copied (it begins inside the row).
-template <int G, int NV>
-__device__ __forceinline__ void copied_vec(uint8_t* ring, int pieces, int stage, int first, const char* row, int cols,
-                                           int t, int e, int bf16, Pair v[4]) {
-  constexpr int T = kCtaThreads<G>;
-  const int c0 = (t + G * e) * 8;
-  if (c0 + 8 > cols) {
-    load_last(row, cols, c0, bf16, v);
-  } else if (bf16) {
-    widen8(*piece<T>(ring, pieces, stage, first + e), v);
+// Vector e of the row copied to src.
+template <int G, int NV, bool BF16>
+__device__ __forceinline__ void copied(uint32_t src, int e, const char* row, bool full, int left, Pair v[4]) {
+  constexpr int T = kCtaThreads<G>, kBytes = BF16 ? 16 : 32;
+  if (!full) {
+    load_last<BF16>(row + e * (G * kBytes), left, v);
+  } else if (BF16) {
+    widen8(shared16(src + e * (T * kBytes)), v);
   } else {
-    const uint4 a = *piece<T>(ring, pieces, stage, first + 2 * e), b = *piece<T>(ring, pieces, stage, first + 2 * e + 1);
+    const uint4 a = shared16(src + e * (T * kBytes)), b = shared16(src + e * (T * kBytes) + T * 16);
     v[0] = bits_pair(a.x, a.y), v[1] = bits_pair(a.z, a.w), v[2] = bits_pair(b.x, b.y), v[3] = bits_pair(b.z, b.w);
   }
 }
-__device__ __forceinline__ void store_vec(char* row, int cols, int c0, int bf16, const Pair v[4]) {
+template <bool BF16>
+__device__ __forceinline__ void store_vec(char* at, bool full, int left, const Pair v[4]) {
   float f[8];
   floats8(v, f);
-  if (c0 + 8 <= cols) {
-    store8(row, c0, bf16, f);
+  if (full) {
+    store8(at, 0, BF16, f);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (c0 + k < cols) store_elem(row, c0 + k, bf16, f[k]);
+      if (k < left) store_elem(at, k, BF16, f[k]);
   }
 }
 // Eight values of a parameter vector from column c0 on; `wide`: it starts on a 16-byte boundary.
@@ -144,122 +138,146 @@ __device__ __forceinline__ void load_param(const void* p, int cols, int c0, int 
     pairs8(f, v);
   }
 }
-// 0 in the columns past the row's end.
-__device__ __forceinline__ void clear_past(Pair v[4], int cols, int c0) {
+// 0 in the columns past the row's end, of which `left` are before it.
+__device__ __forceinline__ void clear_past(Pair v[4], int left) {
   float f[8];
   floats8(v, f);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    if (c0 + k >= cols) f[k] = 0.0f;
+    if (k >= left) f[k] = 0.0f;
   pairs8(f, v);
 }
 
 // Stages: the row at work and the next ones.
 constexpr int kFwdStages = 3;
-template <int NV, bool XBF16>
-constexpr int kFwdPieces = NV * (XBF16 ? 1 : 2);
 
-template <int G, int NV, bool XBF16>
-__global__ void __launch_bounds__(kCtaThreads<G>, 768 / kCtaThreads<G>) k_norm_fwd(NormFwdArgs a, bool pwide) {
+// YBF16: type of y.  CTAs per SM: as many as 64 or 80 registers a thread allow.
+template <int G, int NV, bool XBF16, bool YBF16>
+__global__ void __launch_bounds__(kCtaThreads<G>, (NV == 1 ? 1024 : G == 64 ? 640 : 768) / kCtaThreads<G>)
+    k_norm_fwd(NormFwdArgs a, bool pwide) {
   __shared__ float red[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
-  constexpr int kGroups = kCtaThreads<G> / G, kP = kFwdPieces<NV, XBF16>;
+  constexpr int T = kCtaThreads<G>, kGroups = T / G, kX = XBF16 ? 16 : 32, kY = YBF16 ? 16 : 32;
+  constexpr uint32_t kStage = NV * T * kX;
+  constexpr bool kKeep = NV <= 2;  // gamma and beta stay in registers
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const int64_t step = int64_t(gridDim.x) * kGroups, first = int64_t(blockIdx.x) * kGroups + grp;
-  const auto x_row = [&](int64_t row) { return at(a.x, row * a.ldx, XBF16); };
+  bool full[NV], some[NV];
+  Pair gm[NV][4], bt[NV][4];
 #pragma unroll
-  for (int i = 0; i < kFwdStages - 1; ++i) {
-    const int64_t row = first + i * step;
-    if (row < a.rows) copy_row<G, NV>(ring, kP, i, 0, x_row(row), cols, t, XBF16);
-    cp_async_commit();
+  for (int e = 0; e < NV; ++e) {
+    const int c0 = (t + G * e) * 8;
+    full[e] = c0 + 8 <= cols, some[e] = c0 < cols;
+    if constexpr (kKeep) {
+      load_param(a.gamma, cols, c0, a.param_bf16, pwide, 1.0f, gm[e]);
+      load_param(a.beta, cols, c0, a.param_bf16, pwide, 0.0f, bt[e]);
+    }
   }
-  int stage = 0, turn = 0;
-  // the CTA's groups go through the loop together
-  for (int64_t row = first; row - grp < a.rows; row += step) {
-    const bool live = row < a.rows;
-    const int64_t ahead = row + (kFwdStages - 1) * step;
-    if (ahead < a.rows) copy_row<G, NV>(ring, kP, stage == 0 ? kFwdStages - 1 : stage - 1, 0, x_row(ahead), cols, t, XBF16);
+  const float inv_cols = 1.0f / float(cols);
+  const int64_t x_step = step * a.ldx * (XBF16 ? 2 : 4), y_step = step * a.ldy * (YBF16 ? 2 : 4);
+  const char* xp = at(a.x, first * a.ldx, XBF16) + t * kX;  // the row at work
+  const char* xa = xp;                                      // the next to be copied
+  char* yp = at(a.y, first * a.ldy, YBF16) + t * kY;
+  const uint32_t base = smem_addr(ring) + threadIdx.x * 16, end = base + kFwdStages * kStage;
+  uint32_t cur = base, nxt = base;
+  int64_t ahead = first;
+  const auto copy_next = [&]() {
+    if (ahead < a.rows) copy_row<G, NV, XBF16>(nxt, xa, full);
     cp_async_commit();
+    ahead += step, xa += x_step;
+    if ((nxt += kStage) == end) nxt = base;
+  };
+#pragma unroll
+  for (int i = 0; i < kFwdStages - 1; ++i) copy_next();
+  int turn = 0;
+  // the CTA's groups go through the loop together
+  for (int64_t row = first; row - grp < a.rows; row += step, xp += x_step, yp += y_step) {
+    const bool live = row < a.rows;
+    copy_next();
     cp_async_wait<kFwdStages - 1>();
     Pair x[NV][4];
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      if (live && (t + G * e) * 8 < cols) {
-        copied_vec<G, NV>(ring, kP, stage, 0, x_row(row), cols, t, e, XBF16, x[e]);
+      if (some[e] && live) {
+        copied<G, NV, XBF16>(cur, e, xp, full[e], cols - (t + G * e) * 8, x[e]);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[e][k] = pair(0.0f, 0.0f);
       }
     }
-    if (++stage == kFwdStages) stage = 0;
+    if ((cur += kStage) == end) cur = base;
     float mean = 0.0f;
     if (!a.rms) {
-      Pair s2 = pair(0.0f, 0.0f), s3 = s2;
+      Pair s2 = x[0][0] + x[0][1], s3 = x[0][2] + x[0][3];
 #pragma unroll
-      for (int e = 0; e < NV; ++e) s2 = s2 + (x[e][0] + x[e][1]), s3 = s3 + (x[e][2] + x[e][3]);
+      for (int e = 1; e < NV; ++e) s2 = s2 + (x[e][0] + x[e][1]), s3 = s3 + (x[e][2] + x[e][3]);
       const float2 h = halves(s2 + s3);
       float s[1] = {h.x + h.y};
       group_sum<G>(s, red[turn]);
       turn ^= 1;
-      mean = s[0] / float(cols);
-    }
-    const Pair less = pair(-mean, -mean);
-    Pair q2 = pair(0.0f, 0.0f), q3 = q2;
+      mean = s[0] * inv_cols;
+      const Pair less = pair(-mean, -mean);
 #pragma unroll
-    for (int e = 0; e < NV; ++e) {
-      const int c0 = (t + G * e) * 8;
-      if (c0 < cols) {
-        if (!a.rms) {
+      for (int e = 0; e < NV; ++e) {
+        if (!some[e]) continue;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[e][k] = x[e][k] + less;
-          if (c0 + 8 > cols) clear_past(x[e], cols, c0);
-        }
-        q2 = fma(x[e][0], x[e][0], q2), q3 = fma(x[e][1], x[e][1], q3);
-        q2 = fma(x[e][2], x[e][2], q2), q3 = fma(x[e][3], x[e][3], q3);
+        for (int k = 0; k < 4; ++k) x[e][k] = x[e][k] + less;
+        if (!full[e]) clear_past(x[e], cols - (t + G * e) * 8);
       }
+    }
+    Pair q2 = x[0][0] * x[0][0], q3 = x[0][1] * x[0][1];
+    q2 = fma(x[0][2], x[0][2], q2), q3 = fma(x[0][3], x[0][3], q3);
+#pragma unroll
+    for (int e = 1; e < NV; ++e) {
+      q2 = fma(x[e][0], x[e][0], q2), q3 = fma(x[e][1], x[e][1], q3);
+      q2 = fma(x[e][2], x[e][2], q2), q3 = fma(x[e][3], x[e][3], q3);
     }
     const float2 h = halves(q2 + q3);
     float q[1] = {h.x + h.y};
     group_sum<G>(q, red[turn]);
     turn ^= 1;
-    const float rstd = 1.0f / sqrtf(q[0] / float(cols) + a.eps);
+    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv_cols, a.eps));
     if (t == 0 && live) {
       if (a.mean != nullptr && !a.rms) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
     if (!live) continue;  // whole warps
     const Pair r2 = pair(rstd, rstd);
-    char* yr = at(a.y, row * a.ldy, a.y_bf16);
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      const int c0 = (t + G * e) * 8;
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[e][k] = x[e][k] * r2;
-      if (a.codes != nullptr) {
+    }
+    if (a.codes != nullptr) {
+      int8_t* codes = a.codes + row * nb * kCkptBlock + t * 8;
+      uint8_t* scales = a.scales + row * nb + t / 4;
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
         // a block is four lanes, whether or not the row reaches all of them
         float f[8];
         floats8(x[e], f);
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = max(m, mag_bits(f[k]));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        if (c0 < nb * kCkptBlock) {
-          *reinterpret_cast<uint2*>(a.codes + row * nb * kCkptBlock + c0) = ckpt_pack8(f, m);
-          if ((c0 & 31) == 0) a.scales[row * nb + c0 / kCkptBlock] = uint8_t(ckpt_scale(m));
+        const uint32_t m = block_magnitude(f);
+        if ((t + G * e) / 4 < nb) {
+          *reinterpret_cast<uint2*>(codes + e * (G * 8)) = ckpt_pack8(f, m);
+          if ((t & 3) == 0) scales[e * (G / 4)] = uint8_t(ckpt_scale(m));
         }
       }
-      if (c0 < cols) {
-        if (a.gamma != nullptr || a.beta != nullptr) {
-          Pair g[4], b[4];
-          load_param(a.gamma, cols, c0, a.param_bf16, pwide, 1.0f, g);
-          load_param(a.beta, cols, c0, a.param_bf16, pwide, 0.0f, b);
+    }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[e][k] = fma(x[e][k], g[k], b[k]);
-        }
-        store_vec(yr, cols, c0, a.y_bf16, x[e]);
+    for (int e = 0; e < NV; ++e) {
+      if (!some[e]) continue;
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[e][k] = fma(x[e][k], gm[e][k], bt[e][k]);
+      } else {
+        Pair g[4], b[4];
+        load_param(a.gamma, cols, (t + G * e) * 8, a.param_bf16, pwide, 1.0f, g);
+        load_param(a.beta, cols, (t + G * e) * 8, a.param_bf16, pwide, 0.0f, b);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[e][k] = fma(x[e][k], g[k], b[k]);
       }
+      store_vec<YBF16>(yp + e * (G * kY), full[e], cols - (t + G * e) * 8, x[e]);
     }
   }
 }
@@ -453,52 +471,76 @@ __device__ __forceinline__ void write_partials(const NormBwdArgs& a, float* sum,
   }
 }
 
-// 16-byte pieces of one stage: dy, then x (or codes: half a piece per vector), then the residual
-// (fp32 takes two per vector).
-template <int NV>
-__host__ __device__ __forceinline__ int bwd_pieces(int y_bf16, int x_bf16, bool ckpt, bool residual) {
-  return NV * ((y_bf16 ? 1 : 2) + (ckpt || x_bf16 ? 1 : 2) + (residual ? (x_bf16 ? 1 : 2) : 0));
-}
 // As many rows ahead as shared memory holds for the widest types (a row of 8192 fp32 columns with
 // fp32 dy and residual takes 96 KB).
-template <int G, bool XBF16>
-constexpr int kBwdStages = G == 512 && !XBF16 ? 2 : 3;
+template <int G, bool XBF16, bool YBF16>
+constexpr int kBwdStages = G == 512 && !(XBF16 && YBF16) ? 2 : 3;
 
-template <int G, int NV, bool XBF16, bool CKPT>
+template <int G, int NV, bool XBF16, bool YBF16, bool CKPT>
 __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (NV == 1 ? 768 : 512) / kCtaThreads<G>)
     k_norm_bwd(NormBwdArgs a, bool pwide) {
   __shared__ float red[2][64];
   extern __shared__ __align__(16) uint8_t ring[];  // the stages, and gamma; after the rows, [2][cols] sums
-  constexpr int T = kCtaThreads<G>, kGroups = T / G, kStages = kBwdStages<G, XBF16>;
+  constexpr int T = kCtaThreads<G>, kGroups = T / G, kStages = kBwdStages<G, XBF16, YBF16>;
+  constexpr int kX = XBF16 ? 16 : 32, kY = YBF16 ? 16 : 32;
+  constexpr uint32_t at_x = NV * T * kY, at_r = at_x + NV * T * (CKPT ? 16 : kX);
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const int64_t step = int64_t(gridDim.x) * kGroups, first = int64_t(blockIdx.x) * kGroups + grp;
-  const int pieces = bwd_pieces<NV>(a.y_bf16, XBF16, CKPT, a.residual != nullptr);
-  const int at_x = NV * (a.y_bf16 ? 1 : 2), at_r = at_x + NV * (CKPT || XBF16 ? 1 : 2);
-  // gamma: each thread's own values in shared memory behind the stages
-  ulonglong2* gamma = reinterpret_cast<ulonglong2*>(piece<T>(ring, pieces, kStages, 0));
+  const bool with_r = a.residual != nullptr;
+  const uint32_t stage_bytes = at_r + (with_r ? NV * T * kX : 0);
+  const uint32_t base = smem_addr(ring) + threadIdx.x * 16, end = base + kStages * stage_bytes;
+  const uint32_t gamma = end;  // each thread's own values behind the stages
+  bool full[NV], some[NV];
   Pair dg[NV][4], db[NV][4];
 #pragma unroll
   for (int e = 0; e < NV; ++e) {
+    const int c0 = (t + G * e) * 8;
+    full[e] = c0 + 8 <= cols, some[e] = c0 < cols;
     Pair v[4];
-    load_param(a.gamma, cols, (t + G * e) * 8, a.param_bf16, pwide, 1.0f, v);
-    gamma[2 * e * T] = make_ulonglong2(v[0].u, v[1].u);
-    gamma[(2 * e + 1) * T] = make_ulonglong2(v[2].u, v[3].u);
+    load_param(a.gamma, cols, c0, a.param_bf16, pwide, 1.0f, v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 lo = halves(v[2 * i]), hi = halves(v[2 * i + 1]);
+      to_shared16(gamma + (2 * e + i) * T * 16, make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y),
+                                                           __float_as_uint(hi.x), __float_as_uint(hi.y)));
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) dg[e][k] = db[e][k] = pair(0.0f, 0.0f);
   }
-  const auto copy = [&](int64_t row, int stage) {
-    copy_row<G, NV>(ring, pieces, stage, 0, at(a.dy, row * a.lddy, a.y_bf16), cols, t, a.y_bf16);
-    if constexpr (CKPT) {
+  const float inv_cols = 1.0f / float(cols);
+  const int64_t x_step = step * a.ldx * (XBF16 ? 2 : 4), r_step = step * a.ldr * (XBF16 ? 2 : 4);
+  const int64_t d_step = step * a.lddy * (YBF16 ? 2 : 4), o_step = step * a.lddx * (XBF16 ? 2 : 4);
+  const int64_t c_step = step * nb * kCkptBlock;
+  // the row at work, and the next to be copied
+  const char* dp = at(a.dy, first * a.lddy, YBF16) + t * kY;
+  const char* xp = CKPT ? nullptr : at(a.x, first * a.ldx, XBF16) + t * kX;
+  const char* rp = with_r ? at(a.residual, first * a.ldr, XBF16) + t * kX : nullptr;
+  char* op = at(a.dx, first * a.lddx, XBF16) + t * kX;
+  const char *da = dp, *xa = xp, *ra = rp;
+  const int8_t* ca = CKPT ? a.codes + first * nb * kCkptBlock + t * 8 : nullptr;
+  uint32_t cur = base, nxt = base;
+  int64_t ahead = first;
+  const auto copy_next = [&]() {
+    if (ahead < a.rows) {
+      copy_row<G, NV, YBF16>(nxt, da, full);
+      if constexpr (CKPT) {
 #pragma unroll
-      for (int e = 0; e < NV; ++e)  // the padding of a ragged block is part of it
-        if ((t + G * e) * 8 < cols)
-          cp_async8(piece<T>(ring, pieces, stage, at_x + e), a.codes + row * nb * kCkptBlock + (t + G * e) * 8);
-    } else {
-      copy_row<G, NV>(ring, pieces, stage, at_x, at(a.x, row * a.ldx, XBF16), cols, t, XBF16);
+        for (int e = 0; e < NV; ++e)  // the padding of a ragged block is part of it
+          if (some[e]) copy_to_shared8(nxt + at_x + e * (T * 16), ca + e * (G * 8));
+      } else {
+        copy_row<G, NV, XBF16>(nxt + at_x, xa, full);
+      }
+      if (with_r) copy_row<G, NV, XBF16>(nxt + at_r, ra, full);
     }
-    if (a.residual != nullptr)
-      copy_row<G, NV>(ring, pieces, stage, at_r, at(a.residual, row * a.ldr, XBF16), cols, t, XBF16);
+    cp_async_commit();
+    ahead += step, da += d_step;
+    if constexpr (CKPT)
+      ca += c_step;
+    else
+      xa += x_step;
+    if (with_r) ra += r_step;
+    if ((nxt += stage_bytes) == end) nxt = base;
   };
   // What of the next row goes to registers: its statistics and scales.
   float next_rstd = 0.0f, next_mean = 0.0f;
@@ -508,22 +550,16 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     if (!CKPT && !a.rms) next_mean = __ldg(a.mean + row);
     if constexpr (CKPT) {
 #pragma unroll
-      for (int e = 0; e < NV; ++e)
-        next_scale[e] = (t + G * e) * 8 < cols ? __ldg(a.scales + row * nb + (t + G * e) / 4) : 1u;
+      for (int e = 0; e < NV; ++e) next_scale[e] = some[e] ? __ldg(a.scales + row * nb + (t + G * e) / 4) : 1u;
     }
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (first + i * step < a.rows) copy(first + i * step, i);
-    cp_async_commit();
-  }
+  for (int i = 0; i < kStages - 1; ++i) copy_next();
   if (first < a.rows) load(first);
-  int stage = 0, turn = 0;
+  int turn = 0;
   for (int64_t row = first; row - grp < a.rows; row += step) {
     const bool live = row < a.rows;
-    const int64_t ahead = row + (kStages - 1) * step;
-    if (ahead < a.rows) copy(ahead, stage == 0 ? kStages - 1 : stage - 1);
-    cp_async_commit();
+    copy_next();
     cp_async_wait<kStages - 1>();
     const float rstd = next_rstd;
     const Pair r2 = pair(rstd, rstd), m2 = pair(-next_mean * rstd, -next_mean * rstd);
@@ -534,27 +570,28 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     }
     // dy, the normalised values and gamma of vector e, read from shared memory before and after the sums
     const auto values = [&](int e, Pair (&d)[4], Pair (&xh)[4], Pair (&gm)[4]) {
-      const int c0 = (t + G * e) * 8;
-      copied_vec<G, NV>(ring, pieces, stage, 0, at(a.dy, row * a.lddy, a.y_bf16), cols, t, e, a.y_bf16, d);
+      const int left = cols - (t + G * e) * 8;
+      copied<G, NV, YBF16>(cur, e, dp, full[e], left, d);
       if constexpr (CKPT) {
-        const uint2 w = *reinterpret_cast<const uint2*>(piece<T>(ring, pieces, stage, at_x + e));
+        const uint2 w = shared8(cur + at_x + e * (T * 16));
         ckpt_pairs4(w.x, scale[e], xh);
         ckpt_pairs4(w.y, scale[e], xh + 2);
       } else {
-        copied_vec<G, NV>(ring, pieces, stage, at_x, at(a.x, row * a.ldx, XBF16), cols, t, e, XBF16, xh);
+        copied<G, NV, XBF16>(cur + at_x, e, xp, full[e], left, xh);
 #pragma unroll
         for (int k = 0; k < 4; ++k) xh[k] = fma(xh[k], r2, m2);
       }
-      if (c0 + 8 > cols) clear_past(xh, cols, c0);  // (a bad block's padding reads back as NaN)
-      const ulonglong2 lo = gamma[2 * e * T], hi = gamma[(2 * e + 1) * T];
-      gm[0].u = lo.x, gm[1].u = lo.y, gm[2].u = hi.x, gm[3].u = hi.y;
+      if (!full[e]) clear_past(xh, left);  // (a bad block's padding reads back as NaN)
+      const uint4 lo = shared16(gamma + 2 * e * T * 16), hi = shared16(gamma + (2 * e + 1) * T * 16);
+      gm[0] = bits_pair(lo.x, lo.y), gm[1] = bits_pair(lo.z, lo.w);
+      gm[2] = bits_pair(hi.x, hi.y), gm[3] = bits_pair(hi.z, hi.w);
     };
     float s[2] = {0.0f, 0.0f};
     if (live) {
       Pair s0 = pair(0.0f, 0.0f), s1 = s0;
 #pragma unroll
       for (int e = 0; e < NV; ++e) {
-        if ((t + G * e) * 8 >= cols) continue;
+        if (!some[e]) continue;
         Pair d[4], xh[4], gm[4];
         values(e, d, xh, gm);
 #pragma unroll
@@ -574,27 +611,27 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     turn ^= 1;
     if (live) {
       // dx = r (g - c1 - xhat c2) + residual
-      const float c1 = a.rms ? 0.0f : s[0] / float(cols) * -rstd, c2 = s[1] / float(cols) * -rstd;
+      const float c1 = a.rms ? 0.0f : s[0] * inv_cols * -rstd, c2 = s[1] * inv_cols * -rstd;
       const Pair k1 = pair(c1, c1), k2 = pair(c2, c2);
-      char* dxr = at(a.dx, row * a.lddx, XBF16);
 #pragma unroll
       for (int e = 0; e < NV; ++e) {
-        const int c0 = (t + G * e) * 8;
-        if (c0 >= cols) continue;
+        if (!some[e]) continue;
         Pair d[4], xh[4], gm[4], r[4];
         values(e, d, xh, gm);
-        if (a.residual != nullptr) {
-          copied_vec<G, NV>(ring, pieces, stage, at_r, at(a.residual, row * a.ldr, XBF16), cols, t, e, XBF16, r);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) r[k] = r[k] + fma(xh[k], k2, fma(d[k] * gm[k], r2, k1));
-        } else {
+        for (int k = 0; k < 4; ++k) d[k] = fma(xh[k], k2, fma(d[k] * gm[k], r2, k1));
+        if (with_r) {
+          copied<G, NV, XBF16>(cur + at_r, e, rp, full[e], cols - (t + G * e) * 8, r);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) r[k] = fma(xh[k], k2, fma(d[k] * gm[k], r2, k1));
+          for (int k = 0; k < 4; ++k) d[k] = d[k] + r[k];
         }
-        store_vec(dxr, cols, c0, XBF16, r);
+        store_vec<XBF16>(op + e * (G * kX), full[e], cols - (t + G * e) * 8, d);
       }
     }
-    if (++stage == kStages) stage = 0;
+    dp += d_step, op += o_step;
+    if (!CKPT) xp += x_step;
+    if (with_r) rp += r_step;
+    if ((cur += stage_bytes) == end) cur = base;
   }
   if (a.partials == nullptr) return;
   cp_async_wait<0>();
@@ -763,45 +800,52 @@ bool wide_rows(const void* p, int64_t ld, int64_t rows, int bf16) {
 bool wide_vec(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Narrow kernels hold half as many columns a thread, in groups of twice the threads.
-template <int G, int NV>
-cudaError_t fwd(const NormFwdArgs& a, bool wide, bool pwide, cudaStream_t s) {
-  static LayerGrid cache[4];
-  constexpr int T = kCtaThreads<G>;
+template <int G, int NV, bool XBF16, bool YBF16>
+cudaError_t fwd_launch(const NormFwdArgs& a, bool wide, bool pwide, cudaStream_t s) {
+  static LayerGrid cache[2];
+  constexpr int H = NV == 1 ? G : 2 * G, NE = NV == 1 ? 8 : NV * 4;
+  const int T = wide ? kCtaThreads<G> : kCtaThreads<H>, groups = T / (wide ? G : H);
+  const auto wide_kernel = k_norm_fwd<G, NV, XBF16, YBF16>;
+  const auto narrow_kernel = k_norm_fwd_narrow<H, NE, XBF16>;
+  const size_t sm = wide ? size_t(kFwdStages) * NV * kCtaThreads<G> * (XBF16 ? 16 : 32) : 0;
   int cap = 0;
-  if (wide) {
-    const auto kernel = a.x_bf16 ? k_norm_fwd<G, NV, true> : k_norm_fwd<G, NV, false>;
-    const size_t sm = size_t(kFwdStages) * (a.x_bf16 ? kFwdPieces<NV, true> : kFwdPieces<NV, false>) * T * 16;
-    const cudaError_t e = layer_grid(cache[a.x_bf16], reinterpret_cast<const void*>(kernel), T, sm, sm, &cap);
-    if (e != cudaSuccess) return e;
-    const int64_t want = (a.rows + T / G - 1) / (T / G);
-    kernel<<<unsigned(want < cap ? want : cap), T, sm, s>>>(a, pwide);
-  } else {
-    constexpr int H = NV == 1 ? G : 2 * G, NE = NV == 1 ? 8 : NV * 4, TN = kCtaThreads<H>;
-    const auto kernel = a.x_bf16 ? k_norm_fwd_narrow<H, NE, true> : k_norm_fwd_narrow<H, NE, false>;
-    const cudaError_t e = layer_grid(cache[2 + a.x_bf16], reinterpret_cast<const void*>(kernel), TN, 0, 0, &cap);
-    if (e != cudaSuccess) return e;
-    const int64_t want = (a.rows + TN / H - 1) / (TN / H);
-    kernel<<<unsigned(want < cap ? want : cap), TN, 0, s>>>(a);
-  }
+  const cudaError_t e = wide ? layer_grid(cache[0], reinterpret_cast<const void*>(wide_kernel), T, sm, sm, &cap)
+                             : layer_grid(cache[1], reinterpret_cast<const void*>(narrow_kernel), T, sm, sm, &cap);
+  if (e != cudaSuccess) return e;
+  const int64_t want = (a.rows + groups - 1) / groups;
+  const unsigned grid = unsigned(want < cap ? want : cap);
+  if (wide)
+    wide_kernel<<<grid, T, sm, s>>>(a, pwide);
+  else
+    narrow_kernel<<<grid, T, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-template <int G, int NV, bool XBF16, bool CKPT>
+template <int G, int NV>
+cudaError_t fwd(const NormFwdArgs& a, bool wide, bool pwide, cudaStream_t s) {
+  if (a.x_bf16)
+    return a.y_bf16 ? fwd_launch<G, NV, true, true>(a, wide, pwide, s) : fwd_launch<G, NV, true, false>(a, wide, pwide, s);
+  return a.y_bf16 ? fwd_launch<G, NV, false, true>(a, wide, pwide, s) : fwd_launch<G, NV, false, false>(a, wide, pwide, s);
+}
+
+template <int G, int NV, bool XBF16, bool YBF16, bool CKPT>
 cudaError_t bwd_launch(const NormBwdArgs& a, bool wide, bool pwide, int* parts, cudaStream_t s) {
-  static LayerGrid cache[5];  // wide: occupancy depends on the stage's size, of which there are four
+  static LayerGrid cache[3];  // wide: occupancy depends on whether a stage holds a residual
   constexpr int H = NV == 1 ? G : 2 * G, NE = NV == 1 ? 8 : NV * 4;
-  const auto wide_kernel = k_norm_bwd<G, NV, XBF16, CKPT>;
+  const auto wide_kernel = k_norm_bwd<G, NV, XBF16, YBF16, CKPT>;
   const auto narrow_kernel = k_norm_bwd_narrow<H, NE, XBF16, CKPT>;
   const int T = wide ? kCtaThreads<G> : kCtaThreads<H>, groups = T / (wide ? G : H);
-  const auto bytes = [](int y_bf16, bool residual) {
-    return (size_t(kBwdStages<G, XBF16>) * bwd_pieces<NV>(y_bf16, XBF16, CKPT, residual) + 2 * NV) * kCtaThreads<G> * 16;
+  const auto bytes = [](bool residual) {
+    constexpr int kX = XBF16 ? 16 : 32, kY = YBF16 ? 16 : 32;
+    return size_t(NV) * kCtaThreads<G> *
+           (kBwdStages<G, XBF16, YBF16> * (kY + (CKPT ? 16 : kX) + (residual ? kX : 0)) + 32);
   };
-  static_assert(kCtaThreads<G> * 16 * 2 >= G * 8 * 8 || kCtaThreads<G> == G, "the sums fit where the stages were");
-  const size_t sm = wide ? bytes(a.y_bf16, a.residual != nullptr) : size_t(groups > 1 ? H * NE * 8 : 0);
+  static_assert(kCtaThreads<G> == G || 2 * kCtaThreads<G> * 16 >= 2 * G * 8 * 4, "the sums fit where the stages were");
+  const size_t sm = wide ? bytes(a.residual != nullptr) : size_t(groups > 1 ? H * NE * 8 : 0);
   int cap = 0;
-  const cudaError_t e = wide ? layer_grid(cache[(a.y_bf16 ? 1 : 0) + (a.residual != nullptr ? 2 : 0)],
-                                          reinterpret_cast<const void*>(wide_kernel), T, sm, bytes(0, true), &cap)
-                             : layer_grid(cache[4], reinterpret_cast<const void*>(narrow_kernel), T, sm, sm, &cap);
+  const cudaError_t e = wide ? layer_grid(cache[a.residual != nullptr], reinterpret_cast<const void*>(wide_kernel), T, sm,
+                                          bytes(true), &cap)
+                             : layer_grid(cache[2], reinterpret_cast<const void*>(narrow_kernel), T, sm, sm, &cap);
   if (e != cudaSuccess) return e;
   if (cap > kNormPartials) cap = kNormPartials;
   const int64_t want = (a.rows + groups - 1) / groups;
@@ -813,12 +857,18 @@ cudaError_t bwd_launch(const NormBwdArgs& a, bool wide, bool pwide, int* parts, 
   return cudaGetLastError();
 }
 
+template <int G, int NV, bool XBF16>
+cudaError_t bwd_y(const NormBwdArgs& a, bool wide, bool pwide, int* parts, cudaStream_t s) {
+  const bool ck = a.x == nullptr;
+  if (a.y_bf16)
+    return ck ? bwd_launch<G, NV, XBF16, true, true>(a, wide, pwide, parts, s)
+              : bwd_launch<G, NV, XBF16, true, false>(a, wide, pwide, parts, s);
+  return ck ? bwd_launch<G, NV, XBF16, false, true>(a, wide, pwide, parts, s)
+            : bwd_launch<G, NV, XBF16, false, false>(a, wide, pwide, parts, s);
+}
 template <int G, int NV>
 cudaError_t bwd(const NormBwdArgs& a, bool wide, bool pwide, int* parts, cudaStream_t s) {
-  const bool ck = a.x == nullptr;
-  if (a.x_bf16)
-    return ck ? bwd_launch<G, NV, true, true>(a, wide, pwide, parts, s) : bwd_launch<G, NV, true, false>(a, wide, pwide, parts, s);
-  return ck ? bwd_launch<G, NV, false, true>(a, wide, pwide, parts, s) : bwd_launch<G, NV, false, false>(a, wide, pwide, parts, s);
+  return a.x_bf16 ? bwd_y<G, NV, true>(a, wide, pwide, parts, s) : bwd_y<G, NV, false>(a, wide, pwide, parts, s);
 }
 
 }  // namespace
@@ -831,8 +881,8 @@ cudaError_t launch_norm_forward(const NormFwdArgs& a, cudaStream_t s) {
   if (pitch <= 512) return fwd<32, 2>(a, wide, pwide, s);
   if (pitch <= 1024) return fwd<64, 2>(a, wide, pwide, s);
   if (pitch <= 2048) return fwd<128, 2>(a, wide, pwide, s);
-  if (pitch <= 4096) return fwd<128, 4>(a, wide, pwide, s);
-  if (pitch <= 8192) return fwd<256, 4>(a, wide, pwide, s);
+  if (pitch <= 4096) return fwd<256, 2>(a, wide, pwide, s);
+  if (pitch <= 8192) return fwd<512, 2>(a, wide, pwide, s);
   if (pitch <= 16384) return fwd<512, 4>(a, wide, pwide, s);
   (a.x_bf16 ? k_norm_fwd_long<true> : k_norm_fwd_long<false>)<<<unsigned(a.rows), kLoop, 0, s>>>(a);
   return cudaGetLastError();
