@@ -96,12 +96,12 @@ __device__ __forceinline__ void load_last(const char* at, int left, Pair v[4]) {
   for (int k = 0; k < 8; ++k) f[k] = k < left ? load_elem_rw(at, k, BF16) : 0.0f;
   pairs8(f, v);
 }
-// Vector e of the row copied to src.
-template <int G, int NV, bool BF16>
-__device__ __forceinline__ void copied(uint32_t src, int e, const char* row, bool full, int left, Pair v[4]) {
+// Vector e of the row copied to src; row() is its place in memory.
+template <int G, int NV, bool BF16, typename Row>
+__device__ __forceinline__ void copied(uint32_t src, int e, Row row, bool full, int left, Pair v[4]) {
   constexpr int T = kCtaThreads<G>, kBytes = BF16 ? 16 : 32;
   if (!full) {
-    load_last<BF16>(row + e * (G * kBytes), left, v);
+    load_last<BF16>(row() + e * (G * kBytes), left, v);
   } else if (BF16) {
     widen8(shared16(src + e * (T * kBytes)), v);
   } else {
@@ -153,7 +153,7 @@ constexpr int kFwdStages = 3;
 
 // YBF16: type of y.  CTAs per SM: as many as 64 or 80 registers a thread allow.
 template <int G, int NV, bool XBF16, bool YBF16>
-__global__ void __launch_bounds__(kCtaThreads<G>, (NV == 1 ? 1024 : G == 64 ? 640 : 768) / kCtaThreads<G>)
+__global__ void __launch_bounds__(kCtaThreads<G>, (NV == 1 ? 1024 : G <= 64 ? 640 : 768) / kCtaThreads<G>)
     k_norm_fwd(NormFwdArgs a, bool pwide) {
   __shared__ float red[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, (NV == 1 ? 1024 : G == 64 ? 64
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
       if (some[e] && live) {
-        copied<G, NV, XBF16>(cur, e, xp, full[e], cols - (t + G * e) * 8, x[e]);
+        copied<G, NV, XBF16>(cur, e, [&] { return xp; }, full[e], cols - (t + G * e) * 8, x[e]);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[e][k] = pair(0.0f, 0.0f);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, (NV == 1 ? 1024 : G == 64 ? 64
     float q[1] = {h.x + h.y};
     group_sum<G>(q, red[turn]);
     turn ^= 1;
-    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv_cols, a.eps));
+    const float rstd = rsqrtf(fmaf(q[0], inv_cols, a.eps));
     if (t == 0 && live) {
       if (a.mean != nullptr && !a.rms) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, 768 / kCtaThreads<G>) k_norm_f
     q[0] += q1;
     group_sum<G>(q, red[turn]);
     turn ^= 1;
-    const float rstd = 1.0f / sqrtf(q[0] / float(cols) + a.eps);
+    const float rstd = rsqrtf(q[0] / float(cols) + a.eps);
     if (t == 0 && live) {
       if (a.mean != nullptr && !a.rms) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kLoop) k_norm_fwd_long(NormFwdArgs a) {
     q[0] = fmaf(d, d, q[0]);
   }
   group_sum<kLoop>(q, red[1]);
-  const float rstd = 1.0f / sqrtf(q[0] / float(cols) + a.eps);
+  const float rstd = rsqrtf(q[0] / float(cols) + a.eps);
   if (threadIdx.x == 0) {
     if (a.mean != nullptr && !a.rms) a.mean[row] = mean;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -509,38 +509,25 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     for (int k = 0; k < 4; ++k) dg[e][k] = db[e][k] = pair(0.0f, 0.0f);
   }
   const float inv_cols = 1.0f / float(cols);
-  const int64_t x_step = step * a.ldx * (XBF16 ? 2 : 4), r_step = step * a.ldr * (XBF16 ? 2 : 4);
-  const int64_t d_step = step * a.lddy * (YBF16 ? 2 : 4), o_step = step * a.lddx * (XBF16 ? 2 : 4);
-  const int64_t c_step = step * nb * kCkptBlock;
-  // the row at work, and the next to be copied
-  const char* dp = at(a.dy, first * a.lddy, YBF16) + t * kY;
-  const char* xp = CKPT ? nullptr : at(a.x, first * a.ldx, XBF16) + t * kX;
-  const char* rp = with_r ? at(a.residual, first * a.ldr, XBF16) + t * kX : nullptr;
-  char* op = at(a.dx, first * a.lddx, XBF16) + t * kX;
-  const char *da = dp, *xa = xp, *ra = rp;
-  const int8_t* ca = CKPT ? a.codes + first * nb * kCkptBlock + t * 8 : nullptr;
-  uint32_t cur = base, nxt = base;
-  int64_t ahead = first;
-  const auto copy_next = [&]() {
+  // the thread's place in a row of each matrix
+  const auto dy_at = [&](int64_t row) { return at(a.dy, row * a.lddy, YBF16) + t * kY; };
+  const auto x_at = [&](int64_t row) { return at(a.x, row * a.ldx, XBF16) + t * kX; };
+  const auto r_at = [&](int64_t row) { return at(a.residual, row * a.ldr, XBF16) + t * kX; };
+  uint32_t cur = base;
+  const auto copy_next = [&](int64_t ahead, uint32_t nxt) {
     if (ahead < a.rows) {
-      copy_row<G, NV, YBF16>(nxt, da, full);
+      copy_row<G, NV, YBF16>(nxt, dy_at(ahead), full);
       if constexpr (CKPT) {
+        const int8_t* codes = a.codes + ahead * nb * kCkptBlock + t * 8;
 #pragma unroll
         for (int e = 0; e < NV; ++e)  // the padding of a ragged block is part of it
-          if (some[e]) copy_to_shared8(nxt + at_x + e * (T * 16), ca + e * (G * 8));
+          if (some[e]) copy_to_shared8(nxt + at_x + e * (T * 16), codes + e * (G * 8));
       } else {
-        copy_row<G, NV, XBF16>(nxt + at_x, xa, full);
+        copy_row<G, NV, XBF16>(nxt + at_x, x_at(ahead), full);
       }
-      if (with_r) copy_row<G, NV, XBF16>(nxt + at_r, ra, full);
+      if (with_r) copy_row<G, NV, XBF16>(nxt + at_r, r_at(ahead), full);
     }
     cp_async_commit();
-    ahead += step, da += d_step;
-    if constexpr (CKPT)
-      ca += c_step;
-    else
-      xa += x_step;
-    if (with_r) ra += r_step;
-    if ((nxt += stage_bytes) == end) nxt = base;
   };
   // What of the next row goes to registers: its statistics and scales.
   float next_rstd = 0.0f, next_mean = 0.0f;
@@ -554,12 +541,12 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     }
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) copy_next();
+  for (int i = 0; i < kStages - 1; ++i) copy_next(first + i * step, base + i * stage_bytes);
   if (first < a.rows) load(first);
   int turn = 0;
   for (int64_t row = first; row - grp < a.rows; row += step) {
     const bool live = row < a.rows;
-    copy_next();
+    copy_next(row + (kStages - 1) * step, (cur == base ? end : cur) - stage_bytes);
     cp_async_wait<kStages - 1>();
     const float rstd = next_rstd;
     const Pair r2 = pair(rstd, rstd), m2 = pair(-next_mean * rstd, -next_mean * rstd);
@@ -571,13 +558,13 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     // dy, the normalised values and gamma of vector e, read from shared memory before and after the sums
     const auto values = [&](int e, Pair (&d)[4], Pair (&xh)[4], Pair (&gm)[4]) {
       const int left = cols - (t + G * e) * 8;
-      copied<G, NV, YBF16>(cur, e, dp, full[e], left, d);
+      copied<G, NV, YBF16>(cur, e, [&] { return dy_at(row); }, full[e], left, d);
       if constexpr (CKPT) {
         const uint2 w = shared8(cur + at_x + e * (T * 16));
         ckpt_pairs4(w.x, scale[e], xh);
         ckpt_pairs4(w.y, scale[e], xh + 2);
       } else {
-        copied<G, NV, XBF16>(cur + at_x, e, xp, full[e], left, xh);
+        copied<G, NV, XBF16>(cur + at_x, e, [&] { return x_at(row); }, full[e], left, xh);
 #pragma unroll
         for (int k = 0; k < 4; ++k) xh[k] = fma(xh[k], r2, m2);
       }
@@ -610,6 +597,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     group_sum<G>(s, red[turn]);
     turn ^= 1;
     if (live) {
+      char* op = at(a.dx, row * a.lddx, XBF16) + t * kX;
       // dx = r (g - c1 - xhat c2) + residual
       const float c1 = a.rms ? 0.0f : s[0] * inv_cols * -rstd, c2 = s[1] * inv_cols * -rstd;
       const Pair k1 = pair(c1, c1), k2 = pair(c2, c2);
@@ -621,16 +609,13 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
 #pragma unroll
         for (int k = 0; k < 4; ++k) d[k] = fma(xh[k], k2, fma(d[k] * gm[k], r2, k1));
         if (with_r) {
-          copied<G, NV, XBF16>(cur + at_r, e, rp, full[e], cols - (t + G * e) * 8, r);
+          copied<G, NV, XBF16>(cur + at_r, e, [&] { return r_at(row); }, full[e], cols - (t + G * e) * 8, r);
 #pragma unroll
           for (int k = 0; k < 4; ++k) d[k] = d[k] + r[k];
         }
         store_vec<XBF16>(op + e * (G * kX), full[e], cols - (t + G * e) * 8, d);
       }
     }
-    dp += d_step, op += o_step;
-    if (!CKPT) xp += x_step;
-    if (with_r) rp += r_step;
     if ((cur += stage_bytes) == end) cur = base;
   }
   if (a.partials == nullptr) return;
@@ -649,7 +634,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
 }
 
 template <int G, int NE, bool XBF16, bool CKPT>
-__global__ void __launch_bounds__(kCtaThreads<G>, 512 / kCtaThreads<G>) k_norm_bwd_narrow(NormBwdArgs a) {
+__global__ void __launch_bounds__(kCtaThreads<G>, (G >= 512 ? 1024 : 512) / kCtaThreads<G>) k_norm_bwd_narrow(NormBwdArgs a) {
   __shared__ float red[2][64];
   extern __shared__ float sums[];  // [2][cols] where a CTA holds several groups
   constexpr int kGroups = kCtaThreads<G> / G;
