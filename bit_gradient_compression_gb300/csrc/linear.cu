@@ -35,13 +35,13 @@ constexpr int kChunkPitch = 36;                // floats per row of 32 columns: 
 
 __device__ unsigned long long g_timeouts;
 
-template <int BN, bool LOADERS>
+template <int BN, bool LOADERS, bool PAIR>
 struct Shape {
   // Epilogue warps: two per quarter of the accumulator's lanes, or one where loader warps need the registers.
   static constexpr int kEpi = LOADERS ? 4 : 8;
   static constexpr int kWarps = 4 + kEpi + (LOADERS ? kLoadWarps : 0);
   static constexpr int kStageOut = kEpi * kChunk * kChunkPitch * 4;
-  static constexpr int kABytes = kTileM * kTileK * 2, kBBytes = BN * kTileK * 2, kStage = kABytes + kBBytes;
+  static constexpr int kABytes = kTileM * kTileK * 2, kBRows = PAIR ? BN / 2 : BN, kBBytes = kBRows * kTileK * 2, kStage = kABytes + kBBytes;
   static constexpr int kStages = 200 * 1024 / kStage;
   static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
   static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 256 + kStageOut;
@@ -292,11 +292,11 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
 
 // ------------------------------------------------------------------ the kernel
 
-template <int BN, bool LOADERS>
-__global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
+template <int BN, bool LOADERS, bool PAIR>
+__global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
     k_linear(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
              const __grid_constant__ Params p) {
-  using S = Shape<BN, LOADERS>;
+  using S = Shape<BN, LOADERS, PAIR>;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t bars = base + S::kStages * S::kStage;
@@ -309,28 +309,35 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
   static_assert(8 * (2 * S::kStages + 6) <= 256, "barriers fit behind the stages");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int rank = p.split > 1 ? int(cluster_rank()) : 0;
-  const int64_t workers = gridDim.x / p.split, worker = blockIdx.x / p.split;
+  const int rank = PAIR || p.split > 1 ? int(cluster_rank()) : 0;
+  const int ctas = PAIR ? 2 : p.split;  // of a cluster: they share a tile
+  const int64_t workers = gridDim.x / ctas, worker = blockIdx.x / ctas;
   const int64_t tiles = p.tiles_m * p.tiles_n;
-  const int kt0 = int(int64_t(p.ktiles) * rank / p.split), kt1 = int(int64_t(p.ktiles) * (rank + 1) / p.split);
+  const int kt0 = PAIR ? 0 : int(int64_t(p.ktiles) * rank / p.split);
+  const int kt1 = PAIR ? p.ktiles : int(int64_t(p.ktiles) * (rank + 1) / p.split);
+  // First output column of the CTA's part of a tile, and first row.
+  const auto col0 = [&](int64_t tm) { return PAIR ? tm * (2 * kTileM) + rank * kTileM : tm * kTileM; };
+  // The CTA that issues a pair's products is its first; its barriers count for both.
+  const auto lead = [&](uint32_t bar) { return PAIR ? cluster_addr(bar, 0) : bar; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full(s), 1 + (LOADERS ? kLoadWarps : 0));
+      mbar_init(full(s), 1 + (LOADERS ? kLoadWarps * (PAIR ? 2 : 1) : 0));
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), S::kEpi);
+      mbar_init(acc_empty(b), S::kEpi * (PAIR ? 2 : 1));
     }
     mbar_init(drain, 1);
     mbar_init_fence();
     if (p.a_tma) tma_prefetch_map(&ta);
     if (p.b_tma) tma_prefetch_map(&tb);
   }
-  if (warp == 2) tmem_alloc(tmem_at, S::kTmemCols);
+  if (warp == 2) tmem_alloc<PAIR>(tmem_at, S::kTmemCols);
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the barriers of both are ready
   tc_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at));
@@ -343,31 +350,38 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
     for (int64_t tile = worker; tile < tiles && !gave_up; tile += workers) {
       int64_t tm, tn;
       tile_at(p, tile, &tm, &tn);
-      const int m0 = int(tm * kTileM), n0 = int(tn * BN);
+      const int m0 = int(col0(tm)), n0 = int(tn * BN) + (PAIR ? rank * S::kBRows : 0);
       for (int kt = kt0; kt < kt1; ++kt) {
         if (!mbar_wait(empty(stage), phase ^ 1, p.wait_ns)) {
           gave_up = true;
           break;
         }
-        const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes;
+        const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes, bar = lead(full(stage));
         const int k0 = kt * kTileK;
-        mbar_arrive_expect(full(stage), (p.a_tma ? S::kABytes : 0) + (p.b_tma ? S::kBBytes : 0));
+        const auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
+          if constexpr (PAIR)
+            tma_load_2d_pair(dst, map, x, y, bar);
+          else
+            tma_load_2d(dst, map, x, y, bar);
+        };
+        // the bytes of both CTAs of a pair
+        if (!PAIR || rank == 0)
+          mbar_arrive_expect(full(stage), ((p.a_tma ? S::kABytes : 0) + (p.b_tma ? S::kBBytes : 0)) * (PAIR ? 2 : 1));
         if (p.a_tma) {
           if (!p.a.a_mn) {
-            tma_load_2d(sa, &ta, k0, m0, full(stage));
+            load(sa, &ta, k0, m0);
           } else {
 #pragma unroll
-            for (int c = 0; c < kTileM / 64; ++c)
-              tma_load_2d(sa + c * (kTileK * 128), &ta, m0 + c * 64, k0, full(stage));
+            for (int c = 0; c < kTileM / 64; ++c) load(sa + c * (kTileK * 128), &ta, m0 + c * 64, k0);
           }
         }
         if (p.b_tma) {
           if (!p.a.b_mn) {
-            tma_load_2d(sb, &tb, k0, n0, full(stage));
+            load(sb, &tb, k0, n0);
           } else {
 #pragma unroll
-            for (int c = 0; c < (BN < 64 ? 1 : BN / 64); ++c)
-              tma_load_2d(sb + c * (kTileK * 128), &tb, n0 + c * 64, k0, full(stage));
+            for (int c = 0; c < (S::kBRows < 64 ? 1 : S::kBRows / 64); ++c)
+              load(sb + c * (kTileK * 128), &tb, n0 + c * 64, k0);
           }
         }
         ++issued;
@@ -375,15 +389,20 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
       }
     }
     if (gave_up) {
-      // let the copies in flight land before the CTA ends
-      for (int i = 0; i < S::kStages && i < issued; ++i) {
-        if (--stage < 0) stage = S::kStages - 1, phase ^= 1;
-        if (!mbar_wait(full(stage), phase, p.wait_ns)) break;
+      // Let the copies in flight land before the CTA ends.  (The second CTA of a pair has them counted
+      // at the first's barriers; it waits a time in which any copy has landed.)
+      if (PAIR && rank != 0) {
+        for (int i = 0; i < 100; ++i) __nanosleep(100000);
+      } else {
+        for (int i = 0; i < S::kStages && i < issued; ++i) {
+          if (--stage < 0) stage = S::kStages - 1, phase ^= 1;
+          if (!mbar_wait(full(stage), phase, p.wait_ns)) break;
+        }
       }
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {
     // ---- products
-    const uint32_t desc = mma_desc(kTileM, BN, p.a.a_mn, p.a.b_mn);
+    const uint32_t desc = mma_desc(PAIR ? 2 * kTileM : kTileM, BN, p.a.a_mn, p.a.b_mn);
     const uint32_t chunk = kTileK * 128;
     const uint64_t astep = p.a.a_mn ? 2048 / 16 : 32 / 16, bstep = p.a.b_mn ? 2048 / 16 : 32 / 16;
     int stage = 0, phase = 0, buf = 0, bphase = 0;
@@ -404,17 +423,17 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
         const uint32_t sa = base + stage * S::kStage;
         const uint64_t da = smem_desc(sa, chunk), db = smem_desc(sa + S::kABytes, chunk);
 #pragma unroll
-        for (int k = 0; k < kTileK / 16; ++k) mma_bf16(d, da + k * astep, db + k * bstep, desc, kt > kt0 || k > 0);
-        mma_commit(empty(stage));
+        for (int k = 0; k < kTileK / 16; ++k) mma_bf16<PAIR>(d, da + k * astep, db + k * bstep, desc, kt > kt0 || k > 0);
+        mma_commit<PAIR>(empty(stage));
         if (++stage == S::kStages) stage = 0, phase ^= 1;
       }
       if (gave_up) break;
-      mma_commit(acc_full(buf));
+      mma_commit<PAIR>(acc_full(buf));
       buf ^= 1;
       if (buf == 0) bphase ^= 1;
     }
     if (gave_up) {
-      mma_commit(drain);
+      mma_commit<PAIR>(drain);
       mbar_wait(drain, 0, p.wait_ns);
     }
   } else if (warp >= 4 && warp < 4 + S::kEpi) {
@@ -433,7 +452,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
       Columns col;
       Ahead ahead[kChunk / 8];
       if (p.split == 1) {
-        col = columns_of(p.a, tm * kTileM + q * 32 + seg * 8);
+        col = columns_of(p.a, col0(tm) + q * 32 + seg * 8);
 #pragma unroll
         for (int i = 0; i < kChunk / 8; ++i) {
           const int j = half * kChunk + i * 8 + sub;
@@ -446,7 +465,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
           break;
         }
         tc_fence_after();
-        if (half * kChunk >= rows && lane == 0) mbar_arrive(acc_empty(buf));
+        if (half * kChunk >= rows && lane == 0) mbar_arrive_cluster(lead(acc_empty(buf)));
       }
 #pragma unroll 1
       for (int j0 = half * kChunk; j0 < rows; j0 += kStride) {
@@ -458,7 +477,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
             // the warp's part of the accumulator has been read
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(buf));
+            if (lane == 0) mbar_arrive_cluster(lead(acc_empty(buf)));
           }
         } else {
 #pragma unroll
@@ -502,7 +521,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
       if (pkt == kt0) {
         int64_t tm, tn;
         tile_at(p, ptile, &tm, &tn);
-        pm0 = tm * kTileM;
+        pm0 = col0(tm);
       }
       fetch_ckpt(c, p.a, nb, pm0, int64_t(pkt) * kTileK, tid);
       if (++pkt == kt1) pkt = kt0, ptile += workers;
@@ -532,12 +551,13 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
             }
           if (++turn == kAheadCkpt) turn = 0;
         } else if (!p.a_tma) {
-          fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, tm * kTileM, p.a.M, k0, p.a.K, tid);
+          fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, col0(tm), p.a.M, k0, p.a.K, tid);
         }
-        if (!p.b_tma) fill_plain<BN>(sb, p.a.b, p.a.ldb, p.a.b_mn, tn * BN, p.a.N, k0, p.a.K, tid);
+        if (!p.b_tma)
+          fill_plain<S::kBRows>(sb, p.a.b, p.a.ldb, p.a.b_mn, tn * BN + (PAIR ? rank * S::kBRows : 0), p.a.N, k0, p.a.K, tid);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full(stage));
+        if (lane == 0) mbar_arrive_cluster(lead(full(stage)));
         if (++stage == S::kStages) stage = 0, phase ^= 1;
       }
     }
@@ -545,7 +565,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
   if (gave_up && lane == 0) atomicAdd(&g_timeouts, 1ull);
   __syncwarp();
 
-  if (p.split > 1) {
+  if (!PAIR && p.split > 1) {
     // One tile per cluster.  Its parts lie in the CTAs' shared memory as [n][m]; each CTA adds up
     // and finishes its share of the rows.
     cluster_sync();
@@ -578,7 +598,8 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS>::kWarps * 32, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 2) tmem_free(tmem, S::kTmemCols);
+  if constexpr (PAIR) cluster_sync();  // neither leaves while the other may read or signal it
+  if (warp == 2) tmem_free<PAIR>(tmem, S::kTmemCols);
 }
 
 // ------------------------------------------------------------------ launch
@@ -617,15 +638,15 @@ cudaError_t make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int BN, bool LOADERS>
+template <int BN, bool LOADERS, bool PAIR>
 cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
-  using S = Shape<BN, LOADERS>;
+  using S = Shape<BN, LOADERS, PAIR>;
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(k_linear<BN, LOADERS>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+    e = cudaFuncSetAttribute(k_linear<BN, LOADERS, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
@@ -636,11 +657,12 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   if (p.b_tma && p.ktiles > 0) {
-    e = a.b_mn ? make_map(&tb, a.b, a.K, a.N, a.ldb, kTileK) : make_map(&tb, a.b, a.N, a.K, a.ldb, BN);
+    e = a.b_mn ? make_map(&tb, a.b, a.K, a.N, a.ldb, kTileK) : make_map(&tb, a.b, a.N, a.K, a.ldb, S::kBRows);
     if (e != cudaSuccess) return e;
   }
   const int64_t tiles = p.tiles_m * p.tiles_n;
-  const int64_t grid = p.split > 1 ? tiles * p.split : (tiles < sms ? tiles : sms);
+  const int ctas = PAIR ? 2 : p.split;
+  const int64_t workers = p.split > 1 || tiles < sms / ctas ? tiles : sms / ctas, grid = workers * ctas;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(grid));
@@ -649,11 +671,11 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(p.split);
+  attr[0].val.clusterDim.x = unsigned(ctas);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_linear<BN, LOADERS>, ta, tb, p);
+  return cudaLaunchKernelEx(&cfg, k_linear<BN, LOADERS, PAIR>, ta, tb, p);
 }
 
 }  // namespace
@@ -673,41 +695,47 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && (a.N <= 1 || a.ldo * oe % 16 == 0);
   p.res_wide = reinterpret_cast<uintptr_t>(a.residual) % 16 == 0 && (a.N <= 1 || a.ldr * oe % 16 == 0);
   const bool loaders = !p.a_tma || !p.b_tma;
-  p.tiles_m = (a.M + kTileM - 1) / kTileM;
 
-  // The tile's width and the split of k that finish first by this estimate (in units of a 256-wide
-  // tile's 64 k): waves x (each part's k tiles at the width's rate + a fixed cost of filling the
-  // pipeline and of the epilogue).
+  // The tile's width, the split of k or the pairing of CTAs that finish first by this estimate (in
+  // units of a 256-wide tile's 64 k): waves x (each part's k tiles at the width's rate + a fixed cost
+  // of filling the pipeline and of the epilogue).
   static const int widths[] = {16, 32, 64, 128, 256};
   int best_bn = 0, best_split = 1;
+  bool best_pair = false;
   double best = 0.0;
+  const auto consider = [&](int bn, int split, bool pair) {
+    const int64_t tm = (a.M + (pair ? 2 : 1) * kTileM - 1) / ((pair ? 2 : 1) * kTileM), tn = (a.N + bn - 1) / bn;
+    const int64_t tiles = tm * tn, slots = sms / (pair ? 2 : split);
+    if (split > 1 && (p.ktiles < 2 * split || tiles > slots)) return;
+    const double waves = double((tiles + slots - 1) / slots);
+    double per_k = bn >= 256 ? 1.0 : bn == 128 ? 0.6 : bn == 64 ? 0.4 : 0.35;
+    if (pair) per_k *= 0.85;
+    const double t = waves * (double((p.ktiles + split - 1) / split) * per_k + 4.0 + bn / 64.0 + (split > 1 || pair ? 3.0 : 0.0));
+    if (best_bn == 0 || t < best) best = t, best_bn = bn, best_split = split, best_pair = pair;
+  };
   for (const int bn : widths) {
     if (bn < 64 && (a.b_mn || loaders)) continue;
     if (bn > 64 && bn / 2 >= a.N) continue;  // more than half of it would be empty
-    const int64_t tn = (a.N + bn - 1) / bn, tiles = p.tiles_m * tn;
-    for (int split = 1; split <= 8; split *= 2) {
-      if (split > 1 && (p.ktiles < 2 * split || tiles * split > sms)) break;
-      const double waves = double((tiles * split + sms - 1) / sms);
-      const double per_k = bn >= 256 ? 1.0 : bn == 128 ? 0.6 : bn == 64 ? 0.4 : 0.35;
-      const double t = waves * (double((p.ktiles + split - 1) / split) * per_k + 4.0 + bn / 64.0 + (split > 1 ? 3.0 : 0.0));
-      if (best_bn == 0 || t < best) best = t, best_bn = bn, best_split = split;
-    }
+    for (int split = 1; split <= 8; split *= 2) consider(bn, split, false);
+    if (bn == 256) consider(bn, 1, true);
   }
   p.split = best_split;
+  p.tiles_m = (a.M + (best_pair ? 2 : 1) * kTileM - 1) / ((best_pair ? 2 : 1) * kTileM);
   p.tiles_n = (a.N + best_bn - 1) / best_bn;
+  if (best_pair) return loaders ? launch<256, true, true>(p, sms, s) : launch<256, false, true>(p, sms, s);
   if (loaders) {
     switch (best_bn) {
-      case 64: return launch<64, true>(p, sms, s);
-      case 128: return launch<128, true>(p, sms, s);
-      default: return launch<256, true>(p, sms, s);
+      case 64: return launch<64, true, false>(p, sms, s);
+      case 128: return launch<128, true, false>(p, sms, s);
+      default: return launch<256, true, false>(p, sms, s);
     }
   }
   switch (best_bn) {
-    case 16: return launch<16, false>(p, sms, s);
-    case 32: return launch<32, false>(p, sms, s);
-    case 64: return launch<64, false>(p, sms, s);
-    case 128: return launch<128, false>(p, sms, s);
-    default: return launch<256, false>(p, sms, s);
+    case 16: return launch<16, false, false>(p, sms, s);
+    case 32: return launch<32, false, false>(p, sms, s);
+    case 64: return launch<64, false, false>(p, sms, s);
+    case 128: return launch<128, false, false>(p, sms, s);
+    default: return launch<256, false, false>(p, sms, s);
   }
 }
 
