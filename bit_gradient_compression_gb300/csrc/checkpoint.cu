@@ -111,23 +111,6 @@ __global__ void __launch_bounds__(kThreads) k_encode_narrow(EncodeArgs a, Diviso
   }
 }
 
-// Four codes as four bf16, with no detour over fp32.  Under the exponent of 2^7 a bf16's seven
-// mantissa bits count whole units: 0x4300 | (c & 0x7F) is 128 + (c & 0x7F) and 0x4300 | (c & 0x80) is
-// 128 or, for a negative code, 256, so their difference is the code, and its product with a power of
-// two is exact.
-__device__ __forceinline__ uint2 decode4_bf16(uint32_t w, __nv_bfloat162 step) {
-  uint32_t r[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t u = __byte_perm(w, 0x43u, i ? 0x4342 : 0x4140);
-    const uint32_t lo = u & 0xFF7FFF7Fu, hi = u & 0xFF80FF80u;
-    const __nv_bfloat162 v = __hmul2(__hsub2(reinterpret_cast<const __nv_bfloat162&>(lo),
-                                             reinterpret_cast<const __nv_bfloat162&>(hi)), step);
-    r[i] = reinterpret_cast<const uint32_t&>(v);
-  }
-  return make_uint2(r[0], r[1]);
-}
-
 // Runs as in k_encode_wide, for rows of out that start on 16-byte boundaries.  PLAIN: the values as they are.
 template <bool BF16, bool PLAIN>
 __global__ void __launch_bounds__(kThreads) k_decode_wide(DecodeArgs a, Divisor per_row, int64_t nb, int64_t runs) {
@@ -155,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_wide(DecodeArgs a, Divisor 
       if (e * 256 >= left) continue;
       const bool full = e * 256 + 8 <= left;
       if (PLAIN && BF16 && full) {
-        const __nv_bfloat162 st = __float2bfloat162_rn(ckpt_step(sc[e]));
+        const uint32_t st = ckpt_step_bf16x2(sc[e]);
         const uint2 lo = decode4_bf16(w[e].x, st), hi = decode4_bf16(w[e].y, st);
         *reinterpret_cast<uint4*>(out + e * 512) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         continue;

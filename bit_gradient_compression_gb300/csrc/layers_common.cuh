@@ -227,6 +227,26 @@ __device__ __forceinline__ void ckpt_pairs4(uint32_t w, uint32_t scale, Pair v[2
                  __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 | 2 * k))) + off) * st2;
 }
 
+// Four codes as four bf16, with no detour over fp32.  Under the exponent of 2^7 a bf16's seven
+// mantissa bits count whole units: 0x4300 | (c & 0x7F) is 128 + (c & 0x7F) and 0x4300 | (c & 0x80) is
+// 128 or, for a negative code, 256, so their difference is the code, and its product with a power of
+// two is exact.
+__device__ __forceinline__ uint2 decode4_bf16(uint32_t w, uint32_t step_bf16x2) {
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = __byte_perm(w, 0x43u, i ? 0x4342 : 0x4140);
+    asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}"
+        : "=r"(r[i])
+        : "r"(u & 0xFF7FFF7Fu), "r"(u & 0xFF80FF80u), "r"(step_bf16x2));
+  }
+  return make_uint2(r[0], r[1]);
+}
+// 2^e twice in bf16 (NaN for a bad block).
+__device__ __forceinline__ uint32_t ckpt_step_bf16x2(uint32_t scale) {
+  return scale == kCkptBad ? 0x7FC07FC0u : scale * 0x00800080u;
+}
+
 // ---------------------------------------------------------------------------
 // Activations and their slopes, in fp32.  exp is __expf (within 2 + |x| * 2^-22 units of the last
 // place) and the quotients are __fdividef (2 units); both stay below 1e-6 relative here.

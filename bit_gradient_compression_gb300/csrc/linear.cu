@@ -29,7 +29,7 @@ namespace loco {
 namespace {
 
 constexpr int kTileM = 128, kTileK = 64;
-constexpr int kLoadWarps = 8;
+constexpr int kLoadWarps = 8, kLoadGroups = 4;  // loader warps work in pairs, each on every fourth k tile
 constexpr int kChunk = 16;                     // output rows an epilogue warp turns over at a time
 constexpr int kChunkPitch = 36;                // floats per row of 32 columns: 16-byte reads of 8 rows x 4 lanes meet no bank twice
 
@@ -52,7 +52,7 @@ struct Params {
   int a_tma, b_tma;
   int out_wide, res_wide;  // rows of out and residual start on 16-byte boundaries
   int64_t tiles_m, tiles_n;
-  int ktiles, split;
+  int ktiles, split, slots;  // slots: tiles that are worked on at once
   uint64_t wait_ns;  // limit of every wait, longer than the longest tile
 };
 
@@ -93,74 +93,114 @@ __device__ __forceinline__ void ld_shared8(uint32_t src, float (&v)[8]) {
                : "memory");
 }
 
-// A tile of ROWS (m or n) x 64 (k) bf16 values by plain loads; 0 outside the matrix.
+// Sixteen bytes that begin `off` bytes (a multiple of 2) into x and run on into y.
+__device__ __forceinline__ uint4 shifted16(uint4 x, uint4 y, uint32_t off) {
+  uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+  const uint32_t pick = off & 2 ? 0x5432u : 0x3210u;
+  return make_uint4(__byte_perm(w[0], w[1], pick), __byte_perm(w[1], w[2], pick), __byte_perm(w[2], w[3], pick),
+                    __byte_perm(w[3], w[4], pick));
+}
+
+// A tile of ROWS (m or n) x 64 (k) bf16 values by the 64 threads of a loader group; 0 outside the
+// matrix.  A unit that starts on no 16-byte boundary is put together from the aligned sixteen bytes on
+// either side, which lie in the matrix but for its very first and last; those, and units the matrix
+// ends in, go element by element.  The loads of a batch carry no branches, so that all are in flight.
+constexpr int kGroupThreads = kLoadWarps / kLoadGroups * 32;
 template <int ROWS>
 __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_t ld, int mn, int64_t row0,
                                            int64_t rows, int64_t k0, int64_t ks, int tid) {
-  constexpr int kItems = ROWS * 8;  // 16-byte units
-  const int per = mn ? ROWS / 8 : 8;
+  constexpr int kItems = ROWS * 8, kBatch = 4;  // 16-byte units
+  static_assert(kItems % (kGroupThreads * kBatch) == 0, "whole batches");
+  const int per = mn ? ROWS / 8 : 8, shift = mn ? (ROWS == 256 ? 5 : ROWS == 128 ? 4 : 3) : 3;
   const int64_t r0 = mn ? k0 : row0, rlim = mn ? ks : rows, c0 = mn ? row0 : k0, clim = mn ? rows : ks;
-  const uint16_t* base = static_cast<const uint16_t*>(src);
-#pragma unroll 2
-  for (int i = tid; i < kItems; i += kLoadWarps * 32) {
-    const int r = i / per, u = i - r * per;
-    const int64_t row = r0 + r, col = c0 + u * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < rlim && col < clim) {
-      const uint16_t* q = base + row * ld + col;
-      if (col + 8 <= clim && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-        v = __ldg(reinterpret_cast<const uint4*>(q));
-      } else {
-        uint32_t h[8];
+  const char* lo = static_cast<const char*>(src);
+  const char* hi = lo + ((rlim - 1) * ld + clim) * 2;
+  const char* tile = lo + (r0 * ld + c0) * 2;
+  const int rleft = int(min(rlim - r0, int64_t(ROWS))), cleft = int(min(clim - c0, int64_t(ROWS < 64 ? 64 : ROWS)));
+  const int64_t pitch = ld * 2;
+  for (int i0 = tid; i0 < kItems; i0 += kGroupThreads * kBatch) {
+    uint4 x[kBatch], y[kBatch];
+    const char* q[kBatch];
+    bool whole[kBatch];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = col + k < clim ? uint32_t(__ldg(q + k)) : 0u;
-        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1);
+      q[i] = tile + r * pitch + u * 16;
+      const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(q[i])) & 15u;
+      const char* b = q[i] - off;
+      whole[i] = r < rleft && u * 8 + 8 <= cleft && b >= lo && (off == 0 || b + 32 <= hi);
+      x[i] = y[i] = make_uint4(0, 0, 0, 0);
+      if (whole[i]) {
+        x[i] = __ldg(reinterpret_cast<const uint4*>(b));
+        y[i] = __ldg(reinterpret_cast<const uint4*>(off ? b + 16 : b));
       }
     }
-    st_shared16(dst + unit_offset(mn, r, u), v);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1);
+      uint4 v = shifted16(x[i], y[i], uint32_t(reinterpret_cast<uintptr_t>(q[i])) & 15u);
+      if (!whole[i] && r < rleft && u * 8 < cleft) {
+        uint32_t h[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          h[k] = u * 8 + k < cleft ? uint32_t(__ldg(reinterpret_cast<const uint16_t*>(q[i]) + k)) : 0u;
+        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+      }
+      st_shared16(dst + unit_offset(mn, r, u), v);
+    }
   }
 }
 
 // A thread's share of a tile of 128 (m) x 64 (k) values of a checkpoint [k][m]: 16 codes along m of
-// two k rows, with their scales.  Fetched kAheadCkpt k tiles before they are turned into bf16, as a k
-// tile's products take less time than memory takes to answer.
-constexpr int kAheadCkpt = 3;
+// every eighth k row, with their scales.
+constexpr int kPartRows = kTileK * (kTileM / 16) / kGroupThreads;
 struct CkptPart {
-  uint4 w[2];
-  uint32_t scale[2];
+  uint4 w[kPartRows];
+  uint32_t scale[kPartRows];
 };
 
-__device__ __forceinline__ void fetch_ckpt(CkptPart& c, const LinearArgs& a, int64_t nb, int64_t m0, int64_t k0, int tid) {
+// Where a thread's codes of one k tile lie.
+struct CkptPlace {
+  const int8_t* codes;
+  const uint8_t* scales;
+  int left;  // k rows of the checkpoint from the thread's first on, 0 past its columns
+};
+__device__ __forceinline__ CkptPlace ckpt_place(const LinearArgs& a, int64_t nb, int64_t m0, int64_t k0, int tid) {
   const int h = tid & 7;
-  const int64_t blk = m0 / kCkptBlock + h / 2;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t k = k0 + tid / 8 + i * (kLoadWarps * 4);
-    c.w[i] = make_uint4(0, 0, 0, 0);
-    c.scale[i] = 1;
-    if (k < a.K && blk < nb) {
-      const int64_t at = k * nb + blk;
-      c.w[i] = __ldg(reinterpret_cast<const uint4*>(a.a_codes + at * kCkptBlock) + (h & 1));
-      c.scale[i] = __ldg(a.a_scales + at);
-    }
+  const int64_t blk = m0 / kCkptBlock + h / 2, first = k0 + tid / 8;
+  return {a.a_codes + (first * nb + blk) * kCkptBlock + (h & 1) * 16, a.a_scales + first * nb + blk,
+          blk < nb ? int(max(int64_t(0), min(a.K - first, int64_t(kTileK)))) : 0};
+}
+__device__ __forceinline__ void fetch_ckpt(CkptPart& c, int i, const CkptPlace& at, int64_t nb) {
+  c.w[i] = make_uint4(0, 0, 0, 0);
+  c.scale[i] = 1;
+  if (i * (kGroupThreads / 8) < at.left) {
+    const int64_t row = i * (kGroupThreads / 8) * nb;
+    c.w[i] = __ldg(reinterpret_cast<const uint4*>(at.codes + row * kCkptBlock));
+    c.scale[i] = __ldg(at.scales + row);
   }
 }
 
-__device__ __forceinline__ void fill_ckpt(uint32_t dst, const CkptPart& c, int tid) {
-  const int h = tid & 7, second = h >> 2;  // the upper 64 columns start with their odd unit: 8 lanes, 8 bank groups
+// Turns a part into bf16 in the stage and fetches the next into the registers that come free, so that a
+// load has a whole k tile's work to arrive.
+__device__ __forceinline__ void fill_ckpt(uint32_t dst, CkptPart& c, const CkptPlace& next, int64_t nb, int tid) {
+  static_assert(kGroupThreads == 64, "a thread's k rows are 8 apart: one place in the swizzle");
+  // the upper 64 columns start with their odd unit: 8 lanes, 8 bank groups
+  const int h = tid & 7, second = h >> 2;
+  const uint32_t d0 = dst + unit_offset(1, tid / 8, 2 * h + second), d1 = dst + unit_offset(1, tid / 8, 2 * h + 1 - second);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = tid / 8 + i * (kLoadWarps * 4);
-    const float st = ckpt_step(c.scale[i]);
-    float v[16];
-    ckpt_unpack4(c.w[i].x, st, v), ckpt_unpack4(c.w[i].y, st, v + 4);
-    ckpt_unpack4(c.w[i].z, st, v + 8), ckpt_unpack4(c.w[i].w, st, v + 12);
-    const uint4 lo = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                pack_bf16x2(v[6], v[7]));
-    const uint4 hi = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
-                                pack_bf16x2(v[14], v[15]));
-    st_shared16(dst + unit_offset(1, r, 2 * h + second), second ? hi : lo);
-    st_shared16(dst + unit_offset(1, r, 2 * h + 1 - second), second ? lo : hi);
+  for (int i = 0; i < kPartRows; ++i) {
+    const uint32_t st = ckpt_step_bf16x2(c.scale[i]);
+    const uint4 w = c.w[i];
+    fetch_ckpt(c, i, next, nb);
+    const uint2 a = decode4_bf16(second ? w.z : w.x, st), b = decode4_bf16(second ? w.w : w.y, st);
+    st_shared16(d0 + i * 1024, make_uint4(a.x, a.y, b.x, b.y));
+    const uint2 e = decode4_bf16(second ? w.x : w.z, st), f = decode4_bf16(second ? w.y : w.w, st);
+    st_shared16(d1 + i * 1024, make_uint4(e.x, e.y, f.x, f.y));
   }
 }
 
@@ -322,7 +362,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full(s), 1 + (LOADERS ? kLoadWarps * (PAIR ? 2 : 1) : 0));
+      mbar_init(full(s), 1 + (LOADERS ? kLoadWarps / kLoadGroups * (PAIR ? 2 : 1) : 0));
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -508,58 +548,65 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
       buf ^= 1;
       if (buf == 0) bphase ^= 1;
     }
-  } else if (LOADERS && warp >= 4 + S::kEpi) {
-    // ---- plain loads and checkpoints
-    const int tid = threadIdx.x - (4 + S::kEpi) * 32;
+  } else if (warp >= 4 + S::kEpi) {
+    if constexpr (LOADERS) {
+    // ---- plain loads and checkpoints.  A k tile takes a group longer than its products take, mostly
+    // in waiting; four groups on four k tiles keep up with them.
+    const int index = warp - 4 - S::kEpi, group = index / (kLoadWarps / kLoadGroups);
+    const int tid = threadIdx.x % kGroupThreads;
     const int64_t nb = (p.a.M + kCkptBlock - 1) / kCkptBlock;
     const bool ckpt = p.a.a_codes != nullptr;
-    CkptPart part[kAheadCkpt];
-    int64_t ptile = worker, pm0 = 0;  // what is fetched next
-    int pkt = kt0;
-    const auto fetch_next = [&](CkptPart& c) {
-      if (ptile >= tiles) return;
-      if (pkt == kt0) {
-        int64_t tm, tn;
-        tile_at(p, ptile, &tm, &tn);
-        pm0 = col0(tm);
-      }
-      fetch_ckpt(c, p.a, nb, pm0, int64_t(pkt) * kTileK, tid);
-      if (++pkt == kt1) pkt = kt0, ptile += workers;
+    const int nk = kt1 - kt0;
+    // position of a step of this CTA's k tiles, all tiles counted through
+    struct Place {
+      int64_t tile, tm, tn;
+      int kt;
     };
-    if (ckpt && kt0 < kt1) {
-#pragma unroll
-      for (int i = 0; i < kAheadCkpt; ++i) fetch_next(part[i]);
+    const auto advance = [&](Place& at, int by) {
+      at.kt += by;
+      bool moved = by == 0;
+      while (at.kt >= kt1 && at.tile < tiles) at.kt -= nk, at.tile += workers, moved = true;
+      if (moved && at.tile < tiles) tile_at(p, at.tile, &at.tm, &at.tn);
+    };
+    Place now{worker, 0, 0, kt0};
+    if (nk > 0) {
+      advance(now, 0);
+      advance(now, group);
+    } else {
+      now.tile = tiles;
     }
-    int stage = 0, phase = 0, turn = 0;
-    for (int64_t tile = worker; tile < tiles && !gave_up; tile += workers) {
-      int64_t tm, tn;
-      tile_at(p, tile, &tm, &tn);
-      for (int kt = kt0; kt < kt1; ++kt) {
-        if (!warp_wait(empty(stage), phase ^ 1, p.wait_ns)) {
-          gave_up = true;
-          break;
-        }
-        const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes;
-        const int64_t k0 = int64_t(kt) * kTileK;
-        if (ckpt) {
-          // each part in its own registers: moving them along would wait for their loads
+    CkptPart part;
+    const auto place = [&](const Place& at) {
+      if (at.tile >= tiles) return CkptPlace{p.a.a_codes, p.a.a_scales, 0};
+      return ckpt_place(p.a, nb, col0(at.tm), int64_t(at.kt) * kTileK, tid);
+    };
+    if (ckpt) {
+      const CkptPlace at = place(now);
 #pragma unroll
-          for (int i = 0; i < kAheadCkpt; ++i)
-            if (turn == i) {
-              fill_ckpt(sa, part[i], tid);
-              fetch_next(part[i]);
-            }
-          if (++turn == kAheadCkpt) turn = 0;
-        } else if (!p.a_tma) {
-          fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, col0(tm), p.a.M, k0, p.a.K, tid);
-        }
-        if (!p.b_tma)
-          fill_plain<S::kBRows>(sb, p.a.b, p.a.ldb, p.a.b_mn, tn * BN + (PAIR ? rank * S::kBRows : 0), p.a.N, k0, p.a.K, tid);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead(full(stage)));
-        if (++stage == S::kStages) stage = 0, phase ^= 1;
+      for (int i = 0; i < kPartRows; ++i) fetch_ckpt(part, i, at, nb);
+    }
+    int stage = group, phase = 0;
+    static_assert(S::kStages >= kLoadGroups, "a group's first stage is one of the ring's");
+    while (now.tile < tiles) {
+      if (!warp_wait(empty(stage), phase ^ 1, p.wait_ns)) {
+        gave_up = true;
+        break;
       }
+      const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes;
+      const int64_t k0 = int64_t(now.kt) * kTileK;
+      if (!p.b_tma)
+        fill_plain<S::kBRows>(sb, p.a.b, p.a.ldb, p.a.b_mn, now.tn * BN + (PAIR ? rank * S::kBRows : 0), p.a.N, k0, p.a.K,
+                              tid);
+      if (!ckpt && !p.a_tma)
+        fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, col0(now.tm), p.a.M, k0, p.a.K, tid);
+      advance(now, kLoadGroups);
+      if (ckpt) fill_ckpt(sa, part, place(now), nb, tid);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead(full(stage)));
+      stage += kLoadGroups;
+      if (stage >= S::kStages) stage -= S::kStages, phase ^= 1;
+    }
     }
   }
   if (gave_up && lane == 0) atomicAdd(&g_timeouts, 1ull);
@@ -639,7 +686,7 @@ cudaError_t make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols
 }
 
 template <int BN, bool LOADERS, bool PAIR>
-cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
+cudaError_t launch(const Params& p, cudaStream_t s) {
   using S = Shape<BN, LOADERS, PAIR>;
   static std::atomic<bool> ready[64];
   int dev = 0;
@@ -662,7 +709,7 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
   }
   const int64_t tiles = p.tiles_m * p.tiles_n;
   const int ctas = PAIR ? 2 : p.split;
-  const int64_t workers = p.split > 1 || tiles < sms / ctas ? tiles : sms / ctas, grid = workers * ctas;
+  const int64_t workers = p.split > 1 || tiles < p.slots ? tiles : p.slots, grid = workers * ctas;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(grid));
@@ -678,12 +725,39 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_linear<BN, LOADERS, PAIR>, ta, tb, p);
 }
 
+// Clusters of 1, 2, 4 and 8 CTAs of these kernels (one CTA per SM) that the current device holds at
+// once: fewer than its SMs would make up, as a cluster lies within one group of SMs.
+cudaError_t cluster_slots(int (&slots)[4]) {
+  static std::atomic<int> known[64][4];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  using S = Shape<64, false, false>;
+  for (int i = 0; i < 4; ++i) {
+    if (dev < 64 && (slots[i] = known[dev][i].load(std::memory_order_relaxed)) > 0) continue;
+    e = cudaFuncSetAttribute(k_linear<64, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(8 * 64);
+    cfg.blockDim = dim3(S::kWarps * 32);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(&slots[i], k_linear<64, false, false>, &cfg)) != cudaSuccess) return e;
+    if (slots[i] < 1) slots[i] = 1;
+    if (dev < 64) known[dev][i].store(slots[i], std::memory_order_relaxed);
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
-  int sms = 0;
-  cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   Params p{};
   p.a = a;
   p.a_tma = a.a_codes == nullptr && tma_can(a.a, a.a_mn ? a.K : a.M, a.lda);
@@ -699,15 +773,17 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   // The tile's width, the split of k or the pairing of CTAs that finish first by this estimate (in
   // units of a 256-wide tile's 64 k): waves x (each part's k tiles at the width's rate + a fixed cost
   // of filling the pipeline and of the epilogue).
+  int slots[4];  // clusters of 1, 2, 4, 8 CTAs that the device runs at once
+  if ((e = cluster_slots(slots)) != cudaSuccess) return e;
   static const int widths[] = {16, 32, 64, 128, 256};
   int best_bn = 0, best_split = 1;
   bool best_pair = false;
   double best = 0.0;
   const auto consider = [&](int bn, int split, bool pair) {
     const int64_t tm = (a.M + (pair ? 2 : 1) * kTileM - 1) / ((pair ? 2 : 1) * kTileM), tn = (a.N + bn - 1) / bn;
-    const int64_t tiles = tm * tn, slots = sms / (pair ? 2 : split);
-    if (split > 1 && (p.ktiles < 2 * split || tiles > slots)) return;
-    const double waves = double((tiles + slots - 1) / slots);
+    const int64_t tiles = tm * tn, most = slots[pair || split == 2 ? 1 : split == 4 ? 2 : split == 8 ? 3 : 0];
+    if (split > 1 && (p.ktiles < 2 * split || tiles > most)) return;
+    const double waves = double((tiles + most - 1) / most);
     double per_k = bn >= 256 ? 1.0 : bn == 128 ? 0.6 : bn == 64 ? 0.4 : 0.35;
     if (pair) per_k *= 0.85;
     const double t = waves * (double((p.ktiles + split - 1) / split) * per_k + 4.0 + bn / 64.0 + (split > 1 || pair ? 3.0 : 0.0));
@@ -717,25 +793,26 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     if (bn < 64 && (a.b_mn || loaders)) continue;
     if (bn > 64 && bn / 2 >= a.N) continue;  // more than half of it would be empty
     for (int split = 1; split <= 8; split *= 2) consider(bn, split, false);
-    if (bn == 256) consider(bn, 1, true);
+    if (bn == 256 && !loaders) consider(bn, 1, true);
   }
   p.split = best_split;
+  p.slots = slots[best_pair ? 1 : 0];
   p.tiles_m = (a.M + (best_pair ? 2 : 1) * kTileM - 1) / ((best_pair ? 2 : 1) * kTileM);
   p.tiles_n = (a.N + best_bn - 1) / best_bn;
-  if (best_pair) return loaders ? launch<256, true, true>(p, sms, s) : launch<256, false, true>(p, sms, s);
+  if (best_pair) return launch<256, false, true>(p, s);
   if (loaders) {
     switch (best_bn) {
-      case 64: return launch<64, true, false>(p, sms, s);
-      case 128: return launch<128, true, false>(p, sms, s);
-      default: return launch<256, true, false>(p, sms, s);
+      case 64: return launch<64, true, false>(p, s);
+      case 128: return launch<128, true, false>(p, s);
+      default: return launch<256, true, false>(p, s);
     }
   }
   switch (best_bn) {
-    case 16: return launch<16, false, false>(p, sms, s);
-    case 32: return launch<32, false, false>(p, sms, s);
-    case 64: return launch<64, false, false>(p, sms, s);
-    case 128: return launch<128, false, false>(p, sms, s);
-    default: return launch<256, false, false>(p, sms, s);
+    case 16: return launch<16, false, false>(p, s);
+    case 32: return launch<32, false, false>(p, s);
+    case 64: return launch<64, false, false>(p, s);
+    case 128: return launch<128, false, false>(p, s);
+    default: return launch<256, false, false>(p, s);
   }
 }
 
