@@ -156,51 +156,58 @@ __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_
 }
 
 // A thread's share of a tile of 128 (m) x 64 (k) values of a checkpoint [k][m]: 16 codes along m of
-// every eighth k row, with their scales.
-constexpr int kPartRows = kTileK * (kTileM / 16) / kGroupThreads;
+// every eighth k row, with their scales.  Lanes 0-3 and 4-7 of eight hold 64 columns of two
+// neighbouring rows, whose places in the swizzle differ in their lowest bit: 8 lanes, 8 bank groups.
+constexpr int kPartRows = 8;
+static_assert(kGroupThreads * kPartRows == kTileK * kTileM / 16, "64 threads hold a tile");
 struct CkptPart {
   uint4 w[kPartRows];
   uint32_t scale[kPartRows];
 };
+__device__ __forceinline__ int part_row(int tid) { return ((tid >> 2) & 1) + ((tid >> 4) << 1); }  // the first
+__device__ __forceinline__ int part_half(int tid) { return (tid & 3) + ((tid >> 3) & 1) * 4; }     // of 8 along m
 
 // Where a thread's codes of one k tile lie.
 struct CkptPlace {
   const int8_t* codes;
   const uint8_t* scales;
-  int left;  // k rows of the checkpoint from the thread's first on, 0 past its columns
+  int left;    // k rows of the checkpoint from the thread's first on, 0 past its columns
+  bool whole;  // the whole tile lies in it
 };
 __device__ __forceinline__ CkptPlace ckpt_place(const LinearArgs& a, int64_t nb, int64_t m0, int64_t k0, int tid) {
-  const int h = tid & 7;
-  const int64_t blk = m0 / kCkptBlock + h / 2, first = k0 + tid / 8;
+  const int h = part_half(tid);
+  const int64_t blk = m0 / kCkptBlock + h / 2, first = k0 + part_row(tid);
   return {a.a_codes + (first * nb + blk) * kCkptBlock + (h & 1) * 16, a.a_scales + first * nb + blk,
-          blk < nb ? int(max(int64_t(0), min(a.K - first, int64_t(kTileK)))) : 0};
+          blk < nb ? int(max(int64_t(0), min(a.K - first, int64_t(kTileK)))) : 0,
+          m0 + kTileM <= nb * kCkptBlock && k0 + kTileK <= a.K};
 }
 __device__ __forceinline__ void fetch_ckpt(CkptPart& c, int i, const CkptPlace& at, int64_t nb) {
-  c.w[i] = make_uint4(0, 0, 0, 0);
-  c.scale[i] = 1;
-  if (i * (kGroupThreads / 8) < at.left) {
-    const int64_t row = i * (kGroupThreads / 8) * nb;
+  const int64_t row = i * 8 * nb;
+  if (at.whole) {
     c.w[i] = __ldg(reinterpret_cast<const uint4*>(at.codes + row * kCkptBlock));
     c.scale[i] = __ldg(at.scales + row);
+  } else {
+    c.w[i] = make_uint4(0, 0, 0, 0);
+    c.scale[i] = 1;
+    if (i * 8 < at.left) {
+      c.w[i] = __ldg(reinterpret_cast<const uint4*>(at.codes + row * kCkptBlock));
+      c.scale[i] = __ldg(at.scales + row);
+    }
   }
 }
-
 // Turns a part into bf16 in the stage and fetches the next into the registers that come free, so that a
 // load has a whole k tile's work to arrive.
 __device__ __forceinline__ void fill_ckpt(uint32_t dst, CkptPart& c, const CkptPlace& next, int64_t nb, int tid) {
-  static_assert(kGroupThreads == 64, "a thread's k rows are 8 apart: one place in the swizzle");
-  // the upper 64 columns start with their odd unit: 8 lanes, 8 bank groups
-  const int h = tid & 7, second = h >> 2;
-  const uint32_t d0 = dst + unit_offset(1, tid / 8, 2 * h + second), d1 = dst + unit_offset(1, tid / 8, 2 * h + 1 - second);
+  const uint32_t d0 = dst + unit_offset(1, part_row(tid), 2 * part_half(tid));
+  const uint32_t d1 = dst + unit_offset(1, part_row(tid), 2 * part_half(tid) + 1);
 #pragma unroll
   for (int i = 0; i < kPartRows; ++i) {
     const uint32_t st = ckpt_step_bf16x2(c.scale[i]);
-    const uint4 w = c.w[i];
+    const uint2 v0 = decode4_bf16(c.w[i].x, st), v1 = decode4_bf16(c.w[i].y, st);
+    const uint2 v2 = decode4_bf16(c.w[i].z, st), v3 = decode4_bf16(c.w[i].w, st);
     fetch_ckpt(c, i, next, nb);
-    const uint2 a = decode4_bf16(second ? w.z : w.x, st), b = decode4_bf16(second ? w.w : w.y, st);
-    st_shared16(d0 + i * 1024, make_uint4(a.x, a.y, b.x, b.y));
-    const uint2 e = decode4_bf16(second ? w.x : w.z, st), f = decode4_bf16(second ? w.y : w.w, st);
-    st_shared16(d1 + i * 1024, make_uint4(e.x, e.y, f.x, f.y));
+    st_shared16(d0 + i * 1024, make_uint4(v0.x, v0.y, v1.x, v1.y));
+    st_shared16(d1 + i * 1024, make_uint4(v2.x, v2.y, v3.x, v3.y));
   }
 }
 
@@ -459,6 +466,9 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
           gave_up = true;
           break;
         }
+        // Orders the loaders' writes, seen through the barrier, before the tensor core's reads.  (A fence
+        // by the loaders themselves would wait for their loads of the next k tiles.)
+        if (LOADERS) fence_async_shared();
         tc_fence_after();
         const uint32_t sa = base + stage * S::kStage;
         const uint64_t da = smem_desc(sa, chunk), db = smem_desc(sa + S::kABytes, chunk);
@@ -577,7 +587,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
     }
     CkptPart part;
     const auto place = [&](const Place& at) {
-      if (at.tile >= tiles) return CkptPlace{p.a.a_codes, p.a.a_scales, 0};
+      if (at.tile >= tiles) return CkptPlace{p.a.a_codes, p.a.a_scales, 0, false};
       return ckpt_place(p.a, nb, col0(at.tm), int64_t(at.kt) * kTileK, tid);
     };
     if (ckpt) {
@@ -601,7 +611,6 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
         fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, col0(now.tm), p.a.M, k0, p.a.K, tid);
       advance(now, kLoadGroups);
       if (ckpt) fill_ckpt(sa, part, place(now), nb, tid);
-      fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(lead(full(stage)));
       stage += kLoadGroups;
@@ -647,6 +656,99 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
   tc_fence_after();
   if constexpr (PAIR) cluster_sync();  // neither leaves while the other may read or signal it
   if (warp == 2) tmem_free<PAIR>(tmem, S::kTmemCols);
+}
+
+// ------------------------------------------------------------------ few rows
+
+// A forward pass of at most TT <= 4 rows of x: bound by reading w once.  32 rows of w per CTA, four per
+// warp: a lane takes 8 of every 256 k of them, kAhead such loads of each row in flight, and the warp
+// adds up its lanes.  The tensor cores would have 128 x 16 tiles mostly of zeros to fill, and too few of them
+// to keep every SM reading.
+constexpr int kRowWarps = 8, kRowsPerWarp = 4;
+
+template <int TT>
+__global__ void __launch_bounds__(kRowWarps * 32, 2) k_linear_rows(const __grid_constant__ Params p) {
+  __shared__ float sums[TT][kRowWarps * kRowsPerWarp + 4];
+  const LinearArgs& a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int64_t m0 = int64_t(blockIdx.x) * (kRowWarps * kRowsPerWarp);
+  const uint16_t* w = static_cast<const uint16_t*>(a.a);
+  const uint16_t* x = static_cast<const uint16_t*>(a.b);
+  const uint16_t* rows[kRowsPerWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) rows[i] = w + min(m0 + warp * kRowsPerWarp + i, a.M - 1) * a.lda;
+  Pair acc[kRowsPerWarp][TT];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[i][t] = pair(0.0f, 0.0f);
+  const auto step = [&](const uint4 (&wv)[kRowsPerWarp], int64_t k) {
+    Pair wp[kRowsPerWarp][4];
+#pragma unroll
+    for (int i = 0; i < kRowsPerWarp; ++i) widen8(wv[i], wp[i]);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      Pair xp[4];
+      widen8(t < a.N ? __ldg(reinterpret_cast<const uint4*>(x + t * a.ldb + k)) : make_uint4(0, 0, 0, 0), xp);
+#pragma unroll
+      for (int i = 0; i < kRowsPerWarp; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][t] = fma(wp[i][j], xp[j], acc[i][t]);
+    }
+  };
+  constexpr int kAhead = TT <= 2 ? 4 : 2;
+  int64_t k = lane * 8;
+  for (; k + (kAhead - 1) * 256 + 8 <= a.K; k += kAhead * 256) {
+    uint4 wv[kAhead][kRowsPerWarp];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < kRowsPerWarp; ++i) wv[j][i] = __ldcs(reinterpret_cast<const uint4*>(rows[i] + k + j * 256));
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) step(wv[j], k + j * 256);
+  }
+  for (; k + 8 <= a.K; k += 256) {
+    uint4 wv[kRowsPerWarp];
+#pragma unroll
+    for (int i = 0; i < kRowsPerWarp; ++i) wv[i] = __ldcs(reinterpret_cast<const uint4*>(rows[i] + k));
+    step(wv, k);
+  }
+  const int64_t last = (a.K & ~int64_t(7)) + lane;  // the values after the last whole eight
+  if (last < a.K) {
+#pragma unroll
+    for (int i = 0; i < kRowsPerWarp; ++i)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        if (t < a.N)
+          acc[i][t] = acc[i][t] + pair(bf16_bits_to_f32(__ldg(rows[i] + last)) * bf16_bits_to_f32(__ldg(x + t * a.ldb + last)), 0.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float2 h = halves(acc[i][t]);
+      float v = h.x + h.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      if (lane == 0) sums[t][warp * kRowsPerWarp + i] = v;
+    }
+  __syncthreads();
+  if (warp == 0) {
+    const int t = lane / 4, seg = lane & 3;
+    const bool row = t < a.N;
+    const Columns col = columns_of(a, m0 + seg * 8);
+    const Ahead h = fetch_ahead(p, col, t, row);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = row ? sums[t < TT ? t : 0][seg * 8 + j] : 0.0f;
+    finish(p, col, v, t, row, h);
+  }
+}
+
+template <int TT>
+cudaError_t launch_rows(const Params& p, cudaStream_t s) {
+  k_linear_rows<TT><<<unsigned((p.a.M + 31) / 32), kRowWarps * 32, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ launch
@@ -769,6 +871,12 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && (a.N <= 1 || a.ldo * oe % 16 == 0);
   p.res_wide = reinterpret_cast<uintptr_t>(a.residual) % 16 == 0 && (a.N <= 1 || a.ldr * oe % 16 == 0);
   const bool loaders = !p.a_tma || !p.b_tma;
+
+  // Few rows of x and rows of w enough for every SM (1 row, 11008 x 4096: 24.8 us with tensor cores).
+  if (!a.a_mn && !a.b_mn && !loaders && a.N <= 4 && p.ktiles > 0 && a.M >= 32 * 76) {
+    p.split = 1;
+    return a.N == 1 ? launch_rows<1>(p, s) : a.N == 2 ? launch_rows<2>(p, s) : launch_rows<4>(p, s);
+  }
 
   // The tile's width, the split of k or the pairing of CTAs that finish first by this estimate (in
   // units of a 256-wide tile's 64 k): waves x (each part's k tiles at the width's rate + a fixed cost

@@ -270,6 +270,7 @@ def test_norm_nan_stays_in_its_row(L, cols, pad):
 LIN = [(1, 1, 1), (3, 7, 5), (1, 130, 64), (16, 128, 64), (17, 129, 65), (33, 257, 200), (64, 96, 72), (5, 4100, 512),
        (130, 384, 1024), (200, 31, 2049), (512, 256, 2048), (1000, 520, 136), (2100, 4500, 320)]
 # products long enough in every direction for pairs of CTAs, several tiles each, ragged at every edge
+LIN_FEW = [(1, 4096, 520), (2, 2500, 1027), (4, 2432, 264), (5, 4100, 40), (8, 3000, 512), (7, 2440, 9), (9, 4096, 520)]
 LIN_LARGE = [(1100, 2300, 2056), (2304, 2060, 2500)]
 # row pitches beyond the width, offset of the first element: TMA takes the first, plain loads the rest
 LAYOUTS = [("even", 0), ("odd", 0), ("even", 1)]
@@ -293,7 +294,7 @@ def linear_forward_ref(x, w, bias, name, residual):
     return z, tol, y, ytol
 
 
-@pytest.mark.parametrize("T,N,K", LIN + LIN_LARGE)
+@pytest.mark.parametrize("T,N,K", LIN + LIN_FEW + LIN_LARGE)
 @pytest.mark.parametrize("layout,off", LAYOUTS)
 @pytest.mark.parametrize("variant", range(5))
 def test_linear_forward(L, T, N, K, layout, off, variant):
