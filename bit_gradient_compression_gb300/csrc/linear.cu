@@ -365,11 +365,19 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
   // First output column of the CTA's part of a tile, and first row.
   const auto col0 = [&](int64_t tm) { return PAIR ? tm * (2 * kTileM) + rank * kTileM : tm * kTileM; };
   // The CTA that issues a pair's products is its first; its barriers count for both.
+  static_assert(!(PAIR && LOADERS), "a pair's operands come by TMA: loaders would have to publish across CTAs");
   const auto lead = [&](uint32_t bar) { return PAIR ? cluster_addr(bar, 0) : bar; };
+  // A warp has read its part of an accumulator (ordered by tcgen05 fences: no memory is handed over).
+  const auto drained = [&](uint32_t bar) {
+    if (PAIR)
+      mbar_arrive_remote(lead(bar));
+    else
+      mbar_arrive(bar);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full(s), 1 + (LOADERS ? kLoadWarps / kLoadGroups * (PAIR ? 2 : 1) : 0));
+      mbar_init(full(s), 1 + (LOADERS ? kLoadWarps / kLoadGroups : 0));
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -515,7 +523,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
           break;
         }
         tc_fence_after();
-        if (half * kChunk >= rows && lane == 0) mbar_arrive_cluster(lead(acc_empty(buf)));
+        if (half * kChunk >= rows && lane == 0) drained(acc_empty(buf));
       }
 #pragma unroll 1
       for (int j0 = half * kChunk; j0 < rows; j0 += kStride) {
@@ -527,7 +535,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
             // the warp's part of the accumulator has been read
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead(acc_empty(buf)));
+            if (lane == 0) drained(acc_empty(buf));
           }
         } else {
 #pragma unroll
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
       advance(now, kLoadGroups);
       if (ckpt) fill_ckpt(sa, part, place(now), nb, tid);
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(lead(full(stage)));
+      if (lane == 0) mbar_arrive(full(stage));
       stage += kLoadGroups;
       if (stage >= S::kStages) stage -= S::kStages, phase ^= 1;
     }
