@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_wide(DecodeArgs a, Divisor 
               v[k] = fmaf(v[k], a.gamma ? load_elem(a.gamma, c + k, a.param_bf16) : 1.0f,
                           a.beta ? load_elem(a.beta, c + k, a.param_bf16) : 0.0f);
         }
-        apply_act8(v, a.act);
+        apply_act(v, a.act);
       }
       if (full) {
         store8(out, e * 256, BF16, v);
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) k_decode_narrow(DecodeArgs a, Diviso
         if (++j == per_row.d) j = 0;
       }
     }
-    apply_act8(v, a.act);
+    apply_act(v, a.act);
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       const int64_t col = blk * kCkptBlock + lane;

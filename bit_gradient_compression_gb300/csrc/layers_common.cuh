@@ -291,11 +291,12 @@ __device__ __forceinline__ float act_slope(float v, int act) {
   }
 }
 
-// v = act(v) and v *= act'(z), eight values at a time with the branch outside.
-__device__ __forceinline__ void apply_act8(float (&v)[8], int act) {
+// v = act(v) and v *= act'(z) for N values, with the choice made once.
+template <int N>
+__device__ __forceinline__ void apply_act(float (&v)[N], int act) {
 #define LOCO_EACH(A)               \
   case A:                          \
-    _Pragma("unroll") for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], A); \
+    _Pragma("unroll") for (int k = 0; k < N; ++k) v[k] = act_value(v[k], A); \
     break
   switch (act) {
     LOCO_EACH(LOCO_ACT_RELU);
@@ -306,10 +307,11 @@ __device__ __forceinline__ void apply_act8(float (&v)[8], int act) {
   }
 #undef LOCO_EACH
 }
-__device__ __forceinline__ void mul_slope8(float (&v)[8], const float (&z)[8], int act) {
+template <int N>
+__device__ __forceinline__ void mul_slope(float (&v)[N], const float (&z)[N], int act) {
 #define LOCO_EACH(A)               \
   case A:                          \
-    _Pragma("unroll") for (int k = 0; k < 8; ++k) v[k] *= act_slope(z[k], A); \
+    _Pragma("unroll") for (int k = 0; k < N; ++k) v[k] *= act_slope(z[k], A); \
     break
   switch (act) {
     LOCO_EACH(LOCO_ACT_RELU);

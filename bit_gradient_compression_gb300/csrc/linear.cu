@@ -85,7 +85,7 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
 __device__ __forceinline__ void st_shared4(uint32_t dst, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
 }
-__device__ __forceinline__ void ld_shared8(uint32_t src, float (&v)[8]) {
+__device__ __forceinline__ void ld_shared8(uint32_t src, float* v) {
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(src) : "memory");
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
@@ -310,9 +310,9 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
     const float st = ckpt_step(h.zs);
     ckpt_unpack4(h.z.x, st, z);
     ckpt_unpack4(h.z.y, st, z + 4);
-    mul_slope8(v, z, a.act);
+    mul_slope(v, z, a.act);
   } else {
-    apply_act8(v, a.act);
+    apply_act(v, a.act);
   }
   if (a.residual != nullptr) {
     const uint32_t w[8] = {h.r0.x, h.r0.y, h.r0.z, h.r0.w, h.r1.x, h.r1.y, h.r1.z, h.r1.w};
@@ -334,6 +334,95 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k < c.live) store_elem(a.out, at + k, a.out_bf16, v[k]);
+  }
+}
+
+// The same where the tile lies wholly inside an output of wide rows: rows n and n + 8 of the lane's
+// columns at a time, with no bounds, and each choice made once for sixteen values.
+__device__ __forceinline__ void fetch_whole(const LinearArgs& a, const Columns& c, int64_t n, int64_t nb, Ahead (&h)[2]) {
+  if (a.residual != nullptr) {
+    const int oe = a.out_bf16 ? 2 : 4;
+    const char* q = static_cast<const char*>(a.residual) + (n * a.ldr + c.m) * oe;
+    const int64_t eight = 8 * a.ldr * oe;
+    h[0].r0 = *reinterpret_cast<const uint4*>(q);
+    h[1].r0 = *reinterpret_cast<const uint4*>(q + eight);
+    if (!a.out_bf16) {
+      h[0].r1 = *reinterpret_cast<const uint4*>(q + 16);
+      h[1].r1 = *reinterpret_cast<const uint4*>(q + eight + 16);
+    }
+  }
+  if (a.z_codes != nullptr) {
+    const int64_t at = n * nb * kCkptBlock + c.m;
+    h[0].z = __ldg(reinterpret_cast<const uint2*>(a.z_codes + at));
+    h[1].z = __ldg(reinterpret_cast<const uint2*>(a.z_codes + at + 8 * nb * kCkptBlock));
+    h[0].zs = __ldg(a.z_scales + at / kCkptBlock);
+    h[1].zs = __ldg(a.z_scales + at / kCkptBlock + 8 * nb);
+  }
+}
+__device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns& c, float (&v)[16], int64_t n, int64_t nb,
+                                             const Ahead (&h)[2]) {
+  if (a.col_scale != nullptr || a.col_shift != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float rs = a.col_shift != nullptr ? __ldg(a.row_sum + n + 8 * i) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[8 * i + k] = fmaf(c.add[k], rs, v[8 * i + k] * c.mul[k]);
+    }
+  } else if (a.bias != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] += c.add[k & 7];
+  }
+  if (a.save_codes != nullptr) {
+    const int64_t at = n * nb * kCkptBlock + c.m;
+    const uint32_t m0 = block_magnitude(v), m1 = block_magnitude(v + 8);
+    *reinterpret_cast<uint2*>(a.save_codes + at) = ckpt_pack8(v, m0);
+    *reinterpret_cast<uint2*>(a.save_codes + at + 8 * nb * kCkptBlock) = ckpt_pack8(v + 8, m1);
+    if ((c.m & 31) == 0) {
+      a.save_scales[at / kCkptBlock] = uint8_t(ckpt_scale(m0));
+      a.save_scales[at / kCkptBlock + 8 * nb] = uint8_t(ckpt_scale(m1));
+    }
+  }
+  if (a.z_codes != nullptr) {
+    float z[16];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Pair q[4];
+      ckpt_pairs4(h[i].z.x, h[i].zs, q);
+      ckpt_pairs4(h[i].z.y, h[i].zs, q + 2);
+      floats8(q, z + 8 * i);
+    }
+    mul_slope(v, z, a.act);
+  } else {
+    apply_act(v, a.act);
+  }
+  const int oe = a.out_bf16 ? 2 : 4;
+  char* out = static_cast<char*>(a.out) + (n * a.ldo + c.m) * oe;
+  const int64_t eight = 8 * a.ldo * oe;
+  if (a.out_bf16) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float* u = v + 8 * i;
+      if (a.residual != nullptr) {
+        const uint32_t w[4] = {h[i].r0.x, h[i].r0.y, h[i].r0.z, h[i].r0.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          u[2 * k] += __uint_as_float(w[k] << 16), u[2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint4*>(out + i * eight) = make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]),
+                                                              pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float* u = v + 8 * i;
+      if (a.residual != nullptr) {
+        const uint32_t w[8] = {h[i].r0.x, h[i].r0.y, h[i].r0.z, h[i].r0.w, h[i].r1.x, h[i].r1.y, h[i].r1.z, h[i].r1.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] += __uint_as_float(w[k]);
+      }
+      *reinterpret_cast<float4*>(out + i * eight) = make_float4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<float4*>(out + i * eight + 16) = make_float4(u[4], u[5], u[6], u[7]);
+    }
   }
 }
 
@@ -509,12 +598,21 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
       const int rows = int(min(int64_t(BN), p.a.N - n0));
       Columns col;
       Ahead ahead[kChunk / 8];
+      static_assert(kChunk == 16, "finish_whole takes two rows of eight");
+      // wholly inside an output of wide rows?
+      const bool whole = p.split == 1 && rows == BN && col0(tm) + kTileM <= p.a.M && p.out_wide &&
+                         (p.a.residual == nullptr || p.res_wide);
+      const int64_t nb = (p.a.M + kCkptBlock - 1) / kCkptBlock;
       if (p.split == 1) {
         col = columns_of(p.a, col0(tm) + q * 32 + seg * 8);
+        if (whole) {
+          if (half * kChunk < BN) fetch_whole(p.a, col, n0 + half * kChunk + sub, nb, ahead);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kChunk / 8; ++i) {
-          const int j = half * kChunk + i * 8 + sub;
-          ahead[i] = fetch_ahead(p, col, n0 + j, j < rows);
+          for (int i = 0; i < kChunk / 8; ++i) {
+            const int j = half * kChunk + i * 8 + sub;
+            ahead[i] = fetch_ahead(p, col, n0 + j, j < rows);
+          }
         }
       }
       if (kt0 < kt1) {
@@ -551,16 +649,23 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) st_shared4(mine + uint32_t(i * kChunkPitch + lane) * 4, w[i]);
         __syncwarp();
-        float v[kChunk / 8][8];
+        float v[kChunk / 8 * 8];
 #pragma unroll
-        for (int i = 0; i < kChunk / 8; ++i) ld_shared8(mine + uint32_t((i * 8 + sub) * kChunkPitch + seg * 8) * 4, v[i]);
+        for (int i = 0; i < kChunk / 8; ++i) ld_shared8(mine + uint32_t((i * 8 + sub) * kChunkPitch + seg * 8) * 4, v + 8 * i);
         __syncwarp();
+        if (whole) {
+          const Ahead now[2] = {ahead[0], ahead[1]};
+          if (j0 + kStride < BN) fetch_whole(p.a, col, n0 + j0 + kStride + sub, nb, ahead);
+          finish_whole(p.a, col, v, n0 + j0 + sub, nb, now);
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < kChunk / 8; ++i) {
           const Ahead now = ahead[i];
           const int j = j0 + i * 8 + sub, nx = j + kStride;
           ahead[i] = fetch_ahead(p, col, n0 + nx, nx < rows);
-          finish(p, col, v[i], n0 + j, j < rows, now);
+          float (&u)[8] = reinterpret_cast<float (&)[8]>(v[8 * i]);
+          finish(p, col, u, n0 + j, j < rows, now);
         }
       }
       buf ^= 1;
@@ -674,8 +779,8 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
 // to keep every SM reading.
 constexpr int kRowWarps = 8, kRowsPerWarp = 4;
 
-template <int TT>
-__global__ void __launch_bounds__(kRowWarps * 32, 2) k_linear_rows(const __grid_constant__ Params p) {
+template <int TT, int kAhead>
+__global__ void __launch_bounds__(kRowWarps * 32, kAhead == 2 && TT == 1 ? 3 : 2) k_linear_rows(const __grid_constant__ Params p) {
   __shared__ float sums[TT][kRowWarps * kRowsPerWarp + 4];
   const LinearArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -704,7 +809,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) k_linear_rows(const __grid_
         for (int j = 0; j < 4; ++j) acc[i][t] = fma(wp[i][j], xp[j], acc[i][t]);
     }
   };
-  constexpr int kAhead = TT <= 2 ? 4 : 2;
   int64_t k = lane * 8;
   for (; k + (kAhead - 1) * 256 + 8 <= a.K; k += kAhead * 256) {
     uint4 wv[kAhead][kRowsPerWarp];
@@ -753,9 +857,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) k_linear_rows(const __grid_
   }
 }
 
-template <int TT>
-cudaError_t launch_rows(const Params& p, cudaStream_t s) {
-  k_linear_rows<TT><<<unsigned((p.a.M + 31) / 32), kRowWarps * 32, 0, s>>>(p);
+// Four loads of a row in flight where there are few CTAs per SM, else two and more CTAs (1 row of x:
+// 4096 x 11008 21.2 against 18.7 us, 11008 x 4096 14.6 against 18.6 us).
+cudaError_t launch_rows(const Params& p, int sms, cudaStream_t s) {
+  const unsigned grid = unsigned((p.a.M + 31) / 32);
+  const bool deep = int64_t(grid) <= 2 * int64_t(sms);
+  const auto kernel = p.a.N == 1   ? (deep ? k_linear_rows<1, 4> : k_linear_rows<1, 2>)
+                      : p.a.N == 2 ? (deep ? k_linear_rows<2, 4> : k_linear_rows<2, 2>)
+                                   : k_linear_rows<4, 2>;
+  kernel<<<grid, kRowWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -880,17 +990,17 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   p.res_wide = reinterpret_cast<uintptr_t>(a.residual) % 16 == 0 && (a.N <= 1 || a.ldr * oe % 16 == 0);
   const bool loaders = !p.a_tma || !p.b_tma;
 
+  int slots[4];  // clusters of 1, 2, 4, 8 CTAs that the device runs at once
+  if ((e = cluster_slots(slots)) != cudaSuccess) return e;
   // Few rows of x and rows of w enough for every SM (1 row, 11008 x 4096: 24.8 us with tensor cores).
   if (!a.a_mn && !a.b_mn && !loaders && a.N <= 4 && p.ktiles > 0 && a.M >= 32 * 76) {
     p.split = 1;
-    return a.N == 1 ? launch_rows<1>(p, s) : a.N == 2 ? launch_rows<2>(p, s) : launch_rows<4>(p, s);
+    return launch_rows(p, slots[0], s);
   }
 
   // The tile's width, the split of k or the pairing of CTAs that finish first by this estimate (in
   // units of a 256-wide tile's 64 k): waves x (each part's k tiles at the width's rate + a fixed cost
   // of filling the pipeline and of the epilogue).
-  int slots[4];  // clusters of 1, 2, 4, 8 CTAs that the device runs at once
-  if ((e = cluster_slots(slots)) != cudaSuccess) return e;
   static const int widths[] = {16, 32, 64, 128, 256};
   int best_bn = 0, best_split = 1;
   bool best_pair = false;
