@@ -107,8 +107,8 @@ __device__ __forceinline__ uint4 shifted16(uint4 x, uint4 y, uint32_t off) {
 
 // A tile of ROWS (m or n) x 64 (k) bf16 values by the 64 threads of a loader group; 0 outside the
 // matrix.  A unit that starts on no 16-byte boundary is put together from the aligned sixteen bytes on
-// either side, which lie in the matrix but for its very first and last; those, and units the matrix
-// ends in, go element by element.  The loads of a batch carry no branches, so that all are in flight.
+// either side, which lie in the matrix but for its very first and last; those go element by element,
+// and what a unit holds past the matrix's columns is cleared.  The loads of a batch carry no branches, so that all are in flight.
 constexpr int kGroupThreads = kLoadWarps / kLoadGroups * 32;
 template <int ROWS>
 __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_t ld, int mn, int64_t row0,
@@ -122,33 +122,65 @@ __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_
   const char* tile = lo + (r0 * ld + c0) * 2;
   const int rleft = int(min(rlim - r0, int64_t(ROWS))), cleft = int(min(clim - c0, int64_t(ROWS < 64 ? 64 : ROWS)));
   const int64_t pitch = ld * 2;
+  // inside the matrix by at least an element's sixteen bytes on every side: no bounds
+  if (r0 + (mn ? kTileK : ROWS) <= rlim && c0 + (mn ? ROWS : kTileK) <= clim && tile - lo >= 16 &&
+      hi - (tile + ((mn ? kTileK : ROWS) - 1) * pitch + (mn ? ROWS : kTileK) * 2) >= 16) {
+    const int per_step = kGroupThreads >> shift;  // rows between a thread's units
+    const char* q = tile + (tid >> shift) * pitch + (tid & (per - 1)) * 16;
+    const int64_t next = per_step * pitch;
+#pragma unroll 1
+    for (int i0 = tid; i0 < kItems; i0 += kGroupThreads * kBatch) {
+      uint4 x[kBatch], y[kBatch];
+      uint32_t off[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        off[i] = uint32_t(reinterpret_cast<uintptr_t>(q)) & 15u;
+        const uint4* b = reinterpret_cast<const uint4*>(q - off[i]);
+        x[i] = __ldg(b);
+        y[i] = __ldg(b + 1);
+        q += next;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int at = i0 + i * kGroupThreads;
+        st_shared16(dst + unit_offset(mn, at >> shift, at & (per - 1)), shifted16(x[i], y[i], off[i]));
+      }
+    }
+    return;
+  }
   for (int i0 = tid; i0 < kItems; i0 += kGroupThreads * kBatch) {
     uint4 x[kBatch], y[kBatch];
     const char* q[kBatch];
-    bool whole[kBatch];
+    bool safe[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1);
       q[i] = tile + r * pitch + u * 16;
       const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(q[i])) & 15u;
       const char* b = q[i] - off;
-      whole[i] = r < rleft && u * 8 + 8 <= cleft && b >= lo && (off == 0 || b + 32 <= hi);
+      safe[i] = r < rleft && u * 8 < cleft && b >= lo && b + (off ? 32 : 16) <= hi;
       x[i] = y[i] = make_uint4(0, 0, 0, 0);
-      if (whole[i]) {
+      if (safe[i]) {
         x[i] = __ldg(reinterpret_cast<const uint4*>(b));
         y[i] = __ldg(reinterpret_cast<const uint4*>(off ? b + 16 : b));
       }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1);
+      const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1), n = cleft - u * 8;
       uint4 v = shifted16(x[i], y[i], uint32_t(reinterpret_cast<uintptr_t>(q[i])) & 15u);
-      if (!whole[i] && r < rleft && u * 8 < cleft) {
-        uint32_t h[8];
+      if (r < rleft && n > 0 && (n < 8 || !safe[i])) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          h[k] = u * 8 + k < cleft ? uint32_t(__ldg(reinterpret_cast<const uint16_t*>(q[i]) + k)) : 0u;
-        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t keep = k & 1 ? 0x0000FFFFu : 0xFFFF0000u;  // the other half of the word
+          if (k >= n)
+            w[k / 2] &= keep;
+          else if (!safe[i])
+            w[k / 2] = (w[k / 2] & keep) |
+                       uint32_t(__ldg(reinterpret_cast<const uint16_t*>(q[i]) + k)) << (k & 1 ? 16 : 0);
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
       }
       st_shared16(dst + unit_offset(mn, r, u), v);
     }
