@@ -50,8 +50,10 @@ struct Shape {
 struct Params {
   LinearArgs a;
   int a_tma, b_tma;
+  int a_cut, b_cut;        // the operand's map is cut into 64-wide columns: one box per tile (see make_cut_map)
   int out_wide, res_wide;  // rows of out and residual start on 16-byte boundaries
   int64_t tiles_m, tiles_n;
+  int bn;                    // output rows of a tile: the kernel's BN, or fewer (a multiple of 16, of 32 in a pair)
   int ktiles, split, slots;  // slots: tiles that are worked on at once
   uint64_t wait_ns;  // limit of every wait, longer than the longest tile
 };
@@ -483,7 +485,8 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
   const int64_t tiles = p.tiles_m * p.tiles_n;
   const int kt0 = PAIR ? 0 : int(int64_t(p.ktiles) * rank / p.split);
   const int kt1 = PAIR ? p.ktiles : int(int64_t(p.ktiles) * (rank + 1) / p.split);
-  // First output column of the CTA's part of a tile, and first row.
+  const int brows = PAIR ? p.bn / 2 : p.bn;  // rows of B that the CTA loads
+  // First output column of the CTA's part of a tile.
   const auto col0 = [&](int64_t tm) { return PAIR ? tm * (2 * kTileM) + rank * kTileM : tm * kTileM; };
   // The CTA that issues a pair's products is its first; its barriers count for both.
   static_assert(!(PAIR && LOADERS), "a pair's operands come by TMA: loaders would have to publish across CTAs");
@@ -526,7 +529,10 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
     for (int64_t tile = worker; tile < tiles && !gave_up; tile += workers) {
       int64_t tm, tn;
       tile_at(p, tile, &tm, &tn);
-      const int m0 = int(col0(tm)), n0 = int(tn * BN) + (PAIR ? rank * S::kBRows : 0);
+      const int m0 = int(col0(tm)), n0 = int(tn * p.bn) + (PAIR ? rank * brows : 0);
+      // B's boxes are whole ones: 64 wide along n, however little of the last is used
+      const int bboxes = (brows + 63) / 64;
+      const uint32_t bbytes = p.a.b_mn ? uint32_t(bboxes) * (kTileK * 128) : uint32_t(brows) * 128;
       for (int kt = kt0; kt < kt1; ++kt) {
         if (!mbar_wait(empty(stage), phase ^ 1, p.wait_ns)) {
           gave_up = true;
@@ -534,30 +540,26 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
         }
         const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes, bar = lead(full(stage));
         const int k0 = kt * kTileK;
-        const auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
-          if constexpr (PAIR)
-            tma_load_2d_pair(dst, map, x, y, bar);
-          else
-            tma_load_2d(dst, map, x, y, bar);
-        };
         // the bytes of both CTAs of a pair
         if (!PAIR || rank == 0)
-          mbar_arrive_expect(full(stage), ((p.a_tma ? S::kABytes : 0) + (p.b_tma ? S::kBBytes : 0)) * (PAIR ? 2 : 1));
+          mbar_arrive_expect(full(stage), ((p.a_tma ? S::kABytes : 0) + (p.b_tma ? bbytes : 0)) * (PAIR ? 2 : 1));
         if (p.a_tma) {
           if (!p.a.a_mn) {
-            load(sa, &ta, k0, m0);
+            tma_load_2d<PAIR>(sa, &ta, k0, m0, bar);
+          } else if (p.a_cut) {
+            tma_load_3d<PAIR>(sa, &ta, 0, k0, m0 / 64, bar);
           } else {
 #pragma unroll
-            for (int c = 0; c < kTileM / 64; ++c) load(sa + c * (kTileK * 128), &ta, m0 + c * 64, k0);
+            for (int c = 0; c < kTileM / 64; ++c) tma_load_2d<PAIR>(sa + c * (kTileK * 128), &ta, m0 + c * 64, k0, bar);
           }
         }
         if (p.b_tma) {
           if (!p.a.b_mn) {
-            load(sb, &tb, k0, n0);
+            tma_load_2d<PAIR>(sb, &tb, k0, n0, bar);
+          } else if (p.b_cut) {
+            tma_load_3d<PAIR>(sb, &tb, 0, k0, n0 / 64, bar);
           } else {
-#pragma unroll
-            for (int c = 0; c < (S::kBRows < 64 ? 1 : S::kBRows / 64); ++c)
-              load(sb + c * (kTileK * 128), &tb, n0 + c * 64, k0);
+            for (int c = 0; c < bboxes; ++c) tma_load_2d<PAIR>(sb + c * (kTileK * 128), &tb, n0 + c * 64, k0, bar);
           }
         }
         ++issued;
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
     }
   } else if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {
     // ---- products
-    const uint32_t desc = mma_desc(PAIR ? 2 * kTileM : kTileM, BN, p.a.a_mn, p.a.b_mn);
+    const uint32_t desc = mma_desc(PAIR ? 2 * kTileM : kTileM, p.bn, p.a.a_mn, p.a.b_mn);
     const uint32_t chunk = kTileK * 128;
     const uint64_t astep = p.a.a_mn ? 2048 / 16 : 32 / 16, bstep = p.a.b_mn ? 2048 / 16 : 32 / 16;
     int stage = 0, phase = 0, buf = 0, bphase = 0;
@@ -626,19 +628,19 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
     for (int64_t tile = worker; tile < tiles; tile += workers) {
       int64_t tm, tn;
       tile_at(p, tile, &tm, &tn);
-      const int64_t n0 = tn * BN;
-      const int rows = int(min(int64_t(BN), p.a.N - n0));
+      const int64_t n0 = tn * p.bn;
+      const int rows = int(min(int64_t(p.bn), p.a.N - n0));
       Columns col;
       Ahead ahead[kChunk / 8];
       static_assert(kChunk == 16, "finish_whole takes two rows of eight");
       // wholly inside an output of wide rows?
-      const bool whole = p.split == 1 && rows == BN && col0(tm) + kTileM <= p.a.M && p.out_wide &&
+      const bool whole = p.split == 1 && rows == p.bn && col0(tm) + kTileM <= p.a.M && p.out_wide &&
                          (p.a.residual == nullptr || p.res_wide);
       const int64_t nb = (p.a.M + kCkptBlock - 1) / kCkptBlock;
       if (p.split == 1) {
         col = columns_of(p.a, col0(tm) + q * 32 + seg * 8);
         if (whole) {
-          if (half * kChunk < BN) fetch_whole(p.a, col, n0 + half * kChunk + sub, nb, ahead);
+          if (half * kChunk < rows) fetch_whole(p.a, col, n0 + half * kChunk + sub, nb, ahead);
         } else {
 #pragma unroll
           for (int i = 0; i < kChunk / 8; ++i) {
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
         __syncwarp();
         if (whole) {
           const Ahead now[2] = {ahead[0], ahead[1]};
-          if (j0 + kStride < BN) fetch_whole(p.a, col, n0 + j0 + kStride + sub, nb, ahead);
+          if (j0 + kStride < rows) fetch_whole(p.a, col, n0 + j0 + kStride + sub, nb, ahead);
           finish_whole(p.a, col, v, n0 + j0 + sub, nb, now);
           continue;
         }
@@ -750,8 +752,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
       const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes;
       const int64_t k0 = int64_t(now.kt) * kTileK;
       if (!p.b_tma)
-        fill_plain<S::kBRows>(sb, p.a.b, p.a.ldb, p.a.b_mn, now.tn * BN + (PAIR ? rank * S::kBRows : 0), p.a.N, k0, p.a.K,
-                              tid);
+        fill_plain<S::kBRows>(sb, p.a.b, p.a.ldb, p.a.b_mn, now.tn * p.bn, p.a.N, k0, p.a.K, tid);
       if (!ckpt && !p.a_tma)
         fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, col0(now.tm), p.a.M, k0, p.a.K, tid);
       advance(now, kLoadGroups);
@@ -775,8 +776,8 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
     const int q = warp & 3, side = warp / 4, sides = S::kWarps / 4;
     const int sub = lane / 4, seg = lane & 3;
     const Columns col = columns_of(p.a, tm * kTileM + q * 32 + seg * 8);
-    const int64_t n0 = tn * BN;
-    const int rows = int(min(int64_t(BN), p.a.N - n0));
+    const int64_t n0 = tn * p.bn;
+    const int rows = int(min(int64_t(p.bn), p.a.N - n0));
     const int share = (rows + p.split - 1) / p.split, lo = share * rank, hi = min(rows, lo + share);
     for (int j0 = lo + side * 8; j0 < hi; j0 += sides * 8) {
       const int j = min(j0 + sub, hi - 1);
@@ -937,9 +938,29 @@ cudaError_t make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Map of a bf16 matrix of `rows` rows of `cols` contiguous values, cols a multiple of 64, as columns of
+// 64: boxes of 64 x 64 rows x `columns`, which arrive column after column.  A tile whose rows run along
+// m or n is one such box instead of two to four: the thread that issues them is busy enough (8192 x 14336
+// x 4096 weight gradient 683 -> 598 us).
+cudaError_t make_cut_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int columns) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {64, cuuint64_t(rows), cuuint64_t(cols / 64)};
+  const cuuint64_t strides[2] = {cuuint64_t((ld + 7) / 8 * 8) * 2, 128};
+  const cuuint32_t box[3] = {64, kTileK, cuuint32_t(columns)}, one[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int BN, bool LOADERS, bool PAIR>
-cudaError_t launch(const Params& p, cudaStream_t s) {
+cudaError_t launch(const Params& in, cudaStream_t s) {
   using S = Shape<BN, LOADERS, PAIR>;
+  Params p = in;
+  const int brows = PAIR ? p.bn / 2 : p.bn;
+  p.a_cut = p.a.a_mn && p.a.M % 64 == 0;
+  p.b_cut = p.a.b_mn && p.a.N % 64 == 0 && brows % 64 == 0;
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -952,11 +973,15 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   CUtensorMap ta{}, tb{};
   const LinearArgs& a = p.a;
   if (p.a_tma && p.ktiles > 0) {
-    e = a.a_mn ? make_map(&ta, a.a, a.K, a.M, a.lda, kTileK) : make_map(&ta, a.a, a.M, a.K, a.lda, kTileM);
+    e = p.a_cut ? make_cut_map(&ta, a.a, a.K, a.M, a.lda, kTileM / 64)
+        : a.a_mn ? make_map(&ta, a.a, a.K, a.M, a.lda, kTileK)
+                 : make_map(&ta, a.a, a.M, a.K, a.lda, kTileM);
     if (e != cudaSuccess) return e;
   }
   if (p.b_tma && p.ktiles > 0) {
-    e = a.b_mn ? make_map(&tb, a.b, a.K, a.N, a.ldb, kTileK) : make_map(&tb, a.b, a.N, a.K, a.ldb, S::kBRows);
+    e = p.b_cut ? make_cut_map(&tb, a.b, a.K, a.N, a.ldb, brows / 64)
+        : a.b_mn ? make_map(&tb, a.b, a.K, a.N, a.ldb, kTileK)
+                 : make_map(&tb, a.b, a.N, a.K, a.ldb, brows);
     if (e != cudaSuccess) return e;
   }
   const int64_t tiles = p.tiles_m * p.tiles_n;
@@ -1033,7 +1058,6 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   // The tile's width, the split of k or the pairing of CTAs that finish first by this estimate (in
   // units of a 256-wide tile's 64 k): waves x (each part's k tiles at the width's rate + a fixed cost
   // of filling the pipeline and of the epilogue).
-  static const int widths[] = {16, 32, 64, 128, 256};
   int best_bn = 0, best_split = 1;
   bool best_pair = false;
   double best = 0.0;
@@ -1041,19 +1065,24 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     const int64_t tm = (a.M + (pair ? 2 : 1) * kTileM - 1) / ((pair ? 2 : 1) * kTileM), tn = (a.N + bn - 1) / bn;
     const int64_t tiles = tm * tn, most = slots[pair || split == 2 ? 1 : split == 4 ? 2 : split == 8 ? 3 : 0];
     if (split > 1 && (p.ktiles < 2 * split || tiles > most)) return;
+    // B's boxes along n are 64 wide: with parts of boxes, lines are fetched twice (8192 x 14336 x 4096
+    // weight gradient at 224: 705 us, at 256: 577 us)
+    if (a.b_mn && bn % (pair ? 128 : 64) != 0) return;
     const double waves = double((tiles + most - 1) / most);
-    double per_k = bn >= 256 ? 1.0 : bn == 128 ? 0.6 : bn == 64 ? 0.4 : 0.35;
-    if (pair) per_k *= 0.85;
+    const double per_k = (bn < 64 ? 0.35 : 0.2 + bn / 320.0) * (pair ? 0.85 : 1.0);
     const double t = waves * (double((p.ktiles + split - 1) / split) * per_k + 4.0 + bn / 64.0 + (split > 1 || pair ? 3.0 : 0.0));
     if (best_bn == 0 || t < best) best = t, best_bn = bn, best_split = split, best_pair = pair;
   };
+  // Widths between the kernels' own fill a last wave better (4096 x 4096 x 4096 at 224: 4 whole waves).
+  static const int widths[] = {16, 32, 64, 128, 160, 192, 224, 256};
   for (const int bn : widths) {
     if (bn < 64 && (a.b_mn || loaders)) continue;
     if (bn > 64 && bn / 2 >= a.N) continue;  // more than half of it would be empty
     for (int split = 1; split <= 8; split *= 2) consider(bn, split, false);
-    if (bn == 256 && !loaders) consider(bn, 1, true);
+    if (bn > 128 && !loaders) consider(bn, 1, true);
   }
   p.split = best_split;
+  p.bn = best_bn;
   p.slots = slots[best_pair ? 1 : 0];
   p.tiles_m = (a.M + (best_pair ? 2 : 1) * kTileM - 1) / ((best_pair ? 2 : 1) * kTileM);
   p.tiles_n = (a.N + best_bn - 1) / best_bn;
