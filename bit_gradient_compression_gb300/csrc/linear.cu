@@ -35,10 +35,18 @@ constexpr int kChunkPitch = 36;                // floats per row of 32 columns: 
 
 __device__ unsigned long long g_timeouts;
 
-template <int BN, bool LOADERS, bool PAIR>
+// What an epilogue may be asked for.  A kernel carries the code of its kind alone: with all of it in
+// every kernel, the epilogue's loop missed the instruction cache (a third of its stalls).
+enum Epilogue {
+  kPlain = 0,    // the sums, and a bias
+  kForward = 1,  // bias, activation, checkpoint
+  kAny = 2       // scale and shift, residual, slope of a checkpoint as well
+};
+
+template <int BN, bool LOADERS, bool PAIR, int EPI>
 struct Shape {
   // Epilogue warps: two per quarter of the accumulator's lanes, or one where loader warps need the registers.
-  static constexpr int kEpi = LOADERS ? 4 : 8;
+  static constexpr int kEpi = LOADERS ? 4 : EPI == kAny ? 8 : 12;
   static constexpr int kWarps = 4 + kEpi + (LOADERS ? kLoadWarps : 0);
   static constexpr int kStageOut = kEpi * kChunk * kChunkPitch * 4;
   static constexpr int kABytes = kTileM * kTileK * 2, kBRows = PAIR ? BN / 2 : BN, kBBytes = kBRows * kTileK * 2, kStage = kABytes + kBBytes;
@@ -258,14 +266,15 @@ struct Columns {
   float add[8];   // col_shift, or the bias
 };
 
+template <int EPI>
 __device__ __forceinline__ Columns columns_of(const LinearArgs& a, int64_t m) {
   Columns c;
   c.m = m;
   c.live = int(max(int64_t(0), min(int64_t(8), a.M - m)));
-  const void* add = a.col_shift != nullptr ? a.col_shift : a.bias;
+  const void* add = EPI == kAny && a.col_shift != nullptr ? a.col_shift : a.bias;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    c.mul[k] = a.col_scale != nullptr && k < c.live ? load_elem(a.col_scale, m + k, a.param_bf16) : 1.0f;
+    c.mul[k] = EPI == kAny && a.col_scale != nullptr && k < c.live ? load_elem(a.col_scale, m + k, a.param_bf16) : 1.0f;
     c.add[k] = add != nullptr && k < c.live ? load_elem(add, m + k, a.param_bf16) : 0.0f;
   }
   return c;
@@ -278,13 +287,14 @@ struct Ahead {
   uint32_t zs;    // and their scale
 };
 
+template <int EPI>
 __device__ __forceinline__ Ahead fetch_ahead(const Params& p, const Columns& c, int64_t n, bool row) {
   const LinearArgs& a = p.a;
   Ahead h;
   h.r0 = h.r1 = make_uint4(0, 0, 0, 0);
   h.z = make_uint2(0, 0);
   h.zs = 1;
-  if (!row || c.live <= 0) return h;
+  if (EPI != kAny || !row || c.live <= 0) return h;
   if (a.residual != nullptr) {
     const char* q = static_cast<const char*>(a.residual) + (n * a.ldr + c.m) * (a.out_bf16 ? 2 : 4);
     if (p.res_wide && c.live == 8) {
@@ -312,10 +322,11 @@ __device__ __forceinline__ Ahead fetch_ahead(const Params& p, const Columns& c, 
 }
 
 // Row n of the lane's columns, v the sums over k.  Every lane of the warp takes part; `row`: the row exists.
+template <int EPI>
 __device__ __forceinline__ void finish(const Params& p, const Columns& c, float (&v)[8], int64_t n, bool row,
                                        const Ahead& h) {
   const LinearArgs& a = p.a;
-  if (a.col_scale != nullptr || a.col_shift != nullptr) {
+  if (EPI == kAny && (a.col_scale != nullptr || a.col_shift != nullptr)) {
     const float rs = a.col_shift != nullptr && row ? __ldg(a.row_sum + n) : 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = fmaf(c.add[k], rs, v[k] * c.mul[k]);
@@ -323,7 +334,7 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += c.add[k];
   }
-  if (a.save_codes != nullptr) {
+  if (EPI != kPlain && a.save_codes != nullptr) {
     uint32_t mag = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -339,16 +350,16 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
     }
   }
   if (!row || c.live <= 0) return;
-  if (a.z_codes != nullptr) {
+  if (EPI == kAny && a.z_codes != nullptr) {
     float z[8];
     const float st = ckpt_step(h.zs);
     ckpt_unpack4(h.z.x, st, z);
     ckpt_unpack4(h.z.y, st, z + 4);
     mul_slope(v, z, a.act);
-  } else {
+  } else if (EPI != kPlain) {
     apply_act(v, a.act);
   }
-  if (a.residual != nullptr) {
+  if (EPI == kAny && a.residual != nullptr) {
     const uint32_t w[8] = {h.r0.x, h.r0.y, h.r0.z, h.r0.w, h.r1.x, h.r1.y, h.r1.z, h.r1.w};
     if (a.out_bf16) {
 #pragma unroll
@@ -373,7 +384,9 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
 
 // The same where the tile lies wholly inside an output of wide rows: rows n and n + 8 of the lane's
 // columns at a time, with no bounds, and each choice made once for sixteen values.
+template <int EPI>
 __device__ __forceinline__ void fetch_whole(const LinearArgs& a, const Columns& c, int64_t n, int64_t nb, Ahead (&h)[2]) {
+  if (EPI != kAny) return;
   if (a.residual != nullptr) {
     const int oe = a.out_bf16 ? 2 : 4;
     const char* q = static_cast<const char*>(a.residual) + (n * a.ldr + c.m) * oe;
@@ -393,9 +406,10 @@ __device__ __forceinline__ void fetch_whole(const LinearArgs& a, const Columns& 
     h[1].zs = __ldg(a.z_scales + at / kCkptBlock + 8 * nb);
   }
 }
+template <int EPI>
 __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns& c, float (&v)[16], int64_t n, int64_t nb,
                                              const Ahead (&h)[2]) {
-  if (a.col_scale != nullptr || a.col_shift != nullptr) {
+  if (EPI == kAny && (a.col_scale != nullptr || a.col_shift != nullptr)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float rs = a.col_shift != nullptr ? __ldg(a.row_sum + n + 8 * i) : 0.0f;
@@ -406,7 +420,7 @@ __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns&
 #pragma unroll
     for (int k = 0; k < 16; ++k) v[k] += c.add[k & 7];
   }
-  if (a.save_codes != nullptr) {
+  if (EPI != kPlain && a.save_codes != nullptr) {
     const int64_t at = n * nb * kCkptBlock + c.m;
     const uint32_t m0 = block_magnitude(v), m1 = block_magnitude(v + 8);
     *reinterpret_cast<uint2*>(a.save_codes + at) = ckpt_pack8(v, m0);
@@ -416,7 +430,7 @@ __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns&
       a.save_scales[at / kCkptBlock + 8 * nb] = uint8_t(ckpt_scale(m1));
     }
   }
-  if (a.z_codes != nullptr) {
+  if (EPI == kAny && a.z_codes != nullptr) {
     float z[16];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -426,7 +440,7 @@ __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns&
       floats8(q, z + 8 * i);
     }
     mul_slope(v, z, a.act);
-  } else {
+  } else if (EPI != kPlain) {
     apply_act(v, a.act);
   }
   const int oe = a.out_bf16 ? 2 : 4;
@@ -436,7 +450,7 @@ __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns&
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float* u = v + 8 * i;
-      if (a.residual != nullptr) {
+      if (EPI == kAny && a.residual != nullptr) {
         const uint32_t w[4] = {h[i].r0.x, h[i].r0.y, h[i].r0.z, h[i].r0.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -449,7 +463,7 @@ __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns&
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float* u = v + 8 * i;
-      if (a.residual != nullptr) {
+      if (EPI == kAny && a.residual != nullptr) {
         const uint32_t w[8] = {h[i].r0.x, h[i].r0.y, h[i].r0.z, h[i].r0.w, h[i].r1.x, h[i].r1.y, h[i].r1.z, h[i].r1.w};
 #pragma unroll
         for (int k = 0; k < 8; ++k) u[k] += __uint_as_float(w[k]);
@@ -462,11 +476,11 @@ __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns&
 
 // ------------------------------------------------------------------ the kernel
 
-template <int BN, bool LOADERS, bool PAIR>
-__global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
+template <int BN, bool LOADERS, bool PAIR, int EPI>
+__global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
     k_linear(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
              const __grid_constant__ Params p) {
-  using S = Shape<BN, LOADERS, PAIR>;
+  using S = Shape<BN, LOADERS, PAIR, EPI>;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t bars = base + S::kStages * S::kStage;
@@ -638,14 +652,14 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
                          (p.a.residual == nullptr || p.res_wide);
       const int64_t nb = (p.a.M + kCkptBlock - 1) / kCkptBlock;
       if (p.split == 1) {
-        col = columns_of(p.a, col0(tm) + q * 32 + seg * 8);
+        col = columns_of<EPI>(p.a, col0(tm) + q * 32 + seg * 8);
         if (whole) {
-          if (half * kChunk < rows) fetch_whole(p.a, col, n0 + half * kChunk + sub, nb, ahead);
+          if (half * kChunk < rows) fetch_whole<EPI>(p.a, col, n0 + half * kChunk + sub, nb, ahead);
         } else {
 #pragma unroll
           for (int i = 0; i < kChunk / 8; ++i) {
             const int j = half * kChunk + i * 8 + sub;
-            ahead[i] = fetch_ahead(p, col, n0 + j, j < rows);
+            ahead[i] = fetch_ahead<EPI>(p, col, n0 + j, j < rows);
           }
         }
       }
@@ -689,17 +703,17 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
         __syncwarp();
         if (whole) {
           const Ahead now[2] = {ahead[0], ahead[1]};
-          if (j0 + kStride < rows) fetch_whole(p.a, col, n0 + j0 + kStride + sub, nb, ahead);
-          finish_whole(p.a, col, v, n0 + j0 + sub, nb, now);
+          if (j0 + kStride < rows) fetch_whole<EPI>(p.a, col, n0 + j0 + kStride + sub, nb, ahead);
+          finish_whole<EPI>(p.a, col, v, n0 + j0 + sub, nb, now);
           continue;
         }
 #pragma unroll
         for (int i = 0; i < kChunk / 8; ++i) {
           const Ahead now = ahead[i];
           const int j = j0 + i * 8 + sub, nx = j + kStride;
-          ahead[i] = fetch_ahead(p, col, n0 + nx, nx < rows);
+          ahead[i] = fetch_ahead<EPI>(p, col, n0 + nx, nx < rows);
           float (&u)[8] = reinterpret_cast<float (&)[8]>(v[8 * i]);
-          finish(p, col, u, n0 + j, j < rows, now);
+          finish<EPI>(p, col, u, n0 + j, j < rows, now);
         }
       }
       buf ^= 1;
@@ -775,14 +789,14 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
     tile_at(p, worker, &tm, &tn);
     const int q = warp & 3, side = warp / 4, sides = S::kWarps / 4;
     const int sub = lane / 4, seg = lane & 3;
-    const Columns col = columns_of(p.a, tm * kTileM + q * 32 + seg * 8);
+    const Columns col = columns_of<EPI>(p.a, tm * kTileM + q * 32 + seg * 8);
     const int64_t n0 = tn * p.bn;
     const int rows = int(min(int64_t(p.bn), p.a.N - n0));
     const int share = (rows + p.split - 1) / p.split, lo = share * rank, hi = min(rows, lo + share);
     for (int j0 = lo + side * 8; j0 < hi; j0 += sides * 8) {
       const int j = min(j0 + sub, hi - 1);
       const bool row = j0 + sub < hi;
-      const Ahead h = fetch_ahead(p, col, n0 + j, row);
+      const Ahead h = fetch_ahead<EPI>(p, col, n0 + j, row);
       const uint32_t at = base + uint32_t((j * kTileM + q * 32 + seg * 8) * 4);
       float v[8];
 #pragma unroll
@@ -793,7 +807,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += w[k];
       }
-      finish(p, col, v, n0 + j, row, h);
+      finish<EPI>(p, col, v, n0 + j, row, h);
     }
     cluster_sync();
   }
@@ -812,7 +826,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR>::kWarps * 32, 1)
 // to keep every SM reading.
 constexpr int kRowWarps = 8, kRowsPerWarp = 4;
 
-template <int TT, int kAhead>
+template <int TT, int kAhead, int EPI = kAny>
 __global__ void __launch_bounds__(kRowWarps * 32, kAhead == 2 && TT == 1 ? 3 : 2) k_linear_rows(const __grid_constant__ Params p) {
   __shared__ float sums[TT][kRowWarps * kRowsPerWarp + 4];
   const LinearArgs& a = p.a;
@@ -881,12 +895,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, kAhead == 2 && TT == 1 ? 3 : 2
   if (warp == 0) {
     const int t = lane / 4, seg = lane & 3;
     const bool row = t < a.N;
-    const Columns col = columns_of(a, m0 + seg * 8);
-    const Ahead h = fetch_ahead(p, col, t, row);
+    const Columns col = columns_of<EPI>(a, m0 + seg * 8);
+    const Ahead h = fetch_ahead<EPI>(p, col, t, row);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = row ? sums[t < TT ? t : 0][seg * 8 + j] : 0.0f;
-    finish(p, col, v, t, row, h);
+    finish<EPI>(p, col, v, t, row, h);
   }
 }
 
@@ -954,9 +968,9 @@ cudaError_t make_cut_map(CUtensorMap* map, const void* p, int64_t rows, int64_t 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int BN, bool LOADERS, bool PAIR>
-cudaError_t launch(const Params& in, cudaStream_t s) {
-  using S = Shape<BN, LOADERS, PAIR>;
+template <int BN, bool LOADERS, bool PAIR, int EPI>
+cudaError_t launch_kind(const Params& in, cudaStream_t s) {
+  using S = Shape<BN, LOADERS, PAIR, EPI>;
   Params p = in;
   const int brows = PAIR ? p.bn / 2 : p.bn;
   p.a_cut = p.a.a_mn && p.a.M % 64 == 0;
@@ -966,7 +980,7 @@ cudaError_t launch(const Params& in, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(k_linear<BN, LOADERS, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+    e = cudaFuncSetAttribute(k_linear<BN, LOADERS, PAIR, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
@@ -999,7 +1013,19 @@ cudaError_t launch(const Params& in, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_linear<BN, LOADERS, PAIR>, ta, tb, p);
+  return cudaLaunchKernelEx(&cfg, k_linear<BN, LOADERS, PAIR, EPI>, ta, tb, p);
+}
+
+// Kernels of 128 columns and more come in the three kinds.
+template <int BN, bool LOADERS, bool PAIR>
+cudaError_t launch(const Params& p, cudaStream_t s) {
+  const LinearArgs& a = p.a;
+  if constexpr (BN >= 128 && !LOADERS) {
+    const bool any = a.col_scale != nullptr || a.col_shift != nullptr || a.residual != nullptr || a.z_codes != nullptr;
+    if (!any && a.act == LOCO_ACT_NONE && a.save_codes == nullptr) return launch_kind<BN, LOADERS, PAIR, kPlain>(p, s);
+    if (!any) return launch_kind<BN, LOADERS, PAIR, kForward>(p, s);
+  }
+  return launch_kind<BN, LOADERS, PAIR, kAny>(p, s);
 }
 
 // Clusters of 1, 2, 4 and 8 CTAs of these kernels (one CTA per SM) that the current device holds at
@@ -1009,10 +1035,10 @@ cudaError_t cluster_slots(int (&slots)[4]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  using S = Shape<64, false, false>;
+  using S = Shape<64, false, false, kAny>;
   for (int i = 0; i < 4; ++i) {
     if (dev < 64 && (slots[i] = known[dev][i].load(std::memory_order_relaxed)) > 0) continue;
-    e = cudaFuncSetAttribute(k_linear<64, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+    e = cudaFuncSetAttribute(k_linear<64, false, false, kAny>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(8 * 64);
@@ -1024,7 +1050,7 @@ cudaError_t cluster_slots(int (&slots)[4]) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaOccupancyMaxActiveClusters(&slots[i], k_linear<64, false, false>, &cfg)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&slots[i], k_linear<64, false, false, kAny>, &cfg)) != cudaSuccess) return e;
     if (slots[i] < 1) slots[i] = 1;
     if (dev < 64) known[dev][i].store(slots[i], std::memory_order_relaxed);
   }
