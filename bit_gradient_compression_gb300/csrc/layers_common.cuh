@@ -248,23 +248,52 @@ __device__ __forceinline__ uint32_t ckpt_step_bf16x2(uint32_t scale) {
 }
 
 // ---------------------------------------------------------------------------
-// Activations and their slopes, in fp32.  exp is __expf (within 2 + |x| * 2^-22 units of the last
-// place) and the quotients are __fdividef (2 units); both stay below 1e-6 relative here.
-// A NaN stays one through every activation and slope.
+// Activations and their slopes, in fp32.  2^x and 1/x are the hardware's approximations (2 and 1 units
+// of the last place) on arguments and results that may be flushed to zero: a term below 2^-126 beside
+// 1, or a sigmoid below it.  A NaN stays one through every activation and slope.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+__device__ __forceinline__ float exp2_f(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_f(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2E = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid_f(float v) { return rcp_f(1.0f + exp2_f(v * -kLog2E)); }
 
 constexpr float kGeluK2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluC = 0.044715f;
 
+// The normal distribution function at v and, through `e`, exp(-v^2 / 2): the rational approximation
+// 7.1.26 of Abramowitz and Stegun (Handbook of Mathematical Functions, 1964) for
+// erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2), t = 1 / (1 + 0.3275911 x), x = |v| / sqrt 2, within 1.5e-7;
+// the lower tail comes out without cancellation.
+__device__ __forceinline__ float normal_cdf(float v, float* e) {
+  const float t = rcp_f(fmaf(fabsf(v), 0.3275911f * 0.70710678118654752f, 1.0f));
+  *e = exp2_f(v * v * (-0.5f * kLog2E));
+  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  q = fmaf(t, q, 0.5f * 1.421413741f);
+  q = fmaf(t, q, 0.5f * -0.284496736f);
+  q = fmaf(t, q, 0.5f * 0.254829592f);
+  q *= t * *e;  // half of erfc
+  return v > 0.0f ? 1.0f - q : q;
+}
+
 __device__ __forceinline__ float act_value(float v, int act) {
   switch (act) {
     case LOCO_ACT_RELU: return v <= 0.0f ? 0.0f : v;
-    case LOCO_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case LOCO_ACT_GELU: {
+      float e;
+      return v * normal_cdf(v, &e);
+    }
     case LOCO_ACT_GELU_TANH: {
       // (1 + tanh u) / 2 = sigmoid(2u); beyond |v| = 20 it is 0 or 1 in fp32
       const float c = fminf(fmaxf(v, -20.0f), 20.0f);
-      return v * sigmoid_f(kGeluK2 * fmaf(kGeluC * c * c, c, c));
+      return v * sigmoid_f(c * fmaf(c * c, kGeluK2 * kGeluC, kGeluK2));
     }
     case LOCO_ACT_SILU: return v * sigmoid_f(v);
     default: return v;
@@ -274,13 +303,15 @@ __device__ __forceinline__ float act_value(float v, int act) {
 __device__ __forceinline__ float act_slope(float v, int act) {
   switch (act) {
     case LOCO_ACT_RELU: return v > 0.0f ? 1.0f : (v == v ? 0.0f : v);
-    case LOCO_ACT_GELU:
-      return fmaf(v * 0.3989422804014327f, __expf(-0.5f * fminf(v * v, 160.0f)),
-                  0.5f * (1.0f + erff(v * 0.70710678118654752f)));
+    case LOCO_ACT_GELU: {
+      float e;
+      const float p = normal_cdf(v, &e);
+      return fmaf(v * 0.3989422804014327f, e, p);
+    }
     case LOCO_ACT_GELU_TANH: {
       const float c = fminf(fmaxf(v, -20.0f), 20.0f), q = c * c;
-      const float s = sigmoid_f(kGeluK2 * fmaf(kGeluC * q, c, c));
-      const float d = fmaf(c * s * (1.0f - s), kGeluK2 * fmaf(3.0f * kGeluC, q, 1.0f), s);
+      const float s = sigmoid_f(c * fmaf(q, kGeluK2 * kGeluC, kGeluK2));
+      const float d = fmaf(c * s * (1.0f - s), fmaf(q, 3.0f * kGeluK2 * kGeluC, kGeluK2), s);
       return v == v ? d : v;
     }
     case LOCO_ACT_SILU: {

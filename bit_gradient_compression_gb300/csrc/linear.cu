@@ -120,10 +120,10 @@ __device__ __forceinline__ uint4 shifted16(uint4 x, uint4 y, uint32_t off) {
 // either side, which lie in the matrix but for its very first and last; those go element by element,
 // and what a unit holds past the matrix's columns is cleared.  The loads of a batch carry no branches, so that all are in flight.
 constexpr int kGroupThreads = kLoadWarps / kLoadGroups * 32;
-template <int ROWS>
+template <int ROWS, int kBatch>
 __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_t ld, int mn, int64_t row0,
                                            int64_t rows, int64_t k0, int64_t ks, int tid) {
-  constexpr int kItems = ROWS * 8, kBatch = 4;  // 16-byte units
+  constexpr int kItems = ROWS * 8;  // 16-byte units
   static_assert(kItems % (kGroupThreads * kBatch) == 0, "whole batches");
   const int per = mn ? ROWS / 8 : 8, shift = mn ? (ROWS == 256 ? 5 : ROWS == 128 ? 4 : 3) : 3;
   const int64_t r0 = mn ? k0 : row0, rlim = mn ? ks : rows, c0 = mn ? row0 : k0, clim = mn ? rows : ks;
@@ -158,12 +158,13 @@ __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_
     }
     return;
   }
-  for (int i0 = tid; i0 < kItems; i0 += kGroupThreads * kBatch) {
-    uint4 x[kBatch], y[kBatch];
-    const char* q[kBatch];
-    bool safe[kBatch];
+  constexpr int kEdge = 4;
+  for (int i0 = tid; i0 < kItems; i0 += kGroupThreads * kEdge) {
+    uint4 x[kEdge], y[kEdge];
+    const char* q[kEdge];
+    bool safe[kEdge];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kEdge; ++i) {
       const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1);
       q[i] = tile + r * pitch + u * 16;
       const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(q[i])) & 15u;
@@ -176,7 +177,7 @@ __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kEdge; ++i) {
       const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1), n = cleft - u * 8;
       uint4 v = shifted16(x[i], y[i], uint32_t(reinterpret_cast<uintptr_t>(q[i])) & 15u);
       if (r < rleft && n > 0 && (n < 8 || !safe[i])) {
@@ -726,7 +727,6 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
     const int index = warp - 4 - S::kEpi, group = index / (kLoadWarps / kLoadGroups);
     const int tid = threadIdx.x % kGroupThreads;
     const int64_t nb = (p.a.M + kCkptBlock - 1) / kCkptBlock;
-    const bool ckpt = p.a.a_codes != nullptr;
     const int nk = kt1 - kt0;
     // position of a step of this CTA's k tiles, all tiles counted through
     struct Place {
@@ -746,35 +746,46 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
     } else {
       now.tile = tiles;
     }
-    CkptPart part;
     const auto place = [&](const Place& at) {
       if (at.tile >= tiles) return CkptPlace{p.a.a_codes, p.a.a_scales, 0, false};
       return ckpt_place(p.a, nb, col0(at.tm), int64_t(at.kt) * kTileK, tid);
     };
-    if (ckpt) {
+    int stage = group, phase = 0;
+    static_assert(S::kStages >= kLoadGroups, "a group's first stage is one of the ring's");
+    // Fills the stages of the group's k tiles; fill(stage) goes on to the next of them.
+    const auto walk = [&](auto fill) {
+      while (now.tile < tiles) {
+        if (!warp_wait(empty(stage), phase ^ 1, p.wait_ns)) {
+          gave_up = true;
+          break;
+        }
+        fill(base + stage * S::kStage);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(stage));
+        stage += kLoadGroups;
+        if (stage >= S::kStages) stage -= S::kStages, phase ^= 1;
+      }
+    };
+    if (p.a.a_codes != nullptr) {
+      CkptPart part;
       const CkptPlace at = place(now);
 #pragma unroll
       for (int i = 0; i < kPartRows; ++i) fetch_ckpt(part, i, at, nb);
-    }
-    int stage = group, phase = 0;
-    static_assert(S::kStages >= kLoadGroups, "a group's first stage is one of the ring's");
-    while (now.tile < tiles) {
-      if (!warp_wait(empty(stage), phase ^ 1, p.wait_ns)) {
-        gave_up = true;
-        break;
-      }
-      const uint32_t sa = base + stage * S::kStage, sb = sa + S::kABytes;
-      const int64_t k0 = int64_t(now.kt) * kTileK;
-      if (!p.b_tma)
-        fill_plain<S::kBRows>(sb, p.a.b, p.a.ldb, p.a.b_mn, now.tn * p.bn, p.a.N, k0, p.a.K, tid);
-      if (!ckpt && !p.a_tma)
-        fill_plain<kTileM>(sa, p.a.a, p.a.lda, p.a.a_mn, col0(now.tm), p.a.M, k0, p.a.K, tid);
-      advance(now, kLoadGroups);
-      if (ckpt) fill_ckpt(sa, part, place(now), nb, tid);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full(stage));
-      stage += kLoadGroups;
-      if (stage >= S::kStages) stage -= S::kStages, phase ^= 1;
+      walk([&](uint32_t sa) {
+        if (!p.b_tma)
+          fill_plain<S::kBRows, 4>(sa + S::kABytes, p.a.b, p.a.ldb, p.a.b_mn, now.tn * p.bn, p.a.N,
+                                   int64_t(now.kt) * kTileK, p.a.K, tid);
+        advance(now, kLoadGroups);
+        fill_ckpt(sa, part, place(now), nb, tid);
+      });
+    } else {
+      walk([&](uint32_t sa) {
+        const int64_t k0 = int64_t(now.kt) * kTileK;
+        if (!p.b_tma)
+          fill_plain<S::kBRows, 8>(sa + S::kABytes, p.a.b, p.a.ldb, p.a.b_mn, now.tn * p.bn, p.a.N, k0, p.a.K, tid);
+        if (!p.a_tma) fill_plain<kTileM, 8>(sa, p.a.a, p.a.lda, p.a.a_mn, col0(now.tm), p.a.M, k0, p.a.K, tid);
+        advance(now, kLoadGroups);
+      });
     }
     }
   }
