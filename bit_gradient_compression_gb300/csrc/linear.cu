@@ -40,7 +40,8 @@ __device__ unsigned long long g_timeouts;
 enum Epilogue {
   kPlain = 0,    // the sums, and a bias
   kForward = 1,  // bias, activation, checkpoint
-  kAny = 2       // scale and shift, residual, slope of a checkpoint as well
+  kWeight = 2,   // scale and shift
+  kAny = 3       // all of it, with a residual and the slope at a checkpoint
 };
 
 template <int BN, bool LOADERS, bool PAIR, int EPI>
@@ -132,23 +133,29 @@ __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_
   const char* tile = lo + (r0 * ld + c0) * 2;
   const int rleft = int(min(rlim - r0, int64_t(ROWS))), cleft = int(min(clim - c0, int64_t(ROWS < 64 ? 64 : ROWS)));
   const int64_t pitch = ld * 2;
-  // inside the matrix by at least an element's sixteen bytes on every side: no bounds
-  if (r0 + (mn ? kTileK : ROWS) <= rlim && c0 + (mn ? ROWS : kTileK) <= clim && tile - lo >= 16 &&
-      hi - (tile + ((mn ? kTileK : ROWS) - 1) * pitch + (mn ? ROWS : kTileK) * 2) >= 16) {
-    const int per_step = kGroupThreads >> shift;  // rows between a thread's units
-    const char* q = tile + (tid >> shift) * pitch + (tid & (per - 1)) * 16;
-    const int64_t next = per_step * pitch;
+  // A tile whose 64 k all exist.  What lies past the matrix along m or n only reaches outputs that are
+  // never stored, so rows there are taken from the last that exists and addresses past the end from
+  // the end; the tiles at the matrix's very beginning and end, whose units may not reach around
+  // themselves, go below unless they start on a boundary or end before it.
+  const int rlast = rleft < (mn ? kTileK : ROWS) ? rleft - 1 : (mn ? kTileK : ROWS) - 1;
+  const char* end = tile + rlast * pitch + (mn ? min(cleft, ROWS) : kTileK) * 2;
+  if (k0 + kTileK <= ks && (tile - lo >= 16 || (reinterpret_cast<uintptr_t>(lo) & 15) == 0) && hi - end >= 64) {
+    const bool clamp_rows = !mn && rleft < ROWS, clamp_ends = mn && cleft < ROWS;
+    // the last aligned place to read 32 bytes from, or up to 29 bytes before it: past every unit in use
+    const char* most = lo + (((hi - lo) - 32) & ~int64_t(15)) - (reinterpret_cast<uintptr_t>(lo) & 15);
 #pragma unroll 1
     for (int i0 = tid; i0 < kItems; i0 += kGroupThreads * kBatch) {
       uint4 x[kBatch], y[kBatch];
       uint32_t off[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
+        const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1);
+        const char* q = tile + (clamp_rows ? min(r, rlast) : r) * pitch + u * 16;
         off[i] = uint32_t(reinterpret_cast<uintptr_t>(q)) & 15u;
-        const uint4* b = reinterpret_cast<const uint4*>(q - off[i]);
-        x[i] = __ldg(b);
-        y[i] = __ldg(b + 1);
-        q += next;
+        const char* b = q - off[i];
+        if (clamp_ends && b > most) b = most;
+        x[i] = __ldg(reinterpret_cast<const uint4*>(b));
+        y[i] = __ldg(reinterpret_cast<const uint4*>(b) + 1);
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -272,10 +279,10 @@ __device__ __forceinline__ Columns columns_of(const LinearArgs& a, int64_t m) {
   Columns c;
   c.m = m;
   c.live = int(max(int64_t(0), min(int64_t(8), a.M - m)));
-  const void* add = EPI == kAny && a.col_shift != nullptr ? a.col_shift : a.bias;
+  const void* add = EPI >= kWeight && a.col_shift != nullptr ? a.col_shift : a.bias;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    c.mul[k] = EPI == kAny && a.col_scale != nullptr && k < c.live ? load_elem(a.col_scale, m + k, a.param_bf16) : 1.0f;
+    c.mul[k] = EPI >= kWeight && a.col_scale != nullptr && k < c.live ? load_elem(a.col_scale, m + k, a.param_bf16) : 1.0f;
     c.add[k] = add != nullptr && k < c.live ? load_elem(add, m + k, a.param_bf16) : 0.0f;
   }
   return c;
@@ -327,7 +334,7 @@ template <int EPI>
 __device__ __forceinline__ void finish(const Params& p, const Columns& c, float (&v)[8], int64_t n, bool row,
                                        const Ahead& h) {
   const LinearArgs& a = p.a;
-  if (EPI == kAny && (a.col_scale != nullptr || a.col_shift != nullptr)) {
+  if (EPI >= kWeight && (a.col_scale != nullptr || a.col_shift != nullptr)) {
     const float rs = a.col_shift != nullptr && row ? __ldg(a.row_sum + n) : 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = fmaf(c.add[k], rs, v[k] * c.mul[k]);
@@ -335,7 +342,7 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += c.add[k];
   }
-  if (EPI != kPlain && a.save_codes != nullptr) {
+  if ((EPI == kForward || EPI == kAny) && a.save_codes != nullptr) {
     uint32_t mag = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -357,7 +364,7 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
     ckpt_unpack4(h.z.x, st, z);
     ckpt_unpack4(h.z.y, st, z + 4);
     mul_slope(v, z, a.act);
-  } else if (EPI != kPlain) {
+  } else if (EPI == kForward || EPI == kAny) {
     apply_act(v, a.act);
   }
   if (EPI == kAny && a.residual != nullptr) {
@@ -410,7 +417,7 @@ __device__ __forceinline__ void fetch_whole(const LinearArgs& a, const Columns& 
 template <int EPI>
 __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns& c, float (&v)[16], int64_t n, int64_t nb,
                                              const Ahead (&h)[2]) {
-  if (EPI == kAny && (a.col_scale != nullptr || a.col_shift != nullptr)) {
+  if (EPI >= kWeight && (a.col_scale != nullptr || a.col_shift != nullptr)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float rs = a.col_shift != nullptr ? __ldg(a.row_sum + n + 8 * i) : 0.0f;
@@ -421,7 +428,7 @@ __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns&
 #pragma unroll
     for (int k = 0; k < 16; ++k) v[k] += c.add[k & 7];
   }
-  if (EPI != kPlain && a.save_codes != nullptr) {
+  if ((EPI == kForward || EPI == kAny) && a.save_codes != nullptr) {
     const int64_t at = n * nb * kCkptBlock + c.m;
     const uint32_t m0 = block_magnitude(v), m1 = block_magnitude(v + 8);
     *reinterpret_cast<uint2*>(a.save_codes + at) = ckpt_pack8(v, m0);
@@ -441,7 +448,7 @@ __device__ __forceinline__ void finish_whole(const LinearArgs& a, const Columns&
       floats8(q, z + 8 * i);
     }
     mul_slope(v, z, a.act);
-  } else if (EPI != kPlain) {
+  } else if (EPI == kForward || EPI == kAny) {
     apply_act(v, a.act);
   }
   const int oe = a.out_bf16 ? 2 : 4;
@@ -1027,14 +1034,18 @@ cudaError_t launch_kind(const Params& in, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_linear<BN, LOADERS, PAIR, EPI>, ta, tb, p);
 }
 
-// Kernels of 128 columns and more come in the three kinds.
+// Kernels of 128 columns and more come in kinds; those with loaders in all but the forward one.
 template <int BN, bool LOADERS, bool PAIR>
 cudaError_t launch(const Params& p, cudaStream_t s) {
   const LinearArgs& a = p.a;
-  if constexpr (BN >= 128 && !LOADERS) {
-    const bool any = a.col_scale != nullptr || a.col_shift != nullptr || a.residual != nullptr || a.z_codes != nullptr;
-    if (!any && a.act == LOCO_ACT_NONE && a.save_codes == nullptr) return launch_kind<BN, LOADERS, PAIR, kPlain>(p, s);
-    if (!any) return launch_kind<BN, LOADERS, PAIR, kForward>(p, s);
+  const bool affine = a.col_scale != nullptr || a.col_shift != nullptr, more = a.residual != nullptr || a.z_codes != nullptr;
+  const bool forward = a.act != LOCO_ACT_NONE || a.save_codes != nullptr;
+  if constexpr (BN >= 128) {
+    if (!more && !forward && !affine) return launch_kind<BN, LOADERS, PAIR, kPlain>(p, s);
+    if constexpr (LOADERS)
+      if (!more && !forward) return launch_kind<BN, LOADERS, PAIR, kWeight>(p, s);
+    if constexpr (!LOADERS)
+      if (!more && !affine) return launch_kind<BN, LOADERS, PAIR, kForward>(p, s);
   }
   return launch_kind<BN, LOADERS, PAIR, kAny>(p, s);
 }
