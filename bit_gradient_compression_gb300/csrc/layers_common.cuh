@@ -157,6 +157,46 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int bf16, const float
   }
 }
 
+// Sixteen bytes that begin `off` bytes (a multiple of 2) into x and run on into y.
+__device__ __forceinline__ uint4 shifted16(uint4 x, uint4 y, uint32_t off) {
+  uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+  const uint32_t pick = off & 2 ? 0x5432u : 0x3210u;
+  return make_uint4(__byte_perm(w[0], w[1], pick), __byte_perm(w[1], w[2], pick), __byte_perm(w[2], w[3], pick),
+                    __byte_perm(w[3], w[4], pick));
+}
+
+// Eight elements from any place, where [lo, hi) is the matrix in memory: put together from the aligned
+// sixteen bytes around them, or element by element where those would leave the matrix.
+template <bool BF16>
+__device__ __forceinline__ void load8_any(const char* q, const char* lo, const char* hi, float v[8]) {
+  constexpr int kBytes = BF16 ? 16 : 32;
+  const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(q)) & 15u;
+  const char* b = q - off;
+  if (b >= lo && b + kBytes + (off ? 16 : 0) <= hi) {
+    const uint4* p = reinterpret_cast<const uint4*>(b);
+    const uint4* last = p + (kBytes / 16 - (off ? 0 : 1));
+    if (BF16) {
+      const uint4 w = shifted16(__ldg(p), __ldg(last), off);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[2 * k] = __uint_as_float(u[k] << 16), v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    } else {
+      const uint4 x = __ldg(p), y = __ldg(p + 1), z = __ldg(last);
+      const uint4 a = shifted16(x, y, off), c = shifted16(y, z, off);
+      v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+      v[4] = __uint_as_float(c.x), v[5] = __uint_as_float(c.y), v[6] = __uint_as_float(c.z), v[7] = __uint_as_float(c.w);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = load_elem(q, k, BF16);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // 8-bit checkpoints: a block of 32 values shares the step 2^e, e = max(floor(log2 A) - 6, -126).
 // The exponent field of A's bits is floor(log2 A) + 127 (0 for a subnormal A), so the scale byte

@@ -104,18 +104,6 @@ __device__ __forceinline__ void ld_shared8(uint32_t src, float* v) {
                : "memory");
 }
 
-// Sixteen bytes that begin `off` bytes (a multiple of 2) into x and run on into y.
-__device__ __forceinline__ uint4 shifted16(uint4 x, uint4 y, uint32_t off) {
-  uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
-  const uint32_t pick = off & 2 ? 0x5432u : 0x3210u;
-  return make_uint4(__byte_perm(w[0], w[1], pick), __byte_perm(w[1], w[2], pick), __byte_perm(w[2], w[3], pick),
-                    __byte_perm(w[3], w[4], pick));
-}
-
 // A tile of ROWS (m or n) x 64 (k) bf16 values by the 64 threads of a loader group; 0 outside the
 // matrix.  A unit that starts on no 16-byte boundary is put together from the aligned sixteen bytes on
 // either side, which lie in the matrix but for its very first and last; those go element by element,

@@ -157,13 +157,19 @@ def _addr(x) -> int:
     return x.data_ptr()
 
 
+_raw_stream = None  # torch's stream handle of a device, without a Stream object around it; set once CUDA is there
+
+
 def _stream(stream) -> int:
+    global _raw_stream
     if stream is None:
         import torch
-        if not torch.cuda.is_available():
-            return 0
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
-        return raw(torch.cuda.current_device()) if raw is not None else torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            if not torch.cuda.is_available():
+                return 0
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
