@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libloco.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 SOURCES = ["abi.cu", "compress.cu", "decode_reduce.cu", "adam.cu", "sgd.cu",
            "layers_abi.cu", "checkpoint.cu", "norm.cu", "linear.cu"]
@@ -82,7 +84,23 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str =
         tmp = out + f".tmp{os.getpid()}"
         subprocess.check_call([nvcc(), *LINK_FLAGS, "-o", tmp, *objs])
         os.replace(tmp, out)
+    if out == LIB:
+        build_marshal(force)
     return out
+
+
+def build_marshal(force: bool = False) -> str | None:
+    """Compile the Python binding's marshalling module beside libloco.so (None where Python's headers are
+    missing: the binding then marshals in Python)."""
+    src, inc = os.path.join(CSRC, "marshal.c"), sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(inc, "Python.h")) or shutil.which("gcc") is None:
+        return None
+    if force or _stale(MARSHAL, [src, os.path.join(INCLUDE, "loco.h")]):
+        tmp = MARSHAL + f".tmp{os.getpid()}"
+        subprocess.check_call(["gcc", "-std=c11", "-O2", "-Wall", "-fPIC", "-shared", "-I", inc, "-I", INCLUDE, src, "-o", tmp,
+                               "-L", PKG, "-lloco", "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":

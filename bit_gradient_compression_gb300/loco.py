@@ -262,12 +262,22 @@ def loco_shard_range(n: int, block: int, W: int, j: int) -> tuple[int, int]:
 # two-dimensional tensors whose rows are contiguous (any row pitch).
 # --------------------------------------------------------------------------
 
+# The same marshalling in C (csrc/marshal.c): its functions return the status of the call they made, or
+# None where an argument is not as the entry point wants it; the code below then says what is wrong.
+try:
+    from bit_gradient_compression_gb300 import _marshal
+except ImportError:
+    class _marshal:  # built without Python's headers
+        init = ckpt_encode = ckpt_decode = norm_forward = norm_backward = linear_forward = staticmethod(lambda *a: None)
+        linear_backward_input = linear_backward_weight = init
+
 _DTYPES: dict = {}  # torch.dtype -> loco_dtype, filled on first use (torch is imported only then)
 
 
 def _dtypes():
     import torch
     _DTYPES.update({torch.float32: LOCO_F32, torch.bfloat16: LOCO_BF16})
+    _marshal.init(torch.float32, torch.bfloat16, torch.int8, torch.uint8)
     return _DTYPES
 
 
@@ -369,6 +379,9 @@ def loco_ckpt_scale_bytes(rows: int, cols: int) -> int:
 
 def loco_ckpt_encode(x, codes, scales, *, stream=None):
     """8-bit checkpoint of x [rows, cols]: int8 codes [rows, nb*32], uint8 scales [rows, nb], nb = ceil(cols/32)."""
+    status = _marshal.ckpt_encode(x, codes, scales, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     rows, cols = _dims(x, "x")
     px, ldx = _mat(x, "x", rows, cols)
     pc, ps = _ckpt(codes, scales, rows, cols)
@@ -377,6 +390,9 @@ def loco_ckpt_encode(x, codes, scales, *, stream=None):
 
 def loco_ckpt_decode(codes, scales, out, *, act: int = LOCO_ACT_NONE, gamma=None, beta=None, stream=None):
     """out [rows, cols] = act(values of the checkpoint * gamma + beta)."""
+    status = _marshal.ckpt_decode(codes, scales, out, act, gamma, beta, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     rows, cols = _dims(out, "out")
     po, ldo = _mat(out, "out", rows, cols)
     pc, ps = _ckpt(codes, scales, rows, cols)
@@ -388,6 +404,9 @@ def loco_ckpt_decode(codes, scales, out, *, act: int = LOCO_ACT_NONE, gamma=None
 def loco_norm_forward(cfg: loco_norm_config, x, gamma, beta, y, *, mean=None, rstd=None, codes=None, scales=None,
                       stream=None):
     """y = norm(x) * gamma + beta per row; optionally its statistics and an 8-bit checkpoint of the normalised rows."""
+    status = _marshal.norm_forward(cfg.kind, cfg.eps, x, gamma, beta, y, mean, rstd, codes, scales, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     rows, cols = _dims(x, "x")
     px, ldx = _mat(x, "x", rows, cols)
     py, ldy = _mat(y, "y", rows, cols)
@@ -404,6 +423,10 @@ def loco_norm_workspace_bytes(rows: int, cols: int) -> int:
 def loco_norm_backward(cfg: loco_norm_config, dy, gamma, rstd, dx, *, x=None, mean=None, codes=None, scales=None,
                        residual=None, dgamma=None, dbeta=None, workspace=None, stream=None):
     """Gradients of loco_norm_forward, from x or from the checkpoint of the normalised rows."""
+    status = _marshal.norm_backward(cfg.kind, cfg.eps, dy, gamma, rstd, dx, x, mean, codes, scales, residual, dgamma,
+                                    dbeta, workspace, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     rows, cols = _dims(dy, "dy")
     pdy, lddy = _mat(dy, "dy", rows, cols)
     px, ldx = _mat(x, "x", rows, cols)
@@ -421,6 +444,9 @@ def loco_norm_backward(cfg: loco_norm_config, dy, gamma, rstd, dx, *, x=None, me
 def loco_linear_forward(x, w, y, *, act: int = LOCO_ACT_NONE, bias=None, residual=None, codes=None, scales=None,
                         stream=None):
     """y = act(x w^T + bias) + residual; optionally an 8-bit checkpoint of the pre-activation.  x, w bf16."""
+    status = _marshal.linear_forward(x, w, y, act, bias, residual, codes, scales, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     T, K = _dims(x, "x")
     N, _ = _dims(w, "w")
     _bf16(x, "x")
@@ -438,6 +464,9 @@ def loco_linear_forward(x, w, y, *, act: int = LOCO_ACT_NONE, bias=None, residua
 def loco_linear_backward_input(dy, w, dx, *, act: int = LOCO_ACT_NONE, codes=None, scales=None, residual=None,
                                stream=None):
     """dx = (dy w) * act'(z) + residual, z from the checkpoint of the layer below's pre-activation.  dy, w bf16."""
+    status = _marshal.linear_backward_input(dy, w, dx, act, codes, scales, residual, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     T, N = _dims(dy, "dy")
     _, K = _dims(w, "w")
     _bf16(dy, "dy")
@@ -458,6 +487,10 @@ def loco_linear_workspace_bytes(N: int) -> int:
 def loco_linear_backward_weight(dy, dw, *, x=None, codes=None, scales=None, gamma=None, beta=None, db=None,
                                 workspace=None, stream=None):
     """dw = dy^T x, db = column sums of dy; x [T, K] bf16, or gamma * (values of a checkpoint) + beta."""
+    status = _marshal.linear_backward_weight(dy, dw, x, codes, scales, gamma, beta, db, workspace,
+                                             _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     T, N = _dims(dy, "dy")
     _, K = _dims(dw, "dw")
     _bf16(dy, "dy")
