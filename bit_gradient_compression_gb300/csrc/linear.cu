@@ -83,10 +83,10 @@ __device__ __forceinline__ void tile_at(const Params& p, int64_t tile, int64_t* 
 
 // ------------------------------------------------------------------ loaders
 
-// Byte offset of 16-byte unit u of row r of a tile whose rows run along k (128 bytes each), or of
-// unit u (8 values along m or n) of k-row r: 64-value chunks of 64 rows.
-__device__ __forceinline__ uint32_t unit_offset(int mn, int r, int u) {
-  return (mn ? uint32_t(u >> 3) * (kTileK * 128) : 0u) + uint32_t(r) * 128 + uint32_t(((u & 7) ^ (r & 7)) << 4);
+// Byte offset of 16-byte unit u (8 values along m) of k-row r of a tile that runs along m: 64-value
+// chunks of 64 rows of 128 bytes.  (A tile that runs along k has 128 bytes of k in each row, swizzled alike.)
+__device__ __forceinline__ uint32_t unit_offset(int r, int u) {
+  return uint32_t(u >> 3) * (kTileK * 128) + uint32_t(r) * 128 + uint32_t(((u & 7) ^ (r & 7)) << 4);
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
@@ -96,6 +96,11 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
 __device__ __forceinline__ void st_shared4(uint32_t dst, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t ld_shared4(uint32_t src) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(src) : "memory");
+  return v;
+}
 __device__ __forceinline__ void ld_shared8(uint32_t src, float* v) {
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(src) : "memory");
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -104,91 +109,88 @@ __device__ __forceinline__ void ld_shared8(uint32_t src, float* v) {
                : "memory");
 }
 
-// A tile of ROWS (m or n) x 64 (k) bf16 values by the 64 threads of a loader group; 0 outside the
+// A tile of ROWS (m or n) x 64 (k) bf16 values by the 64 threads of a loader group; 0 for k past the
 // matrix.  A unit that starts on no 16-byte boundary is put together from the aligned sixteen bytes on
-// either side, which lie in the matrix but for its very first and last; those go element by element,
-// and what a unit holds past the matrix's columns is cleared.  The loads of a batch carry no branches, so that all are in flight.
+// either side.  A thread takes the units of every eighth row at the same place in the row (and, along m or
+// n, of the next 128 bytes): eight rows are a multiple of 16 bytes, so all its units lie equally far from a
+// boundary, and the places it reads and writes are eight rows apart.  Every load of a batch is made, without
+// branches, so that all are in flight: those that would leave the matrix are moved inside it.  What they give
+// for rows or columns past the matrix along m or n only reaches outputs that are never stored.  In the tiles
+// at its edges along k, and where it begins and ends, the units are then mended: cleared past the last k, and
+// read element by element where the aligned pieces around them are not all in the matrix.
 constexpr int kGroupThreads = kLoadWarps / kLoadGroups * 32;
 template <int ROWS, int kBatch>
 __device__ __forceinline__ void fill_plain(uint32_t dst, const void* src, int64_t ld, int mn, int64_t row0,
                                            int64_t rows, int64_t k0, int64_t ks, int tid) {
-  constexpr int kItems = ROWS * 8;  // 16-byte units
-  static_assert(kItems % (kGroupThreads * kBatch) == 0, "whole batches");
-  const int per = mn ? ROWS / 8 : 8, shift = mn ? (ROWS == 256 ? 5 : ROWS == 128 ? 4 : 3) : 3;
+  constexpr int kUnits = ROWS / 8;  // of a thread
+  static_assert(kGroupThreads == 64 && kUnits % kBatch == 0 && 8 % kBatch == 0, "whole batches of one column of units");
   const int64_t r0 = mn ? k0 : row0, rlim = mn ? ks : rows, c0 = mn ? row0 : k0, clim = mn ? rows : ks;
   const char* lo = static_cast<const char*>(src);
   const char* hi = lo + ((rlim - 1) * ld + clim) * 2;
   const char* tile = lo + (r0 * ld + c0) * 2;
-  const int rleft = int(min(rlim - r0, int64_t(ROWS))), cleft = int(min(clim - c0, int64_t(ROWS < 64 ? 64 : ROWS)));
+  const int all_rows = mn ? kTileK : ROWS, all_cols = mn ? ROWS : kTileK;
+  const int rleft = int(min(rlim - r0, int64_t(all_rows))), cleft = int(min(clim - c0, int64_t(all_cols)));
   const int64_t pitch = ld * 2;
-  // A tile whose 64 k all exist.  What lies past the matrix along m or n only reaches outputs that are
-  // never stored, so rows there are taken from the last that exists and addresses past the end from
-  // the end; the tiles at the matrix's very beginning and end, whose units may not reach around
-  // themselves, go below unless they start on a boundary or end before it.
-  const int rlast = rleft < (mn ? kTileK : ROWS) ? rleft - 1 : (mn ? kTileK : ROWS) - 1;
-  const char* end = tile + rlast * pitch + (mn ? min(cleft, ROWS) : kTileK) * 2;
-  if (k0 + kTileK <= ks && (tile - lo >= 16 || (reinterpret_cast<uintptr_t>(lo) & 15) == 0) && hi - end >= 64) {
-    const bool clamp_rows = !mn && rleft < ROWS, clamp_ends = mn && cleft < ROWS;
-    // the last aligned place to read 32 bytes from, or up to 29 bytes before it: past every unit in use
-    const char* most = lo + (((hi - lo) - 32) & ~int64_t(15)) - (reinterpret_cast<uintptr_t>(lo) & 15);
+  const char* end = tile + (rleft - 1) * pitch + cleft * 2;  // of what the tile holds of the matrix
+  const bool edge = k0 + kTileK > ks || (tile - lo < 16 && (reinterpret_cast<uintptr_t>(lo) & 15) != 0) || hi - end < 32;
+  const bool inside = !edge && rleft == all_rows && cleft == all_cols;
+  // the first and the last aligned places to read 32 bytes from
+  const char* first = lo + (-reinterpret_cast<uintptr_t>(lo) & 15);
+  const char* most = hi - 32 - (reinterpret_cast<uintptr_t>(hi) & 15);
+  const bool any = most >= first;
+  const int r = tid >> 3, u = tid & 7;
+  const char* q = tile + r * pitch + u * 16;
+  const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(q)) & 15u, to = dst + r * 128 + ((u ^ r) << 4);
+  const int64_t step = 8 * pitch;
+  if (any) {
 #pragma unroll 1
-    for (int i0 = tid; i0 < kItems; i0 += kGroupThreads * kBatch) {
+    for (int i0 = 0; i0 < kUnits; i0 += kBatch) {
       uint4 x[kBatch], y[kBatch];
-      uint32_t off[kBatch];
+      const char* b = q - off + (mn ? (i0 & 7) * step + (i0 >> 3) * 128 : i0 * step);
+      if (inside) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1);
-        const char* q = tile + (clamp_rows ? min(r, rlast) : r) * pitch + u * 16;
-        off[i] = uint32_t(reinterpret_cast<uintptr_t>(q)) & 15u;
-        const char* b = q - off[i];
-        if (clamp_ends && b > most) b = most;
-        x[i] = __ldg(reinterpret_cast<const uint4*>(b));
-        y[i] = __ldg(reinterpret_cast<const uint4*>(b) + 1);
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int at = i0 + i * kGroupThreads;
-        st_shared16(dst + unit_offset(mn, at >> shift, at & (per - 1)), shifted16(x[i], y[i], off[i]));
-      }
-    }
-    return;
-  }
-  constexpr int kEdge = 4;
-  for (int i0 = tid; i0 < kItems; i0 += kGroupThreads * kEdge) {
-    uint4 x[kEdge], y[kEdge];
-    const char* q[kEdge];
-    bool safe[kEdge];
-#pragma unroll
-    for (int i = 0; i < kEdge; ++i) {
-      const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1);
-      q[i] = tile + r * pitch + u * 16;
-      const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(q[i])) & 15u;
-      const char* b = q[i] - off;
-      safe[i] = r < rleft && u * 8 < cleft && b >= lo && b + (off ? 32 : 16) <= hi;
-      x[i] = y[i] = make_uint4(0, 0, 0, 0);
-      if (safe[i]) {
-        x[i] = __ldg(reinterpret_cast<const uint4*>(b));
-        y[i] = __ldg(reinterpret_cast<const uint4*>(off ? b + 16 : b));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kEdge; ++i) {
-      const int at = i0 + i * kGroupThreads, r = at >> shift, u = at & (per - 1), n = cleft - u * 8;
-      uint4 v = shifted16(x[i], y[i], uint32_t(reinterpret_cast<uintptr_t>(q[i])) & 15u);
-      if (r < rleft && n > 0 && (n < 8 || !safe[i])) {
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t keep = k & 1 ? 0x0000FFFFu : 0xFFFF0000u;  // the other half of the word
-          if (k >= n)
-            w[k / 2] &= keep;
-          else if (!safe[i])
-            w[k / 2] = (w[k / 2] & keep) |
-                       uint32_t(__ldg(reinterpret_cast<const uint16_t*>(q[i]) + k)) << (k & 1 ? 16 : 0);
+        for (int i = 0; i < kBatch; ++i) {
+          x[i] = __ldg(reinterpret_cast<const uint4*>(b));
+          y[i] = __ldg(reinterpret_cast<const uint4*>(b) + 1);
+          b += step;
         }
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const char* c = b < first ? first : b > most ? most : b;
+          x[i] = __ldg(reinterpret_cast<const uint4*>(c));
+          y[i] = __ldg(reinterpret_cast<const uint4*>(c) + 1);
+          b += step;
+        }
       }
-      st_shared16(dst + unit_offset(mn, r, u), v);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) st_shared16(to + (i0 + i) * 1024, shifted16(x[i], y[i], off));
+    }
+  }
+  if (!edge) return;
+#pragma unroll 1
+  for (int i = 0; i < kUnits; ++i) {
+    const int ri = r + (mn ? i & 7 : i) * 8, ui = u + (mn ? i >> 3 : 0) * 8, n = ri < rleft ? cleft - ui * 8 : 0;
+    const char* at = tile + ri * pitch + ui * 16;
+    const bool safe = any && at - off >= first && at - off <= most;
+    if (n >= 8 && safe) continue;
+    if (n <= 0) {
+      st_shared16(to + i * 1024, make_uint4(0, 0, 0, 0));
+      continue;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t w = 0;
+      if (n > 2 * k) {
+        if (safe) {
+          w = ld_shared4(to + i * 1024 + 4 * k);
+        } else {
+          w = __ldg(reinterpret_cast<const uint16_t*>(at) + 2 * k);
+          if (n > 2 * k + 1) w |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(at) + 2 * k + 1)) << 16;
+        }
+        if (n == 2 * k + 1) w &= 0xFFFFu;
+      }
+      st_shared4(to + i * 1024 + 4 * k, w);
     }
   }
 }
@@ -236,8 +238,8 @@ __device__ __forceinline__ void fetch_ckpt(CkptPart& c, int i, const CkptPlace& 
 // Turns a part into bf16 in the stage and fetches the next into the registers that come free, so that a
 // load has a whole k tile's work to arrive.
 __device__ __forceinline__ void fill_ckpt(uint32_t dst, CkptPart& c, const CkptPlace& next, int64_t nb, int tid) {
-  const uint32_t d0 = dst + unit_offset(1, part_row(tid), 2 * part_half(tid));
-  const uint32_t d1 = dst + unit_offset(1, part_row(tid), 2 * part_half(tid) + 1);
+  const uint32_t d0 = dst + unit_offset(part_row(tid), 2 * part_half(tid));
+  const uint32_t d1 = dst + unit_offset(part_row(tid), 2 * part_half(tid) + 1);
 #pragma unroll
   for (int i = 0; i < kPartRows; ++i) {
     const uint32_t st = ckpt_step_bf16x2(c.scale[i]);
@@ -318,9 +320,10 @@ __device__ __forceinline__ Ahead fetch_ahead(const Params& p, const Columns& c, 
 }
 
 // Row n of the lane's columns, v the sums over k.  Every lane of the warp takes part; `row`: the row exists.
+// With `keep` the result goes back to that place in shared memory instead of the output.
 template <int EPI>
 __device__ __forceinline__ void finish(const Params& p, const Columns& c, float (&v)[8], int64_t n, bool row,
-                                       const Ahead& h) {
+                                       const Ahead& h, uint32_t keep = 0) {
   const LinearArgs& a = p.a;
   if (EPI >= kWeight && (a.col_scale != nullptr || a.col_shift != nullptr)) {
     const float rs = a.col_shift != nullptr && row ? __ldg(a.row_sum + n) : 0.0f;
@@ -369,7 +372,10 @@ __device__ __forceinline__ void finish(const Params& p, const Columns& c, float 
     }
   }
   const int64_t at = n * a.ldo + c.m;
-  if (p.out_wide && c.live == 8) {
+  if (keep != 0) {
+    st_shared16(keep, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+    st_shared16(keep + 16, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+  } else if (p.out_wide && c.live == 8) {
     store8(a.out, at, a.out_bf16, v);
   } else {
 #pragma unroll
@@ -647,6 +653,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
       const bool whole = p.split == 1 && rows == p.bn && col0(tm) + kTileM <= p.a.M && p.out_wide &&
                          (p.a.residual == nullptr || p.res_wide);
       const int64_t nb = (p.a.M + kCkptBlock - 1) / kCkptBlock;
+      const int64_t m0 = col0(tm) + q * 32;  // the warp's columns
       if (p.split == 1) {
         col = columns_of<EPI>(p.a, col0(tm) + q * 32 + seg * 8);
         if (whole) {
@@ -709,7 +716,19 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
           const int j = j0 + i * 8 + sub, nx = j + kStride;
           ahead[i] = fetch_ahead<EPI>(p, col, n0 + nx, nx < rows);
           float (&u)[8] = reinterpret_cast<float (&)[8]>(v[8 * i]);
-          finish<EPI>(p, col, u, n0 + j, j < rows, now);
+          finish<EPI>(p, col, u, n0 + j, j < rows, now,
+                      p.out_wide ? 0u : mine + uint32_t((i * 8 + sub) * kChunkPitch + seg * 8) * 4);
+        }
+        if (!p.out_wide) {
+          // Rows that take no 16-byte stores: a column per lane, so that a store meets one row's lines and
+          // not those of eight rows (4095 x 4097 x 4099, bf16 output: 192 us with stores of eight rows, 136 us so, both of aligned operands).
+          __syncwarp();
+          const int some = m0 + lane < p.a.M ? min(rows - j0, kChunk) : 0;
+          int64_t at = (n0 + j0) * p.a.ldo + m0 + lane;
+#pragma unroll 4
+          for (int i = 0; i < some; ++i, at += p.a.ldo)
+            store_elem(p.a.out, at, p.a.out_bf16, __uint_as_float(ld_shared4(mine + uint32_t(i * kChunkPitch + lane) * 4)));
+          __syncwarp();
         }
       }
       buf ^= 1;
