@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libloco.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 
 SOURCES = ["abi.cu", "compress.cu", "decode_reduce.cu", "adam.cu", "sgd.cu",
-           "layers_abi.cu", "checkpoint.cu", "norm.cu", "linear.cu"]
+           "layers_abi.cu", "checkpoint.cu", "norm.cu", "align.cu", "linear.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false: no multiply-add contraction anywhere; every fp32 product and sum

@@ -285,6 +285,22 @@ loco_status loco_norm_backward(const loco_norm_config* cfg, const void* dy, int6
   return launch_result(launch_norm_backward(a, reinterpret_cast<cudaStream_t>(stream)), "loco_norm_backward");
 }
 
+loco_status loco_linear_align(const void* src, int64_t lds, int64_t rows, int64_t cols, void* dst, int64_t ldd,
+                              loco_stream_t stream) {
+  LOCO_TRY(check_dim(rows, 0, "rows"));
+  LOCO_TRY(check_dim(cols, 0, "cols"));
+  if (rows == 0 || cols == 0) return done();
+  if (ldd < cols || ldd % 8 != 0 || ldd > kMaxDim)
+    return fail(LOCO_ERR_INVALID_ARG, "ldd = %lld must be a multiple of 8 in [cols, LOCO_MAX_DIM]", (long long)ldd);
+  Args g;
+  g.add(src, rows, cols, lds, 2, 2, "src");
+  g.outputs();
+  g.add(dst, rows, (cols + 7) / 8 * 8, ldd, 2, 16, "dst");
+  LOCO_TRY(g.check());
+  return launch_result(launch_align(AlignArgs{src, lds, rows, cols, dst, ldd}, reinterpret_cast<cudaStream_t>(stream)),
+                       "loco_linear_align");
+}
+
 loco_status loco_linear_forward(const loco_linear_config* cfg, const void* x, int64_t ldx, const void* w, int64_t ldw,
                                 const void* bias, const void* residual, int64_t ldr, int64_t T, int64_t N, int64_t K,
                                 void* y, int64_t ldy, int8_t* codes, uint8_t* scales, loco_stream_t stream) {

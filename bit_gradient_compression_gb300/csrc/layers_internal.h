@@ -94,6 +94,13 @@ struct LinearArgs {
   int out_bf16;
 };
 
+struct AlignArgs {
+  const void* src;          // [rows, cols] bf16
+  int64_t lds, rows, cols;
+  void* dst;                // on a 16-byte boundary, ldd a multiple of 8
+  int64_t ldd;
+};
+
 struct ColSumArgs {
   const void* x;            // [rows, cols] bf16
   int64_t ldx, rows, cols;
@@ -106,6 +113,7 @@ cudaError_t launch_ckpt_encode(const EncodeArgs& a, cudaStream_t s);
 cudaError_t launch_ckpt_decode(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_norm_forward(const NormFwdArgs& a, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormBwdArgs& a, cudaStream_t s);
+cudaError_t launch_align(const AlignArgs& a, cudaStream_t s);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_col_sum(const ColSumArgs& a, cudaStream_t s);
 cudaError_t read_linear_timeouts(int64_t* count);

@@ -18,6 +18,8 @@
 
 static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_is_contiguous;
 static PyObject *t_f32, *t_bf16, *t_i8, *t_u8; /* torch's dtype objects, set by init() */
+static double align_work;                        /* loco.py's ALIGN_WORK and ALIGN_ROWS, set by init() */
+static int64_t align_rows;
 
 /* One argument: 1 found, 0 not as wanted (the caller gives up), never an exception left behind. */
 typedef struct {
@@ -118,6 +120,54 @@ static int bytes_of(PyObject* t, void** p, int64_t* n) {
   return d == t_u8 && (stride == 1 || *n <= 1) && address(t, p);
 }
 
+/*
+ * Copies the operands of a product over t rows to aligned rows where that pays (loco.py says when; least: the
+ * fewest rows), in one piece of memory of alloc(bytes), which the caller releases after its call; without
+ * alloc it gives up.
+ * Returns 1, or 0 to give up, or -1 for a failed copy with its status in *status.
+ */
+static int align(Mat* x, Mat* w, int64_t t, int64_t n, int64_t k, int64_t least, PyObject* alloc,
+                 loco_stream_t st, PyObject** held, int* status) {
+  Mat* m[2] = {x, w};
+  int64_t at[2] = {0, 0}, bytes = 0;
+  *held = NULL;
+  if (t < least || (double)t * (double)n * (double)k < align_work) return 1;
+  for (int i = 0; i < 2; ++i) {
+    if (m[i]->p == NULL || ((uintptr_t)m[i]->p % 16 == 0 && (m[i]->rows <= 1 || m[i]->ld % 8 == 0))) continue;
+    at[i] = bytes;
+    bytes += (m[i]->rows * ((m[i]->cols + 7) / 8 * 16) + 255) / 256 * 256;
+    m[i]->dtype = -3; /* to be copied */
+  }
+  if (bytes == 0) return 1;
+  if (alloc == Py_None) return 0;
+  PyObject* size = PyLong_FromLongLong(bytes);
+  *held = size == NULL ? NULL : PyObject_CallOneArg(alloc, size);
+  Py_XDECREF(size);
+  void* base;
+  if (*held == Py_None) return 1; /* no memory: the product reads them as they lie */
+  if (*held == NULL || !address(*held, &base)) return 0;
+  for (int i = 0; i < 2; ++i) {
+    if (m[i]->dtype != -3) continue;
+    const int64_t pitch = (m[i]->cols + 7) / 8 * 8;
+    *status = loco_linear_align(m[i]->p, m[i]->ld, m[i]->rows, m[i]->cols, (char*)base + at[i], pitch, st);
+    if (*status != LOCO_OK) return -1;
+    m[i]->p = (char*)base + at[i], m[i]->ld = pitch;
+  }
+  return 1;
+}
+#define ALIGN(x, w, t, n, k, least, alloc)                              \
+  PyObject* held;                                                       \
+  int status;                                                           \
+  const int ready = align(x, w, t, n, k, least, alloc, st, &held, &status); \
+  if (ready < 1) {                                                      \
+    Py_XDECREF(held);                                                   \
+    return ready < 0 ? PyLong_FromLong(status) : give_up();             \
+  }
+#define CALL_ALIGNED(call)                       \
+  Py_BEGIN_ALLOW_THREADS status = (call);        \
+  Py_END_ALLOW_THREADS Py_XDECREF(held);         \
+  return PyLong_FromLong(status)
+
 /* The one type of two tensors, where -1 is a tensor that is not there; -2, and so on from there, where they differ. */
 static int one(int a, int b) { return a == -1 ? b : b == -1 || a == b ? a : -2; }
 static int or_f32(int d) { return d == -1 ? LOCO_F32 : d; }
@@ -204,9 +254,9 @@ static PyObject* norm_backward(PyObject* self, PyObject* const* a, Py_ssize_t n)
                           db, w, nw, st));
 }
 
-/* (x, w, y, act, bias, residual, codes, scales, stream) */
+/* (x, w, y, act, bias, residual, codes, scales, stream, alloc) */
 static PyObject* linear_forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  ARGS(9);
+  ARGS(10);
   Mat x, w, y, res;
   void *b, *c, *s;
   int pd = -1;
@@ -216,12 +266,14 @@ static PyObject* linear_forward(PyObject* self, PyObject* const* a, Py_ssize_t n
   const loco_linear_config cfg = {(int32_t)integer(a[3]), one(y.dtype, res.dtype), or_f32(pd)};
   const loco_stream_t st = STREAM(a[8]);
   WANT(cfg.out_dtype >= 0);
-  CALL(loco_linear_forward(&cfg, x.p, x.ld, w.p, w.ld, b, res.p, res.ld, x.rows, w.rows, x.cols, y.p, y.ld, c, s, st));
+  ALIGN(&x, &w, x.rows, w.rows, x.cols, align_rows, a[9]);
+  CALL_ALIGNED(loco_linear_forward(&cfg, x.p, x.ld, w.p, w.ld, b, res.p, res.ld, x.rows, w.rows, x.cols, y.p, y.ld, c, s,
+                                   st));
 }
 
-/* (dy, w, dx, act, codes, scales, residual, stream) */
+/* (dy, w, dx, act, codes, scales, residual, stream, alloc) */
 static PyObject* linear_backward_input(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  ARGS(8);
+  ARGS(9);
   Mat dy, w, dx, res;
   void *c, *s;
   WANT(a[0] != Py_None && a[1] != Py_None && a[2] != Py_None && mat(a[0], -1, -1, &dy) && mat(a[1], dy.cols, -1, &w));
@@ -230,13 +282,14 @@ static PyObject* linear_backward_input(PyObject* self, PyObject* const* a, Py_ss
   const loco_linear_config cfg = {(int32_t)integer(a[3]), one(dx.dtype, res.dtype), LOCO_F32};
   const loco_stream_t st = STREAM(a[7]);
   WANT(cfg.out_dtype >= 0);
-  CALL(loco_linear_backward_input(&cfg, dy.p, dy.ld, w.p, w.ld, c, s, res.p, res.ld, dy.rows, dy.cols, w.cols, dx.p,
-                                  dx.ld, st));
+  ALIGN(&dy, &w, dy.rows, dy.cols, w.cols, align_rows, a[8]);
+  CALL_ALIGNED(loco_linear_backward_input(&cfg, dy.p, dy.ld, w.p, w.ld, c, s, res.p, res.ld, dy.rows, dy.cols, w.cols,
+                                          dx.p, dx.ld, st));
 }
 
-/* (dy, dw, x, codes, scales, gamma, beta, db, workspace, stream) */
+/* (dy, dw, x, codes, scales, gamma, beta, db, workspace, stream, alloc) */
 static PyObject* linear_backward_weight(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  ARGS(10);
+  ARGS(11);
   Mat dy, dw, x;
   void *c, *s, *g, *b, *db, *w;
   int64_t nw;
@@ -249,16 +302,19 @@ static PyObject* linear_backward_weight(PyObject* self, PyObject* const* a, Py_s
   const loco_linear_config cfg = {LOCO_ACT_NONE, od, or_f32(pd)};
   const loco_stream_t st = STREAM(a[9]);
   WANT(1);
-  CALL(loco_linear_backward_weight(&cfg, dy.p, dy.ld, x.p, x.ld, c, s, g, b, dy.rows, dy.cols, dw.cols, dw.p, dw.ld, db,
-                                   w, nw, st));
+  ALIGN(&dy, &x, dy.rows, dy.cols, dw.cols, 0, a[10]);
+  CALL_ALIGNED(loco_linear_backward_weight(&cfg, dy.p, dy.ld, x.p, x.ld, c, s, g, b, dy.rows, dy.cols, dw.cols, dw.p,
+                                           dw.ld, db, w, nw, st));
 }
 
-/* init(float32, bfloat16, int8, uint8): torch's dtype objects.  Until then every function returns None. */
+/* init(float32, bfloat16, int8, uint8, ALIGN_WORK, ALIGN_ROWS).  Until then every function returns None. */
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "four dtypes");
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "four dtypes and two numbers");
     return NULL;
   }
+  align_work = PyFloat_AsDouble(a[4]), align_rows = integer(a[5]);
+  if (PyErr_Occurred()) return NULL;
   PyObject** to[4] = {&t_f32, &t_bf16, &t_i8, &t_u8};
   for (int i = 0; i < 4; ++i) {
     Py_INCREF(a[i]);

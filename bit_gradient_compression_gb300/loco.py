@@ -5,7 +5,8 @@ but turn tensors (or raw integer device addresses) into pointers and sizes,
 pick the current torch CUDA stream, and raise ``LocoError`` on a non-OK
 status.  All arithmetic runs in the CUDA kernels of ``libloco.so``; there is
 no CPU or PyTorch fallback: if the library is missing, importing this module
-fails.
+fails.  The layer calls take torch's memory in one case, for aligned copies of
+operands of large products (see ALIGN_WORK); everything else is the caller's.
 """
 from __future__ import annotations
 
@@ -29,7 +30,8 @@ LOCO_MAX_N = 1 << 48
 EXPORTS = ("loco_num_blocks", "loco_code_bytes", "loco_compress", "loco_compress_e8", "loco_decode_reduce",
            "loco_adam_step", "loco_adam_step_bf16", "loco_sgd_step", "loco_shard_range", "loco_status_string",
            "loco_last_error", "loco_ckpt_code_bytes", "loco_ckpt_scale_bytes", "loco_ckpt_encode", "loco_ckpt_decode",
-           "loco_norm_forward", "loco_norm_workspace_bytes", "loco_norm_backward", "loco_linear_forward",
+           "loco_norm_forward", "loco_norm_workspace_bytes", "loco_norm_backward", "loco_linear_align",
+           "loco_linear_forward",
            "loco_linear_backward_input", "loco_linear_workspace_bytes", "loco_linear_backward_weight",
            "loco_linear_timeouts")
 
@@ -118,6 +120,8 @@ lib.loco_norm_workspace_bytes.restype = _i64
 lib.loco_norm_backward.argtypes = [_norm, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
                                    _i64, _vp, _vp, _vp, _i64, _vp]
 lib.loco_norm_backward.restype = ctypes.c_int
+lib.loco_linear_align.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp]
+lib.loco_linear_align.restype = ctypes.c_int
 lib.loco_linear_forward.argtypes = [_lin, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp,
                                     _vp]
 lib.loco_linear_forward.restype = ctypes.c_int
@@ -262,6 +266,13 @@ def loco_shard_range(n: int, block: int, W: int, j: int) -> tuple[int, int]:
 # two-dimensional tensors whose rows are contiguous (any row pitch).
 # --------------------------------------------------------------------------
 
+# A linear layer's operand whose rows start on no 16-byte boundary is copied to aligned rows first, in memory
+# of torch's allocator, in products of at least this many multiplications (a call for T, N, K = 200, 1000, 1001:
+# 18.6 us as they lie, 20.6 us copied; 333, 1407, 2049: 28.0 and 24.8 us; 4095, 4097, 4099: 440 and 144 us), and
+# where w is an operand in those over at least this many rows, as a copy of w costs more than reading it once
+# (input gradient of 64 rows, 11007, 4097: 47 us as they lie, 61 us copied; of 129, 1407, 2049: 24.7 and 23.9 us).
+ALIGN_WORK, ALIGN_ROWS = 1 << 28, 96
+
 # The same marshalling in C (csrc/marshal.c): its functions return the status of the call they made, or
 # None where an argument is not as the entry point wants it; the code below then says what is wrong.
 try:
@@ -277,7 +288,7 @@ _DTYPES: dict = {}  # torch.dtype -> loco_dtype, filled on first use (torch is i
 def _dtypes():
     import torch
     _DTYPES.update({torch.float32: LOCO_F32, torch.bfloat16: LOCO_BF16})
-    _marshal.init(torch.float32, torch.bfloat16, torch.int8, torch.uint8)
+    _marshal.init(torch.float32, torch.bfloat16, torch.int8, torch.uint8, ALIGN_WORK, ALIGN_ROWS)
     return _DTYPES
 
 
@@ -441,43 +452,83 @@ def loco_norm_backward(cfg: loco_norm_config, dy, gamma, rstd, dx, *, x=None, me
                                   _vec(dgamma, "dgamma", cols), _vec(dbeta, "dbeta", cols), pw, nw, _stream(stream)))
 
 
+def loco_linear_align(src, dst, *, stream=None):
+    """dst [rows, cols] = src, both bf16; the rows of dst start on 16-byte boundaries and are followed by zeros up to
+    the next multiple of 8 columns."""
+    rows, cols = _dims(src, "src")
+    _bf16(src, "src")
+    _bf16(dst, "dst")
+    ps, lds = _mat(src, "src", rows, cols)
+    pd, ldd = _mat(dst, "dst", rows, cols)
+    _check(lib.loco_linear_align(ps, lds, rows, cols, pd, ldd, _stream(stream)))
+
+
+def _scratch(nbytes: int):
+    """Memory for a call on the current stream; None if there is none left."""
+    import torch
+    try:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    except torch.cuda.OutOfMemoryError:
+        return None
+
+
+def _operand(t, name: str, rows: int, cols: int, product, stream: int, least: int = 0):
+    """(address, row pitch, what keeps it) of an operand of a product of T, N, K, in aligned rows where that pays."""
+    p, ld = _mat(t, name, rows, cols)
+    T, N, K = product
+    if (t is None or T < least or T * N * K < ALIGN_WORK or not t.is_cuda
+            or (p % 16 == 0 and (rows <= 1 or ld % 8 == 0))):
+        return p, ld, None
+    import torch
+    pitch = -(-cols // 8) * 8
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, t.device)):  # memory comes and goes in its order
+        copy = _scratch(rows * pitch * 2)
+    if copy is None:
+        return p, ld, None
+    _check(lib.loco_linear_align(p, ld, rows, cols, copy.data_ptr(), pitch, stream))
+    return copy.data_ptr(), pitch, copy
+
+
 def loco_linear_forward(x, w, y, *, act: int = LOCO_ACT_NONE, bias=None, residual=None, codes=None, scales=None,
                         stream=None):
     """y = act(x w^T + bias) + residual; optionally an 8-bit checkpoint of the pre-activation.  x, w bf16."""
-    status = _marshal.linear_forward(x, w, y, act, bias, residual, codes, scales, _stream(stream))
+    status = _marshal.linear_forward(x, w, y, act, bias, residual, codes, scales, _stream(stream),
+                                     _scratch if stream is None else None)
     if status is not None:
         return _check(status) if status else None
     T, K = _dims(x, "x")
     N, _ = _dims(w, "w")
     _bf16(x, "x")
     _bf16(w, "w")
-    px, ldx = _mat(x, "x", T, K)
-    pw, ldw = _mat(w, "w", N, K)
+    st = _stream(stream)
     pr, ldr = _mat(residual, "residual", T, N)
     py, ldy = _mat(y, "y", T, N)
     pc, ps = _ckpt(codes, scales, T, N)
-    c = _linear_ref(act, _one_dtype("y and residual", y, residual), _one_dtype("bias", bias))
-    _check(lib.loco_linear_forward(c, px, ldx, pw, ldw, _vec(bias, "bias", N), pr, ldr, T, N, K, py, ldy, pc, ps,
-                                   _stream(stream)))
+    c, pb = _linear_ref(act, _one_dtype("y and residual", y, residual), _one_dtype("bias", bias)), _vec(bias, "bias", N)
+    px, ldx, _x = _operand(x, "x", T, K, (T, N, K), st, ALIGN_ROWS)
+    pw, ldw, _w = _operand(w, "w", N, K, (T, N, K), st, ALIGN_ROWS)
+    _check(lib.loco_linear_forward(c, px, ldx, pw, ldw, pb, pr, ldr, T, N, K, py, ldy, pc, ps, st))
 
 
 def loco_linear_backward_input(dy, w, dx, *, act: int = LOCO_ACT_NONE, codes=None, scales=None, residual=None,
                                stream=None):
     """dx = (dy w) * act'(z) + residual, z from the checkpoint of the layer below's pre-activation.  dy, w bf16."""
-    status = _marshal.linear_backward_input(dy, w, dx, act, codes, scales, residual, _stream(stream))
+    status = _marshal.linear_backward_input(dy, w, dx, act, codes, scales, residual, _stream(stream),
+                                            _scratch if stream is None else None)
     if status is not None:
         return _check(status) if status else None
     T, N = _dims(dy, "dy")
     _, K = _dims(w, "w")
     _bf16(dy, "dy")
     _bf16(w, "w")
-    pdy, lddy = _mat(dy, "dy", T, N)
-    pw, ldw = _mat(w, "w", N, K)
+    st = _stream(stream)
     pr, ldr = _mat(residual, "residual", T, K)
     pdx, lddx = _mat(dx, "dx", T, K)
     pc, ps = _ckpt(codes, scales, T, K)
     c = _linear_ref(act, _one_dtype("dx and residual", dx, residual), LOCO_F32)
-    _check(lib.loco_linear_backward_input(c, pdy, lddy, pw, ldw, pc, ps, pr, ldr, T, N, K, pdx, lddx, _stream(stream)))
+    pdy, lddy, _dy = _operand(dy, "dy", T, N, (T, N, K), st, ALIGN_ROWS)
+    pw, ldw, _w = _operand(w, "w", N, K, (T, N, K), st, ALIGN_ROWS)
+    _check(lib.loco_linear_backward_input(c, pdy, lddy, pw, ldw, pc, ps, pr, ldr, T, N, K, pdx, lddx, st))
 
 
 def loco_linear_workspace_bytes(N: int) -> int:
@@ -488,21 +539,21 @@ def loco_linear_backward_weight(dy, dw, *, x=None, codes=None, scales=None, gamm
                                 workspace=None, stream=None):
     """dw = dy^T x, db = column sums of dy; x [T, K] bf16, or gamma * (values of a checkpoint) + beta."""
     status = _marshal.linear_backward_weight(dy, dw, x, codes, scales, gamma, beta, db, workspace,
-                                             _stream(stream))
+                                             _stream(stream), _scratch if stream is None else None)
     if status is not None:
         return _check(status) if status else None
     T, N = _dims(dy, "dy")
     _, K = _dims(dw, "dw")
     _bf16(dy, "dy")
     _bf16(x, "x")
-    pdy, lddy = _mat(dy, "dy", T, N)
-    px, ldx = _mat(x, "x", T, K)
+    st = _stream(stream)
     pdw, lddw = _mat(dw, "dw", N, K)
     pc, ps = _ckpt(codes, scales, T, K)
-    pw, nw = _workspace(workspace)
+    pg, pb, pdb, (pw, nw) = _vec(gamma, "gamma", K), _vec(beta, "beta", K), _vec(db, "db", N), _workspace(workspace)
     c = _linear_ref(LOCO_ACT_NONE, _one_dtype("dw and db", dw, db), _one_dtype("gamma and beta", gamma, beta))
-    _check(lib.loco_linear_backward_weight(c, pdy, lddy, px, ldx, pc, ps, _vec(gamma, "gamma", K), _vec(beta, "beta", K),
-                                           T, N, K, pdw, lddw, _vec(db, "db", N), pw, nw, _stream(stream)))
+    pdy, lddy, _dy = _operand(dy, "dy", T, N, (T, N, K), st)
+    px, ldx, _x = _operand(x, "x", T, K, (T, N, K), st)
+    _check(lib.loco_linear_backward_weight(c, pdy, lddy, px, ldx, pc, ps, pg, pb, T, N, K, pdw, lddw, pdb, pw, nw, st))
 
 
 def loco_linear_timeouts() -> int:

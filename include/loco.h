@@ -389,6 +389,19 @@ LOCO_API loco_status loco_norm_backward(const loco_norm_config* cfg, const void*
                                void* dbeta, void* workspace, int64_t ws_bytes, loco_stream_t stream);
 
 /*
+ * loco_linear_align — copies a bf16 matrix src [rows, cols] to rows that start
+ * on 16-byte boundaries: dst 16-byte aligned, ldd a multiple of 8.  The columns
+ * from cols to the next multiple of 8 are written as zeros (dst holds them in
+ * its last row too).  The entry points below take operands with any pitch, but
+ * the tensor memory accelerator only reads aligned rows: in large
+ * products a copy costs less than reading operands as they lie (T = 4095, N =
+ * 4097, K = 4099: 438 us as they lie, 136 us with both copied).  rows == 0 or
+ * cols == 0 is an empty call.
+ */
+LOCO_API loco_status loco_linear_align(const void* src, int64_t lds, int64_t rows, int64_t cols, void* dst,
+                                       int64_t ldd, loco_stream_t stream);
+
+/*
  * loco_linear_forward — z = x w^T + bias ;  y = act(z) + residual.
  * x [T, K] and w [N, K] bf16, products exact and accumulated in fp32; bias [N]
  * of param_dtype or NULL; residual [T, N] and y [T, N] of out_dtype, residual

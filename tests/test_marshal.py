@@ -54,12 +54,14 @@ def test_same_functions():
                                        None, None, 0),
     lambda c, s: marshal.norm_backward(0, 1e-5, t(4, 64), None, t(4), t(4, 64), t(4, 64), t(4), None, None, None, None,
                                        None, t(64), 0),
-    lambda c, s: marshal.linear_forward(t(4, 32), t(64, 32, d=B), t(4, 64), 0, None, None, None, None, 0),
-    lambda c, s: marshal.linear_forward(t(4, 32, d=B), t(64, 32, d=B), t(4, 64), 0, None, t(4, 64, d=B), None, None, 0),
-    lambda c, s: marshal.linear_backward_input(t(4, 32, d=B), t(31, 64, d=B), t(4, 64), 0, c, s, None, 0),
+    lambda c, s: marshal.linear_forward(t(4, 32), t(64, 32, d=B), t(4, 64), 0, None, None, None, None, 0, None),
+    lambda c, s: marshal.linear_forward(t(4, 32, d=B), t(64, 32, d=B), t(4, 64), 0, None, t(4, 64, d=B), None, None, 0,
+                                        None),
+    lambda c, s: marshal.linear_backward_input(t(4, 32, d=B), t(31, 64, d=B), t(4, 64), 0, c, s, None, 0, None),
     lambda c, s: marshal.linear_backward_weight(t(4, 32, d=B), t(32, 64), t(4, 64), None, None, None, None, None, None,
-                                                0),
-    lambda c, s: marshal.linear_backward_weight(t(4, 32, d=B), t(32, 64), None, c, s, None, None, t(32, d=B), None, 0),
+                                                0, None),
+    lambda c, s: marshal.linear_backward_weight(t(4, 32, d=B), t(32, 64), None, c, s, None, None, t(32, d=B), None, 0,
+                                                None),
 ])
 def test_gives_up(call):
     L._dtypes()
