@@ -297,11 +297,20 @@ struct Elem<true> {
 __device__ __forceinline__ float elem_value(float v) { return v; }
 __device__ __forceinline__ float elem_value(uint16_t v) { return bf16_bits_to_f32(v); }
 
+// A row's columns as they lie in memory, so that a row ahead takes few registers and no conversions.
+// RW: the kernel may write this row later.
 template <int G, int NE, bool BF16, bool RW>
-__device__ __forceinline__ void load_cols(const char* row, int cols, int t, float (&v)[NE]) {
+__device__ __forceinline__ void fetch_cols(const char* row, int cols, int t, typename Elem<BF16>::type (&v)[NE]) {
   const typename Elem<BF16>::type* q = reinterpret_cast<const typename Elem<BF16>::type*>(row) + t;
 #pragma unroll
-  for (int j = 0; j < NE; ++j) v[j] = t < cols - G * j ? elem_value(RW ? q[G * j] : __ldg(q + G * j)) : 0.0f;
+  for (int j = 0; j < NE; ++j) v[j] = t < cols - G * j ? (RW ? q[G * j] : __ldg(q + G * j)) : typename Elem<BF16>::type(0);
+}
+template <int G, int NE, bool BF16>
+__device__ __forceinline__ void load_cols(const char* row, int cols, int t, float (&v)[NE]) {
+  typename Elem<BF16>::type raw[NE];
+  fetch_cols<G, NE, BF16, false>(row, cols, t, raw);
+#pragma unroll
+  for (int j = 0; j < NE; ++j) v[j] = elem_value(raw[j]);
 }
 template <int G, int NE>
 __device__ __forceinline__ void load_cols(const void* p, int cols, int t, int bf16, float none, float (&v)[NE]) {
@@ -309,9 +318,9 @@ __device__ __forceinline__ void load_cols(const void* p, int cols, int t, int bf
 #pragma unroll
     for (int j = 0; j < NE; ++j) v[j] = none;
   } else if (bf16) {
-    load_cols<G, NE, true, false>(static_cast<const char*>(p), cols, t, v);
+    load_cols<G, NE, true>(static_cast<const char*>(p), cols, t, v);
   } else {
-    load_cols<G, NE, false, false>(static_cast<const char*>(p), cols, t, v);
+    load_cols<G, NE, false>(static_cast<const char*>(p), cols, t, v);
   }
 }
 template <int G, int NE>
@@ -330,22 +339,27 @@ __device__ __forceinline__ void store_cols(char* row, int cols, int t, int bf16,
 }
 
 template <int G, int NE, bool XBF16>
-__global__ void __launch_bounds__(kCtaThreads<G>, 768 / kCtaThreads<G>) k_norm_fwd_narrow(NormFwdArgs a) {
+__global__ void __launch_bounds__(kCtaThreads<G>, (G == 512 ? 1024 : 768) / kCtaThreads<G>) k_norm_fwd_narrow(NormFwdArgs a) {
   __shared__ float red[2][32];
   constexpr int kGroups = kCtaThreads<G> / G;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const int64_t step = int64_t(gridDim.x) * kGroups;
   int turn = 0;
-  for (int64_t row = int64_t(blockIdx.x) * kGroups + grp; row - grp < a.rows; row += step) {
+  typename Elem<XBF16>::type next[NE];
+  const auto fetch = [&](int64_t row) {
+    fetch_cols<G, NE, XBF16, false>(at(a.x, row * a.ldx, XBF16), row < a.rows ? cols : 0, t, next);
+  };
+  const int64_t first = int64_t(blockIdx.x) * kGroups + grp;
+  constexpr bool kAhead = NE <= 8;  // more columns a thread leave no registers for a row ahead
+  if (kAhead) fetch(first);
+  for (int64_t row = first; row - grp < a.rows; row += step) {
     const bool live = row < a.rows;
     float x[NE];
-    if (live) {
-      load_cols<G, NE, XBF16, false>(at(a.x, row * a.ldx, XBF16), cols, t, x);
-    } else {
+    if (!kAhead) fetch(row);
 #pragma unroll
-      for (int j = 0; j < NE; ++j) x[j] = 0.0f;
-    }
+    for (int j = 0; j < NE; ++j) x[j] = elem_value(next[j]);
+    if (kAhead) fetch(row + step);
     float mean = 0.0f;
     if (!a.rms) {
       float s[1] = {0.0f}, s1 = 0.0f;
@@ -633,36 +647,55 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
   });
 }
 
-template <int G, int NE, bool XBF16, bool CKPT>
-__global__ void __launch_bounds__(kCtaThreads<G>, (G >= 512 ? 1024 : 512) / kCtaThreads<G>) k_norm_bwd_narrow(NormBwdArgs a) {
+template <int G, int NE, bool XBF16, bool YBF16, bool CKPT>
+__global__ void __launch_bounds__(kCtaThreads<G>, (G >= 1024 ? 1024 : 512) / kCtaThreads<G>) k_norm_bwd_narrow(NormBwdArgs a) {
   __shared__ float red[2][64];
   extern __shared__ float sums[];  // [2][cols] where a CTA holds several groups
   constexpr int kGroups = kCtaThreads<G> / G;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
   const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const int64_t step = int64_t(gridDim.x) * kGroups;
+  constexpr bool kAhead = G < 1024;  // 1024 threads leave no registers for a row ahead
   float dg[NE], db[NE];
 #pragma unroll
   for (int j = 0; j < NE; ++j) dg[j] = db[j] = 0.0f;
   int turn = 0;
-  for (int64_t row = int64_t(blockIdx.x) * kGroups + grp; row - grp < a.rows; row += step) {
+  typename Elem<YBF16>::type next_d[NE];
+  typename Elem<XBF16>::type next_x[NE];
+  uint32_t next_c[NE];  // a code and its scale
+  const auto fetch = [&](int64_t row) {
+    const int n = row < a.rows ? cols : 0;
+    fetch_cols<G, NE, YBF16, false>(at(a.dy, row * a.lddy, YBF16), n, t, next_d);
+    if constexpr (CKPT) {
+      const int8_t* c = a.codes + row * nb * kCkptBlock + t;
+      const uint8_t* sc = a.scales + row * nb + t / kCkptBlock;
+#pragma unroll
+      for (int j = 0; j < NE; ++j)
+        next_c[j] = t < n - G * j ? uint32_t(uint8_t(__ldg(c + G * j))) | uint32_t(__ldg(sc + G / kCkptBlock * j)) << 8 : 0u;
+    } else {
+      fetch_cols<G, NE, XBF16, false>(at(a.x, row * a.ldx, XBF16), n, t, next_x);
+    }
+  };
+  const int64_t first = int64_t(blockIdx.x) * kGroups + grp;
+  if (kAhead) fetch(first);
+  for (int64_t row = first; row - grp < a.rows; row += step) {
     const bool live = row < a.rows;
     float d[NE], xh[NE], s[2] = {0.0f, 0.0f}, rstd = 0.0f;
+    if (!kAhead) fetch(row);
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      d[j] = elem_value(next_d[j]);
+      xh[j] = CKPT ? float(int8_t(next_c[j])) * ckpt_step(next_c[j] >> 8) : elem_value(next_x[j]);
+    }
+    if (kAhead) fetch(row + step);
+    typename Elem<XBF16>::type r[kAhead ? NE : 1];
+    if constexpr (kAhead)
+      if (a.residual != nullptr)
+        fetch_cols<G, NE, XBF16, true>(at(a.residual, row * a.ldr, XBF16), live ? cols : 0, t, r);
     if (live) {
       rstd = __ldg(a.rstd + row);
-      if (a.y_bf16)
-        load_cols<G, NE, true, false>(at(a.dy, row * a.lddy, true), cols, t, d);
-      else
-        load_cols<G, NE, false, false>(at(a.dy, row * a.lddy, false), cols, t, d);
-      if constexpr (CKPT) {
-        const int8_t* c = a.codes + row * nb * kCkptBlock + t;
-        const uint8_t* sc = a.scales + row * nb + t / kCkptBlock;
-#pragma unroll
-        for (int j = 0; j < NE; ++j)
-          xh[j] = t < cols - G * j ? float(__ldg(c + G * j)) * ckpt_step(__ldg(sc + G / kCkptBlock * j)) : 0.0f;
-      } else {
+      if constexpr (!CKPT) {
         const float mean = a.rms ? 0.0f : __ldg(a.mean + row);
-        load_cols<G, NE, XBF16, false>(at(a.x, row * a.ldx, XBF16), cols, t, xh);
 #pragma unroll
         for (int j = 0; j < NE; ++j) xh[j] = t < cols - G * j ? (xh[j] - mean) * rstd : 0.0f;
       }
@@ -682,10 +715,16 @@ __global__ void __launch_bounds__(kCtaThreads<G>, (G >= 512 ? 1024 : 512) / kCta
     if (!live) continue;  // whole warps
     const float c1 = a.rms ? 0.0f : s[0] / float(cols), c2 = s[1] / float(cols);
     if (a.residual != nullptr) {
-      float r[NE];
-      load_cols<G, NE, XBF16, true>(at(a.residual, row * a.ldr, XBF16), cols, t, r);
 #pragma unroll
-      for (int j = 0; j < NE; ++j) d[j] = fmaf(rstd, fmaf(-xh[j], c2, d[j] - c1), r[j]);
+      for (int j = 0; j < NE; ++j) {
+        float v = 0.0f;
+        if constexpr (kAhead) {
+          v = elem_value(r[j]);
+        } else if (t < cols - G * j) {
+          v = load_elem_rw(at(a.residual, row * a.ldr, XBF16), t + G * j, XBF16);
+        }
+        d[j] = fmaf(rstd, fmaf(-xh[j], c2, d[j] - c1), v);
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < NE; ++j) d[j] = rstd * fmaf(-xh[j], c2, d[j] - c1);
@@ -818,7 +857,7 @@ cudaError_t bwd_launch(const NormBwdArgs& a, bool wide, bool pwide, int* parts, 
   static LayerGrid cache[3];  // wide: occupancy depends on whether a stage holds a residual
   constexpr int H = NV == 1 ? G : 2 * G, NE = NV == 1 ? 8 : NV * 4;
   const auto wide_kernel = k_norm_bwd<G, NV, XBF16, YBF16, CKPT>;
-  const auto narrow_kernel = k_norm_bwd_narrow<H, NE, XBF16, CKPT>;
+  const auto narrow_kernel = k_norm_bwd_narrow<H, NE, XBF16, YBF16, CKPT>;
   const int T = wide ? kCtaThreads<G> : kCtaThreads<H>, groups = T / (wide ? G : H);
   const auto bytes = [](bool residual) {
     constexpr int kX = XBF16 ? 16 : 32, kY = YBF16 ? 16 : 32;
