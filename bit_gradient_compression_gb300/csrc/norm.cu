@@ -15,16 +15,23 @@
 // so the next rows have to be on their way meanwhile: WIDE threads copy their
 // own 16-byte pieces of the next kStages - 1 rows into shared memory (cp.async;
 // nobody else reads them, so no barrier is needed), the others load the next
-// row into registers.
+// row into registers where they have them to spare.
 //
 // In the backward pass each thread keeps the sums of dgamma and dbeta of its own
 // columns in registers over all its rows, one partial row per CTA goes to the
 // workspace, and a second kernel adds the partial rows in order: no atomics, the
 // same result every run.
+//
+// 16384 x 4096 bf16: forward 55 us (4.9 TB/s; 73 us with the checkpoint), bound by
+// the two barriers a row with one row's work per CTA between them; backward 102 us
+// (3.9 TB/s), with a residual 112 us, from a checkpoint 102 us, bound by
+// instructions (20 an element) at two CTAs a SM, which its registers allow.
+// Rows that take no 16-byte loads, 16384 x 2047: forward 53 us, backward 87 us.
 #include <atomic>
 
 #include "device_common.cuh"
 #include "layers_common.cuh"
+#include "tensor_core.cuh"
 
 namespace loco {
 
@@ -461,14 +468,40 @@ __global__ void __launch_bounds__(kLoop) k_norm_fwd_long(NormFwdArgs a) {
 
 // ---------------------------------------------------------------------------------------- backward
 
+// Rows of more columns than the registers of a CTA hold the sums of go to a cluster of two CTAs, 8192
+// columns to the first and the rest to the second (16-byte boundaries and whole blocks of a checkpoint).
+// Each sees its columns as a matrix of its own; the sums of a row are exchanged.  4096 x 16384 bf16 takes
+// 152 us so, against 718 us in three passes over memory (the sums, dx, the columns' sums).
+constexpr int kHalf = 8192;
+__device__ __forceinline__ void own_half(NormBwdArgs& a, bool xbf16, int rank) {
+  const int64_t c = int64_t(rank) * kHalf;
+  const auto shift = [&](const void* p, int bf16) { return p == nullptr ? p : at(p, c, bf16); };
+  a.dy = shift(a.dy, a.y_bf16);
+  a.x = shift(a.x, xbf16);
+  a.gamma = shift(a.gamma, a.param_bf16);
+  a.residual = shift(a.residual, xbf16);
+  a.dx = const_cast<void*>(shift(a.dx, xbf16));
+  if (a.codes != nullptr) a.codes += c, a.scales += c / kCkptBlock;
+  if (a.partials != nullptr) a.partials += c;
+}
+// The sums of both CTAs, in their order; consecutive calls alternate between two places.
+__device__ __forceinline__ void cluster_sum(float (&s)[2], float (*place)[2], int turn) {
+  if (threadIdx.x == 0) place[turn][0] = s[0], place[turn][1] = s[1];
+  cluster_sync();
+  const uint32_t p = smem_u32(place[turn]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    s[i] = cluster_load(cluster_addr(p + 4 * i, 0)) + cluster_load(cluster_addr(p + 4 * i, 1));
+}
+
 // Partial sums of a CTA's rows to the workspace.  `mine(c, i)` gives a thread's sum i (0 dgamma, 1
 // dbeta) of its columns through `each`; where a CTA holds several groups they add up one after another
 // in shared memory first.
 template <int G, typename Each>
-__device__ __forceinline__ void write_partials(const NormBwdArgs& a, float* sum, Each each) {
+__device__ __forceinline__ void write_partials(const NormBwdArgs& a, int64_t part, float* sum, Each each) {
   constexpr int T = kCtaThreads<G>, kGroups = T / G;
   const int cols = int(a.cols), grp = threadIdx.x / G;
-  float* out = a.partials + int64_t(blockIdx.x) * 2 * cols;
+  float* out = a.partials + part * 2 * cols;
   if constexpr (kGroups == 1) {
     each([&](int c, float dg, float db) { out[c] = dg, out[cols + c] = db; });
   } else {
@@ -490,17 +523,21 @@ __device__ __forceinline__ void write_partials(const NormBwdArgs& a, float* sum,
 template <int G, bool XBF16, bool YBF16>
 constexpr int kBwdStages = G == 512 && !(XBF16 && YBF16) ? 2 : 3;
 
-template <int G, int NV, bool XBF16, bool YBF16, bool CKPT>
+template <int G, int NV, bool XBF16, bool YBF16, bool CKPT, bool PAIR = false>
 __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (NV == 1 ? 768 : 512) / kCtaThreads<G>)
     k_norm_bwd(NormBwdArgs a, bool pwide) {
   __shared__ float red[2][64];
+  __shared__ float halves_sum[2][2];
   extern __shared__ __align__(16) uint8_t ring[];  // the stages, and gamma; after the rows, [2][cols] sums
   constexpr int T = kCtaThreads<G>, kGroups = T / G, kStages = kBwdStages<G, XBF16, YBF16>;
   constexpr int kX = XBF16 ? 16 : 32, kY = YBF16 ? 16 : 32;
   constexpr uint32_t at_x = NV * T * kY, at_r = at_x + NV * T * (CKPT ? 16 : kX);
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
-  const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
-  const int64_t step = int64_t(gridDim.x) * kGroups, first = int64_t(blockIdx.x) * kGroups + grp;
+  const int nb = int((a.cols + kCkptBlock - 1) / kCkptBlock), rank = PAIR ? int(cluster_rank()) : 0;
+  const int cols = PAIR ? (rank ? int(a.cols) - kHalf : kHalf) : int(a.cols);  // this CTA's
+  const int64_t block = PAIR ? blockIdx.x / 2 : blockIdx.x, blocks = PAIR ? gridDim.x / 2 : gridDim.x;
+  const int64_t step = blocks * kGroups, first = block * kGroups + grp;
+  if constexpr (PAIR) own_half(a, XBF16, rank);
   const bool with_r = a.residual != nullptr;
   const uint32_t stage_bytes = at_r + (with_r ? NV * T * kX : 0);
   const uint32_t base = smem_addr(ring) + threadIdx.x * 16, end = base + kStages * stage_bytes;
@@ -522,7 +559,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
 #pragma unroll
     for (int k = 0; k < 4; ++k) dg[e][k] = db[e][k] = pair(0.0f, 0.0f);
   }
-  const float inv_cols = 1.0f / float(cols);
+  const float inv_cols = 1.0f / float(int(a.cols));
   // the thread's place in a row of each matrix
   const auto dy_at = [&](int64_t row) { return at(a.dy, row * a.lddy, YBF16) + t * kY; };
   const auto x_at = [&](int64_t row) { return at(a.x, row * a.ldx, XBF16) + t * kX; };
@@ -609,6 +646,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     }
     if (row + step < a.rows) load(row + step);
     group_sum<G>(s, red[turn]);
+    if constexpr (PAIR) cluster_sum(s, halves_sum, turn);
     turn ^= 1;
     if (live) {
       char* op = at(a.dx, row * a.lddx, XBF16) + t * kX;
@@ -632,9 +670,10 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     }
     if ((cur += stage_bytes) == end) cur = base;
   }
+  if constexpr (PAIR) cluster_sync();  // the other has read this one's last sums
   if (a.partials == nullptr) return;
   cp_async_wait<0>();
-  write_partials<G>(a, reinterpret_cast<float*>(ring), [&](auto put) {
+  write_partials<G>(a, block, reinterpret_cast<float*>(ring), [&](auto put) {
 #pragma unroll
     for (int e = 0; e < NV; ++e)
 #pragma unroll
@@ -647,14 +686,18 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
   });
 }
 
-template <int G, int NE, bool XBF16, bool YBF16, bool CKPT>
+template <int G, int NE, bool XBF16, bool YBF16, bool CKPT, bool PAIR = false>
 __global__ void __launch_bounds__(kCtaThreads<G>, (G >= 1024 ? 1024 : 512) / kCtaThreads<G>) k_norm_bwd_narrow(NormBwdArgs a) {
   __shared__ float red[2][64];
+  __shared__ float halves_sum[2][2];
   extern __shared__ float sums[];  // [2][cols] where a CTA holds several groups
   constexpr int kGroups = kCtaThreads<G> / G;
   const int t = threadIdx.x % G, grp = threadIdx.x / G;
-  const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
-  const int64_t step = int64_t(gridDim.x) * kGroups;
+  const int nb = int((a.cols + kCkptBlock - 1) / kCkptBlock), rank = PAIR ? int(cluster_rank()) : 0;
+  const int cols = PAIR ? (rank ? int(a.cols) - kHalf : kHalf) : int(a.cols);  // this CTA's
+  const int64_t block = PAIR ? blockIdx.x / 2 : blockIdx.x, blocks = PAIR ? gridDim.x / 2 : gridDim.x;
+  const int64_t step = blocks * kGroups;
+  if constexpr (PAIR) own_half(a, XBF16, rank);
   constexpr bool kAhead = G < 1024;  // 1024 threads leave no registers for a row ahead
   float dg[NE], db[NE];
 #pragma unroll
@@ -676,7 +719,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, (G >= 1024 ? 1024 : 512) / kCt
       fetch_cols<G, NE, XBF16, false>(at(a.x, row * a.ldx, XBF16), n, t, next_x);
     }
   };
-  const int64_t first = int64_t(blockIdx.x) * kGroups + grp;
+  const int64_t first = block * kGroups + grp;
   if (kAhead) fetch(first);
   for (int64_t row = first; row - grp < a.rows; row += step) {
     const bool live = row < a.rows;
@@ -711,9 +754,10 @@ __global__ void __launch_bounds__(kCtaThreads<G>, (G >= 1024 ? 1024 : 512) / kCt
       }
     }
     group_sum<G>(s, red[turn]);
+    if constexpr (PAIR) cluster_sum(s, halves_sum, turn);
     turn ^= 1;
     if (!live) continue;  // whole warps
-    const float c1 = a.rms ? 0.0f : s[0] / float(cols), c2 = s[1] / float(cols);
+    const float c1 = a.rms ? 0.0f : s[0] / float(int(a.cols)), c2 = s[1] / float(int(a.cols));
     if (a.residual != nullptr) {
 #pragma unroll
       for (int j = 0; j < NE; ++j) {
@@ -731,66 +775,137 @@ __global__ void __launch_bounds__(kCtaThreads<G>, (G >= 1024 ? 1024 : 512) / kCt
     }
     store_cols<G, NE>(at(a.dx, row * a.lddx, XBF16), cols, t, XBF16, d);
   }
+  if constexpr (PAIR) cluster_sync();  // the other has read this one's last sums
   if (a.partials == nullptr) return;
-  write_partials<G>(a, sums, [&](auto put) {
+  write_partials<G>(a, block, sums, [&](auto put) {
 #pragma unroll
     for (int j = 0; j < NE; ++j)
       if (t < cols - G * j) put(t + G * j, dg[j], db[j]);
   });
 }
 
-// One normalised value, for rows too long for registers.
+// Rows too long for registers: eight columns a thread at a time, the sums of a row in one kernel (which
+// the L2 cache serves its second pass), those of the columns in another.
+
+// Columns c to c + 7 of one row, 0 past its end: 16-byte loads, put together from two where they have to be.
+template <bool BF16>
+__device__ __forceinline__ void load_eight(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t row, int64_t c,
+                                           float v[8]) {
+  const char* lo = static_cast<const char*>(p);
+  if (c + 8 <= cols) {
+    load8_any<BF16>(at(p, row * ld + c, BF16), lo, at(p, (rows - 1) * ld + cols, BF16), v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? load_elem(p, row * ld + c + k, BF16) : 0.0f;
+  }
+}
+// dy and the normalised values of eight columns.
 template <bool XBF16>
-__device__ __forceinline__ float xhat_at(const NormBwdArgs& a, int64_t row, int64_t c, int64_t nb, float mean, float rstd) {
-  if (a.x != nullptr) return (load_elem(a.x, row * a.ldx + c, XBF16) - mean) * rstd;
-  return float(__ldg(a.codes + row * nb * kCkptBlock + c)) * ckpt_step(__ldg(a.scales + row * nb + c / kCkptBlock));
+__device__ __forceinline__ void long_values(const NormBwdArgs& a, int64_t row, int64_t c, int64_t nb, float mean, float rstd,
+                                            float (&d)[8], float (&xh)[8]) {
+  if (a.y_bf16)
+    load_eight<true>(a.dy, a.lddy, a.rows, a.cols, row, c, d);
+  else
+    load_eight<false>(a.dy, a.lddy, a.rows, a.cols, row, c, d);
+  if (a.x != nullptr) {
+    load_eight<XBF16>(a.x, a.ldx, a.rows, a.cols, row, c, xh);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) xh[k] = (xh[k] - mean) * rstd;
+  } else {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.codes + row * nb * kCkptBlock + c));
+    const float step = ckpt_step(__ldg(a.scales + row * nb + c / kCkptBlock));
+    ckpt_unpack4(w.x, step, xh);
+    ckpt_unpack4(w.y, step, xh + 4);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (c + k >= a.cols) xh[k] = 0.0f;  // (a bad block's padding reads back as NaN)
+}
+__device__ __forceinline__ void load_gamma(const NormBwdArgs& a, int64_t c, float (&g)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = a.gamma != nullptr && c + k < a.cols ? load_elem(a.gamma, c + k, a.param_bf16) : 1.0f;
 }
 
+// wide: rows of dx and of the residual start on 16-byte boundaries.
 template <bool XBF16>
-__global__ void __launch_bounds__(kLoop) k_norm_bwd_long(NormBwdArgs a) {
+__global__ void __launch_bounds__(kLoop, 1) k_norm_bwd_long(NormBwdArgs a, bool wide) {
   __shared__ float red[64];
   const int64_t row = blockIdx.x, cols = a.cols, nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const float rstd = a.rstd[row], mean = a.x == nullptr || a.rms ? 0.0f : a.mean[row];
   float s[2] = {0.0f, 0.0f};
-  for (int64_t c = threadIdx.x; c < cols; c += kLoop) {
-    const float g = load_elem(a.dy, row * a.lddy + c, a.y_bf16) *
-                    (a.gamma ? load_elem(a.gamma, c, a.param_bf16) : 1.0f);
-    s[0] += g;
-    s[1] = fmaf(g, xhat_at<XBF16>(a, row, c, nb, mean, rstd), s[1]);
+#pragma unroll 2
+  for (int64_t c = threadIdx.x * 8; c < cols; c += kLoop * 8) {
+    float d[8], xh[8], g[8];
+    long_values<XBF16>(a, row, c, nb, mean, rstd, d, xh);
+    load_gamma(a, c, g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      d[k] *= g[k];
+      s[0] += d[k];
+      s[1] = fmaf(d[k], xh[k], s[1]);
+    }
   }
   group_sum<kLoop>(s, red);
   const float c1 = a.rms ? 0.0f : s[0] / float(cols), c2 = s[1] / float(cols);
-  for (int64_t c = threadIdx.x; c < cols; c += kLoop) {
-    const float g = load_elem(a.dy, row * a.lddy + c, a.y_bf16) *
-                    (a.gamma ? load_elem(a.gamma, c, a.param_bf16) : 1.0f);
-    const float r = a.residual != nullptr ? load_elem_rw(a.residual, row * a.ldr + c, XBF16) : 0.0f;
-    store_elem(a.dx, row * a.lddx + c, XBF16,
-               fmaf(rstd, fmaf(-xhat_at<XBF16>(a, row, c, nb, mean, rstd), c2, g - c1), r));
+#pragma unroll 2
+  for (int64_t c = threadIdx.x * 8; c < cols; c += kLoop * 8) {
+    float d[8], xh[8], g[8];
+    long_values<XBF16>(a, row, c, nb, mean, rstd, d, xh);
+    load_gamma(a, c, g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) d[k] = rstd * fmaf(-xh[k], c2, d[k] * g[k] - c1);
+    const bool full = wide && c + 8 <= cols;
+    if (a.residual != nullptr) {
+      if (full) {
+        load8<true>(a.residual, row * a.ldr + c, XBF16, g);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = c + k < cols ? load_elem_rw(a.residual, row * a.ldr + c + k, XBF16) : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] += g[k];
+    }
+    if (full) {
+      store8(a.dx, row * a.lddx + c, XBF16, d);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < cols) store_elem(a.dx, row * a.lddx + c + k, XBF16, d[k]);
+    }
   }
 }
 
-// Column sums of a slice of rows, for the long rows: 32 columns per CTA, 8 rows at a time.
+// Column sums of a slice of rows: 256 columns per CTA, a warp every eighth row.
+constexpr int kColWarps = 8, kColStrip = 256;
 template <bool XBF16>
-__global__ void __launch_bounds__(256) k_norm_bwd_cols(NormBwdArgs a, int64_t rows_per) {
-  __shared__ float sm[2][8][32];
+__global__ void __launch_bounds__(kColWarps * 32) k_norm_bwd_cols(NormBwdArgs a, int64_t rows_per) {
+  __shared__ float sm[2][kColWarps][kColStrip];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int64_t c = int64_t(blockIdx.x) * 32 + lane, nb = (a.cols + kCkptBlock - 1) / kCkptBlock;
+  const int64_t c = int64_t(blockIdx.x) * kColStrip + lane * 8, nb = (a.cols + kCkptBlock - 1) / kCkptBlock;
   const int64_t lo = int64_t(blockIdx.y) * rows_per, hi = min(lo + rows_per, a.rows);
-  float dg = 0.0f, db = 0.0f;
-  if (c < a.cols)
-    for (int64_t row = lo + warp; row < hi; row += 8) {
-      const float d = load_elem(a.dy, row * a.lddy + c, a.y_bf16);
-      const float mean = a.x == nullptr || a.rms ? 0.0f : __ldg(a.mean + row);
-      dg = fmaf(d, xhat_at<XBF16>(a, row, c, nb, mean, __ldg(a.rstd + row)), dg);
-      db += d;
+  float dg[8], db[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) dg[k] = db[k] = 0.0f;
+  if (c < a.cols) {
+#pragma unroll 2
+    for (int64_t row = lo + warp; row < hi; row += kColWarps) {
+      float d[8], xh[8];
+      long_values<XBF16>(a, row, c, nb, a.x == nullptr || a.rms ? 0.0f : __ldg(a.mean + row), __ldg(a.rstd + row), d, xh);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dg[k] = fmaf(d[k], xh[k], dg[k]), db[k] += d[k];
     }
-  sm[0][warp][lane] = dg, sm[1][warp][lane] = db;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sm[0][warp][k * 32 + lane] = dg[k], sm[1][warp][k * 32 + lane] = db[k];
   __syncthreads();
-  if (warp < 2 && c < a.cols) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t col = int64_t(blockIdx.x) * kColStrip + lane * 8 + warp;
+    if (col >= a.cols) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += sm[warp][w][lane];
-    a.partials[(int64_t(blockIdx.y) * 2 + warp) * a.cols + c] = v;
+    for (int w = 0; w < kColWarps; ++w) v += sm[i][w][threadIdx.x];
+    a.partials[(int64_t(blockIdx.y) * 2 + i) * a.cols + col] = v;
   }
 }
 
@@ -823,6 +938,35 @@ bool wide_rows(const void* p, int64_t ld, int64_t rows, int bf16) {
 }
 bool wide_vec(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+void pair_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int pairs, int threads, size_t smem, cudaStream_t s) {
+  cfg->gridDim = dim3(unsigned(pairs) * 2);
+  cfg->blockDim = dim3(unsigned(threads));
+  cfg->dynamicSmemBytes = smem;
+  cfg->stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+// Clusters of two CTAs that the current device holds at once, at most kNormPartials.  (The kernel's limit
+// of shared memory has been set by layer_grid.)
+template <typename Kernel>
+cudaError_t pair_slots(LayerGrid& cache, Kernel kernel, int threads, size_t smem, int* slots) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < LayerGrid::kDevices && (*slots = cache.cap[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  pair_config(&cfg, attr, kNormPartials, threads, smem, nullptr);
+  if ((e = cudaOccupancyMaxActiveClusters(slots, kernel, &cfg)) != cudaSuccess) return e;
+  if (*slots < 1) return cudaErrorInvalidConfiguration;
+  if (*slots > kNormPartials) *slots = kNormPartials;
+  if (dev < LayerGrid::kDevices) cache.cap[dev].store(*slots, std::memory_order_release);
+  return cudaSuccess;
+}
+
 // Narrow kernels hold half as many columns a thread, in groups of twice the threads.
 template <int G, int NV, bool XBF16, bool YBF16>
 cudaError_t fwd_launch(const NormFwdArgs& a, bool wide, bool pwide, cudaStream_t s) {
@@ -852,12 +996,20 @@ cudaError_t fwd(const NormFwdArgs& a, bool wide, bool pwide, cudaStream_t s) {
   return a.y_bf16 ? fwd_launch<G, NV, false, true>(a, wide, pwide, s) : fwd_launch<G, NV, false, false>(a, wide, pwide, s);
 }
 
-template <int G, int NV, bool XBF16, bool YBF16, bool CKPT>
+template <typename Kernel, typename... Args>
+cudaError_t launch_pairs(Kernel kernel, int pairs, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  pair_config(&cfg, attr, pairs, threads, smem, s);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int G, int NV, bool PAIR, bool XBF16, bool YBF16, bool CKPT>
 cudaError_t bwd_launch(const NormBwdArgs& a, bool wide, bool pwide, int* parts, cudaStream_t s) {
   static LayerGrid cache[3];  // wide: occupancy depends on whether a stage holds a residual
   constexpr int H = NV == 1 ? G : 2 * G, NE = NV == 1 ? 8 : NV * 4;
-  const auto wide_kernel = k_norm_bwd<G, NV, XBF16, YBF16, CKPT>;
-  const auto narrow_kernel = k_norm_bwd_narrow<H, NE, XBF16, YBF16, CKPT>;
+  const auto wide_kernel = k_norm_bwd<G, NV, XBF16, YBF16, CKPT, PAIR>;
+  const auto narrow_kernel = k_norm_bwd_narrow<H, NE, XBF16, YBF16, CKPT, PAIR>;
   const int T = wide ? kCtaThreads<G> : kCtaThreads<H>, groups = T / (wide ? G : H);
   const auto bytes = [](bool residual) {
     constexpr int kX = XBF16 ? 16 : 32, kY = YBF16 ? 16 : 32;
@@ -871,6 +1023,14 @@ cudaError_t bwd_launch(const NormBwdArgs& a, bool wide, bool pwide, int* parts, 
                                           bytes(true), &cap)
                              : layer_grid(cache[2], reinterpret_cast<const void*>(narrow_kernel), T, sm, sm, &cap);
   if (e != cudaSuccess) return e;
+  if constexpr (PAIR) {
+    static LayerGrid pairs[3];
+    const cudaError_t f = wide ? pair_slots(pairs[a.residual != nullptr], wide_kernel, T, sm, &cap)
+                               : pair_slots(pairs[2], narrow_kernel, T, sm, &cap);
+    if (f != cudaSuccess) return f;
+    *parts = int(a.rows < cap ? a.rows : cap);
+    return wide ? launch_pairs(wide_kernel, *parts, T, sm, s, a, pwide) : launch_pairs(narrow_kernel, *parts, T, sm, s, a);
+  }
   if (cap > kNormPartials) cap = kNormPartials;
   const int64_t want = (a.rows + groups - 1) / groups;
   *parts = int(want < cap ? want : cap);
@@ -881,18 +1041,18 @@ cudaError_t bwd_launch(const NormBwdArgs& a, bool wide, bool pwide, int* parts, 
   return cudaGetLastError();
 }
 
-template <int G, int NV, bool XBF16>
+template <int G, int NV, bool PAIR, bool XBF16>
 cudaError_t bwd_y(const NormBwdArgs& a, bool wide, bool pwide, int* parts, cudaStream_t s) {
   const bool ck = a.x == nullptr;
   if (a.y_bf16)
-    return ck ? bwd_launch<G, NV, XBF16, true, true>(a, wide, pwide, parts, s)
-              : bwd_launch<G, NV, XBF16, true, false>(a, wide, pwide, parts, s);
-  return ck ? bwd_launch<G, NV, XBF16, false, true>(a, wide, pwide, parts, s)
-            : bwd_launch<G, NV, XBF16, false, false>(a, wide, pwide, parts, s);
+    return ck ? bwd_launch<G, NV, PAIR, XBF16, true, true>(a, wide, pwide, parts, s)
+              : bwd_launch<G, NV, PAIR, XBF16, true, false>(a, wide, pwide, parts, s);
+  return ck ? bwd_launch<G, NV, PAIR, XBF16, false, true>(a, wide, pwide, parts, s)
+            : bwd_launch<G, NV, PAIR, XBF16, false, false>(a, wide, pwide, parts, s);
 }
-template <int G, int NV>
+template <int G, int NV, bool PAIR = false>
 cudaError_t bwd(const NormBwdArgs& a, bool wide, bool pwide, int* parts, cudaStream_t s) {
-  return a.x_bf16 ? bwd_y<G, NV, true>(a, wide, pwide, parts, s) : bwd_y<G, NV, false>(a, wide, pwide, parts, s);
+  return a.x_bf16 ? bwd_y<G, NV, PAIR, true>(a, wide, pwide, parts, s) : bwd_y<G, NV, PAIR, false>(a, wide, pwide, parts, s);
 }
 
 }  // namespace
@@ -926,19 +1086,22 @@ cudaError_t launch_norm_backward(const NormBwdArgs& a, cudaStream_t s) {
     else if (pitch <= 1024) e = bwd<128, 1>(a, wide, pwide, &parts, s);
     else if (pitch <= 2048) e = bwd<256, 1>(a, wide, pwide, &parts, s);
     else if (pitch <= 4096) e = bwd<256, 2>(a, wide, pwide, &parts, s);
-    else if (pitch <= 8192) e = bwd<512, 2>(a, wide, pwide, &parts, s);
+    else if (pitch <= kHalf) e = bwd<512, 2>(a, wide, pwide, &parts, s);
+    else if (pitch <= 2 * kHalf) e = bwd<512, 2, true>(a, wide, pwide, &parts, s);
     else {
       if (a.partials != nullptr) {
         // before dx, which may overwrite a residual but none of these inputs
-        const int64_t strips = (a.cols + 31) / 32;
+        const int64_t strips = (a.cols + kColStrip - 1) / kColStrip;
         const int64_t want = (a.rows + 63) / 64;
         parts = int(want < 64 ? want : 64);
         const int64_t per = (a.rows + parts - 1) / parts;
         const dim3 grid{unsigned(strips), unsigned(parts)};
-        (a.x_bf16 ? k_norm_bwd_cols<true> : k_norm_bwd_cols<false>)<<<grid, 256, 0, s>>>(a, per);
+        (a.x_bf16 ? k_norm_bwd_cols<true> : k_norm_bwd_cols<false>)<<<grid, kColWarps * 32, 0, s>>>(a, per);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
       }
-      (a.x_bf16 ? k_norm_bwd_long<true> : k_norm_bwd_long<false>)<<<unsigned(a.rows), kLoop, 0, s>>>(a);
+      const bool out_wide = wide_rows(a.dx, a.lddx, a.rows, a.x_bf16) &&
+                            (a.residual == nullptr || wide_rows(a.residual, a.ldr, a.rows, a.x_bf16));
+      (a.x_bf16 ? k_norm_bwd_long<true> : k_norm_bwd_long<false>)<<<unsigned(a.rows), kLoop, 0, s>>>(a, out_wide);
       e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
