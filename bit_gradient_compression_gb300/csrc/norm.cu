@@ -430,8 +430,7 @@ constexpr int kLoop = 512;
 template <bool XBF16>
 __global__ void __launch_bounds__(kLoop) k_norm_fwd_long(NormFwdArgs a) {
   __shared__ float red[2][32];
-  const int64_t row = blockIdx.x;
-  const int cols = int(a.cols), nb = (cols + kCkptBlock - 1) / kCkptBlock;
+  const int64_t row = blockIdx.x, cols = a.cols, nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const char* xr = at(a.x, row * a.ldx, XBF16);
   float mean = 0.0f;
   if (!a.rms) {
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(kLoop) k_norm_fwd_long(NormFwdArgs a) {
     if (a.rstd != nullptr) a.rstd[row] = rstd;
   }
   char* yr = at(a.y, row * a.ldy, a.y_bf16);
-  const int64_t pitch = int64_t(nb) * kCkptBlock;  // a multiple of 32: whole warps enter and leave together
+  const int64_t pitch = nb * kCkptBlock;  // a multiple of 32: whole warps enter and leave together
   for (int64_t c = threadIdx.x; c < pitch; c += kLoop) {
     const float v = c < cols ? (load_elem(xr, c, XBF16) - mean) * rstd : 0.0f;
     if (a.codes != nullptr) {
