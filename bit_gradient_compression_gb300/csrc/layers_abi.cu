@@ -373,7 +373,7 @@ loco_status loco_linear_backward_weight(const loco_linear_config* cfg, const voi
   LOCO_TRY(check_linear(cfg, T, N, K));
   if (N == 0 || (K == 0 && db == nullptr)) return done();
   const size_t oe = elem_size(cfg->out_dtype), pe = elem_size(cfg->param_dtype);
-  const bool from_ckpt = x == nullptr;
+  const bool from_ckpt = x == nullptr && T > 0;  // (an empty x may be NULL; without rows nothing but zeros is written)
   const bool shift = from_ckpt && beta != nullptr && K > 0;
   const int64_t need = shift ? loco_linear_workspace_bytes(N) : 0;
   if (need > 0 && workspace == nullptr) return fail(LOCO_ERR_INVALID_ARG, "workspace is NULL");

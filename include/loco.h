@@ -437,7 +437,8 @@ LOCO_API int64_t loco_linear_workspace_bytes(int64_t N);
  *   dw_nk = gamma_k * (sum_t dy_tn v_tk) + beta_k * db_n.
  * dw [N, K] and db [N] of out_dtype; db may be NULL.  cfg->act is not read.
  * workspace (ws_bytes >= loco_linear_workspace_bytes(N)) may be NULL without
- * beta.  T == 0 writes zeros.
+ * beta, and with x.  T == 0 writes zeros, whatever x, gamma and beta are; it
+ * reads none of them and needs no workspace.
  */
 LOCO_API loco_status loco_linear_backward_weight(const loco_linear_config* cfg, const void* dy, int64_t lddy,
                                         const void* x, int64_t ldx, const int8_t* codes, const uint8_t* scales,
