@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
     copy_next(row + (kStages - 1) * step, (cur == base ? end : cur) - stage_bytes);
     cp_async_wait<kStages - 1>();
     const float rstd = next_rstd;
-    const Pair r2 = pair(rstd, rstd), m2 = pair(-next_mean * rstd, -next_mean * rstd);
+    const Pair r2 = pair(rstd, rstd), less = pair(-next_mean, -next_mean);
     uint32_t scale[NV];
     if constexpr (CKPT) {
 #pragma unroll
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kCtaThreads<G>, G == 512 ? 1 : G < 128 ? 5 : (
       } else {
         copied<G, NV, XBF16>(cur + at_x, e, [&] { return x_at(row); }, full[e], left, xh);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) xh[k] = fma(xh[k], r2, m2);
+        for (int k = 0; k < 4; ++k) xh[k] = (xh[k] + less) * r2;  // nearly exact; x r - m r rounds m r, for the whole row alike
       }
       if (!full[e]) clear_past(xh, left);  // (a bad block's padding reads back as NaN)
       const uint4 lo = shared16(gamma + 2 * e * T * 16), hi = shared16(gamma + (2 * e + 1) * T * 16);
