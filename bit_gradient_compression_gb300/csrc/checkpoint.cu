@@ -7,7 +7,7 @@
 // start on no 16-byte boundary are read and written in aligned pieces all the
 // same, shifted together from two of them.
 // 16384 x 11008 bf16: encode 89 us (6.1 TB/s, 90 % of a copy's rate), decode 96 us
-// (5.7), through SiLU 97 us, through GELU 132 us (bound by the erf's arithmetic);
+// (5.7), through SiLU 97 us, through GELU 150 us (bound by the distribution function's arithmetic);
 // fp32 encode 135 us (6.7).  16384 x 4095 bf16: encode 85 us, decode 58 us.
 #include <atomic>
 

@@ -284,7 +284,12 @@ LOCO_API loco_status loco_shard_range(int64_t n, int32_t block, int32_t W, int32
  * out of range is LOCO_ERR_INVALID_ARG, an unknown dtype, activation or kind
  * LOCO_ERR_UNSUPPORTED, a misaligned pointer LOCO_ERR_MISALIGNED.
  * Arithmetic is binary32 (sums, statistics and accumulators included); an
- * output is rounded once, to its own type.  NaN and infinities propagate as
+ * output is rounded once, to its own type.  Activations use the hardware's 2^x
+ * and 1/x: with u = 2^-24 their relative error is at most (10 + 1.5 |v|) u for
+ * SiLU, (26 + 1.13 v^2) u for GELU and (10 + 6 |g|) u for its tanh form, g = 2
+ * sqrt(2/pi) (v + 0.044715 v^3), in the lower tails too; a slope's is at most
+ * twice that, relative to the sum of its two terms' magnitudes.  An activation
+ * or slope below 2^-100 in magnitude may come out as 0.  NaN and infinities propagate as
  * the formulas have it: an output that reads none is not touched by them.
  * Results do not change from run to run.
  * ========================================================================== */
