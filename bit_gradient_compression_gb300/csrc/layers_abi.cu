@@ -285,6 +285,19 @@ loco_status loco_norm_backward(const loco_norm_config* cfg, const void* dy, int6
   return launch_result(launch_norm_backward(a, reinterpret_cast<cudaStream_t>(stream)), "loco_norm_backward");
 }
 
+int32_t loco_matrices_overlap(const void* a, int64_t lda, int64_t rows_a, int64_t cols_a, int32_t bytes_a, const void* b,
+                              int64_t ldb, int64_t rows_b, int64_t cols_b, int32_t bytes_b) {
+  if (a == nullptr || b == nullptr || rows_a < 1 || cols_a < 1 || rows_b < 1 || cols_b < 1) return 0;
+  const Mat x{a, rows_a, cols_a, rows_a == 1 ? cols_a : lda, size_t(bytes_a), 1, ""};
+  const Mat y{b, rows_b, cols_b, rows_b == 1 ? cols_b : ldb, size_t(bytes_b), 1, ""};
+  for (const Mat* m : {&x, &y}) {
+    // what no entry point takes: not known to lie apart
+    if (m->elem < 1 || m->elem > 16 || m->cols > LOCO_MAX_N || m->ld < m->cols) return 1;
+    if (m->rows > 1 && (m->rows > kMaxDim || m->ld > kMaxDim)) return 1;
+  }
+  return mats_overlap(x, y);
+}
+
 loco_status loco_linear_align(const void* src, int64_t lds, int64_t rows, int64_t cols, void* dst, int64_t ldd,
                               loco_stream_t stream) {
   LOCO_TRY(check_dim(rows, 0, "rows"));

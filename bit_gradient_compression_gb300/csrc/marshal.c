@@ -120,20 +120,34 @@ static int bytes_of(PyObject* t, void** p, int64_t* n) {
   return d == t_u8 && (stride == 1 || *n <= 1) && address(t, p);
 }
 
+/* An output of a product: a matrix of elements of so many bytes, a contiguous one as one row of bytes. */
+typedef struct {
+  const void* p;
+  int64_t ld, rows, cols;
+  int elem;
+} Out;
+static int size_of(int dtype) { return dtype == LOCO_BF16 ? 2 : 4; }
+static Out out_mat(const Mat* m) { return (Out){m->p, m->ld, m->rows, m->cols, size_of(m->dtype)}; }
+static Out out_row(const void* p, int64_t bytes) { return (Out){p, bytes, 1, bytes, 1}; }
+
 /*
  * Copies the operands of a product over t rows to aligned rows where that pays (loco.py says when; least: the
  * fewest rows), in one piece of memory of alloc(bytes), which the caller releases after its call; without
- * alloc it gives up.
+ * alloc it gives up.  Operands stay as they lie where an output overlaps one: the call then refuses them.
  * Returns 1, or 0 to give up, or -1 for a failed copy with its status in *status.
  */
-static int align(Mat* x, Mat* w, int64_t t, int64_t n, int64_t k, int64_t least, PyObject* alloc,
-                 loco_stream_t st, PyObject** held, int* status) {
+static int align(Mat* x, Mat* w, int64_t t, int64_t n, int64_t k, int64_t least, const Out* outs, int n_outs,
+                 PyObject* alloc, loco_stream_t st, PyObject** held, int* status) {
   Mat* m[2] = {x, w};
   int64_t at[2] = {0, 0}, bytes = 0;
   *held = NULL;
   if (t < least || (double)t * (double)n * (double)k < align_work) return 1;
   for (int i = 0; i < 2; ++i) {
     if (m[i]->p == NULL || ((uintptr_t)m[i]->p % 16 == 0 && (m[i]->rows <= 1 || m[i]->ld % 8 == 0))) continue;
+    for (int o = 0; o < n_outs; ++o)
+      if (loco_matrices_overlap(m[i]->p, m[i]->ld, m[i]->rows, m[i]->cols, 2, outs[o].p, outs[o].ld, outs[o].rows,
+                                outs[o].cols, outs[o].elem))
+        return 1;
     at[i] = bytes;
     bytes += (m[i]->rows * ((m[i]->cols + 7) / 8 * 16) + 255) / 256 * 256;
     m[i]->dtype = -3; /* to be copied */
@@ -155,13 +169,16 @@ static int align(Mat* x, Mat* w, int64_t t, int64_t n, int64_t k, int64_t least,
   }
   return 1;
 }
-#define ALIGN(x, w, t, n, k, least, alloc)                              \
-  PyObject* held;                                                       \
-  int status;                                                           \
-  const int ready = align(x, w, t, n, k, least, alloc, st, &held, &status); \
-  if (ready < 1) {                                                      \
-    Py_XDECREF(held);                                                   \
-    return ready < 0 ? PyLong_FromLong(status) : give_up();             \
+/* The outputs follow alloc. */
+#define ALIGN(x, w, t, n, k, least, alloc, ...)                                                                     \
+  const Out outs[] = {__VA_ARGS__};                                                                                 \
+  PyObject* held;                                                                                                   \
+  int status;                                                                                                       \
+  const int ready =                                                                                                 \
+      align(x, w, t, n, k, least, outs, (int)(sizeof outs / sizeof outs[0]), alloc, st, &held, &status);            \
+  if (ready < 1) {                                                                                                  \
+    Py_XDECREF(held);                                                                                               \
+    return ready < 0 ? PyLong_FromLong(status) : give_up();                                                         \
   }
 #define CALL_ALIGNED(call)                       \
   Py_BEGIN_ALLOW_THREADS status = (call);        \
@@ -266,7 +283,8 @@ static PyObject* linear_forward(PyObject* self, PyObject* const* a, Py_ssize_t n
   const loco_linear_config cfg = {(int32_t)integer(a[3]), one(y.dtype, res.dtype), or_f32(pd)};
   const loco_stream_t st = STREAM(a[8]);
   WANT(cfg.out_dtype >= 0);
-  ALIGN(&x, &w, x.rows, w.rows, x.cols, align_rows, a[9]);
+  ALIGN(&x, &w, x.rows, w.rows, x.cols, align_rows, a[9], out_mat(&y), out_row(c, loco_ckpt_code_bytes(x.rows, w.rows)),
+        out_row(s, loco_ckpt_scale_bytes(x.rows, w.rows)));
   CALL_ALIGNED(loco_linear_forward(&cfg, x.p, x.ld, w.p, w.ld, b, res.p, res.ld, x.rows, w.rows, x.cols, y.p, y.ld, c, s,
                                    st));
 }
@@ -282,7 +300,7 @@ static PyObject* linear_backward_input(PyObject* self, PyObject* const* a, Py_ss
   const loco_linear_config cfg = {(int32_t)integer(a[3]), one(dx.dtype, res.dtype), LOCO_F32};
   const loco_stream_t st = STREAM(a[7]);
   WANT(cfg.out_dtype >= 0);
-  ALIGN(&dy, &w, dy.rows, dy.cols, w.cols, align_rows, a[8]);
+  ALIGN(&dy, &w, dy.rows, dy.cols, w.cols, align_rows, a[8], out_mat(&dx));
   CALL_ALIGNED(loco_linear_backward_input(&cfg, dy.p, dy.ld, w.p, w.ld, c, s, res.p, res.ld, dy.rows, dy.cols, w.cols,
                                           dx.p, dx.ld, st));
 }
@@ -302,7 +320,8 @@ static PyObject* linear_backward_weight(PyObject* self, PyObject* const* a, Py_s
   const loco_linear_config cfg = {LOCO_ACT_NONE, od, or_f32(pd)};
   const loco_stream_t st = STREAM(a[9]);
   WANT(1);
-  ALIGN(&dy, &x, dy.rows, dy.cols, dw.cols, 0, a[10]);
+  ALIGN(&dy, &x, dy.rows, dy.cols, dw.cols, 0, a[10], out_mat(&dw), out_row(db, dy.cols * size_of(od)),
+        out_row(w, x.p == NULL && b != NULL ? loco_linear_workspace_bytes(dy.cols) : 0));
   CALL_ALIGNED(loco_linear_backward_weight(&cfg, dy.p, dy.ld, x.p, x.ld, c, s, g, b, dy.rows, dy.cols, dw.cols, dw.p,
                                            dw.ld, db, w, nw, st));
 }

@@ -31,9 +31,8 @@ EXPORTS = ("loco_num_blocks", "loco_code_bytes", "loco_compress", "loco_compress
            "loco_adam_step", "loco_adam_step_bf16", "loco_sgd_step", "loco_shard_range", "loco_status_string",
            "loco_last_error", "loco_ckpt_code_bytes", "loco_ckpt_scale_bytes", "loco_ckpt_encode", "loco_ckpt_decode",
            "loco_norm_forward", "loco_norm_workspace_bytes", "loco_norm_backward", "loco_linear_align",
-           "loco_linear_forward",
-           "loco_linear_backward_input", "loco_linear_workspace_bytes", "loco_linear_backward_weight",
-           "loco_linear_timeouts")
+           "loco_matrices_overlap", "loco_linear_forward", "loco_linear_backward_input", "loco_linear_workspace_bytes",
+           "loco_linear_backward_weight", "loco_linear_timeouts")
 
 
 class LocoError(RuntimeError):
@@ -122,6 +121,8 @@ lib.loco_norm_backward.argtypes = [_norm, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _
 lib.loco_norm_backward.restype = ctypes.c_int
 lib.loco_linear_align.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp]
 lib.loco_linear_align.restype = ctypes.c_int
+lib.loco_matrices_overlap.argtypes = [_vp, _i64, _i64, _i64, _i32, _vp, _i64, _i64, _i64, _i32]
+lib.loco_matrices_overlap.restype = _i32
 lib.loco_linear_forward.argtypes = [_lin, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp,
                                     _vp]
 lib.loco_linear_forward.restype = ctypes.c_int
@@ -472,12 +473,25 @@ def _scratch(nbytes: int):
         return None
 
 
-def _operand(t, name: str, rows: int, cols: int, product, stream: int, least: int = 0):
-    """(address, row pitch, what keeps it) of an operand of a product of T, N, K, in aligned rows where that pays."""
+def loco_matrices_overlap(a: int, lda: int, rows_a: int, cols_a: int, bytes_a: int,
+                          b: int, ldb: int, rows_b: int, cols_b: int, bytes_b: int) -> bool:
+    """Whether two matrices, given by their addresses, row pitches, sizes and element sizes, may share a byte."""
+    return bool(lib.loco_matrices_overlap(a, lda, rows_a, cols_a, bytes_a, b, ldb, rows_b, cols_b, bytes_b))
+
+
+def _row(p: int, size: int):
+    """A contiguous output of `size` bytes as a matrix of one row."""
+    return p, size, 1, size, 1
+
+
+def _operand(t, name: str, rows: int, cols: int, product, stream: int, outputs, least: int = 0):
+    """(address, row pitch, what keeps it) of an operand of a product of T, N, K, in aligned rows where that pays.
+    One that an output overlaps (each as loco_matrices_overlap takes it) stays as it lies: the call then refuses it."""
     p, ld = _mat(t, name, rows, cols)
     T, N, K = product
     if (t is None or T < least or T * N * K < ALIGN_WORK or not t.is_cuda
-            or (p % 16 == 0 and (rows <= 1 or ld % 8 == 0))):
+            or (p % 16 == 0 and (rows <= 1 or ld % 8 == 0))
+            or any(loco_matrices_overlap(p, ld, rows, cols, 2, *o) for o in outputs)):
         return p, ld, None
     import torch
     pitch = -(-cols // 8) * 8
@@ -505,8 +519,9 @@ def loco_linear_forward(x, w, y, *, act: int = LOCO_ACT_NONE, bias=None, residua
     py, ldy = _mat(y, "y", T, N)
     pc, ps = _ckpt(codes, scales, T, N)
     c, pb = _linear_ref(act, _one_dtype("y and residual", y, residual), _one_dtype("bias", bias)), _vec(bias, "bias", N)
-    px, ldx, _x = _operand(x, "x", T, K, (T, N, K), st, ALIGN_ROWS)
-    pw, ldw, _w = _operand(w, "w", N, K, (T, N, K), st, ALIGN_ROWS)
+    outs = ((py, ldy, T, N, y.element_size()), _row(pc, loco_ckpt_code_bytes(T, N)), _row(ps, loco_ckpt_scale_bytes(T, N)))
+    px, ldx, _x = _operand(x, "x", T, K, (T, N, K), st, outs, ALIGN_ROWS)
+    pw, ldw, _w = _operand(w, "w", N, K, (T, N, K), st, outs, ALIGN_ROWS)
     _check(lib.loco_linear_forward(c, px, ldx, pw, ldw, pb, pr, ldr, T, N, K, py, ldy, pc, ps, st))
 
 
@@ -526,8 +541,9 @@ def loco_linear_backward_input(dy, w, dx, *, act: int = LOCO_ACT_NONE, codes=Non
     pdx, lddx = _mat(dx, "dx", T, K)
     pc, ps = _ckpt(codes, scales, T, K)
     c = _linear_ref(act, _one_dtype("dx and residual", dx, residual), LOCO_F32)
-    pdy, lddy, _dy = _operand(dy, "dy", T, N, (T, N, K), st, ALIGN_ROWS)
-    pw, ldw, _w = _operand(w, "w", N, K, (T, N, K), st, ALIGN_ROWS)
+    outs = ((pdx, lddx, T, K, dx.element_size()),)
+    pdy, lddy, _dy = _operand(dy, "dy", T, N, (T, N, K), st, outs, ALIGN_ROWS)
+    pw, ldw, _w = _operand(w, "w", N, K, (T, N, K), st, outs, ALIGN_ROWS)
     _check(lib.loco_linear_backward_input(c, pdy, lddy, pw, ldw, pc, ps, pr, ldr, T, N, K, pdx, lddx, st))
 
 
@@ -551,8 +567,10 @@ def loco_linear_backward_weight(dy, dw, *, x=None, codes=None, scales=None, gamm
     pc, ps = _ckpt(codes, scales, T, K)
     pg, pb, pdb, (pw, nw) = _vec(gamma, "gamma", K), _vec(beta, "beta", K), _vec(db, "db", N), _workspace(workspace)
     c = _linear_ref(LOCO_ACT_NONE, _one_dtype("dw and db", dw, db), _one_dtype("gamma and beta", gamma, beta))
-    pdy, lddy, _dy = _operand(dy, "dy", T, N, (T, N, K), st)
-    px, ldx, _x = _operand(x, "x", T, K, (T, N, K), st)
+    outs = ((pdw, lddw, N, K, dw.element_size()), _row(pdb, N * dw.element_size()),
+            _row(pw, loco_linear_workspace_bytes(N) if x is None and beta is not None else 0))
+    pdy, lddy, _dy = _operand(dy, "dy", T, N, (T, N, K), st, outs)
+    px, ldx, _x = _operand(x, "x", T, K, (T, N, K), st, outs)
     _check(lib.loco_linear_backward_weight(c, pdy, lddy, px, ldx, pc, ps, pg, pb, T, N, K, pdw, lddw, pdb, pw, nw, st))
 
 

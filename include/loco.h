@@ -407,6 +407,17 @@ LOCO_API loco_status loco_linear_align(const void* src, int64_t lds, int64_t row
                                        int64_t ldd, loco_stream_t stream);
 
 /*
+ * Whether two matrices of elements of bytes_a and bytes_b (1 to 16) bytes may
+ * share a byte: 1 or 0, by the rule of the entry points (of different pitches
+ * and several rows each, whether their ranges of memory meet; else exactly).
+ * An entry point that is given a copy of an operand cannot see what the
+ * operand itself overlaps: this can.  A NULL or empty matrix overlaps none;
+ * sizes that no entry point takes give 1.
+ */
+LOCO_API int32_t loco_matrices_overlap(const void* a, int64_t lda, int64_t rows_a, int64_t cols_a, int32_t bytes_a,
+                                       const void* b, int64_t ldb, int64_t rows_b, int64_t cols_b, int32_t bytes_b);
+
+/*
  * loco_linear_forward — z = x w^T + bias ;  y = act(z) + residual.
  * x [T, K] and w [N, K] bf16, products exact and accumulated in fp32; bias [N]
  * of param_dtype or NULL; residual [T, N] and y [T, N] of out_dtype, residual
