@@ -593,8 +593,13 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
         if (++stage == S::kStages) stage = 0, phase ^= 1;
       }
     }
+    // The CTA stays until the products have read its last stages: their signals come here, and say that the copies landed.
+    for (int i = 0, s = stage, ph = phase; i < S::kStages && !gave_up; ++i) {
+      gave_up = !mbar_wait(empty(s), ph ^ 1, p.wait_ns);
+      if (++s == S::kStages) s = 0, ph ^= 1;
+    }
     if (gave_up) {
-      // Let the copies in flight land before the CTA ends.  (The second CTA of a pair has them counted
+      // Let the copies in flight land at least.  (The second CTA of a pair has them counted
       // at the first's barriers; it waits a time in which any copy has landed.)
       if (PAIR && rank != 0) {
         for (int i = 0; i < 100; ++i) __nanosleep(100000);
@@ -610,6 +615,7 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
     const uint32_t desc = mma_desc(PAIR ? 2 * kTileM : kTileM, p.bn, p.a.a_mn, p.a.b_mn);
     const uint32_t chunk = kTileK * 128;
     const uint64_t astep = p.a.a_mn ? 2048 / 16 : 32 / 16, bstep = p.a.b_mn ? 2048 / 16 : 32 / 16;
+    bool ran = false;
     int stage = 0, phase = 0, buf = 0, bphase = 0;
     for (int64_t tile = worker; tile < tiles && !gave_up; tile += workers) {
       if (kt0 == kt1) break;
@@ -637,9 +643,12 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
       }
       if (gave_up) break;
       mma_commit<PAIR>(acc_full(buf));
+      ran = true;
       buf ^= 1;
       if (buf == 0) bphase ^= 1;
     }
+    // Nor does tensor memory go while products write it, even if the epilogue gave its wait up.
+    if (!gave_up && ran) gave_up = !mbar_wait(acc_full(buf ^ 1), buf == 0 ? bphase ^ 1 : bphase, p.wait_ns);
     if (gave_up) {
       mma_commit<PAIR>(drain);
       mbar_wait(drain, 0, p.wait_ns);
@@ -820,14 +829,17 @@ __global__ void __launch_bounds__(Shape<BN, LOADERS, PAIR, EPI>::kWarps * 32, 1)
   if (!PAIR && p.split > 1) {
     // One tile per cluster.  Its parts lie in the CTAs' shared memory as [n][m]; each CTA adds up
     // and finishes its share of the rows.
-    cluster_sync();
     int64_t tm, tn;
     tile_at(p, worker, &tm, &tn);
+    const int64_t n0 = tn * p.bn;
+    const int rows = int(min(int64_t(p.bn), p.a.N - n0));
+    // A part whose sums did not come is NaN, not what its memory holds: so is the output then.
+    if (__syncthreads_or(gave_up))
+      for (int i = threadIdx.x; i < rows * kTileM; i += S::kWarps * 32) st_shared4(base + uint32_t(i) * 4, 0x7FC00000u);
+    cluster_sync();
     const int q = warp & 3, side = warp / 4, sides = S::kWarps / 4;
     const int sub = lane / 4, seg = lane & 3;
     const Columns col = columns_of<EPI>(p.a, tm * kTileM + q * 32 + seg * 8);
-    const int64_t n0 = tn * p.bn;
-    const int rows = int(min(int64_t(p.bn), p.a.N - n0));
     const int share = (rows + p.split - 1) / p.split, lo = share * rank, hi = min(rows, lo + share);
     for (int j0 = lo + side * 8; j0 < hi; j0 += sides * 8) {
       const int j = min(j0 + sub, hi - 1);

@@ -465,9 +465,11 @@ LOCO_API loco_status loco_linear_backward_weight(const loco_linear_config* cfg, 
 /*
  * Waits inside the linear-layer kernels (a tile's copies, a tile's products)
  * end after two seconds and 20 microseconds per 64 of the summed dimension at
- * most; a kernel that gave one up leaves its output unwritten in part and counts it.  This reads the count of the current
- * device since the library was loaded into *count (host).  It synchronises
- * with the device: for diagnosis, not for the training loop.
+ * most; a kernel that gave one up counts it.  What it had not finished of its
+ * output is then not written, or, where several CTAs add up parts of a sum, NaN
+ * (and the checkpoint's scales 255).  This reads the count of the current device
+ * since the library was loaded into *count (host).  It synchronises with the
+ * device: for diagnosis, not for the training loop.
  */
 LOCO_API loco_status loco_linear_timeouts(int64_t* count);
 
