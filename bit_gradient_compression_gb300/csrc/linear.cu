@@ -27,9 +27,15 @@
 // board's power).  Measured, one launch at a time, in TFLOP/s against 1917 of the
 // largest library product: forward 8192 x 14336 x 4096 504 us, 1906; with tanh
 // GELU and a checkpoint of the pre-activation 595 us, 1615; input gradient 517 us,
-// 1860; weight gradient 588 us, 1635 (operands along m and n, whose boxes are four
-// times as many); from a checkpoint 720 us, 1335 (the loaders' conversion).
+// 1860; weight gradient 531 us, 1810; from a checkpoint 673 us, 1430, with a column
+// scale 711 us (the loaders' conversion, which every n tile repeats: decoding the
+// codes first and taking the product of that is 559 us).
 // Few rows are bound by reading w, small products by filling the pipeline once.
+//
+// The tensor cores add in fp32 but cut each partial sum instead of rounding it.  Of the
+// sum of its terms' magnitudes, in units of 2^-24, a sum over k = 4096 (11008) is off by
+// 0.32 (0.58) on average and 2.2 (3.6) at most; sums rounded in fp32 by 0.16 (0.19) and
+// 3.1 (3.2).  It is the accumulator that the hardware has.
 #include <atomic>
 
 #include "layers_common.cuh"

@@ -24,8 +24,9 @@
 //
 // 16384 x 4096 bf16: forward 55 us (4.9 TB/s; 73 us with the checkpoint), bound by
 // the two barriers a row with one row's work per CTA between them; backward 102 us
-// (3.9 TB/s), with a residual 112 us, from a checkpoint 102 us, bound by
-// instructions (20 an element) at two CTAs a SM, which its registers allow.
+// (3.9 TB/s), with a residual 112 us, from a checkpoint 102 us, bound by waiting
+// for each row's two sums (it issues in half of its cycles, at a quarter of the
+// warps: the two CTAs a SM that its registers allow).
 // Rows that take no 16-byte loads, 16384 x 2047: forward 53 us, backward 87 us.
 #include <atomic>
 

@@ -419,7 +419,10 @@ LOCO_API int32_t loco_matrices_overlap(const void* a, int64_t lda, int64_t rows_
 
 /*
  * loco_linear_forward — z = x w^T + bias ;  y = act(z) + residual.
- * x [T, K] and w [N, K] bf16, products exact and accumulated in fp32; bias [N]
+ * x [T, K] and w [N, K] bf16, products exact and accumulated in fp32 (but for a
+ * few rows by the tensor cores, which cut a partial sum rather than round it: up
+ * to 2.2 units of 2^-24 of the sum of the terms' magnitudes measured at K =
+ * 4096, 3.6 at 11008); bias [N]
  * of param_dtype or NULL; residual [T, N] and y [T, N] of out_dtype, residual
  * may be NULL or y itself.  codes/scales: checkpoint of z [T, N], out, both or
  * neither.  T == 0 or N == 0 is an empty call; K == 0 gives z = bias.
