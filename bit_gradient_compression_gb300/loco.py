@@ -479,6 +479,11 @@ def loco_matrices_overlap(a: int, lda: int, rows_a: int, cols_a: int, bytes_a: i
     return bool(lib.loco_matrices_overlap(a, lda, rows_a, cols_a, bytes_a, b, ldb, rows_b, cols_b, bytes_b))
 
 
+def _output(t, p: int, ld: int, rows: int, cols: int):
+    """An output as loco_matrices_overlap takes a matrix (one that is not there has address 0)."""
+    return p, ld, rows, cols, 1 if t is None else t.element_size()
+
+
 def _row(p: int, size: int):
     """A contiguous output of `size` bytes as a matrix of one row."""
     return p, size, 1, size, 1
@@ -519,7 +524,7 @@ def loco_linear_forward(x, w, y, *, act: int = LOCO_ACT_NONE, bias=None, residua
     py, ldy = _mat(y, "y", T, N)
     pc, ps = _ckpt(codes, scales, T, N)
     c, pb = _linear_ref(act, _one_dtype("y and residual", y, residual), _one_dtype("bias", bias)), _vec(bias, "bias", N)
-    outs = ((py, ldy, T, N, y.element_size()), _row(pc, loco_ckpt_code_bytes(T, N)), _row(ps, loco_ckpt_scale_bytes(T, N)))
+    outs = (_output(y, py, ldy, T, N), _row(pc, loco_ckpt_code_bytes(T, N)), _row(ps, loco_ckpt_scale_bytes(T, N)))
     px, ldx, _x = _operand(x, "x", T, K, (T, N, K), st, outs, ALIGN_ROWS)
     pw, ldw, _w = _operand(w, "w", N, K, (T, N, K), st, outs, ALIGN_ROWS)
     _check(lib.loco_linear_forward(c, px, ldx, pw, ldw, pb, pr, ldr, T, N, K, py, ldy, pc, ps, st))
@@ -541,7 +546,7 @@ def loco_linear_backward_input(dy, w, dx, *, act: int = LOCO_ACT_NONE, codes=Non
     pdx, lddx = _mat(dx, "dx", T, K)
     pc, ps = _ckpt(codes, scales, T, K)
     c = _linear_ref(act, _one_dtype("dx and residual", dx, residual), LOCO_F32)
-    outs = ((pdx, lddx, T, K, dx.element_size()),)
+    outs = (_output(dx, pdx, lddx, T, K),)
     pdy, lddy, _dy = _operand(dy, "dy", T, N, (T, N, K), st, outs, ALIGN_ROWS)
     pw, ldw, _w = _operand(w, "w", N, K, (T, N, K), st, outs, ALIGN_ROWS)
     _check(lib.loco_linear_backward_input(c, pdy, lddy, pw, ldw, pc, ps, pr, ldr, T, N, K, pdx, lddx, st))
@@ -567,7 +572,7 @@ def loco_linear_backward_weight(dy, dw, *, x=None, codes=None, scales=None, gamm
     pc, ps = _ckpt(codes, scales, T, K)
     pg, pb, pdb, (pw, nw) = _vec(gamma, "gamma", K), _vec(beta, "beta", K), _vec(db, "db", N), _workspace(workspace)
     c = _linear_ref(LOCO_ACT_NONE, _one_dtype("dw and db", dw, db), _one_dtype("gamma and beta", gamma, beta))
-    outs = ((pdw, lddw, N, K, dw.element_size()), _row(pdb, N * dw.element_size()),
+    outs = (_output(dw, pdw, lddw, N, K), _row(pdb, N * dw.element_size()),
             _row(pw, loco_linear_workspace_bytes(N) if x is None and beta is not None else 0))
     pdy, lddy, _dy = _operand(dy, "dy", T, N, (T, N, K), st, outs)
     px, ldx, _x = _operand(x, "x", T, K, (T, N, K), st, outs)

@@ -115,3 +115,12 @@ def test_columns_of_one_buffer():
     want = torch.empty(T, N, dtype=B, device="cuda")
     L.loco_linear_forward(kept, w, want)
     assert copies and torch.equal(y, want) and torch.equal(x, kept)
+
+
+def test_no_output():
+    """An output that is not there is refused by the entry point, whichever way the call is marshalled."""
+    x, w, dy = (torch.zeros(s, dtype=B) for s in ((T, K), (N, K), (T, N)))
+    for call in (lambda: L.loco_linear_forward(x, w, None, stream=0), lambda: L.loco_linear_backward_input(dy, w, None, stream=0)):
+        with pytest.raises(L.LocoError) as e:
+            call()
+        assert e.value.status == L.LOCO_ERR_INVALID_ARG
