@@ -202,7 +202,7 @@ def _prepare_join(c, g):
 
 def _prepare_logprob(c, g):
     R, V, dt = c["rows"], c["vocab"], DTYPES[c["x"]]
-    st = {"case": c, "ws": None}
+    st = {"case": c}
     z = torch.randn(R, V + c["pad"], generator=g, device="cuda") * 2.5
     y = torch.randint(0, V, (R,), generator=g, device="cuda")
     rows = torch.arange(R, device="cuda")
@@ -314,11 +314,8 @@ def _run_own(st):
                              dgate=st["dgate"], drow_gate=st["drowgate"], workspace=st["ws"])
         return _join_grads(st)
     if op == "logprob_forward":
-        if st["ws"] is None:
-            st["ws"] = torch.empty(L.loco_logprob_workspace_bytes(c["rows"], c["vocab"], c["top"]), dtype=torch.uint8,
-                                   device="cuda")
         L.loco_logprob_forward(st["logits"], st["targets"], st["logp"], lse=st["lse"], entropy=st["entropy"],
-                               top_ids=st["ids"], top_logp=st["alts"], scale=c["scale"], workspace=st["ws"])
+                               top_ids=st["ids"], top_logp=st["alts"], scale=c["scale"])
         return _logprob_outputs(st)
     if op == "logprob_backward":
         L.loco_logprob_backward(st["logits"], st["targets"], st["lse"], st["dlogits"], dlogp=st["dlogp"],
