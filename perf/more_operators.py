@@ -498,7 +498,7 @@ def _mix(x):
 
 def _random_bits(st):
     """32 random bits for each element of [nb, 256]."""
-    key = _mix(torch.full_like(st["id"], st["case"]["dither"] ^ (st["t"] & 0xFFFFFFFF)))
+    key = _mix(_mix(torch.full_like(st["id"], st["case"]["dither"])) ^ (st["t"] & 0xFFFFFFFF))
     e = st["inside"] * BLOCK
     key = _mix(_mix(key ^ st["id"]) ^ (e >> 32))
     return _mix(((e & 0xFFFFFFFF)[:, None] + torch.arange(BLOCK, device="cuda")) ^ key[:, None])
