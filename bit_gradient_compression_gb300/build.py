@@ -24,7 +24,8 @@ LIB = os.path.join(PKG, "libloco.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 
 SOURCES = ["abi.cu", "compress.cu", "decode_reduce.cu", "adam.cu", "sgd.cu",
-           "layers_abi.cu", "checkpoint.cu", "norm.cu", "align.cu", "linear.cu"]
+           "layers_abi.cu", "checkpoint.cu", "norm.cu", "align.cu", "linear.cu",
+           "steps_abi.cu", "join_forward.cu", "join_backward.cu", "logprob.cu", "adam_tensors.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false: no multiply-add contraction anywhere; every fp32 product and sum

@@ -26,6 +26,25 @@ constexpr uint32_t kTwo23Bits = 0x4B000000u;
 __device__ __forceinline__ float bf16lo_to_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi_to_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// IEEE square root and quotient with a zero operand handled by a select: the
+// operation is evaluated on 1 instead and the exact IEEE result put back
+// (sqrt(+-0) = +-0; +-0 / d = +-0 for a finite d > 0), so an element whose
+// mean gradient has been exactly zero (m = v = 0) does not send its warp down
+// the special-value path of the rounded square root or division.  The results
+// are those of __fsqrt_rn / __fdiv_rn for every input.  Measured: with 2.5 %
+// of the means exactly zero (two ranks' 4-bit codes of Gaussian gradients) the
+// step ran at 71 % of the HBM copy rate without the selects and 97 % with them.
+__device__ __forceinline__ float sqrt_zsel(float x) {
+  const bool z = x == 0.0f;
+  const float r = __fsqrt_rn(z ? 1.0f : x);
+  return z ? x : r;
+}
+__device__ __forceinline__ float div_zsel(float n, float d) {
+  const bool z = n == 0.0f && d > 0.0f && d < INFINITY;
+  const float r = __fdiv_rn(z ? 1.0f : n, d);
+  return z ? n : r;
+}
+
 // Streaming loads/stores: data is touched once, keep it out of L1 and mark it
 // evict-first in L2.
 __device__ __forceinline__ float4 ld_stream(const float4* p) { return __ldcs(p); }

@@ -1,0 +1,335 @@
+// What the forward and the backward kernels of a join share: rows in registers, and sums over a row.
+//
+// A row belongs to a team: a warp, a CTA of G threads, or a cluster of up to eight such CTAs, each of which
+// has the next G * E columns.  A thread holds E columns: whole 16-byte vectors t, t + G, ... (Vec), or single
+// columns t, t + G, ... where rows start on no 16-byte boundary (Cols).
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "device_common.cuh"
+#include "layers_common.cuh"
+#include "steps_internal.h"
+
+namespace loco {
+
+namespace {
+
+template <int G>
+constexpr int kTeamCta = G < 128 ? 128 : G;  // threads of a CTA
+
+// Columns in vectors of eight, of a type known when compiled.
+template <int G, int E, bool BF16>
+struct Vec {
+  static constexpr bool kWide = true, kShort = BF16;
+  static constexpr int kRaw = E / 8 * (BF16 ? 1 : 2);
+  uint4 w[kRaw];
+
+  __device__ static __forceinline__ int column(int t, int i) { return (t + G * (i / 8)) * 8 + i % 8; }
+
+  __device__ __forceinline__ void load(const void* p, int64_t row, int64_t ld, int t, int cols, int) {
+    const char* q = static_cast<const char*>(p) + row * ld * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) {
+      const int c0 = (t + G * e) * 8;
+      if (c0 + 8 <= cols) {
+        const uint4* v = reinterpret_cast<const uint4*>(q + c0 * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int k = 0; k < (BF16 ? 1 : 2); ++k) w[e * (BF16 ? 1 : 2) + k] = __ldcs(v + k);
+      } else {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = c0 + k < cols ? load_elem_rw(q, c0 + k, BF16) : 0.0f;
+        if (BF16) {
+          w[e] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+        } else {
+          w[2 * e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+          w[2 * e + 1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) {
+      if (BF16) {
+        const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[e * 8 + 2 * k] = bf16lo_to_f32(u[k]), v[e * 8 + 2 * k + 1] = bf16hi_to_f32(u[k]);
+      } else {
+        const uint32_t u[8] = {w[2 * e].x, w[2 * e].y, w[2 * e].z, w[2 * e].w,
+                               w[2 * e + 1].x, w[2 * e + 1].y, w[2 * e + 1].z, w[2 * e + 1].w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[e * 8 + k] = __uint_as_float(u[k]);
+      }
+    }
+  }
+  __device__ static __forceinline__ void store(void* p, int64_t row, int64_t ld, int t, int cols, int, const float (&v)[E]) {
+    char* q = static_cast<char*>(p) + row * ld * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) {
+      const int c0 = (t + G * e) * 8;
+      if (c0 + 8 <= cols) {
+        store8(q, c0, BF16, v + e * 8);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c0 + k < cols) store_elem(q, c0 + k, BF16, v[e * 8 + k]);
+      }
+    }
+  }
+};
+
+// Single columns, of a type known at run time.
+template <int G, int E>
+struct Cols {
+  static constexpr bool kWide = false, kShort = false;
+  float f[E];
+
+  __device__ static __forceinline__ int column(int t, int i) { return t + G * i; }
+
+  __device__ __forceinline__ void load(const void* p, int64_t row, int64_t ld, int t, int cols, int bf16) {
+    const char* q = static_cast<const char*>(p) + row * ld * (bf16 ? 2 : 4);
+    if (bf16) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = t + G * i < cols ? load_elem_rw(q, t + G * i, 1) : 0.0f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = t + G * i < cols ? load_elem_rw(q, t + G * i, 0) : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[E]) const {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = f[i];
+  }
+  __device__ static __forceinline__ void store(void* p, int64_t row, int64_t ld, int t, int cols, int bf16, const float (&v)[E]) {
+    char* q = static_cast<char*>(p) + row * ld * (bf16 ? 2 : 4);
+    if (bf16) {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (t + G * i < cols) store_elem(q, t + G * i, 1, v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (t + G * i < cols) store_elem(q, t + G * i, 0, v[i]);
+    }
+  }
+};
+
+// A vector of parameters at a thread's columns: `none` where it is not given, `past` behind the row's end.
+// wide: it takes 16-byte loads.
+template <typename Row, int E>
+__device__ __forceinline__ void params(const void* p, int t, int cols, int bf16, bool wide, float none, float past, float (&v)[E]) {
+  if (Row::kWide && wide && p != nullptr && Row::column(t, E - 1) < cols) {
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) load8(p, Row::column(t, e * 8), bf16, v + e * 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = Row::column(t, i);
+      v[i] = c < cols ? (p != nullptr ? load_elem(p, c, bf16) : none) : past;
+    }
+  }
+}
+
+// Value rounded to the type it is stored in.
+__device__ __forceinline__ float as_stored(float v, int bf16) {
+  return bf16 ? bf16_bits_to_f32(uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(v)))) : v;
+}
+
+__device__ __forceinline__ float warp_total(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// What a team's warps tell one another: N values of each.  Consecutive calls alternate between two areas, so
+// that one barrier each is enough.  In a cluster every warp writes its values into each CTA's memory.
+constexpr int kMaxCluster = 8;
+template <int G, bool CL>
+struct Board {
+  static constexpr int kW = G / 32, kAll = kW * (CL ? kMaxCluster : 1);
+  float v[2][3][kAll < 32 ? 32 : kAll];
+};
+template <int G, bool CL>
+struct Team {
+  Board<G, CL>* board;
+  int turn, ctas, rank;
+
+  // Values of the team's warps, lane by lane: N of them for each entry lane, lane + 32, ... below warps().
+  __device__ __forceinline__ int warps() const { return G / 32 * ctas; }
+  template <int N>
+  __device__ __forceinline__ void tell(const float (&v)[N]) {
+    const int warp = threadIdx.x / 32 % (G / 32), lane = threadIdx.x & 31;
+    if constexpr (CL) {
+      if (lane < ctas) {
+        Board<G, CL>* to = cooperative_groups::this_cluster().map_shared_rank(board, lane);
+#pragma unroll
+        for (int i = 0; i < N; ++i) to->v[turn][i][rank * (G / 32) + warp] = v[i];
+      }
+      cooperative_groups::this_cluster().sync();
+    } else {
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) board->v[turn][i][warp] = v[i];
+      }
+      __syncthreads();
+    }
+  }
+  // Sums over the team, the same in all its threads.
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_total(v[i]);
+    if constexpr (G > 32) {
+      constexpr int kW = G / 32;
+      const int lane = threadIdx.x & 31;
+      tell(v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if constexpr (CL) {
+          v[i] = 0.0f;
+          for (int k = lane; k < kW * ctas; k += 32) v[i] += board->v[turn][i][k];
+          v[i] = warp_total(v[i]);
+        } else {
+          v[i] = board->v[turn][i][lane % kW];
+#pragma unroll
+          for (int o = kW / 2; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+        }
+      }
+      turn ^= 1;
+    }
+  }
+};
+
+// How many columns the warps have.
+struct Counts {
+  float inv_warp, inv_cols;  // of this thread's warp, and of the row
+  float warp[4];             // columns of the team's warps lane, lane + 32, ...
+};
+
+// Mean and variance of a row with one exchange between its warps: each warp takes its own mean and then its squared
+// deviations from that; together they make the row's mean, and the variance with what the warps' means are off it.
+// No difference of large sums: a row far from 0 loses no digits.  v is 0 past the row's end, of which cols columns
+// are this CTA's.
+template <typename Row, int G, int E, bool CL>
+__device__ __forceinline__ void layer_stats(Team<G, CL>& team, const float (&v)[E], int t, int cols, const Counts& n,
+                                            float* mean, float* var) {
+  float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; i += 2) s0 += v[i], s1 += v[i + 1];
+  const float m = warp_total(s0 + s1) * n.inv_warp;
+  float q0 = 0.0f, q1 = 0.0f;
+  if (Row::column(t, E - 1) < cols) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const float a = v[i] - m, b = v[i + 1] - m;
+      q0 = fmaf(a, a, q0), q1 = fmaf(b, b, q1);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float a = Row::column(t, i) < cols ? v[i] - m : 0.0f;
+      q0 = fmaf(a, a, q0);
+    }
+  }
+  float w[2] = {m, warp_total(q0 + q1)};
+  if constexpr (G > 32) {
+    constexpr int kW = G / 32, kEntries = CL ? kMaxCluster * kW / 32 : 1;
+    const int lane = threadIdx.x & 31;
+    team.tell(w);
+    const Board<G, CL>& board = *team.board;
+    const auto across = [](float x) {
+#pragma unroll
+      for (int o = CL ? 16 : kW / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+      return x;
+    };
+    const float c = board.v[team.turn][0][0];  // the first warp's mean
+    float d[kEntries], q = 0.0f, s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) {
+      const int at = CL ? lane + 32 * k : lane % kW;
+      d[k] = n.warp[k] > 0.0f ? board.v[team.turn][0][at] - c : 0.0f;
+      q += n.warp[k] > 0.0f ? board.v[team.turn][1][at] : 0.0f;
+      s = fmaf(n.warp[k], d[k], s);
+    }
+    const float off = across(s) * n.inv_cols;
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) q = fmaf(n.warp[k] * (d[k] - off), d[k] - off, q);
+    w[0] = c + off, w[1] = across(q);
+    team.turn ^= 1;
+  }
+  *mean = w[0];
+  *var = w[1] * n.inv_cols;
+}
+
+// all: columns of the row, of which this CTA has `cols`.
+template <typename Row, int G, int E, bool CL>
+__device__ __forceinline__ Counts row_counts(const Team<G, CL>& team, int t, int cols, int64_t all) {
+  const auto of = [](int thread, int columns) {
+    int k = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) k += Row::column(thread, i) < columns;
+    return k;
+  };
+  Counts n;
+  const float w = warp_total(float(of(t, cols)));
+  n.inv_warp = w > 0.0f ? 1.0f / w : 0.0f;
+  n.inv_cols = 1.0f / float(all);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    n.warp[k] = 0.0f;
+    const int at = CL ? int(threadIdx.x & 31) + 32 * k : int(threadIdx.x & 31) % (G / 32);
+    if (G > 32 && at < team.warps() && (CL || k == 0)) {
+      int64_t left = all - int64_t(at / (G / 32)) * G * E;  // columns of that warp's CTA
+      left = left < 0 ? 0 : left > G * E ? G * E : left;
+      int c = 0;
+      for (int l = 0; l < 32; ++l) c += of(at % (G / 32) * 32 + l, int(left));
+      n.warp[k] = float(c);
+    }
+  }
+  return n;
+}
+
+// Columns c0 and on of a matrix or vector that may be missing.
+__device__ __forceinline__ const void* from_column(const void* p, int64_t c0, int bf16) {
+  return p == nullptr ? nullptr : static_cast<const char*>(p) + c0 * (bf16 ? 2 : 4);
+}
+__device__ __forceinline__ void* from_column(void* p, int64_t c0, int bf16) {
+  return p == nullptr ? nullptr : static_cast<char*>(p) + c0 * (bf16 ? 2 : 4);
+}
+
+inline bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+inline bool on16(const void* p, int64_t ld, int64_t rows, int bf16) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld % (bf16 ? 8 : 4) == 0));
+}
+
+// CTAs of a grid whose teams walk the rows: `teams` of them in a CTA, or one in a cluster of `ctas`; at most
+// `cap` CTAs, which the device holds at once.
+inline int64_t team_ctas(int64_t rows, int cap, int teams, int ctas) {
+  if (ctas > 1) {
+    const int64_t most = cap / ctas > 0 ? cap / ctas : 1;
+    return (rows < most ? rows : most) * ctas;
+  }
+  const int64_t want = (rows + teams - 1) / teams;
+  return want < cap ? want : cap;
+}
+template <typename Args>
+cudaError_t launch_teams(void (*kernel)(Args, bool), int64_t rows, int cap, int threads, int teams, int ctas, cudaStream_t s,
+                         const Args& a, bool pwide) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = dim3(unsigned(team_ctas(rows, cap, teams, ctas)));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = s;
+  if (ctas > 1) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = unsigned(ctas), attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, a, pwide);
+}
+
+}  // namespace
+
+}  // namespace loco

@@ -1,0 +1,200 @@
+// Joins a block's output to the residual stream and normalises the sum for the next block
+// (loco_join_forward): two reads and two writes a value, one pass.
+//
+// A row stays in registers from its loads to its last store (join_common.cuh says who holds what); the
+// next row is on its way meanwhile.  Each norm costs one round of sums: a RMS norm's squares, or a layer
+// norm's mean and squared deviations together.  The second norm is that of the stream as it is stored,
+// rounded to its type, which is what the backward pass will read.
+// Rows of more than 4096 columns are shared by the CTAs of a cluster; those of more than 32768 go through L2:
+// their CTA reads them once for every step.
+#include "join_common.cuh"
+
+namespace loco {
+
+namespace {
+
+template <int G, int E, bool CL, typename RowX, typename RowY>
+__global__ void __launch_bounds__(kTeamCta<G>) k_join_fwd(const JoinFwdArgs args, bool pwide) {
+  __shared__ Board<G, CL> board;
+  constexpr int kTeams = kTeamCta<G> / G;
+  JoinFwdArgs a = args;
+  const int t = threadIdx.x % G, place = threadIdx.x / G;
+  Team<G, CL> team{&board, 0, 1, 0};
+  int64_t c0 = 0, first = int64_t(blockIdx.x) * kTeams + place, step = int64_t(gridDim.x) * kTeams;
+  if constexpr (CL) {
+    const auto cluster = cooperative_groups::this_cluster();
+    team.ctas = int(cluster.num_blocks()), team.rank = int(cluster.block_rank());
+    c0 = int64_t(team.rank) * G * E, first = blockIdx.x / team.ctas, step = gridDim.x / team.ctas;
+    a.x = from_column(a.x, c0, a.x_bf16), a.y = from_column(a.y, c0, a.y_bf16);
+    a.h = from_column(a.h, c0, a.x_bf16), a.u = from_column(a.u, c0, a.y_bf16);
+    a.post_gamma = from_column(a.post_gamma, c0, a.param_bf16), a.post_beta = from_column(a.post_beta, c0, a.param_bf16);
+    a.gate = from_column(a.gate, c0, a.param_bf16);
+    a.gamma = from_column(a.gamma, c0, a.param_bf16), a.beta = from_column(a.beta, c0, a.param_bf16);
+    cluster.sync();  // every CTA's board is there
+  }
+  const int64_t rest = a.cols - c0;
+  const int cols = rest <= 0 ? 0 : rest < G * E ? int(rest) : G * E;
+  const Counts n = row_counts<RowX, G, E, CL>(team, t, cols, a.cols);
+  const auto stats = [&](const float (&v)[E], float* mean, float* rstd) {
+    float var;
+    if (a.rms) {
+      float q[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < E; i += 2) q[0] = fmaf(v[i], v[i], q[0]), q[1] = fmaf(v[i + 1], v[i + 1], q[1]);
+      float s[1] = {q[0] + q[1]};
+      team.sum(s);
+      *mean = 0.0f, var = s[0] * n.inv_cols;
+    } else {
+      layer_stats<RowX>(team, v, t, cols, n, mean, &var);
+    }
+    *rstd = rsqrtf(var + a.eps);
+  };
+  // h = a x + w (yh pg + pb), pg and pb with the gate in them, 0 past the row's end
+  float pg[E], pb[E], gm[E], bt[E];
+  {
+    float g[E];
+    params<RowX>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, g);
+    params<RowX>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, pg);
+    params<RowX>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, pb);
+#pragma unroll
+    for (int i = 0; i < E; ++i) pg[i] *= g[i], pb[i] *= g[i];
+  }
+  params<RowX>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, gm);
+  params<RowX>(a.beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, bt);
+  RowX xn;
+  RowY yn;
+  const auto fetch = [&](int64_t row) {
+    if (row >= a.rows) return;
+    xn.load(a.x, row, a.ldx, t, cols, a.x_bf16);
+    yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
+  };
+  fetch(first);
+  for (int64_t row = first; row - (kTeams > 1 ? place : 0) < a.rows; row += step) {
+    const bool live = row < a.rows;  // (where it is not, the values are the last row's, and nothing is stored)
+    float x[E], y[E];
+    xn.values(x), yn.values(y);
+    fetch(row + step);
+    float m1 = 0.0f, r1 = 1.0f, m2 = 0.0f, r2 = 1.0f;
+    if (a.post) stats(y, &m1, &r1);
+    const float w = a.s * (a.row_gate != nullptr && live ? __ldg(a.row_gate + row) : 1.0f);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = as_stored(fmaf(w, fmaf((y[i] - m1) * r1, pg[i], pb[i]), a.a * x[i]), a.x_bf16);
+    if (live) RowX::store(a.h, row, a.ldh, t, cols, a.x_bf16, x);
+    if (a.u != nullptr) {
+      stats(x, &m2, &r2);
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = fmaf((x[i] - m2) * r2, gm[i], bt[i]);
+      if (live) RowY::store(a.u, row, a.ldu, t, cols, a.y_bf16, x);
+    }
+    if (a.stats != nullptr && t == 0 && live && team.rank == 0) {
+      a.stats[row] = m1, a.stats[a.rows + row] = r1;
+      a.stats[2 * a.rows + row] = m2, a.stats[3 * a.rows + row] = r2;
+    }
+  }
+}
+
+// Rows of any length: a CTA of 1024 reads its row for each mean, variance and output.
+__global__ void __launch_bounds__(1024) k_join_fwd_long(const JoinFwdArgs a) {
+  __shared__ Board<1024, false> board;
+  Team<1024, false> team{&board, 0, 1, 0};
+  const auto sum = [&](float v) {
+    float s[1] = {v};
+    team.sum(s);
+    return s[0];
+  };
+  const float inv_cols = 1.0f / float(a.cols);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const int64_t x0 = row * a.ldx, y0 = row * a.ldy, h0 = row * a.ldh, u0 = row * a.ldu;
+    const auto stats = [&](const void* p, int64_t at, int bf16, float* mean, float* rstd) {
+      float m = 0.0f;
+      if (!a.rms) {
+        float s = 0.0f;
+        for (int64_t j = threadIdx.x; j < a.cols; j += 1024) s += load_elem_rw(p, at + j, bf16);
+        m = sum(s) * inv_cols;
+      }
+      float q = 0.0f;
+      for (int64_t j = threadIdx.x; j < a.cols; j += 1024) {
+        const float d = load_elem_rw(p, at + j, bf16) - m;
+        q = fmaf(d, d, q);
+      }
+      *mean = m, *rstd = rsqrtf(fmaf(sum(q), inv_cols, a.eps));
+    };
+    float m1 = 0.0f, r1 = 1.0f, m2 = 0.0f, r2 = 1.0f;
+    if (a.post) stats(a.y, y0, a.y_bf16, &m1, &r1);
+    const float w = a.s * (a.row_gate != nullptr ? a.row_gate[row] : 1.0f);
+    // a thread reads back only what it wrote itself
+    for (int64_t j = threadIdx.x; j < a.cols; j += 1024) {
+      const float pg = a.post_gamma != nullptr ? load_elem(a.post_gamma, j, a.param_bf16) : 1.0f;
+      const float pb = a.post_beta != nullptr ? load_elem(a.post_beta, j, a.param_bf16) : 0.0f;
+      const float g = a.gate != nullptr ? load_elem(a.gate, j, a.param_bf16) : 1.0f;
+      const float v = fmaf((load_elem(a.y, y0 + j, a.y_bf16) - m1) * r1, pg, pb);
+      store_elem(a.h, h0 + j, a.x_bf16, fmaf(w * g, v, a.a * load_elem_rw(a.x, x0 + j, a.x_bf16)));
+    }
+    if (a.u != nullptr) {
+      stats(a.h, h0, a.x_bf16, &m2, &r2);
+      for (int64_t j = threadIdx.x; j < a.cols; j += 1024) {
+        const float g = a.gamma != nullptr ? load_elem(a.gamma, j, a.param_bf16) : 1.0f;
+        const float b = a.beta != nullptr ? load_elem(a.beta, j, a.param_bf16) : 0.0f;
+        store_elem(a.u, u0 + j, a.y_bf16, fmaf((load_elem_rw(a.h, h0 + j, a.x_bf16) - m2) * r2, g, b));
+      }
+    }
+    if (a.stats != nullptr && threadIdx.x == 0) {
+      a.stats[row] = m1, a.stats[a.rows + row] = r1;
+      a.stats[2 * a.rows + row] = m2, a.stats[3 * a.rows + row] = r2;
+    }
+  }
+}
+
+template <int G, int E, bool CL, typename RowX, typename RowY>
+cudaError_t run(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
+  static LayerGrid grid;
+  int cap = 0;
+  const void* kernel = reinterpret_cast<const void*>(&k_join_fwd<G, E, CL, RowX, RowY>);
+  const cudaError_t e = layer_grid(grid, kernel, kTeamCta<G>, 0, 0, &cap);
+  if (e != cudaSuccess) return e;
+  return launch_teams(k_join_fwd<G, E, CL, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeamCta<G> / G, ctas, s, a, pwide);
+}
+template <int G, int E, bool CL>
+cudaError_t run_vec(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
+  if (!a.x_bf16) {
+    return a.y_bf16 ? run<G, E, CL, Vec<G, E, false>, Vec<G, E, true>>(a, pwide, ctas, s)
+                    : run<G, E, CL, Vec<G, E, false>, Vec<G, E, false>>(a, pwide, ctas, s);
+  }
+  return run<G, E, CL, Vec<G, E, true>, Vec<G, E, true>>(a, pwide, ctas, s);
+}
+template <int G, int E, bool CL>
+cudaError_t run_cols(const JoinFwdArgs& a, int ctas, cudaStream_t s) {
+  return run<G, E, CL, Cols<G, E>, Cols<G, E>>(a, false, ctas, s);
+}
+
+cudaError_t run_long(const JoinFwdArgs& a, cudaStream_t s) {
+  static LayerGrid grid;
+  int cap = 0;
+  const cudaError_t e = layer_grid(grid, reinterpret_cast<const void*>(&k_join_fwd_long), 1024, 0, 0, &cap);
+  if (e != cudaSuccess) return e;
+  k_join_fwd_long<<<int(a.rows < cap ? a.rows : cap), 1024, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_join_forward(const JoinFwdArgs& a, cudaStream_t s) {
+  const bool wide = on16(a.x, a.ldx, a.rows, a.x_bf16) && on16(a.h, a.ldh, a.rows, a.x_bf16) &&
+                    on16(a.y, a.ldy, a.rows, a.y_bf16) && on16(a.u, a.ldu, a.rows, a.y_bf16) && !(a.x_bf16 && !a.y_bf16);
+  const bool pwide = on16(a.post_gamma) && on16(a.post_beta) && on16(a.gate) && on16(a.gamma) && on16(a.beta);
+  const int ctas = int((a.cols + 4095) / 4096);
+  if (ctas > kMaxCluster) return run_long(a, s);
+  if (wide) {
+    if (a.cols <= 256) return run_vec<32, 8, false>(a, pwide, 1, s);
+    if (a.cols <= 1024) return run_vec<128, 8, false>(a, pwide, 1, s);
+    if (a.cols <= 2048) return run_vec<256, 8, false>(a, pwide, 1, s);
+    if (a.cols <= 4096) return run_vec<512, 8, false>(a, pwide, 1, s);
+    return run_vec<512, 8, true>(a, pwide, ctas, s);
+  }
+  if (a.cols <= 256) return run_cols<32, 8, false>(a, 1, s);
+  if (a.cols <= 1024) return run_cols<128, 8, false>(a, 1, s);
+  if (a.cols <= 4096) return run_cols<512, 8, false>(a, 1, s);
+  return run_cols<512, 8, true>(a, ctas, s);
+}
+
+}  // namespace loco

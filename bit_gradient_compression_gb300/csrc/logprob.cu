@@ -1,0 +1,518 @@
+// Log probabilities of given tokens with entropies and the most likely alternatives, and the gradient
+// of the logits (loco_logprob_forward, loco_logprob_backward).
+//
+// Forward, one pass over a row: each thread keeps its running maximum M, S = sum 2^t and D = sum 2^t t
+// with t = (z - M) scale log2(e), rescaled once a tile when the maximum grows; (M, S, D) of threads,
+// warps and CTAs are joined pairwise.  lse = M scale + ln S, entropy = ln S - ln 2 D / S (in deviations
+// from M, so that neither loses digits to the size of the logits).
+//
+// Alternatives: every warp lists what may be among its own largest: values above `thr`, the least of its
+// `top` largest so far.  The first tile's threshold is the top-th largest of the lanes' maxima, below
+// which no value of the warp can be needed.  Columns of one warp come in ascending order, so a later
+// value that equals the threshold loses the tie and `>` is enough.  The list is ordered by counting for
+// each key how many are above it; keys (value, then lower column) are all different, so the outcome does
+// not depend on the order in which lanes appended.
+//
+// A row is read by a warp (short rows), by a CTA of eight, or, where rows are few, by a cluster of up to
+// eight CTAs whose results the first joins through distributed shared memory: one launch, no workspace.
+// Rows start at any multiple of the element size: the elements before the first 16-byte boundary and
+// after the last whole vector are taken one by one.
+#include <cooperative_groups.h>
+
+#include "device_common.cuh"
+#include "layers_common.cuh"
+#include "steps_internal.h"
+
+namespace loco {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 8, kThreadsLp = 32 * kWarps;
+constexpr int kVectors = 4;                 // 16-byte vectors of a thread in one tile
+constexpr float kLowest = -3.402823466e38f; // maximum of nothing; a row's lowest finite value may equal it
+constexpr float kLeast = -200.0f;           // 2^t is 0 from here down; keeps t finite under -inf
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kListed = 64;                 // keys a warp's list holds before a vector is taken
+typedef unsigned long long Key;             // value in order, then the complement of the column; 0: none
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Bits that order like the values, both zeros alike.
+__device__ __forceinline__ uint32_t in_order(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float out_of_order(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+__device__ __forceinline__ Key key_of(float v, int64_t column) {
+  return Key(in_order(v)) << 32 | (0xFFFFFFFFu - uint32_t(column));
+}
+__device__ __forceinline__ float key_value(Key k) { return out_of_order(uint32_t(k >> 32)); }
+__device__ __forceinline__ int64_t key_column(Key k) { return int64_t(0xFFFFFFFFu - uint32_t(k)); }
+
+// M, S and D of a part of a row.
+struct Part {
+  float m, s, d;
+};
+// Both parts under the larger maximum; c = scale log2(e).
+__device__ __forceinline__ Part join(Part a, Part b, float c) {
+  const float m = max_nan(a.m, b.m);
+  const float ta = max_nan((a.m - m) * c, kLeast), tb = max_nan((b.m - m) * c, kLeast);
+  const float fa = exp2_f(ta), fb = exp2_f(tb);
+  return Part{m, fmaf(fa, a.s, fb * b.s), fmaf(fa, fmaf(a.s, ta, a.d), fb * fmaf(b.s, tb, b.d))};
+}
+
+template <bool BF16>
+constexpr int kVec = BF16 ? 8 : 4;
+
+// A row of which [head, head + vectors * kVec) is in whole 16-byte vectors.
+template <bool BF16>
+struct RowShape {
+  int64_t head, vectors;
+};
+template <bool BF16>
+__device__ __forceinline__ RowShape<BF16> row_shape(const void* row, int64_t cols) {
+  constexpr int kElem = BF16 ? 2 : 4;
+  const int64_t lead = int64_t((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / kElem;
+  const int64_t head = lead < cols ? lead : cols;
+  return RowShape<BF16>{head, (cols - head) / kVec<BF16>};
+}
+
+template <bool BF16>
+__device__ __forceinline__ float largest(uint4 w) {
+  if (BF16) {
+    const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(w.x, w.y), max_nan_bf16x2(w.z, w.w));
+    return max_nan(bf16lo_to_f32(m), bf16hi_to_f32(m));
+  }
+  return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)), max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+template <bool BF16>
+__device__ __forceinline__ void to_pairs(uint4 w, Pair (&v)[kVec<BF16> / 2]) {
+  if constexpr (BF16) {
+    v[0] = widen(w.x), v[1] = widen(w.y), v[2] = widen(w.z), v[3] = widen(w.w);
+  } else {
+    v[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y)), v[1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
+}
+
+// A warp's list of candidates.
+struct List {
+  Key* keys;   // kListed + 32 * 8
+  Key* kept;   // LOCO_MAX_TOP
+  int* count;
+  int top;
+  float thr;   // what is not above it is not needed
+
+  // Keeps the `top` largest, in order.
+  __device__ __forceinline__ void order(int lane) {
+    __syncwarp();
+    const int n = *count;
+    for (int i = lane; i < n; i += 32) {
+      const Key k = keys[i];
+      int above = 0;
+      for (int j = 0; j < n; ++j) above += keys[j] > k;
+      if (above < top) kept[above] = k;
+    }
+    __syncwarp();
+    const int left = n < top ? n : top;
+    if (lane < left) keys[lane] = kept[lane];
+    if (lane == 0) *count = left;
+    __syncwarp();
+    if (left == top) thr = key_value(keys[top - 1]);
+  }
+  // Appends the values of a vector that are above the threshold (all lanes of the warp; v: kVec values from column on).
+  template <int N>
+  __device__ __forceinline__ void append(const float (&v)[N], int64_t column, int lane) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (v[k] > thr) keys[atomicAdd(count, 1)] = key_of(v[k], column + k);
+    __syncwarp();
+    if (*count > kListed) order(lane);
+  }
+  // The threshold that the first tile's lane maxima give: at least `top` values are not below the top-th of them.
+  __device__ __forceinline__ void first(float lane_max, int lane) {
+    uint32_t u = in_order(lane_max), k = 0;
+    for (int i = 0; i < top; ++i) {
+      k = __reduce_max_sync(0xFFFFFFFFu, u);
+      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, u == k)) - 1) u = 0;
+    }
+    if (k <= in_order(-INFINITY)) return;
+    // the value before it, so that `>` takes it too (two steps down from zero, whose neighbour is -0)
+    const float t = out_of_order(k - (k == 0x80000000u ? 2u : 1u));
+    if (t > thr) thr = t;
+  }
+};
+
+template <bool TOP>
+struct Shared {
+  Part part[kWarps];
+  Part cta;
+};
+template <>
+struct Shared<true> {
+  Part part[kWarps];
+  Part cta;
+  Key keys[kWarps][kListed + 256];
+  Key kept[kWarps][LOCO_MAX_TOP];
+  Key cta_top[LOCO_MAX_TOP];
+  int count[kWarps];
+};
+
+// The `top` largest of `lists` ordered lists of `top` keys (0: none), by threads 0 .. lists * top - 1; `out` was 0.
+template <typename At>
+__device__ __forceinline__ void merge_lists(At at, int lists, int top, Key* out) {
+  const int i = threadIdx.x;
+  if (i >= lists * top) return;
+  const int l = i / top;
+  int rank = i % top;
+  const Key k = at(l, rank);
+  if (k == 0) return;
+  for (int o = 0; o < lists && rank < top; ++o) {
+    if (o == l) continue;
+    int lo = 0, hi = top;  // keys of list o above k
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (at(o, mid) > k)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    rank += lo;
+  }
+  if (rank < top) out[rank] = k;
+}
+
+// WPR: warps of a row's part (1: a CTA takes eight rows, 8: one).  CLUSTER: several CTAs to a row.
+template <bool BF16, int WPR, bool TOP, bool CLUSTER>
+__global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs a) {
+  __shared__ Shared<TOP> sh;
+  constexpr int kElem = BF16 ? 2 : 4, V = kVec<BF16>, kTeam = 32 * WPR;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, t = threadIdx.x % kTeam;
+  int parts = 1, me = 0;
+  if constexpr (CLUSTER) {
+    parts = int(cg::this_cluster().num_blocks());
+    me = int(cg::this_cluster().block_rank());
+  }
+  const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * kWarps + warp : int64_t(blockIdx.x) / parts;
+  if (WPR == 1 && row >= a.rows) return;  // whole warps, and no barrier follows
+  const char* z = static_cast<const char*>(a.logits) + row * a.ld * kElem;
+  const RowShape<BF16> shape = row_shape<BF16>(z, a.vocab);
+  const int64_t v_lo = shape.vectors * me / parts, v_hi = shape.vectors * (me + 1) / parts;
+  const uint4* vec = reinterpret_cast<const uint4*>(z + shape.head * kElem);
+  const float c = a.scale * kLog2E;
+  const Pair c2 = pair(c, c);
+
+  Part mine{kLowest, 0.0f, 0.0f};
+  List list{};
+  if constexpr (TOP) {
+    list = List{sh.keys[warp], sh.kept[warp], &sh.count[warp], a.top, -INFINITY};
+    if (lane == 0) sh.count[warp] = 0;
+    __syncwarp();
+  }
+  // single elements at the row's ends
+  const auto take_one = [&](int64_t from, int n) {
+    float v[1] = {t < n ? load_elem(z, from + t, BF16) : -INFINITY};
+    const float m = max_nan(mine.m, v[0]);
+    const float e = max_nan((v[0] - m) * c, kLeast), s = exp2_f(e);
+    mine = join(mine, Part{m, s, s * e}, c);
+    if constexpr (TOP) {
+      if (__any_sync(0xFFFFFFFFu, v[0] > list.thr)) list.append(v, from + t, lane);
+    }
+  };
+  if (me == 0 && shape.head > 0 && t < 32) take_one(0, int(shape.head));
+
+  uint4 next[kVectors];
+  const uint4 none = BF16 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
+                          : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  const auto fetch = [&](int64_t from) {
+#pragma unroll
+    for (int q = 0; q < kVectors; ++q) next[q] = from + q * kTeam < v_hi ? __ldcs(vec + from + q * kTeam) : none;
+  };
+  fetch(v_lo + t);
+  bool first = true;
+  for (int64_t i = v_lo; i < v_hi; i += kVectors * kTeam) {
+    uint4 w[kVectors];
+#pragma unroll
+    for (int q = 0; q < kVectors; ++q) w[q] = next[q];
+    fetch(i + kVectors * kTeam + t);
+    float top[kVectors], m = mine.m;
+#pragma unroll
+    for (int q = 0; q < kVectors; ++q) top[q] = largest<BF16>(w[q]), m = max_nan(m, top[q]);
+    const float down = max_nan((mine.m - m) * c, kLeast), f = exp2_f(down);
+    Pair s2 = pair(f * mine.s, 0.0f), d2 = pair(f * fmaf(mine.s, down, mine.d), 0.0f);
+    const Pair less = pair(-m, -m);
+#pragma unroll
+    for (int q = 0; q < kVectors; ++q) {
+      Pair v[V / 2];
+      to_pairs<BF16>(w[q], v);
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        float2 x = halves((v[k] + less) * c2);
+        x.x = max_nan(x.x, kLeast), x.y = max_nan(x.y, kLeast);
+        const Pair e2 = pair(exp2_f(x.x), exp2_f(x.y));
+        s2 = s2 + e2;
+        d2 = fma(e2, pair(x.x, x.y), d2);
+      }
+    }
+    const float2 s = halves(s2), d = halves(d2);
+    mine = Part{m, s.x + s.y, d.x + d.y};
+    if constexpr (TOP) {
+      float tile = top[0];
+#pragma unroll
+      for (int q = 1; q < kVectors; ++q) tile = max_nan(tile, top[q]);
+      if (first) list.first(tile, lane);
+      first = false;
+      if (__any_sync(0xFFFFFFFFu, tile > list.thr)) {
+#pragma unroll
+        for (int q = 0; q < kVectors; ++q) {
+          if (!__any_sync(0xFFFFFFFFu, top[q] > list.thr)) continue;
+          Pair v[V / 2];
+          to_pairs<BF16>(w[q], v);
+          float x[V];
+#pragma unroll
+          for (int k = 0; k < V / 2; ++k) {
+            const float2 h = halves(v[k]);
+            x[2 * k] = h.x, x[2 * k + 1] = h.y;
+          }
+          list.append(x, shape.head + (i + q * kTeam + t) * V, lane);
+        }
+      }
+    }
+  }
+  const int64_t tail = shape.head + shape.vectors * V;
+  if (me == parts - 1 && tail < a.vocab && t < 32) take_one(tail, int(a.vocab - tail));
+
+  // the warp's part
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Part other{__shfl_xor_sync(0xFFFFFFFFu, mine.m, o), __shfl_xor_sync(0xFFFFFFFFu, mine.s, o),
+                     __shfl_xor_sync(0xFFFFFFFFu, mine.d, o)};
+    // the same order of operands in both lanes: the same result
+    mine = lane & o ? join(other, mine, c) : join(mine, other, c);
+  }
+  if constexpr (TOP) {
+    list.order(lane);
+    const int n = *list.count;
+    if (lane >= n && lane < a.top) list.keys[lane] = 0;
+    __syncwarp();
+  }
+  Part all = mine;
+  const Key* best = TOP ? list.keys : nullptr;
+  if constexpr (WPR > 1) {
+    if (lane == 0) sh.part[warp] = mine;
+    if constexpr (TOP) {
+      if (threadIdx.x < LOCO_MAX_TOP) sh.cta_top[threadIdx.x] = 0;
+    }
+    __syncthreads();
+    all = sh.part[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) all = join(all, sh.part[w], c);
+    if constexpr (TOP) {
+      merge_lists([&](int l, int i) { return sh.keys[l][i]; }, kWarps, a.top, sh.cta_top);
+      best = sh.cta_top;
+    }
+    if constexpr (CLUSTER) {
+      if (threadIdx.x == 0) sh.cta = all;
+      const auto cluster = cg::this_cluster();
+      cluster.sync();
+      if (me == 0) {
+        all = sh.cta;
+        for (int p = 1; p < parts; ++p) all = join(all, *cluster.map_shared_rank(&sh.cta, p), c);
+        if constexpr (TOP) {
+          // the CTAs' lists beside one another, then merged as the warps' were
+          if (threadIdx.x < parts * a.top)
+            sh.keys[threadIdx.x / a.top][threadIdx.x % a.top] =
+                cluster.map_shared_rank(sh.cta_top, threadIdx.x / a.top)[threadIdx.x % a.top];
+        }
+      }
+      cluster.sync();  // nobody leaves before it has been read
+      if (me != 0) return;
+      if constexpr (TOP) {
+        if (threadIdx.x < LOCO_MAX_TOP) sh.cta_top[threadIdx.x] = 0;
+        __syncthreads();
+        merge_lists([&](int l, int i) { return sh.keys[l][i]; }, parts, a.top, sh.cta_top);
+      }
+    }
+    if constexpr (TOP) __syncthreads();
+  }
+
+  const bool nan = all.s != all.s, empty = all.s == 0.0f;
+  const float ls = empty ? 0.0f : logf(all.s);
+  if (t == 0) {
+    if (a.lse != nullptr) a.lse[row] = empty ? -INFINITY : fmaf(all.m, a.scale, ls);
+    if (a.entropy != nullptr) a.entropy[row] = empty ? 0.0f : ls - kLn2 * (all.d / all.s);
+    if (a.logp != nullptr) {
+      const int64_t y = a.targets[row];
+      float v = 0.0f;
+      if (y >= a.vocab)
+        v = __uint_as_float(0x7FC00000u);
+      else if (y >= 0)
+        v = empty ? -INFINITY : (load_elem(z, y, BF16) - all.m) * a.scale - ls;
+      a.logp[row] = nan && y >= 0 ? all.s : v;
+    }
+  }
+  if constexpr (TOP) {
+    if (t < a.top) {
+      const Key k = best[t];
+      const bool some = k != 0 && !nan;
+      if (a.top_ids != nullptr) a.top_ids[row * a.top + t] = some ? key_column(k) : -1;
+      if (a.top_logp != nullptr)
+        a.top_logp[row * a.top + t] = nan ? all.s : some ? (key_value(k) - all.m) * a.scale - ls : -INFINITY;
+    }
+  }
+}
+
+template <bool BF16, int WPR, bool TOP, bool CLUSTER>
+cudaError_t run_fwd(const LogprobFwdArgs& a, int parts, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = dim3(unsigned(WPR == 1 ? (a.rows + kWarps - 1) / kWarps : a.rows * parts));
+  cfg.blockDim = dim3(kThreadsLp);
+  cfg.stream = s;
+  if (CLUSTER) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = unsigned(parts), attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, k_logprob_fwd<BF16, WPR, TOP, CLUSTER>, a);
+}
+template <bool BF16, bool TOP>
+cudaError_t run_fwd_shape(const LogprobFwdArgs& a, int sms, cudaStream_t s) {
+  if (a.vocab <= 1024) return run_fwd<BF16, 1, TOP, false>(a, 1, s);
+  // several CTAs to a row while the grid leaves SMs without work and a part still fills a CTA's threads once
+  int parts = 1;
+  while (parts < 8 && a.rows * parts * 2 <= 2 * sms && a.vocab >= int64_t(parts) * 2 * kThreadsLp * kVec<BF16>) parts *= 2;
+  return parts == 1 ? run_fwd<BF16, 8, TOP, false>(a, 1, s) : run_fwd<BF16, 8, TOP, true>(a, parts, s);
+}
+
+// ---------------------------------------------------------------------------------------- backward
+
+// dlogits_j = p_j (A + B t_j) (+ C at the given token), t_j = (z_j - lse) log2(e), p_j = 2^t_j.
+struct Slope {
+  float c, lse2, a, b, at;
+  int64_t target;  // -1: none
+  bool zero;
+};
+__device__ __forceinline__ float slope_at(float z, const Slope& k) {
+  const float t = max_nan(fmaf(z, k.c, -k.lse2), kLeast);
+  return exp2_f(t) * fmaf(k.b, t, k.a);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_one(void* row, int64_t i, float v) {
+  store_elem(row, i, BF16, v);
+}
+
+template <bool BF16, int WPR>
+__global__ void __launch_bounds__(kThreadsLp) k_logprob_bwd(const LogprobBwdArgs a, int parts) {
+  constexpr int kElem = BF16 ? 2 : 4, V = kVec<BF16>, kTeam = 32 * WPR;
+  const int warp = threadIdx.x / 32, t = threadIdx.x % kTeam;
+  const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * kWarps + warp : int64_t(blockIdx.x) / parts;
+  const int me = WPR == 1 ? 0 : int(int64_t(blockIdx.x) % parts);
+  if (row >= a.rows) return;
+  const char* z = static_cast<const char*>(a.logits) + row * a.ld * kElem;
+  char* o = static_cast<char*>(a.dlogits) + row * a.ldd * kElem;
+  const int64_t y = a.dlogp != nullptr ? __ldg(a.targets + row) : -1;
+  const float lse = __ldg(a.lse + row);
+  const float d = a.dlogp != nullptr && y >= 0 ? (y < a.vocab ? __ldg(a.dlogp + row) : __uint_as_float(0x7FC00000u)) : 0.0f;
+  const float dh = a.dentropy != nullptr ? __ldg(a.dentropy + row) : 0.0f;
+  const float h = a.dentropy != nullptr ? __ldg(a.entropy + row) : 0.0f;
+  const bool zero = lse == -INFINITY;
+  Slope k;
+  k.c = a.scale * kLog2E, k.lse2 = lse * kLog2E;
+  k.a = -a.scale * fmaf(dh, h, d), k.b = -a.scale * dh * kLn2, k.at = a.scale * d;
+  if (zero) k.lse2 = 0.0f, k.c = 0.0f, k.a = k.b = 0.0f;
+  const int64_t target = y >= 0 && y < a.vocab && !zero ? y : -1;
+  // (an empty row's logits are all -inf: times a zero c they would be NaN)
+  const auto value = [&](float v, int64_t col) {
+    const float g = zero ? 0.0f : slope_at(v, k);
+    return col == target ? g + k.at : g;
+  };
+  const RowShape<BF16> shape = row_shape<BF16>(z, a.vocab);
+  if ((reinterpret_cast<uintptr_t>(z) & 15) == (reinterpret_cast<uintptr_t>(o) & 15)) {
+    const int64_t v_lo = shape.vectors * me / parts, v_hi = shape.vectors * (me + 1) / parts;
+    const int64_t tail = shape.head + shape.vectors * V;
+    if (me == 0 && t < shape.head) store_one<BF16>(o, t, value(load_elem_rw(z, t, BF16), t));
+    if (me == parts - 1 && t < a.vocab - tail)
+      store_one<BF16>(o, tail + t, value(load_elem_rw(z, tail + t, BF16), tail + t));
+    for (int64_t i = v_lo + t; i < v_hi; i += 4 * kTeam) {
+      uint4 w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i + q * kTeam < v_hi) w[q] = __ldcs(reinterpret_cast<const uint4*>(z + shape.head * kElem) + i + q * kTeam);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (i + q * kTeam >= v_hi) continue;
+        const int64_t col = shape.head + (i + q * kTeam) * V;
+        Pair v[V / 2];
+        to_pairs<BF16>(w[q], v);
+        float g[V];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 f = halves(v[j]);
+          g[2 * j] = value(f.x, col + 2 * j), g[2 * j + 1] = value(f.y, col + 2 * j + 1);
+        }
+        uint4 r;
+        if (BF16)
+          r = make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[V - 4], g[V - 3]),
+                         pack_bf16x2(g[V - 2], g[V - 1]));
+        else
+          r = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
+        __stcs(reinterpret_cast<uint4*>(o + shape.head * kElem) + i + q * kTeam, r);
+      }
+    }
+  } else {
+    // rows of logits and gradient start at different places within 16 bytes: neighbouring lanes take neighbouring elements
+    const int64_t lo = a.vocab * me / parts, hi = a.vocab * (me + 1) / parts;
+    for (int64_t i = lo + t; i < hi; i += 8 * kTeam) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = i + q * kTeam < hi ? load_elem_rw(z, i + q * kTeam, BF16) : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (i + q * kTeam < hi) store_one<BF16>(o, i + q * kTeam, value(v[q], i + q * kTeam));
+    }
+  }
+}
+
+template <bool BF16>
+cudaError_t run_bwd(const LogprobBwdArgs& a, int sms, cudaStream_t s) {
+  if (a.vocab <= 1024) {
+    k_logprob_bwd<BF16, 1><<<unsigned((a.rows + kWarps - 1) / kWarps), kThreadsLp, 0, s>>>(a, 1);
+  } else {
+    int parts = 1;
+    while (parts < 64 && a.rows * parts * 2 <= 8 * sms && a.vocab >= int64_t(parts) * 2 * kThreadsLp * kVec<BF16>) parts *= 2;
+    k_logprob_bwd<BF16, 8><<<unsigned(a.rows * parts), kThreadsLp, 0, s>>>(a, parts);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_logprob_forward(const LogprobFwdArgs& a, cudaStream_t s) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  if (a.top > 0) return a.bf16 ? run_fwd_shape<true, true>(a, sms, s) : run_fwd_shape<false, true>(a, sms, s);
+  return a.bf16 ? run_fwd_shape<true, false>(a, sms, s) : run_fwd_shape<false, false>(a, sms, s);
+}
+
+cudaError_t launch_logprob_backward(const LogprobBwdArgs& a, cudaStream_t s) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  return a.bf16 ? run_bwd<true>(a, sms, s) : run_bwd<false>(a, sms, s);
+}
+
+}  // namespace loco

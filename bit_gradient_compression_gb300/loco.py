@@ -23,6 +23,9 @@ LOCO_SCALE_ABSMAX, LOCO_SCALE_FIXED = 0, 1
 LOCO_ACT_NONE, LOCO_ACT_RELU, LOCO_ACT_GELU, LOCO_ACT_GELU_TANH, LOCO_ACT_SILU = 0, 1, 2, 3, 4
 LOCO_NORM_LAYER, LOCO_NORM_RMS = 0, 1
 LOCO_CKPT_BLOCK = 32
+LOCO_STATE_BLOCK = 256
+LOCO_STATE_M, LOCO_STATE_V = 0, 1
+LOCO_MAX_TOP = 32
 LOCO_MAX_DIM = 0x7FFFFFFF
 LOCO_MAX_RANKS = 16
 LOCO_MAX_N = 1 << 48
@@ -32,7 +35,9 @@ EXPORTS = ("loco_num_blocks", "loco_code_bytes", "loco_compress", "loco_compress
            "loco_last_error", "loco_ckpt_code_bytes", "loco_ckpt_scale_bytes", "loco_ckpt_encode", "loco_ckpt_decode",
            "loco_norm_forward", "loco_norm_workspace_bytes", "loco_norm_backward", "loco_linear_align",
            "loco_matrices_overlap", "loco_linear_forward", "loco_linear_backward_input", "loco_linear_workspace_bytes",
-           "loco_linear_backward_weight", "loco_linear_timeouts")
+           "loco_linear_backward_weight", "loco_linear_timeouts", "loco_join_forward", "loco_join_workspace_bytes",
+           "loco_join_backward", "loco_logprob_forward", "loco_logprob_backward", "loco_adam_tensors",
+           "loco_adam_state_decode")
 
 
 class LocoError(RuntimeError):
@@ -62,6 +67,23 @@ class loco_linear_config(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32)]
 
 
+class loco_join_config(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("post", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float), ("x_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class loco_adam_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_steps", ctypes.c_void_p), ("v_steps", ctypes.c_void_p), ("param_bf16", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("lr_scale", ctypes.c_float), ("decay_scale", ctypes.c_float)]
+
+
+class loco_adam_tensors_config(ctypes.Structure):
+    _fields_ = [("state_bits", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("dither", ctypes.c_uint32)]
+
+
 def make_config(bits=4, block=256, beta=0.9, err_scale_mult=4.0, reset_period=0, fixed_scale=None):
     return loco_config(bits, block, LOCO_SCALE_FIXED if fixed_scale is not None else LOCO_SCALE_ABSMAX,
                        float(fixed_scale or 0.0), float(beta), float(err_scale_mult), int(reset_period))
@@ -75,6 +97,12 @@ def make_adam(lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, bias_c
 def make_norm(kind=LOCO_NORM_LAYER, eps=1e-5):
     """A norm's kind and eps; the calls fill in the types of the tensors they are given."""
     return loco_norm_config(kind, float(eps), LOCO_F32, LOCO_F32, LOCO_F32, LOCO_F32)
+
+
+def make_join(kind=LOCO_NORM_LAYER, eps=1e-5, post=True, residual_scale=1.0, block_scale=1.0):
+    """A join's norms and scales; the calls fill in the types of the tensors they are given."""
+    return loco_join_config(kind, int(post), float(eps), float(residual_scale), float(block_scale), LOCO_F32, LOCO_F32,
+                            LOCO_F32, LOCO_F32)
 
 
 if not os.path.exists(LIB_PATH):
@@ -136,6 +164,24 @@ lib.loco_linear_backward_weight.argtypes = [_lin, _vp, _i64, _vp, _i64, _vp, _vp
 lib.loco_linear_backward_weight.restype = ctypes.c_int
 lib.loco_linear_timeouts.argtypes = [ctypes.POINTER(_i64)]
 lib.loco_linear_timeouts.restype = ctypes.c_int
+_join = ctypes.POINTER(loco_join_config)
+lib.loco_join_forward.argtypes = [_join, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp,
+                                  _i64, _vp, _vp]
+lib.loco_join_forward.restype = ctypes.c_int
+lib.loco_join_workspace_bytes.argtypes = [_i64, _i64]
+lib.loco_join_workspace_bytes.restype = _i64
+lib.loco_join_backward.argtypes = [_join, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
+lib.loco_join_backward.restype = ctypes.c_int
+lib.loco_logprob_forward.argtypes = [_vp, _i32, _i64, _i64, _i64, ctypes.c_float, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
+lib.loco_logprob_forward.restype = ctypes.c_int
+lib.loco_logprob_backward.argtypes = [_vp, _i32, _i64, _i64, _i64, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
+lib.loco_logprob_backward.restype = ctypes.c_int
+lib.loco_adam_tensors.argtypes = [ctypes.POINTER(loco_adam_tensors_config), ctypes.POINTER(loco_adam_tensor), _i32,
+                                  ctypes.POINTER(loco_adam_hparams), _i64, _vp, _vp]
+lib.loco_adam_tensors.restype = ctypes.c_int
+lib.loco_adam_state_decode.argtypes = [_i32, _vp, _vp, _i64, _vp, _i32, _vp]
+lib.loco_adam_state_decode.restype = ctypes.c_int
 lib.loco_status_string.argtypes = [ctypes.c_int]
 lib.loco_status_string.restype = ctypes.c_char_p
 lib.loco_last_error.argtypes = []
@@ -584,3 +630,188 @@ def loco_linear_timeouts() -> int:
     v = ctypes.c_int64()
     _check(lib.loco_linear_timeouts(ctypes.byref(v)))
     return v.value
+
+
+# --------------------------------------------------------------------------
+# Joins of blocks, log probabilities of given tokens, AdamW on many tensors.
+# --------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def _join_ref(*fields):
+    return ctypes.byref(loco_join_config(*fields))
+
+
+def _join_cfg(cfg, x: int, y: int, param: int, grad: int):
+    return _join_ref(cfg.kind, cfg.post, cfg.eps, cfg.residual_scale, cfg.block_scale, x, y, param, grad)
+
+
+def _stats(t, rows: int) -> int:
+    if t is None:
+        return 0
+    if (_DTYPES or _dtypes()).get(t.dtype) != LOCO_F32 or t.shape != (4, rows) or not t.is_contiguous():
+        raise ValueError(f"stats must be contiguous torch.float32 {(4, rows)} (got {t.dtype} {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def loco_join_forward(cfg: loco_join_config, x, y, h, u=None, *, gamma=None, beta=None, post_gamma=None, post_beta=None,
+                      gate=None, row_gate=None, stats=None, stream=None):
+    """h = residual_scale x + block_scale row_gate gate norm(y), u = norm(h): both norms with their own parameters
+    (without post, y itself; without u, no second norm).  stats [4, rows]: what the backward pass needs."""
+    rows, cols = _dims(x, "x")
+    px, ldx = _mat(x, "x", rows, cols)
+    py, ldy = _mat(y, "y", rows, cols)
+    ph, ldh = _mat(h, "h", rows, cols)
+    pu, ldu = _mat(u, "u", rows, cols)
+    c = _join_cfg(cfg, _one_dtype("x and h", x, h), _one_dtype("y and u", y, u),
+                  _one_dtype("gammas, betas and gate", gamma, beta, post_gamma, post_beta, gate), LOCO_F32)
+    _check(lib.loco_join_forward(c, px, ldx, py, ldy, rows, cols, _vec(post_gamma, "post_gamma", cols),
+                                 _vec(post_beta, "post_beta", cols), _vec(gate, "gate", cols),
+                                 _f32(row_gate, "row_gate", rows), _vec(gamma, "gamma", cols), _vec(beta, "beta", cols),
+                                 ph, ldh, pu, ldu, _stats(stats, rows), _stream(stream)))
+
+
+def loco_join_workspace_bytes(rows: int, cols: int) -> int:
+    return lib.loco_join_workspace_bytes(rows, cols)
+
+
+def loco_join_backward(cfg: loco_join_config, dh, du, h, y, stats, dx, dy, *, gamma=None, post_gamma=None, post_beta=None,
+                       gate=None, row_gate=None, dgamma=None, dbeta=None, dpost_gamma=None, dpost_beta=None, dgate=None,
+                       drow_gate=None, workspace=None, stream=None):
+    """Gradients of loco_join_forward: dx of the stream, dy of the block's output, and those of the parameters that
+    are given.  dh or du may be None (zeros)."""
+    rows, cols = _dims(dx, "dx")
+    pdh, lddh = _mat(dh, "dh", rows, cols)
+    pdu, lddu = _mat(du, "du", rows, cols)
+    ph, ldh = _mat(h, "h", rows, cols)
+    py, ldy = _mat(y, "y", rows, cols)
+    pdx, lddx = _mat(dx, "dx", rows, cols)
+    pdy, lddy = _mat(dy, "dy", rows, cols)
+    pw, nw = _workspace(workspace)
+    c = _join_cfg(cfg, _one_dtype("dh, h and dx", dh, h, dx), _one_dtype("du, y and dy", du, y, dy),
+                  _one_dtype("gammas, betas and gate", gamma, post_gamma, post_beta, gate),
+                  _one_dtype("the parameters' gradients", dgamma, dbeta, dpost_gamma, dpost_beta, dgate))
+    _check(lib.loco_join_backward(c, pdh, lddh, pdu, lddu, ph, ldh, py, ldy, _stats(stats, rows), rows, cols,
+                                  _vec(post_gamma, "post_gamma", cols), _vec(post_beta, "post_beta", cols),
+                                  _vec(gate, "gate", cols), _f32(row_gate, "row_gate", rows), _vec(gamma, "gamma", cols),
+                                  pdx, lddx, pdy, lddy, _vec(dpost_gamma, "dpost_gamma", cols),
+                                  _vec(dpost_beta, "dpost_beta", cols), _vec(dgate, "dgate", cols),
+                                  _f32(drow_gate, "drow_gate", rows), _vec(dgamma, "dgamma", cols),
+                                  _vec(dbeta, "dbeta", cols), pw, nw, _stream(stream)))
+
+
+def _i64_of(t, name: str, shape) -> int:
+    if t is None:
+        return 0
+    import torch
+    if t.dtype != torch.int64 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous torch.int64 {shape} (got {t.dtype} {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def loco_logprob_forward(logits, targets, logp, *, lse=None, entropy=None, top_ids=None, top_logp=None, scale: float = 1.0,
+                         stream=None):
+    """Log probabilities of the given tokens under softmax(scale * logits) [rows, vocab], with the rows' log sums, their
+    entropies and, where top_ids and top_logp [rows, top] are given, the most likely tokens."""
+    rows, vocab = _dims(logits, "logits")
+    pz, ld = _mat(logits, "logits", rows, vocab)
+    top = 0
+    for t, name in ((top_ids, "top_ids"), (top_logp, "top_logp")):
+        if t is not None:
+            if t.dim() != 2 or t.shape[0] != rows or (top_ids is not None and t.shape != top_ids.shape):
+                raise ValueError(f"{name} must be [rows, top] (got {tuple(t.shape)})")
+            top = t.shape[1]
+    if top_logp is not None and not top_logp.is_contiguous():
+        raise ValueError("top_logp must be contiguous")
+    alts = None if top_logp is None else top_logp.view(-1)
+    _check(lib.loco_logprob_forward(pz, _dtype(logits, "logits"), ld, rows, vocab, scale, _i64_of(targets, "targets", (rows,)),
+                                    _f32(logp, "logp", rows), _f32(lse, "lse", rows), _f32(entropy, "entropy", rows), top,
+                                    _i64_of(top_ids, "top_ids", (rows, top)), _f32(alts, "top_logp", rows * top),
+                                    _stream(stream)))
+
+
+def loco_logprob_backward(logits, targets, lse, dlogits, *, dlogp=None, entropy=None, dentropy=None, scale: float = 1.0,
+                          stream=None):
+    """dlogits (may be the logits) for the gradients of logp and of the entropies; lse and entropy from the forward pass."""
+    rows, vocab = _dims(logits, "logits")
+    pz, ld = _mat(logits, "logits", rows, vocab)
+    pd, ldd = _mat(dlogits, "dlogits", rows, vocab)
+    _check(lib.loco_logprob_backward(pz, _one_dtype("logits and dlogits", logits, dlogits), ld, rows, vocab, scale,
+                                     _i64_of(targets, "targets", (rows,)), _f32(lse, "lse", rows),
+                                     _f32(entropy, "entropy", rows), _f32(dlogp, "dlogp", rows),
+                                     _f32(dentropy, "dentropy", rows), pd, ldd, _stream(stream)))
+
+
+class AdamTensors:
+    """The tensors of loco_adam_tensors with their types: their addresses, and the tensors themselves, which it keeps."""
+
+    def __init__(self, array, count: int, cfg: loco_adam_tensors_config, tensors):
+        self.array, self.count, self.cfg, self.tensors = array, count, cfg, tensors
+
+
+def make_adam_tensors(params, grads, ms, vs, *, m_steps=None, v_steps=None, params_bf16=None, lr_scales=None,
+                      decay_scales=None, dither: int = 0) -> AdamTensors:
+    """The tensors of an optimizer step, from lists of contiguous tensors of one length.
+
+    params fp32 or bf16, grads fp32 or bf16; ms and vs fp32 of the params' sizes, or int8 and uint8 codes of whole blocks
+    of 256 (then m_steps and v_steps hold an fp32 step for each block).  params_bf16: where the updated fp32 parameters go
+    in bf16.  lr_scales, decay_scales: factors of the learning rate and of the weight decay (1 where not given).  dither:
+    the seed of the rounding of 8-bit states and bf16 parameters, 0 for rounding to nearest.
+
+    The list is made once and used for every step, as long as its tensors stay where they are.
+    """
+    import torch
+    count, f32 = len(params), torch.float32
+    eight = m_steps is not None or v_steps is not None
+    lists = [("params", params, None), ("grads", grads, None), ("ms", ms, torch.int8 if eight else f32),
+             ("vs", vs, torch.uint8 if eight else f32), ("m_steps", m_steps, f32), ("v_steps", v_steps, f32),
+             ("params_bf16", params_bf16, torch.bfloat16)]
+    if eight and (m_steps is None or v_steps is None):
+        raise ValueError("m_steps and v_steps go together")
+    addresses = []
+    for name, tensors, dtype in lists:
+        if tensors is None:
+            addresses.append([None] * count)
+            continue
+        if len(tensors) != count:
+            raise ValueError(f"{name} must list {count} tensors (got {len(tensors)})")
+        for i, (t, p) in enumerate(zip(tensors, params)):
+            nb = -(-p.numel() // LOCO_STATE_BLOCK)
+            want = nb if name.endswith("steps") else nb * LOCO_STATE_BLOCK if eight and name in ("ms", "vs") else p.numel()
+            if dtype is not None and t.dtype != dtype:
+                raise ValueError(f"{name}[{i}] must be {dtype} (got {t.dtype})")
+            if t.numel() != want or not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must hold {want} contiguous elements (got {tuple(t.shape)})")
+        addresses.append([t.data_ptr() or None for t in tensors])
+    for name, values in (("lr_scales", lr_scales), ("decay_scales", decay_scales)):
+        if values is not None and len(values) != count:
+            raise ValueError(f"{name} must list {count} factors (got {len(values)})")
+    if not 0 <= dither < 1 << 32:
+        raise ValueError(f"dither = {dither} outside [0, 2^32)")
+    array = (loco_adam_tensor * max(count, 1))(*(
+        loco_adam_tensor(*(a[i] for a in addresses), params[i].numel(), 1.0 if lr_scales is None else float(lr_scales[i]),
+                         1.0 if decay_scales is None else float(decay_scales[i])) for i in range(count)))
+    cfg = loco_adam_tensors_config(8 if eight else 32, _one_dtype("params", *params), _one_dtype("grads", *grads), dither)
+    return AdamTensors(array, count, cfg, [tensors for _, tensors, _ in lists])
+
+
+def loco_adam_tensors(tensors: AdamTensors, hp: loco_adam_hparams, t: int, *, grad_scale=None, stream=None):
+    """One Adam(W) step on every tensor of the list, in place.  grad_scale: one fp32 value on the device, the factor of
+    every gradient (of clipping, of a loss scale)."""
+    _check(lib.loco_adam_tensors(ctypes.byref(tensors.cfg), tensors.array, tensors.count, ctypes.byref(hp), t,
+                                 0 if grad_scale is None else _f32(grad_scale.view(-1), "grad_scale", 1), _stream(stream)))
+
+
+def loco_adam_state_decode(codes, steps, out, *, stream=None):
+    """out [n] (fp32 or bf16) = the values of an 8-bit state: int8 codes of a first moment, uint8 codes of a second."""
+    import torch
+    kind = {torch.int8: LOCO_STATE_M, torch.uint8: LOCO_STATE_V}.get(codes.dtype)
+    if kind is None:
+        raise ValueError(f"codes must be torch.int8 or torch.uint8 (got {codes.dtype})")
+    n = out.numel()
+    nb = -(-n // LOCO_STATE_BLOCK)
+    if codes.numel() != nb * LOCO_STATE_BLOCK or not codes.is_contiguous():
+        raise ValueError(f"codes must be {nb * LOCO_STATE_BLOCK} contiguous codes (got {tuple(codes.shape)})")
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    _check(lib.loco_adam_state_decode(kind, codes.data_ptr(), _f32(steps.view(-1), "steps", nb), n, out.data_ptr(),
+                                      _dtype(out, "out"), _stream(stream)))

@@ -476,6 +476,179 @@ LOCO_API loco_status loco_linear_backward_weight(const loco_linear_config* cfg, 
  */
 LOCO_API loco_status loco_linear_timeouts(int64_t* count);
 
+/* ==========================================================================
+ * Joins of blocks, the loss on given tokens, and AdamW on many tensors.
+ * Matrices, alignment, overlaps, statuses and arithmetic as for the layers
+ * above, except where an entry point says otherwise.
+ * ========================================================================== */
+
+typedef struct {
+  int32_t kind;            /* loco_norm_kind of both norms                                   */
+  int32_t post;            /* 1: the block's output y is normalised; 0: taken as it is       */
+  float   eps;             /* added to both variances; finite, >= 0                          */
+  float   residual_scale;  /* a: factor of the residual stream; finite                       */
+  float   block_scale;     /* s: factor of the block's output; finite                        */
+  int32_t x_dtype;         /* loco_dtype of x, h, dh and dx (the residual stream)            */
+  int32_t y_dtype;         /* loco_dtype of y, u, dy and du                                  */
+  int32_t param_dtype;     /* loco_dtype of the gammas, the betas and the gate               */
+  int32_t grad_dtype;      /* loco_dtype of the gradients of those                           */
+} loco_join_config;
+
+/*
+ * loco_join_forward — joins a block's output y [rows, cols] to the residual
+ * stream x [rows, cols] and normalises the sum for the next block.  Per row i:
+ *   post:    m1, r1 = statistics of y_i (as loco_norm_forward's);  n_j = (y_j - m1) * r1 * post_gamma_j + post_beta_j
+ *   else:    m1 = 0, r1 = 1;                                       n_j = y_j * post_gamma_j + post_beta_j
+ *   h_j = a * x_j + s * row_gate_i * gate_j * n_j, rounded to x_dtype
+ *   m2, r2 = statistics of the h_i that is written;  u_j = (h_j - m2) * r2 * gamma_j + beta_j
+ * post_gamma, post_beta, gate, gamma, beta [cols] of param_dtype and row_gate
+ * [rows] fp32 may each be NULL (1, or 0 for the betas).  h may be x itself.
+ * u may be NULL: then nothing is normalised, gamma and beta are not read and
+ * m2 = 0, r2 = 1.  stats [4, rows] fp32, out, may be NULL: m1, r1, m2, r2 of
+ * every row (0 in the place of a RMS norm's mean).  rows == 0 is an empty call.
+ */
+LOCO_API loco_status loco_join_forward(const loco_join_config* cfg, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                              int64_t rows, int64_t cols, const void* post_gamma, const void* post_beta,
+                              const void* gate, const float* row_gate, const void* gamma, const void* beta, void* h,
+                              int64_t ldh, void* u, int64_t ldu, float* stats, loco_stream_t stream);
+
+/* Bytes of workspace loco_join_backward needs for the gradients of parameters; 0 for sizes out of range. */
+LOCO_API int64_t loco_join_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * loco_join_backward — gradients of loco_join_forward for dh [rows, cols]
+ * (x_dtype, of the stream h) and du [rows, cols] (y_dtype, of u).  With yh =
+ * (y - m1) r1 (y without post), hh = (h - m2) r2 and the statistics of the
+ * forward pass:
+ *   q_j = du_j * gamma_j
+ *   t_j = dh_j + r2 * (q_j - [LAYER: mean_k q_k] - hh_j * mean_k(q_k * hh_k))
+ *   dx_j = a * t_j
+ *   c_j = s * row_gate_i * gate_j * t_j ;  p_j = c_j * post_gamma_j
+ *   dy_j = post: r1 * (p_j - [LAYER: mean_k p_k] - yh_j * mean_k(p_k * yh_k)), else p_j
+ *   dgamma_j = sum_i du_ij * hh_ij            dbeta_j = sum_i du_ij
+ *   dpost_gamma_j = sum_i c_ij * yh_ij        dpost_beta_j = sum_i c_ij
+ *   dgate_j = sum_i s * row_gate_i * t_ij * n_ij ;  drow_gate_i = sum_j s * gate_j * t_ij * n_ij
+ * dh or du may be NULL (zeros; without du, h is not read, dgamma and dbeta are
+ * zeros); dx may be dh itself.  y may be NULL without post where neither dgate,
+ * drow_gate nor dpost_gamma is asked for.  The gradients of parameters [cols]
+ * (grad_dtype) and drow_gate [rows] fp32 may each be NULL; workspace (ws_bytes >=
+ * loco_join_workspace_bytes) may be NULL where no gradient of a parameter of
+ * [cols] is asked for.  stats as the forward pass wrote them.  rows == 0 writes
+ * zeros to the gradients of parameters.
+ */
+LOCO_API loco_status loco_join_backward(const loco_join_config* cfg, const void* dh, int64_t lddh, const void* du,
+                               int64_t lddu, const void* h, int64_t ldh, const void* y, int64_t ldy,
+                               const float* stats, int64_t rows, int64_t cols, const void* post_gamma,
+                               const void* post_beta, const void* gate, const float* row_gate, const void* gamma,
+                               void* dx, int64_t lddx, void* dy, int64_t lddy, void* dpost_gamma, void* dpost_beta,
+                               void* dgate, float* drow_gate, void* dgamma, void* dbeta, void* workspace,
+                               int64_t ws_bytes, loco_stream_t stream);
+
+/* Most alternatives of a row that loco_logprob_forward lists. */
+#define LOCO_MAX_TOP 32
+
+/*
+ * loco_logprob_forward — log probabilities of given tokens.  Per row i of the
+ * logits [rows, vocab] (dtype), z_j = scale * logits_ij (scale finite, > 0):
+ *   lse = log(sum_j exp(z_j)) ;  logp = z_t - lse, t = targets_i
+ *   entropy = lse - sum_j p_j z_j, p_j = exp(z_j - lse)
+ *   top_ids, top_logp: the `top` largest logits' columns and z_j - lse, the
+ *   largest first, of equal ones the lowest column first
+ * targets [rows] int64, may be NULL where logp is: a row whose target is negative
+ * has no given token, and its logp is 0; a target >= vocab gives NaN.  logp,
+ * lse, entropy [rows] fp32, top_ids [rows, top] int64 and top_logp [rows, top]
+ * fp32 may each be NULL; 0 <= top <= LOCO_MAX_TOP.
+ * A logit of -inf is a token that cannot come: it has probability 0 and is not
+ * among the alternatives; where fewer than top are left the rest are -1 and
+ * -inf.  A row of which nothing is left has lse = logp = -inf and entropy 0.  A
+ * row that holds a NaN or +inf has NaN outputs and -1 for top_ids.
+ * vocab >= 1; rows == 0 is an empty call.
+ */
+LOCO_API loco_status loco_logprob_forward(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                                 float scale, const int64_t* targets, float* logp, float* lse, float* entropy,
+                                 int32_t top, int64_t* top_ids, float* top_logp, loco_stream_t stream);
+
+/*
+ * loco_logprob_backward — gradient of the logits for dlogp and dentropy [rows]
+ * fp32, each of which may be NULL (zeros):
+ *   dlogits_j = scale * (dlogp * ([j == t] - p_j) - dentropy * p_j * (z_j - lse + entropy))
+ * lse and entropy [rows] as the forward pass wrote them (entropy is read only
+ * with dentropy).  dlogits [rows, vocab] of the logits' dtype may be the logits
+ * themselves.  dlogp is taken as 0 in rows whose target is negative; targets may
+ * be NULL without dlogp.  Rows of which nothing is left get zeros, rows whose lse
+ * is NaN or whose target is >= vocab (with dlogp) NaN.
+ */
+LOCO_API loco_status loco_logprob_backward(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                                  float scale, const int64_t* targets, const float* lse, const float* entropy,
+                                  const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                                  loco_stream_t stream);
+
+/* Values of an 8-bit optimizer state that share one step. */
+#define LOCO_STATE_BLOCK 256
+
+/* One tensor of loco_adam_tensors; its pointers are device memory. */
+typedef struct {
+  void*       param;       /* [n] param_dtype, in/out                                          */
+  const void* grad;        /* [n] grad_dtype                                                   */
+  void*       m;           /* first moment, in/out: [n] fp32, or [nb * 256] int8 codes          */
+  void*       v;           /* second moment, in/out: [n] fp32, or [nb * 256] uint8 codes        */
+  float*      m_steps;     /* [nb] in/out, nb = ceil(n / 256), with 8-bit states; else ignored */
+  float*      v_steps;     /* [nb] in/out, likewise                                            */
+  uint16_t*   param_bf16;  /* [n] out: the updated fp32 parameters in bf16; may be NULL        */
+  int64_t     n;           /* elements; 0 is allowed (nothing is read or written)              */
+  float       lr_scale;    /* factor of the learning rate for this tensor                      */
+  float       decay_scale; /* factor of the weight decay (0: none)                             */
+} loco_adam_tensor;
+
+typedef struct {
+  int32_t  state_bits;   /* 32 or 8                                                            */
+  int32_t  param_dtype;  /* loco_dtype of every param                                          */
+  int32_t  grad_dtype;   /* loco_dtype of every grad                                           */
+  uint32_t dither;       /* 0: codes and bf16 params to nearest; else the seed of their dither */
+} loco_adam_tensors_config;
+
+/*
+ * loco_adam_tensors — one Adam(W) step on `count` tensors (host array, read
+ * during the call), in one launch for every 384 of them.  Per element, in this
+ * order, every product and sum rounded on its own:
+ *   g   = f32(grad) * *grad_scale              (grad_scale: device fp32, NULL: 1)
+ *   p   = p - (lr_i*wd_i)*p                    lr_i = lr*lr_scale, wd_i = weight_decay*decay_scale
+ *   m, v, den, p = p - c1*(m/den)              as loco_adam_step, c1 from lr_i
+ * lr_i, wd_i and their product are formed in fp32.
+ * 32-bit states are fp32 m and v.  8-bit states hold, for every 256 elements of
+ * a tensor (the last block may be shorter; its padding codes are 0),
+ *   m       = code * m_step,      code in [-127, 127], m_step = A/127, A = max |m|
+ *   sqrt(v) = code * v_step,      code in [0, 255],    v_step = S/255, S = max sqrt(v)
+ *   v       = (code*v_step) * (code*v_step)
+ *   code    = rint_even(x + d),   x = m * (127/A) or sqrt(v) * (255/S)
+ * A nonzero sqrt(v) never gets the code 0 but 1, so that no element is divided by
+ * eps alone.  A block with A (or S) below 127 (255) / FLT_MAX is held as zeros;
+ * one with a NaN or an infinity reads as NaN.  Zeros start a run.
+ * d = 0 without dither: then a change below half a step is lost.  With dither,
+ * d = (b - 127.5)/256 and the stored value is right on average: b = bits 0-7 (m),
+ * 8-15 (v) of r = mix(lo32(e) ^ mix(mix(mix(mix(dither) ^ lo32(t)) ^ i) ^ (e >> 32)))
+ * for element e of tensor i of the call, where mix is, on 32 bits,
+ *   x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85; x ^= x >> 16
+ * bf16 params are rounded to nearest even; with dither, r >> 16 is added to the
+ * fp32 bits before the lower half is cut off.
+ * param_bf16 must be NULL with bf16 params.  Buffers need their element type's
+ * alignment, codes 16 bytes; 16-byte aligned ones take the wide loads.  Nothing
+ * written may overlap another buffer of the call.
+ * hp: lr, lr_scale, decay_scale, weight_decay finite; else as loco_adam_step.
+ * t = 1-based step.  count == 0 is an empty call.
+ */
+LOCO_API loco_status loco_adam_tensors(const loco_adam_tensors_config* cfg, const loco_adam_tensor* tensors, int32_t count,
+                              const loco_adam_hparams* hp, int64_t t, const float* grad_scale, loco_stream_t stream);
+
+typedef enum {
+  LOCO_STATE_M = 0,  /* first moment: int8 codes   */
+  LOCO_STATE_V = 1   /* second moment: uint8 codes */
+} loco_state_kind;
+
+/* out [n] (out_dtype) = the values of an 8-bit state: code * step (M) or its square (V). */
+LOCO_API loco_status loco_adam_state_decode(int32_t kind, const void* codes, const float* steps, int64_t n, void* out,
+                                   int32_t out_dtype, loco_stream_t stream);
+
 /* Static text for a status code. */
 LOCO_API const char* loco_status_string(loco_status s);
 
