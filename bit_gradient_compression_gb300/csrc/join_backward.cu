@@ -16,15 +16,25 @@ namespace loco {
 
 namespace {
 
+// Rows on their way: the one at work and the next.  Behind them a thread's own parameters (gm and pg below) lie in
+// shared memory, where it alone reads them: in registers they would cost every second CTA of an SM.
+constexpr int kStages = 2;
+template <int G, int E, typename RowX, typename RowY>
+constexpr size_t kRing = size_t(kTeamCta<G>) * (kStages * 2 * (RowX::kBytes + RowY::kBytes) + 2 * E * sizeof(float));
+
 // SUMS: 4, or 2 where neither sum c nor sum du is wanted (a RMS norm without betas).
 template <int G, int E, bool CL, int SUMS, typename RowX, typename RowY>
-__global__ void __launch_bounds__(kTeamCta<G>, 1) k_join_bwd(const JoinBwdArgs args, bool pwide) {
+__global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort && SUMS == 2 && !CL> * 32 / kTeamCta<G>)
+    k_join_bwd(const JoinBwdArgs args, bool pwide) {
   __shared__ Board<G, CL> board;
-  constexpr int kTeams = kTeamCta<G> / G;
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, P = E / 2;
   JoinBwdArgs a = args;
   const int t = threadIdx.x % G, place = threadIdx.x / G;
   Team<G, CL> team{&board, 0, 1, 0};
-  int64_t c0 = 0, first = int64_t(blockIdx.x) * kTeams + place, step = int64_t(gridDim.x) * kTeams;
+  int64_t c0 = 0;
+  uint32_t first = blockIdx.x * kTeams + place, step = gridDim.x * kTeams;  // (rows are below 2^31)
+  const uint32_t n_rows = uint32_t(a.rows);
   if constexpr (CL) {
     const auto cluster = cooperative_groups::this_cluster();
     team.ctas = int(cluster.num_blocks()), team.rank = int(cluster.block_rank());
@@ -40,111 +50,144 @@ __global__ void __launch_bounds__(kTeamCta<G>, 1) k_join_bwd(const JoinBwdArgs a
   const int cols = rest <= 0 ? 0 : rest < G * E ? int(rest) : G * E;
   const float inv_cols = 1.0f / float(a.cols);
   const bool level = !a.rms;
-  float sums[SUMS][E];  // c yh, du hh (, c, du)
+  const Pair zero = both(0.0f);
+  Pair sums[SUMS][P];  // c yh, du hh (, c, du)
 #pragma unroll
   for (int k = 0; k < SUMS; ++k) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) sums[k][i] = 0.0f;
+    for (int i = 0; i < P; ++i) sums[k][i] = zero;
   }
   // q = du gm ; p = t w pg, pg with the gate and the scale in it, 0 past the row's end: whatever else a thread
   // has there (deviations of nothing from a mean) then reaches no sum of the row
-  constexpr bool kKeep = RowX::kShort;  // wider elements leave no registers for them: a thread's own places in shared memory
-  __shared__ float4 own[kKeep ? 1 : E / 2][kKeep ? 1 : kTeamCta<G>];
-  float gm[E], pg[E];
-  params<RowX>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, gm);
-  params<RowX>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, pg);
+  const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
+  constexpr uint32_t kStage = kThreadsCta * 2 * (RowX::kBytes + RowY::kBytes), kOwn = kStages * kStage;
+  {
+    Pair g[P], v[P];
+    params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, g);
+    params<RowX, E>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
 #pragma unroll
-  for (int i = 0; i < E; ++i) pg[i] *= a.s * gm[i];
-  params<RowX>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, gm);
-  const auto recall = [&](int first, float (&v)[E]) {
-    if constexpr (!kKeep) {
-#pragma unroll
-      for (int i = 0; i < E; i += 4) {
-        const float4 f = own[first + i / 4][threadIdx.x];
-        v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
-      }
-    }
-  };
-  if constexpr (!kKeep) {
-#pragma unroll
-    for (int i = 0; i < E; i += 4) {
-      own[i / 4][threadIdx.x] = make_float4(gm[i], gm[i + 1], gm[i + 2], gm[i + 3]);
-      own[(E + i) / 4][threadIdx.x] = make_float4(pg[i], pg[i + 1], pg[i + 2], pg[i + 3]);
-    }
+    for (int i = 0; i < P; ++i) v[i] = v[i] * (g[i] * both(a.s));
+    keep<E, kThreadsCta>(base + kOwn, 1, v);
+    params<RowX, E>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
+    keep<E, kThreadsCta>(base + kOwn, 0, v);
   }
-  constexpr bool kAhead = RowX::kShort;  // wider elements leave no registers for a row ahead
   RowX dhn, hn;
   RowY dun, yn;
-  const auto fetch = [&](int64_t row) {
-    if (row >= a.rows) return;
-    if (a.dh != nullptr) dhn.load(a.dh, row, a.lddh, t, cols, a.x_bf16);
-    if (a.du != nullptr) {
-      dun.load(a.du, row, a.lddu, t, cols, a.y_bf16);
-      hn.load(a.h, row, a.ldh, t, cols, a.x_bf16);
-    }
-    if (a.y != nullptr) yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
-  };
-  if constexpr (kAhead) fetch(first);
-  for (int64_t row = first; row - (kTeams > 1 ? place : 0) < a.rows; row += step) {
-    const bool live = row < a.rows;
-    if constexpr (!kAhead) fetch(row);
-    float dt[E], du[E], h[E], y[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) dt[i] = du[i] = h[i] = y[i] = 0.0f;
-    if (live) {
-      if (a.dh != nullptr) dhn.values(dt);
-      if (a.du != nullptr) dun.values(du), hn.values(h);
-      if (a.y != nullptr) yn.values(y);
-    }
-    float m1 = 0.0f, r1 = 1.0f, m2 = 0.0f, r2 = 1.0f, w = 1.0f;
-    if (live) {
-      if (a.post) m1 = __ldg(a.stats + row), r1 = __ldg(a.stats + a.rows + row);
-      if (a.du != nullptr) m2 = __ldg(a.stats + 2 * a.rows + row), r2 = __ldg(a.stats + 3 * a.rows + row);
-      if (a.row_gate != nullptr) w = __ldg(a.row_gate + row);
-    }
-    if constexpr (kAhead) fetch(row + step);
-    if (a.du != nullptr) {
-      recall(0, gm);
-      float s[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        h[i] = (h[i] - m2) * r2;
-        sums[1][i] = fmaf(du[i], h[i], sums[1][i]);
-        if constexpr (SUMS == 4) sums[3][i] += du[i];
-        du[i] *= gm[i];
-        s[0] += du[i];
-        s[1] = fmaf(du[i], h[i], s[1]);
+  uint32_t slot = 0;
+  const auto fetch = [&](uint32_t row) {
+    dhn.at = base + slot * kStage, hn.at = dhn.at + kThreadsCta * RowX::kBytes;
+    dun.at = hn.at + kThreadsCta * RowX::kBytes, yn.at = dun.at + kThreadsCta * RowY::kBytes;
+    if (row < n_rows) {
+      if (a.dh != nullptr) dhn.load(a.dh, row, a.lddh, t, cols, a.x_bf16);
+      if (a.du != nullptr) {
+        dun.load(a.du, row, a.lddu, t, cols, a.y_bf16);
+        hn.load(a.h, row, a.ldh, t, cols, a.x_bf16);
       }
-      team.sum(s);
-      const float c1 = level ? s[0] * inv_cols : 0.0f, c2 = s[1] * inv_cols;
-#pragma unroll
-      for (int i = 0; i < E; ++i) dt[i] = fmaf(r2, du[i] - c1 - h[i] * c2, dt[i]);
+      if (a.y != nullptr) yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
     }
+    cp_async_commit();
+    slot ^= 1;
+  };
+  constexpr bool kAhead = RowX::kWide;  // single columns leave no registers for a row ahead
+  if constexpr (kAhead) fetch(first);
+  const Pair a2 = both(a.a);
+  for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
+    const bool live = row < n_rows;
+    if constexpr (!kAhead) fetch(row);
+    RowX dhc = dhn, hc = hn;
+    RowY duc = dun, yc = yn;
+    float m2 = 0.0f, r2 = 1.0f;
+    if (live && a.du != nullptr) m2 = __ldg(a.stats + 2 * a.rows + row), r2 = __ldg(a.stats + 3 * a.rows + row);
+    if constexpr (kAhead) {
+      fetch(row + step);
+      cp_async_wait<1>();
+    }
+    Pair dt[P], du[P];
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    if (a.du != nullptr && live) {
+      Pair h[P], g[P];
+      duc.values(du), hc.values(h);
+      recall<E, kThreadsCta>(base + kOwn, 0, g);
+      const Pair less = both(-m2), f = both(r2);
+      Pair s0 = zero, s1 = zero;
 #pragma unroll
-    for (int i = 0; i < E; ++i) du[i] = a.a * dt[i];
-    if (live) RowX::store(a.dx, row, a.lddx, t, cols, a.x_bf16, du);
-    recall(E / 4, pg);
-    float s[3] = {0.0f, 0.0f, 0.0f};  // of p / w, of p yh / w and of t s gate post_beta
+      for (int i = 0; i < P; ++i) {
+        h[i] = (h[i] + less) * f;
+        sums[1][i] = fma(du[i], h[i], sums[1][i]);
+        if constexpr (SUMS == 4) sums[3][i] = sums[3][i] + du[i];
+        du[i] = du[i] * g[i];
+        s0 = s0 + du[i];
+        s1 = fma(du[i], h[i], s1);
+        dt[i] = h[i];
+      }
+      s[0] = total(s0), s[1] = total(s1);
+    }
+    float m1 = 0.0f, r1 = 1.0f, w = 1.0f;
+    if (live && a.post) m1 = __ldg(a.stats + row), r1 = __ldg(a.stats + a.rows + row);
+    if (live && a.row_gate != nullptr) w = __ldg(a.row_gate + row);
+    if (a.du != nullptr) {
+      float two[2] = {s[0], s[1]};
+      team.sum(two);
+      const Pair c1 = both(level ? -two[0] * inv_cols : 0.0f), c2 = both(-two[1] * inv_cols);
+      if (live) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      y[i] = (y[i] - m1) * r1;
-      if (!live) dt[i] = 0.0f;
-      const float c = dt[i] * w;
-      sums[0][i] = fmaf(c, y[i], sums[0][i]);
-      if constexpr (SUMS == 4) sums[2][i] += c;
-      du[i] = dt[i] * pg[i];
-      s[0] += du[i];
-      s[1] = fmaf(du[i], y[i], s[1]);
+        for (int i = 0; i < P; ++i) dt[i] = fma(dt[i], c2, du[i] + c1);  // over r2
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) dt[i] = zero;
+    }
+    if (live) {
+      if (a.dh != nullptr) {
+        dhc.values(du);
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) du[i] = zero;
+      }
+      const Pair f = both(r2);
+#pragma unroll
+      for (int i = 0; i < P; ++i) dt[i] = fma(f, dt[i], du[i]), du[i] = a2 * dt[i];
+      RowX::store(a.dx, row, a.lddx, t, cols, a.x_bf16, du);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) dt[i] = zero;
+    }
+    // over w: p and p yh, and t s gate post_beta
+    Pair y[P];
+    s[0] = s[1] = s[2] = 0.0f;
+    if (a.y != nullptr && live) {
+      yc.values(y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) y[i] = zero;
+    }
+    {
+      Pair g[P];
+      recall<E, kThreadsCta>(base + kOwn, 1, g);
+      const Pair less = both(-m1), f = both(r1), w2 = both(w);
+      Pair s0 = zero, s1 = zero;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        y[i] = (y[i] + less) * f;
+        const Pair c = dt[i] * w2;
+        sums[0][i] = fma(c, y[i], sums[0][i]);
+        if constexpr (SUMS == 4) sums[2][i] = sums[2][i] + c;
+        du[i] = dt[i] * g[i];
+        s0 = s0 + du[i];
+        s1 = fma(du[i], y[i], s1);
+      }
+      s[0] = total(s0), s[1] = total(s1);
     }
     if (a.drow_gate != nullptr) {
       if (a.post_beta != nullptr) {
-        float v[E];
-        params<RowX>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, v);
+        Pair v[P], d = zero;
+        params<RowX, E>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, v);
 #pragma unroll
-        for (int i = 0; i < E; ++i) dt[i] *= v[i];
-        params<RowX>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
+        for (int i = 0; i < P; ++i) dt[i] = dt[i] * v[i];
+        params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
 #pragma unroll
-        for (int i = 0; i < E; ++i) s[2] = fmaf(dt[i], v[i], s[2]);
+        for (int i = 0; i < P; ++i) d = fma(dt[i], v[i], d);
+        s[2] = total(d);
       }
       team.sum(s);
       if (t == 0 && live && team.rank == 0) a.drow_gate[row] = fmaf(a.s, s[2], s[1]);
@@ -153,16 +196,17 @@ __global__ void __launch_bounds__(kTeamCta<G>, 1) k_join_bwd(const JoinBwdArgs a
       team.sum(two);
       s[0] = two[0], s[1] = two[1];
     }
+    if (!live) continue;  // whole teams
     if (a.post) {
-      const float c1 = level ? s[0] * inv_cols : 0.0f, c2 = s[1] * inv_cols;
-      const float f = w * r1;
+      const Pair c1 = both(level ? -s[0] * inv_cols : 0.0f), c2 = both(-s[1] * inv_cols), f = both(w * r1);
 #pragma unroll
-      for (int i = 0; i < E; ++i) du[i] = f * (du[i] - c1 - y[i] * c2);
+      for (int i = 0; i < P; ++i) du[i] = f * fma(y[i], c2, du[i] + c1);
     } else if (a.row_gate != nullptr) {
+      const Pair f = both(w);
 #pragma unroll
-      for (int i = 0; i < E; ++i) du[i] *= w;
+      for (int i = 0; i < P; ++i) du[i] = f * du[i];
     }
-    if (live) RowY::store(a.dy, row, a.lddy, t, cols, a.y_bf16, du);
+    RowY::store(a.dy, row, a.lddy, t, cols, a.y_bf16, du);
   }
   if (a.partials == nullptr) return;
   // one partial row a team of CTAs; the teams of a CTA are added through shared memory in their order
@@ -174,18 +218,22 @@ __global__ void __launch_bounds__(kTeamCta<G>, 1) k_join_bwd(const JoinBwdArgs a
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const int c = RowX::column(t, i);
-        if (c < cols) out[kOrder[k] * a.cols + c] = sums[k][i];
+        const float2 v = halves(sums[k][i / 2]);
+        if (c < cols) out[kOrder[k] * a.cols + c] = i % 2 ? v.y : v.x;
       }
     }
   } else {
-    __shared__ float rows[kTeams][G * E];
+    float(*rows)[G * E] = reinterpret_cast<float(*)[G * E]>(ring + kOwn);  // (no thread needs its parameters any more)
 #pragma unroll
     for (int k = 0; k < SUMS; ++k) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < E; ++i) rows[place][RowX::column(t, i)] = sums[k][i];
+      for (int i = 0; i < E; ++i) {
+        const float2 v = halves(sums[k][i / 2]);
+        rows[place][RowX::column(t, i)] = i % 2 ? v.y : v.x;
+      }
       __syncthreads();
-      for (int c = threadIdx.x; c < cols; c += kTeamCta<G>) {
+      for (int c = threadIdx.x; c < cols; c += kThreadsCta) {
         float v = rows[0][c];
 #pragma unroll
         for (int q = 1; q < kTeams; ++q) v += rows[q][c];
@@ -265,38 +313,46 @@ __global__ void __launch_bounds__(1024) k_join_bwd_long(const JoinBwdArgs a) {
   }
 }
 
-// Adds the partial rows of 32 columns: 32 lanes of columns, eight warps of partial rows, joined in order.
-__global__ void __launch_bounds__(256) k_join_bwd_params(const JoinBwdArgs a, int partials, int sums) {
+// Adds the partial rows of 32 columns: warp w takes every eighth row of one of the four sums, eight rows' loads
+// under way at a time; the eight are joined in order.
+__global__ void __launch_bounds__(1024) k_join_bwd_params(const JoinBwdArgs a, int partials, int sums) {
   __shared__ float part[8][kJoinSums][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = warp % kJoinSums, group = warp / kJoinSums;
   const int64_t c = int64_t(blockIdx.x) * 32 + lane;
-  float v[kJoinSums] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < a.cols) {
-    for (int p = warp; p < partials; p += 8) {
-      const float* q = a.partials + int64_t(p) * kJoinSums * a.cols + c;
-      v[0] += q[0], v[2] += q[2 * a.cols];
-      if (sums == 4) v[1] += q[a.cols], v[3] += q[3 * a.cols];
-    }
-  }
+  float v = 0.0f;
+  if (c < a.cols && (sums == 4 || k % 2 == 0)) {
+    const float* q = a.partials + k * a.cols + c;
+    const int64_t row = kJoinSums * a.cols;
+    int p = group;
+    for (; p + 56 < partials; p += 64) {
+      float x[8];
 #pragma unroll
-  for (int k = 0; k < kJoinSums; ++k) part[warp][k][lane] = v[k];
+      for (int i = 0; i < 8; ++i) x[i] = __ldcs(q + (p + 8 * i) * row);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += x[i];
+    }
+    for (; p < partials; p += 8) v += __ldcs(q + p * row);
+  }
+  part[group][k][lane] = v;
   __syncthreads();
   if (warp != 0 || c >= a.cols) return;
+  float s[kJoinSums];
 #pragma unroll
-  for (int k = 0; k < kJoinSums; ++k) {
+  for (int i = 0; i < kJoinSums; ++i) {
+    s[i] = part[0][i][lane];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) v[k] += part[w][k][lane];
+    for (int w = 1; w < 8; ++w) s[i] += part[w][i][lane];
   }
   const float g = a.s * (a.gate != nullptr ? load_elem(a.gate, c, a.param_bf16) : 1.0f);
-  if (a.dpost_gamma != nullptr) store_elem(a.dpost_gamma, c, a.grad_bf16, g * v[0]);
-  if (a.dpost_beta != nullptr) store_elem(a.dpost_beta, c, a.grad_bf16, g * v[1]);
+  if (a.dpost_gamma != nullptr) store_elem(a.dpost_gamma, c, a.grad_bf16, g * s[0]);
+  if (a.dpost_beta != nullptr) store_elem(a.dpost_beta, c, a.grad_bf16, g * s[1]);
   if (a.dgate != nullptr) {
     const float pg = a.post_gamma != nullptr ? load_elem(a.post_gamma, c, a.param_bf16) : 1.0f;
-    const float d = a.post_beta != nullptr ? load_elem(a.post_beta, c, a.param_bf16) * v[1] : 0.0f;
-    store_elem(a.dgate, c, a.grad_bf16, a.s * fmaf(pg, v[0], d));
+    const float d = a.post_beta != nullptr ? load_elem(a.post_beta, c, a.param_bf16) * s[1] : 0.0f;
+    store_elem(a.dgate, c, a.grad_bf16, a.s * fmaf(pg, s[0], d));
   }
-  if (a.dgamma != nullptr) store_elem(a.dgamma, c, a.grad_bf16, v[2]);
-  if (a.dbeta != nullptr) store_elem(a.dbeta, c, a.grad_bf16, v[3]);
+  if (a.dgamma != nullptr) store_elem(a.dgamma, c, a.grad_bf16, s[2]);
+  if (a.dbeta != nullptr) store_elem(a.dbeta, c, a.grad_bf16, s[3]);
 }
 
 template <int G, int E, bool CL, int SUMS, typename RowX, typename RowY>
@@ -304,12 +360,18 @@ cudaError_t run(const JoinBwdArgs& a, bool pwide, int ctas, int* partials, cudaS
   static LayerGrid grid;
   int cap = 0;
   const void* kernel = reinterpret_cast<const void*>(&k_join_bwd<G, E, CL, SUMS, RowX, RowY>);
-  const cudaError_t e = layer_grid(grid, kernel, kTeamCta<G>, 0, 0, &cap);
+  constexpr size_t kSmem = kRing<G, E, RowX, RowY>;
+  const cudaError_t e = layer_grid(grid, kernel, kTeamCta<G>, kSmem, kSmem, &cap);
   if (e != cudaSuccess) return e;
-  if (a.partials != nullptr && cap > kJoinPartials * ctas) cap = kJoinPartials * ctas;
   constexpr int kTeams = kTeamCta<G> / G;
+  if (a.partials != nullptr) {
+    // few rows: four at least to a team, so that the partial rows stay fewer than a quarter of the rows
+    const int64_t most = a.rows / (4 * kTeams) * ctas;
+    if (cap > kJoinPartials * ctas) cap = kJoinPartials * ctas;
+    if (cap > most) cap = most > ctas ? int(most) : ctas;
+  }
   *partials = int(team_ctas(a.rows, cap, kTeams, ctas) / ctas);
-  return launch_teams(k_join_bwd<G, E, CL, SUMS, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeams, ctas, s, a, pwide);
+  return launch_teams(k_join_bwd<G, E, CL, SUMS, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeams, ctas, kSmem, s, a, pwide);
 }
 template <int G, int E, bool CL, typename RowX, typename RowY>
 cudaError_t run_sums(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* partials, cudaStream_t s) {
@@ -372,7 +434,7 @@ cudaError_t launch_join_backward(const JoinBwdArgs& a, cudaStream_t s) {
   }
   if (a.dpost_gamma == nullptr && a.dpost_beta == nullptr && a.dgate == nullptr && a.dgamma == nullptr && a.dbeta == nullptr)
     return cudaSuccess;
-  k_join_bwd_params<<<unsigned((a.cols + 31) / 32), 256, 0, s>>>(a, partials, sums);
+  k_join_bwd_params<<<unsigned((a.cols + 31) / 32), 1024, 0, s>>>(a, partials, sums);
   return cudaGetLastError();
 }
 

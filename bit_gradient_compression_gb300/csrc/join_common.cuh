@@ -18,72 +18,88 @@ namespace {
 template <int G>
 constexpr int kTeamCta = G < 128 ? 128 : G;  // threads of a CTA
 
-// Columns in vectors of eight, of a type known when compiled.
+// Warps of an SM that a kernel's registers are fitted for (32: 64 registers a thread).
+template <int G, bool LEAN>
+constexpr int kWarpsWanted = G == 32 ? 12 : LEAN ? 32 : 16;
+
+// Pairs of the values of eight columns from their 16-byte words.
+template <bool BF16>
+__device__ __forceinline__ void words_to_pairs(const uint4 (&w)[BF16 ? 1 : 2], Pair* v) {
+  if constexpr (BF16) {
+    v[0] = widen(w[0].x), v[1] = widen(w[0].y), v[2] = widen(w[0].z), v[3] = widen(w[0].w);
+  } else {
+    v[0] = pair(__uint_as_float(w[0].x), __uint_as_float(w[0].y)), v[1] = pair(__uint_as_float(w[0].z), __uint_as_float(w[0].w));
+    v[2] = pair(__uint_as_float(w[1].x), __uint_as_float(w[1].y)), v[3] = pair(__uint_as_float(w[1].z), __uint_as_float(w[1].w));
+  }
+}
+
+// Columns in vectors of eight, of a type known when compiled.  A row on its way lies in shared memory: a thread
+// copies its own vectors there (cp.async; nobody else reads them, so no barrier is needed), the one that the row
+// ends in and those behind it element by element, as zeros past the end.
 template <int G, int E, bool BF16>
 struct Vec {
   static constexpr bool kWide = true, kShort = BF16;
-  static constexpr int kRaw = E / 8 * (BF16 ? 1 : 2);
-  uint4 w[kRaw];
+  static constexpr int kElem = BF16 ? 2 : 4, kPieces = E / 8 * (BF16 ? 1 : 2), kBytes = kPieces * 16;  // of a thread and row
+  uint32_t at;  // its first piece in shared memory; pieces lie a CTA's threads apart
 
   __device__ static __forceinline__ int column(int t, int i) { return (t + G * (i / 8)) * 8 + i % 8; }
 
   __device__ __forceinline__ void load(const void* p, int64_t row, int64_t ld, int t, int cols, int) {
-    const char* q = static_cast<const char*>(p) + row * ld * (BF16 ? 2 : 4);
+    const char* q = static_cast<const char*>(p) + row * ld * kElem;
 #pragma unroll
     for (int e = 0; e < E / 8; ++e) {
       const int c0 = (t + G * e) * 8;
+      const uint32_t to = at + e * (kPieces / (E / 8)) * (kTeamCta<G> * 16);
       if (c0 + 8 <= cols) {
-        const uint4* v = reinterpret_cast<const uint4*>(q + c0 * (BF16 ? 2 : 4));
-#pragma unroll
-        for (int k = 0; k < (BF16 ? 1 : 2); ++k) w[e * (BF16 ? 1 : 2) + k] = __ldcs(v + k);
+        copy_to_shared16(to, q + c0 * kElem);
+        if (!BF16) copy_to_shared16(to + kTeamCta<G> * 16, q + c0 * kElem + 16);
       } else {
         float f[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] = c0 + k < cols ? load_elem_rw(q, c0 + k, BF16) : 0.0f;
         if (BF16) {
-          w[e] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          to_shared16(to, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
         } else {
-          w[2 * e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-          w[2 * e + 1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+          to_shared16(to, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+          to_shared16(to + kTeamCta<G> * 16,
+                      make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
         }
       }
     }
   }
-  __device__ __forceinline__ void values(float (&v)[E]) const {
+  __device__ __forceinline__ void values(Pair (&v)[E / 2]) const {
 #pragma unroll
     for (int e = 0; e < E / 8; ++e) {
-      if (BF16) {
-        const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+      uint4 w[BF16 ? 1 : 2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[e * 8 + 2 * k] = bf16lo_to_f32(u[k]), v[e * 8 + 2 * k + 1] = bf16hi_to_f32(u[k]);
-      } else {
-        const uint32_t u[8] = {w[2 * e].x, w[2 * e].y, w[2 * e].z, w[2 * e].w,
-                               w[2 * e + 1].x, w[2 * e + 1].y, w[2 * e + 1].z, w[2 * e + 1].w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[e * 8 + k] = __uint_as_float(u[k]);
-      }
+      for (int k = 0; k < (BF16 ? 1 : 2); ++k) w[k] = shared16(at + (e * (BF16 ? 1 : 2) + k) * (kTeamCta<G> * 16));
+      words_to_pairs<BF16>(w, v + e * 4);
     }
   }
-  __device__ static __forceinline__ void store(void* p, int64_t row, int64_t ld, int t, int cols, int, const float (&v)[E]) {
-    char* q = static_cast<char*>(p) + row * ld * (BF16 ? 2 : 4);
+  __device__ static __forceinline__ void store(void* p, int64_t row, int64_t ld, int t, int cols, int, const Pair (&v)[E / 2]) {
+    char* q = static_cast<char*>(p) + row * ld * kElem;
 #pragma unroll
     for (int e = 0; e < E / 8; ++e) {
       const int c0 = (t + G * e) * 8;
+      float f[8];
+      floats8(v + e * 4, f);
       if (c0 + 8 <= cols) {
-        store8(q, c0, BF16, v + e * 8);
+        store8(q, c0, BF16, f);
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (c0 + k < cols) store_elem(q, c0 + k, BF16, v[e * 8 + k]);
+          if (c0 + k < cols) store_elem(q, c0 + k, BF16, f[k]);
       }
     }
   }
 };
 
-// Single columns, of a type known at run time.
+// Single columns, of a type known at run time.  A row on its way is in registers.
 template <int G, int E>
 struct Cols {
   static constexpr bool kWide = false, kShort = false;
+  static constexpr int kBytes = 0;
+  uint32_t at;
   float f[E];
 
   __device__ static __forceinline__ int column(int t, int i) { return t + G * i; }
@@ -98,20 +114,26 @@ struct Cols {
       for (int i = 0; i < E; ++i) f[i] = t + G * i < cols ? load_elem_rw(q, t + G * i, 0) : 0.0f;
     }
   }
-  __device__ __forceinline__ void values(float (&v)[E]) const {
+  __device__ __forceinline__ void values(Pair (&v)[E / 2]) const {
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = f[i];
+    for (int i = 0; i < E / 2; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
   }
-  __device__ static __forceinline__ void store(void* p, int64_t row, int64_t ld, int t, int cols, int bf16, const float (&v)[E]) {
+  __device__ static __forceinline__ void store(void* p, int64_t row, int64_t ld, int t, int cols, int bf16, const Pair (&v)[E / 2]) {
     char* q = static_cast<char*>(p) + row * ld * (bf16 ? 2 : 4);
+    float x[E];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 h = halves(v[i]);
+      x[2 * i] = h.x, x[2 * i + 1] = h.y;
+    }
     if (bf16) {
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (t + G * i < cols) store_elem(q, t + G * i, 1, v[i]);
+        if (t + G * i < cols) store_elem(q, t + G * i, 1, x[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (t + G * i < cols) store_elem(q, t + G * i, 0, v[i]);
+        if (t + G * i < cols) store_elem(q, t + G * i, 0, x[i]);
     }
   }
 };
@@ -119,7 +141,8 @@ struct Cols {
 // A vector of parameters at a thread's columns: `none` where it is not given, `past` behind the row's end.
 // wide: it takes 16-byte loads.
 template <typename Row, int E>
-__device__ __forceinline__ void params(const void* p, int t, int cols, int bf16, bool wide, float none, float past, float (&v)[E]) {
+__device__ __forceinline__ void params(const void* p, int t, int cols, int bf16, bool wide, float none, float past, Pair* out) {
+  float v[E];
   if (Row::kWide && wide && p != nullptr && Row::column(t, E - 1) < cols) {
 #pragma unroll
     for (int e = 0; e < E / 8; ++e) load8(p, Row::column(t, e * 8), bf16, v + e * 8);
@@ -130,17 +153,45 @@ __device__ __forceinline__ void params(const void* p, int t, int cols, int bf16,
       v[i] = c < cols ? (p != nullptr ? load_elem(p, c, bf16) : none) : past;
     }
   }
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) out[i] = pair(v[2 * i], v[2 * i + 1]);
 }
 
-// Value rounded to the type it is stored in.
-__device__ __forceinline__ float as_stored(float v, int bf16) {
-  return bf16 ? bf16_bits_to_f32(uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(v)))) : v;
+// Values rounded to the type they are stored in.
+__device__ __forceinline__ Pair as_stored(Pair v, int bf16) {
+  if (!bf16) return v;
+  const float2 h = halves(v);
+  return widen(pack_bf16x2(h.x, h.y));
+}
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ float total(Pair v) {
+  const float2 h = halves(v);
+  return h.x + h.y;
 }
 
 __device__ __forceinline__ float warp_total(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+
+// A thread's own E parameters in shared memory: pieces of four, a CTA's threads apart, the `which`-th vector of them.
+template <int E, int THREADS>
+__device__ __forceinline__ void keep(uint32_t at, int which, const Pair* v) {
+#pragma unroll
+  for (int i = 0; i < E / 2; i += 2) {
+    const float2 lo = halves(v[i]), hi = halves(v[i + 1]);
+    to_shared16(at + (which * (E / 4) + i / 2) * (THREADS * 16),
+                make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y)));
+  }
+}
+template <int E, int THREADS>
+__device__ __forceinline__ void recall(uint32_t at, int which, Pair* v) {
+#pragma unroll
+  for (int i = 0; i < E / 2; i += 2) {
+    const uint4 w = shared16(at + (which * (E / 4) + i / 2) * (THREADS * 16));
+    v[i] = pair(__uint_as_float(w.x), __uint_as_float(w.y)), v[i + 1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
 }
 
 // What a team's warps tell one another: N values of each.  Consecutive calls alternate between two areas, so
@@ -212,28 +263,21 @@ struct Counts {
 // deviations from that; together they make the row's mean, and the variance with what the warps' means are off it.
 // No difference of large sums: a row far from 0 loses no digits.  v is 0 past the row's end, of which cols columns
 // are this CTA's.
-template <typename Row, int G, int E, bool CL>
-__device__ __forceinline__ void layer_stats(Team<G, CL>& team, const float (&v)[E], int t, int cols, const Counts& n,
+template <typename Row, int E, int G, bool CL>
+__device__ __forceinline__ void layer_stats(Team<G, CL>& team, const Pair (&v)[E / 2], int t, int cols, const Counts& n,
                                             float* mean, float* var) {
-  float s0 = 0.0f, s1 = 0.0f;
+  Pair s2 = v[0], q2 = both(0.0f);
 #pragma unroll
-  for (int i = 0; i < E; i += 2) s0 += v[i], s1 += v[i + 1];
-  const float m = warp_total(s0 + s1) * n.inv_warp;
-  float q0 = 0.0f, q1 = 0.0f;
-  if (Row::column(t, E - 1) < cols) {
+  for (int i = 1; i < E / 2; ++i) s2 = s2 + v[i];
+  const float m = warp_total(total(s2)) * n.inv_warp;
+  const Pair less = both(-m);
 #pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const float a = v[i] - m, b = v[i + 1] - m;
-      q0 = fmaf(a, a, q0), q1 = fmaf(b, b, q1);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float a = Row::column(t, i) < cols ? v[i] - m : 0.0f;
-      q0 = fmaf(a, a, q0);
-    }
+  for (int i = 0; i < E / 2; ++i) {
+    Pair d = v[i] + less;
+    if (Row::column(t, 2 * i + 1) >= cols) d = pair(Row::column(t, 2 * i) < cols ? halves(d).x : 0.0f, 0.0f);
+    q2 = fma(d, d, q2);
   }
-  float w[2] = {m, warp_total(q0 + q1)};
+  float w[2] = {m, warp_total(total(q2))};
   if constexpr (G > 32) {
     constexpr int kW = G / 32, kEntries = CL ? kMaxCluster * kW / 32 : 1;
     const int lane = threadIdx.x & 31;
@@ -315,12 +359,13 @@ inline int64_t team_ctas(int64_t rows, int cap, int teams, int ctas) {
   return want < cap ? want : cap;
 }
 template <typename Args>
-cudaError_t launch_teams(void (*kernel)(Args, bool), int64_t rows, int cap, int threads, int teams, int ctas, cudaStream_t s,
-                         const Args& a, bool pwide) {
+cudaError_t launch_teams(void (*kernel)(Args, bool), int64_t rows, int cap, int threads, int teams, int ctas, size_t smem,
+                         cudaStream_t s, const Args& a, bool pwide) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   cfg.gridDim = dim3(unsigned(team_ctas(rows, cap, teams, ctas)));
   cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   if (ctas > 1) {
     attr.id = cudaLaunchAttributeClusterDimension;

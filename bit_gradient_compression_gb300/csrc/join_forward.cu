@@ -13,14 +13,24 @@ namespace loco {
 
 namespace {
 
+// Rows on their way: the one at work and the next.  Behind them a thread's own gamma and beta lie in shared memory,
+// where it alone reads them: in registers they would cost every second CTA of an SM.
+constexpr int kStages = 2;
+template <int G, int E, typename RowX, typename RowY>
+constexpr size_t kRing = size_t(kTeamCta<G>) * (kStages * (RowX::kBytes + RowY::kBytes) + 2 * E * sizeof(float));
+
 template <int G, int E, bool CL, typename RowX, typename RowY>
-__global__ void __launch_bounds__(kTeamCta<G>) k_join_fwd(const JoinFwdArgs args, bool pwide) {
+__global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort> * 32 / kTeamCta<G>)
+    k_join_fwd(const JoinFwdArgs args, bool pwide) {
   __shared__ Board<G, CL> board;
-  constexpr int kTeams = kTeamCta<G> / G;
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>;
   JoinFwdArgs a = args;
   const int t = threadIdx.x % G, place = threadIdx.x / G;
   Team<G, CL> team{&board, 0, 1, 0};
-  int64_t c0 = 0, first = int64_t(blockIdx.x) * kTeams + place, step = int64_t(gridDim.x) * kTeams;
+  int64_t c0 = 0;
+  uint32_t first = blockIdx.x * kTeams + place, step = gridDim.x * kTeams;  // (rows are below 2^31)
+  const uint32_t n_rows = uint32_t(a.rows);
   if constexpr (CL) {
     const auto cluster = cooperative_groups::this_cluster();
     team.ctas = int(cluster.num_blocks()), team.rank = int(cluster.block_rank());
@@ -35,55 +45,78 @@ __global__ void __launch_bounds__(kTeamCta<G>) k_join_fwd(const JoinFwdArgs args
   const int64_t rest = a.cols - c0;
   const int cols = rest <= 0 ? 0 : rest < G * E ? int(rest) : G * E;
   const Counts n = row_counts<RowX, G, E, CL>(team, t, cols, a.cols);
-  const auto stats = [&](const float (&v)[E], float* mean, float* rstd) {
+  const auto stats = [&](const Pair (&v)[E / 2], float* mean, float* rstd) {
     float var;
     if (a.rms) {
-      float q[2] = {0.0f, 0.0f};
+      Pair q = v[0] * v[0];
 #pragma unroll
-      for (int i = 0; i < E; i += 2) q[0] = fmaf(v[i], v[i], q[0]), q[1] = fmaf(v[i + 1], v[i + 1], q[1]);
-      float s[1] = {q[0] + q[1]};
+      for (int i = 1; i < E / 2; ++i) q = fma(v[i], v[i], q);
+      float s[1] = {total(q)};
       team.sum(s);
       *mean = 0.0f, var = s[0] * n.inv_cols;
     } else {
-      layer_stats<RowX>(team, v, t, cols, n, mean, &var);
+      layer_stats<RowX, E>(team, v, t, cols, n, mean, &var);
     }
     *rstd = rsqrtf(var + a.eps);
   };
   // h = a x + w (yh pg + pb), pg and pb with the gate in them, 0 past the row's end
-  float pg[E], pb[E], gm[E], bt[E];
-  {
-    float g[E];
-    params<RowX>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, g);
-    params<RowX>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, pg);
-    params<RowX>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, pb);
+  Pair pg[E / 2], pb[E / 2], gm[E / 2];
+  params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, gm);
+  params<RowX, E>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, pg);
+  params<RowX, E>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, pb);
 #pragma unroll
-    for (int i = 0; i < E; ++i) pg[i] *= g[i], pb[i] *= g[i];
-  }
-  params<RowX>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, gm);
-  params<RowX>(a.beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, bt);
+  for (int i = 0; i < E / 2; ++i) pg[i] = pg[i] * gm[i], pb[i] = pb[i] * gm[i];
+  const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
+  constexpr uint32_t kStage = kThreadsCta * (RowX::kBytes + RowY::kBytes), kOwn = kStages * kStage;
+  params<RowX, E>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, gm);
+  keep<E, kThreadsCta>(base + kOwn, 0, gm);
+  params<RowX, E>(a.beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, gm);
+  keep<E, kThreadsCta>(base + kOwn, 1, gm);
   RowX xn;
   RowY yn;
-  const auto fetch = [&](int64_t row) {
-    if (row >= a.rows) return;
-    xn.load(a.x, row, a.ldx, t, cols, a.x_bf16);
-    yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
+  uint32_t slot = 0;
+  const auto fetch = [&](uint32_t row) {
+    xn.at = base + slot * kStage, yn.at = xn.at + kThreadsCta * RowX::kBytes;
+    if (row < n_rows) {
+      xn.load(a.x, row, a.ldx, t, cols, a.x_bf16);
+      yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
+    }
+    cp_async_commit();
+    slot ^= 1;
   };
   fetch(first);
-  for (int64_t row = first; row - (kTeams > 1 ? place : 0) < a.rows; row += step) {
-    const bool live = row < a.rows;  // (where it is not, the values are the last row's, and nothing is stored)
-    float x[E], y[E];
-    xn.values(x), yn.values(y);
-    fetch(row + step);
+  const Pair a2 = both(a.a);
+  for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
+    const bool live = row < n_rows;  // (where it is not, the values are an earlier row's, and nothing is stored)
+    Pair x[E / 2], y[E / 2];
+    if constexpr (RowX::kWide) {
+      RowX xc = xn;
+      RowY yc = yn;
+      fetch(row + step);
+      cp_async_wait<1>();
+      xc.values(x), yc.values(y);
+    } else {
+      xn.values(x), yn.values(y);
+      fetch(row + step);
+    }
     float m1 = 0.0f, r1 = 1.0f, m2 = 0.0f, r2 = 1.0f;
     if (a.post) stats(y, &m1, &r1);
-    const float w = a.s * (a.row_gate != nullptr && live ? __ldg(a.row_gate + row) : 1.0f);
+    const Pair w = both(a.s * (a.row_gate != nullptr && live ? __ldg(a.row_gate + row) : 1.0f));
+    const Pair l1 = both(-m1), f1 = both(r1);
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = as_stored(fmaf(w, fmaf((y[i] - m1) * r1, pg[i], pb[i]), a.a * x[i]), a.x_bf16);
+    for (int i = 0; i < E / 2; ++i) {
+      const Pair v = fma((y[i] + l1) * f1, pg[i], pb[i]);
+      x[i] = as_stored(fma(w, v, a2 * x[i]), a.x_bf16);
+    }
     if (live) RowX::store(a.h, row, a.ldh, t, cols, a.x_bf16, x);
     if (a.u != nullptr) {
       stats(x, &m2, &r2);
+      const Pair l2 = both(-m2), f2 = both(r2);
+      Pair g[E / 2], b[E / 2];
+      recall<E, kThreadsCta>(base + kOwn, 0, g);
+      recall<E, kThreadsCta>(base + kOwn, 1, b);
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = fmaf((x[i] - m2) * r2, gm[i], bt[i]);
+      for (int i = 0; i < E / 2; ++i) x[i] = fma((x[i] + l2) * f2, g[i], b[i]);
       if (live) RowY::store(a.u, row, a.ldu, t, cols, a.y_bf16, x);
     }
     if (a.stats != nullptr && t == 0 && live && team.rank == 0) {
@@ -150,9 +183,11 @@ cudaError_t run(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
   static LayerGrid grid;
   int cap = 0;
   const void* kernel = reinterpret_cast<const void*>(&k_join_fwd<G, E, CL, RowX, RowY>);
-  const cudaError_t e = layer_grid(grid, kernel, kTeamCta<G>, 0, 0, &cap);
+  constexpr size_t kSmem = kRing<G, E, RowX, RowY>;
+  const cudaError_t e = layer_grid(grid, kernel, kTeamCta<G>, kSmem, kSmem, &cap);
   if (e != cudaSuccess) return e;
-  return launch_teams(k_join_fwd<G, E, CL, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeamCta<G> / G, ctas, s, a, pwide);
+  return launch_teams(k_join_fwd<G, E, CL, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeamCta<G> / G, ctas, kSmem, s, a,
+                      pwide);
 }
 template <int G, int E, bool CL>
 cudaError_t run_vec(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {

@@ -17,7 +17,7 @@
 #include "loco.h"
 
 static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_is_contiguous;
-static PyObject *t_f32, *t_bf16, *t_i8, *t_u8; /* torch's dtype objects, set by init() */
+static PyObject *t_f32, *t_bf16, *t_i8, *t_u8, *t_i64; /* torch's dtype objects, set by init() */
 static double align_work;                        /* loco.py's ALIGN_WORK and ALIGN_ROWS, set by init() */
 static int64_t align_rows;
 
@@ -326,16 +326,129 @@ static PyObject* linear_backward_weight(PyObject* self, PyObject* const* a, Py_s
                                            dw.ld, db, w, nw, st));
 }
 
-/* init(float32, bfloat16, int8, uint8, ALIGN_WORK, ALIGN_ROWS).  Until then every function returns None. */
+/* A contiguous tensor of the type `want` and of the shape [count], or [rows, count / rows] where rows is not 0. */
+static int whole(PyObject* t, PyObject* want, int64_t rows, int64_t count, void** p) {
+  int64_t v[2];
+  *p = NULL;
+  if (t == Py_None) return 1;
+  PyObject* d = PyObject_GetAttr(t, s_dtype);
+  Py_XDECREF(d);
+  if (d != want || !ints(PyObject_GetAttr(t, s_shape), rows ? 2 : 1, v)) return 0;
+  if (rows ? v[0] != rows || v[0] * v[1] != count : v[0] != count) return 0;
+  PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+  Py_XDECREF(c);
+  return c == Py_True && address(t, p);
+}
+
+/* (kind, post, eps, a, s, x, y, h, u, gamma, beta, post_gamma, post_beta, gate, row_gate, stats, stream) */
+static PyObject* join_forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  ARGS(17);
+  Mat x, y, h, u;
+  void *g, *b, *pg, *pb, *gate, *rg, *st;
+  int pd = -1, f = LOCO_F32;
+  WANT(a[5] != Py_None && a[6] != Py_None && a[7] != Py_None && mat(a[5], -1, -1, &x) && mat(a[6], x.rows, x.cols, &y));
+  WANT(mat(a[7], x.rows, x.cols, &h) && mat(a[8], x.rows, x.cols, &u));
+  WANT(vec(a[9], x.cols, &pd, &g) && vec(a[10], x.cols, &pd, &b) && vec(a[11], x.cols, &pd, &pg));
+  WANT(vec(a[12], x.cols, &pd, &pb) && vec(a[13], x.cols, &pd, &gate) && vec(a[14], x.rows, &f, &rg));
+  WANT(whole(a[15], t_f32, 4, 4 * x.rows, &st));
+  const loco_join_config cfg = {(int32_t)integer(a[0]), (int32_t)integer(a[1]), (float)PyFloat_AsDouble(a[2]),
+                                (float)PyFloat_AsDouble(a[3]), (float)PyFloat_AsDouble(a[4]), one(x.dtype, h.dtype),
+                                one(y.dtype, u.dtype), or_f32(pd), LOCO_F32};
+  const loco_stream_t stream = STREAM(a[16]);
+  WANT(cfg.x_dtype >= 0 && cfg.y_dtype >= 0);
+  CALL(loco_join_forward(&cfg, x.p, x.ld, y.p, y.ld, x.rows, x.cols, pg, pb, gate, rg, g, b, h.p, h.ld, u.p, u.ld, st,
+                         stream));
+}
+
+/* (kind, post, eps, a, s, dh, du, h, y, stats, dx, dy, gamma, post_gamma, post_beta, gate, row_gate, dgamma, dbeta,
+   dpost_gamma, dpost_beta, dgate, drow_gate, workspace, stream) */
+static PyObject* join_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  ARGS(25);
+  Mat dh, du, h, y, dx, dy;
+  void *st, *g, *pg, *pb, *gate, *rg, *dg, *db, *dpg, *dpb, *dgate, *drg, *w;
+  int64_t nw;
+  int pd = -1, gd = -1, f = LOCO_F32;
+  WANT(a[10] != Py_None && a[11] != Py_None && mat(a[10], -1, -1, &dx) && mat(a[11], dx.rows, dx.cols, &dy));
+  WANT(mat(a[5], dx.rows, dx.cols, &dh) && mat(a[6], dx.rows, dx.cols, &du) && mat(a[7], dx.rows, dx.cols, &h));
+  WANT(mat(a[8], dx.rows, dx.cols, &y) && whole(a[9], t_f32, 4, 4 * dx.rows, &st));
+  WANT(vec(a[12], dx.cols, &pd, &g) && vec(a[13], dx.cols, &pd, &pg) && vec(a[14], dx.cols, &pd, &pb));
+  WANT(vec(a[15], dx.cols, &pd, &gate) && vec(a[16], dx.rows, &f, &rg) && vec(a[17], dx.cols, &gd, &dg));
+  WANT(vec(a[18], dx.cols, &gd, &db) && vec(a[19], dx.cols, &gd, &dpg) && vec(a[20], dx.cols, &gd, &dpb));
+  WANT(vec(a[21], dx.cols, &gd, &dgate) && vec(a[22], dx.rows, &f, &drg) && bytes_of(a[23], &w, &nw));
+  const loco_join_config cfg = {(int32_t)integer(a[0]), (int32_t)integer(a[1]), (float)PyFloat_AsDouble(a[2]),
+                                (float)PyFloat_AsDouble(a[3]), (float)PyFloat_AsDouble(a[4]),
+                                one(one(dh.dtype, h.dtype), dx.dtype), one(one(du.dtype, y.dtype), dy.dtype), or_f32(pd),
+                                or_f32(gd)};
+  const loco_stream_t stream = STREAM(a[24]);
+  WANT(cfg.x_dtype >= 0 && cfg.y_dtype >= 0);
+  CALL(loco_join_backward(&cfg, dh.p, dh.ld, du.p, du.ld, h.p, h.ld, y.p, y.ld, st, dx.rows, dx.cols, pg, pb, gate, rg, g,
+                          dx.p, dx.ld, dy.p, dy.ld, dpg, dpb, dgate, drg, dg, db, w, nw, stream));
+}
+
+/* (logits, targets, logp, lse, entropy, top_ids, top_logp, scale, stream) */
+static PyObject* logprob_forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  ARGS(9);
+  Mat z;
+  void *y, *lp, *lse, *h, *ids, *alts;
+  int64_t v[2], top = 0;
+  int f = LOCO_F32;
+  WANT(a[0] != Py_None && mat(a[0], -1, -1, &z) && whole(a[1], t_i64, 0, z.rows, &y));
+  WANT(vec(a[2], z.rows, &f, &lp) && vec(a[3], z.rows, &f, &lse) && vec(a[4], z.rows, &f, &h));
+  for (int i = 5; i < 7; ++i) {
+    if (a[i] == Py_None) continue;
+    WANT(ints(PyObject_GetAttr(a[i], s_shape), 2, v) && (i == 5 || a[5] == Py_None || v[1] == top));
+    top = v[1];
+  }
+  WANT(z.rows > 0 && top <= LOCO_MAX_TOP && whole(a[5], t_i64, z.rows, z.rows * top, &ids) &&
+       whole(a[6], t_f32, z.rows, z.rows * top, &alts));
+  const float scale = (float)PyFloat_AsDouble(a[7]);
+  const loco_stream_t stream = STREAM(a[8]);
+  WANT(1);
+  CALL(loco_logprob_forward(z.p, z.dtype, z.ld, z.rows, z.cols, scale, y, lp, lse, h, (int32_t)top, ids, alts, stream));
+}
+
+/* (logits, targets, lse, dlogits, dlogp, entropy, dentropy, scale, stream) */
+static PyObject* logprob_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  ARGS(9);
+  Mat z, dz;
+  void *y, *lse, *dl, *h, *dh;
+  int f = LOCO_F32;
+  WANT(a[0] != Py_None && a[3] != Py_None && mat(a[0], -1, -1, &z) && mat(a[3], z.rows, z.cols, &dz));
+  WANT(z.dtype == dz.dtype && whole(a[1], t_i64, 0, z.rows, &y) && vec(a[2], z.rows, &f, &lse));
+  WANT(vec(a[4], z.rows, &f, &dl) && vec(a[5], z.rows, &f, &h) && vec(a[6], z.rows, &f, &dh));
+  const float scale = (float)PyFloat_AsDouble(a[7]);
+  const loco_stream_t stream = STREAM(a[8]);
+  WANT(1);
+  CALL(loco_logprob_backward(z.p, z.dtype, z.ld, z.rows, z.cols, scale, y, lse, h, dl, dh, dz.p, dz.ld, stream));
+}
+
+/* (codes, steps, out, stream), all of one dimension */
+static PyObject* adam_state_decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  ARGS(4);
+  void *c, *s, *o;
+  int64_t count;
+  int od = -1;
+  WANT(a[0] != Py_None && a[1] != Py_None && a[2] != Py_None && ints(PyObject_GetAttr(a[2], s_shape), 1, &count));
+  const int64_t nb = (count + LOCO_STATE_BLOCK - 1) / LOCO_STATE_BLOCK;
+  PyObject* d = PyObject_GetAttr(a[0], s_dtype);
+  Py_XDECREF(d);
+  WANT(d == t_i8 || d == t_u8);
+  WANT(whole(a[0], d, 0, nb * LOCO_STATE_BLOCK, &c) && whole(a[1], t_f32, 0, nb, &s) && vec(a[2], count, &od, &o));
+  const loco_stream_t stream = STREAM(a[3]);
+  WANT(1);
+  CALL(loco_adam_state_decode(d == t_u8 ? LOCO_STATE_V : LOCO_STATE_M, c, s, count, o, od, stream));
+}
+
+/* init(float32, bfloat16, int8, uint8, int64, ALIGN_WORK, ALIGN_ROWS).  Until then every function returns None. */
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "four dtypes and two numbers");
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "five dtypes and two numbers");
     return NULL;
   }
-  align_work = PyFloat_AsDouble(a[4]), align_rows = integer(a[5]);
+  align_work = PyFloat_AsDouble(a[5]), align_rows = integer(a[6]);
   if (PyErr_Occurred()) return NULL;
-  PyObject** to[4] = {&t_f32, &t_bf16, &t_i8, &t_u8};
-  for (int i = 0; i < 4; ++i) {
+  PyObject** to[5] = {&t_f32, &t_bf16, &t_i8, &t_u8, &t_i64};
+  for (int i = 0; i < 5; ++i) {
     Py_INCREF(a[i]);
     Py_XSETREF(*to[i], a[i]);
   }
@@ -346,6 +459,8 @@ static PyMethodDef methods[] = {
 #define METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
     METHOD(init),          METHOD(ckpt_encode),    METHOD(ckpt_decode),           METHOD(norm_forward),
     METHOD(norm_backward), METHOD(linear_forward), METHOD(linear_backward_input), METHOD(linear_backward_weight),
+    METHOD(join_forward),  METHOD(join_backward),  METHOD(logprob_forward),       METHOD(logprob_backward),
+    METHOD(adam_state_decode),
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -327,7 +327,8 @@ try:
 except ImportError:
     class _marshal:  # built without Python's headers
         init = ckpt_encode = ckpt_decode = norm_forward = norm_backward = linear_forward = staticmethod(lambda *a: None)
-        linear_backward_input = linear_backward_weight = init
+        linear_backward_input = linear_backward_weight = join_forward = join_backward = logprob_forward = init
+        logprob_backward = adam_state_decode = init
 
 _DTYPES: dict = {}  # torch.dtype -> loco_dtype, filled on first use (torch is imported only then)
 
@@ -335,7 +336,7 @@ _DTYPES: dict = {}  # torch.dtype -> loco_dtype, filled on first use (torch is i
 def _dtypes():
     import torch
     _DTYPES.update({torch.float32: LOCO_F32, torch.bfloat16: LOCO_BF16})
-    _marshal.init(torch.float32, torch.bfloat16, torch.int8, torch.uint8, ALIGN_WORK, ALIGN_ROWS)
+    _marshal.init(torch.float32, torch.bfloat16, torch.int8, torch.uint8, torch.int64, ALIGN_WORK, ALIGN_ROWS)
     return _DTYPES
 
 
@@ -657,6 +658,10 @@ def loco_join_forward(cfg: loco_join_config, x, y, h, u=None, *, gamma=None, bet
                       gate=None, row_gate=None, stats=None, stream=None):
     """h = residual_scale x + block_scale row_gate gate norm(y), u = norm(h): both norms with their own parameters
     (without post, y itself; without u, no second norm).  stats [4, rows]: what the backward pass needs."""
+    status = _marshal.join_forward(cfg.kind, cfg.post, cfg.eps, cfg.residual_scale, cfg.block_scale, x, y, h, u, gamma, beta,
+                                   post_gamma, post_beta, gate, row_gate, stats, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     rows, cols = _dims(x, "x")
     px, ldx = _mat(x, "x", rows, cols)
     py, ldy = _mat(y, "y", rows, cols)
@@ -679,6 +684,11 @@ def loco_join_backward(cfg: loco_join_config, dh, du, h, y, stats, dx, dy, *, ga
                        drow_gate=None, workspace=None, stream=None):
     """Gradients of loco_join_forward: dx of the stream, dy of the block's output, and those of the parameters that
     are given.  dh or du may be None (zeros)."""
+    status = _marshal.join_backward(cfg.kind, cfg.post, cfg.eps, cfg.residual_scale, cfg.block_scale, dh, du, h, y, stats,
+                                    dx, dy, gamma, post_gamma, post_beta, gate, row_gate, dgamma, dbeta, dpost_gamma,
+                                    dpost_beta, dgate, drow_gate, workspace, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     rows, cols = _dims(dx, "dx")
     pdh, lddh = _mat(dh, "dh", rows, cols)
     pdu, lddu = _mat(du, "du", rows, cols)
@@ -712,6 +722,9 @@ def loco_logprob_forward(logits, targets, logp, *, lse=None, entropy=None, top_i
                          stream=None):
     """Log probabilities of the given tokens under softmax(scale * logits) [rows, vocab], with the rows' log sums, their
     entropies and, where top_ids and top_logp [rows, top] are given, the most likely tokens."""
+    status = _marshal.logprob_forward(logits, targets, logp, lse, entropy, top_ids, top_logp, scale, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     rows, vocab = _dims(logits, "logits")
     pz, ld = _mat(logits, "logits", rows, vocab)
     top = 0
@@ -732,6 +745,9 @@ def loco_logprob_forward(logits, targets, logp, *, lse=None, entropy=None, top_i
 def loco_logprob_backward(logits, targets, lse, dlogits, *, dlogp=None, entropy=None, dentropy=None, scale: float = 1.0,
                           stream=None):
     """dlogits (may be the logits) for the gradients of logp and of the entropies; lse and entropy from the forward pass."""
+    status = _marshal.logprob_backward(logits, targets, lse, dlogits, dlogp, entropy, dentropy, scale, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     rows, vocab = _dims(logits, "logits")
     pz, ld = _mat(logits, "logits", rows, vocab)
     pd, ldd = _mat(dlogits, "dlogits", rows, vocab)
@@ -803,6 +819,9 @@ def loco_adam_tensors(tensors: AdamTensors, hp: loco_adam_hparams, t: int, *, gr
 
 def loco_adam_state_decode(codes, steps, out, *, stream=None):
     """out [n] (fp32 or bf16) = the values of an 8-bit state: int8 codes of a first moment, uint8 codes of a second."""
+    status = _marshal.adam_state_decode(codes, steps, out, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     import torch
     kind = {torch.int8: LOCO_STATE_M, torch.uint8: LOCO_STATE_V}.get(codes.dtype)
     if kind is None:
