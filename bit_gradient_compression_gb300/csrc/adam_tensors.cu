@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kUnit = LOCO_STATE_BLOCK;
 constexpr int kThreadsAdam = 256;
-constexpr int kGroup = 8;  // consecutive units of a warp
+constexpr int kGroup = 8;  // most consecutive units of a warp
 
 struct Elem4 {
   float f[4];
@@ -52,37 +52,41 @@ __device__ __forceinline__ uint32_t bf16_dithered(float p, uint32_t r) {
   return p == p ? (b + (r >> 16)) >> 16 : (b >> 16) | 0x40u;
 }
 
-// One code of a state under 1/step; `least` is the smallest code (with the rounding's offset).
-__device__ __forceinline__ uint32_t state_code(float value, float inv, float d, bool dither, uint32_t least) {
-  float x = __fmul_rn(value, inv);
-  if (dither) x = __fadd_rn(x, d);
-  const uint32_t q = __float_as_uint(__fadd_rn(x, kRoundMagic));
-  return least ? max(q, least) : q;
-}
-// d of a byte of the random bits: (b - 127.5) / 256, exact.
-__device__ __forceinline__ float dither_of(uint32_t r, int byte) {
-  const float b = __uint_as_float(__byte_perm(r, kTwo23Bits, 0x7440 | byte)) - 8388608.0f;
-  return (b - 127.5f) * 0.00390625f;
+// Products of pairs that feed sums: a packed product alone would be joined with the sum into one rounding, a fused
+// one with -0 (which the compiler does not know) is rounded like a product and stays.
+struct Rounded {
+  Pair none;
+  __device__ __forceinline__ Pair mul(Pair a, Pair b) const { return fma(a, b, none); }
+};
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+
+// d = (b - 127.5) / 256 of byte 0 or 1 of the random bits, exact: 2b + 1 in the low bits of 2^14, whose last place is
+// 2^-9, less 2^14 + 1/2.
+__device__ __forceinline__ Pair dither_of(uint32_t r0, uint32_t r1, int byte) {
+  const uint32_t u0 = byte ? r0 >> 7 : r0 << 1, u1 = byte ? r1 >> 7 : r1 << 1;
+  return pair(__uint_as_float((u0 & 0x1FEu) | 0x46800001u), __uint_as_float((u1 & 0x1FEu) | 0x46800001u)) + both(-16384.5f);
 }
 
-// 1/step and the step of a block whose largest magnitude has the bits `top`, for `most` codes.
-__device__ __forceinline__ void state_step(uint32_t top, float most, float* inv, float* step, bool* bad) {
+// 1/step and the step of a block whose largest magnitude has the bits `top`, for `most` codes: 1/step is 0 for a block
+// that is held as zeros, or as NaN.
+__device__ __forceinline__ void state_step(uint32_t top, float most, float* inv, float* step) {
   const float a = __uint_as_float(top);
-  *bad = top >= 0x7F800000u;
+  const bool bad = top >= 0x7F800000u;
   const float i = __fdiv_rn(most, a);
-  const bool some = !*bad && i <= 3.402823466e38f;  // (0 and what is too small for 1/step: zeros)
+  const bool some = !bad && i <= 3.402823466e38f;  // (0 and what is too small for 1/step: zeros)
   *inv = some ? i : 0.0f;
-  *step = *bad ? __uint_as_float(0x7FC00000u) : some ? __fdiv_rn(a, most) : 0.0f;
+  *step = bad ? __uint_as_float(0x7FC00000u) : some ? __fdiv_rn(a, most) : 0.0f;
 }
 
 template <int BITS, bool PBF16, bool GBF16, bool DITHER, int MAX>
-__global__ void __launch_bounds__(kThreadsAdam) k_adam_tensors(const __grid_constant__ AdamTensorList<MAX> l) {
+__global__ void __launch_bounds__(kThreadsAdam, PBF16 && DITHER ? 2 : 3) k_adam_tensors(const __grid_constant__ AdamTensorList<MAX> l, int group) {
   const int lane = threadIdx.x & 31;
   const uint32_t units = l.first[l.count];
   const uint32_t warps = gridDim.x * (kThreadsAdam / 32);
   const float scale = l.a.grad_scale != nullptr ? __ldg(l.a.grad_scale) : 1.0f;
-  for (uint64_t u0 = uint64_t(blockIdx.x * (kThreadsAdam / 32) + threadIdx.x / 32) * kGroup; u0 < units;
-       u0 += uint64_t(warps) * kGroup) {
+  const Rounded rn{both(l.a.neg_zero)};
+  for (uint64_t u0 = uint64_t(blockIdx.x * (kThreadsAdam / 32) + threadIdx.x / 32) * group; u0 < units;
+       u0 += uint64_t(warps) * group) {
     int lo = 0, hi = l.count;  // first[lo] <= u0 < first[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(kThreadsAdam) k_adam_tensors(const __grid_cons
       else
         hi = mid;
     }
-    const uint32_t end = uint32_t(u0 + kGroup < units ? u0 + kGroup : units);
+    const uint32_t end = uint32_t(u0 + group < units ? u0 + group : units);
     for (uint32_t u = uint32_t(u0); u < end; ++u) {
       while (u >= l.first[lo + 1]) ++lo;
       const AdamTensor& t = l.t[lo];
@@ -99,8 +103,8 @@ __global__ void __launch_bounds__(kThreadsAdam) k_adam_tensors(const __grid_cons
       const int64_t e0 = int64_t(b) * kUnit;
       const int left = t.n - e0 < kUnit ? int(t.n - e0) : kUnit;
       const bool wide = t.wide && left == kUnit;
-      // element j of a lane: lane * 4 + j % 4 + j / 4 * 128 (wide), else lane + 32 * j
-      float p[8], g[8], m[8], v[8], root[8];
+      // element j of a lane: lane * 4 + j % 4 + j / 4 * 128 (wide), else lane + 32 * j; past the end everything is 0
+      float p[8], g[8], m[8], v[8];
       if (wide) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -127,9 +131,10 @@ __global__ void __launch_bounds__(kThreadsAdam) k_adam_tensors(const __grid_cons
           }
         }
       }
+      Pair ms{}, vs{};
       if constexpr (BITS == 8) {
-        const float ms = t.m_steps[b], vs = t.v_steps[b];
-        uint32_t mc[8], vc[8];
+        ms = both(t.m_steps[b]), vs = both(t.v_steps[b]);
+        // codes under the exponent of 2^23: the floats 2^23 + code (and 128 for a signed one)
         if (wide) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -138,34 +143,50 @@ __global__ void __launch_bounds__(kThreadsAdam) k_adam_tensors(const __grid_cons
             const uint32_t vw = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              mc[q * 4 + k] = __byte_perm(mw, kTwo23Bits, 0x7440 | k);
-              vc[q * 4 + k] = __byte_perm(vw, kTwo23Bits, 0x7440 | k);
+              m[q * 4 + k] = __uint_as_float(__byte_perm(mw, kTwo23Bits, 0x7440 | k));
+              v[q * 4 + k] = __uint_as_float(__byte_perm(vw, kTwo23Bits, 0x7440 | k));
             }
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            mc[j] = kTwo23Bits | (static_cast<const uint8_t*>(t.m)[e0 + lane + 32 * j] ^ 0x80u);
-            vc[j] = kTwo23Bits | static_cast<const uint8_t*>(t.v)[e0 + lane + 32 * j];
+            m[j] = __uint_as_float(kTwo23Bits | (static_cast<const uint8_t*>(t.m)[e0 + lane + 32 * j] ^ 0x80u));
+            v[j] = __uint_as_float(kTwo23Bits | static_cast<const uint8_t*>(t.v)[e0 + lane + 32 * j]);
           }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          m[j] = __fmul_rn(__uint_as_float(mc[j]) - 8388736.0f, ms);
-          const float s = __fmul_rn(__uint_as_float(vc[j]) - 8388608.0f, vs);
-          v[j] = __fmul_rn(s, s);
-        }
       }
+      float root[8];
+      uint32_t mtop = 0, vtop = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        g[j] = __fmul_rn(g[j], scale);
-        p[j] = __fsub_rn(p[j], __fmul_rn(t.lr_wd, p[j]));
-        m[j] = __fadd_rn(__fmul_rn(l.a.beta1, m[j]), __fmul_rn(l.a.one_minus_beta1, g[j]));
-        v[j] = __fadd_rn(__fmul_rn(l.a.beta2, v[j]), __fmul_rn(l.a.one_minus_beta2, __fmul_rn(g[j], g[j])));
-        if (BITS == 8 || !l.a.eps_inside_sqrt) root[j] = sqrt_zsel(v[j]);
-        const float den = l.a.eps_inside_sqrt ? sqrt_zsel(__fadd_rn(__fmul_rn(v[j], l.a.c2), l.a.eps))
-                                              : __fadd_rn(__fmul_rn(root[j], l.a.c2), l.a.eps);
-        p[j] = __fsub_rn(p[j], __fmul_rn(t.c1, div_zsel(m[j], den)));
+      for (int j = 0; j < 8; j += 2) {
+        Pair m2 = pair(m[j], m[j + 1]), v2 = pair(v[j], v[j + 1]), p2 = pair(p[j], p[j + 1]), g2 = pair(g[j], g[j + 1]);
+        if constexpr (BITS == 8) {
+          m2 = rn.mul(m2 + both(-8388736.0f), ms);
+          v2 = rn.mul(v2 + both(-8388608.0f), vs);
+          v2 = rn.mul(v2, v2);
+        }
+        g2 = rn.mul(g2, both(scale));
+        p2 = p2 + rn.mul(both(-t.lr_wd), p2);
+        m2 = rn.mul(both(l.a.beta1), m2) + rn.mul(both(l.a.one_minus_beta1), g2);
+        v2 = rn.mul(both(l.a.beta2), v2) + rn.mul(both(l.a.one_minus_beta2), rn.mul(g2, g2));
+        const float2 mf = halves(m2), vf = halves(v2);
+        m[j] = mf.x, m[j + 1] = mf.y, v[j] = vf.x, v[j + 1] = vf.y;
+        if (BITS == 8 || !l.a.eps_inside_sqrt) root[j] = sqrt_zsel(vf.x), root[j + 1] = sqrt_zsel(vf.y);
+        Pair den;
+        if (l.a.eps_inside_sqrt) {
+          const float2 x = halves(rn.mul(v2, both(l.a.c2)) + both(l.a.eps));
+          den = pair(sqrt_zsel(x.x), sqrt_zsel(x.y));
+        } else {
+          den = rn.mul(pair(root[j], root[j + 1]), both(l.a.c2)) + both(l.a.eps);
+        }
+        const float2 df = halves(den);
+        p2 = p2 + rn.mul(both(-t.c1), pair(div_zsel(mf.x, df.x), div_zsel(mf.y, df.y)));
+        const float2 pf = halves(p2);
+        p[j] = pf.x, p[j + 1] = pf.y;
+        if constexpr (BITS == 8) {
+          mtop = max(mtop, max(mag_bits(mf.x), mag_bits(mf.y)));
+          vtop = max(vtop, max(__float_as_uint(root[j]), __float_as_uint(root[j + 1])) & 0x7FFFFFFFu);
+        }
       }
       uint32_t r[8];
       if constexpr (DITHER) {
@@ -175,27 +196,29 @@ __global__ void __launch_bounds__(kThreadsAdam) k_adam_tensors(const __grid_cons
           r[j] = mix32((uint32_t(e0) + (wide ? uint32_t(lane * 4 + j % 4 + j / 4 * 128) : uint32_t(lane + 32 * j))) ^ key);
       }
       if constexpr (BITS == 8) {
-        uint32_t mtop = 0, vtop = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // (past a tensor's end everything is 0)
-          mtop = max(mtop, mag_bits(m[j]));
-          vtop = max(vtop, mag_bits(root[j]));
-        }
         mtop = __reduce_max_sync(0xFFFFFFFFu, mtop);
         vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
         float minv, vinv, mstep, vstep;
-        bool mbad, vbad;
-        state_step(mtop, 127.0f, &minv, &mstep, &mbad);
-        state_step(vtop, 255.0f, &vinv, &vstep, &vbad);
-        constexpr uint32_t kZero = 0x4B400000u;
+        state_step(mtop, 127.0f, &minv, &mstep);
+        state_step(vtop, 255.0f, &vinv, &vstep);
         uint32_t mc[8], vc[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          mc[j] = state_code(m[j], minv, DITHER ? dither_of(r[j], 0) : 0.0f, DITHER, 0);
-          vc[j] = state_code(root[j], vinv, DITHER ? dither_of(r[j], 1) : 0.0f, DITHER, root[j] > 0.0f ? kZero + 1 : kZero);
-          if (mbad || minv == 0.0f) mc[j] = 0;
-          if (vbad || vinv == 0.0f) vc[j] = 0;
+        for (int j = 0; j < 8; j += 2) {
+          Pair x = rn.mul(pair(m[j], m[j + 1]), both(minv)), y = rn.mul(pair(root[j], root[j + 1]), both(vinv));
+          if constexpr (DITHER) x = x + dither_of(r[j], r[j + 1], 0), y = y + dither_of(r[j], r[j + 1], 1);
+          const float2 xf = halves(x + both(kRoundMagic)), yf = halves(y + both(kRoundMagic));
+          constexpr uint32_t kZero = 0x4B400000u;  // the bits of a rounded 0
+          mc[j] = __float_as_uint(xf.x), mc[j + 1] = __float_as_uint(xf.y);
+          vc[j] = max(__float_as_uint(yf.x), root[j] > 0.0f ? kZero + 1 : kZero);
+          vc[j + 1] = max(__float_as_uint(yf.y), root[j + 1] > 0.0f ? kZero + 1 : kZero);
+        }
+        if (minv == 0.0f) {  // a block held as zeros, or as NaN
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mc[j] = 0;
+        }
+        if (vinv == 0.0f) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) vc[j] = 0;
         }
         if (lane == 0) t.m_steps[b] = mstep, t.v_steps[b] = vstep;
         if (wide) {
@@ -264,9 +287,12 @@ cudaError_t run(const AdamTensorList<MAX>& l, cudaStream_t s) {
   const cudaError_t e =
       layer_grid(grid, reinterpret_cast<const void*>(&k_adam_tensors<BITS, PBF16, GBF16, DITHER, MAX>), kThreadsAdam, 0, 0, &cap);
   if (e != cudaSuccess) return e;
-  constexpr int64_t kCta = int64_t(kThreadsAdam / 32) * kGroup;
-  const int64_t want = (int64_t(l.first[l.count]) + kCta - 1) / kCta;
-  k_adam_tensors<BITS, PBF16, GBF16, DITHER, MAX><<<int(want < cap ? want : cap), kThreadsAdam, 0, s>>>(l);
+  // few units: one to a warp, before any warp takes a second
+  constexpr int64_t kCta = kThreadsAdam / 32;
+  const int64_t units = l.first[l.count], all = cap * kCta;
+  const int group = int(units >= all * kGroup ? kGroup : units <= all ? 1 : units / all);
+  const int64_t want = (units + kCta * group - 1) / (kCta * group);
+  k_adam_tensors<BITS, PBF16, GBF16, DITHER, MAX><<<int(want < cap ? want : cap), kThreadsAdam, 0, s>>>(l, group);
   return cudaGetLastError();
 }
 

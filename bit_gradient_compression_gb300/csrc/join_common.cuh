@@ -310,14 +310,16 @@ __device__ __forceinline__ void layer_stats(Team<G, CL>& team, const Pair (&v)[E
 // all: columns of the row, of which this CTA has `cols`.
 template <typename Row, int G, int E, bool CL>
 __device__ __forceinline__ Counts row_counts(const Team<G, CL>& team, int t, int cols, int64_t all) {
-  const auto of = [](int thread, int columns) {
+  // of the columns of one CTA, those of its warp: runs of 32 threads' columns, G threads' apart
+  const auto of = [](int warp, int columns) {
+    constexpr int kRun = Row::kWide ? 256 : 32, kApart = Row::kWide ? G * 8 : G;
     int k = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) k += Row::column(thread, i) < columns;
-    return k;
+    for (int i = 0; i < E * 32 / kRun; ++i) k += min(max(columns - (warp * kRun + i * kApart), 0), kRun);
+    return float(k);
   };
   Counts n;
-  const float w = warp_total(float(of(t, cols)));
+  const float w = of(t / 32, cols);
   n.inv_warp = w > 0.0f ? 1.0f / w : 0.0f;
   n.inv_cols = 1.0f / float(all);
 #pragma unroll
@@ -325,11 +327,8 @@ __device__ __forceinline__ Counts row_counts(const Team<G, CL>& team, int t, int
     n.warp[k] = 0.0f;
     const int at = CL ? int(threadIdx.x & 31) + 32 * k : int(threadIdx.x & 31) % (G / 32);
     if (G > 32 && at < team.warps() && (CL || k == 0)) {
-      int64_t left = all - int64_t(at / (G / 32)) * G * E;  // columns of that warp's CTA
-      left = left < 0 ? 0 : left > G * E ? G * E : left;
-      int c = 0;
-      for (int l = 0; l < 32; ++l) c += of(at % (G / 32) * 32 + l, int(left));
-      n.warp[k] = float(c);
+      const int64_t left = all - int64_t(at / (G / 32)) * G * E;  // columns of that warp's CTA
+      n.warp[k] = of(at % (G / 32), left <= 0 ? 0 : left < G * E ? int(left) : G * E);
     }
   }
   return n;

@@ -6,10 +6,12 @@
 // warps and CTAs are joined pairwise.  lse = M scale + ln S, entropy = ln S - ln 2 D / S (in deviations
 // from M, so that neither loses digits to the size of the logits).
 //
-// Alternatives: every warp lists what may be among its own largest: values above `thr`, the least of its
+// Alternatives: every warp lists what may be among the largest: values above `thr`, the least of its own
 // `top` largest so far.  The first tile's threshold is the top-th largest of the lanes' maxima, below
-// which no value of the warp can be needed.  Columns of one warp come in ascending order, so a later
-// value that equals the threshold loses the tie and `>` is enough.  The list is ordered by counting for
+// which no value of the warp can be needed; and the warps of a CTA tell one another their each-th
+// largest, each = ceil(top / warps), of which the least is a threshold for all.  Columns of one warp come
+// in ascending order, so a later value that equals its own threshold loses the tie and `>` is enough;
+// against a threshold of other warps a value that equals it is kept.  Lists are ordered by counting for
 // each key how many are above it; keys (value, then lower column) are all different, so the outcome does
 // not depend on the order in which lanes appended.
 //
@@ -106,12 +108,26 @@ __device__ __forceinline__ void to_pairs(uint4 w, Pair (&v)[kVec<BF16> / 2]) {
   }
 }
 
+// Where its `top`-th largest begins, as each warp of a team knows it: `each` is the place in a warp's own order that
+// makes `top` of them in all (ceil(top / warps)).
+struct Floors {
+  uint32_t* at;  // in_order of the each-th largest of every warp so far; 0: not that many
+  int warps, each;
+};
+
+// The value before the one whose in_order is k: what is above it is not below the value (two steps down from zero,
+// whose neighbour is -0).
+__device__ __forceinline__ float value_before(uint32_t k) {
+  return k <= 0x007FFFFFu ? -INFINITY : out_of_order(k - (k == 0x80000000u ? 2u : 1u));
+}
+
 // A warp's list of candidates.
 struct List {
   Key* keys;   // kListed + 32 * 8
   Key* kept;   // LOCO_MAX_TOP
   int* count;
-  int top;
+  Floors floors;
+  int top, warp;
   float thr;   // what is not above it is not needed
 
   // Keeps the `top` largest, in order.
@@ -121,6 +137,7 @@ struct List {
     for (int i = lane; i < n; i += 32) {
       const Key k = keys[i];
       int above = 0;
+#pragma unroll 8
       for (int j = 0; j < n; ++j) above += keys[j] > k;
       if (above < top) kept[above] = k;
     }
@@ -129,7 +146,11 @@ struct List {
     if (lane < left) keys[lane] = kept[lane];
     if (lane == 0) *count = left;
     __syncwarp();
-    if (left == top) thr = key_value(keys[top - 1]);
+    if (left == top) {
+      const float t = key_value(keys[top - 1]);
+      if (t > thr) thr = t;
+    }
+    if (left >= floors.each && lane == 0) floors.at[warp] = uint32_t(keys[floors.each - 1] >> 32);
   }
   // Appends the values of a vector that are above the threshold (all lanes of the warp; v: kVec values from column on).
   template <int N>
@@ -140,16 +161,26 @@ struct List {
     __syncwarp();
     if (*count > kListed) order(lane);
   }
-  // The threshold that the first tile's lane maxima give: at least `top` values are not below the top-th of them.
+  // What the lanes' maxima of the first tile say: at least `top` of the warp's values are not below the top-th of them.
   __device__ __forceinline__ void first(float lane_max, int lane) {
-    uint32_t u = in_order(lane_max), k = 0;
-    for (int i = 0; i < top; ++i) {
-      k = __reduce_max_sync(0xFFFFFFFFu, u);
-      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, u == k)) - 1) u = 0;
+    uint32_t u = in_order(lane_max);
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2) {  // descending over the lanes
+#pragma unroll
+      for (int d = size / 2; d > 0; d /= 2) {
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, u, d);
+        u = ((lane & d) == 0) == ((lane & size) == 0) ? max(u, o) : min(u, o);
+      }
     }
-    if (k <= in_order(-INFINITY)) return;
-    // the value before it, so that `>` takes it too (two steps down from zero, whose neighbour is -0)
-    const float t = out_of_order(k - (k == 0x80000000u ? 2u : 1u));
+    const float t = value_before(__shfl_sync(0xFFFFFFFFu, u, top - 1));
+    if (t > thr) thr = t;
+    if (lane == floors.each - 1 && u > 0x007FFFFFu) floors.at[warp] = u;
+  }
+  // The warps' floors together: `top` values of the row are not below the least of them.  (One read early or late
+  // is only a lower one: what is left out is never needed.)
+  __device__ __forceinline__ void share(int lane) {
+    const uint32_t f = *reinterpret_cast<volatile uint32_t*>(floors.at + lane % floors.warps);
+    const float t = value_before(__reduce_min_sync(0xFFFFFFFFu, f));
     if (t > thr) thr = t;
   }
 };
@@ -165,32 +196,21 @@ struct Shared<true> {
   Part cta;
   Key keys[kWarps][kListed + 256];
   Key kept[kWarps][LOCO_MAX_TOP];
-  Key cta_top[LOCO_MAX_TOP];
-  int count[kWarps];
+  Key chosen[kWarps * kListed];  // of all warps' lists, what can be among the largest
+  Key best[LOCO_MAX_TOP];
+  int count[kWarps], n_chosen;
+  uint32_t floors[kWarps], least[kWarps];
 };
 
-// The `top` largest of `lists` ordered lists of `top` keys (0: none), by threads 0 .. lists * top - 1; `out` was 0.
-template <typename At>
-__device__ __forceinline__ void merge_lists(At at, int lists, int top, Key* out) {
-  const int i = threadIdx.x;
-  if (i >= lists * top) return;
-  const int l = i / top;
-  int rank = i % top;
-  const Key k = at(l, rank);
-  if (k == 0) return;
-  for (int o = 0; o < lists && rank < top; ++o) {
-    if (o == l) continue;
-    int lo = 0, hi = top;  // keys of list o above k
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (at(o, mid) > k)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    rank += lo;
+// The `top` largest of chosen[0, n), in order, by all threads of the CTA; `best` was 0.
+__device__ __forceinline__ void choose(const Key* chosen, int n, int top, Key* best) {
+  for (int i = threadIdx.x; i < n; i += kThreadsLp) {
+    const Key k = chosen[i];
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) above += chosen[j] > k;
+    if (above < top) best[above] = k;
   }
-  if (rank < top) out[rank] = k;
 }
 
 // WPR: warps of a row's part (1: a CTA takes eight rows, 8: one).  CLUSTER: several CTAs to a row.
@@ -216,9 +236,16 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
   Part mine{kLowest, 0.0f, 0.0f};
   List list{};
   if constexpr (TOP) {
-    list = List{sh.keys[warp], sh.kept[warp], &sh.count[warp], a.top, -INFINITY};
-    if (lane == 0) sh.count[warp] = 0;
+    // a row of one warp has its floor to itself
+    const Floors floors{WPR == 1 ? &sh.floors[warp] : sh.floors, WPR, (a.top + WPR - 1) / WPR};
+    list = List{sh.keys[warp], sh.kept[warp], &sh.count[warp], floors, a.top, WPR == 1 ? 0 : warp, -INFINITY};
+    if (lane == 0) sh.count[warp] = 0, sh.floors[warp] = 0;
     __syncwarp();
+    if constexpr (WPR > 1) {
+      if (threadIdx.x < LOCO_MAX_TOP) sh.best[threadIdx.x] = 0;
+      if (threadIdx.x == 0) sh.n_chosen = 0;
+      __syncthreads();
+    }
   }
   // single elements at the row's ends
   const auto take_one = [&](int64_t from, int n) {
@@ -271,7 +298,10 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
       float tile = top[0];
 #pragma unroll
       for (int q = 1; q < kVectors; ++q) tile = max_nan(tile, top[q]);
-      if (first) list.first(tile, lane);
+      if (first)
+        list.first(tile, lane);
+      else if (WPR > 1)
+        list.share(lane);
       first = false;
       if (__any_sync(0xFFFFFFFFu, tile > list.thr)) {
 #pragma unroll
@@ -301,26 +331,33 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
     // the same order of operands in both lanes: the same result
     mine = lane & o ? join(other, mine, c) : join(mine, other, c);
   }
-  if constexpr (TOP) {
+  Part all = mine;
+  const Key* best = nullptr;
+  if constexpr (TOP && WPR == 1) {
     list.order(lane);
     const int n = *list.count;
     if (lane >= n && lane < a.top) list.keys[lane] = 0;
     __syncwarp();
+    best = list.keys;
   }
-  Part all = mine;
-  const Key* best = TOP ? list.keys : nullptr;
   if constexpr (WPR > 1) {
     if (lane == 0) sh.part[warp] = mine;
     if constexpr (TOP) {
-      if (threadIdx.x < LOCO_MAX_TOP) sh.cta_top[threadIdx.x] = 0;
+      if (lane == 0) sh.least[warp] = in_order(list.thr);
     }
     __syncthreads();
     all = sh.part[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) all = join(all, sh.part[w], c);
     if constexpr (TOP) {
-      merge_lists([&](int l, int i) { return sh.keys[l][i]; }, kWarps, a.top, sh.cta_top);
-      best = sh.cta_top;
+      // no value below the highest of the warps' thresholds can be among the largest; each list holds kListed at most
+      const uint32_t least = __reduce_max_sync(0xFFFFFFFFu, sh.least[lane % kWarps]);
+      const int n = *list.count;
+      for (int i = lane; i < n; i += 32)
+        if (uint32_t(list.keys[i] >> 32) >= least) sh.chosen[atomicAdd(&sh.n_chosen, 1)] = list.keys[i];
+      __syncthreads();
+      choose(sh.chosen, sh.n_chosen, a.top, sh.best);
+      best = sh.best;
     }
     if constexpr (CLUSTER) {
       if (threadIdx.x == 0) sh.cta = all;
@@ -330,18 +367,17 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
         all = sh.cta;
         for (int p = 1; p < parts; ++p) all = join(all, *cluster.map_shared_rank(&sh.cta, p), c);
         if constexpr (TOP) {
-          // the CTAs' lists beside one another, then merged as the warps' were
+          // the CTAs' lists beside one another (0 where one has fewer)
           if (threadIdx.x < parts * a.top)
-            sh.keys[threadIdx.x / a.top][threadIdx.x % a.top] =
-                cluster.map_shared_rank(sh.cta_top, threadIdx.x / a.top)[threadIdx.x % a.top];
+            sh.chosen[threadIdx.x] = cluster.map_shared_rank(sh.best, threadIdx.x / a.top)[threadIdx.x % a.top];
         }
       }
       cluster.sync();  // nobody leaves before it has been read
       if (me != 0) return;
       if constexpr (TOP) {
-        if (threadIdx.x < LOCO_MAX_TOP) sh.cta_top[threadIdx.x] = 0;
+        if (threadIdx.x < LOCO_MAX_TOP) sh.best[threadIdx.x] = 0;
         __syncthreads();
-        merge_lists([&](int l, int i) { return sh.keys[l][i]; }, parts, a.top, sh.cta_top);
+        choose(sh.chosen, parts * a.top, a.top, sh.best);
       }
     }
     if constexpr (TOP) __syncthreads();

@@ -392,6 +392,7 @@ loco_status loco_adam_tensors(const loco_adam_tensors_config* cfg, const loco_ad
     a.c2 = hp->eps_inside_sqrt ? float(1.0 / bc2) : float(1.0 / sqrt(bc2));
   }
   a.eps = hp->eps, a.eps_inside_sqrt = hp->eps_inside_sqrt != 0;
+  a.neg_zero = -0.0f;
   a.grad_scale = grad_scale;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (count <= kAdamFew) return launch_some<kAdamFew>(*cfg, tensors, 0, count, *hp, t, a, s);

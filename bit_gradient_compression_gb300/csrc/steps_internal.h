@@ -104,6 +104,7 @@ constexpr int kAdamFew = 24, kAdamMany = 384;
 
 struct AdamTensorsArgs {
   float beta1, beta2, one_minus_beta1, one_minus_beta2, c2, eps;
+  float neg_zero;  // -0.0f, unknown when the kernel is compiled
   int eps_inside_sqrt;
   const float* grad_scale;
 };
