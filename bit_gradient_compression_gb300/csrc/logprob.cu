@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
           }
           list.append(x, shape.head + (i + q * kTeam + t) * V, lane);
         }
+        list.order(lane);  // the thresholds move up with every tile that had something: later ones seldom have
       }
     }
   }

@@ -439,6 +439,22 @@ static PyObject* adam_state_decode(PyObject* self, PyObject* const* a, Py_ssize_
   CALL(loco_adam_state_decode(d == t_u8 ? LOCO_STATE_V : LOCO_STATE_M, c, s, count, o, od, stream));
 }
 
+/* (address of the config, address of the tensors, count, address of the hyper-parameters, t, grad_scale, stream) */
+static PyObject* adam_tensors(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  ARGS(7);
+  void* scale = NULL;
+  int f = LOCO_F32;
+  WANT(a[5] == Py_None || vec(a[5], 1, &f, &scale));
+  const loco_adam_tensors_config* cfg = (const void*)(uintptr_t)PyLong_AsUnsignedLongLong(a[0]);
+  const loco_adam_tensor* tensors = (const void*)(uintptr_t)PyLong_AsUnsignedLongLong(a[1]);
+  const int32_t count = (int32_t)integer(a[2]);
+  const loco_adam_hparams* hp = (const void*)(uintptr_t)PyLong_AsUnsignedLongLong(a[3]);
+  const int64_t t = integer(a[4]);
+  const loco_stream_t stream = STREAM(a[6]);
+  WANT(1);
+  CALL(loco_adam_tensors(cfg, tensors, count, hp, t, scale, stream));
+}
+
 /* init(float32, bfloat16, int8, uint8, int64, ALIGN_WORK, ALIGN_ROWS).  Until then every function returns None. */
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (n != 7) {
@@ -460,7 +476,7 @@ static PyMethodDef methods[] = {
     METHOD(init),          METHOD(ckpt_encode),    METHOD(ckpt_decode),           METHOD(norm_forward),
     METHOD(norm_backward), METHOD(linear_forward), METHOD(linear_backward_input), METHOD(linear_backward_weight),
     METHOD(join_forward),  METHOD(join_backward),  METHOD(logprob_forward),       METHOD(logprob_backward),
-    METHOD(adam_state_decode),
+    METHOD(adam_state_decode), METHOD(adam_tensors),
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -67,6 +67,15 @@ loco_status fail_tensor(loco_status st, int i, const char* buffer, const char* w
   return fail(st, "tensors[%d].%s %s", i, buffer, what);
 }
 
+constexpr int kNameSize = 40;
+const char* buffer_name(const Range& r, char (&name)[kNameSize]) {
+  if (r.tensor < 0)
+    snprintf(name, kNameSize, "grad_scale");
+  else
+    snprintf(name, kNameSize, "tensors[%d].%s", r.tensor, kBufferNames[int(r.buffer)]);
+  return name;
+}
+
 // Every buffer of every tensor, one kind after another (tensors of a kind mostly share their allocations):
 // null, alignment and extent, then whether anything that is written overlaps anything else.
 loco_status check_tensors(const loco_adam_tensors_config& cfg, const loco_adam_tensor* t, int32_t count,
@@ -112,21 +121,21 @@ loco_status check_tensors(const loco_adam_tensors_config& cfg, const loco_adam_t
     const uintptr_t lo = reinterpret_cast<uintptr_t>(grad_scale);
     all->r[all->n++] = Range{lo, lo + 4, -1, 1, false};
   }
-  // extents, a few at a time in the order above
+  // extents, a few at a time in the order above; the index of one that fails is put to its name afterwards
   constexpr int kAtOnce = 64;
   for (int64_t at = 0; at < all->n; at += kAtOnce) {
     BufCheck c[kAtOnce];
-    char names[kAtOnce][40];
     const int n = int(std::min<int64_t>(kAtOnce, all->n - at));
     for (int k = 0; k < n; ++k) {
       const Range& r = all->r[at + k];
-      if (r.tensor < 0)
-        snprintf(names[k], sizeof names[k], "grad_scale");
-      else
-        snprintf(names[k], sizeof names[k], "tensors[%d].%s", r.tensor, kBufferNames[int(r.buffer)]);
-      c[k] = BufCheck{reinterpret_cast<const void*>(r.lo), size_t(r.hi - r.lo), 1, names[k]};
+      c[k] = BufCheck{reinterpret_cast<const void*>(r.lo), size_t(r.hi - r.lo), 1, kBufferNames[int(r.buffer)]};
     }
-    LOCO_TRY(check_buffers(c, n));
+    if (check_buffers(c, n) == LOCO_OK) continue;
+    for (int k = 0; k < n; ++k) {
+      char name[kNameSize];
+      c[k].name = buffer_name(all->r[at + k], name);
+      LOCO_TRY(check_buffers(c + k, 1));
+    }
   }
   // by their beginnings: what is written must begin after all before it end, what is read after all written before it
   std::sort(all->r, all->r + all->n, [](const Range& a, const Range& b) { return a.lo < b.lo; });
@@ -135,16 +144,8 @@ loco_status check_tensors(const loco_adam_tensors_config& cfg, const loco_adam_t
     const Range& r = all->r[i];
     const Range* other = r.out ? last : last_out;
     if (other != nullptr && r.lo < other->hi) {
-      char a[40], b[40];
-      const Range* two[2] = {other, &r};
-      char* text[2] = {a, b};
-      for (int k = 0; k < 2; ++k) {
-        if (two[k]->tensor < 0)
-          snprintf(text[k], 40, "grad_scale");
-        else
-          snprintf(text[k], 40, "tensors[%d].%s", two[k]->tensor, kBufferNames[int(two[k]->buffer)]);
-      }
-      return fail(LOCO_ERR_INVALID_ARG, "%s overlaps %s", a, b);
+      char a[kNameSize], b[kNameSize];
+      return fail(LOCO_ERR_INVALID_ARG, "%s overlaps %s", buffer_name(*other, a), buffer_name(r, b));
     }
     if (last == nullptr || r.hi > last->hi) last = &r;
     if (r.out && (last_out == nullptr || r.hi > last_out->hi)) last_out = &r;

@@ -328,7 +328,7 @@ except ImportError:
     class _marshal:  # built without Python's headers
         init = ckpt_encode = ckpt_decode = norm_forward = norm_backward = linear_forward = staticmethod(lambda *a: None)
         linear_backward_input = linear_backward_weight = join_forward = join_backward = logprob_forward = init
-        logprob_backward = adam_state_decode = init
+        logprob_backward = adam_state_decode = adam_tensors = init
 
 _DTYPES: dict = {}  # torch.dtype -> loco_dtype, filled on first use (torch is imported only then)
 
@@ -762,6 +762,7 @@ class AdamTensors:
 
     def __init__(self, array, count: int, cfg: loco_adam_tensors_config, tensors):
         self.array, self.count, self.cfg, self.tensors = array, count, cfg, tensors
+        self.addresses = ctypes.addressof(cfg), ctypes.addressof(array)
 
 
 def make_adam_tensors(params, grads, ms, vs, *, m_steps=None, v_steps=None, params_bf16=None, lr_scales=None,
@@ -813,6 +814,10 @@ def make_adam_tensors(params, grads, ms, vs, *, m_steps=None, v_steps=None, para
 def loco_adam_tensors(tensors: AdamTensors, hp: loco_adam_hparams, t: int, *, grad_scale=None, stream=None):
     """One Adam(W) step on every tensor of the list, in place.  grad_scale: one fp32 value on the device, the factor of
     every gradient (of clipping, of a loss scale)."""
+    status = _marshal.adam_tensors(tensors.addresses[0], tensors.addresses[1], tensors.count, ctypes.addressof(hp), t,
+                                   grad_scale, _stream(stream))
+    if status is not None:
+        return _check(status) if status else None
     _check(lib.loco_adam_tensors(ctypes.byref(tensors.cfg), tensors.array, tensors.count, ctypes.byref(hp), t,
                                  0 if grad_scale is None else _f32(grad_scale.view(-1), "grad_scale", 1), _stream(stream)))
 

@@ -159,6 +159,53 @@ def test_near_the_64_bit_update(L):
     assert bool(((v.double() - v64).abs() <= 4 * U * v64).all())
 
 
+@pytest.mark.parametrize("eps,inside", [(0.0, False), (1e-8, False), (1e-30, True)])
+def test_every_root_and_quotient(L, eps, inside):
+    """All 2^24 roots of [1, 4), so every denominator of [1, 2), under a numerator each: the IEEE operations' bits."""
+    x = (torch.arange(1 << 24, device="cuda", dtype=torch.int32) + 0x3F800000).view(F32)
+    hp = L.make_adam(lr=1.0, beta1=0.5, beta2=0.5, eps=eps, bias_correction=False, eps_inside_sqrt=inside)
+    for k, scale in ((1, 1.0), (2, 2.0 ** -40), (3, 2.0 ** 40), (4, 2.0 ** -46), (5, 2.0 ** 50)):
+        m = torch.rand(x.numel(), generator=gen(k), device="cuda") + 0.5 if k > 1 else torch.full_like(x, 2.0)
+        p, z = torch.zeros_like(x), torch.zeros_like(x)
+        v = x * (2.0 * scale * scale)       # halved by the step, exactly
+        want = S.adam(p, z, m.clone(), v.clone(), hp, 1)
+        L.loco_adam_tensors(L.make_adam_tensors([p], [z], [m], [v]), hp, 1)
+        assert same(p, want[0]) and same(m, want[1]) and same(v, want[2])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_every_exponent(L, bits):
+    """Parameters, gradients and states of every exponent, subnormal ones and zeros of both signs among them."""
+    n = 1 << 20
+    g = gen(36)
+    rand = lambda lo, hi: torch.ldexp(torch.rand(n, generator=g, device="cuda") + 0.5,  # noqa: E731
+                                      torch.randint(lo, hi, (n,), generator=g, device="cuda"))
+    sign = lambda: torch.randint(0, 2, (n,), generator=g, device="cuda") * 2.0 - 1.0  # noqa: E731
+    p, gr = rand(-20, 3) * sign(), rand(-140, 60) * sign()
+    p[::7], gr[::5], gr[1::5] = -0.0, 0.0, -0.0
+    hp = L.make_adam(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1)
+    if bits == 32:
+        m, v, kw = rand(-148, 60) * sign(), rand(-148, 100), {}
+        m[::3], v[::3], m[1::9] = 0.0, 0.0, -0.0
+    else:
+        nb = n // 256
+        m = torch.randint(-127, 128, (n,), generator=g, device="cuda", dtype=torch.int8)
+        v = torch.randint(0, 256, (n,), generator=g, device="cuda", dtype=torch.uint8)
+        kw = dict(m_steps=[rand(-140, 50)[:nb].contiguous()], v_steps=[rand(-74, 40)[:nb].contiguous()])
+    for wide in (True, False):
+        q, states = p.clone(), [m.clone(), v.clone()]
+        steps = {k: [t[0].clone()] for k, t in kw.items()}
+        st = dict(p=[q], g=[gr], m=states[:1], v=states[1:], ms=steps.get("m_steps"), vs=steps.get("v_steps"), scales=[1.0], decay=[1.0])
+        if not wide:        # an odd place in its buffer
+            buf = torch.zeros(n + 1, device="cuda")
+            buf[1:] = q
+            st["p"] = [buf[1:]]
+        want = expect(st, 0, bits, F32, hp, 4, 21, None)
+        L.loco_adam_tensors(L.make_adam_tensors(st["p"], [gr], states[:1], states[1:], dither=21, **steps), hp, 4)
+        for name in ["p", "m", "v"] + (["ms", "vs"] if bits == 8 else []):
+            assert same(st[name][0], want[name]), name
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_zeros_and_values_that_are_not_finite(L, bits):
     """Blocks of zeros stay zeros; a NaN or an infinity stays within its block of 256 of its tensor."""
