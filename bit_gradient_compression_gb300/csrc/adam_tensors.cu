@@ -222,7 +222,7 @@ struct Staged {
 };
 
 template <int BITS, bool PBF16, bool GBF16, bool DITHER, int MAX>
-__global__ void __launch_bounds__(kThreadsAdam, BITS == 32 ? 2 : 3) k_adam_tensors(const __grid_constant__ AdamTensorList<MAX> l, uint32_t group) {
+__global__ void __launch_bounds__(kThreadsAdam, BITS == 32 ? 2 : 3) k_step_tensors(const __grid_constant__ AdamTensorList<MAX> l, uint32_t group) {
   extern __shared__ __align__(16) uint8_t ring[];  // two stages
   using Stage = Staged<PBF16, GBF16>;
   const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
@@ -448,14 +448,14 @@ cudaError_t run(const AdamTensorList<MAX>& l, cudaStream_t s) {
   int cap = 0;
   constexpr size_t kSmem = BITS == 8 ? 2 * size_t(Staged<PBF16, GBF16>::kStage) : 0;
   const cudaError_t e =
-      layer_grid(grid, reinterpret_cast<const void*>(&k_adam_tensors<BITS, PBF16, GBF16, DITHER, MAX>), kThreadsAdam, kSmem, kSmem, &cap);
+      layer_grid(grid, reinterpret_cast<const void*>(&k_step_tensors<BITS, PBF16, GBF16, DITHER, MAX>), kThreadsAdam, kSmem, kSmem, &cap);
   if (e != cudaSuccess) return e;
   // few units: one to a warp, before any warp takes a second
   constexpr int64_t kCta = kThreadsAdam / 32;
   const int64_t units = l.first[l.count], all = cap * kCta;
   const int group = int(units >= all * kGroup ? kGroup : units <= all ? 1 : units / all);
   const int64_t want = (units + kCta * group - 1) / (kCta * group);
-  k_adam_tensors<BITS, PBF16, GBF16, DITHER, MAX><<<int(want < cap ? want : cap), kThreadsAdam, kSmem, s>>>(l, group);
+  k_step_tensors<BITS, PBF16, GBF16, DITHER, MAX><<<int(want < cap ? want : cap), kThreadsAdam, kSmem, s>>>(l, group);
   return cudaGetLastError();
 }
 

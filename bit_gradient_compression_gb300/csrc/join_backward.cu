@@ -1,7 +1,7 @@
 // Gradients of a join (loco_join_backward): four reads and two writes a value, one pass over the rows,
 // and a small kernel that adds up the parameters' gradients.
 //
-// As in the forward pass a row stays in registers and the next one is on its way (join_common.cuh).
+// As in the forward pass a row stays on the SM and the next one is on its way (join_common.cuh).
 // Two rounds of sums a row: through the norm in front of the next block, then through the one behind
 // this block, whose gradient the first makes.  Of the parameters' gradients only four sums over rows are
 // needed, with c_j = t_j row_gate (no gate, no scale):
@@ -16,19 +16,18 @@ namespace loco {
 
 namespace {
 
-// Rows on their way: the one at work and the next.  Behind them a thread's own parameters (gm and pg below) lie in
-// shared memory, where it alone reads them: in registers they would cost every second CTA of an SM.
+// Rows on their way: the one at work and the next.  Behind them a thread's own parameters (gm and pg below).
 constexpr int kStages = 2;
 template <int G, int E, typename RowX, typename RowY>
 constexpr size_t kRing = size_t(kTeamCta<G>) * (kStages * 2 * (RowX::kBytes + RowY::kBytes) + 2 * E * sizeof(float));
 
 // SUMS: 4, or 2 where neither sum c nor sum du is wanted (a RMS norm without betas).
 template <int G, int E, bool CL, int SUMS, typename RowX, typename RowY>
-__global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort && SUMS == 2 && !CL> * 32 / kTeamCta<G>)
+__global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G == 32) ? 256 : 512) / kTeamCta<G>)
     k_join_bwd(const JoinBwdArgs args, bool pwide) {
   __shared__ Board<G, CL> board;
   extern __shared__ __align__(16) uint8_t ring[];
-  constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, P = E / 2;
+  constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, P = E / 2, C = E / 8;
   JoinBwdArgs a = args;
   const int t = threadIdx.x % G, place = threadIdx.x / G;
   Team<G, CL> team{&board, 0, 1, 0};
@@ -73,6 +72,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort && S
   }
   RowX dhn, hn;
   RowY dun, yn;
+  float m1n = 0.0f, r1n = 1.0f, m2n = 0.0f, r2n = 1.0f, wn = 1.0f;
   uint32_t slot = 0;
   const auto fetch = [&](uint32_t row) {
     dhn.at = base + slot * kStage, hn.at = dhn.at + kThreadsCta * RowX::kBytes;
@@ -84,10 +84,14 @@ __global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort && S
         hn.load(a.h, row, a.ldh, t, cols, a.x_bf16);
       }
       if (a.y != nullptr) yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
+      if (a.post) m1n = __ldg(a.stats + row), r1n = __ldg(a.stats + a.rows + row);
+      if (a.du != nullptr) m2n = __ldg(a.stats + 2 * a.rows + row), r2n = __ldg(a.stats + 3 * a.rows + row);
+      if (a.row_gate != nullptr) wn = __ldg(a.row_gate + row);
     }
     cp_async_commit();
     slot ^= 1;
   };
+  cudaTriggerProgrammaticLaunchCompletion();  // the parameters' kernel may wait on its SMs
   constexpr bool kAhead = RowX::kWide;  // single columns leave no registers for a row ahead
   if constexpr (kAhead) fetch(first);
   const Pair a2 = both(a.a);
@@ -96,99 +100,95 @@ __global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort && S
     if constexpr (!kAhead) fetch(row);
     RowX dhc = dhn, hc = hn;
     RowY duc = dun, yc = yn;
-    float m2 = 0.0f, r2 = 1.0f;
-    if (live && a.du != nullptr) m2 = __ldg(a.stats + 2 * a.rows + row), r2 = __ldg(a.stats + 3 * a.rows + row);
+    const float m1 = m1n, r1 = r1n, m2 = m2n, r2 = r2n, w = wn;
     if constexpr (kAhead) {
       fetch(row + step);
       cp_async_wait<1>();
     }
-    Pair dt[P], du[P];
+    // What a value takes part in is formed anew from shared memory in each of the three passes over the row's
+    // columns: registers hold the sums over rows and t.
     float s[3] = {0.0f, 0.0f, 0.0f};
-    if (a.du != nullptr && live) {
-      Pair h[P], g[P];
-      duc.values(du), hc.values(h);
-      recall<E, kThreadsCta>(base + kOwn, 0, g);
-      const Pair less = both(-m2), f = both(r2);
-      Pair s0 = zero, s1 = zero;
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        h[i] = (h[i] + less) * f;
-        sums[1][i] = fma(du[i], h[i], sums[1][i]);
-        if constexpr (SUMS == 4) sums[3][i] = sums[3][i] + du[i];
-        du[i] = du[i] * g[i];
-        s0 = s0 + du[i];
-        s1 = fma(du[i], h[i], s1);
-        dt[i] = h[i];
-      }
-      s[0] = total(s0), s[1] = total(s1);
-    }
-    float m1 = 0.0f, r1 = 1.0f, w = 1.0f;
-    if (live && a.post) m1 = __ldg(a.stats + row), r1 = __ldg(a.stats + a.rows + row);
-    if (live && a.row_gate != nullptr) w = __ldg(a.row_gate + row);
     if (a.du != nullptr) {
+      if (live) {
+        const Pair less = both(-m2), f = both(r2);
+        Pair s0 = zero, s1 = zero;
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+          Pair du[4], h[4], g[4];
+          duc.eight(e, du), hc.eight(e, h);
+          recall<E, kThreadsCta>(base + kOwn, 0, e, g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[i] = (h[i] + less) * f;
+            sums[1][e * 4 + i] = fma(du[i], h[i], sums[1][e * 4 + i]);
+            if constexpr (SUMS == 4) sums[3][e * 4 + i] = sums[3][e * 4 + i] + du[i];
+            du[i] = du[i] * g[i];
+            s0 = s0 + du[i];
+            s1 = fma(du[i], h[i], s1);
+          }
+        }
+        s[0] = total(s0), s[1] = total(s1);
+      }
       float two[2] = {s[0], s[1]};
       team.sum(two);
-      const Pair c1 = both(level ? -two[0] * inv_cols : 0.0f), c2 = both(-two[1] * inv_cols);
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) dt[i] = fma(dt[i], c2, du[i] + c1);  // over r2
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; ++i) dt[i] = zero;
+      s[0] = level ? -two[0] * inv_cols : 0.0f, s[1] = -two[1] * inv_cols;
     }
+    Pair dt[P];
     if (live) {
-      if (a.dh != nullptr) {
-        dhc.values(du);
-      } else {
+      const Pair l2 = both(-m2), f2 = both(r2), c1 = both(s[0]), c2 = both(s[1]), l1 = both(-m1), f1 = both(r1), w2 = both(w);
+      Pair s0 = zero, s1 = zero, s2 = zero;
+      char* out = static_cast<char*>(a.dx) + row * a.lddx * (a.x_bf16 ? 2 : 4);
 #pragma unroll
-        for (int i = 0; i < P; ++i) du[i] = zero;
+      for (int e = 0; e < C; ++e) {
+        Pair v[4], g[4], h[4];
+        if (a.dh != nullptr) {
+          dhc.eight(e, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = zero;
+        }
+        if (a.du != nullptr) {
+          Pair du[4];
+          duc.eight(e, du), hc.eight(e, h);
+          recall<E, kThreadsCta>(base + kOwn, 0, e, g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = fma(f2, fma((h[i] + l2) * f2, c2, fma(du[i], g[i], c1)), v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dt[e * 4 + i] = v[i], v[i] = a2 * v[i];
+        RowX::store(out, e, t, cols, a.x_bf16, v);
+        if (a.y != nullptr) {
+          yc.eight(e, h);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = zero;
+        }
+        recall<E, kThreadsCta>(base + kOwn, 1, e, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const Pair yh = (h[i] + l1) * f1, c = dt[e * 4 + i] * w2;
+          sums[0][e * 4 + i] = fma(c, yh, sums[0][e * 4 + i]);
+          if constexpr (SUMS == 4) sums[2][e * 4 + i] = sums[2][e * 4 + i] + c;
+          const Pair p = dt[e * 4 + i] * g[i];  // over w
+          s0 = s0 + p;
+          s1 = fma(p, yh, s1);
+        }
       }
-      const Pair f = both(r2);
+      if (a.drow_gate != nullptr && a.post_beta != nullptr) {
+        // t s gate post_beta, over s
+        Pair b[P], v[P];
+        params<RowX, E>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, b);
 #pragma unroll
-      for (int i = 0; i < P; ++i) dt[i] = fma(f, dt[i], du[i]), du[i] = a2 * dt[i];
-      RowX::store(a.dx, row, a.lddx, t, cols, a.x_bf16, du);
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; ++i) dt[i] = zero;
-    }
-    // over w: p and p yh, and t s gate post_beta
-    Pair y[P];
-    s[0] = s[1] = s[2] = 0.0f;
-    if (a.y != nullptr && live) {
-      yc.values(y);
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; ++i) y[i] = zero;
-    }
-    {
-      Pair g[P];
-      recall<E, kThreadsCta>(base + kOwn, 1, g);
-      const Pair less = both(-m1), f = both(r1), w2 = both(w);
-      Pair s0 = zero, s1 = zero;
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        y[i] = (y[i] + less) * f;
-        const Pair c = dt[i] * w2;
-        sums[0][i] = fma(c, y[i], sums[0][i]);
-        if constexpr (SUMS == 4) sums[2][i] = sums[2][i] + c;
-        du[i] = dt[i] * g[i];
-        s0 = s0 + du[i];
-        s1 = fma(du[i], y[i], s1);
-      }
-      s[0] = total(s0), s[1] = total(s1);
-    }
-    if (a.drow_gate != nullptr) {
-      if (a.post_beta != nullptr) {
-        Pair v[P], d = zero;
-        params<RowX, E>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, v);
-#pragma unroll
-        for (int i = 0; i < P; ++i) dt[i] = dt[i] * v[i];
+        for (int i = 0; i < P; ++i) b[i] = dt[i] * b[i];
         params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
 #pragma unroll
-        for (int i = 0; i < P; ++i) d = fma(dt[i], v[i], d);
-        s[2] = total(d);
+        for (int i = 0; i < P; ++i) s2 = fma(b[i], v[i], s2);
       }
+      s[0] = total(s0), s[1] = total(s1), s[2] = total(s2);
+    } else {
+      s[0] = s[1] = s[2] = 0.0f;
+    }
+    if (a.drow_gate != nullptr) {
       team.sum(s);
       if (t == 0 && live && team.rank == 0) a.drow_gate[row] = fmaf(a.s, s[2], s[1]);
     } else if (a.post) {
@@ -197,16 +197,25 @@ __global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort && S
       s[0] = two[0], s[1] = two[1];
     }
     if (!live) continue;  // whole teams
-    if (a.post) {
-      const Pair c1 = both(level ? -s[0] * inv_cols : 0.0f), c2 = both(-s[1] * inv_cols), f = both(w * r1);
+    {
+      const Pair c1 = both(a.post && level ? -s[0] * inv_cols : 0.0f), c2 = both(a.post ? -s[1] * inv_cols : 0.0f);
+      const Pair l1 = both(-m1), f1 = both(r1), f = both(w * r1);
+      char* out = static_cast<char*>(a.dy) + row * a.lddy * (a.y_bf16 ? 2 : 4);
 #pragma unroll
-      for (int i = 0; i < P; ++i) du[i] = f * fma(y[i], c2, du[i] + c1);
-    } else if (a.row_gate != nullptr) {
-      const Pair f = both(w);
+      for (int e = 0; e < C; ++e) {
+        Pair y[4], g[4];
+        recall<E, kThreadsCta>(base + kOwn, 1, e, g);
+        if (a.post) {
+          yc.eight(e, y);
 #pragma unroll
-      for (int i = 0; i < P; ++i) du[i] = f * du[i];
+          for (int i = 0; i < 4; ++i) g[i] = f * fma((y[i] + l1) * f1, c2, fma(dt[e * 4 + i], g[i], c1));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g[i] = f * (dt[e * 4 + i] * g[i]);
+        }
+        RowY::store(out, e, t, cols, a.y_bf16, g);
+      }
     }
-    RowY::store(a.dy, row, a.lddy, t, cols, a.y_bf16, du);
   }
   if (a.partials == nullptr) return;
   // one partial row a team of CTAs; the teams of a CTA are added through shared memory in their order
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort && S
 }
 
 // Rows of any length: a CTA of 1024 reads its row for each sum and output, and its partial sums lie in the workspace.
-__global__ void __launch_bounds__(1024) k_join_bwd_long(const JoinBwdArgs a) {
+__global__ void __launch_bounds__(1024, 1) k_join_bwd_long(const JoinBwdArgs a) {
   __shared__ Board<1024, false> board;
   Team<1024, false> team{&board, 0, 1, 0};
   const float inv_cols = 1.0f / float(a.cols);
@@ -313,35 +322,41 @@ __global__ void __launch_bounds__(1024) k_join_bwd_long(const JoinBwdArgs a) {
   }
 }
 
-// Adds the partial rows of 32 columns: warp w takes every eighth row of one of the four sums, eight rows' loads
-// under way at a time; the eight are joined in order.
+// Adds the partial rows of 32 columns, of two sums at a time: those behind the block (y) or those of the next norm.
+// A warp takes every sixteenth partial row of one of the two, sixteen rows' loads under way at a time; the sixteen are
+// joined in order.
 __global__ void __launch_bounds__(1024) k_join_bwd_params(const JoinBwdArgs a, int partials, int sums) {
-  __shared__ float part[8][kJoinSums][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = warp % kJoinSums, group = warp / kJoinSums;
+  constexpr int kGroups = 16;
+  __shared__ float part[kGroups][2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = warp % 2, group = warp / 2, next = blockIdx.y;
   const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+  cudaGridDependencySynchronize();  // launched while the rows' kernel runs
   float v = 0.0f;
-  if (c < a.cols && (sums == 4 || k % 2 == 0)) {
-    const float* q = a.partials + k * a.cols + c;
+  if (c < a.cols && (sums == 4 || k == 0)) {
     const int64_t row = kJoinSums * a.cols;
-    int p = group;
-    for (; p + 56 < partials; p += 64) {
-      float x[8];
+    const float* q = a.partials + (next * 2 + k) * a.cols + c + group * row;
+    for (int p = group; p < partials; p += kGroups * 16, q += kGroups * 16 * row) {
+      float x[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __ldcs(q + (p + 8 * i) * row);
+      for (int i = 0; i < 16; ++i) x[i] = p + i * kGroups < partials ? __ldcs(q + i * kGroups * row) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v += x[i];
+      for (int i = 0; i < 16; ++i) v += x[i];
     }
-    for (; p < partials; p += 8) v += __ldcs(q + p * row);
   }
   part[group][k][lane] = v;
   __syncthreads();
   if (warp != 0 || c >= a.cols) return;
-  float s[kJoinSums];
+  float s[2];
 #pragma unroll
-  for (int i = 0; i < kJoinSums; ++i) {
+  for (int i = 0; i < 2; ++i) {
     s[i] = part[0][i][lane];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s[i] += part[w][i][lane];
+    for (int w = 1; w < kGroups; ++w) s[i] += part[w][i][lane];
+  }
+  if (next) {
+    if (a.dgamma != nullptr) store_elem(a.dgamma, c, a.grad_bf16, s[0]);
+    if (a.dbeta != nullptr) store_elem(a.dbeta, c, a.grad_bf16, s[1]);
+    return;
   }
   const float g = a.s * (a.gate != nullptr ? load_elem(a.gate, c, a.param_bf16) : 1.0f);
   if (a.dpost_gamma != nullptr) store_elem(a.dpost_gamma, c, a.grad_bf16, g * s[0]);
@@ -351,8 +366,6 @@ __global__ void __launch_bounds__(1024) k_join_bwd_params(const JoinBwdArgs a, i
     const float d = a.post_beta != nullptr ? load_elem(a.post_beta, c, a.param_bf16) * s[1] : 0.0f;
     store_elem(a.dgate, c, a.grad_bf16, a.s * fmaf(pg, s[0], d));
   }
-  if (a.dgamma != nullptr) store_elem(a.dgamma, c, a.grad_bf16, s[2]);
-  if (a.dbeta != nullptr) store_elem(a.dbeta, c, a.grad_bf16, s[3]);
 }
 
 template <int G, int E, bool CL, int SUMS, typename RowX, typename RowY>
@@ -378,12 +391,14 @@ cudaError_t run_sums(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* 
   return sums == 4 ? run<G, E, CL, 4, RowX, RowY>(a, pwide, ctas, partials, s)
                    : run<G, E, CL, 2, RowX, RowY>(a, pwide, ctas, partials, s);
 }
+template <int G, bool CL>
+cudaError_t run_f32(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* partials, cudaStream_t s) {
+  return a.y_bf16 ? run_sums<G, 8, CL, Vec<G, 8, false>, Vec<G, 8, true>>(a, pwide, ctas, sums, partials, s)
+                  : run_sums<G, 8, CL, Vec<G, 8, false>, Vec<G, 8, false>>(a, pwide, ctas, sums, partials, s);
+}
+// bf16 rows: sixteen columns to a thread, so that half as many warps add up their sums.
 template <int G, int E, bool CL>
-cudaError_t run_vec(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* partials, cudaStream_t s) {
-  if (!a.x_bf16) {
-    return a.y_bf16 ? run_sums<G, E, CL, Vec<G, E, false>, Vec<G, E, true>>(a, pwide, ctas, sums, partials, s)
-                    : run_sums<G, E, CL, Vec<G, E, false>, Vec<G, E, false>>(a, pwide, ctas, sums, partials, s);
-  }
+cudaError_t run_bf16(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* partials, cudaStream_t s) {
   return run_sums<G, E, CL, Vec<G, E, true>, Vec<G, E, true>>(a, pwide, ctas, sums, partials, s);
 }
 template <int G, int E, bool CL>
@@ -412,11 +427,18 @@ cudaError_t rows_kernel(const JoinBwdArgs& a, int* sums, int* partials, cudaStre
   if (ctas > kMaxCluster) return run_long(a, partials, s);
   if (wide) {
     if (a.dbeta == nullptr && a.dpost_beta == nullptr && (a.dgate == nullptr || a.post_beta == nullptr)) *sums = 2;
-    if (a.cols <= 256) return run_vec<32, 8, false>(a, pwide, 1, *sums, partials, s);
-    if (a.cols <= 1024) return run_vec<128, 8, false>(a, pwide, 1, *sums, partials, s);
-    if (a.cols <= 2048) return run_vec<256, 8, false>(a, pwide, 1, *sums, partials, s);
-    if (a.cols <= 4096) return run_vec<512, 8, false>(a, pwide, 1, *sums, partials, s);
-    return run_vec<512, 8, true>(a, pwide, ctas, *sums, partials, s);
+    if (a.x_bf16) {
+      if (a.cols <= 256) return run_bf16<32, 8, false>(a, pwide, 1, *sums, partials, s);
+      if (a.cols <= 512) return run_bf16<32, 16, false>(a, pwide, 1, *sums, partials, s);
+      if (a.cols <= 2048) return run_bf16<128, 16, false>(a, pwide, 1, *sums, partials, s);
+      if (a.cols <= 4096) return run_bf16<256, 16, false>(a, pwide, 1, *sums, partials, s);
+      return run_bf16<256, 16, true>(a, pwide, ctas, *sums, partials, s);
+    }
+    if (a.cols <= 256) return run_f32<32, false>(a, pwide, 1, *sums, partials, s);
+    if (a.cols <= 1024) return run_f32<128, false>(a, pwide, 1, *sums, partials, s);
+    if (a.cols <= 2048) return run_f32<256, false>(a, pwide, 1, *sums, partials, s);
+    if (a.cols <= 4096) return run_f32<512, false>(a, pwide, 1, *sums, partials, s);
+    return run_f32<512, true>(a, pwide, ctas, *sums, partials, s);
   }
   if (a.cols <= 256) return run_cols<32, 8, false>(a, 1, partials, s);
   if (a.cols <= 1024) return run_cols<128, 8, false>(a, 1, partials, s);
@@ -434,8 +456,13 @@ cudaError_t launch_join_backward(const JoinBwdArgs& a, cudaStream_t s) {
   }
   if (a.dpost_gamma == nullptr && a.dpost_beta == nullptr && a.dgate == nullptr && a.dgamma == nullptr && a.dbeta == nullptr)
     return cudaSuccess;
-  k_join_bwd_params<<<unsigned((a.cols + 31) / 32), 1024, 0, s>>>(a, partials, sums);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = dim3(unsigned((a.cols + 31) / 32), 2), cfg.blockDim = dim3(1024), cfg.stream = s;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr, cfg.numAttrs = a.rows > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_join_bwd_params, a, partials, sums);
 }
 
 }  // namespace loco

@@ -18,10 +18,6 @@ namespace {
 template <int G>
 constexpr int kTeamCta = G < 128 ? 128 : G;  // threads of a CTA
 
-// Warps of an SM that a kernel's registers are fitted for (32: 64 registers a thread).
-template <int G, bool LEAN>
-constexpr int kWarpsWanted = G == 32 ? 12 : LEAN ? 32 : 16;
-
 // Pairs of the values of eight columns from their 16-byte words.
 template <bool BF16>
 __device__ __forceinline__ void words_to_pairs(const uint4 (&w)[BF16 ? 1 : 2], Pair* v) {
@@ -67,29 +63,23 @@ struct Vec {
       }
     }
   }
-  __device__ __forceinline__ void values(Pair (&v)[E / 2]) const {
+  // Its columns 8 e to 8 e + 7 as four pairs.
+  __device__ __forceinline__ void eight(int e, Pair (&v)[4]) const {
+    uint4 w[BF16 ? 1 : 2];
 #pragma unroll
-    for (int e = 0; e < E / 8; ++e) {
-      uint4 w[BF16 ? 1 : 2];
-#pragma unroll
-      for (int k = 0; k < (BF16 ? 1 : 2); ++k) w[k] = shared16(at + (e * (BF16 ? 1 : 2) + k) * (kTeamCta<G> * 16));
-      words_to_pairs<BF16>(w, v + e * 4);
-    }
+    for (int k = 0; k < (BF16 ? 1 : 2); ++k) w[k] = shared16(at + (e * (BF16 ? 1 : 2) + k) * (kTeamCta<G> * 16));
+    words_to_pairs<BF16>(w, v);
   }
-  __device__ static __forceinline__ void store(void* p, int64_t row, int64_t ld, int t, int cols, int, const Pair (&v)[E / 2]) {
-    char* q = static_cast<char*>(p) + row * ld * kElem;
+  __device__ static __forceinline__ void store(char* row, int e, int t, int cols, int, const Pair (&v)[4]) {
+    const int c0 = (t + G * e) * 8;
+    float f[8];
+    floats8(v, f);
+    if (c0 + 8 <= cols) {
+      store8(row, c0, BF16, f);
+    } else {
 #pragma unroll
-    for (int e = 0; e < E / 8; ++e) {
-      const int c0 = (t + G * e) * 8;
-      float f[8];
-      floats8(v + e * 4, f);
-      if (c0 + 8 <= cols) {
-        store8(q, c0, BF16, f);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c0 + k < cols) store_elem(q, c0 + k, BF16, f[k]);
-      }
+      for (int k = 0; k < 8; ++k)
+        if (c0 + k < cols) store_elem(row, c0 + k, BF16, f[k]);
     }
   }
 };
@@ -114,26 +104,21 @@ struct Cols {
       for (int i = 0; i < E; ++i) f[i] = t + G * i < cols ? load_elem_rw(q, t + G * i, 0) : 0.0f;
     }
   }
-  __device__ __forceinline__ void values(Pair (&v)[E / 2]) const {
+  __device__ __forceinline__ void eight(int e, Pair (&v)[4]) const {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) v[i] = pair(f[e * 8 + 2 * i], f[e * 8 + 2 * i + 1]);
   }
-  __device__ static __forceinline__ void store(void* p, int64_t row, int64_t ld, int t, int cols, int bf16, const Pair (&v)[E / 2]) {
-    char* q = static_cast<char*>(p) + row * ld * (bf16 ? 2 : 4);
-    float x[E];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const float2 h = halves(v[i]);
-      x[2 * i] = h.x, x[2 * i + 1] = h.y;
-    }
+  __device__ static __forceinline__ void store(char* row, int e, int t, int cols, int bf16, const Pair (&v)[4]) {
+    float x[8];
+    floats8(v, x);
     if (bf16) {
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (t + G * i < cols) store_elem(q, t + G * i, 1, x[i]);
+      for (int i = 0; i < 8; ++i)
+        if (t + G * (e * 8 + i) < cols) store_elem(row, t + G * (e * 8 + i), 1, x[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (t + G * i < cols) store_elem(q, t + G * i, 0, x[i]);
+      for (int i = 0; i < 8; ++i)
+        if (t + G * (e * 8 + i) < cols) store_elem(row, t + G * (e * 8 + i), 0, x[i]);
     }
   }
 };
@@ -175,7 +160,8 @@ __device__ __forceinline__ float warp_total(float v) {
   return v;
 }
 
-// A thread's own E parameters in shared memory: pieces of four, a CTA's threads apart, the `which`-th vector of them.
+// A thread's own parameters in shared memory, where it alone reads them: the `which`-th vector of E of them, in pieces
+// of four, a CTA's threads apart.
 template <int E, int THREADS>
 __device__ __forceinline__ void keep(uint32_t at, int which, const Pair* v) {
 #pragma unroll
@@ -186,10 +172,10 @@ __device__ __forceinline__ void keep(uint32_t at, int which, const Pair* v) {
   }
 }
 template <int E, int THREADS>
-__device__ __forceinline__ void recall(uint32_t at, int which, Pair* v) {
+__device__ __forceinline__ void recall(uint32_t at, int which, int e, Pair (&v)[4]) {
 #pragma unroll
-  for (int i = 0; i < E / 2; i += 2) {
-    const uint4 w = shared16(at + (which * (E / 4) + i / 2) * (THREADS * 16));
+  for (int i = 0; i < 4; i += 2) {
+    const uint4 w = shared16(at + (which * (E / 4) + e * 2 + i / 2) * (THREADS * 16));
     v[i] = pair(__uint_as_float(w.x), __uint_as_float(w.y)), v[i + 1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
   }
 }
@@ -207,49 +193,80 @@ struct Team {
   Board<G, CL>* board;
   int turn, ctas, rank;
 
-  // Values of the team's warps, lane by lane: N of them for each entry lane, lane + 32, ... below warps().
   __device__ __forceinline__ int warps() const { return G / 32 * ctas; }
-  template <int N>
-  __device__ __forceinline__ void tell(const float (&v)[N]) {
-    const int warp = threadIdx.x / 32 % (G / 32), lane = threadIdx.x & 31;
+  // Value `which` of this warp; lane `lane` of `lanes` neighbours tells it to the cluster's CTA of that number.
+  __device__ __forceinline__ void write(int which, int lane, float v) {
+    const int warp = threadIdx.x / 32 % (G / 32);
     if constexpr (CL) {
-      if (lane < ctas) {
-        Board<G, CL>* to = cooperative_groups::this_cluster().map_shared_rank(board, lane);
-#pragma unroll
-        for (int i = 0; i < N; ++i) to->v[turn][i][rank * (G / 32) + warp] = v[i];
-      }
-      cooperative_groups::this_cluster().sync();
+      if (lane < ctas)
+        cooperative_groups::this_cluster().map_shared_rank(board, lane)->v[turn][which][rank * (G / 32) + warp] = v;
     } else {
-      if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) board->v[turn][i][warp] = v[i];
-      }
-      __syncthreads();
+      if (lane == 0) board->v[turn][which][warp] = v;
     }
   }
+  __device__ __forceinline__ void meet() {
+    if constexpr (CL)
+      cooperative_groups::this_cluster().sync();
+    else
+      __syncthreads();
+  }
+  // Sum of the warps' values `which` in each of the 16 lanes of a half warp.
+  __device__ __forceinline__ float read(int which) const {
+    constexpr int kW = G / 32;
+    const int l = threadIdx.x & 15;
+    float v;
+    if constexpr (CL) {
+      v = 0.0f;
+      for (int k = l; k < kW * ctas; k += 16) v += board->v[turn][which][k];
+    } else if constexpr (kW > 16) {
+      v = board->v[turn][which][l] + board->v[turn][which][l + 16];
+    } else {
+      v = board->v[turn][which][l % kW];
+    }
+#pragma unroll
+    for (int o = CL || kW > 16 ? 8 : kW / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  }
   // Sums over the team, the same in all its threads.
-  template <int N>
-  __device__ __forceinline__ void sum(float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_total(v[i]);
+  __device__ __forceinline__ void sum(float (&v)[1]) {
+    v[0] = warp_total(v[0]);
     if constexpr (G > 32) {
-      constexpr int kW = G / 32;
-      const int lane = threadIdx.x & 31;
-      tell(v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if constexpr (CL) {
-          v[i] = 0.0f;
-          for (int k = lane; k < kW * ctas; k += 32) v[i] += board->v[turn][i][k];
-          v[i] = warp_total(v[i]);
-        } else {
-          v[i] = board->v[turn][i][lane % kW];
-#pragma unroll
-          for (int o = kW / 2; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-        }
-      }
+      write(0, threadIdx.x & 31, v[0]);
+      meet();
+      v[0] = read(0);
       turn ^= 1;
     }
+  }
+  // Two values: the halves of a warp take one each after the first step.
+  __device__ __forceinline__ float warp_sum_of_two(float a, float b) {
+    const bool upper = threadIdx.x & 16;
+    float x = (upper ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
+  }
+  __device__ __forceinline__ void sum(float (&v)[2]) {
+    float x = warp_sum_of_two(v[0], v[1]);
+    if constexpr (G > 32) {
+      write((threadIdx.x & 16) / 16, threadIdx.x & 15, x);
+      meet();
+      x = read((threadIdx.x & 16) / 16);
+      turn ^= 1;
+    }
+    v[0] = __shfl_sync(0xFFFFFFFFu, x, 0), v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
+  }
+  __device__ __forceinline__ void sum(float (&v)[3]) {
+    float x = warp_sum_of_two(v[0], v[1]);
+    v[2] = warp_total(v[2]);
+    if constexpr (G > 32) {
+      write((threadIdx.x & 16) / 16, threadIdx.x & 15, x);
+      write(2, threadIdx.x & 31, v[2]);
+      meet();
+      x = read((threadIdx.x & 16) / 16);
+      v[2] = read(2);
+      turn ^= 1;
+    }
+    v[0] = __shfl_sync(0xFFFFFFFFu, x, 0), v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
   }
 };
 
@@ -279,9 +296,11 @@ __device__ __forceinline__ void layer_stats(Team<G, CL>& team, const Pair (&v)[E
   }
   float w[2] = {m, warp_total(total(q2))};
   if constexpr (G > 32) {
+    team.write(0, threadIdx.x & 31, w[0]);
+    team.write(1, threadIdx.x & 31, w[1]);
+    team.meet();
     constexpr int kW = G / 32, kEntries = CL ? kMaxCluster * kW / 32 : 1;
     const int lane = threadIdx.x & 31;
-    team.tell(w);
     const Board<G, CL>& board = *team.board;
     const auto across = [](float x) {
 #pragma unroll

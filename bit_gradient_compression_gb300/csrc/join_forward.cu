@@ -13,18 +13,20 @@ namespace loco {
 
 namespace {
 
-// Rows on their way: the one at work and the next.  Behind them a thread's own gamma and beta lie in shared memory,
-// where it alone reads them: in registers they would cost every second CTA of an SM.
+// Rows on their way: the one at work and the next.  Behind them lie a thread's own parameters: pg and, where there are
+// betas, pb (with the gate in them), gamma and beta.
 constexpr int kStages = 2;
 template <int G, int E, typename RowX, typename RowY>
-constexpr size_t kRing = size_t(kTeamCta<G>) * (kStages * (RowX::kBytes + RowY::kBytes) + 2 * E * sizeof(float));
+size_t ring_bytes(bool betas) {
+  return size_t(kTeamCta<G>) * (kStages * (RowX::kBytes + RowY::kBytes) + (betas ? 4 : 2) * E * sizeof(float));
+}
 
 template <int G, int E, bool CL, typename RowX, typename RowY>
-__global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort> * 32 / kTeamCta<G>)
+__global__ void __launch_bounds__(kTeamCta<G>, (RowX::kShort ? 768 : 512) / kTeamCta<G>)
     k_join_fwd(const JoinFwdArgs args, bool pwide) {
   __shared__ Board<G, CL> board;
   extern __shared__ __align__(16) uint8_t ring[];
-  constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>;
+  constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, C = E / 8;
   JoinFwdArgs a = args;
   const int t = threadIdx.x % G, place = threadIdx.x / G;
   Team<G, CL> team{&board, 0, 1, 0};
@@ -59,65 +61,102 @@ __global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort> * 3
     }
     *rstd = rsqrtf(var + a.eps);
   };
-  // h = a x + w (yh pg + pb), pg and pb with the gate in them, 0 past the row's end
-  Pair pg[E / 2], pb[E / 2], gm[E / 2];
-  params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, gm);
-  params<RowX, E>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, pg);
-  params<RowX, E>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, pb);
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) pg[i] = pg[i] * gm[i], pb[i] = pb[i] * gm[i];
   const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
   constexpr uint32_t kStage = kThreadsCta * (RowX::kBytes + RowY::kBytes), kOwn = kStages * kStage;
-  params<RowX, E>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, gm);
-  keep<E, kThreadsCta>(base + kOwn, 0, gm);
-  params<RowX, E>(a.beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, gm);
-  keep<E, kThreadsCta>(base + kOwn, 1, gm);
+  const bool betas = a.post_beta != nullptr || a.beta != nullptr;
+  {
+    // h = a x + w (yh pg + pb), pg and pb with the gate in them, 0 past the row's end
+    Pair g[E / 2], v[E / 2];
+    params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, g);
+    params<RowX, E>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) v[i] = v[i] * g[i];
+    keep<E, kThreadsCta>(base + kOwn, 0, v);
+    if (betas) {
+      params<RowX, E>(a.post_beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, v);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) v[i] = v[i] * g[i];
+      keep<E, kThreadsCta>(base + kOwn, 2, v);
+      params<RowX, E>(a.beta, t, cols, a.param_bf16, pwide, 0.0f, 0.0f, v);
+      keep<E, kThreadsCta>(base + kOwn, 3, v);
+    }
+    params<RowX, E>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
+    keep<E, kThreadsCta>(base + kOwn, 1, v);
+  }
   RowX xn;
   RowY yn;
+  float wn = 1.0f;
   uint32_t slot = 0;
   const auto fetch = [&](uint32_t row) {
     xn.at = base + slot * kStage, yn.at = xn.at + kThreadsCta * RowX::kBytes;
     if (row < n_rows) {
       xn.load(a.x, row, a.ldx, t, cols, a.x_bf16);
       yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
+      if (a.row_gate != nullptr) wn = __ldg(a.row_gate + row);
     }
     cp_async_commit();
     slot ^= 1;
   };
-  fetch(first);
+  constexpr bool kAhead = RowX::kWide;  // (a row of single columns ahead, in registers, is slower: 777 x 2049 14 -> 19 us)
+  if constexpr (kAhead) fetch(first);
   const Pair a2 = both(a.a);
   for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
     const bool live = row < n_rows;  // (where it is not, the values are an earlier row's, and nothing is stored)
-    Pair x[E / 2], y[E / 2];
-    if constexpr (RowX::kWide) {
-      RowX xc = xn;
-      RowY yc = yn;
+    if constexpr (!kAhead) fetch(row);
+    const RowX xc = xn;
+    const RowY yc = yn;
+    const Pair w = both(a.s * wn);
+    if constexpr (kAhead) {
       fetch(row + step);
       cp_async_wait<1>();
-      xc.values(x), yc.values(y);
-    } else {
-      xn.values(x), yn.values(y);
-      fetch(row + step);
+    }
+    Pair h[E / 2];  // y, then the joined stream
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+      Pair v[4];
+      yc.eight(e, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[e * 4 + i] = v[i];
     }
     float m1 = 0.0f, r1 = 1.0f, m2 = 0.0f, r2 = 1.0f;
-    if (a.post) stats(y, &m1, &r1);
-    const Pair w = both(a.s * (a.row_gate != nullptr && live ? __ldg(a.row_gate + row) : 1.0f));
+    if (a.post) stats(h, &m1, &r1);
     const Pair l1 = both(-m1), f1 = both(r1);
+    char* out = static_cast<char*>(a.h) + row * a.ldh * (a.x_bf16 ? 2 : 4);
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const Pair v = fma((y[i] + l1) * f1, pg[i], pb[i]);
-      x[i] = as_stored(fma(w, v, a2 * x[i]), a.x_bf16);
+    for (int e = 0; e < C; ++e) {
+      Pair x[4], pg[4];
+      xc.eight(e, x);
+      recall<E, kThreadsCta>(base + kOwn, 0, e, pg);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pg[i] = (h[e * 4 + i] + l1) * f1 * pg[i];
+      if (betas) {
+        Pair pb[4];
+        recall<E, kThreadsCta>(base + kOwn, 2, e, pb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pg[i] = pg[i] + pb[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = as_stored(fma(w, pg[i], a2 * x[i]), a.x_bf16), h[e * 4 + i] = x[i];
+      if (live) RowX::store(out, e, t, cols, a.x_bf16, x);
     }
-    if (live) RowX::store(a.h, row, a.ldh, t, cols, a.x_bf16, x);
     if (a.u != nullptr) {
-      stats(x, &m2, &r2);
+      stats(h, &m2, &r2);
       const Pair l2 = both(-m2), f2 = both(r2);
-      Pair g[E / 2], b[E / 2];
-      recall<E, kThreadsCta>(base + kOwn, 0, g);
-      recall<E, kThreadsCta>(base + kOwn, 1, b);
+      out = static_cast<char*>(a.u) + row * a.ldu * (a.y_bf16 ? 2 : 4);
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) x[i] = fma((x[i] + l2) * f2, g[i], b[i]);
-      if (live) RowY::store(a.u, row, a.ldu, t, cols, a.y_bf16, x);
+      for (int e = 0; e < C; ++e) {
+        Pair g[4];
+        recall<E, kThreadsCta>(base + kOwn, 1, e, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = (h[e * 4 + i] + l2) * f2 * g[i];
+        if (betas) {
+          Pair b[4];
+          recall<E, kThreadsCta>(base + kOwn, 3, e, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g[i] = g[i] + b[i];
+        }
+        if (live) RowY::store(out, e, t, cols, a.y_bf16, g);
+      }
     }
     if (a.stats != nullptr && t == 0 && live && team.rank == 0) {
       a.stats[row] = m1, a.stats[a.rows + row] = r1;
@@ -127,7 +166,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, kWarpsWanted<G, RowX::kShort> * 3
 }
 
 // Rows of any length: a CTA of 1024 reads its row for each mean, variance and output.
-__global__ void __launch_bounds__(1024) k_join_fwd_long(const JoinFwdArgs a) {
+__global__ void __launch_bounds__(1024, 1) k_join_fwd_long(const JoinFwdArgs a) {
   __shared__ Board<1024, false> board;
   Team<1024, false> team{&board, 0, 1, 0};
   const auto sum = [&](float v) {
@@ -180,21 +219,23 @@ __global__ void __launch_bounds__(1024) k_join_fwd_long(const JoinFwdArgs a) {
 
 template <int G, int E, bool CL, typename RowX, typename RowY>
 cudaError_t run(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
-  static LayerGrid grid;
+  static LayerGrid grid[2];
   int cap = 0;
   const void* kernel = reinterpret_cast<const void*>(&k_join_fwd<G, E, CL, RowX, RowY>);
-  constexpr size_t kSmem = kRing<G, E, RowX, RowY>;
-  const cudaError_t e = layer_grid(grid, kernel, kTeamCta<G>, kSmem, kSmem, &cap);
+  const bool betas = a.post_beta != nullptr || a.beta != nullptr;
+  const size_t smem = ring_bytes<G, E, RowX, RowY>(betas);
+  const cudaError_t e = layer_grid(grid[betas], kernel, kTeamCta<G>, smem, ring_bytes<G, E, RowX, RowY>(true), &cap);
   if (e != cudaSuccess) return e;
-  return launch_teams(k_join_fwd<G, E, CL, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeamCta<G> / G, ctas, kSmem, s, a,
-                      pwide);
+  return launch_teams(k_join_fwd<G, E, CL, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeamCta<G> / G, ctas, smem, s, a, pwide);
 }
+template <int G, bool CL>
+cudaError_t run_f32(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
+  return a.y_bf16 ? run<G, 8, CL, Vec<G, 8, false>, Vec<G, 8, true>>(a, pwide, ctas, s)
+                  : run<G, 8, CL, Vec<G, 8, false>, Vec<G, 8, false>>(a, pwide, ctas, s);
+}
+// bf16 rows: sixteen columns to a thread, so that half as many warps add up their sums.
 template <int G, int E, bool CL>
-cudaError_t run_vec(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
-  if (!a.x_bf16) {
-    return a.y_bf16 ? run<G, E, CL, Vec<G, E, false>, Vec<G, E, true>>(a, pwide, ctas, s)
-                    : run<G, E, CL, Vec<G, E, false>, Vec<G, E, false>>(a, pwide, ctas, s);
-  }
+cudaError_t run_bf16(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
   return run<G, E, CL, Vec<G, E, true>, Vec<G, E, true>>(a, pwide, ctas, s);
 }
 template <int G, int E, bool CL>
@@ -219,12 +260,19 @@ cudaError_t launch_join_forward(const JoinFwdArgs& a, cudaStream_t s) {
   const bool pwide = on16(a.post_gamma) && on16(a.post_beta) && on16(a.gate) && on16(a.gamma) && on16(a.beta);
   const int ctas = int((a.cols + 4095) / 4096);
   if (ctas > kMaxCluster) return run_long(a, s);
+  if (wide && a.x_bf16) {
+    if (a.cols <= 256) return run_bf16<32, 8, false>(a, pwide, 1, s);
+    if (a.cols <= 512) return run_bf16<32, 16, false>(a, pwide, 1, s);
+    if (a.cols <= 2048) return run_bf16<128, 16, false>(a, pwide, 1, s);
+    if (a.cols <= 4096) return run_bf16<256, 16, false>(a, pwide, 1, s);
+    return run_bf16<256, 16, true>(a, pwide, ctas, s);
+  }
   if (wide) {
-    if (a.cols <= 256) return run_vec<32, 8, false>(a, pwide, 1, s);
-    if (a.cols <= 1024) return run_vec<128, 8, false>(a, pwide, 1, s);
-    if (a.cols <= 2048) return run_vec<256, 8, false>(a, pwide, 1, s);
-    if (a.cols <= 4096) return run_vec<512, 8, false>(a, pwide, 1, s);
-    return run_vec<512, 8, true>(a, pwide, ctas, s);
+    if (a.cols <= 256) return run_f32<32, false>(a, pwide, 1, s);
+    if (a.cols <= 1024) return run_f32<128, false>(a, pwide, 1, s);
+    if (a.cols <= 2048) return run_f32<256, false>(a, pwide, 1, s);
+    if (a.cols <= 4096) return run_f32<512, false>(a, pwide, 1, s);
+    return run_f32<512, true>(a, pwide, ctas, s);
   }
   if (a.cols <= 256) return run_cols<32, 8, false>(a, 1, s);
   if (a.cols <= 1024) return run_cols<128, 8, false>(a, 1, s);

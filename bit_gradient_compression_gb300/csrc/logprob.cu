@@ -123,12 +123,14 @@ __device__ __forceinline__ float value_before(uint32_t k) {
 
 // A warp's list of candidates.
 struct List {
-  Key* keys;   // kListed + 32 * 8
+  Key* keys;   // kListed + 32 * 4
   Key* kept;   // LOCO_MAX_TOP
   int* count;
   Floors floors;
   int top, warp;
   float thr;   // what is not above it is not needed
+  static constexpr int kEach = LOCO_MAX_TOP / kWarps;
+  uint32_t best[kEach];  // largest of the noted maxima, in order
 
   // Keeps the `top` largest, in order.
   __device__ __forceinline__ void order(int lane) {
@@ -150,16 +152,42 @@ struct List {
       const float t = key_value(keys[top - 1]);
       if (t > thr) thr = t;
     }
-    if (left >= floors.each && lane == 0) floors.at[warp] = uint32_t(keys[floors.each - 1] >> 32);
   }
   // Appends the values of a vector that are above the threshold (all lanes of the warp; v: kVec values from column on).
+  // An order in its midst raises the threshold for later vectors only: of one vector, a lane's last columns are before
+  // the next lane's first ones, and would win a tie with them.
   template <int N>
   __device__ __forceinline__ void append(const float (&v)[N], int64_t column, int lane) {
+    const float limit = thr;
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (v[k] > thr) keys[atomicAdd(count, 1)] = key_of(v[k], column + k);
-    __syncwarp();
-    if (*count > kListed) order(lane);
+    for (int k = 0; k < N; ++k) {
+      if (v[k] > limit) keys[atomicAdd(count, 1)] = key_of(v[k], column + k);
+      if (k % 4 == 3 || k == N - 1) {  // of four values a lane there is room
+        __syncwarp();
+        if (*count > kListed) order(lane);
+      }
+    }
+  }
+  // Notes a tile's candidates among the warp's floor: the each-th largest of the lanes' maxima and of those before (a
+  // lower bound, as a lane may have had more than one).
+  __device__ __forceinline__ void note(float lane_max, int lane) {
+    uint32_t u = in_order(lane_max);
+    u = u > 0x007FFFFFu ? u : 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (i >= floors.each) break;
+      uint32_t k = __reduce_max_sync(0xFFFFFFFFu, u);
+      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, u == k)) - 1) u = 0;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {  // into its place, the least falls out
+        const uint32_t above = max(best[j], k);
+        k = min(best[j], k), best[j] = above;
+      }
+    }
+    uint32_t f = best[0];
+#pragma unroll
+    for (int j = 1; j < kEach; ++j) f = j < floors.each ? best[j] : f;
+    if (lane == 0) floors.at[warp] = f;
   }
   // What the lanes' maxima of the first tile say: at least `top` of the warp's values are not below the top-th of them.
   __device__ __forceinline__ void first(float lane_max, int lane) {
@@ -174,7 +202,6 @@ struct List {
     }
     const float t = value_before(__shfl_sync(0xFFFFFFFFu, u, top - 1));
     if (t > thr) thr = t;
-    if (lane == floors.each - 1 && u > 0x007FFFFFu) floors.at[warp] = u;
   }
   // The warps' floors together: `top` values of the row are not below the least of them.  (One read early or late
   // is only a lower one: what is left out is never needed.)
@@ -185,22 +212,35 @@ struct List {
   }
 };
 
+constexpr int kMaxParts = 8;  // CTAs of a cluster
 template <bool TOP>
 struct Shared {
   Part part[kWarps];
-  Part cta;
+  Part ctas[kMaxParts];
 };
 template <>
 struct Shared<true> {
   Part part[kWarps];
-  Part cta;
-  Key keys[kWarps][kListed + 256];
+  Part ctas[kMaxParts];
+  Key lists[kMaxParts * LOCO_MAX_TOP];  // the CTAs' largest
+  Key keys[kWarps][kListed + 128];
   Key kept[kWarps][LOCO_MAX_TOP];
   Key chosen[kWarps * kListed];  // of all warps' lists, what can be among the largest
   Key best[LOCO_MAX_TOP];
   int count[kWarps], n_chosen;
   uint32_t floors[kWarps], least[kWarps];
 };
+
+// Eight parts, each held by every eighth lane, put together.
+__device__ __forceinline__ Part join_eight(Part x, int lane, float c) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    const Part other{__shfl_xor_sync(0xFFFFFFFFu, x.m, o), __shfl_xor_sync(0xFFFFFFFFu, x.s, o),
+                     __shfl_xor_sync(0xFFFFFFFFu, x.d, o)};
+    x = lane & o ? join(other, x, c) : join(x, other, c);
+  }
+  return x;
+}
 
 // The `top` largest of chosen[0, n), in order, by all threads of the CTA; `best` was 0.
 __device__ __forceinline__ void choose(const Key* chosen, int n, int top, Key* best) {
@@ -215,14 +255,16 @@ __device__ __forceinline__ void choose(const Key* chosen, int n, int top, Key* b
 
 // WPR: warps of a row's part (1: a CTA takes eight rows, 8: one).  CLUSTER: several CTAs to a row.
 template <bool BF16, int WPR, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs a) {
+__global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdArgs a) {
   __shared__ Shared<TOP> sh;
+  extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kElem = BF16 ? 2 : 4, V = kVec<BF16>, kTeam = 32 * WPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, t = threadIdx.x % kTeam;
   int parts = 1, me = 0;
   if constexpr (CLUSTER) {
     parts = int(cg::this_cluster().num_blocks());
     me = int(cg::this_cluster().block_rank());
+    cg::this_cluster().barrier_arrive();  // waited for before the first CTA's memory is written
   }
   const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * kWarps + warp : int64_t(blockIdx.x) / parts;
   if (WPR == 1 && row >= a.rows) return;  // whole warps, and no barrier follows
@@ -238,7 +280,7 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
   if constexpr (TOP) {
     // a row of one warp has its floor to itself
     const Floors floors{WPR == 1 ? &sh.floors[warp] : sh.floors, WPR, (a.top + WPR - 1) / WPR};
-    list = List{sh.keys[warp], sh.kept[warp], &sh.count[warp], floors, a.top, WPR == 1 ? 0 : warp, -INFINITY};
+    list = List{sh.keys[warp], sh.kept[warp], &sh.count[warp], floors, a.top, WPR == 1 ? 0 : warp, -INFINITY, {0, 0, 0, 0}};
     if (lane == 0) sh.count[warp] = 0, sh.floors[warp] = 0;
     __syncwarp();
     if constexpr (WPR > 1) {
@@ -259,23 +301,37 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
   };
   if (me == 0 && shape.head > 0 && t < 32) take_one(0, int(shape.head));
 
-  uint4 next[kVectors];
+  // Tiles of four vectors a thread; the next one is on its way to shared memory (cp.async by the thread that will read
+  // it, so no barrier is needed).
   const uint4 none = BF16 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
                           : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  constexpr uint32_t kPiece = kThreadsLp * 16, kStage = kVectors * kPiece;
+  const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
+  uint32_t slot = 0;
   const auto fetch = [&](int64_t from) {
 #pragma unroll
-    for (int q = 0; q < kVectors; ++q) next[q] = from + q * kTeam < v_hi ? __ldcs(vec + from + q * kTeam) : none;
+    for (int q = 0; q < kVectors; ++q) {
+      if (from + q * kTeam < v_hi)
+        copy_to_shared16(base + slot + q * kPiece, vec + from + q * kTeam);
+      else
+        to_shared16(base + slot + q * kPiece, none);
+    }
+    cp_async_commit();
+    slot ^= kStage;
   };
   fetch(v_lo + t);
   bool first = true;
   for (int64_t i = v_lo; i < v_hi; i += kVectors * kTeam) {
+    const uint32_t at = base + (slot ^ kStage);
+    fetch(i + kVectors * kTeam + t);
+    cp_async_wait<1>();
     uint4 w[kVectors];
 #pragma unroll
-    for (int q = 0; q < kVectors; ++q) w[q] = next[q];
-    fetch(i + kVectors * kTeam + t);
-    float top[kVectors], m = mine.m;
+    for (int q = 0; q < kVectors; ++q) w[q] = shared16(at + q * kPiece);
+    float tile = largest<BF16>(w[0]);
 #pragma unroll
-    for (int q = 0; q < kVectors; ++q) top[q] = largest<BF16>(w[q]), m = max_nan(m, top[q]);
+    for (int q = 1; q < kVectors; ++q) tile = max_nan(tile, largest<BF16>(w[q]));
+    const float m = max_nan(mine.m, tile);
     const float down = max_nan((mine.m - m) * c, kLeast), f = exp2_f(down);
     Pair s2 = pair(f * mine.s, 0.0f), d2 = pair(f * fmaf(mine.s, down, mine.d), 0.0f);
     const Pair less = pair(-m, -m);
@@ -295,9 +351,6 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
     const float2 s = halves(s2), d = halves(d2);
     mine = Part{m, s.x + s.y, d.x + d.y};
     if constexpr (TOP) {
-      float tile = top[0];
-#pragma unroll
-      for (int q = 1; q < kVectors; ++q) tile = max_nan(tile, top[q]);
       if (first)
         list.first(tile, lane);
       else if (WPR > 1)
@@ -306,9 +359,10 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
       if (__any_sync(0xFFFFFFFFu, tile > list.thr)) {
 #pragma unroll
         for (int q = 0; q < kVectors; ++q) {
-          if (!__any_sync(0xFFFFFFFFu, top[q] > list.thr)) continue;
+          const uint4 again = shared16(at + q * kPiece);  // (not kept in registers for this)
+          if (!__any_sync(0xFFFFFFFFu, largest<BF16>(again) > list.thr)) continue;
           Pair v[V / 2];
-          to_pairs<BF16>(w[q], v);
+          to_pairs<BF16>(again, v);
           float x[V];
 #pragma unroll
           for (int k = 0; k < V / 2; ++k) {
@@ -317,7 +371,11 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
           }
           list.append(x, shape.head + (i + q * kTeam + t) * V, lane);
         }
-        list.order(lane);  // the thresholds move up with every tile that had something: later ones seldom have
+        // the thresholds move up with every tile that had something: later ones seldom have
+        if (WPR > 1)
+          list.note(tile, lane);
+        else
+          list.order(lane);
       }
     }
   }
@@ -347,9 +405,7 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
       if (lane == 0) sh.least[warp] = in_order(list.thr);
     }
     __syncthreads();
-    all = sh.part[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) all = join(all, sh.part[w], c);
+    all = join_eight(sh.part[lane % kWarps], lane, c);
     if constexpr (TOP) {
       // no value below the highest of the warps' thresholds can be among the largest; each list holds kListed at most
       const uint32_t least = __reduce_max_sync(0xFFFFFFFFu, sh.least[lane % kWarps]);
@@ -361,24 +417,22 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_fwd(const LogprobFwdArgs
       best = sh.best;
     }
     if constexpr (CLUSTER) {
-      if (threadIdx.x == 0) sh.cta = all;
+      // everything goes to the first CTA
       const auto cluster = cg::this_cluster();
-      cluster.sync();
-      if (me == 0) {
-        all = sh.cta;
-        for (int p = 1; p < parts; ++p) all = join(all, *cluster.map_shared_rank(&sh.cta, p), c);
-        if constexpr (TOP) {
-          // the CTAs' lists beside one another (0 where one has fewer)
-          if (threadIdx.x < parts * a.top)
-            sh.chosen[threadIdx.x] = cluster.map_shared_rank(sh.best, threadIdx.x / a.top)[threadIdx.x % a.top];
-        }
+      cluster.barrier_wait();
+      Shared<TOP>* to = cluster.map_shared_rank(&sh, 0);
+      if (threadIdx.x == 0) to->ctas[me] = all;
+      if constexpr (TOP) {
+        __syncthreads();
+        if (threadIdx.x < a.top) to->lists[me * a.top + threadIdx.x] = sh.best[threadIdx.x];
       }
-      cluster.sync();  // nobody leaves before it has been read
+      cluster.sync();
       if (me != 0) return;
+      all = join_eight(lane % kMaxParts < parts ? sh.ctas[lane % kMaxParts] : Part{kLowest, 0.0f, 0.0f}, lane, c);
       if constexpr (TOP) {
         if (threadIdx.x < LOCO_MAX_TOP) sh.best[threadIdx.x] = 0;
         __syncthreads();
-        choose(sh.chosen, parts * a.top, a.top, sh.best);
+        choose(sh.lists, parts * a.top, a.top, sh.best);
       }
     }
     if constexpr (TOP) __syncthreads();
@@ -416,7 +470,13 @@ cudaError_t run_fwd(const LogprobFwdArgs& a, int parts, cudaStream_t s) {
   cudaLaunchAttribute attr;
   cfg.gridDim = dim3(unsigned(WPR == 1 ? (a.rows + kWarps - 1) / kWarps : a.rows * parts));
   cfg.blockDim = dim3(kThreadsLp);
+  cfg.dynamicSmemBytes = 2 * kVectors * kThreadsLp * 16;
   cfg.stream = s;
+  static LayerGrid grid;  // (asked for the memory that a CTA takes)
+  int cap = 0;
+  const cudaError_t e = layer_grid(grid, reinterpret_cast<const void*>(&k_logprob_fwd<BF16, WPR, TOP, CLUSTER>), kThreadsLp,
+                                   cfg.dynamicSmemBytes, cfg.dynamicSmemBytes + sizeof(Shared<TOP>), &cap);
+  if (e != cudaSuccess) return e;
   if (CLUSTER) {
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = unsigned(parts), attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
