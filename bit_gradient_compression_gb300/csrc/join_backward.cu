@@ -19,14 +19,15 @@ namespace {
 // Rows on their way: the one at work and the next.  Behind them a thread's own parameters (gm and pg below).
 constexpr int kStages = 2;
 template <int G, int E, typename RowX, typename RowY>
-constexpr size_t kRing = size_t(kTeamCta<G>) * (kStages * 2 * (RowX::kBytes + RowY::kBytes) + 2 * E * sizeof(float));
+constexpr size_t kRing = size_t(kStages) * 2 * (RowX::kBytes + RowY::kBytes) + size_t(kTeamCta<G>) * 2 * E * sizeof(float);
 
-// SUMS: 4, or 2 where neither sum c nor sum du is wanted (a RMS norm without betas).
-template <int G, int E, bool CL, int SUMS, typename RowX, typename RowY>
+// SUMS: 4, or 2 where neither sum c nor sum du is wanted (no betas).
+// RMS: no mean is taken, and the reciprocal roots stay out of the products.  (It changes how dx and dy round, SUMS does
+// not: they do not depend on which parameters' gradients are asked for.)
+template <int G, int E, bool CL, int SUMS, bool RMS, typename RowX, typename RowY>
 __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G == 32) ? 256 : 512) / kTeamCta<G>)
     k_join_bwd(const JoinBwdArgs args, bool pwide) {
   __shared__ Board<G, CL> board;
-  extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, P = E / 2, C = E / 8;
   JoinBwdArgs a = args;
   const int t = threadIdx.x % G, place = threadIdx.x / G;
@@ -47,6 +48,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
   }
   const int64_t rest = a.cols - c0;
   const int cols = rest <= 0 ? 0 : rest < G * E ? int(rest) : G * E;
+  const Edges edges{n_rows - 1, rest < (1 << 30) ? int(rest) : 1 << 30, c0 == 0};
   const float inv_cols = 1.0f / float(a.cols);
   const bool level = !a.rms;
   const Pair zero = both(0.0f);
@@ -58,8 +60,8 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
   }
   // q = du gm ; p = t w pg, pg with the gate and the scale in it, 0 past the row's end: whatever else a thread
   // has there (deviations of nothing from a mean) then reaches no sum of the row
-  const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
-  constexpr uint32_t kStage = kThreadsCta * 2 * (RowX::kBytes + RowY::kBytes), kOwn = kStages * kStage;
+  const uint32_t base = threadIdx.x * 16;
+  constexpr uint32_t kStage = 2 * (RowX::kBytes + RowY::kBytes), kOwn = kStages * kStage;
   {
     Pair g[P], v[P];
     params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, g);
@@ -75,15 +77,15 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
   float m1n = 0.0f, r1n = 1.0f, m2n = 0.0f, r2n = 1.0f, wn = 1.0f;
   uint32_t slot = 0;
   const auto fetch = [&](uint32_t row) {
-    dhn.at = base + slot * kStage, hn.at = dhn.at + kThreadsCta * RowX::kBytes;
-    dun.at = hn.at + kThreadsCta * RowX::kBytes, yn.at = dun.at + kThreadsCta * RowY::kBytes;
+    dhn.at = base + slot * kStage, hn.at = dhn.at + RowX::kBytes;
+    dun.at = hn.at + RowX::kBytes, yn.at = dun.at + RowY::kBytes;
     if (row < n_rows) {
-      if (a.dh != nullptr) dhn.load(a.dh, row, a.lddh, t, cols, a.x_bf16);
+      if (a.dh != nullptr) dhn.load(a.dh, row, a.lddh, t, cols, edges);
       if (a.du != nullptr) {
-        dun.load(a.du, row, a.lddu, t, cols, a.y_bf16);
-        hn.load(a.h, row, a.ldh, t, cols, a.x_bf16);
+        dun.load(a.du, row, a.lddu, t, cols, edges);
+        hn.load(a.h, row, a.ldh, t, cols, edges);
       }
-      if (a.y != nullptr) yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
+      if (a.y != nullptr) yn.load(a.y, row, a.ldy, t, cols, edges);
       if (a.post) m1n = __ldg(a.stats + row), r1n = __ldg(a.stats + a.rows + row);
       if (a.du != nullptr) m2n = __ldg(a.stats + 2 * a.rows + row), r2n = __ldg(a.stats + 3 * a.rows + row);
       if (a.row_gate != nullptr) wn = __ldg(a.row_gate + row);
@@ -92,18 +94,19 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
     slot ^= 1;
   };
   cudaTriggerProgrammaticLaunchCompletion();  // the parameters' kernel may wait on its SMs
-  constexpr bool kAhead = RowX::kWide;  // single columns leave no registers for a row ahead
-  if constexpr (kAhead) fetch(first);
+  fetch(first);
   const Pair a2 = both(a.a);
   for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
     const bool live = row < n_rows;
-    if constexpr (!kAhead) fetch(row);
     RowX dhc = dhn, hc = hn;
     RowY duc = dun, yc = yn;
     const float m1 = m1n, r1 = r1n, m2 = m2n, r2 = r2n, w = wn;
-    if constexpr (kAhead) {
-      fetch(row + step);
-      cp_async_wait<1>();
+    fetch(row + step);
+    cp_async_wait<1>();
+    if (live) {
+      if (a.dh != nullptr) dhc.settle(t, cols);
+      if (a.du != nullptr) duc.settle(t, cols), hc.settle(t, cols);
+      if (a.y != nullptr) yc.settle(t, cols);
     }
     // What a value takes part in is formed anew from shared memory in each of the three passes over the row's
     // columns: registers hold the sums over rows and t.
@@ -117,6 +120,15 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
           Pair du[4], h[4], g[4];
           duc.eight(e, du), hc.eight(e, h);
           recall<E, kThreadsCta>(base + kOwn, 0, e, g);
+          if constexpr (RMS) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s1 = fma(du[i] * g[i], h[i], s1);  // over r2
+              sums[1][e * 4 + i] = fma(du[i], h[i] * f, sums[1][e * 4 + i]);
+              if constexpr (SUMS == 4) sums[3][e * 4 + i] = sums[3][e * 4 + i] + du[i];
+            }
+            continue;
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             h[i] = (h[i] + less) * f;
@@ -129,13 +141,19 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
         }
         s[0] = total(s0), s[1] = total(s1);
       }
-      float two[2] = {s[0], s[1]};
-      team.sum(two);
-      s[0] = level ? -two[0] * inv_cols : 0.0f, s[1] = -two[1] * inv_cols;
+      if constexpr (RMS) {
+        float one[1] = {s[1]};
+        team.sum(one);
+        s[1] = -one[0] * inv_cols * r2 * r2;  // of h in (t - dh) / r2
+      } else {
+        float two[2] = {s[0], s[1]};
+        team.sum(two);
+        s[0] = level ? -two[0] * inv_cols : 0.0f, s[1] = -two[1] * inv_cols;
+      }
     }
     Pair dt[P];
     if (live) {
-      const Pair l2 = both(-m2), f2 = both(r2), c1 = both(s[0]), c2 = both(s[1]), l1 = both(-m1), f1 = both(r1), w2 = both(w);
+      const Pair l2 = both(-m2), f2 = both(r2), c1 = both(s[0]), c2 = both(s[1]), l1 = both(-m1), f1 = both(r1), w2 = both(RMS ? w * r1 : w);
       Pair s0 = zero, s1 = zero, s2 = zero;
       char* out = static_cast<char*>(a.dx) + row * a.lddx * (a.x_bf16 ? 2 : 4);
 #pragma unroll
@@ -152,11 +170,16 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
           duc.eight(e, du), hc.eight(e, h);
           recall<E, kThreadsCta>(base + kOwn, 0, e, g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = fma(f2, fma((h[i] + l2) * f2, c2, fma(du[i], g[i], c1)), v[i]);
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (RMS)
+              v[i] = fma(f2, fma(h[i], c2, du[i] * g[i]), v[i]);
+            else
+              v[i] = fma(f2, fma((h[i] + l2) * f2, c2, fma(du[i], g[i], c1)), v[i]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) dt[e * 4 + i] = v[i], v[i] = a2 * v[i];
-        RowX::store(out, e, t, cols, a.x_bf16, v);
+        RowX::store(out, e, t, cols, v);
         if (a.y != nullptr) {
           yc.eight(e, h);
         } else {
@@ -166,12 +189,18 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
         recall<E, kThreadsCta>(base + kOwn, 1, e, g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const Pair yh = (h[i] + l1) * f1, c = dt[e * 4 + i] * w2;
-          sums[0][e * 4 + i] = fma(c, yh, sums[0][e * 4 + i]);
-          if constexpr (SUMS == 4) sums[2][e * 4 + i] = sums[2][e * 4 + i] + c;
           const Pair p = dt[e * 4 + i] * g[i];  // over w
-          s0 = s0 + p;
-          s1 = fma(p, yh, s1);
+          if constexpr (RMS) {
+            sums[0][e * 4 + i] = fma(dt[e * 4 + i], h[i] * w2, sums[0][e * 4 + i]);
+            if constexpr (SUMS == 4) sums[2][e * 4 + i] = fma(dt[e * 4 + i], both(w), sums[2][e * 4 + i]);
+            s1 = fma(p, h[i], s1);  // over r1
+          } else {
+            const Pair yh = (h[i] + l1) * f1, c = dt[e * 4 + i] * w2;
+            sums[0][e * 4 + i] = fma(c, yh, sums[0][e * 4 + i]);
+            if constexpr (SUMS == 4) sums[2][e * 4 + i] = sums[2][e * 4 + i] + c;
+            s0 = s0 + p;
+            s1 = fma(p, yh, s1);
+          }
         }
       }
       if (a.drow_gate != nullptr && a.post_beta != nullptr) {
@@ -184,7 +213,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
 #pragma unroll
         for (int i = 0; i < P; ++i) s2 = fma(b[i], v[i], s2);
       }
-      s[0] = total(s0), s[1] = total(s1), s[2] = total(s2);
+      s[0] = total(s0), s[1] = RMS ? total(s1) * r1 : total(s1), s[2] = total(s2);
     } else {
       s[0] = s[1] = s[2] = 0.0f;
     }
@@ -192,13 +221,19 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
       team.sum(s);
       if (t == 0 && live && team.rank == 0) a.drow_gate[row] = fmaf(a.s, s[2], s[1]);
     } else if (a.post) {
-      float two[2] = {s[0], s[1]};
-      team.sum(two);
-      s[0] = two[0], s[1] = two[1];
+      if constexpr (RMS) {
+        float one[1] = {s[1]};
+        team.sum(one);
+        s[1] = one[0];
+      } else {
+        float two[2] = {s[0], s[1]};
+        team.sum(two);
+        s[0] = two[0], s[1] = two[1];
+      }
     }
     if (!live) continue;  // whole teams
     {
-      const Pair c1 = both(a.post && level ? -s[0] * inv_cols : 0.0f), c2 = both(a.post ? -s[1] * inv_cols : 0.0f);
+      const Pair c1 = both(a.post && level ? -s[0] * inv_cols : 0.0f), c2 = both(a.post ? -s[1] * inv_cols * (RMS ? r1 : 1.0f) : 0.0f);
       const Pair l1 = both(-m1), f1 = both(r1), f = both(w * r1);
       char* out = static_cast<char*>(a.dy) + row * a.lddy * (a.y_bf16 ? 2 : 4);
 #pragma unroll
@@ -208,12 +243,17 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
         if (a.post) {
           yc.eight(e, y);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) g[i] = f * fma((y[i] + l1) * f1, c2, fma(dt[e * 4 + i], g[i], c1));
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (RMS)
+              g[i] = f * fma(y[i], c2, dt[e * 4 + i] * g[i]);
+            else
+              g[i] = f * fma((y[i] + l1) * f1, c2, fma(dt[e * 4 + i], g[i], c1));
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) g[i] = f * (dt[e * 4 + i] * g[i]);
         }
-        RowY::store(out, e, t, cols, a.y_bf16, g);
+        RowY::store(out, e, t, cols, g);
       }
     }
   }
@@ -232,7 +272,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
       }
     }
   } else {
-    float(*rows)[G * E] = reinterpret_cast<float(*)[G * E]>(ring + kOwn);  // (no thread needs its parameters any more)
+    float(*rows)[G * E] = reinterpret_cast<float(*)[G * E]>(ring() + kOwn);  // (no thread needs its parameters any more)
 #pragma unroll
     for (int k = 0; k < SUMS; ++k) {
       __syncthreads();
@@ -368,11 +408,11 @@ __global__ void __launch_bounds__(1024) k_join_bwd_params(const JoinBwdArgs a, i
   }
 }
 
-template <int G, int E, bool CL, int SUMS, typename RowX, typename RowY>
+template <int G, int E, bool CL, int SUMS, bool RMS, typename RowX, typename RowY>
 cudaError_t run(const JoinBwdArgs& a, bool pwide, int ctas, int* partials, cudaStream_t s) {
   static LayerGrid grid;
   int cap = 0;
-  const void* kernel = reinterpret_cast<const void*>(&k_join_bwd<G, E, CL, SUMS, RowX, RowY>);
+  const void* kernel = reinterpret_cast<const void*>(&k_join_bwd<G, E, CL, SUMS, RMS, RowX, RowY>);
   constexpr size_t kSmem = kRing<G, E, RowX, RowY>;
   const cudaError_t e = layer_grid(grid, kernel, kTeamCta<G>, kSmem, kSmem, &cap);
   if (e != cudaSuccess) return e;
@@ -384,26 +424,32 @@ cudaError_t run(const JoinBwdArgs& a, bool pwide, int ctas, int* partials, cudaS
     if (cap > most) cap = most > ctas ? int(most) : ctas;
   }
   *partials = int(team_ctas(a.rows, cap, kTeams, ctas) / ctas);
-  return launch_teams(k_join_bwd<G, E, CL, SUMS, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeams, ctas, kSmem, s, a, pwide);
+  return launch_teams(k_join_bwd<G, E, CL, SUMS, RMS, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeams, ctas, kSmem, s, a, pwide);
 }
 template <int G, int E, bool CL, typename RowX, typename RowY>
 cudaError_t run_sums(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* partials, cudaStream_t s) {
-  return sums == 4 ? run<G, E, CL, 4, RowX, RowY>(a, pwide, ctas, partials, s)
-                   : run<G, E, CL, 2, RowX, RowY>(a, pwide, ctas, partials, s);
+  if (!a.rms) return run<G, E, CL, 4, false, RowX, RowY>(a, pwide, ctas, partials, s);
+  return sums == 4 ? run<G, E, CL, 4, true, RowX, RowY>(a, pwide, ctas, partials, s)
+                   : run<G, E, CL, 2, true, RowX, RowY>(a, pwide, ctas, partials, s);
 }
 template <int G, bool CL>
 cudaError_t run_f32(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* partials, cudaStream_t s) {
-  return a.y_bf16 ? run_sums<G, 8, CL, Vec<G, 8, false>, Vec<G, 8, true>>(a, pwide, ctas, sums, partials, s)
-                  : run_sums<G, 8, CL, Vec<G, 8, false>, Vec<G, 8, false>>(a, pwide, ctas, sums, partials, s);
+  return a.y_bf16 ? run_sums<G, 8, CL, Vec<G, 8, false, false>, Vec<G, 8, true, false>>(a, pwide, ctas, sums, partials, s)
+                  : run_sums<G, 8, CL, Vec<G, 8, false, false>, Vec<G, 8, false, false>>(a, pwide, ctas, sums, partials, s);
 }
 // bf16 rows: sixteen columns to a thread, so that half as many warps add up their sums.
 template <int G, int E, bool CL>
 cudaError_t run_bf16(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* partials, cudaStream_t s) {
-  return run_sums<G, E, CL, Vec<G, E, true>, Vec<G, E, true>>(a, pwide, ctas, sums, partials, s);
+  return run_sums<G, E, CL, Vec<G, E, true, false>, Vec<G, E, true, false>>(a, pwide, ctas, sums, partials, s);
 }
 template <int G, int E, bool CL>
-cudaError_t run_cols(const JoinBwdArgs& a, int ctas, int* partials, cudaStream_t s) {
-  return run<G, E, CL, 4, Cols<G, E>, Cols<G, E>>(a, false, ctas, partials, s);
+cudaError_t run_any(const JoinBwdArgs& a, bool pwide, int ctas, int* partials, cudaStream_t s) {
+  if (a.x_bf16) {
+    return a.y_bf16 ? run<G, E, CL, 4, false, Vec<G, E, true, true>, Vec<G, E, true, true>>(a, pwide, ctas, partials, s)
+                    : run<G, E, CL, 4, false, Vec<G, E, true, true>, Vec<G, E, false, true>>(a, pwide, ctas, partials, s);
+  }
+  return a.y_bf16 ? run<G, E, CL, 4, false, Vec<G, E, false, true>, Vec<G, E, true, true>>(a, pwide, ctas, partials, s)
+                  : run<G, E, CL, 4, false, Vec<G, E, false, true>, Vec<G, E, false, true>>(a, pwide, ctas, partials, s);
 }
 cudaError_t run_long(const JoinBwdArgs& a, int* partials, cudaStream_t s) {
   static LayerGrid grid;
@@ -426,7 +472,7 @@ cudaError_t rows_kernel(const JoinBwdArgs& a, int* sums, int* partials, cudaStre
   *sums = 4;
   if (ctas > kMaxCluster) return run_long(a, partials, s);
   if (wide) {
-    if (a.dbeta == nullptr && a.dpost_beta == nullptr && (a.dgate == nullptr || a.post_beta == nullptr)) *sums = 2;
+    if (a.rms && a.dbeta == nullptr && a.dpost_beta == nullptr && (a.dgate == nullptr || a.post_beta == nullptr)) *sums = 2;
     if (a.x_bf16) {
       if (a.cols <= 256) return run_bf16<32, 8, false>(a, pwide, 1, *sums, partials, s);
       if (a.cols <= 512) return run_bf16<32, 16, false>(a, pwide, 1, *sums, partials, s);
@@ -440,10 +486,10 @@ cudaError_t rows_kernel(const JoinBwdArgs& a, int* sums, int* partials, cudaStre
     if (a.cols <= 4096) return run_f32<512, false>(a, pwide, 1, *sums, partials, s);
     return run_f32<512, true>(a, pwide, ctas, *sums, partials, s);
   }
-  if (a.cols <= 256) return run_cols<32, 8, false>(a, 1, partials, s);
-  if (a.cols <= 1024) return run_cols<128, 8, false>(a, 1, partials, s);
-  if (a.cols <= 4096) return run_cols<512, 8, false>(a, 1, partials, s);
-  return run_cols<512, 8, true>(a, ctas, partials, s);
+  if (a.cols <= 256) return run_any<32, 8, false>(a, pwide, 1, partials, s);
+  if (a.cols <= 1024) return run_any<128, 8, false>(a, pwide, 1, partials, s);
+  if (a.cols <= 4096) return run_any<512, 8, false>(a, pwide, 1, partials, s);
+  return run_any<512, 8, true>(a, pwide, ctas, partials, s);
 }
 
 }  // namespace

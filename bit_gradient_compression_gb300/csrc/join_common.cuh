@@ -1,8 +1,7 @@
 // What the forward and the backward kernels of a join share: rows in registers, and sums over a row.
 //
 // A row belongs to a team: a warp, a CTA of G threads, or a cluster of up to eight such CTAs, each of which
-// has the next G * E columns.  A thread holds E columns: whole 16-byte vectors t, t + G, ... (Vec), or single
-// columns t, t + G, ... where rows start on no 16-byte boundary (Cols).
+// has the next G * E columns.  A thread holds E columns, vectors t, t + G, ... of eight.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -18,6 +17,15 @@ namespace {
 template <int G>
 constexpr int kTeamCta = G < 128 ? 128 : G;  // threads of a CTA
 
+// The CTA's dynamic shared memory: rows on their way and the threads' own parameters, by byte offsets.  (Read and written
+// as plain memory, so that the compiler may order the accesses; the copies into it and their waits are barriers to that.)
+__device__ __forceinline__ uint8_t* ring() {
+  extern __shared__ __align__(16) uint8_t join_ring[];
+  return join_ring;
+}
+__device__ __forceinline__ uint4 ring16(uint32_t at) { return *reinterpret_cast<const uint4*>(ring() + at); }
+__device__ __forceinline__ void to_ring16(uint32_t at, uint4 v) { *reinterpret_cast<uint4*>(ring() + at) = v; }
+
 // Pairs of the values of eight columns from their 16-byte words.
 template <bool BF16>
 __device__ __forceinline__ void words_to_pairs(const uint4 (&w)[BF16 ? 1 : 2], Pair* v) {
@@ -29,97 +37,164 @@ __device__ __forceinline__ void words_to_pairs(const uint4 (&w)[BF16 ? 1 : 2], P
   }
 }
 
-// Columns in vectors of eight, of a type known when compiled.  A row on its way lies in shared memory: a thread
-// copies its own vectors there (cp.async; nobody else reads them, so no barrier is needed), the one that the row
-// ends in and those behind it element by element, as zeros past the end.
-template <int G, int E, bool BF16>
+// Where a matrix ends, for rows that lie anywhere: its last row, and the columns from this CTA's first to the row's end.
+struct Edges {
+  uint32_t last_row;
+  int rest;
+  bool first;  // this CTA has the rows' first columns
+};
+
+// Bytes [from, to) of sixteen, both even, to the sixteen-byte aligned place q.
+__device__ __forceinline__ void store_part(char* q, uint4 w, uint32_t from, uint32_t to) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) {
+    if (from <= 4 * i && 4 * i + 4 <= to) {
+      *reinterpret_cast<uint32_t*>(q + 4 * i) = u[i];
+    } else {
+      if (from <= 4 * i && 4 * i + 2 <= to) *reinterpret_cast<uint16_t*>(q + 4 * i) = uint16_t(u[i]);
+      if (from <= 4 * i + 2 && 4 * i + 4 <= to) *reinterpret_cast<uint16_t*>(q + 4 * i + 2) = uint16_t(u[i] >> 16);
+    }
+  }
+}
+
+// Columns in vectors of eight.  A row on its way lies in shared memory: a thread copies its own vectors there (cp.async;
+// nobody else reads them, so no barrier is needed), and `settle` puts zeros behind the row's end.
+// ANY: rows may start at any element.  Then shared memory holds the aligned sixteen bytes as they lie in memory, a
+// thread copies those that its vector begins in, and a warp's last lane the ones that the last vector ends in too;
+// `settle` shifts a vector out of its own bytes and the next lane's.  A vector is stored as the aligned sixteen bytes
+// that it shares with the lane before it, whose last bytes come by a shuffle; only what sticks out at the ends of a
+// warp's run is stored in smaller pieces.
+template <int G, int E, bool BF16, bool ANY>
 struct Vec {
-  static constexpr bool kWide = true, kShort = BF16;
-  static constexpr int kElem = BF16 ? 2 : 4, kPieces = E / 8 * (BF16 ? 1 : 2), kBytes = kPieces * 16;  // of a thread and row
-  uint32_t at;  // its first piece in shared memory; pieces lie a CTA's threads apart
+  static constexpr bool kShort = BF16;
+  static constexpr int kElem = BF16 ? 2 : 4, kWhole = BF16 ? 1 : 2;  // pieces of a vector
+  static constexpr uint32_t kApart = kTeamCta<G> * 16;               // of a thread's pieces
+  static constexpr uint32_t kVector = kWhole * kApart + (ANY ? kTeamCta<G> / 2 : 0), kBytes = E / 8 * kVector;  // of a CTA and row
+  uint32_t at;   // its first piece in shared memory
+  uint32_t off;  // bytes by which the row's vectors are off a sixteen-byte boundary
 
   __device__ static __forceinline__ int column(int t, int i) { return (t + G * (i / 8)) * 8 + i % 8; }
+  // Piece k of vector e; k = kWhole is the first of the next lane, or, behind the last lane, the warp's own.
+  __device__ __forceinline__ uint32_t piece(int e, int k) const {
+    if (k < kWhole) return at + e * kVector + k * kApart;
+    const bool last = (threadIdx.x & 31) == 31;
+    return last ? at - threadIdx.x * 16 + e * kVector + kWhole * kApart + threadIdx.x / 32 * 16 : at + e * kVector + 16;
+  }
 
-  __device__ __forceinline__ void load(const void* p, int64_t row, int64_t ld, int t, int cols, int) {
+  __device__ __forceinline__ void load(const void* p, uint32_t row, int64_t ld, int t, int cols, const Edges& edges) {
     const char* q = static_cast<const char*>(p) + row * ld * kElem;
+    off = ANY ? uint32_t(reinterpret_cast<uintptr_t>(q)) & 15u : 0u;
 #pragma unroll
     for (int e = 0; e < E / 8; ++e) {
       const int c0 = (t + G * e) * 8;
-      const uint32_t to = at + e * (kPieces / (E / 8)) * (kTeamCta<G> * 16);
-      if (c0 + 8 <= cols) {
-        copy_to_shared16(to, q + c0 * kElem);
-        if (!BF16) copy_to_shared16(to + kTeamCta<G> * 16, q + c0 * kElem + 16);
-      } else {
-        float f[8];
+      if (c0 >= cols + (ANY ? 8 : 0)) continue;  // (with ANY, the lane behind the last has that one's end in its piece)
+      const char* v = q + c0 * kElem;
+      // Behind a row's end the matrix goes on, with what lies between its rows or with the next row: only the pieces of
+      // the first vector of the first row and of the last vectors of the last one may reach out of it.
+      const bool in = !((off != 0 && row == 0 && edges.first && c0 == 0) ||
+                        (row == edges.last_row && c0 + 8 + (off != 0 ? 16 / kElem : 0) > edges.rest));
+      if (in) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = c0 + k < cols ? load_elem_rw(q, c0 + k, BF16) : 0.0f;
-        if (BF16) {
-          to_shared16(to, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
-        } else {
-          to_shared16(to, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
-          to_shared16(to + kTeamCta<G> * 16,
-                      make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+        for (int k = 0; k < kWhole; ++k)
+          if (k == 0 || c0 < cols) copy_to_shared16(smem_addr(ring()) + piece(e, k), v - off + k * 16);
+        if (ANY && off != 0 && (threadIdx.x & 31) == 31 && c0 < cols)
+          copy_to_shared16(smem_addr(ring()) + piece(e, kWhole), v - off + kWhole * 16);
+      } else {
+        // element by element, with what the lane before has in this one's first piece
+        const int before = ANY && c0 > 0 ? int(off) / kElem : 0, n = min(cols - c0, 8);
+#pragma unroll 1
+        for (int k = -before; k < n; ++k) {
+          const uint32_t byte = off + k * kElem, place = piece(e, byte / 16) + byte % 16;
+          if (BF16)
+            *reinterpret_cast<uint16_t*>(ring() + place) = *reinterpret_cast<const uint16_t*>(v + k * 2);
+          else
+            *reinterpret_cast<uint32_t*>(ring() + place) = *reinterpret_cast<const uint32_t*>(v + k * 4);
         }
+      }
+    }
+  }
+  // Puts a row that has arrived in place, and zeros behind its end (all lanes of a warp).
+  __device__ __forceinline__ void settle(int t, int cols) const {
+    if (ANY) __syncwarp();
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) {
+      const int left = (cols - (t + G * e) * 8) * kElem;  // bytes of the row from here on
+      if (!ANY && left >= 8 * kElem) continue;
+      uint4 w[kWhole + 1];
+#pragma unroll
+      for (int k = 0; k < kWhole + (ANY ? 1 : 0); ++k) w[k] = ring16(piece(e, k));
+      if (ANY) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kWhole; ++k)
+          if (off != 0) w[k] = shifted16(w[k], w[k + 1], off);
+      }
+#pragma unroll
+      for (int k = 0; k < kWhole; ++k) {
+        if (left < 8 * kElem) {
+          uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = left - k * 16 - i * 4;
+            u[i] = n >= 4 ? u[i] : n > 0 ? u[i] & 0xFFFFu : 0u;
+          }
+          w[k] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        to_ring16(piece(e, k), w[k]);
       }
     }
   }
   // Its columns 8 e to 8 e + 7 as four pairs.
   __device__ __forceinline__ void eight(int e, Pair (&v)[4]) const {
-    uint4 w[BF16 ? 1 : 2];
+    uint4 w[kWhole];
 #pragma unroll
-    for (int k = 0; k < (BF16 ? 1 : 2); ++k) w[k] = shared16(at + (e * (BF16 ? 1 : 2) + k) * (kTeamCta<G> * 16));
+    for (int k = 0; k < kWhole; ++k) w[k] = ring16(piece(e, k));
     words_to_pairs<BF16>(w, v);
   }
-  __device__ static __forceinline__ void store(char* row, int e, int t, int cols, int, const Pair (&v)[4]) {
+  // (all lanes of a warp)
+  __device__ static __forceinline__ void store(char* row, int e, int t, int cols, const Pair (&v)[4]) {
     const int c0 = (t + G * e) * 8;
     float f[8];
     floats8(v, f);
-    if (c0 + 8 <= cols) {
-      store8(row, c0, BF16, f);
-    } else {
+    const uint32_t out = ANY ? uint32_t(reinterpret_cast<uintptr_t>(row)) & 15u : 0u;
+    if (!ANY || out == 0) {
+      if (c0 + 8 <= cols) {
+        store8(row, c0, BF16, f);
+      } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c0 + k < cols) store_elem(row, c0 + k, BF16, f[k]);
+        for (int k = 0; k < 8; ++k)
+          if (c0 + k < cols) store_elem(row, c0 + k, BF16, f[k]);
+      }
+      return;
     }
-  }
-};
-
-// Single columns, of a type known at run time.  A row on its way is in registers.
-template <int G, int E>
-struct Cols {
-  static constexpr bool kWide = false, kShort = false;
-  static constexpr int kBytes = 0;
-  uint32_t at;
-  float f[E];
-
-  __device__ static __forceinline__ int column(int t, int i) { return t + G * i; }
-
-  __device__ __forceinline__ void load(const void* p, int64_t row, int64_t ld, int t, int cols, int bf16) {
-    const char* q = static_cast<const char*>(p) + row * ld * (bf16 ? 2 : 4);
-    if (bf16) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = t + G * i < cols ? load_elem_rw(q, t + G * i, 1) : 0.0f;
+    const int lane = threadIdx.x & 31;
+    uint4 w[kWhole];
+    if constexpr (BF16) {
+      w[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
     } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = t + G * i < cols ? load_elem_rw(q, t + G * i, 0) : 0.0f;
+      w[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+      w[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
     }
-  }
-  __device__ __forceinline__ void eight(int e, Pair (&v)[4]) const {
+    const uint4 last = w[kWhole - 1];
+    uint4 before = make_uint4(__shfl_up_sync(0xFFFFFFFFu, last.x, 1), __shfl_up_sync(0xFFFFFFFFu, last.y, 1),
+                              __shfl_up_sync(0xFFFFFFFFu, last.z, 1), __shfl_up_sync(0xFFFFFFFFu, last.w, 1));
+    if (c0 >= cols) return;
+    // bytes of the vector, counted from the boundary before it: [out, end)
+    const uint32_t end = out + uint32_t(min(cols - c0, 8) * kElem);
+    char* q = row + c0 * kElem - out;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = pair(f[e * 8 + 2 * i], f[e * 8 + 2 * i + 1]);
-  }
-  __device__ static __forceinline__ void store(char* row, int e, int t, int cols, int bf16, const Pair (&v)[4]) {
-    float x[8];
-    floats8(v, x);
-    if (bf16) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (t + G * (e * 8 + i) < cols) store_elem(row, t + G * (e * 8 + i), 1, x[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (t + G * (e * 8 + i) < cols) store_elem(row, t + G * (e * 8 + i), 0, x[i]);
+    for (int k = 0; k < kWhole; ++k) {
+      const uint4 x = shifted16(before, w[k], 16 - out);
+      if ((k > 0 || lane > 0) && end >= uint32_t(16 * k + 16))
+        *reinterpret_cast<uint4*>(q + k * 16) = x;
+      else if (end > uint32_t(16 * k))
+        store_part(q + k * 16, x, k == 0 && lane == 0 ? out : 0u, min(end - 16 * k, 16u));
+      before = w[k];
     }
+    // the last bytes, where no lane behind takes them
+    if (end > uint32_t(16 * kWhole) && (lane == 31 || c0 + 8 >= cols))
+      store_part(q + 16 * kWhole, shifted16(before, before, 16 - out), 0u, end - 16 * kWhole);
   }
 };
 
@@ -128,7 +203,7 @@ struct Cols {
 template <typename Row, int E>
 __device__ __forceinline__ void params(const void* p, int t, int cols, int bf16, bool wide, float none, float past, Pair* out) {
   float v[E];
-  if (Row::kWide && wide && p != nullptr && Row::column(t, E - 1) < cols) {
+  if (wide && p != nullptr && Row::column(t, E - 1) < cols) {
 #pragma unroll
     for (int e = 0; e < E / 8; ++e) load8(p, Row::column(t, e * 8), bf16, v + e * 8);
   } else {
@@ -167,7 +242,7 @@ __device__ __forceinline__ void keep(uint32_t at, int which, const Pair* v) {
 #pragma unroll
   for (int i = 0; i < E / 2; i += 2) {
     const float2 lo = halves(v[i]), hi = halves(v[i + 1]);
-    to_shared16(at + (which * (E / 4) + i / 2) * (THREADS * 16),
+    to_ring16(at + (which * (E / 4) + i / 2) * (THREADS * 16),
                 make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y)));
   }
 }
@@ -175,7 +250,7 @@ template <int E, int THREADS>
 __device__ __forceinline__ void recall(uint32_t at, int which, int e, Pair (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; i += 2) {
-    const uint4 w = shared16(at + (which * (E / 4) + e * 2 + i / 2) * (THREADS * 16));
+    const uint4 w = ring16(at + (which * (E / 4) + e * 2 + i / 2) * (THREADS * 16));
     v[i] = pair(__uint_as_float(w.x), __uint_as_float(w.y)), v[i + 1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
   }
 }
@@ -329,9 +404,9 @@ __device__ __forceinline__ void layer_stats(Team<G, CL>& team, const Pair (&v)[E
 // all: columns of the row, of which this CTA has `cols`.
 template <typename Row, int G, int E, bool CL>
 __device__ __forceinline__ Counts row_counts(const Team<G, CL>& team, int t, int cols, int64_t all) {
-  // of the columns of one CTA, those of its warp: runs of 32 threads' columns, G threads' apart
+  // of the columns of one CTA, those of its warp: runs of 32 threads' vectors, G threads' apart
   const auto of = [](int warp, int columns) {
-    constexpr int kRun = Row::kWide ? 256 : 32, kApart = Row::kWide ? G * 8 : G;
+    constexpr int kRun = 256, kApart = G * 8;
     int k = 0;
 #pragma unroll
     for (int i = 0; i < E * 32 / kRun; ++i) k += min(max(columns - (warp * kRun + i * kApart), 0), kRun);

@@ -18,14 +18,13 @@ namespace {
 constexpr int kStages = 2;
 template <int G, int E, typename RowX, typename RowY>
 size_t ring_bytes(bool betas) {
-  return size_t(kTeamCta<G>) * (kStages * (RowX::kBytes + RowY::kBytes) + (betas ? 4 : 2) * E * sizeof(float));
+  return size_t(kStages) * (RowX::kBytes + RowY::kBytes) + size_t(kTeamCta<G>) * (betas ? 4 : 2) * E * sizeof(float);
 }
 
 template <int G, int E, bool CL, typename RowX, typename RowY>
-__global__ void __launch_bounds__(kTeamCta<G>, (RowX::kShort ? 768 : 512) / kTeamCta<G>)
+__global__ void __launch_bounds__(kTeamCta<G>, (E == 16 ? 768 : 1024) / kTeamCta<G>)
     k_join_fwd(const JoinFwdArgs args, bool pwide) {
   __shared__ Board<G, CL> board;
-  extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, C = E / 8;
   JoinFwdArgs a = args;
   const int t = threadIdx.x % G, place = threadIdx.x / G;
@@ -46,6 +45,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, (RowX::kShort ? 768 : 512) / kTea
   }
   const int64_t rest = a.cols - c0;
   const int cols = rest <= 0 ? 0 : rest < G * E ? int(rest) : G * E;
+  const Edges edges{n_rows - 1, rest < (1 << 30) ? int(rest) : 1 << 30, c0 == 0};
   const Counts n = row_counts<RowX, G, E, CL>(team, t, cols, a.cols);
   const auto stats = [&](const Pair (&v)[E / 2], float* mean, float* rstd) {
     float var;
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kTeamCta<G>, (RowX::kShort ? 768 : 512) / kTea
     }
     *rstd = rsqrtf(var + a.eps);
   };
-  const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
-  constexpr uint32_t kStage = kThreadsCta * (RowX::kBytes + RowY::kBytes), kOwn = kStages * kStage;
+  const uint32_t base = threadIdx.x * 16;
+  constexpr uint32_t kStage = RowX::kBytes + RowY::kBytes, kOwn = kStages * kStage;
   const bool betas = a.post_beta != nullptr || a.beta != nullptr;
   {
     // h = a x + w (yh pg + pb), pg and pb with the gate in them, 0 past the row's end
@@ -88,28 +88,25 @@ __global__ void __launch_bounds__(kTeamCta<G>, (RowX::kShort ? 768 : 512) / kTea
   float wn = 1.0f;
   uint32_t slot = 0;
   const auto fetch = [&](uint32_t row) {
-    xn.at = base + slot * kStage, yn.at = xn.at + kThreadsCta * RowX::kBytes;
+    xn.at = base + slot * kStage, yn.at = xn.at + RowX::kBytes;
     if (row < n_rows) {
-      xn.load(a.x, row, a.ldx, t, cols, a.x_bf16);
-      yn.load(a.y, row, a.ldy, t, cols, a.y_bf16);
+      xn.load(a.x, row, a.ldx, t, cols, edges);
+      yn.load(a.y, row, a.ldy, t, cols, edges);
       if (a.row_gate != nullptr) wn = __ldg(a.row_gate + row);
     }
     cp_async_commit();
     slot ^= 1;
   };
-  constexpr bool kAhead = RowX::kWide;  // (a row of single columns ahead, in registers, is slower: 777 x 2049 14 -> 19 us)
-  if constexpr (kAhead) fetch(first);
+  fetch(first);
   const Pair a2 = both(a.a);
   for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
     const bool live = row < n_rows;  // (where it is not, the values are an earlier row's, and nothing is stored)
-    if constexpr (!kAhead) fetch(row);
     const RowX xc = xn;
     const RowY yc = yn;
     const Pair w = both(a.s * wn);
-    if constexpr (kAhead) {
-      fetch(row + step);
-      cp_async_wait<1>();
-    }
+    fetch(row + step);
+    cp_async_wait<1>();
+    if (live) xc.settle(t, cols), yc.settle(t, cols);
     Pair h[E / 2];  // y, then the joined stream
 #pragma unroll
     for (int e = 0; e < C; ++e) {
@@ -137,7 +134,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, (RowX::kShort ? 768 : 512) / kTea
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = as_stored(fma(w, pg[i], a2 * x[i]), a.x_bf16), h[e * 4 + i] = x[i];
-      if (live) RowX::store(out, e, t, cols, a.x_bf16, x);
+      if (live) RowX::store(out, e, t, cols, x);
     }
     if (a.u != nullptr) {
       stats(h, &m2, &r2);
@@ -155,7 +152,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, (RowX::kShort ? 768 : 512) / kTea
 #pragma unroll
           for (int i = 0; i < 4; ++i) g[i] = g[i] + b[i];
         }
-        if (live) RowY::store(out, e, t, cols, a.y_bf16, g);
+        if (live) RowY::store(out, e, t, cols, g);
       }
     }
     if (a.stats != nullptr && t == 0 && live && team.rank == 0) {
@@ -230,17 +227,27 @@ cudaError_t run(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
 }
 template <int G, bool CL>
 cudaError_t run_f32(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
-  return a.y_bf16 ? run<G, 8, CL, Vec<G, 8, false>, Vec<G, 8, true>>(a, pwide, ctas, s)
-                  : run<G, 8, CL, Vec<G, 8, false>, Vec<G, 8, false>>(a, pwide, ctas, s);
+  return a.y_bf16 ? run<G, 8, CL, Vec<G, 8, false, false>, Vec<G, 8, true, false>>(a, pwide, ctas, s)
+                  : run<G, 8, CL, Vec<G, 8, false, false>, Vec<G, 8, false, false>>(a, pwide, ctas, s);
 }
 // bf16 rows: sixteen columns to a thread, so that half as many warps add up their sums.
 template <int G, int E, bool CL>
 cudaError_t run_bf16(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
-  return run<G, E, CL, Vec<G, E, true>, Vec<G, E, true>>(a, pwide, ctas, s);
+  return run<G, E, CL, Vec<G, E, true, false>, Vec<G, E, true, false>>(a, pwide, ctas, s);
 }
 template <int G, int E, bool CL>
-cudaError_t run_cols(const JoinFwdArgs& a, int ctas, cudaStream_t s) {
-  return run<G, E, CL, Cols<G, E>, Cols<G, E>>(a, false, ctas, s);
+cudaError_t run_any_bf16(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
+  return a.y_bf16 ? run<G, E, CL, Vec<G, E, true, true>, Vec<G, E, true, true>>(a, pwide, ctas, s)
+                  : run<G, E, CL, Vec<G, E, true, true>, Vec<G, E, false, true>>(a, pwide, ctas, s);
+}
+template <int G, int E, bool CL>
+cudaError_t run_any_f32(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
+  return a.y_bf16 ? run<G, E, CL, Vec<G, E, false, true>, Vec<G, E, true, true>>(a, pwide, ctas, s)
+                  : run<G, E, CL, Vec<G, E, false, true>, Vec<G, E, false, true>>(a, pwide, ctas, s);
+}
+template <int G>
+cudaError_t run_any(const JoinFwdArgs& a, bool pwide, cudaStream_t s) {
+  return a.x_bf16 ? run_any_bf16<G, 8, false>(a, pwide, 1, s) : run_any_f32<G, 8, false>(a, pwide, 1, s);
 }
 
 cudaError_t run_long(const JoinFwdArgs& a, cudaStream_t s) {
@@ -274,10 +281,10 @@ cudaError_t launch_join_forward(const JoinFwdArgs& a, cudaStream_t s) {
     if (a.cols <= 4096) return run_f32<512, false>(a, pwide, 1, s);
     return run_f32<512, true>(a, pwide, ctas, s);
   }
-  if (a.cols <= 256) return run_cols<32, 8, false>(a, 1, s);
-  if (a.cols <= 1024) return run_cols<128, 8, false>(a, 1, s);
-  if (a.cols <= 4096) return run_cols<512, 8, false>(a, 1, s);
-  return run_cols<512, 8, true>(a, ctas, s);
+  if (a.cols <= 256) return run_any<32>(a, pwide, s);
+  if (a.cols <= 1024) return run_any<128>(a, pwide, s);
+  if (a.cols <= 4096) return a.x_bf16 ? run_any_bf16<256, 16, false>(a, pwide, 1, s) : run_any_f32<512, 8, false>(a, pwide, 1, s);
+  return a.x_bf16 ? run_any_bf16<256, 16, true>(a, pwide, ctas, s) : run_any_f32<512, 8, true>(a, pwide, ctas, s);
 }
 
 }  // namespace loco

@@ -311,3 +311,51 @@ def test_empty_batch(L):
     L.loco_join_backward(cfg, e, e, e, e, None, torch.empty(0, 40, device="cuda"), torch.empty(0, 40, device="cuda"),
                          gate=gate, **v)
     assert not any(t.any() for t in v.values())
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 5), (2, 15), (3, 37), (4, 256), (5, 300), (3, 1025), (2, 4099), (3, 9001), (2, 24577)])
+@pytest.mark.parametrize("xd,yd", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_rows_that_lie_anywhere(L, rows, cols, xd, yd):
+    """Every matrix at its own place and pitch: the same bits as with some at an odd place, and nothing around the
+    outputs is written.  The inputs fill their memory to its last element."""
+    g = gen(19)
+    _, x, y, p = inputs(19, rows, cols, xd, yd, BF16, 0, (True, True, True, True, True))
+    dh, du = rand(g, rows, cols, xd, 0.1), rand(g, rows, cols, yd, 0.1)
+    cfg = cfg_of(L, "layer", True, 0.75, 0.5)
+    q = {k: t for k, t in p.items() if k != "beta"}
+    ws = torch.empty(L.loco_join_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+
+    def placed(t, off, pad):
+        rows_, ld = t.shape[0], cols + pad
+        buf = torch.full((off + (rows_ - 1) * ld + cols,), 3.0, dtype=t.dtype, device="cuda")
+        out = buf.as_strided((rows_, cols), (ld, 1), off)
+        out.copy_(t)
+        return out
+
+    def run(place):
+        outs, checks = [], []
+
+        def out(d, i):
+            off, pad = place(i)
+            buf = torch.full((off + rows * (cols + pad) + 16,), 7.0, dtype=d, device="cuda")
+            t = buf.as_strided((rows, cols), (cols + pad, 1), off)
+            outs.append(t)
+            checks.append((buf, off, pad))
+            return t
+        a, b, c, d = (placed(t, *place(i)) for i, t in enumerate((x, y, dh, du)))
+        h, u, stats = out(xd, 4), out(yd, 5), torch.empty(4, rows, device="cuda")
+        L.loco_join_forward(cfg, a, b, h, u, stats=stats, **p)
+        dx, dy = out(xd, 6), out(yd, 7)
+        v = {k: torch.empty(cols, device="cuda") for k in ("dgamma", "dbeta", "dpost_gamma", "dpost_beta", "dgate")}
+        dr = torch.empty(rows, device="cuda")
+        L.loco_join_backward(cfg, c, d, h, b, stats, dx, dy, drow_gate=dr, workspace=ws, **q, **v)
+        for buf, off, pad in checks:
+            seen = torch.ones_like(buf, dtype=torch.bool)
+            seen.as_strided((rows, cols), (cols + pad, 1), off).fill_(False)
+            assert bool((buf[seen] == 7).all())
+        return [t.clone() for t in outs] + [stats, dr, *v.values()]
+    want = run(lambda i: (1, 0) if i in (0, 4, 2) else (0, -cols % 8))
+    for shift in range(4):
+        got = run(lambda i: ((3 * i + shift) % 9, (5 * i + 2 * shift + 1) % 11))
+        for k, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), (shift, k)
