@@ -488,6 +488,7 @@ cudaError_t rows_kernel(const JoinBwdArgs& a, int* sums, int* partials, cudaStre
   }
   if (a.cols <= 256) return run_any<32, 8, false>(a, pwide, 1, partials, s);
   if (a.cols <= 1024) return run_any<128, 8, false>(a, pwide, 1, partials, s);
+  if (a.cols <= 2048) return run_any<256, 8, false>(a, pwide, 1, partials, s);
   if (a.cols <= 4096) return run_any<512, 8, false>(a, pwide, 1, partials, s);
   return run_any<512, 8, true>(a, pwide, ctas, partials, s);
 }

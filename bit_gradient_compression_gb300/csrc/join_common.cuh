@@ -67,7 +67,7 @@ __device__ __forceinline__ void store_part(char* q, uint4 w, uint32_t from, uint
 // warp's run is stored in smaller pieces.
 template <int G, int E, bool BF16, bool ANY>
 struct Vec {
-  static constexpr bool kShort = BF16;
+  static constexpr int kRun = 256, kRunApart = G * 8;  // a warp's columns: runs, and how far they are apart
   static constexpr int kElem = BF16 ? 2 : 4, kWhole = BF16 ? 1 : 2;  // pieces of a vector
   static constexpr uint32_t kApart = kTeamCta<G> * 16;               // of a thread's pieces
   static constexpr uint32_t kVector = kWhole * kApart + (ANY ? kTeamCta<G> / 2 : 0), kBytes = E / 8 * kVector;  // of a CTA and row
@@ -195,6 +195,36 @@ struct Vec {
     // the last bytes, where no lane behind takes them
     if (end > uint32_t(16 * kWhole) && (lane == 31 || c0 + 8 >= cols))
       store_part(q + 16 * kWhole, shifted16(before, before, 16 - out), 0u, end - 16 * kWhole);
+  }
+};
+
+// Single columns t, t + G, ... of rows that lie anywhere, in registers.  For 32-bit rows in the forward pass, where the
+// shifting of Vec costs more than four times as many loads do (16384 x 4095 with bf16 y, layer norms: 233 us here, 385
+// there; with bf16 rows 232 against 179).
+template <int G, int E, bool BF16>
+struct Cols {
+  static constexpr int kRun = 32, kRunApart = G;
+  static constexpr uint32_t kBytes = 0;
+  uint32_t at;
+  float f[E];
+
+  __device__ static __forceinline__ int column(int t, int i) { return t + G * i; }
+  __device__ __forceinline__ void load(const void* p, uint32_t row, int64_t ld, int t, int cols, const Edges&) {
+    const char* q = static_cast<const char*>(p) + row * ld * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] = t + G * i < cols ? load_elem_rw(q, t + G * i, BF16) : 0.0f;
+  }
+  __device__ __forceinline__ void settle(int, int) const {}
+  __device__ __forceinline__ void eight(int e, Pair (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(f[e * 8 + 2 * i], f[e * 8 + 2 * i + 1]);
+  }
+  __device__ static __forceinline__ void store(char* row, int e, int t, int cols, const Pair (&v)[4]) {
+    float x[8];
+    floats8(v, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t + G * (e * 8 + i) < cols) store_elem(row, t + G * (e * 8 + i), BF16, x[i]);
   }
 };
 
@@ -406,10 +436,9 @@ template <typename Row, int G, int E, bool CL>
 __device__ __forceinline__ Counts row_counts(const Team<G, CL>& team, int t, int cols, int64_t all) {
   // of the columns of one CTA, those of its warp: runs of 32 threads' vectors, G threads' apart
   const auto of = [](int warp, int columns) {
-    constexpr int kRun = 256, kApart = G * 8;
     int k = 0;
 #pragma unroll
-    for (int i = 0; i < E * 32 / kRun; ++i) k += min(max(columns - (warp * kRun + i * kApart), 0), kRun);
+    for (int i = 0; i < E * 32 / Row::kRun; ++i) k += min(max(columns - (warp * Row::kRun + i * Row::kRunApart), 0), Row::kRun);
     return float(k);
   };
   Counts n;

@@ -240,14 +240,10 @@ cudaError_t run_any_bf16(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_
   return a.y_bf16 ? run<G, E, CL, Vec<G, E, true, true>, Vec<G, E, true, true>>(a, pwide, ctas, s)
                   : run<G, E, CL, Vec<G, E, true, true>, Vec<G, E, false, true>>(a, pwide, ctas, s);
 }
-template <int G, int E, bool CL>
-cudaError_t run_any_f32(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
-  return a.y_bf16 ? run<G, E, CL, Vec<G, E, false, true>, Vec<G, E, true, true>>(a, pwide, ctas, s)
-                  : run<G, E, CL, Vec<G, E, false, true>, Vec<G, E, false, true>>(a, pwide, ctas, s);
-}
-template <int G>
-cudaError_t run_any(const JoinFwdArgs& a, bool pwide, cudaStream_t s) {
-  return a.x_bf16 ? run_any_bf16<G, 8, false>(a, pwide, 1, s) : run_any_f32<G, 8, false>(a, pwide, 1, s);
+template <int G, bool CL>
+cudaError_t run_any_f32(const JoinFwdArgs& a, int ctas, cudaStream_t s) {
+  return a.y_bf16 ? run<G, 8, CL, Cols<G, 8, false>, Cols<G, 8, true>>(a, false, ctas, s)
+                  : run<G, 8, CL, Cols<G, 8, false>, Cols<G, 8, false>>(a, false, ctas, s);
 }
 
 cudaError_t run_long(const JoinFwdArgs& a, cudaStream_t s) {
@@ -281,10 +277,18 @@ cudaError_t launch_join_forward(const JoinFwdArgs& a, cudaStream_t s) {
     if (a.cols <= 4096) return run_f32<512, false>(a, pwide, 1, s);
     return run_f32<512, true>(a, pwide, ctas, s);
   }
-  if (a.cols <= 256) return run_any<32>(a, pwide, s);
-  if (a.cols <= 1024) return run_any<128>(a, pwide, s);
-  if (a.cols <= 4096) return a.x_bf16 ? run_any_bf16<256, 16, false>(a, pwide, 1, s) : run_any_f32<512, 8, false>(a, pwide, 1, s);
-  return a.x_bf16 ? run_any_bf16<256, 16, true>(a, pwide, ctas, s) : run_any_f32<512, 8, true>(a, pwide, ctas, s);
+  if (a.x_bf16) {
+    if (a.cols <= 256) return run_any_bf16<32, 8, false>(a, pwide, 1, s);
+    if (a.cols <= 1024) return run_any_bf16<128, 8, false>(a, pwide, 1, s);
+    if (a.cols <= 2048) return run_any_bf16<128, 16, false>(a, pwide, 1, s);
+    if (a.cols <= 4096) return run_any_bf16<256, 16, false>(a, pwide, 1, s);
+    return run_any_bf16<256, 16, true>(a, pwide, ctas, s);
+  }
+  if (a.cols <= 256) return run_any_f32<32, false>(a, 1, s);
+  if (a.cols <= 1024) return run_any_f32<128, false>(a, 1, s);
+  if (a.cols <= 2048) return run_any_f32<256, false>(a, 1, s);
+  if (a.cols <= 4096) return run_any_f32<512, false>(a, 1, s);
+  return run_any_f32<512, true>(a, ctas, s);
 }
 
 }  // namespace loco
