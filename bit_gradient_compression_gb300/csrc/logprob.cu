@@ -6,14 +6,12 @@
 // warps and CTAs are joined pairwise.  lse = M scale + ln S, entropy = ln S - ln 2 D / S (in deviations
 // from M, so that neither loses digits to the size of the logits).
 //
-// Alternatives: every warp lists what may be among the largest: values above `thr`, the least of its own
-// `top` largest so far.  The first tile's threshold is the top-th largest of the lanes' maxima, below
-// which no value of the warp can be needed; and the warps of a CTA tell one another their each-th
-// largest, each = ceil(top / warps), of which the least is a threshold for all.  Columns of one warp come
-// in ascending order, so a later value that equals its own threshold loses the tie and `>` is enough;
-// against a threshold of other warps a value that equals it is kept.  Lists are ordered by counting for
-// each key how many are above it; keys (value, then lower column) are all different, so the outcome does
-// not depend on the order in which lanes appended.
+// Alternatives: every warp keeps its 32 largest so far, one to a lane, in order of keys (value, then lower column;
+// all are different, so the outcome does not depend on the order in which they come).  A value above the warp's
+// threshold `thr` is inserted by a ballot and a shift; thr is the warp's own top-th largest, and where a row has
+// eight warps the least of their each-th largest, each = ceil(top / 8), if that is more.  The first tile's
+// thresholds are the same of the lanes' maxima, of which there cannot be more than of values.  Columns of one warp come in ascending order, so a later value that equals its own threshold loses the tie and `>` is enough;
+// against a threshold of other warps a value that equals it is kept.
 //
 // A row is read by a warp (short rows), by a CTA of eight, or, where rows are few, by a cluster of up to
 // eight CTAs whose results the first joins through distributed shared memory: one launch, no workspace.
@@ -36,7 +34,6 @@ constexpr int kVectors = 4;                 // 16-byte vectors of a thread in on
 constexpr float kLowest = -3.402823466e38f; // maximum of nothing; a row's lowest finite value may equal it
 constexpr float kLeast = -200.0f;           // 2^t is 0 from here down; keeps t finite under -inf
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kListed = 64;                 // keys a warp's list holds before a vector is taken
 typedef unsigned long long Key;             // value in order, then the complement of the column; 0: none
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -108,89 +105,43 @@ __device__ __forceinline__ void to_pairs(uint4 w, Pair (&v)[kVec<BF16> / 2]) {
   }
 }
 
-// Where its `top`-th largest begins, as each warp of a team knows it: `each` is the place in a warp's own order that
-// makes `top` of them in all (ceil(top / warps)).
-struct Floors {
-  uint32_t* at;  // in_order of the each-th largest of every warp so far; 0: not that many
-  int warps, each;
-};
-
 // The value before the one whose in_order is k: what is above it is not below the value (two steps down from zero,
 // whose neighbour is -0).
 __device__ __forceinline__ float value_before(uint32_t k) {
   return k <= 0x007FFFFFu ? -INFINITY : out_of_order(k - (k == 0x80000000u ? 2u : 1u));
 }
 
-// A warp's list of candidates.
-struct List {
-  Key* keys;   // kListed + 32 * 4
-  Key* kept;   // LOCO_MAX_TOP
-  int* count;
-  Floors floors;
-  int top, warp;
+// A warp's largest values.
+struct Largest {
+  Key key;     // of this lane's: the lane-th largest of the warp, 0 where there are not that many
   float thr;   // what is not above it is not needed
-  static constexpr int kEach = LOCO_MAX_TOP / kWarps;
-  uint32_t best[kEach];  // largest of the noted maxima, in order
+  int top;
 
-  // Keeps the `top` largest, in order.
-  __device__ __forceinline__ void order(int lane) {
-    __syncwarp();
-    const int n = *count;
-    for (int i = lane; i < n; i += 32) {
-      const Key k = keys[i];
-      int above = 0;
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) above += keys[j] > k;
-      if (above < top) kept[above] = k;
-    }
-    __syncwarp();
-    const int left = n < top ? n : top;
-    if (lane < left) keys[lane] = kept[lane];
-    if (lane == 0) *count = left;
-    __syncwarp();
-    if (left == top) {
-      const float t = key_value(keys[top - 1]);
-      if (t > thr) thr = t;
-    }
-  }
-  // Appends the values of a vector that are above the threshold (all lanes of the warp; v: kVec values from column on).
-  // An order in its midst raises the threshold for later vectors only: of one vector, a lane's last columns are before
-  // the next lane's first ones, and would win a tie with them.
+  // Inserts the values of a vector that are above the threshold (all lanes of the warp; v: N values, lane 0's from
+  // column on, the next lane's behind them).  The threshold of the vector's begin holds for all of it: a lane's last
+  // columns are before the next lane's first ones, and win a tie with them.
   template <int N>
-  __device__ __forceinline__ void append(const float (&v)[N], int64_t column, int lane) {
+  __device__ __forceinline__ void insert(const float (&v)[N], int64_t column, int lane) {
     const float limit = thr;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      if (v[k] > limit) keys[atomicAdd(count, 1)] = key_of(v[k], column + k);
-      if (k % 4 == 3 || k == N - 1) {  // of four values a lane there is room
-        __syncwarp();
-        if (*count > kListed) order(lane);
+      uint32_t who = __ballot_sync(0xFFFFFFFFu, v[k] > limit);
+      while (who != 0) {
+        const int from = __ffs(who) - 1;
+        who &= who - 1;
+        const Key x = key_of(__shfl_sync(0xFFFFFFFFu, v[k], from), column + from * N + k);
+        const int at = __popc(__ballot_sync(0xFFFFFFFFu, key > x));
+        const Key before = __shfl_up_sync(0xFFFFFFFFu, key, 1);
+        key = lane < at ? key : lane == at ? x : before;
       }
     }
-  }
-  // Notes a tile's candidates among the warp's floor: the each-th largest of the lanes' maxima and of those before (a
-  // lower bound, as a lane may have had more than one).
-  __device__ __forceinline__ void note(float lane_max, int lane) {
-    uint32_t u = in_order(lane_max);
-    u = u > 0x007FFFFFu ? u : 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      if (i >= floors.each) break;
-      uint32_t k = __reduce_max_sync(0xFFFFFFFFu, u);
-      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, u == k)) - 1) u = 0;
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {  // into its place, the least falls out
-        const uint32_t above = max(best[j], k);
-        k = min(best[j], k), best[j] = above;
-      }
-    }
-    uint32_t f = best[0];
-#pragma unroll
-    for (int j = 1; j < kEach; ++j) f = j < floors.each ? best[j] : f;
-    if (lane == 0) floors.at[warp] = f;
+    const uint32_t last = __shfl_sync(0xFFFFFFFFu, uint32_t(key >> 32), top - 1);
+    const float t = last != 0 ? out_of_order(last) : -INFINITY;
+    if (t > thr) thr = t;
   }
   // What the lanes' maxima of the first tile say: at least `top` of the warp's values are not below the top-th of them.
-  __device__ __forceinline__ void first(float lane_max, int lane) {
+  // Returns the lane-th largest of them.
+  __device__ __forceinline__ uint32_t first(float lane_max, int lane) {
     uint32_t u = in_order(lane_max);
 #pragma unroll
     for (int size = 2; size <= 32; size *= 2) {  // descending over the lanes
@@ -202,11 +153,15 @@ struct List {
     }
     const float t = value_before(__shfl_sync(0xFFFFFFFFu, u, top - 1));
     if (t > thr) thr = t;
+    return u;
   }
-  // The warps' floors together: `top` values of the row are not below the least of them.  (One read early or late
-  // is only a lower one: what is left out is never needed.)
-  __device__ __forceinline__ void share(int lane) {
-    const uint32_t f = *reinterpret_cast<volatile uint32_t*>(floors.at + lane % floors.warps);
+  // The each-th largest of every warp of a row: `top` values of the row are not below the least of them.  (One read
+  // early or late is only a lower one: what is left out is never needed.)
+  __device__ __forceinline__ void tell(uint32_t* floors, int each, int warp, int lane) const {
+    if (lane == each - 1) floors[warp] = max(floors[warp], uint32_t(key >> 32));
+  }
+  __device__ __forceinline__ void hear(const uint32_t* floors, int warps, int lane) {
+    const uint32_t f = *reinterpret_cast<const volatile uint32_t*>(floors + lane % warps);
     const float t = value_before(__reduce_min_sync(0xFFFFFFFFu, f));
     if (t > thr) thr = t;
   }
@@ -223,11 +178,9 @@ struct Shared<true> {
   Part part[kWarps];
   Part ctas[kMaxParts];
   Key lists[kMaxParts * LOCO_MAX_TOP];  // the CTAs' largest
-  Key keys[kWarps][kListed + 128];
-  Key kept[kWarps][LOCO_MAX_TOP];
-  Key chosen[kWarps * kListed];  // of all warps' lists, what can be among the largest
+  Key chosen[kWarps * LOCO_MAX_TOP];  // of all warps' largest, what can be among the row's
   Key best[LOCO_MAX_TOP];
-  int count[kWarps], n_chosen;
+  int n_chosen;
   uint32_t floors[kWarps], least[kWarps];
 };
 
@@ -276,18 +229,12 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
   const Pair c2 = pair(c, c);
 
   Part mine{kLowest, 0.0f, 0.0f};
-  List list{};
-  if constexpr (TOP) {
-    // a row of one warp has its floor to itself
-    const Floors floors{WPR == 1 ? &sh.floors[warp] : sh.floors, WPR, (a.top + WPR - 1) / WPR};
-    list = List{sh.keys[warp], sh.kept[warp], &sh.count[warp], floors, a.top, WPR == 1 ? 0 : warp, -INFINITY, {0, 0, 0, 0}};
-    if (lane == 0) sh.count[warp] = 0, sh.floors[warp] = 0;
-    __syncwarp();
-    if constexpr (WPR > 1) {
-      if (threadIdx.x < LOCO_MAX_TOP) sh.best[threadIdx.x] = 0;
-      if (threadIdx.x == 0) sh.n_chosen = 0;
-      __syncthreads();
-    }
+  Largest list{0, -INFINITY, a.top};
+  if constexpr (TOP && WPR > 1) {
+    if (lane == 0) sh.floors[warp] = 0;
+    if (threadIdx.x < LOCO_MAX_TOP) sh.best[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sh.n_chosen = 0;
+    __syncthreads();
   }
   // single elements at the row's ends
   const auto take_one = [&](int64_t from, int n) {
@@ -296,7 +243,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
     const float e = max_nan((v[0] - m) * c, kLeast), s = exp2_f(e);
     mine = join(mine, Part{m, s, s * e}, c);
     if constexpr (TOP) {
-      if (__any_sync(0xFFFFFFFFu, v[0] > list.thr)) list.append(v, from + t, lane);
+      if (__any_sync(0xFFFFFFFFu, v[0] > list.thr)) list.insert(v, from, lane);
     }
   };
   if (me == 0 && shape.head > 0 && t < 32) take_one(0, int(shape.head));
@@ -333,7 +280,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
     for (int q = 1; q < kVectors; ++q) tile = max_nan(tile, largest<BF16>(w[q]));
     const float m = max_nan(mine.m, tile);
     const float down = max_nan((mine.m - m) * c, kLeast), f = exp2_f(down);
-    Pair s2 = pair(f * mine.s, 0.0f), d2 = pair(f * fmaf(mine.s, down, mine.d), 0.0f);
+    Pair s2 = pair(0.0f, 0.0f), d2 = s2;  // of this tile: a long row's sums stay a sum of tiles
     const Pair less = pair(-m, -m);
 #pragma unroll
     for (int q = 0; q < kVectors; ++q) {
@@ -349,14 +296,18 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
       }
     }
     const float2 s = halves(s2), d = halves(d2);
-    mine = Part{m, s.x + s.y, d.x + d.y};
+    mine = Part{m, fmaf(f, mine.s, s.x + s.y), fmaf(f, fmaf(mine.s, down, mine.d), d.x + d.y)};
     if constexpr (TOP) {
-      if (first)
-        list.first(tile, lane);
-      else if (WPR > 1)
-        list.share(lane);
-      first = false;
+      const int each = (a.top + kWarps - 1) / kWarps;
+      if (first) {
+        const uint32_t u = list.first(tile, lane);
+        if (WPR > 1) {
+          if (lane == each - 1) sh.floors[warp] = u;
+          __syncthreads();  // (a row's warps take the same number of tiles)
+        }
+      }
       if (__any_sync(0xFFFFFFFFu, tile > list.thr)) {
+        if (WPR > 1) list.hear(sh.floors, kWarps, lane);
 #pragma unroll
         for (int q = 0; q < kVectors; ++q) {
           const uint4 again = shared16(at + q * kPiece);  // (not kept in registers for this)
@@ -369,14 +320,11 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
             const float2 h = halves(v[k]);
             x[2 * k] = h.x, x[2 * k + 1] = h.y;
           }
-          list.append(x, shape.head + (i + q * kTeam + t) * V, lane);
+          list.insert(x, shape.head + (i + q * kTeam + (t - lane)) * V, lane);
         }
-        // the thresholds move up with every tile that had something: later ones seldom have
-        if (WPR > 1)
-          list.note(tile, lane);
-        else
-          list.order(lane);
+        if (WPR > 1) list.tell(sh.floors, each, warp, lane);
       }
+      first = false;
     }
   }
   const int64_t tail = shape.head + shape.vectors * V;
@@ -391,14 +339,6 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
     mine = lane & o ? join(other, mine, c) : join(mine, other, c);
   }
   Part all = mine;
-  const Key* best = nullptr;
-  if constexpr (TOP && WPR == 1) {
-    list.order(lane);
-    const int n = *list.count;
-    if (lane >= n && lane < a.top) list.keys[lane] = 0;
-    __syncwarp();
-    best = list.keys;
-  }
   if constexpr (WPR > 1) {
     if (lane == 0) sh.part[warp] = mine;
     if constexpr (TOP) {
@@ -407,14 +347,11 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
     __syncthreads();
     all = join_eight(sh.part[lane % kWarps], lane, c);
     if constexpr (TOP) {
-      // no value below the highest of the warps' thresholds can be among the largest; each list holds kListed at most
+      // no value below the highest of the warps' thresholds can be among the largest
       const uint32_t least = __reduce_max_sync(0xFFFFFFFFu, sh.least[lane % kWarps]);
-      const int n = *list.count;
-      for (int i = lane; i < n; i += 32)
-        if (uint32_t(list.keys[i] >> 32) >= least) sh.chosen[atomicAdd(&sh.n_chosen, 1)] = list.keys[i];
+      if (lane < a.top && uint32_t(list.key >> 32) >= least) sh.chosen[atomicAdd(&sh.n_chosen, 1)] = list.key;
       __syncthreads();
       choose(sh.chosen, sh.n_chosen, a.top, sh.best);
-      best = sh.best;
     }
     if constexpr (CLUSTER) {
       // everything goes to the first CTA
@@ -455,7 +392,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
   }
   if constexpr (TOP) {
     if (t < a.top) {
-      const Key k = best[t];
+      const Key k = WPR > 1 ? sh.best[t] : list.key;
       const bool some = k != 0 && !nan;
       if (a.top_ids != nullptr) a.top_ids[row * a.top + t] = some ? key_column(k) : -1;
       if (a.top_logp != nullptr)
@@ -486,7 +423,13 @@ cudaError_t run_fwd(const LogprobFwdArgs& a, int parts, cudaStream_t s) {
 }
 template <bool BF16, bool TOP>
 cudaError_t run_fwd_shape(const LogprobFwdArgs& a, int sms, cudaStream_t s) {
-  if (a.vocab <= 1024) return run_fwd<BF16, 1, TOP, false>(a, 1, s);
+  // A warp to a row where rows fill the warps: its fixed cost is a fifth of a CTA's, its time for one row five times.
+  // (bf16, five alternatives, us as warps / as CTAs: 152 x 2000 7.4 / 5.9, 600 x 2000 7.8 / 9.0, 1216 x 2000 7.8 / 15.4,
+  // 600 x 16000 20 / 13, 1216 x 16000 20 / 24, 4096 x 32000 67 / 92, 8192 x 32000 112 / 177, 4096 x 131072 204 / 217;
+  // without alternatives 4096 x 131072 173 / 165.)
+  const int64_t bytes = a.vocab * (BF16 ? 2 : 4);
+  const int64_t least = a.vocab <= 1024 ? 0 : a.vocab <= 2048 ? 4 : bytes <= 32768 ? 8 : 16;  // rows to an SM
+  if (bytes <= 131072 && a.rows >= least * sms) return run_fwd<BF16, 1, TOP, false>(a, 1, s);
   // several CTAs to a row while the grid leaves SMs without work and a part still fills a CTA's threads once
   int parts = 1;
   while (parts < 8 && a.rows * parts * 2 <= 2 * sms && a.vocab >= int64_t(parts) * 2 * kThreadsLp * kVec<BF16>) parts *= 2;

@@ -31,8 +31,8 @@ def bounds(z, want):
     p = torch.where(logp > -INF, logp.exp(), torch.zeros_like(logp))
     d = torch.where(p > 0, (m[:, None] - z), torch.zeros_like(z))       # deviations from the maximum
     mean_d, ls = (p * d).sum(1), (lse - m)
-    # a thread adds one term of its vocab / 256 (two at a time; of its row's 1024 at most / 32), then 13 joins; a
-    # term's exponent is off by 4 u of its deviation, 2^x by 4 u
+    # a thread adds 16 terms of a tile, two at a time, and its tiles, of vocab / 512 at most (where a warp has the row),
+    # then 13 joins; a term's exponent is off by 4 u of its deviation, 2^x by 4 u
     n = z.shape[1] / 512 + 32 + 16
     rel = n * U + 4 * U + 4 * U * mean_d
     t_lse = rel + 3 * U * (m.abs() + lse.abs() + ls)
@@ -120,6 +120,23 @@ def test_alternatives_in_ordered_rows(L, order, vocab, dtype):
     z = v.to(dtype).repeat(3, 1)
     y = torch.tensor([0, vocab - 1, vocab // 2], device="cuda")
     check_forward(L, z, y, 32, 1.0)
+
+
+@pytest.mark.parametrize("rows,vocab", [(700, 1500), (1300, 4001), (2500, 20003), (2440, 32768)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("top", [0, 3, 32])
+@pytest.mark.parametrize("order", ["random", "up"])
+def test_many_long_rows(L, rows, vocab, dtype, top, order):
+    """So many rows that a warp takes one, with rows in which every value is a candidate and rows that are masked."""
+    g = gen(27)
+    z = logits(g, rows, vocab, dtype, vocab + 3)
+    if order == "up":
+        z.copy_(z.sort(1)[0])
+    z[5] = -INF
+    z[6, : vocab - 2] = -INF
+    z[7, 0] = math.nan
+    z[8] = 1.0
+    check_forward(L, z, torch.randint(0, vocab, (rows,), generator=g, device="cuda"), top, 1.0)
 
 
 @pytest.mark.parametrize("rows,vocab", SHAPES)
