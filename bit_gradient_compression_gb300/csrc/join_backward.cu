@@ -58,20 +58,8 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
 #pragma unroll
     for (int i = 0; i < P; ++i) sums[k][i] = zero;
   }
-  // q = du gm ; p = t w pg, pg with the gate and the scale in it, 0 past the row's end: whatever else a thread
-  // has there (deviations of nothing from a mean) then reaches no sum of the row
   const uint32_t base = threadIdx.x * 16;
   constexpr uint32_t kStage = 2 * (RowX::kBytes + RowY::kBytes), kOwn = kStages * kStage;
-  {
-    Pair g[P], v[P];
-    params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, g);
-    params<RowX, E>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
-#pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = v[i] * (g[i] * both(a.s));
-    keep<E, kThreadsCta>(base + kOwn, 1, v);
-    params<RowX, E>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
-    keep<E, kThreadsCta>(base + kOwn, 0, v);
-  }
   RowX dhn, hn;
   RowY dun, yn;
   float m1n = 0.0f, r1n = 1.0f, m2n = 0.0f, r2n = 1.0f, wn = 1.0f;
@@ -94,7 +82,19 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
     slot ^= 1;
   };
   cudaTriggerProgrammaticLaunchCompletion();  // the parameters' kernel may wait on its SMs
-  fetch(first);
+  fetch(first);  // on its way while the parameters come
+  // q = du gm ; p = t w pg, pg with the gate and the scale in it, 0 past the row's end: whatever else a thread
+  // has there (deviations of nothing from a mean) then reaches no sum of the row
+  {
+    Pair g[P], v[P];
+    params<RowX, E>(a.gate, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, g);
+    params<RowX, E>(a.post_gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = v[i] * (g[i] * both(a.s));
+    keep<E, kThreadsCta>(base + kOwn, 1, v);
+    params<RowX, E>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
+    keep<E, kThreadsCta>(base + kOwn, 0, v);
+  }
   const Pair a2 = both(a.a);
   for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
     const bool live = row < n_rows;
@@ -418,8 +418,12 @@ cudaError_t run(const JoinBwdArgs& a, bool pwide, int ctas, int* partials, cudaS
   if (e != cudaSuccess) return e;
   constexpr int kTeams = kTeamCta<G> / G;
   if (a.partials != nullptr) {
-    // few rows: four at least to a team, so that the partial rows stay fewer than a quarter of the rows
-    const int64_t most = a.rows / (4 * kTeams) * ctas;
+    // few rows: one CTA to an SM, or four rows and more to a team, as partial rows cost the second kernel (us at one, two,
+    // four and eight rows a team: 64 x 4096 bf16 13.5, 15.0, 19.0, 25.6; 500 x 2048 fp32 22.1, 21.6, 18.0, 24.8)
+    int sms = 0;
+    const cudaError_t e2 = sm_count(&sms);
+    if (e2 != cudaSuccess) return e2;
+    const int64_t four = a.rows / (4 * kTeams) * ctas, most = four > sms ? four : sms;
     if (cap > kJoinPartials * ctas) cap = kJoinPartials * ctas;
     if (cap > most) cap = most > ctas ? int(most) : ctas;
   }
@@ -476,6 +480,7 @@ cudaError_t rows_kernel(const JoinBwdArgs& a, int* sums, int* partials, cudaStre
     if (a.x_bf16) {
       if (a.cols <= 256) return run_bf16<32, 8, false>(a, pwide, 1, *sums, partials, s);
       if (a.cols <= 512) return run_bf16<32, 16, false>(a, pwide, 1, *sums, partials, s);
+      if (a.cols <= 1024) return run_bf16<128, 8, false>(a, pwide, 1, *sums, partials, s);
       if (a.cols <= 2048) return run_bf16<128, 16, false>(a, pwide, 1, *sums, partials, s);
       if (a.cols <= 4096) return run_bf16<256, 16, false>(a, pwide, 1, *sums, partials, s);
       return run_bf16<256, 16, true>(a, pwide, ctas, *sums, partials, s);

@@ -389,6 +389,7 @@ template <typename Row, int E, int G, bool CL>
 __device__ __forceinline__ void layer_stats(Team<G, CL>& team, const Pair (&v)[E / 2], int t, int cols, const Counts& n,
                                             float* mean, float* var) {
   Pair s2 = v[0], q2 = both(0.0f);
+  const bool full = Row::column(t, E - 1) < cols;
 #pragma unroll
   for (int i = 1; i < E / 2; ++i) s2 = s2 + v[i];
   const float m = warp_total(total(s2)) * n.inv_warp;
@@ -396,7 +397,7 @@ __device__ __forceinline__ void layer_stats(Team<G, CL>& team, const Pair (&v)[E
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) {
     Pair d = v[i] + less;
-    if (Row::column(t, 2 * i + 1) >= cols) d = pair(Row::column(t, 2 * i) < cols ? halves(d).x : 0.0f, 0.0f);
+    if (!full && Row::column(t, 2 * i + 1) >= cols) d = pair(Row::column(t, 2 * i) < cols ? halves(d).x : 0.0f, 0.0f);
     q2 = fma(d, d, q2);
   }
   float w[2] = {m, warp_total(total(q2))};

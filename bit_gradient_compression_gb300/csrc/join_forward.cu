@@ -64,6 +64,21 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 ? 768 : 1024) / kTeamCta
   const uint32_t base = threadIdx.x * 16;
   constexpr uint32_t kStage = RowX::kBytes + RowY::kBytes, kOwn = kStages * kStage;
   const bool betas = a.post_beta != nullptr || a.beta != nullptr;
+  RowX xn;
+  RowY yn;
+  float wn = 1.0f;
+  uint32_t slot = 0;
+  const auto fetch = [&](uint32_t row) {
+    xn.at = base + slot * kStage, yn.at = xn.at + RowX::kBytes;
+    if (row < n_rows) {
+      xn.load(a.x, row, a.ldx, t, cols, edges);
+      yn.load(a.y, row, a.ldy, t, cols, edges);
+      if (a.row_gate != nullptr) wn = __ldg(a.row_gate + row);
+    }
+    cp_async_commit();
+    slot ^= 1;
+  };
+  fetch(first);  // on its way while the parameters come
   {
     // h = a x + w (yh pg + pb), pg and pb with the gate in them, 0 past the row's end
     Pair g[E / 2], v[E / 2];
@@ -83,21 +98,6 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 ? 768 : 1024) / kTeamCta
     params<RowX, E>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
     keep<E, kThreadsCta>(base + kOwn, 1, v);
   }
-  RowX xn;
-  RowY yn;
-  float wn = 1.0f;
-  uint32_t slot = 0;
-  const auto fetch = [&](uint32_t row) {
-    xn.at = base + slot * kStage, yn.at = xn.at + RowX::kBytes;
-    if (row < n_rows) {
-      xn.load(a.x, row, a.ldx, t, cols, edges);
-      yn.load(a.y, row, a.ldy, t, cols, edges);
-      if (a.row_gate != nullptr) wn = __ldg(a.row_gate + row);
-    }
-    cp_async_commit();
-    slot ^= 1;
-  };
-  fetch(first);
   const Pair a2 = both(a.a);
   for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
     const bool live = row < n_rows;  // (where it is not, the values are an earlier row's, and nothing is stored)
@@ -266,6 +266,7 @@ cudaError_t launch_join_forward(const JoinFwdArgs& a, cudaStream_t s) {
   if (wide && a.x_bf16) {
     if (a.cols <= 256) return run_bf16<32, 8, false>(a, pwide, 1, s);
     if (a.cols <= 512) return run_bf16<32, 16, false>(a, pwide, 1, s);
+    if (a.cols <= 1024) return run_bf16<128, 8, false>(a, pwide, 1, s);
     if (a.cols <= 2048) return run_bf16<128, 16, false>(a, pwide, 1, s);
     if (a.cols <= 4096) return run_bf16<256, 16, false>(a, pwide, 1, s);
     return run_bf16<256, 16, true>(a, pwide, ctas, s);
