@@ -223,7 +223,7 @@ struct Staged {
 
 template <int BITS, bool PBF16, bool GBF16, bool DITHER, int MAX>
 __global__ void __launch_bounds__(kThreadsAdam, BITS == 32 ? 2 : 3) k_step_tensors(const __grid_constant__ AdamTensorList<MAX> l, uint32_t group) {
-  extern __shared__ __align__(16) uint8_t ring[];  // two stages
+  extern __shared__ __align__(128) uint8_t ring[];  // two stages
   using Stage = Staged<PBF16, GBF16>;
   const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
   const int lane = threadIdx.x & 31;

@@ -31,20 +31,17 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
   constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, P = E / 2, C = E / 8;
   JoinBwdArgs a = args;
   const int t = threadIdx.x % G, place = threadIdx.x / G;
-  Team<G, CL> team{&board, 0, 1, 0};
+  Team<G, CL> team(&board);
   int64_t c0 = 0;
   uint32_t first = blockIdx.x * kTeams + place, step = gridDim.x * kTeams;  // (rows are below 2^31)
   const uint32_t n_rows = uint32_t(a.rows);
   if constexpr (CL) {
-    const auto cluster = cooperative_groups::this_cluster();
-    team.ctas = int(cluster.num_blocks()), team.rank = int(cluster.block_rank());
     c0 = int64_t(team.rank) * G * E, first = blockIdx.x / team.ctas, step = gridDim.x / team.ctas;
     a.dh = from_column(a.dh, c0, a.x_bf16), a.du = from_column(a.du, c0, a.y_bf16);
     a.h = from_column(a.h, c0, a.x_bf16), a.y = from_column(a.y, c0, a.y_bf16);
     a.dx = from_column(a.dx, c0, a.x_bf16), a.dy = from_column(a.dy, c0, a.y_bf16);
     a.post_gamma = from_column(a.post_gamma, c0, a.param_bf16), a.post_beta = from_column(a.post_beta, c0, a.param_bf16);
     a.gate = from_column(a.gate, c0, a.param_bf16), a.gamma = from_column(a.gamma, c0, a.param_bf16);
-    cluster.sync();  // every CTA's board is there
   }
   const int64_t rest = a.cols - c0;
   const int cols = rest <= 0 ? 0 : rest < G * E ? int(rest) : G * E;
@@ -257,6 +254,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
       }
     }
   }
+  team.part();
   if (a.partials == nullptr) return;
   // one partial row a team of CTAs; the teams of a CTA are added through shared memory in their order
   float* out = a.partials + (CL ? int64_t(blockIdx.x) / team.ctas : int64_t(blockIdx.x)) * kJoinSums * a.cols + c0;
@@ -295,7 +293,7 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G
 // Rows of any length: a CTA of 1024 reads its row for each sum and output, and its partial sums lie in the workspace.
 __global__ void __launch_bounds__(1024, 1) k_join_bwd_long(const JoinBwdArgs a) {
   __shared__ Board<1024, false> board;
-  Team<1024, false> team{&board, 0, 1, 0};
+  Team<1024, false> team(&board);
   const float inv_cols = 1.0f / float(a.cols);
   const bool level = !a.rms;
   float* out = a.partials == nullptr ? nullptr : a.partials + int64_t(blockIdx.x) * kJoinSums * a.cols;
@@ -515,6 +513,13 @@ cudaError_t launch_join_backward(const JoinBwdArgs& a, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr, cfg.numAttrs = a.rows > 0 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, k_join_bwd_params, a, partials, sums);
+}
+
+cudaError_t read_join_backward_timeouts(int64_t* count) {
+  unsigned long long v = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(&v, g_join_timeouts, sizeof v);
+  if (e == cudaSuccess) *count = int64_t(v);
+  return e;
 }
 
 }  // namespace loco

@@ -6,9 +6,12 @@
 
 #include <cooperative_groups.h>
 
+#include <cstddef>
+
 #include "device_common.cuh"
 #include "layers_common.cuh"
 #include "steps_internal.h"
+#include "tensor_core.cuh"
 
 namespace loco {
 
@@ -20,7 +23,7 @@ constexpr int kTeamCta = G < 128 ? 128 : G;  // threads of a CTA
 // The CTA's dynamic shared memory: rows on their way and the threads' own parameters, by byte offsets.  (Read and written
 // as plain memory, so that the compiler may order the accesses; the copies into it and their waits are barriers to that.)
 __device__ __forceinline__ uint8_t* ring() {
-  extern __shared__ __align__(16) uint8_t join_ring[];
+  extern __shared__ __align__(128) uint8_t join_ring[];
   return join_ring;
 }
 __device__ __forceinline__ uint4 ring16(uint32_t at) { return *reinterpret_cast<const uint4*>(ring() + at); }
@@ -285,93 +288,146 @@ __device__ __forceinline__ void recall(uint32_t at, int which, int e, Pair (&v)[
   }
 }
 
-// What a team's warps tell one another: N values of each.  Consecutive calls alternate between two areas, so
-// that one barrier each is enough.  In a cluster every warp writes its values into each CTA's memory.
-constexpr int kMaxCluster = 8;
+// What a team's warps tell one another: N values of each.  Consecutive exchanges alternate between two areas, so that
+// one barrier each is enough.  In a cluster every warp sends its values into each CTA's memory, where they count at a
+// barrier of the area (st.async; a barrier of the whole cluster would wait for every store to global memory before it
+// as well: 4096 x 8192 bf16 forward 60 us with one, 2048 x 16384 89 us).
+// An area is written again two exchanges later, by a CTA that has what all warps sent in the exchange between, each
+// after it had read this one.
+constexpr int kMaxCluster = 8, kMaxSums = 5;
+constexpr uint64_t kWaitNs = 2000000000;  // longest wait for the cluster
+__device__ unsigned long long g_join_timeouts;  // waits that ran out
+
 template <int G, bool CL>
 struct Board {
   static constexpr int kW = G / 32, kAll = kW * (CL ? kMaxCluster : 1);
-  float v[2][3][kAll < 32 ? 32 : kAll];
+  float v[2][kMaxSums][kAll];
+  uint64_t bar[CL ? 2 : 1];
 };
 template <int G, bool CL>
 struct Team {
   Board<G, CL>* board;
   int turn, ctas, rank;
+  uint32_t peer, parity;  // the board of the cluster's CTA lane % 8; of the areas' barriers, a bit each
+  bool lost;              // a wait ran out: what is read from then on is NaN, and nothing is waited for
 
+  __device__ __forceinline__ Team(Board<G, CL>* b) : board(b), turn(0), ctas(1), rank(0), peer(0), parity(0), lost(false) {
+    if constexpr (CL) {
+      const auto cluster = cooperative_groups::this_cluster();
+      ctas = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+      const uint32_t to = threadIdx.x % kMaxCluster;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(smem_addr(board)), "r"(to < uint32_t(ctas) ? to : 0u));
+      if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&board->bar[0]), 1), mbar_init(smem_addr(&board->bar[1]), 1);
+        mbar_init_fence();
+      }
+      cluster.sync();  // every CTA's board is there
+    }
+  }
+  // Before the kernel ends: no CTA leaves while another may still send to it.
+  __device__ __forceinline__ void part() const {
+    if constexpr (CL) cooperative_groups::this_cluster().sync();
+  }
   __device__ __forceinline__ int warps() const { return G / 32 * ctas; }
-  // Value `which` of this warp; lane `lane` of `lanes` neighbours tells it to the cluster's CTA of that number.
+  // Value `which` of this warp; lane `lane` of at least eight neighbours tells it to the cluster's CTA of that number.
   __device__ __forceinline__ void write(int which, int lane, float v) {
     const int warp = threadIdx.x / 32 % (G / 32);
     if constexpr (CL) {
+      using B = Board<G, CL>;
+      const uint32_t at = peer + uint32_t(offsetof(B, v)) + uint32_t(sizeof(B::v[0])) * turn + uint32_t(sizeof(B::v[0][0])) * which +
+                          uint32_t(rank * (G / 32) + warp) * 4;
       if (lane < ctas)
-        cooperative_groups::this_cluster().map_shared_rank(board, lane)->v[turn][which][rank * (G / 32) + warp] = v;
+        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(at),
+                     "r"(__float_as_uint(v)), "r"(peer + uint32_t(offsetof(B, bar)) + 8 * turn)
+                     : "memory");
     } else {
       if (lane == 0) board->v[turn][which][warp] = v;
     }
   }
-  __device__ __forceinline__ void meet() {
-    if constexpr (CL)
-      cooperative_groups::this_cluster().sync();
-    else
+  // All `n` values of every warp are there.
+  __device__ __forceinline__ void meet(int n) {
+    if constexpr (CL) {
+      const uint32_t bar = smem_addr(&board->bar[turn]);
+      if (threadIdx.x == 0) mbar_arrive_expect(bar, uint32_t(n * warps()) * 4);
+      if (!lost && !arrived(bar, parity >> turn & 1)) {
+        lost = true;
+        if ((threadIdx.x & 31) == 0) atomicAdd(&g_join_timeouts, 1ull);
+      }
+      parity ^= 1u << turn;
+    } else {
       __syncthreads();
+    }
   }
-  // Sum of the warps' values `which` in each of the 16 lanes of a half warp.
+  __device__ __forceinline__ static bool arrived(uint32_t bar, uint32_t parity) {
+    const auto test = [&] {
+      uint32_t done;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done)
+          : "r"(bar), "r"(parity)
+          : "memory");
+      return done != 0;
+    };
+    if (test()) return true;
+    const uint64_t start = global_ns();
+    while (global_ns() - start < kWaitNs)
+      if (test()) return true;
+    return false;
+  }
+  // Sum of the warps' values `which`, in each lane of a group of LANES.
+  template <int LANES>
   __device__ __forceinline__ float read(int which) const {
     constexpr int kW = G / 32;
-    const int l = threadIdx.x & 15;
-    float v;
+    const int l = threadIdx.x % LANES;
+    float v = 0.0f;
     if constexpr (CL) {
-      v = 0.0f;
-      for (int k = l; k < kW * ctas; k += 16) v += board->v[turn][which][k];
-    } else if constexpr (kW > 16) {
-      v = board->v[turn][which][l] + board->v[turn][which][l + 16];
+      for (int k = l; k < kW * ctas; k += LANES) v += board->v[turn][which][k];
+      if (lost) v = __uint_as_float(0x7FC00000u);
+    } else if constexpr (kW >= LANES) {
+#pragma unroll
+      for (int k = 0; k < kW; k += LANES) v += board->v[turn][which][l + k];
     } else {
       v = board->v[turn][which][l % kW];
     }
 #pragma unroll
-    for (int o = CL || kW > 16 ? 8 : kW / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = (CL || kW > LANES ? LANES : kW) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
   }
-  // Sums over the team, the same in all its threads.
-  __device__ __forceinline__ void sum(float (&v)[1]) {
-    v[0] = warp_total(v[0]);
-    if constexpr (G > 32) {
-      write(0, threadIdx.x & 31, v[0]);
-      meet();
-      v[0] = read(0);
-      turn ^= 1;
+  // Sums over the team of N values, the same in all its threads, with one exchange between its warps.  Of two or four
+  // values the halves or quarters of a warp take one each, so that all of them take little more than one does.
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N]) {
+    static_assert(N >= 1 && N <= kMaxSums, "");
+    constexpr int kGroups = N >= 4 ? 4 : N >= 2 ? 2 : 1, kLanes = 32 / kGroups, kRead = kGroups == 4 ? 8 : 16;
+    const int lane = threadIdx.x & 31, group = lane / kLanes, at = lane % kLanes;
+    float x = v[0];
+    if constexpr (kGroups == 4) {
+      const bool upper = lane & 16, odd = lane & 8;
+      const float p = (upper ? v[2] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[2], 16);
+      const float q = (upper ? v[3] : v[1]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[1] : v[3], 16);
+      x = (odd ? q : p) + __shfl_xor_sync(0xFFFFFFFFu, odd ? p : q, 8);
+    } else if constexpr (kGroups == 2) {
+      const bool upper = lane & 16;
+      x = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[1], 16);
     }
-  }
-  // Two values: the halves of a warp take one each after the first step.
-  __device__ __forceinline__ float warp_sum_of_two(float a, float b) {
-    const bool upper = threadIdx.x & 16;
-    float x = (upper ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    return x;
-  }
-  __device__ __forceinline__ void sum(float (&v)[2]) {
-    float x = warp_sum_of_two(v[0], v[1]);
+    for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    constexpr bool kOdd = N > kGroups;  // the last value by itself
+    if constexpr (kOdd) v[N - 1] = warp_total(v[N - 1]);
     if constexpr (G > 32) {
-      write((threadIdx.x & 16) / 16, threadIdx.x & 15, x);
-      meet();
-      x = read((threadIdx.x & 16) / 16);
+      write(group, at, x);
+      if constexpr (kOdd) write(N - 1, lane, v[N - 1]);
+      meet(N);
+      x = read<kRead>(group);
+      if constexpr (kOdd) v[N - 1] = read<kRead>(N - 1);
       turn ^= 1;
     }
-    v[0] = __shfl_sync(0xFFFFFFFFu, x, 0), v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
-  }
-  __device__ __forceinline__ void sum(float (&v)[3]) {
-    float x = warp_sum_of_two(v[0], v[1]);
-    v[2] = warp_total(v[2]);
-    if constexpr (G > 32) {
-      write((threadIdx.x & 16) / 16, threadIdx.x & 15, x);
-      write(2, threadIdx.x & 31, v[2]);
-      meet();
-      x = read((threadIdx.x & 16) / 16);
-      v[2] = read(2);
-      turn ^= 1;
+    if constexpr (kGroups == 1) {
+      v[0] = x;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, x, k * kLanes);
     }
-    v[0] = __shfl_sync(0xFFFFFFFFu, x, 0), v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
   }
 };
 
@@ -381,55 +437,71 @@ struct Counts {
   float warp[4];             // columns of the team's warps lane, lane + 32, ...
 };
 
-// Mean and variance of a row with one exchange between its warps: each warp takes its own mean and then its squared
+// Means and variances of N rows with one exchange between the warps: each warp takes its own mean and then its squared
 // deviations from that; together they make the row's mean, and the variance with what the warps' means are off it.
-// No difference of large sums: a row far from 0 loses no digits.  v is 0 past the row's end, of which cols columns
-// are this CTA's.
-template <typename Row, int E, int G, bool CL>
-__device__ __forceinline__ void layer_stats(Team<G, CL>& team, const Pair (&v)[E / 2], int t, int cols, const Counts& n,
-                                            float* mean, float* var) {
-  Pair s2 = v[0], q2 = both(0.0f);
+// No difference of large sums: a row far from 0 loses no digits.  The rows are 0 past their end, of which cols columns
+// are this CTA's; v(k, i) is pair i of row k.
+template <typename Row, int E, int N, int G, bool CL, typename Values>
+__device__ __forceinline__ void layer_stats(Team<G, CL>& team, const Values& v, int t, int cols, const Counts& n,
+                                            float (&mean)[N], float (&var)[N]) {
   const bool full = Row::column(t, E - 1) < cols;
+  float m[N], q[N];
 #pragma unroll
-  for (int i = 1; i < E / 2; ++i) s2 = s2 + v[i];
-  const float m = warp_total(total(s2)) * n.inv_warp;
-  const Pair less = both(-m);
+  for (int k = 0; k < N; ++k) {
+    Pair s2 = v(k, 0);
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    Pair d = v[i] + less;
-    if (!full && Row::column(t, 2 * i + 1) >= cols) d = pair(Row::column(t, 2 * i) < cols ? halves(d).x : 0.0f, 0.0f);
-    q2 = fma(d, d, q2);
+    for (int i = 1; i < E / 2; ++i) s2 = s2 + v(k, i);
+    m[k] = total(s2);
   }
-  float w[2] = {m, warp_total(total(q2))};
+#pragma unroll
+  for (int k = 0; k < N; ++k) m[k] = warp_total(m[k]) * n.inv_warp;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const Pair less = both(-m[k]);
+    Pair q2 = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      Pair d = v(k, i) + less;
+      if (!full && Row::column(t, 2 * i + 1) >= cols) d = pair(Row::column(t, 2 * i) < cols ? halves(d).x : 0.0f, 0.0f);
+      q2 = fma(d, d, q2);
+    }
+    q[k] = total(q2);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) q[k] = warp_total(q[k]);
   if constexpr (G > 32) {
-    team.write(0, threadIdx.x & 31, w[0]);
-    team.write(1, threadIdx.x & 31, w[1]);
-    team.meet();
-    constexpr int kW = G / 32, kEntries = CL ? kMaxCluster * kW / 32 : 1;
     const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < N; ++k) team.write(2 * k, lane, m[k]), team.write(2 * k + 1, lane, q[k]);
+    team.meet(2 * N);
+    constexpr int kW = G / 32, kEntries = CL ? kMaxCluster * kW / 32 : 1;
     const Board<G, CL>& board = *team.board;
     const auto across = [](float x) {
 #pragma unroll
       for (int o = CL ? 16 : kW / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
       return x;
     };
-    const float c = board.v[team.turn][0][0];  // the first warp's mean
-    float d[kEntries], q = 0.0f, s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kEntries; ++k) {
-      const int at = CL ? lane + 32 * k : lane % kW;
-      d[k] = n.warp[k] > 0.0f ? board.v[team.turn][0][at] - c : 0.0f;
-      q += n.warp[k] > 0.0f ? board.v[team.turn][1][at] : 0.0f;
-      s = fmaf(n.warp[k], d[k], s);
+    for (int k = 0; k < N; ++k) {
+      const float c = team.lost ? __uint_as_float(0x7FC00000u) : board.v[team.turn][2 * k][0];  // the first warp's mean
+      float d[kEntries], s = 0.0f;
+      q[k] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e) {
+        const int at = CL ? lane + 32 * e : lane % kW;
+        d[e] = n.warp[e] > 0.0f ? board.v[team.turn][2 * k][at] - c : 0.0f;
+        q[k] += n.warp[e] > 0.0f ? board.v[team.turn][2 * k + 1][at] : 0.0f;
+        s = fmaf(n.warp[e], d[e], s);
+      }
+      const float off = across(s) * n.inv_cols;
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e) q[k] = fmaf(n.warp[e] * (d[e] - off), d[e] - off, q[k]);
+      m[k] = c + off, q[k] = across(q[k]);
     }
-    const float off = across(s) * n.inv_cols;
-#pragma unroll
-    for (int k = 0; k < kEntries; ++k) q = fmaf(n.warp[k] * (d[k] - off), d[k] - off, q);
-    w[0] = c + off, w[1] = across(q);
     team.turn ^= 1;
   }
-  *mean = w[0];
-  *var = w[1] * n.inv_cols;
+#pragma unroll
+  for (int k = 0; k < N; ++k) mean[k] = m[k], var[k] = q[k] * n.inv_cols;
 }
 
 // all: columns of the row, of which this CTA has `cols`.

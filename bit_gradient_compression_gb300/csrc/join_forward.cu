@@ -21,64 +21,67 @@ size_t ring_bytes(bool betas) {
   return size_t(kStages) * (RowX::kBytes + RowY::kBytes) + size_t(kTeamCta<G>) * (betas ? 4 : 2) * E * sizeof(float);
 }
 
-template <int G, int E, bool CL, typename RowX, typename RowY>
-__global__ void __launch_bounds__(kTeamCta<G>, (E == 16 ? 768 : 1024) / kTeamCta<G>)
+// MERGED: the sums of a row's second norm and those of the next row's first are exchanged together, so that the team's
+// warps meet once a row.
+template <int G, int E, bool CL, bool MERGED, typename RowX, typename RowY>
+__global__ void __launch_bounds__(kTeamCta<G>, (E == 16 || (RowX::kBytes == 0 && (CL || G == 32)) ? 768 : 1024) / kTeamCta<G>)
     k_join_fwd(const JoinFwdArgs args, bool pwide) {
   __shared__ Board<G, CL> board;
   constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, C = E / 8;
   JoinFwdArgs a = args;
   const int t = threadIdx.x % G, place = threadIdx.x / G;
-  Team<G, CL> team{&board, 0, 1, 0};
+  Team<G, CL> team(&board);
   int64_t c0 = 0;
   uint32_t first = blockIdx.x * kTeams + place, step = gridDim.x * kTeams;  // (rows are below 2^31)
   const uint32_t n_rows = uint32_t(a.rows);
   if constexpr (CL) {
-    const auto cluster = cooperative_groups::this_cluster();
-    team.ctas = int(cluster.num_blocks()), team.rank = int(cluster.block_rank());
     c0 = int64_t(team.rank) * G * E, first = blockIdx.x / team.ctas, step = gridDim.x / team.ctas;
     a.x = from_column(a.x, c0, a.x_bf16), a.y = from_column(a.y, c0, a.y_bf16);
     a.h = from_column(a.h, c0, a.x_bf16), a.u = from_column(a.u, c0, a.y_bf16);
     a.post_gamma = from_column(a.post_gamma, c0, a.param_bf16), a.post_beta = from_column(a.post_beta, c0, a.param_bf16);
     a.gate = from_column(a.gate, c0, a.param_bf16);
     a.gamma = from_column(a.gamma, c0, a.param_bf16), a.beta = from_column(a.beta, c0, a.param_bf16);
-    cluster.sync();  // every CTA's board is there
   }
   const int64_t rest = a.cols - c0;
   const int cols = rest <= 0 ? 0 : rest < G * E ? int(rest) : G * E;
   const Edges edges{n_rows - 1, rest < (1 << 30) ? int(rest) : 1 << 30, c0 == 0};
   const Counts n = row_counts<RowX, G, E, CL>(team, t, cols, a.cols);
-  const auto stats = [&](const Pair (&v)[E / 2], float* mean, float* rstd) {
-    float var;
+  // of N rows; v(k, i): pair i of row k
+  const auto stats = [&](auto& mean, auto& rstd, const auto& v) {
+    constexpr int N = sizeof(mean) / sizeof(float);
     if (a.rms) {
-      Pair q = v[0] * v[0];
 #pragma unroll
-      for (int i = 1; i < E / 2; ++i) q = fma(v[i], v[i], q);
-      float s[1] = {total(q)};
-      team.sum(s);
-      *mean = 0.0f, var = s[0] * n.inv_cols;
+      for (int k = 0; k < N; ++k) {
+        Pair q = v(k, 0) * v(k, 0);
+#pragma unroll
+        for (int i = 1; i < E / 2; ++i) q = fma(v(k, i), v(k, i), q);
+        rstd[k] = total(q), mean[k] = 0.0f;
+      }
+      team.sum(rstd);
+#pragma unroll
+      for (int k = 0; k < N; ++k) rstd[k] = rsqrtf(fmaf(rstd[k], n.inv_cols, a.eps));
     } else {
-      layer_stats<RowX, E>(team, v, t, cols, n, mean, &var);
+      layer_stats<RowX, E>(team, v, t, cols, n, mean, rstd);
+#pragma unroll
+      for (int k = 0; k < N; ++k) rstd[k] = rsqrtf(rstd[k] + a.eps);
     }
-    *rstd = rsqrtf(var + a.eps);
   };
   const uint32_t base = threadIdx.x * 16;
   constexpr uint32_t kStage = RowX::kBytes + RowY::kBytes, kOwn = kStages * kStage;
   const bool betas = a.post_beta != nullptr || a.beta != nullptr;
-  RowX xn;
-  RowY yn;
-  float wn = 1.0f;
-  uint32_t slot = 0;
-  const auto fetch = [&](uint32_t row) {
-    xn.at = base + slot * kStage, yn.at = xn.at + RowX::kBytes;
+  RowX x, xn;  // of the row at work and of the next
+  RowY y, yn;
+  float w = 1.0f, wn = 1.0f;
+  const auto fetch = [&](RowX& x, RowY& y, float& w, uint32_t slot, uint32_t row) {
+    x.at = base + slot * kStage, y.at = x.at + RowX::kBytes;
     if (row < n_rows) {
-      xn.load(a.x, row, a.ldx, t, cols, edges);
-      yn.load(a.y, row, a.ldy, t, cols, edges);
-      if (a.row_gate != nullptr) wn = __ldg(a.row_gate + row);
+      x.load(a.x, row, a.ldx, t, cols, edges);
+      y.load(a.y, row, a.ldy, t, cols, edges);
+      if (a.row_gate != nullptr) w = __ldg(a.row_gate + row);
     }
     cp_async_commit();
-    slot ^= 1;
   };
-  fetch(first);  // on its way while the parameters come
+  fetch(x, y, w, 0, first);  // on its way while the parameters come
   {
     // h = a x + w (yh pg + pb), pg and pb with the gate in them, 0 past the row's end
     Pair g[E / 2], v[E / 2];
@@ -98,74 +101,124 @@ __global__ void __launch_bounds__(kTeamCta<G>, (E == 16 ? 768 : 1024) / kTeamCta
     params<RowX, E>(a.gamma, t, cols, a.param_bf16, pwide, 1.0f, 0.0f, v);
     keep<E, kThreadsCta>(base + kOwn, 1, v);
   }
-  const Pair a2 = both(a.a);
-  for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
-    const bool live = row < n_rows;  // (where it is not, the values are an earlier row's, and nothing is stored)
-    const RowX xc = xn;
-    const RowY yc = yn;
-    const Pair w = both(a.s * wn);
-    fetch(row + step);
+  if constexpr (MERGED) {
+    fetch(xn, yn, wn, 1, first + step);
     cp_async_wait<1>();
-    if (live) xc.settle(t, cols), yc.settle(t, cols);
-    Pair h[E / 2];  // y, then the joined stream
+    if (first < n_rows) x.settle(t, cols), y.settle(t, cols);
+  }
+  const auto whole = [](const RowY& from, Pair (&v)[E / 2]) {
 #pragma unroll
     for (int e = 0; e < C; ++e) {
-      Pair v[4];
-      yc.eight(e, v);
+      Pair p[4];
+      from.eight(e, p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[e * 4 + i] = v[i];
+      for (int i = 0; i < 4; ++i) v[e * 4 + i] = p[i];
     }
-    float m1 = 0.0f, r1 = 1.0f, m2 = 0.0f, r2 = 1.0f;
-    if (a.post) stats(h, &m1, &r1);
-    const Pair l1 = both(-m1), f1 = both(r1);
-    char* out = static_cast<char*>(a.h) + row * a.ldh * (a.x_bf16 ? 2 : 4);
+  };
+  float m1 = 0.0f, r1 = 1.0f;
+  const auto first_norm = [&](Pair (&v)[E / 2]) {
+    whole(y, v);
+    if (!a.post) return;
+    float m[1], r[1];
+    stats(m, r, [&](int, int i) { return v[i]; });
+    m1 = m[0], r1 = r[0];
+  };
+  Pair h[E / 2];  // the joined stream; before that, where it is read first, y
+  if (MERGED) first_norm(h);
+  const Pair a2 = both(a.a);
+  uint32_t slot = 0;
+  for (uint32_t row = first; row - (kTeams > 1 ? place : 0) < n_rows; row += step) {
+    // (where a row is not live, the values are an earlier row's, and nothing is stored)
+    const bool live = row < n_rows, next = row + step < n_rows;
+    if constexpr (!MERGED) {
+      slot ^= 1;
+      fetch(xn, yn, wn, slot, row + step);
+      cp_async_wait<1>();
+      if (live) x.settle(t, cols), y.settle(t, cols);
+      first_norm(h);
+    }
+    const Pair l1 = both(-m1), f1 = both(r1), ws = both(a.s * w);
+    char* to_h = static_cast<char*>(a.h) + row * a.ldh * (a.x_bf16 ? 2 : 4);
+    char* to_u = static_cast<char*>(a.u) + row * a.ldu * (a.y_bf16 ? 2 : 4);
 #pragma unroll
     for (int e = 0; e < C; ++e) {
-      Pair x[4], pg[4];
-      xc.eight(e, x);
-      recall<E, kThreadsCta>(base + kOwn, 0, e, pg);
+      Pair v[4], n[4], p[4];
+      x.eight(e, v);
+      if constexpr (MERGED) {
+        y.eight(e, n);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pg[i] = (h[e * 4 + i] + l1) * f1 * pg[i];
+        for (int i = 0; i < 4; ++i) n[i] = h[e * 4 + i];
+      }
+      recall<E, kThreadsCta>(base + kOwn, 0, e, p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n[i] = (n[i] + l1) * f1 * p[i];
       if (betas) {
-        Pair pb[4];
-        recall<E, kThreadsCta>(base + kOwn, 2, e, pb);
+        recall<E, kThreadsCta>(base + kOwn, 2, e, p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pg[i] = pg[i] + pb[i];
+        for (int i = 0; i < 4; ++i) n[i] = n[i] + p[i];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = as_stored(fma(w, pg[i], a2 * x[i]), a.x_bf16), h[e * 4 + i] = x[i];
-      if (live) RowX::store(out, e, t, cols, x);
+      for (int i = 0; i < 4; ++i) v[i] = as_stored(fma(ws, n[i], a2 * v[i]), a.x_bf16), h[e * 4 + i] = v[i];
+      if (!MERGED && live) RowX::store(to_h, e, t, cols, v);
     }
-    if (a.u != nullptr) {
-      stats(h, &m2, &r2);
-      const Pair l2 = both(-m2), f2 = both(r2);
-      out = static_cast<char*>(a.u) + row * a.ldu * (a.y_bf16 ? 2 : 4);
+    // x and y are used up
+    x = xn, y = yn, w = wn;
+    const float m0 = m1, r0 = r1;
+    if constexpr (MERGED) {
+      // their place takes the row after the next
+      fetch(xn, yn, wn, slot, row + 2 * step);
+      slot ^= 1;
+      cp_async_wait<1>();
+      if (next) x.settle(t, cols), y.settle(t, cols);
+    }
+    float m2 = 0.0f, r2 = 1.0f;
+    if (MERGED && a.post && next && a.u != nullptr) {
+      Pair v[E / 2];
+      whole(y, v);
+      float m[2], r[2];
+      stats(m, r, [&](int k, int i) { return k == 0 ? h[i] : v[i]; });
+      m2 = m[0], r2 = r[0], m1 = m[1], r1 = r[1];
+    } else if (MERGED && a.post && next) {
+      Pair v[E / 2];
+      first_norm(v);
+    } else if (a.u != nullptr) {
+      float m[1], r[1];
+      stats(m, r, [&](int, int i) { return h[i]; });
+      m2 = m[0], r2 = r[0];
+    }
+    if (!live) continue;  // whole teams
+    const Pair l2 = both(-m2), f2 = both(r2);
 #pragma unroll
-      for (int e = 0; e < C; ++e) {
-        Pair g[4];
+    for (int e = 0; e < C; ++e) {
+      Pair v[4], g[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = h[e * 4 + i];
+      if (MERGED) RowX::store(to_h, e, t, cols, v);
+      if (a.u != nullptr) {
         recall<E, kThreadsCta>(base + kOwn, 1, e, g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g[i] = (h[e * 4 + i] + l2) * f2 * g[i];
+        for (int i = 0; i < 4; ++i) g[i] = (v[i] + l2) * f2 * g[i];
         if (betas) {
-          Pair b[4];
-          recall<E, kThreadsCta>(base + kOwn, 3, e, b);
+          recall<E, kThreadsCta>(base + kOwn, 3, e, v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) g[i] = g[i] + b[i];
+          for (int i = 0; i < 4; ++i) g[i] = g[i] + v[i];
         }
-        if (live) RowY::store(out, e, t, cols, g);
+        RowY::store(to_u, e, t, cols, g);
       }
     }
-    if (a.stats != nullptr && t == 0 && live && team.rank == 0) {
-      a.stats[row] = m1, a.stats[a.rows + row] = r1;
+    if (a.stats != nullptr && t == 0 && team.rank == 0) {
+      a.stats[row] = m0, a.stats[a.rows + row] = r0;
       a.stats[2 * a.rows + row] = m2, a.stats[3 * a.rows + row] = r2;
     }
   }
+  team.part();
 }
 
 // Rows of any length: a CTA of 1024 reads its row for each mean, variance and output.
 __global__ void __launch_bounds__(1024, 1) k_join_fwd_long(const JoinFwdArgs a) {
   __shared__ Board<1024, false> board;
-  Team<1024, false> team{&board, 0, 1, 0};
+  Team<1024, false> team(&board);
   const auto sum = [&](float v) {
     float s[1] = {v};
     team.sum(s);
@@ -214,16 +267,29 @@ __global__ void __launch_bounds__(1024, 1) k_join_fwd_long(const JoinFwdArgs a) 
   }
 }
 
-template <int G, int E, bool CL, typename RowX, typename RowY>
-cudaError_t run(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
+template <int G, int E, bool CL, bool MERGED, typename RowX, typename RowY>
+cudaError_t run_as(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
   static LayerGrid grid[2];
   int cap = 0;
-  const void* kernel = reinterpret_cast<const void*>(&k_join_fwd<G, E, CL, RowX, RowY>);
+  const void* kernel = reinterpret_cast<const void*>(&k_join_fwd<G, E, CL, MERGED, RowX, RowY>);
   const bool betas = a.post_beta != nullptr || a.beta != nullptr;
   const size_t smem = ring_bytes<G, E, RowX, RowY>(betas);
   const cudaError_t e = layer_grid(grid[betas], kernel, kTeamCta<G>, smem, ring_bytes<G, E, RowX, RowY>(true), &cap);
   if (e != cudaSuccess) return e;
-  return launch_teams(k_join_fwd<G, E, CL, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeamCta<G> / G, ctas, smem, s, a, pwide);
+  return launch_teams(k_join_fwd<G, E, CL, MERGED, RowX, RowY>, a.rows, cap, kTeamCta<G>, kTeamCta<G> / G, ctas, smem, s, a, pwide);
+}
+// Merged exchanges (us: 16384 x 4096 bf16 layer norms 128 instead of 142, 2048 x 16384 bf16 RMS norms 77 instead of 87), but
+// for RMS norms within a CTA, where they only put off the stores (84 us become 87), and for rows in registers, of which
+// there would be too many (16384 x 4095 fp32 350 instead of 256).
+template <int G, int E, bool CL, typename RowX, typename RowY>
+cudaError_t run(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
+  if constexpr (RowX::kBytes == 0) {
+    return run_as<G, E, CL, false, RowX, RowY>(a, pwide, ctas, s);
+  } else if constexpr (CL) {
+    return run_as<G, E, CL, true, RowX, RowY>(a, pwide, ctas, s);
+  } else {
+    return a.rms ? run_as<G, E, CL, false, RowX, RowY>(a, pwide, ctas, s) : run_as<G, E, CL, true, RowX, RowY>(a, pwide, ctas, s);
+  }
 }
 template <int G, bool CL>
 cudaError_t run_f32(const JoinFwdArgs& a, bool pwide, int ctas, cudaStream_t s) {
@@ -290,6 +356,13 @@ cudaError_t launch_join_forward(const JoinFwdArgs& a, cudaStream_t s) {
   if (a.cols <= 2048) return run_any_f32<256, false>(a, 1, s);
   if (a.cols <= 4096) return run_any_f32<512, false>(a, 1, s);
   return run_any_f32<512, true>(a, ctas, s);
+}
+
+cudaError_t read_join_forward_timeouts(int64_t* count) {
+  unsigned long long v = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(&v, g_join_timeouts, sizeof v);
+  if (e == cudaSuccess) *count = int64_t(v);
+  return e;
 }
 
 }  // namespace loco

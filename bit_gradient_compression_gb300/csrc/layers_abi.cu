@@ -5,6 +5,7 @@
 
 #include "layers_args.h"
 #include "layers_internal.h"
+#include "steps_internal.h"
 
 namespace loco {
 
@@ -321,7 +322,12 @@ loco_status loco_linear_backward_weight(const loco_linear_config* cfg, const voi
 
 loco_status loco_linear_timeouts(int64_t* count) {
   if (count == nullptr) return fail(LOCO_ERR_INVALID_ARG, "count is NULL");
-  return launch_result(read_linear_timeouts(count), "loco_linear_timeouts");
+  int64_t linear = 0, forward = 0, backward = 0;
+  cudaError_t e = read_linear_timeouts(&linear);
+  if (e == cudaSuccess) e = read_join_forward_timeouts(&forward);
+  if (e == cudaSuccess) e = read_join_backward_timeouts(&backward);
+  if (e == cudaSuccess) *count = linear + forward + backward;
+  return launch_result(e, "loco_linear_timeouts");
 }
 
 }  // extern "C"

@@ -210,7 +210,7 @@ __device__ __forceinline__ void choose(const Key* chosen, int n, int top, Key* b
 template <bool BF16, int WPR, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdArgs a) {
   __shared__ Shared<TOP> sh;
-  extern __shared__ __align__(16) uint8_t ring[];
+  extern __shared__ __align__(128) uint8_t ring[];
   constexpr int kElem = BF16 ? 2 : 4, V = kVec<BF16>, kTeam = 32 * WPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, t = threadIdx.x % kTeam;
   int parts = 1, me = 0;

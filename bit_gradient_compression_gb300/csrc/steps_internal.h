@@ -132,6 +132,10 @@ __host__ __device__ inline uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// Waits of a cluster's CTAs for one another that ran out, on the current device.
+cudaError_t read_join_forward_timeouts(int64_t* count);
+cudaError_t read_join_backward_timeouts(int64_t* count);
+
 cudaError_t launch_join_forward(const JoinFwdArgs& a, cudaStream_t s);
 cudaError_t launch_join_backward(const JoinBwdArgs& a, cudaStream_t s);
 cudaError_t launch_logprob_forward(const LogprobFwdArgs& a, cudaStream_t s);

@@ -627,7 +627,8 @@ def loco_linear_backward_weight(dy, dw, *, x=None, codes=None, scales=None, gamm
 
 
 def loco_linear_timeouts() -> int:
-    """Waits that the linear-layer kernels gave up on the current device (0 unless something is wrong); synchronises."""
+    """Waits that the linear-layer and join kernels gave up on the current device (0 unless something is wrong);
+    synchronises."""
     v = ctypes.c_int64()
     _check(lib.loco_linear_timeouts(ctypes.byref(v)))
     return v.value
