@@ -294,7 +294,7 @@ __device__ __forceinline__ void recall(uint32_t at, int which, int e, Pair (&v)[
 // as well: 4096 x 8192 bf16 forward 60 us with one, 2048 x 16384 89 us).
 // An area is written again two exchanges later, by a CTA that has what all warps sent in the exchange between, each
 // after it had read this one.
-constexpr int kMaxCluster = 8, kMaxSums = 5;
+constexpr int kMaxCluster = 8, kMaxSums = 4;  // (means and deviations of two rows)
 constexpr uint64_t kWaitNs = 2000000000;  // longest wait for the cluster
 __device__ unsigned long long g_join_timeouts;  // waits that ran out
 
@@ -374,59 +374,50 @@ struct Team {
       if (test()) return true;
     return false;
   }
-  // Sum of the warps' values `which`, in each lane of a group of LANES.
-  template <int LANES>
+  // Sum of the warps' values `which`, in each lane of a half warp.
   __device__ __forceinline__ float read(int which) const {
     constexpr int kW = G / 32;
-    const int l = threadIdx.x % LANES;
+    const int l = threadIdx.x % 16;
     float v = 0.0f;
     if constexpr (CL) {
-      for (int k = l; k < kW * ctas; k += LANES) v += board->v[turn][which][k];
+      for (int k = l; k < kW * ctas; k += 16) v += board->v[turn][which][k];
       if (lost) v = __uint_as_float(0x7FC00000u);
-    } else if constexpr (kW >= LANES) {
-#pragma unroll
-      for (int k = 0; k < kW; k += LANES) v += board->v[turn][which][l + k];
+    } else if constexpr (kW > 16) {
+      v = board->v[turn][which][l] + board->v[turn][which][l + 16];
     } else {
       v = board->v[turn][which][l % kW];
     }
 #pragma unroll
-    for (int o = (CL || kW > LANES ? LANES : kW) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = CL || kW > 16 ? 8 : kW / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
   }
-  // Sums over the team of N values, the same in all its threads, with one exchange between its warps.  Of two or four
-  // values the halves or quarters of a warp take one each, so that all of them take little more than one does.
+  // Sums over the team of N values, the same in all its threads, with one exchange between its warps.  Of two or three
+  // values the first two take a half of a warp each, so that together they take little more than one does.
   template <int N>
   __device__ __forceinline__ void sum(float (&v)[N]) {
-    static_assert(N >= 1 && N <= kMaxSums, "");
-    constexpr int kGroups = N >= 4 ? 4 : N >= 2 ? 2 : 1, kLanes = 32 / kGroups, kRead = kGroups == 4 ? 8 : 16;
-    const int lane = threadIdx.x & 31, group = lane / kLanes, at = lane % kLanes;
+    static_assert(N >= 1 && N <= 3, "");
+    const int lane = threadIdx.x & 31;
+    const bool upper = N > 1 && lane >= 16;
     float x = v[0];
-    if constexpr (kGroups == 4) {
-      const bool upper = lane & 16, odd = lane & 8;
-      const float p = (upper ? v[2] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[2], 16);
-      const float q = (upper ? v[3] : v[1]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[1] : v[3], 16);
-      x = (odd ? q : p) + __shfl_xor_sync(0xFFFFFFFFu, odd ? p : q, 8);
-    } else if constexpr (kGroups == 2) {
-      const bool upper = lane & 16;
+    if constexpr (N == 1)
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
+    else
       x = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[1], 16);
-    }
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    constexpr bool kOdd = N > kGroups;  // the last value by itself
-    if constexpr (kOdd) v[N - 1] = warp_total(v[N - 1]);
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    if constexpr (N == 3) v[2] = warp_total(v[2]);
     if constexpr (G > 32) {
-      write(group, at, x);
-      if constexpr (kOdd) write(N - 1, lane, v[N - 1]);
+      write(upper, N > 1 ? lane % 16 : lane, x);
+      if constexpr (N == 3) write(2, lane, v[2]);
       meet(N);
-      x = read<kRead>(group);
-      if constexpr (kOdd) v[N - 1] = read<kRead>(N - 1);
+      x = read(upper);
+      if constexpr (N == 3) v[2] = read(2);
       turn ^= 1;
     }
-    if constexpr (kGroups == 1) {
+    if constexpr (N == 1) {
       v[0] = x;
     } else {
-#pragma unroll
-      for (int k = 0; k < kGroups; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, x, k * kLanes);
+      v[0] = __shfl_sync(0xFFFFFFFFu, x, 0), v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
     }
   }
 };
