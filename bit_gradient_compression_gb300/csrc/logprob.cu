@@ -9,12 +9,13 @@
 // Alternatives: every warp keeps its 32 largest so far, one to a lane, in order of keys (value, then lower column;
 // all are different, so the outcome does not depend on the order in which they come).  A value above the warp's
 // threshold `thr` is inserted by a ballot and a shift; thr is the warp's own top-th largest, and where a row has
-// eight warps the least of their each-th largest, each = ceil(top / 8), if that is more.  The first tile's
-// thresholds are the same of the lanes' maxima, of which there cannot be more than of values.  Columns of one warp come in ascending order, so a later value that equals its own threshold loses the tie and `>` is enough;
+// several warps the least of their each-th largest, each = ceil(top / warps), if that is more.  The first tile's
+// thresholds are the same of the lanes' maxima, as there are at least as many values that are not below them.  Columns
+// of one warp come in ascending order, so a later value that equals its own threshold loses the tie and `>` is enough;
 // against a threshold of other warps a value that equals it is kept.
 //
-// A row is read by a warp (short rows), by a CTA of eight, or, where rows are few, by a cluster of up to
-// eight CTAs whose results the first joins through distributed shared memory: one launch, no workspace.
+// A row is read by one, two, four or eight warps, more where rows are fewer, or by a cluster of up to eight
+// CTAs of eight warps whose results the first joins through distributed shared memory: one launch, no workspace.
 // Rows start at any multiple of the element size: the elements before the first 16-byte boundary and
 // after the last whole vector are taken one by one.
 #include <cooperative_groups.h>
@@ -168,26 +169,27 @@ struct Largest {
 };
 
 constexpr int kMaxParts = 8;  // CTAs of a cluster
-template <bool TOP>
+template <bool TOP, int W>
 struct Shared {
-  Part part[kWarps];
+  Part part[W];
   Part ctas[kMaxParts];
 };
-template <>
-struct Shared<true> {
-  Part part[kWarps];
+template <int W>
+struct Shared<true, W> {
+  Part part[W];
   Part ctas[kMaxParts];
   Key lists[kMaxParts * LOCO_MAX_TOP];  // the CTAs' largest
-  Key chosen[kWarps * LOCO_MAX_TOP];  // of all warps' largest, what can be among the row's
+  Key chosen[W * LOCO_MAX_TOP];  // of all warps' largest, what can be among the row's
   Key best[LOCO_MAX_TOP];
   int n_chosen;
-  uint32_t floors[kWarps], least[kWarps];
+  uint32_t floors[W], least[W];
 };
 
-// Eight parts, each held by every eighth lane, put together.
-__device__ __forceinline__ Part join_eight(Part x, int lane, float c) {
+// N parts, each held by every N-th lane, put together.
+template <int N>
+__device__ __forceinline__ Part join_lanes(Part x, int lane, float c) {
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
+  for (int o = N / 2; o > 0; o >>= 1) {
     const Part other{__shfl_xor_sync(0xFFFFFFFFu, x.m, o), __shfl_xor_sync(0xFFFFFFFFu, x.s, o),
                      __shfl_xor_sync(0xFFFFFFFFu, x.d, o)};
     x = lane & o ? join(other, x, c) : join(x, other, c);
@@ -196,8 +198,9 @@ __device__ __forceinline__ Part join_eight(Part x, int lane, float c) {
 }
 
 // The `top` largest of chosen[0, n), in order, by all threads of the CTA; `best` was 0.
+template <int THREADS>
 __device__ __forceinline__ void choose(const Key* chosen, int n, int top, Key* best) {
-  for (int i = threadIdx.x; i < n; i += kThreadsLp) {
+  for (int i = threadIdx.x; i < n; i += THREADS) {
     const Key k = chosen[i];
     int above = 0;
 #pragma unroll 8
@@ -206,10 +209,13 @@ __device__ __forceinline__ void choose(const Key* chosen, int n, int top, Key* b
   }
 }
 
-// WPR: warps of a row's part (1: a CTA takes eight rows, 8: one).  CLUSTER: several CTAs to a row.
+// WPR: warps of a row's part (1: a CTA takes eight rows; 2, 4, 8: one).  CLUSTER: several CTAs to a row.
+template <int WPR>
+constexpr int kFwdWarps = WPR == 1 ? kWarps : WPR;  // of a CTA
 template <bool BF16, int WPR, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdArgs a) {
-  __shared__ Shared<TOP> sh;
+__global__ void __launch_bounds__(32 * kFwdWarps<WPR>, 32 / kFwdWarps<WPR>) k_logprob_fwd(const LogprobFwdArgs a) {
+  constexpr int W = kFwdWarps<WPR>;
+  __shared__ Shared<TOP, W> sh;
   extern __shared__ __align__(128) uint8_t ring[];
   constexpr int kElem = BF16 ? 2 : 4, V = kVec<BF16>, kTeam = 32 * WPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, t = threadIdx.x % kTeam;
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
     me = int(cg::this_cluster().block_rank());
     cg::this_cluster().barrier_arrive();  // waited for before the first CTA's memory is written
   }
-  const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * kWarps + warp : int64_t(blockIdx.x) / parts;
+  const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * W + warp : int64_t(blockIdx.x) / parts;
   if (WPR == 1 && row >= a.rows) return;  // whole warps, and no barrier follows
   const char* z = static_cast<const char*>(a.logits) + row * a.ld * kElem;
   const RowShape<BF16> shape = row_shape<BF16>(z, a.vocab);
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
   // it, so no barrier is needed).
   const uint4 none = BF16 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
                           : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-  constexpr uint32_t kPiece = kThreadsLp * 16, kStage = kVectors * kPiece;
+  constexpr uint32_t kPiece = 32 * W * 16, kStage = kVectors * kPiece;
   const uint32_t base = smem_addr(ring) + threadIdx.x * 16;
   uint32_t slot = 0;
   const auto fetch = [&](int64_t from) {
@@ -298,7 +304,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
     const float2 s = halves(s2), d = halves(d2);
     mine = Part{m, fmaf(f, mine.s, s.x + s.y), fmaf(f, fmaf(mine.s, down, mine.d), d.x + d.y)};
     if constexpr (TOP) {
-      const int each = (a.top + kWarps - 1) / kWarps;
+      const int each = (a.top + WPR - 1) / WPR;
       if (first) {
         const uint32_t u = list.first(tile, lane);
         if (WPR > 1) {
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
         }
       }
       if (__any_sync(0xFFFFFFFFu, tile > list.thr)) {
-        if (WPR > 1) list.hear(sh.floors, kWarps, lane);
+        if (WPR > 1) list.hear(sh.floors, WPR, lane);
 #pragma unroll
         for (int q = 0; q < kVectors; ++q) {
           const uint4 again = shared16(at + q * kPiece);  // (not kept in registers for this)
@@ -345,19 +351,19 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
       if (lane == 0) sh.least[warp] = in_order(list.thr);
     }
     __syncthreads();
-    all = join_eight(sh.part[lane % kWarps], lane, c);
+    all = join_lanes<WPR>(sh.part[lane % WPR], lane, c);
     if constexpr (TOP) {
       // no value below the highest of the warps' thresholds can be among the largest
-      const uint32_t least = __reduce_max_sync(0xFFFFFFFFu, sh.least[lane % kWarps]);
+      const uint32_t least = __reduce_max_sync(0xFFFFFFFFu, sh.least[lane % WPR]);
       if (lane < a.top && uint32_t(list.key >> 32) >= least) sh.chosen[atomicAdd(&sh.n_chosen, 1)] = list.key;
       __syncthreads();
-      choose(sh.chosen, sh.n_chosen, a.top, sh.best);
+      choose<32 * W>(sh.chosen, sh.n_chosen, a.top, sh.best);
     }
     if constexpr (CLUSTER) {
       // everything goes to the first CTA
       const auto cluster = cg::this_cluster();
       cluster.barrier_wait();
-      Shared<TOP>* to = cluster.map_shared_rank(&sh, 0);
+      Shared<TOP, W>* to = cluster.map_shared_rank(&sh, 0);
       if (threadIdx.x == 0) to->ctas[me] = all;
       if constexpr (TOP) {
         __syncthreads();
@@ -365,11 +371,11 @@ __global__ void __launch_bounds__(kThreadsLp, 4) k_logprob_fwd(const LogprobFwdA
       }
       cluster.sync();
       if (me != 0) return;
-      all = join_eight(lane % kMaxParts < parts ? sh.ctas[lane % kMaxParts] : Part{kLowest, 0.0f, 0.0f}, lane, c);
+      all = join_lanes<kMaxParts>(lane % kMaxParts < parts ? sh.ctas[lane % kMaxParts] : Part{kLowest, 0.0f, 0.0f}, lane, c);
       if constexpr (TOP) {
         if (threadIdx.x < LOCO_MAX_TOP) sh.best[threadIdx.x] = 0;
         __syncthreads();
-        choose(sh.lists, parts * a.top, a.top, sh.best);
+        choose<32 * W>(sh.lists, parts * a.top, a.top, sh.best);
       }
     }
     if constexpr (TOP) __syncthreads();
@@ -406,13 +412,14 @@ cudaError_t run_fwd(const LogprobFwdArgs& a, int parts, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   cfg.gridDim = dim3(unsigned(WPR == 1 ? (a.rows + kWarps - 1) / kWarps : a.rows * parts));
-  cfg.blockDim = dim3(kThreadsLp);
-  cfg.dynamicSmemBytes = 2 * kVectors * kThreadsLp * 16;
+  constexpr int kThreads = 32 * kFwdWarps<WPR>;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 2 * kVectors * kThreads * 16;
   cfg.stream = s;
   static LayerGrid grid;  // (asked for the memory that a CTA takes)
   int cap = 0;
-  const cudaError_t e = layer_grid(grid, reinterpret_cast<const void*>(&k_logprob_fwd<BF16, WPR, TOP, CLUSTER>), kThreadsLp,
-                                   cfg.dynamicSmemBytes, cfg.dynamicSmemBytes + sizeof(Shared<TOP>), &cap);
+  const cudaError_t e = layer_grid(grid, reinterpret_cast<const void*>(&k_logprob_fwd<BF16, WPR, TOP, CLUSTER>), kThreads,
+                                   cfg.dynamicSmemBytes, cfg.dynamicSmemBytes + sizeof(Shared<TOP, kFwdWarps<WPR>>), &cap);
   if (e != cudaSuccess) return e;
   if (CLUSTER) {
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -423,13 +430,14 @@ cudaError_t run_fwd(const LogprobFwdArgs& a, int parts, cudaStream_t s) {
 }
 template <bool BF16, bool TOP>
 cudaError_t run_fwd_shape(const LogprobFwdArgs& a, int sms, cudaStream_t s) {
-  // A warp to a row where rows fill the warps: its fixed cost is a fifth of a CTA's, its time for one row five times.
-  // (bf16, five alternatives, us as warps / as CTAs: 152 x 2000 7.4 / 5.9, 600 x 2000 7.8 / 9.0, 1216 x 2000 7.8 / 15.4,
-  // 600 x 16000 20 / 13, 1216 x 16000 20 / 24, 4096 x 32000 67 / 92, 8192 x 32000 112 / 177, 4096 x 131072 204 / 217;
-  // without alternatives 4096 x 131072 173 / 165.)
-  const int64_t bytes = a.vocab * (BF16 ? 2 : 4);
-  const int64_t least = a.vocab <= 1024 ? 0 : a.vocab <= 2048 ? 4 : bytes <= 32768 ? 8 : 16;  // rows to an SM
-  if (bytes <= 131072 && a.rows >= least * sms) return run_fwd<BF16, 1, TOP, false>(a, 1, s);
+  // As few warps to a row as still fill the SMs: a row's beginning and end cost the same for each of its warps.  (us with
+  // one, two, four and eight warps, bf16 and five alternatives: 1216 x 2000 8.1, 7.3, 9.4, 16.3; 8192 x 2000 21, 26, 43, 82;
+  // 600 x 16000 20, 14, 12, 13; 4096 x 16000 44, 43, 52, 66; 600 x 131072 77, 47, 40, 39; 1216 x 131072 80, 66, 65, 70;
+  // 4096 x 131072 203, 187, 194, 212.)
+  const int64_t bytes = a.vocab * (BF16 ? 2 : 4), fill = int64_t(sms) * (bytes <= 4096 ? 8 : bytes <= 32768 ? 16 : 32);
+  if (a.vocab <= 1024 || a.rows >= fill) return run_fwd<BF16, 1, TOP, false>(a, 1, s);
+  if (a.rows * 2 >= fill) return run_fwd<BF16, 2, TOP, false>(a, 1, s);
+  if (a.rows * 4 >= fill) return run_fwd<BF16, 4, TOP, false>(a, 1, s);
   // several CTAs to a row while the grid leaves SMs without work and a part still fills a CTA's threads once
   int parts = 1;
   while (parts < 8 && a.rows * parts * 2 <= 2 * sms && a.vocab >= int64_t(parts) * 2 * kThreadsLp * kVec<BF16>) parts *= 2;
