@@ -10,6 +10,11 @@
 // bytes of x + d + 1.5 * 2^23.
 //
 // Every product and sum is rounded on its own, as in loco_adam_step.
+//
+// With 32-bit states HBM is the bound: 1.1e9 elements with bf16 gradients 4.60 ms, 6.7 TB/s, a copy's rate.  With 8-bit
+// states the arithmetic is, 16 bytes and about 100 instructions an element: 1.41e9 elements, dithered, with bf16 copies 4.7
+// ms, 4.8 TB/s (71 % of a copy's rate, issuing in 74 % of the cycles), and 1.3 ms for decoding both states to bf16, 6.4
+// TB/s.  A block's 561152 elements take 7 us with their decodes on the device, less than the host's part of the calls.
 #include "device_common.cuh"
 #include "layers_common.cuh"
 #include "steps_internal.h"
@@ -67,7 +72,7 @@ __device__ __forceinline__ Pair both(float v) { return pair(v, v); }
 // a - b q is exact, the rounded quotient; likewise g + (v - g^2) h for the root, h of 1 / (2 sqrt(v)).  They hold where
 // nothing is lost to the ends of the exponent's range: see `extreme`.  Every root of [1, 4) and every reciprocal of
 // [1, 2) has been compared with the IEEE operations, and quotients of 2^31 random pairs; so are the steps in the tests.
-// With them a step of 10^8 elements and 8-bit states takes 85 instructions an element instead of 111.
+// With them a step with 8-bit states takes about 100 instructions an element instead of 111.
 __device__ __forceinline__ float rsqrt_approx(float v) {
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));

@@ -18,6 +18,12 @@
 // CTAs of eight warps whose results the first joins through distributed shared memory: one launch, no workspace.
 // Rows start at any multiple of the element size: the elements before the first 16-byte boundary and
 // after the last whole vector are taken one by one.
+//
+// 4096 x 131072 bf16: 157 us, 6.8 TB/s, without alternatives, a copy's rate; 192 us with eight of them, where the SMs issue
+// in 78 % of the cycles, 11.6 instructions an element; candidates are most in a row's first tiles.  8192 x 32000 with
+// five: 111 us, 70 % of a copy's rate.  1 x 32000 with twenty: 8.6 us, a launch, a cluster of eight CTAs and their join.
+//
+// Backward, one read and one write a value: 8192 x 32000 bf16 153 us, 6.9 TB/s, a copy's rate.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"

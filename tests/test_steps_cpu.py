@@ -253,6 +253,30 @@ def test_binding_refuses_what_does_not_fit(L):
         L.loco_adam_tensors(L.make_adam_tensors(**good), L.make_adam(), 1, grad_scale=torch.zeros(2))
 
 
+def test_every_wait_is_bounded():
+    """Read in the source, as no test may make a wait run out on a device: the CTAs that share a row wait for one another
+    only in `arrived`, which ends by the clock; what is read after a wait that ran out is NaN, and nothing is waited for."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_gradient_compression_gb300", "csrc")
+    text = {}
+    for name in ("join_common.cuh", "join_forward.cu", "join_backward.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            text[name] = re.sub(r"//[^\n]*", "", f.read())
+    common = text["join_common.cuh"]
+    assert sum(t.count("try_wait") for t in text.values()) == 1
+    assert "mbar_wait" not in "".join(text.values()) and "for (;;)" not in "".join(text.values())
+    wait = common[common.index("bool arrived("):]
+    wait = wait[:wait.index("float read(")]
+    assert re.search(r"while \(global_ns\(\) - start < kWaitNs\)\s+if \(test\(\)\) return true;\s+return false;", wait)
+    assert re.search(r"kWaitNs = (\d+);", common).group(1) == "2000000000"
+    assert "if (!lost && !arrived(" in common and common.count("arrived(") == 2
+    assert "if (lost) v = __uint_as_float(0x7FC00000u);" in common and "team.lost ? __uint_as_float(0x7FC00000u)" in common
+    # no CTA leaves its cluster before the others are done with its memory
+    for name in ("join_forward.cu", "join_backward.cu"):
+        assert text[name].count("team.part();") == 1
+
+
 def test_dither_bits_are_even_and_independent():
     """Each byte of the hash over neighbouring elements, tensors and steps.  A value between two codes is rounded up with
     the probability that its byte exceeds a threshold, so what counts is the distribution function: it may be off by half
