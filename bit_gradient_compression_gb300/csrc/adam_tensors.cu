@@ -14,7 +14,7 @@
 // With 32-bit states HBM is the bound: 1.1e9 elements with bf16 gradients 4.60 ms, 6.7 TB/s, a copy's rate.  With 8-bit
 // states the arithmetic is, 16 bytes and about 100 instructions an element: 1.41e9 elements, dithered, with bf16 copies 4.7
 // ms, 4.8 TB/s (71 % of a copy's rate, issuing in 74 % of the cycles), and 1.3 ms for decoding both states to bf16, 6.4
-// TB/s.  A block's 561152 elements take 7 us with their decodes on the device, less than the host's part of the calls.
+// TB/s.  A block's 353712 elements take 7 us with their decodes on the device, less than the host's part of the calls.
 #include "device_common.cuh"
 #include "layers_common.cuh"
 #include "steps_internal.h"

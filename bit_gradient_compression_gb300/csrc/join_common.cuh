@@ -70,6 +70,7 @@ __device__ __forceinline__ void store_part(char* q, uint4 w, uint32_t from, uint
 // warp's run is stored in smaller pieces.
 template <int G, int E, bool BF16, bool ANY>
 struct Vec {
+  static constexpr int kReachBack = 8, kReach = 24;  // elements (see `load`)
   static constexpr int kRun = 256, kRunApart = G * 8;  // a warp's columns: runs, and how far they are apart
   static constexpr int kElem = BF16 ? 2 : 4, kWhole = BF16 ? 1 : 2;  // pieces of a vector
   static constexpr uint32_t kApart = kTeamCta<G> * 16;               // of a thread's pieces
@@ -93,10 +94,13 @@ struct Vec {
       const int c0 = (t + G * e) * 8;
       if (c0 >= cols + (ANY ? 8 : 0)) continue;  // (with ANY, the lane behind the last has that one's end in its piece)
       const char* v = q + c0 * kElem;
-      // Behind a row's end the matrix goes on, with what lies between its rows or with the next row: only the pieces of
-      // the first vector of the first row and of the last vectors of the last one may reach out of it.
-      const bool in = !((off != 0 && row == 0 && edges.first && c0 == 0) ||
-                        (row == edges.last_row && c0 + 8 + (off != 0 ? 16 / kElem : 0) > edges.rest));
+      // Behind a row's end the matrix goes on, with what lies between its rows or with the next rows: only the pieces of
+      // the first vector of the first rows and of the last vectors of the last ones may reach out of it.  A piece begins
+      // less than eight columns before its vector and ends less than 24 behind the row's end: that is the first row and
+      // the last where the rows are so far apart, and as many as make up so many elements where they are not.
+      const uint32_t head = !ANY || ld >= kReachBack ? 1 : kReachBack, tail = !ANY || ld >= kReach ? 1 : kReach;
+      const bool in = !((off != 0 && row < head && edges.first && c0 == 0) ||
+                        (edges.last_row - row < tail && c0 + 8 + (off != 0 ? 16 / kElem : 0) > edges.rest));
       if (in) {
 #pragma unroll
         for (int k = 0; k < kWhole; ++k)
@@ -202,8 +206,8 @@ struct Vec {
 };
 
 // Single columns t, t + G, ... of rows that lie anywhere, in registers.  For 32-bit rows in the forward pass, where the
-// shifting of Vec costs more than four times as many loads do (16384 x 4095 with bf16 y, layer norms: 233 us here, 385
-// there; with bf16 rows 232 against 179).
+// shifting of Vec costs more than four times as many loads do (16384 x 4095 with bf16 y, layer norms: 255 us here, 385
+// there; with bf16 rows 232 against 184).
 template <int G, int E, bool BF16>
 struct Cols {
   static constexpr int kRun = 32, kRunApart = G;

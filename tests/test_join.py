@@ -302,6 +302,34 @@ def test_results_do_not_change_and_graphs_replay(L):
     assert all(torch.equal(a, b) for a, b in zip(replayed, (h, u, stats, dx, dy, dr, *v.values())))
 
 
+@pytest.mark.parametrize("cols,ld", [(1, 1), (2, 2), (3, 3), (5, 5), (3, 4), (9, 9), (23, 23), (25, 25)])
+@pytest.mark.parametrize("xd,yd", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+@pytest.mark.parametrize("rows", [1, 7, 300])
+def test_narrow_rows_without_gaps(L, cols, ld, xd, yd, rows):
+    """Matrices narrower than a piece, packed, from an odd element of a buffer to its last one: every value arrives and
+    leaves at its place.  Without norms an output is two products and a sum, each off by half a step."""
+    g = gen(19)
+    cfg, a, s = cfg_of(L, "layer", False, 0.75, -0.5), 0.75, -0.5
+
+    def place(dtype, v):
+        t = torch.empty(1 + (rows - 1) * ld + cols, dtype=dtype, device="cuda").as_strided((rows, cols), (ld, 1), 1)
+        return t.copy_(v)
+    x, dh = (place(xd, rand(g, rows, cols, xd)) for _ in range(2))
+    y = place(yd, rand(g, rows, cols, yd))
+    h, dx, dy = place(xd, torch.zeros_like(x)), place(xd, torch.zeros_like(x)), place(yd, torch.zeros_like(y))
+    L.loco_join_forward(cfg, x, y, h)
+    want = a * x.double() + s * y.double()
+    R.close(h, want, 3 * U * (a * x.double().abs() + 0.5 * y.double().abs()) + S.out_tol(want, xd), "h")
+    dgate = torch.empty(cols, device="cuda")
+    ws = torch.empty(L.loco_join_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    L.loco_join_backward(cfg, dh, None, None, y, None, dx, dy, dgate=dgate, workspace=ws)
+    d = dh.double()
+    R.close(dx, a * d, 2 * U * d.abs() + S.out_tol(a * d, xd), "dx")
+    R.close(dy, s * d, 2 * U * d.abs() + S.out_tol(s * d, yd), "dy")
+    terms = (d * y.double()).abs().sum(0)
+    R.close(dgate, s * (d * y.double()).sum(0), (rows + 4) * U * terms, "dgate")
+
+
 def test_empty_batch(L):
     cfg = cfg_of(L, "layer", True)
     e = torch.empty(0, 40, device="cuda")

@@ -253,6 +253,42 @@ def test_binding_refuses_what_does_not_fit(L):
         L.loco_adam_tensors(L.make_adam_tensors(**good), L.make_adam(), 1, grad_scale=torch.zeros(2))
 
 
+def test_pieces_stay_inside_the_matrix():
+    """The join kernels copy rows that lie anywhere as the aligned 16-byte pieces they lie in.  Every piece that is copied
+    whole lies inside the matrix, by the rule that the source states, for narrow matrices at every alignment."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_gradient_compression_gb300", "csrc",
+                        "join_common.cuh")
+    with open(path) as f:
+        text = re.sub(r"\s+", " ", f.read())
+    back, reach = map(int, re.search(r"kReachBack = (\d+), kReach = (\d+);", text).groups())
+    assert "head = !ANY || ld >= kReachBack ? 1 : kReachBack, tail = !ANY || ld >= kReach ? 1 : kReach;" in text
+    assert ("!((off != 0 && row < head && edges.first && c0 == 0) || "
+            "(edges.last_row - row < tail && c0 + 8 + (off != 0 ? 16 / kElem : 0) > edges.rest));") in text
+    for elem in (2, 4):
+        whole = 8 * elem // 16
+        for cols in [*range(1, 30), 250, 257]:
+            for ld in (cols, cols + 1, cols + 7):
+                for rows in (1, 2, 3, 9, 40):
+                    for base in range(0, 16, elem):
+                        end = base + ((rows - 1) * ld + cols) * elem
+                        for row in range(rows):
+                            start = base + row * ld * elem
+                            off = start % 16
+                            for c0 in range(0, cols + 8, 8):
+                                head, tail = 1 if ld >= back else back, 1 if ld >= reach else reach
+                                if (off and row < head and c0 == 0) or (
+                                        rows - 1 - row < tail and c0 + 8 + (16 // elem if off else 0) > cols):
+                                    continue  # element by element
+                                pieces = [k for k in range(whole) if k == 0 or c0 < cols]
+                                if off and c0 < cols:
+                                    pieces.append(whole)  # a warp's last lane's
+                                for k in pieces:
+                                    at = start + c0 * elem - off + 16 * k
+                                    assert base <= at and at + 16 <= end, (elem, cols, ld, rows, base, row, c0, k)
+
+
 def test_every_wait_is_bounded():
     """Read in the source, as no test may make a wait run out on a device: the CTAs that share a row wait for one another
     only in `arrived`, which ends by the clock; what is read after a wait that ran out is NaN, and nothing is waited for."""

@@ -59,6 +59,29 @@ def test_logits_behind_two_billion(L, rows, vocab, ld):
     assert bool(((z[last].double() - exact).abs() <= 40 * 4 * U * p + 2.0 ** -8 * exact.abs() + 1e-30).all())
 
 
+def test_longest_row(L):
+    """A row of LOCO_MAX_DIM logits, 0 but for three: its log sum in closed form, and alternatives from both of its ends."""
+    vocab = (1 << 31) - 1
+    z = torch.zeros(1, vocab, dtype=BF16, device="cuda")
+    z[0, 0], z[0, vocab - 1], z[0, vocab // 2] = 1.0, 2.0, -float("inf")
+    y = torch.tensor([vocab - 1], device="cuda")
+    logp, lse, h = (torch.empty(1, device="cuda") for _ in range(3))
+    ids, alts = torch.empty(1, 3, dtype=torch.int64, device="cuda"), torch.empty(1, 3, device="cuda")
+    L.loco_logprob_forward(z, y, logp, lse=lse, entropy=h, top_ids=ids, top_logp=alts)
+    e = torch.tensor([1.0, 2.0], dtype=torch.float64).exp()
+    total = (vocab - 3) + float(e.sum())
+    want = float(torch.log(torch.tensor(total, dtype=torch.float64)))
+    entropy = want - float((e * torch.tensor([1.0, 2.0], dtype=torch.float64)).sum()) / total
+    # eight CTAs of 256 threads: 16 terms of a tile two at a time, 2^31 / 65536 tiles, 13 joins; then 4 u of the log sum
+    tol = (32768 + 32 + 13) * U + 8 * U * want
+    assert abs(float(lse) - want) <= tol and abs(float(logp) - (2.0 - want)) <= tol and abs(float(h) - entropy) <= 4 * tol
+    assert ids.tolist() == [[vocab - 1, 0, 1]]
+    L.loco_logprob_backward(z, y, lse, z, dlogp=torch.ones(1, device="cuda"))
+    assert abs(float(z[0, vocab - 1]) - 1.0) <= 2.0 ** -8 and float(z[0, vocab // 2]) == 0.0
+    p = torch.tensor(-1.0 / total)
+    assert abs(float(z[0, 12345]) - float(p)) <= (2.0 ** -8 + tol) * abs(float(p))
+
+
 def test_streams_behind_two_billion(L):
     """The last rows of a join of 2.2e9 elements are those of the same rows alone, forward and backward."""
     rows, cols, few = 530000, 4096, 3
