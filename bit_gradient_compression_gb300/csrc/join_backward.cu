@@ -14,7 +14,7 @@
 // 16384 x 4096 bf16 with RMS norms takes 155 us, 5.2 TB/s, 77 % of a copy's rate: with the sums over rows in registers two
 // CTAs of 256 threads fit an SM (24 % of its warps), which issue in 43 % of the cycles and wait for one another at the two
 // sums of each row.  (Merging those of a row with the next one's, as the forward pass does, takes 16 registers more and
-// 171 us.)  Layer norms with betas 228 us; 2048 x 16384 202 us; 16384 x 4095 369 us; 500 x 2048 fp32 16 us, of which the
+// 171 us.)  Layer norms with betas 228 us; 2048 x 16384 202 us; 16384 x 4095 313 us; 500 x 2048 fp32 16 us, of which the
 // second kernel is a third.
 #include "join_common.cuh"
 
@@ -31,7 +31,7 @@ constexpr size_t kRing = size_t(kStages) * 2 * (RowX::kBytes + RowY::kBytes) + s
 // RMS: no mean is taken, and the reciprocal roots stay out of the products.  (It changes how dx and dy round, SUMS does
 // not: they do not depend on which parameters' gradients are asked for.)
 template <int G, int E, bool CL, int SUMS, bool RMS, typename RowX, typename RowY>
-__global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G == 32) ? 256 : 512) / kTeamCta<G>)
+__global__ void __launch_bounds__(kTeamCta<G>, (E == 16 && SUMS == 4 && (CL || G == 32 || RowX::kAny) ? 256 : 512) / kTeamCta<G>)
     k_join_bwd(const JoinBwdArgs args, bool pwide) {
   __shared__ Board<G, CL> board;
   constexpr int kTeams = kTeamCta<G> / G, kThreadsCta = kTeamCta<G>, P = E / 2, C = E / 8;
@@ -459,6 +459,12 @@ cudaError_t run_any(const JoinBwdArgs& a, bool pwide, int ctas, int* partials, c
   return a.y_bf16 ? run<G, E, CL, 4, false, Vec<G, E, false, true>, Vec<G, E, true, true>>(a, pwide, ctas, partials, s)
                   : run<G, E, CL, 4, false, Vec<G, E, false, true>, Vec<G, E, false, true>>(a, pwide, ctas, partials, s);
 }
+template <int G, bool CL>
+cudaError_t run_any_rms(const JoinBwdArgs& a, bool pwide, int ctas, int sums, int* partials, cudaStream_t s) {
+  using Row = Vec<G, 16, true, true>;
+  return sums == 4 ? run<G, 16, CL, 4, true, Row, Row>(a, pwide, ctas, partials, s)
+                   : run<G, 16, CL, 2, true, Row, Row>(a, pwide, ctas, partials, s);
+}
 cudaError_t run_long(const JoinBwdArgs& a, int* partials, cudaStream_t s) {
   static LayerGrid grid;
   int cap = 0;
@@ -477,10 +483,11 @@ cudaError_t rows_kernel(const JoinBwdArgs& a, int* sums, int* partials, cudaStre
                     !(a.x_bf16 && !a.y_bf16);
   const bool pwide = on16(a.post_gamma) && on16(a.post_beta) && on16(a.gate) && on16(a.gamma);
   const int ctas = int((a.cols + 4095) / 4096);
+  const bool needs_betas = a.dbeta != nullptr || a.dpost_beta != nullptr || (a.dgate != nullptr && a.post_beta != nullptr);
   *sums = 4;
   if (ctas > kMaxCluster) return run_long(a, partials, s);
   if (wide) {
-    if (a.rms && a.dbeta == nullptr && a.dpost_beta == nullptr && (a.dgate == nullptr || a.post_beta == nullptr)) *sums = 2;
+    if (a.rms && !needs_betas) *sums = 2;
     if (a.x_bf16) {
       if (a.cols <= 256) return run_bf16<32, 8, false>(a, pwide, 1, *sums, partials, s);
       if (a.cols <= 512) return run_bf16<32, 16, false>(a, pwide, 1, *sums, partials, s);
@@ -494,6 +501,14 @@ cudaError_t rows_kernel(const JoinBwdArgs& a, int* sums, int* partials, cudaStre
     if (a.cols <= 2048) return run_f32<256, false>(a, pwide, 1, *sums, partials, s);
     if (a.cols <= 4096) return run_f32<512, false>(a, pwide, 1, *sums, partials, s);
     return run_f32<512, true>(a, pwide, ctas, *sums, partials, s);
+  }
+  // RMS norms of bf16 rows that lie anywhere: as of aligned ones (16384 x 4095 314 us, 378 with eight columns a thread and
+  // four sums; four sums and sixteen columns take one CTA's registers)
+  if (a.x_bf16 && a.y_bf16 && a.rms && a.cols > 1024) {
+    if (!needs_betas) *sums = 2;
+    if (a.cols <= 2048) return run_any_rms<128, false>(a, pwide, 1, *sums, partials, s);
+    if (a.cols <= 4096) return run_any_rms<256, false>(a, pwide, 1, *sums, partials, s);
+    return run_any_rms<256, true>(a, pwide, ctas, *sums, partials, s);
   }
   if (a.cols <= 256) return run_any<32, 8, false>(a, pwide, 1, partials, s);
   if (a.cols <= 1024) return run_any<128, 8, false>(a, pwide, 1, partials, s);

@@ -70,6 +70,7 @@ __device__ __forceinline__ void store_part(char* q, uint4 w, uint32_t from, uint
 // warp's run is stored in smaller pieces.
 template <int G, int E, bool BF16, bool ANY>
 struct Vec {
+  static constexpr bool kAny = ANY;
   static constexpr int kReachBack = 8, kReach = 24;  // elements (see `load`)
   static constexpr int kRun = 256, kRunApart = G * 8;  // a warp's columns: runs, and how far they are apart
   static constexpr int kElem = BF16 ? 2 : 4, kWhole = BF16 ? 1 : 2;  // pieces of a vector

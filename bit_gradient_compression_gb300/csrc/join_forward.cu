@@ -11,7 +11,7 @@
 // Bound by HBM where rows are bf16 and aligned: 16384 x 4096 with RMS norms 84 us, 6.4 TB/s, 94 % of a copy's rate (as
 // many bytes in flight matter as registers allow, so a thread has sixteen columns, three CTAs an SM); with layer norms
 // and betas 128 us, whose parameters leave shared memory for two CTAs.  Wider rows wait for the cluster (2048 x 16384
-// 76 us of 40), unaligned ones are shifted (16384 x 4095 183 us).  One row of 4096 takes 3.6 us, the launch and three
+// 76 us of 40), unaligned ones are shifted (16384 x 4095 184 us).  One row of 4096 takes 3.6 us, the launch and three
 // trips to memory.
 #include "join_common.cuh"
 
