@@ -11,7 +11,7 @@
 // partial row per CTA goes to the workspace and a second kernel adds the partial rows in order: no
 // atomics, the same result every run.
 //
-// 16384 x 4096 bf16 with RMS norms takes 155 us, 5.2 TB/s, 77 % of a copy's rate: with the sums over rows in registers two
+// 16384 x 4096 bf16 with RMS norms takes 153 us, 5.3 TB/s, 78 % of a copy's rate: with the sums over rows in registers two
 // CTAs of 256 threads fit an SM (24 % of its warps), which issue in 43 % of the cycles and wait for one another at the two
 // sums of each row.  (Merging those of a row with the next one's, as the forward pass does, takes 16 registers more and
 // 171 us.)  Layer norms with betas 228 us; 2048 x 16384 202 us; 16384 x 4095 313 us; 500 x 2048 fp32 16 us, of which the
@@ -367,10 +367,11 @@ __global__ void __launch_bounds__(1024, 1) k_join_bwd_long(const JoinBwdArgs a) 
 }
 
 // Adds the partial rows of 32 columns, of two sums at a time: those behind the block (y) or those of the next norm.
-// A warp takes every sixteenth partial row of one of the two, sixteen rows' loads under way at a time; the sixteen are
-// joined in order.
-__global__ void __launch_bounds__(1024) k_join_bwd_params(const JoinBwdArgs a, int partials, int sums) {
-  constexpr int kGroups = 16;
+// A warp takes every eighth partial row of one of the two, sixteen rows' loads under way at a time; the eight are
+// joined in order.  (512 threads: 16384 x 4096 153 us with the rows, 64 x 4096 10.5; 1024, which fill an SM's registers,
+// 155 and 13.1; 256, 161 and 12.0.)
+__global__ void __launch_bounds__(512) k_join_bwd_params(const JoinBwdArgs a, int partials, int sums) {
+  constexpr int kGroups = 8;
   __shared__ float part[kGroups][2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = warp % 2, group = warp / 2, next = blockIdx.y;
   const int64_t c = int64_t(blockIdx.x) * 32 + lane;
@@ -529,7 +530,7 @@ cudaError_t launch_join_backward(const JoinBwdArgs& a, cudaStream_t s) {
     return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
-  cfg.gridDim = dim3(unsigned((a.cols + 31) / 32), 2), cfg.blockDim = dim3(1024), cfg.stream = s;
+  cfg.gridDim = dim3(unsigned((a.cols + 31) / 32), 2), cfg.blockDim = dim3(512), cfg.stream = s;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr, cfg.numAttrs = a.rows > 0 ? 1 : 0;
