@@ -452,15 +452,37 @@ cudaError_t run_fwd_shape(const LogprobFwdArgs& a, int sms, cudaStream_t s) {
 
 // ---------------------------------------------------------------------------------------- backward
 
-// dlogits_j = p_j (A + B t_j) (+ C at the given token), t_j = (z_j - lse) log2(e), p_j = 2^t_j.
+// dlogits_j = p_j (A + B t_j) (+ C at the given token), t_j = (z_j scale - lse) log2(e), p_j = 2^t_j.  The difference is
+// rounded once, before it is taken to base 2: two products would each be rounded at the size of the logits.
 struct Slope {
-  float c, lse2, a, b, at;
+  float scale, lse, a, b, at;
   int64_t target;  // -1: none
-  bool zero;
 };
 __device__ __forceinline__ float slope_at(float z, const Slope& k) {
-  const float t = max_nan(fmaf(z, k.c, -k.lse2), kLeast);
+  const float t = max_nan(fmaf(z, k.scale, -k.lse) * kLog2E, kLeast);
   return exp2_f(t) * fmaf(k.b, t, k.a);
+}
+
+// 24 bits hold a log sum to 2^-24 of itself, by which p is off: 2^-14 here.  Rows farther from 0 (masked by -1e9 or by the
+// type's lowest value from end to end, so that lse is that value however many tokens share the probability) and those
+// whose log sum is infinite are summed anew, and p taken in deviations from the row's maximum.
+constexpr float kFar = 1024.0f;
+
+// Maximum or sum over a row's team, the same in all its threads.
+template <int WPR, typename Op>
+__device__ __forceinline__ float across(float v, const Op& op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if constexpr (WPR > 1) {
+    __shared__ float part[WPR];
+    __syncthreads();  // (an earlier one's are read)
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) v = op(v, part[w]);
+  }
+  return v;
 }
 
 template <bool BF16>
@@ -482,17 +504,48 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_bwd(const LogprobBwdArgs
   const float d = a.dlogp != nullptr && y >= 0 ? (y < a.vocab ? __ldg(a.dlogp + row) : __uint_as_float(0x7FC00000u)) : 0.0f;
   const float dh = a.dentropy != nullptr ? __ldg(a.dentropy + row) : 0.0f;
   const float h = a.dentropy != nullptr ? __ldg(a.entropy + row) : 0.0f;
-  const bool zero = lse == -INFINITY;
   Slope k;
-  k.c = a.scale * kLog2E, k.lse2 = lse * kLog2E;
+  k.scale = a.scale, k.lse = lse;
   k.a = -a.scale * fmaf(dh, h, d), k.b = -a.scale * dh * kLn2, k.at = a.scale * d;
-  if (zero) k.lse2 = 0.0f, k.c = 0.0f, k.a = k.b = 0.0f;
-  const int64_t target = y >= 0 && y < a.vocab && !zero ? y : -1;
-  // (an empty row's logits are all -inf: times a zero c they would be NaN)
+  k.target = y < a.vocab ? y : -1;
   const auto value = [&](float v, int64_t col) {
-    const float g = zero ? 0.0f : slope_at(v, k);
-    return col == target ? g + k.at : g;
+    const float g = slope_at(v, k);
+    return col == k.target ? g + k.at : g;
   };
+  // columns lo to hi - 1, neighbouring lanes taking neighbouring ones: f(eight values, their first column)
+  const auto each = [&](int64_t lo, int64_t hi, const auto& f) {
+    for (int64_t i = lo + t; i < hi; i += 8 * kTeam) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = i + q * kTeam < hi ? load_elem_rw(z, i + q * kTeam, BF16) : -INFINITY;
+      f(v, i);
+    }
+  };
+  if (fabsf(lse) > kFar) {
+    // one CTA (or warp) has the row: what it reads twice, nobody else may have overwritten
+    if (me != 0) return;
+    float m = -INFINITY, s = 0.0f;
+    each(0, a.vocab, [&](const float (&v)[8], int64_t) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = max_nan(m, v[q]);
+    });
+    m = across<WPR>(m, [](float u, float v) { return max_nan(u, v); });
+    const bool none = m == -INFINITY;  // nothing is left
+    if (!none) {
+      const float c = a.scale * kLog2E;
+      each(0, a.vocab, [&](const float (&v)[8], int64_t) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += exp2_f(max_nan((v[q] - m) * c, kLeast));
+      });
+      k.lse = logf(across<WPR>(s, [](float u, float v) { return u + v; }));
+    }
+    each(0, a.vocab, [&](const float (&v)[8], int64_t i) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (i + q * kTeam < a.vocab) store_one<BF16>(o, i + q * kTeam, none ? 0.0f : value(v[q] - m, i + q * kTeam));
+    });
+    return;
+  }
   const RowShape<BF16> shape = row_shape<BF16>(z, a.vocab);
   if ((reinterpret_cast<uintptr_t>(z) & 15) == (reinterpret_cast<uintptr_t>(o) & 15)) {
     const int64_t v_lo = shape.vectors * me / parts, v_hi = shape.vectors * (me + 1) / parts;
@@ -528,15 +581,12 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_bwd(const LogprobBwdArgs
     }
   } else {
     // rows of logits and gradient start at different places within 16 bytes: neighbouring lanes take neighbouring elements
-    const int64_t lo = a.vocab * me / parts, hi = a.vocab * (me + 1) / parts;
-    for (int64_t i = lo + t; i < hi; i += 8 * kTeam) {
-      float v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = i + q * kTeam < hi ? load_elem_rw(z, i + q * kTeam, BF16) : 0.0f;
+    const int64_t hi = a.vocab * (me + 1) / parts;
+    each(a.vocab * me / parts, hi, [&](const float (&v)[8], int64_t i) {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         if (i + q * kTeam < hi) store_one<BF16>(o, i + q * kTeam, value(v[q], i + q * kTeam));
-    }
+    });
   }
 }
 
