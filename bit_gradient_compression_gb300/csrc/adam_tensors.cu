@@ -95,12 +95,13 @@ __device__ __forceinline__ Pair div_pair(Pair a, Pair b) {
 }
 // Whether one of m, v and the denominator is neither zero nor far enough from the ends of the exponent's range for
 // sqrt_pair (of v > 0) and div_pair: the last place of a remainder, 2^-47 of v or of m, must not be below 2^-149, nor
-// a quotient's exponent out of range.  (NaN counts as ordinary: it stays NaN.)
+// a quotient's exponent out of range.  sqrt_pair of an infinite v is NaN, and so is its denominator: what is not a number
+// within the range counts as extreme.
 constexpr float kSmall = 8.67361738e-19f, kLarge = 1.15292150e18f;  // 2^-60, 2^60
 constexpr float kSmallSquare = 7.88860905e-31f;                     // 2^-100
 __device__ __forceinline__ bool extreme(float m, float v, float den) {
-  return (fabsf(m) < kSmall && m != 0.0f) || fabsf(m) > kLarge || (v < kSmallSquare && v != 0.0f) || den < kSmall ||
-         den > kLarge;
+  return (fabsf(m) < kSmall && m != 0.0f) || fabsf(m) > kLarge || (v < kSmallSquare && v != 0.0f) ||
+         !(den >= kSmall && den <= kLarge);
 }
 
 // d = (b - 127.5) / 256 of byte 0 or 1 of the random bits, exact: the byte under the exponent of 2^7, where it counts
