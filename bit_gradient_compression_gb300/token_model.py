@@ -66,7 +66,6 @@ class TokenModel:
             list(self.master.values()), list(self.grad.values()), codes(torch.int8), codes(torch.uint8), m_steps=steps(),
             v_steps=steps(), params_bf16=list(self.param.values()),
             decay_scales=[float(v.dim() == 2) for v in self.master.values()], dither=dither)
-        self.workspace = torch.empty(0, dtype=torch.uint8, device=dev)
         self.t = 0
 
     def logits(self, x: torch.Tensor):
@@ -106,9 +105,9 @@ class TokenModel:
         its tensor in self.grad.  The logits in `kept` are overwritten."""
         T, dev, p, g = dlogp.shape[0], dlogp.device, self.param, self.grad
         new = lambda *shape: torch.empty(shape, dtype=BF16, device=dev)  # noqa: E731
-        need = max(L.loco_join_workspace_bytes(T, self.H), L.loco_norm_workspace_bytes(T, self.H))
-        if self.workspace.numel() < need:
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        # of this pass, like its other buffers: a captured one writes to it as long as its graph lives
+        workspace = torch.empty(max(L.loco_join_workspace_bytes(T, self.H), L.loco_norm_workspace_bytes(T, self.H)),
+                                dtype=torch.uint8, device=dev)
         dz = kept["logits"]
         L.loco_logprob_backward(dz, kept["targets"], kept["lse"], dz, dlogp=dlogp, entropy=kept["entropy"], dentropy=dentropy)
         du, dh = new(T, self.H), None
@@ -120,7 +119,7 @@ class TokenModel:
             L.loco_join_backward(self.join, dh, du, b["h"], b["y"], b["stats"], dx, dy, gamma=p[f"gamma.{i}"],
                                  post_gamma=p[f"post_gamma.{i}"], post_beta=p.get(f"post_beta.{i}"), gate=p[f"gate.{i}"],
                                  dgamma=g[f"gamma.{i}"], dbeta=g.get(f"beta.{i}"), dpost_gamma=g[f"post_gamma.{i}"],
-                                 dpost_beta=g.get(f"post_beta.{i}"), dgate=g[f"gate.{i}"], workspace=self.workspace)
+                                 dpost_beta=g.get(f"post_beta.{i}"), dgate=g[f"gate.{i}"], workspace=workspace)
             L.loco_ckpt_decode(b["codes"], b["scales"], a, act=self.act)
             L.loco_linear_backward_weight(dy, g[f"w2.{i}"], x=a)
             L.loco_linear_backward_input(dy, p[f"w2.{i}"], da, act=self.act, codes=b["codes"], scales=b["scales"])
@@ -129,7 +128,7 @@ class TokenModel:
             dh = dx
         dx = new(T, self.H)
         L.loco_norm_backward(self.norm, du, p["gamma0"], kept["rstd"], dx, x=kept["x"], mean=kept["mean"], residual=dh,
-                             dgamma=g["gamma0"], dbeta=g.get("beta0"), workspace=self.workspace)
+                             dgamma=g["gamma0"], dbeta=g.get("beta0"), workspace=workspace)
         return dx
 
     def step(self, hp, grad_scale: torch.Tensor | None = None):
