@@ -53,8 +53,6 @@ class MlpBlock:
         self.cfg = L.make_config(bits=bits, block=block, beta=0.9, err_scale_mult=4.0, reset_period=512)
         self.codes = torch.empty(L.loco_code_bytes(self.n, bits, block), dtype=torch.uint8, device=dev)
         self.scales = torch.empty(L.loco_num_blocks(self.n, block), device=dev)
-        self.ws_linear = torch.empty(L.loco_linear_workspace_bytes(ffn), dtype=torch.uint8, device=dev)
-        self.ws_norm = torch.empty(0, dtype=torch.uint8, device=dev)
         self.t = 0
 
     def view(self, bucket: torch.Tensor, name: str) -> torch.Tensor:
@@ -86,19 +84,19 @@ class MlpBlock:
         g = lambda name: self.view(self.grad, name)  # noqa: E731
         h, dz = (torch.empty(T, F, dtype=torch.bfloat16, device=dev) for _ in range(2))
         dy, dx = (torch.empty(T, H, dtype=torch.bfloat16, device=dev) for _ in range(2))
-        need = L.loco_norm_workspace_bytes(T, H)
-        if self.ws_norm.numel() < need:
-            self.ws_norm = torch.empty(need, dtype=torch.uint8, device=dev)
+        # of this pass, like its other buffers: a captured one writes to it as long as its graph lives
+        workspace = torch.empty(max(L.loco_norm_workspace_bytes(T, H), L.loco_linear_workspace_bytes(F)),
+                                dtype=torch.uint8, device=dev)
         codes, scales = kept["pre"]
         L.loco_ckpt_decode(codes, scales, h, act=self.act)
         L.loco_linear_backward_weight(dout, g("w2"), x=h, db=g("b2"))
         L.loco_linear_backward_input(dout, p("w2"), dz, act=self.act, codes=codes, scales=scales)
         codes, scales = kept["norm"]
         L.loco_linear_backward_weight(dz, g("w1"), codes=codes, scales=scales, gamma=p("gamma"), beta=p("beta"),
-                                      db=g("b1"), workspace=self.ws_linear)
+                                      db=g("b1"), workspace=workspace)
         L.loco_linear_backward_input(dz, p("w1"), dy)
         L.loco_norm_backward(self.norm, dy, p("gamma"), kept["rstd"], dx, codes=codes, scales=scales, residual=dout,
-                             dgamma=g("gamma"), dbeta=g("beta"), workspace=self.ws_norm)
+                             dgamma=g("gamma"), dbeta=g("beta"), workspace=workspace)
         return dx
 
     def compress(self):

@@ -23,7 +23,7 @@ def make(kind, device):
     return M.L, model, run
 
 
-@pytest.mark.parametrize("kind", ["token"])
+@pytest.mark.parametrize("kind", ["token", "mlp"])
 def test_every_pass_has_its_own(monkeypatch, kind):
     """On the CPU, with the calls themselves left out: the workspaces that two passes hand over share no memory."""
     from bit_gradient_compression_gb300 import build
@@ -46,7 +46,7 @@ def test_every_pass_has_its_own(monkeypatch, kind):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", ["token"])
+@pytest.mark.parametrize("kind", ["token", "mlp"])
 def test_captured_before_a_larger_batch(kind):
     """A graph captured at few rows, then a pass at more, then replays: the gradients of few rows, and memory that was
     handed out in between is as it was."""
