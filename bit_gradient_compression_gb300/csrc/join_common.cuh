@@ -87,7 +87,9 @@ struct Vec {
     return last ? at - threadIdx.x * 16 + e * kVector + kWhole * kApart + threadIdx.x / 32 * 16 : at + e * kVector + 16;
   }
 
+  // (all lanes of a warp)
   __device__ __forceinline__ void load(const void* p, uint32_t row, int64_t ld, int t, int cols, const Edges& edges) {
+    if (ANY) __syncwarp();  // the next lane, into whose first piece this one may write, is done with what was there
     const char* q = static_cast<const char*>(p) + row * ld * kElem;
     off = ANY ? uint32_t(reinterpret_cast<uintptr_t>(q)) & 15u : 0u;
 #pragma unroll
