@@ -303,6 +303,7 @@ __device__ __forceinline__ void recall(uint32_t at, int which, int e, Pair (&v)[
 // after it had read this one.
 constexpr int kMaxCluster = 8, kMaxSums = 4;  // (means and deviations of two rows)
 constexpr uint64_t kWaitNs = 2000000000;  // longest wait for the cluster
+constexpr uint64_t kLandNs = 10000000;    // more than a store to another CTA takes
 __device__ unsigned long long g_join_timeouts;  // waits that ran out
 
 template <int G, bool CL>
@@ -316,7 +317,9 @@ struct Team {
   Board<G, CL>* board;
   int turn, ctas, rank;
   uint32_t peer, parity;  // the board of the cluster's CTA lane % 8; of the areas' barriers, a bit each
-  bool lost;              // a wait ran out: what is read from then on is NaN, and nothing is waited for
+  // A wait ran out: what is read from then on is NaN, and nothing is waited for, sent or arrived at.  (A value sent ahead
+  // would count at its barrier for one that is missing.)  So the waits of all other warps run out in their turn.
+  bool lost;
 
   __device__ __forceinline__ Team(Board<G, CL>* b) : board(b), turn(0), ctas(1), rank(0), peer(0), parity(0), lost(false) {
     if constexpr (CL) {
@@ -331,9 +334,16 @@ struct Team {
       cluster.sync();  // every CTA's board is there
     }
   }
-  // Before the kernel ends: no CTA leaves while another may still send to it.
+  // Before the kernel ends: no CTA leaves while another may still send to it, or while what one has sent is under way,
+  // which nobody has waited for where a wait ran out.
   __device__ __forceinline__ void part() const {
-    if constexpr (CL) cooperative_groups::this_cluster().sync();
+    if constexpr (CL) {
+      cooperative_groups::this_cluster().sync();
+      if (lost) {
+        const uint64_t start = global_ns();
+        while (global_ns() - start < kLandNs);
+      }
+    }
   }
   __device__ __forceinline__ int warps() const { return G / 32 * ctas; }
   // Value `which` of this warp; lane `lane` of at least eight neighbours tells it to the cluster's CTA of that number.
@@ -343,7 +353,7 @@ struct Team {
       using B = Board<G, CL>;
       const uint32_t at = peer + uint32_t(offsetof(B, v)) + uint32_t(sizeof(B::v[0])) * turn + uint32_t(sizeof(B::v[0][0])) * which +
                           uint32_t(rank * (G / 32) + warp) * 4;
-      if (lane < ctas)
+      if (lane < ctas && !lost)
         asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(at),
                      "r"(__float_as_uint(v)), "r"(peer + uint32_t(offsetof(B, bar)) + 8 * turn)
                      : "memory");
@@ -355,7 +365,7 @@ struct Team {
   __device__ __forceinline__ void meet(int n) {
     if constexpr (CL) {
       const uint32_t bar = smem_addr(&board->bar[turn]);
-      if (threadIdx.x == 0) mbar_arrive_expect(bar, uint32_t(n * warps()) * 4);
+      if (threadIdx.x == 0 && !lost) mbar_arrive_expect(bar, uint32_t(n * warps()) * 4);
       if (!lost && !arrived(bar, parity >> turn & 1)) {
         lost = true;
         if ((threadIdx.x & 31) == 0) atomicAdd(&g_join_timeouts, 1ull);

@@ -470,9 +470,11 @@ LOCO_API loco_status loco_linear_backward_weight(const loco_linear_config* cfg, 
  * end after two seconds and 20 microseconds per 64 of the summed dimension at
  * most; a kernel that gave one up counts it.  What it had not finished of its
  * output is then not written, or, where several CTAs add up parts of a sum, NaN
- * (and the checkpoint's scales 255).  So do, after two seconds, the waits of the
- * CTAs that share a row of loco_join_forward and loco_join_backward (more than
- * 4096 columns), whose rows are then NaN.  This reads the count of the current device
+ * (and the checkpoint's scales 255).  So do, after two seconds, the waits for the
+ * sums of a row that CTAs of loco_join_forward and loco_join_backward share (more
+ * than 4096 columns): where one ran out, what is formed from the sums that did not
+ * come is NaN, in the columns of the threads that waited for them, and so are the
+ * rows that those CTAs have still to take.  This reads the count of the current device
  * since the library was loaded into *count (host).  It synchronises with the
  * device: for diagnosis, not for the training loop.
  */

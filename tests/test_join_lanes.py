@@ -35,3 +35,16 @@ def test_lanes_meet_before_one_writes_into_anothers_place(common):
     settle = body(common[common.index("struct Vec"):], "void settle(")
     assert settle.index("if (ANY) __syncwarp();") < settle.index("ring16(piece(e, k))") < settle.index("to_ring16(piece(e, k)")
     assert settle.count("__syncwarp") == 2
+
+
+def test_a_wait_that_ran_out_leaves_nothing_under_way(common):
+    """A thread whose wait ran out neither sends nor arrives any more: values sent ahead would count at a barrier for ones
+    that are missing, and a second arrival in one phase is one too many.  The others' waits run out in their turn, and a
+    CTA of which one ran out ends only some time after all of the cluster's have done so, when no store is under way."""
+    write, meet, part = (body(common[common.index("struct Team"):], f"void {name}(") for name in ("write", "meet", "part"))
+    assert re.search(r"if \(lane < ctas && !lost\)\s+asm volatile\(\"st\.async", write)
+    assert re.search(r"if \(threadIdx\.x == 0 && !lost\) mbar_arrive_expect\(", meet)
+    together, wait = part.index("this_cluster().sync()"), part.index("if (lost)")
+    assert together < wait and re.search(r"while \(global_ns\(\) - start < kLandNs\);", part[wait:])
+    assert 1_000_000 <= int(re.search(r"kLandNs = (\d+);", common).group(1)) <= 100_000_000
+    assert common.count("st.async") == 1 and common.count("mbar_arrive_expect(") == 1
