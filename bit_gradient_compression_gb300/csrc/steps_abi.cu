@@ -36,7 +36,9 @@ loco_status check_logits(int32_t dtype, int64_t rows, int64_t vocab, float scale
   LOCO_TRY(check_dtype(dtype, "dtype"));
   LOCO_TRY(check_dim(rows, 0, "rows"));
   LOCO_TRY(check_dim(vocab, 1, "vocab"));
-  if (!(scale > 0.0f) || !isfinite(scale)) return fail(LOCO_ERR_INVALID_ARG, "scale = %g must be finite and > 0", scale);
+  constexpr float kLog2E = 1.4426950408889634f;  // (the kernels' exponents are to base 2)
+  if (!(scale > 0.0f) || !isfinite(scale * kLog2E))
+    return fail(LOCO_ERR_INVALID_ARG, "scale = %g must be > 0 and scale * log2(e) finite", scale);
   return LOCO_OK;
 }
 

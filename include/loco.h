@@ -553,7 +553,8 @@ LOCO_API loco_status loco_join_backward(const loco_join_config* cfg, const void*
 
 /*
  * loco_logprob_forward — log probabilities of given tokens.  Per row i of the
- * logits [rows, vocab] (dtype), z_j = scale * logits_ij (scale finite, > 0):
+ * logits [rows, vocab] (dtype), z_j = scale * logits_ij (scale > 0, scale *
+ * log2(e) finite in fp32):
  *   lse = log(sum_j exp(z_j)) ;  logp = z_t - lse, t = targets_i
  *   entropy = lse - sum_j p_j z_j, p_j = exp(z_j - lse)
  *   top_ids, top_logp: the `top` largest logits' columns and z_j - lse, the
