@@ -21,9 +21,10 @@
 //
 // 4096 x 131072 bf16: 157 us, 6.8 TB/s, without alternatives, a copy's rate; 192 us with eight of them, where the SMs issue
 // in 78 % of the cycles, 11.6 instructions an element; candidates are most in a row's first tiles.  8192 x 32000 with
-// five: 111 us, 70 % of a copy's rate.  1 x 32000 with twenty: 8.6 us, a launch, a cluster of eight CTAs and their join.
+// five: 111 us, 70 % of a copy's rate.  1 x 32000 with twenty: 8.8 us, a launch, a cluster of eight CTAs and their join.
 //
-// Backward, one read and one write a value: 8192 x 32000 bf16 153 us, 6.9 TB/s, a copy's rate.
+// Backward, one read and one write a value: 8192 x 32000 bf16 153 us, 6.9 TB/s, a copy's rate, where rows of logits and of
+// the gradient start alike within 16 bytes.  Others go element by element: 333 x 32003 fp32 21 us out of a cold L2, of 12.6.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -465,24 +466,52 @@ __device__ __forceinline__ float slope_at(float z, const Slope& k) {
 
 // 24 bits hold a log sum to 2^-24 of itself, by which p is off: 2^-14 here.  Rows farther from 0 (masked by -1e9 or by the
 // type's lowest value from end to end, so that lse is that value however many tokens share the probability) and those
-// whose log sum is infinite are summed anew, and p taken in deviations from the row's maximum.
+// whose log sum is infinite are summed anew, and p taken in deviations from the row's maximum: one more read (8192 x 32000
+// bf16, all of them such rows, 205 us instead of 155).
 constexpr float kFar = 1024.0f;
 
-// Maximum or sum over a row's team, the same in all its threads.
-template <int WPR, typename Op>
-__device__ __forceinline__ float across(float v, const Op& op) {
+// Maximum and sum of 2^((z - maximum) c) of a row, by its team; the same in all its threads.
+template <bool BF16, int WPR>
+__device__ __forceinline__ Part far_sum(const char* z, const RowShape<BF16>& shape, int64_t cols, float c, int t) {
+  constexpr int kElem = BF16 ? 2 : 4, V = kVec<BF16>, kTeam = 32 * WPR;
+  const uint32_t none = BF16 ? 0xFF80FF80u : 0xFF800000u;
+  const uint4* vec = reinterpret_cast<const uint4*>(z + shape.head * kElem);
+  Part mine{kLowest, 0.0f, 0.0f};
+  const auto take_one = [&](int64_t i) {
+    const float v = load_elem_rw(z, i, BF16), m = max_nan(mine.m, v);
+    mine = join(mine, Part{m, exp2_f(max_nan((v - m) * c, kLeast)), 0.0f}, c);
+  };
+  const int64_t tail = shape.head + shape.vectors * V;
+  if (t < shape.head) take_one(t);
+  if (t < cols - tail) take_one(tail + t);
+  for (int64_t i = t; i < shape.vectors; i += 4 * kTeam) {
+    uint4 w[4];
+    float m = mine.m, s = 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  if constexpr (WPR > 1) {
-    __shared__ float part[WPR];
-    __syncthreads();  // (an earlier one's are read)
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = part[0];
+    for (int q = 0; q < 4; ++q) w[q] = i + q * kTeam < shape.vectors ? vec[i + q * kTeam] : make_uint4(none, none, none, none);
 #pragma unroll
-    for (int w = 1; w < WPR; ++w) v = op(v, part[w]);
+    for (int q = 0; q < 4; ++q) m = max_nan(m, largest<BF16>(w[q]));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      Pair v[V / 2];
+      to_pairs<BF16>(w[q], v);
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 x = halves((v[j] + pair(-m, -m)) * pair(c, c));
+        s += exp2_f(max_nan(x.x, kLeast)) + exp2_f(max_nan(x.y, kLeast));
+      }
+    }
+    mine = Part{m, fmaf(exp2_f(max_nan((mine.m - m) * c, kLeast)), mine.s, s), 0.0f};
   }
-  return v;
+  const int lane = threadIdx.x & 31;
+  mine = join_lanes<32>(mine, lane, c);
+  if constexpr (WPR > 1) {
+    __shared__ Part part[WPR];
+    if (lane == 0) part[threadIdx.x / 32] = mine;
+    __syncthreads();
+    mine = join_lanes<WPR>(part[lane % WPR], lane, c);
+  }
+  return mine;
 }
 
 template <bool BF16>
@@ -508,45 +537,24 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_bwd(const LogprobBwdArgs
   k.scale = a.scale, k.lse = lse;
   k.a = -a.scale * fmaf(dh, h, d), k.b = -a.scale * dh * kLn2, k.at = a.scale * d;
   k.target = y < a.vocab ? y : -1;
+  const RowShape<BF16> shape = row_shape<BF16>(z, a.vocab);
+  float base = 0.0f;  // of the logits: lse is that of their deviations from it
+  if (fabsf(lse) > kFar) {
+    // (in place of the logits one CTA has the row: what it reads first, nobody else may have overwritten)
+    if (z == o) {
+      if (me != 0) return;
+      parts = 1;
+    }
+    const Part sum = far_sum<BF16, WPR>(z, shape, a.vocab, a.scale * kLog2E, t);
+    if (sum.s == 0.0f)
+      k.lse = k.a = k.b = k.at = 0.0f;  // nothing is left
+    else
+      base = sum.m, k.lse = logf(sum.s);
+  }
   const auto value = [&](float v, int64_t col) {
-    const float g = slope_at(v, k);
+    const float g = slope_at(v - base, k);
     return col == k.target ? g + k.at : g;
   };
-  // columns lo to hi - 1, neighbouring lanes taking neighbouring ones: f(eight values, their first column)
-  const auto each = [&](int64_t lo, int64_t hi, const auto& f) {
-    for (int64_t i = lo + t; i < hi; i += 8 * kTeam) {
-      float v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = i + q * kTeam < hi ? load_elem_rw(z, i + q * kTeam, BF16) : -INFINITY;
-      f(v, i);
-    }
-  };
-  if (fabsf(lse) > kFar) {
-    // one CTA (or warp) has the row: what it reads twice, nobody else may have overwritten
-    if (me != 0) return;
-    float m = -INFINITY, s = 0.0f;
-    each(0, a.vocab, [&](const float (&v)[8], int64_t) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) m = max_nan(m, v[q]);
-    });
-    m = across<WPR>(m, [](float u, float v) { return max_nan(u, v); });
-    const bool none = m == -INFINITY;  // nothing is left
-    if (!none) {
-      const float c = a.scale * kLog2E;
-      each(0, a.vocab, [&](const float (&v)[8], int64_t) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s += exp2_f(max_nan((v[q] - m) * c, kLeast));
-      });
-      k.lse = logf(across<WPR>(s, [](float u, float v) { return u + v; }));
-    }
-    each(0, a.vocab, [&](const float (&v)[8], int64_t i) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (i + q * kTeam < a.vocab) store_one<BF16>(o, i + q * kTeam, none ? 0.0f : value(v[q] - m, i + q * kTeam));
-    });
-    return;
-  }
-  const RowShape<BF16> shape = row_shape<BF16>(z, a.vocab);
   if ((reinterpret_cast<uintptr_t>(z) & 15) == (reinterpret_cast<uintptr_t>(o) & 15)) {
     const int64_t v_lo = shape.vectors * me / parts, v_hi = shape.vectors * (me + 1) / parts;
     const int64_t tail = shape.head + shape.vectors * V;
@@ -581,12 +589,17 @@ __global__ void __launch_bounds__(kThreadsLp) k_logprob_bwd(const LogprobBwdArgs
     }
   } else {
     // rows of logits and gradient start at different places within 16 bytes: neighbouring lanes take neighbouring elements
-    const int64_t hi = a.vocab * (me + 1) / parts;
-    each(a.vocab * me / parts, hi, [&](const float (&v)[8], int64_t i) {
+    const int64_t lo = a.vocab * me / parts, hi = a.vocab * (me + 1) / parts;
+    for (int64_t i = lo + t; i < hi; i += 8 * kTeam) {
+      float v[8], g[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = i + q * kTeam < hi ? load_elem_rw(z, i + q * kTeam, BF16) : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) g[q] = value(v[q], i + q * kTeam);
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (i + q * kTeam < hi) store_one<BF16>(o, i + q * kTeam, value(v[q], i + q * kTeam));
-    });
+        if (i + q * kTeam < hi) store_one<BF16>(o, i + q * kTeam, g[q]);
+    }
   }
 }
 

@@ -584,7 +584,7 @@ LOCO_API loco_status loco_logprob_forward(const void* logits, int32_t dtype, int
  * is NaN or whose target is >= vocab (with dlogp) NaN.
  * Where |lse| is above 1024 (rows of nothing but large negative masks among
  * them) or infinite, lse's 24 bits do not hold p, and the row is summed anew,
- * which reads it twice more.
+ * which reads it once more.
  */
 LOCO_API loco_status loco_logprob_backward(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
                                   float scale, const int64_t* targets, const float* lse, const float* entropy,
