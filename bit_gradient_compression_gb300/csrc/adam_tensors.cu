@@ -70,8 +70,8 @@ __device__ __forceinline__ Pair both(float v) { return pair(v, v); }
 // P. Markstein, "Correctness proofs outline for Newton-Raphson based floating-point divide and square root algorithms"
 // (1999): from an approximation y of 1/b, one step makes it the rounded reciprocal, and q + (a - b q) y, whose remainder
 // a - b q is exact, the rounded quotient; likewise g + (v - g^2) h for the root, h of 1 / (2 sqrt(v)).  They hold where
-// nothing is lost to the ends of the exponent's range: see `extreme`.  Every root of [1, 4) and every reciprocal of
-// [1, 2) has been compared with the IEEE operations, and quotients of 2^31 random pairs; so are the steps in the tests.
+// nothing is lost to the ends of the exponent's range: see `extreme`.  The tests compare steps over every root of [1, 4),
+// each the denominator of several quotients, with the IEEE operations.
 // With them a step with 8-bit states takes about 100 instructions an element instead of 111.
 __device__ __forceinline__ float rsqrt_approx(float v) {
   float r;

@@ -14,7 +14,7 @@
 // 16384 x 4096 bf16 with RMS norms takes 153 us, 5.3 TB/s, 78 % of a copy's rate: with the sums over rows in registers two
 // CTAs of 256 threads fit an SM (24 % of its warps), which issue in 43 % of the cycles and wait for one another at the two
 // sums of each row.  (Merging those of a row with the next one's, as the forward pass does, takes 16 registers more and
-// 171 us.)  Layer norms with betas 228 us; 2048 x 16384 202 us; 16384 x 4095 313 us; 500 x 2048 fp32 16 us, of which the
+// 171 us.)  Layer norms with betas 228 us; 2048 x 16384 193 us; 16384 x 4095 311 us; 500 x 2048 fp32 16 us, of which the
 // second kernel is a third.
 #include "join_common.cuh"
 

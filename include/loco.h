@@ -643,7 +643,9 @@ typedef struct {
  * alignment, codes 16 bytes; 16-byte aligned ones take the wide loads.  Nothing
  * written may overlap another buffer of the call.
  * hp: lr, lr_scale, decay_scale, weight_decay finite; else as loco_adam_step.
- * t = 1-based step.  count == 0 is an empty call.
+ * t = 1-based step.  tensors, hp and t are read during the call: a call captured
+ * into a graph repeats that step, with its bias corrections and its dither.
+ * count == 0 is an empty call.
  */
 LOCO_API loco_status loco_adam_tensors(const loco_adam_tensors_config* cfg, const loco_adam_tensor* tensors, int32_t count,
                               const loco_adam_hparams* hp, int64_t t, const float* grad_scale, loco_stream_t stream);
